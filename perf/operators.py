@@ -22,7 +22,9 @@ own = False
 COEFFICIENTS = (3.4445, -4.7750, 2.0315)
 STEPS = 5
 NS_EPS = 1e-7
-LR, WEIGHT_DECAY, MOMENTUM, ADAM_EPS, BETA1, BETA2 = 2e-4, 0.1, 0.95, 1e-8, 0.9, 0.999
+LR, WEIGHT_DECAY, MOMENTUM, ADAM_EPS = 2e-4, 0.1, 0.95, 1e-8
+# the configuration holds its betas in fp32 and 1 - beta is the difference from that value
+BETA1, BETA2 = torch.tensor([0.9, 0.999], dtype=torch.float32).tolist()
 QK_EPS = 1e-6
 DTYPES = {"bf16": torch.bfloat16, "fp32": torch.float32}
 
