@@ -533,6 +533,197 @@ zero_status zero_cpu_adam(const zero_config* cfg, int64_t t, const float* grad, 
                           float* exp_avg, float* exp_avg_sq, uint16_t* param16, int64_t n,
                           int32_t n_threads);
 
+/* ---- Muon: orthogonalised updates of the matrices -------------------------
+ * The pages stop at Adam; this is the optimizer step for a model whose
+ * matrices take an orthogonalised momentum update while everything else
+ * (embeddings, norms, biases, heads) stays with Adam / AdamW in the same
+ * zero_step.  A shard boundary may cut a matrix anywhere, so the update needs
+ * the whole matrix; all shards of the simulated ranks live in one buffer, and
+ * the result does not depend on the stage.
+ */
+
+/*
+ * Newton-Schulz orthogonalisation of a matrix G:
+ *   X = G / (|G|_F + eps), then `steps` times
+ *   X <- a X + b (X X^T) X + c (X X^T)^2 X
+ * an odd polynomial of the singular values that leaves the singular vectors.
+ * The products run on fp16 operands with power-of-two scales (11 bits, and 22
+ * for X while later steps still amplify its rounding) and fp32 sums: about
+ * 1e-3 of the result's norm on matrices of any rank.
+ *  steps    1..32;  a, b, c, eps: finite, eps >= 0; coefficients under which
+ *           a singular value in [0, 1] grows beyond 1024 are refused.
+ */
+typedef struct zero_ns_config {
+  int32_t steps;
+  float a;
+  float b;
+  float c;
+  float eps;
+} zero_ns_config;
+
+/* Workspace of zero_orthogonalize for a stack of `batch` rows x cols matrices
+ * (0 when there is nothing to do).  Errors: ZERO_EINVAL. */
+zero_status zero_orthogonalize_workspace_bytes(const zero_ns_config* cfg, int64_t rows, int64_t cols, int64_t batch,
+                                               int64_t* bytes);
+
+/*
+ * zero_orthogonalize — out[i] = bf16(orthogonalised in[i]) for a stack of
+ * matrices.  No context: errors' text comes from zero_last_error(NULL).
+ *  in         device matrices of in_dtype (zero_grad_dtype), element (r, c) of
+ *             matrix i at i * in_batch_stride + r * in_row_stride + c
+ *             (elements; the batch stride may be 0)
+ *  out        device bf16 matrices, likewise; must not overlap `in`
+ *  workspace  device scratch, 256-byte aligned, kept until the work on
+ *             `stream` has completed
+ * An all-zero matrix gives zeros; one with an inf or NaN gives NaN.
+ * rows, cols or batch of 0: ZERO_OK without device work.
+ * Errors: ZERO_EINVAL (config, sizes, strides, pointers, workspace);
+ * ZERO_ECUDA.
+ */
+zero_status zero_orthogonalize(const zero_ns_config* cfg, int64_t rows, int64_t cols, int64_t batch, const void* in,
+                               int32_t in_dtype, int64_t in_row_stride, int64_t in_batch_stride, void* out,
+                               int64_t out_row_stride, int64_t out_batch_stride, void* workspace,
+                               int64_t workspace_bytes, void* stream);
+
+/* Scale s of a matrix's update: 0.2 sqrt(max(rows, cols)) gives it the RMS of
+ * an Adam update, so that both can share a learning rate and decay; the other
+ * is sqrt(max(1, rows / cols)). */
+#define ZERO_MUON_SCALE_RMS 0
+#define ZERO_MUON_SCALE_ASPECT 1
+
+/*
+ *  lr, momentum, weight_decay   finite; momentum in [0, 1), decay >= 0
+ *  nesterov                     1: update = g + momentum * mom; 0: mom
+ *  scale                        ZERO_MUON_SCALE_*
+ */
+typedef struct zero_muon_config {
+  float lr;
+  float momentum;
+  float weight_decay;
+  int32_t nesterov;
+  int32_t scale;
+  zero_ns_config ns;
+} zero_muon_config;
+
+/* Workspace of zero_enable_muon.  rows / cols as there.  Errors: ZERO_EINVAL, ZERO_ENOMEM. */
+zero_status zero_muon_workspace_bytes(const zero_ctx* ctx, const zero_muon_config* cfg, const int64_t* rows,
+                                      const int64_t* cols, int32_t n_params, int64_t* bytes);
+
+/*
+ * zero_enable_muon — later zero_steps update the given matrices so:
+ *   g   = ((G_0 + G_1) + ... + G_{N-1}) * (1/N)   (times the clip coefficient)
+ *   mom = momentum * mom + g                      (in exp_avg)
+ *   u   = nesterov ? g + momentum * mom : mom
+ *   w   = w * (1 - lr*weight_decay) - lr * s * orthogonalised(u)
+ *   param16 = bf16(w)
+ * and everything else (pads included) as before.  exp_avg_sq is not used for
+ * the matrices.  Clipping (kept or not), the overflow count, capture,
+ * export / import and the gathers work unchanged; zero_set_lr sets Adam's
+ * rate alone.  Calling it again replaces the configuration.
+ *  rows, cols  per parameter: its row-major shape, rows * cols elements; 0, 0
+ *              leaves the parameter with Adam
+ *  workspace   device scratch of zero_muon_workspace_bytes, 256-byte aligned,
+ *              caller-owned, in use by every step until zero_disable_muon
+ * Errors: ZERO_EINVAL (config, shapes, workspace); ZERO_ESTATE (no buffers, a
+ * step awaits post_step); ZERO_ENOTSUP (offload context); ZERO_ENOMEM.  A
+ * zero_step that then fails with ZERO_ECUDA may have updated what was launched
+ * before the failure.
+ */
+zero_status zero_enable_muon(zero_ctx* ctx, const zero_muon_config* cfg, const int64_t* rows, const int64_t* cols,
+                             int32_t n_params, void* workspace, int64_t workspace_bytes);
+
+/* All parameters back to Adam (exp_avg of the matrices then holds their
+ * momentum, exp_avg_sq what it held before).  Errors: ZERO_ESTATE. */
+zero_status zero_disable_muon(zero_ctx* ctx);
+
+/* Learning rate of later Muon updates (a captured step keeps its own). */
+zero_status zero_set_muon_lr(zero_ctx* ctx, float lr);
+
+/* ---- Norm and rotation of queries and keys --------------------------------
+ * Orthogonalised updates move all singular values of the query and key
+ * projections at one rate, which lets attention logits grow; training with
+ * them norms every head's queries and keys.  The two gains are parameters of
+ * the layer's unit (vectors: Adam), and the backward pass writes their
+ * gradient where the replica's flat gradient holds it.
+ */
+
+/*
+ *  q_heads, k_heads  heads per token (0 allowed), head_dim 2..256 (the norm of
+ *                    one element leaves its sign alone, and its gradient in
+ *                    fp32 would be rounding)
+ *  rotary_dim        even, 0..head_dim: the first rotary_dim elements of a head
+ *                    are rotated, the rest only normed
+ *  interleaved       0: element i pairs with i + rotary_dim/2; 1: 2i with 2i+1
+ *  dtype             zero_grad_dtype of queries, keys and their gradients
+ *  gain_dtype        zero_grad_dtype of the gains (bf16: as gathered)
+ *  n_positions       rows of the rotation table
+ *  eps               finite, >= 0
+ */
+typedef struct zero_qk_config {
+  int32_t q_heads;
+  int32_t k_heads;
+  int32_t head_dim;
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int32_t dtype;
+  int32_t gain_dtype;
+  float eps;
+  int64_t n_positions;
+} zero_qk_config;
+
+/* Device heads: element d of head h of token t at t * token_stride +
+ * h * head_stride + d (elements; aligned to the element size). */
+typedef struct zero_heads {
+  void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} zero_heads;
+
+/*
+ * zero_qk_norm_rope — for every token t and head, with x the head's vector,
+ *   y = x / sqrt(mean(x^2) + eps) * gain
+ *   out = y with every pair (y1, y2) of the rotated part turned to
+ *         (y1 cos - y2 sin, y2 cos + y1 sin)
+ * in fp32, rounded once.  A token whose position is outside [0, n_positions)
+ * is padding: its outputs are zero.  Queries and keys share one launch.
+ *  q_gain, k_gain  head_dim elements of gain_dtype, or NULL: no gain
+ *  table           fp32 [n_positions][rotary_dim]: rotary_dim/2 cosines, then
+ *                  as many sines (NULL allowed when rotary_dim is 0)
+ *  positions       int32 per token, or NULL: token t has position t
+ *  q_out, k_out    may be q, k themselves (same strides), else must not
+ *                  overlap them
+ * tokens of 0: ZERO_OK without device work.  No context: errors' text comes
+ * from zero_last_error(NULL).  Errors: ZERO_EINVAL; ZERO_ECUDA.
+ */
+zero_status zero_qk_norm_rope(const zero_qk_config* cfg, int64_t tokens, const zero_heads* q, const zero_heads* k,
+                              const void* q_gain, const void* k_gain, const float* table, const int32_t* positions,
+                              const zero_heads* q_out, const zero_heads* k_out, void* stream);
+
+/* Workspace of zero_qk_norm_rope_backward.  Errors: ZERO_EINVAL. */
+zero_status zero_qk_backward_workspace_bytes(const zero_qk_config* cfg, int64_t tokens, int64_t* bytes);
+
+/*
+ * zero_qk_norm_rope_backward — gradients of zero_qk_norm_rope's inputs from
+ * those of its outputs (dq_out, dk_out), with x the forward input, xn = x *
+ * rstd and h the gradient turned back by the rotation:
+ *   dx = rstd * (gain h - xn mean(gain h xn)),   dgain = sum of h xn
+ * over every token that is not padding (padding tokens' dx are zero, their
+ * gradients are not read into any sum).  The gain sums are fp32 in a fixed
+ * order: the same call gives the same bits.
+ *  dq, dk            may be dq_out, dk_out themselves (same strides)
+ *  dq_gain, dk_gain  head_dim elements of dgain_dtype (zero_grad_dtype),
+ *                    overwritten (zeros for 0 tokens or heads); NULL: not
+ *                    wanted
+ *  workspace         device scratch, 16-byte aligned
+ * Errors: as zero_qk_norm_rope; ZERO_EINVAL for a small workspace.
+ */
+zero_status zero_qk_norm_rope_backward(const zero_qk_config* cfg, int64_t tokens, const zero_heads* dq_out,
+                                       const zero_heads* dk_out, const zero_heads* q, const zero_heads* k,
+                                       const void* q_gain, const void* k_gain, const float* table,
+                                       const int32_t* positions, const zero_heads* dq, const zero_heads* dk,
+                                       void* dq_gain, void* dk_gain, int32_t dgain_dtype, void* workspace,
+                                       int64_t workspace_bytes, void* stream);
+
 /*
  * zero_kernel_timeouts — how many bounded waits of the tile-staged step
  * kernels (used for N = 1..4 or N >= 11 bf16 and N >= 7 fp32 replicas when a

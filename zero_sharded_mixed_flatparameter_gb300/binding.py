@@ -32,10 +32,14 @@ EXPORTED = (
     "zero_make_master_offload", "zero_offload_workspace_bytes", "zero_offload_step", "zero_cpu_adam",
     "zero_debug_inject", "zero_debug_check_failures", "zero_capturable_workspace_bytes", "zero_enable_capturable",
     "zero_disable_capturable", "zero_count_nonfinite", "zero_read_nonfinite", "zero_gather_units",
+    "zero_orthogonalize_workspace_bytes", "zero_orthogonalize", "zero_muon_workspace_bytes", "zero_enable_muon",
+    "zero_disable_muon", "zero_set_muon_lr", "zero_qk_norm_rope", "zero_qk_backward_workspace_bytes",
+    "zero_qk_norm_rope_backward",
 )
 ZERO_CLIP_KEEP_REDUCED = 1
 ZERO_INJECT_MISSING_COPY = 1
 ZERO_INJECT_SHORT_BOUNDS = 2
+ZERO_MUON_SCALE_RMS, ZERO_MUON_SCALE_ASPECT = 0, 1
 
 
 class zero_config(ctypes.Structure):
@@ -47,6 +51,26 @@ class zero_config(ctypes.Structure):
 class zero_buffers(ctypes.Structure):
     _fields_ = [("master", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
                 ("param16", ctypes.c_void_p)]
+
+
+class zero_ns_config(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_int32), ("a", ctypes.c_float), ("b", ctypes.c_float), ("c", ctypes.c_float),
+                ("eps", ctypes.c_float)]
+
+
+class zero_muon_config(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_float), ("momentum", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("nesterov", ctypes.c_int32), ("scale", ctypes.c_int32), ("ns", zero_ns_config)]
+
+
+class zero_qk_config(ctypes.Structure):
+    _fields_ = [("q_heads", ctypes.c_int32), ("k_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("gain_dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("n_positions", ctypes.c_int64)]
+
+
+class zero_heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
 
 
 class ZeroError(RuntimeError):
@@ -111,6 +135,18 @@ def load(path: str = LIB_PATH):
             "zero_capturable_workspace_bytes": [vp, i64, P(i64)],
             "zero_enable_capturable": [vp, vp, i64, i64, vp],
             "zero_disable_capturable": [vp, vp],
+            "zero_orthogonalize_workspace_bytes": [P(zero_ns_config), i64, i64, i64, P(i64)],
+            "zero_orthogonalize": [P(zero_ns_config), i64, i64, i64, vp, i32, i64, i64, vp, i64, i64, vp, i64, vp],
+            "zero_muon_workspace_bytes": [vp, P(zero_muon_config), vp, vp, i32, P(i64)],
+            "zero_enable_muon": [vp, P(zero_muon_config), vp, vp, i32, vp, i64],
+            "zero_disable_muon": [vp],
+            "zero_set_muon_lr": [vp, f32],
+            "zero_qk_norm_rope": [P(zero_qk_config), i64, P(zero_heads), P(zero_heads), vp, vp, vp, vp,
+                                  P(zero_heads), P(zero_heads), vp],
+            "zero_qk_backward_workspace_bytes": [P(zero_qk_config), i64, P(i64)],
+            "zero_qk_norm_rope_backward": [P(zero_qk_config), i64, P(zero_heads), P(zero_heads), P(zero_heads),
+                                           P(zero_heads), vp, vp, vp, vp, P(zero_heads), P(zero_heads), vp, vp, i32,
+                                           vp, i64, vp],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -376,6 +412,80 @@ def zero_grad_norm(ctx: int, stream: int = 0) -> float:
     out = ctypes.c_double()
     _check(load().zero_grad_norm(ctx, ctypes.byref(out), stream or None), ctx)
     return out.value
+
+
+def make_ns_config(steps: int = 5, coefficients: Sequence[float] = (3.4445, -4.7750, 2.0315),
+                   eps: float = 1e-7) -> zero_ns_config:
+    a, b, c = coefficients
+    return zero_ns_config(steps, a, b, c, eps)
+
+
+def zero_orthogonalize_workspace_bytes(cfg: zero_ns_config, rows: int, cols: int, batch: int) -> int:
+    n = ctypes.c_int64()
+    _check(load().zero_orthogonalize_workspace_bytes(ctypes.byref(cfg), rows, cols, batch, ctypes.byref(n)))
+    return n.value
+
+
+def zero_orthogonalize(cfg: zero_ns_config, rows: int, cols: int, batch: int, src: int, in_dtype: int,
+                       in_row_stride: int, in_batch_stride: int, out: int, out_row_stride: int, out_batch_stride: int,
+                       workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(load().zero_orthogonalize(ctypes.byref(cfg), rows, cols, batch, src or None, in_dtype, in_row_stride,
+                                     in_batch_stride, out or None, out_row_stride, out_batch_stride,
+                                     workspace or None, workspace_bytes, stream or None))
+
+
+def make_muon_config(lr: float, momentum: float = 0.95, weight_decay: float = 0.0, nesterov: bool = True,
+                     scale: str = "rms", steps: int = 5, coefficients: Sequence[float] = (3.4445, -4.7750, 2.0315),
+                     eps: float = 1e-7) -> zero_muon_config:
+    scales = {"rms": ZERO_MUON_SCALE_RMS, "aspect": ZERO_MUON_SCALE_ASPECT}
+    if scale not in scales:
+        raise ValueError(f"scale must be one of {sorted(scales)}")
+    return zero_muon_config(lr, momentum, weight_decay, 1 if nesterov else 0, scales[scale],
+                            make_ns_config(steps, coefficients, eps))
+
+
+def zero_muon_workspace_bytes(ctx: int, cfg: zero_muon_config, rows: Sequence[int], cols: Sequence[int]) -> int:
+    n = ctypes.c_int64()
+    _check(load().zero_muon_workspace_bytes(ctx, ctypes.byref(cfg), _i64(rows), _i64(cols), len(rows),
+                                            ctypes.byref(n)), ctx)
+    return n.value
+
+
+def zero_enable_muon(ctx: int, cfg: zero_muon_config, rows: Sequence[int], cols: Sequence[int], workspace: int,
+                     workspace_bytes: int) -> None:
+    _check(load().zero_enable_muon(ctx, ctypes.byref(cfg), _i64(rows), _i64(cols), len(rows), workspace or None,
+                                   workspace_bytes), ctx)
+
+
+def zero_disable_muon(ctx: int) -> None:
+    _check(load().zero_disable_muon(ctx), ctx)
+
+
+def zero_set_muon_lr(ctx: int, lr: float) -> None:
+    _check(load().zero_set_muon_lr(ctx, lr), ctx)
+
+
+def zero_qk_norm_rope(cfg: zero_qk_config, tokens: int, q: zero_heads, k: zero_heads, q_gain: int, k_gain: int,
+                      table: int, positions: int, q_out: zero_heads, k_out: zero_heads, stream: int = 0) -> None:
+    _check(load().zero_qk_norm_rope(ctypes.byref(cfg), tokens, ctypes.byref(q), ctypes.byref(k), q_gain or None,
+                                    k_gain or None, table or None, positions or None, ctypes.byref(q_out),
+                                    ctypes.byref(k_out), stream or None))
+
+
+def zero_qk_backward_workspace_bytes(cfg: zero_qk_config, tokens: int) -> int:
+    n = ctypes.c_int64()
+    _check(load().zero_qk_backward_workspace_bytes(ctypes.byref(cfg), tokens, ctypes.byref(n)))
+    return n.value
+
+
+def zero_qk_norm_rope_backward(cfg: zero_qk_config, tokens: int, dq_out: zero_heads, dk_out: zero_heads,
+                               q: zero_heads, k: zero_heads, q_gain: int, k_gain: int, table: int, positions: int,
+                               dq: zero_heads, dk: zero_heads, dq_gain: int, dk_gain: int, dgain_dtype: int,
+                               workspace: int, workspace_bytes: int, stream: int = 0) -> None:
+    _check(load().zero_qk_norm_rope_backward(
+        ctypes.byref(cfg), tokens, ctypes.byref(dq_out), ctypes.byref(dk_out), ctypes.byref(q), ctypes.byref(k),
+        q_gain or None, k_gain or None, table or None, positions or None, ctypes.byref(dq), ctypes.byref(dk),
+        dq_gain or None, dk_gain or None, dgain_dtype, workspace or None, workspace_bytes, stream or None))
 
 
 def zero_destroy(ctx: int) -> None:

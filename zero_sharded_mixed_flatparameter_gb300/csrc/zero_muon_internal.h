@@ -1,0 +1,145 @@
+// Internal interface of the Newton-Schulz orthogonalisation and of the Muon
+// step (zero_orthogonalize.cpp, zero_muon_kernels.cu, zero_ns_gemm.cu).  Not
+// part of the public ABI.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "zero_internal.h"
+
+struct zero_ns_config;
+
+namespace zfs {
+
+// Matrices of one launch (one shape); more of a shape go in several.
+constexpr int kMaxMats = 64;
+// Elements of one partial sum of a matrix's squared Frobenius norm.  The
+// chunks are relative to the matrix and every thread takes the same elements
+// whatever their alignment, so the norm does not depend on where a layout
+// puts the matrix.
+constexpr long long kNsChunk = 16384;
+
+// ---- the orthogonalisation engine ------------------------------------------
+// One stack of `mats` matrices of r x c.  m is the smaller side, n the larger.
+// X is kept in the given orientation as fp16 with a power-of-two scale (see
+// ns_gemm), pitch ldx; the Gram matrix A and the polynomial P are m x m,
+// pitch ldm.
+struct NsPlan {
+  long long rows = 0, cols = 0;
+  long long m = 0, n = 0;
+  bool tall = false;       // rows > cols
+  int mats = 0;            // matrices in flight (workspace)
+  long long ldx = 0, ldm = 0;
+  long long chunks = 0;    // norm partials per matrix
+  // byte offsets in the workspace
+  long long partials = 0, x_hi[2] = {0, 0}, x_lo[2] = {0, 0}, gram = 0, poly = 0, update = 0, bytes = 0;
+};
+
+// Where the finished stack goes.
+struct NsOut {
+  // Orthogonalised matrices as bf16 (out != nullptr), ...
+  uint16_t* out = nullptr;
+  long long row_stride = 0, mat_stride = 0;
+  // ... or the Muon update of the flat buffer: w = w * decay - step * O.
+  float* master = nullptr;
+  uint16_t* p16 = nullptr;
+  float decay = 1.0f, step = 0.0f;
+  long long total_padded = 0;      // elements of master / p16 (debug bounds checks)
+  const long long* dev_t = nullptr;  // capturable steps: nothing is written once *dev_t >= dev_steps
+  long long dev_steps = 0;
+  long long offset[kMaxMats] = {};
+};
+
+// The layout for `mats` matrices at once; `keep_update`: room for the fp32
+// update (the Muon step's momentum pass writes it, the scale pass reads it).
+NsPlan ns_plan(long long rows, long long cols, int mats, bool keep_update);
+// How many of `batch` equal matrices one pass works on.
+int ns_mats(long long rows, long long cols, long long batch);
+// Checks steps, coefficients and eps; the reason in `why`.
+bool ns_config_ok(const zero_ns_config& cfg, const char** why);
+// From `src` with its norm partials in the workspace to `out`: normalise, then the steps.
+struct MatSource;
+cudaError_t ns_run(const NsPlan& p, const zero_ns_config& cfg, int mats, const MatSource& src, char* ws,
+                   const NsOut& out, cudaStream_t stream, int* launches);
+
+// ---- elementwise passes (zero_muon_kernels.cu) -----------------------------
+// A stack of strided matrices as the orthogonalisation's input.
+struct MatSource {
+  const void* data;
+  int fp32;                 // else bf16
+  long long row_stride, mat_stride;
+  int vec_ok;               // 8-element vectors of a row are aligned
+};
+// Partial sums of squares, [mat][chunk].
+cudaError_t launch_ns_norm(const MatSource& s, const NsPlan& p, int mats, double* partials, cudaStream_t stream);
+// X0 = source / (norm + eps) as scaled fp16 pair (hi, lo).
+struct ScaleArgs {
+  MatSource src;
+  long long rows, cols, ldx;
+  int mats;
+  long long chunks;
+  const double* partials;
+  double eps;
+  float scale;              // power of two of the stored values
+  uint16_t* hi;             // fp16 bits, [mat][row][ldx]
+  uint16_t* lo;             // or nullptr
+};
+cudaError_t launch_ns_scale(const ScaleArgs& a, cudaStream_t stream);
+
+// The Muon step's momentum pass over up to kMaxMats equal matrices of the flat
+// buffer: g = rank-order sum x 1/N x clip, mom = mu mom + g, update = nesterov
+// ? g + mu mom : mom (fp32, [mat][numel]), and the norm partials of the update.
+struct MomentumArgs {
+  int n_ranks, grad_fp32, nesterov, mats;
+  float inv_n, mu;
+  const float* clip;
+  unsigned long long* nonfinite;
+  const long long* dev_t;
+  long long dev_steps;
+  long long numel, chunks;
+  long long total_padded;
+  float* mom;               // exp_avg of the flat buffer
+  float* update;
+  double* partials;
+  long long offset[kMaxMats];
+  const void* g[kMaxMats][kMaxRanks];  // the matrix's gradients, replica by replica
+};
+cudaError_t launch_momentum(const MomentumArgs& a, bool vec, cudaStream_t stream);
+unsigned int muon_debug_failures();
+
+// ---- the products (zero_ns_gemm.cu) ----------------------------------------
+enum NsEpilogue {
+  kNsGram = 0,   // D symmetric: only tiles on and below the diagonal are computed, both halves stored
+  kNsPoly = 1,   // as kNsGram, D = a I + b C + c acc
+  kNsApply = 2,  // X' as a scaled fp16 pair (lo may be absent)
+  kNsOut = 3,    // the finished bf16 matrices
+  kNsMuon = 4    // the update of master and param16
+};
+
+struct GemmOperand {
+  const uint16_t* part[2] = {nullptr, nullptr};  // fp16 bits; the second part is added (hi + lo)
+  long long ld = 0, mat_stride = 0;              // elements
+  bool k_major = true;  // element (i, k) at i * ld + k; else at k * ld + i
+};
+
+struct GemmArgs {
+  long long M = 0, N = 0, K = 0;
+  int mats = 0;
+  GemmOperand a, b;
+  int parts = 1;             // 2: sum over (a.part[p], b.part[p])
+  int epilogue = kNsGram;
+  float alpha = 1.0f;        // power of two that undoes the operands' scales
+  float out_scale = 1.0f;    // power of two of the stored values
+  float ca = 0.0f, cb = 0.0f, cc = 0.0f;  // kNsPoly (cb already undoes C's scale)
+  const uint16_t* c = nullptr;            // kNsPoly: the Gram matrix, laid out as d
+  uint16_t* d = nullptr;
+  uint16_t* d_lo = nullptr;
+  long long ldd = 0, d_mat_stride = 0;
+  NsOut out;
+};
+cudaError_t launch_ns_gemm(const GemmArgs& g, cudaStream_t stream, int* launches);
+unsigned int ns_gemm_debug_failures();
+
+}  // namespace zfs

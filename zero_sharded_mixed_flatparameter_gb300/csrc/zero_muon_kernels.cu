@@ -1,0 +1,259 @@
+// Elementwise passes around the Newton-Schulz orthogonalisation: the Muon
+// momentum pass over the flat buffer, the Frobenius norm of a stack of
+// matrices, and its normalisation into scaled fp16 pairs.
+//
+// All are one pass over memory-resident data and bound by it; the norm is
+// summed per chunk of kNsChunk elements of a matrix, in fp32 over the 64
+// elements of one thread and in fp64 above, each in a fixed order.
+
+#include <cuda_fp16.h>
+
+#include "zero_device.cuh"
+#include "zero_muon_internal.h"
+
+namespace zfs {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPerThread = static_cast<int>(kNsChunk) / kThreads;  // elements per thread and chunk
+static_assert(kPerThread % kVec == 0, "whole vectors per thread");
+
+// Sum over the CTA in a fixed order; valid in thread 0.
+__device__ __forceinline__ double block_sum(double x) {
+  __shared__ double warp_sum[kThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_down_sync(0xffffffffu, x, o);
+  if (threadIdx.x % 32 == 0) warp_sum[threadIdx.x / 32] = x;
+  __syncthreads();
+  double s = 0.0;
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) s += warp_sum[w];
+  }
+  return s;
+}
+
+// Eight consecutive values from element `at` of a bf16 or fp32 array; kVecOk:
+// the address is 16-byte aligned and all eight exist.
+template <bool kFp32, bool kVecOk>
+__device__ __forceinline__ void load8(const void* base, long long at, int count, float* x) {
+  if constexpr (kVecOk) {
+    if constexpr (kFp32) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+      const float4 u = p[0], v = p[1];
+      x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+      x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+    } else {
+      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[2 * k] = bf16_lo(w[k]);
+        x[2 * k + 1] = bf16_hi(w[k]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      x[k] = 0.0f;
+      if (k < count) {
+        if constexpr (kFp32) {
+          x[k] = static_cast<const float*>(base)[at + k];
+        } else {
+          x[k] = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[at + k]) << 16);
+        }
+      }
+    }
+  }
+}
+
+// One chunk of one matrix per CTA (grid: chunk, matrix).  A thread's vectors
+// are kThreads vectors apart, so a warp reads contiguous runs.
+template <bool kFp32, bool kVecOk>
+__global__ void __launch_bounds__(kThreads) momentum_kernel(const __grid_constant__ MomentumArgs a) {
+  if (a.dev_t && *a.dev_t >= a.dev_steps) return;  // capturable: past the captured steps' table
+  const int mat = blockIdx.y;
+  const float clip = a.clip ? *a.clip : 1.0f;
+  const long long base = a.offset[mat];
+  unsigned nf = 0;
+  float sq = 0.0f;
+#pragma unroll 2
+  for (int i = 0; i < kPerThread / kVec; ++i) {
+    const long long e = blockIdx.x * kNsChunk + (static_cast<long long>(i) * kThreads + threadIdx.x) * kVec;
+    if (e >= a.numel) continue;
+    const int count = static_cast<int>(a.numel - e < kVec ? a.numel - e : kVec);
+    if (!ZFS_CHECK(base >= 0 && base + e + count <= a.total_padded)) continue;
+    float g[kVec], x[kVec], m[kVec];
+    load8<kFp32, kVecOk>(a.g[mat][0], e, count, g);
+    for (int r = 1; r < a.n_ranks; ++r) {
+      load8<kFp32, kVecOk>(a.g[mat][r], e, count, x);
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) g[k] = __fadd_rn(g[k], x[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) g[k] = __fmul_rn(g[k], a.inv_n);
+    nf += tally_nonfinite<kVec>(g);
+    load8<true, kVecOk>(a.mom, base + e, count, m);
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      if (a.clip) g[k] = __fmul_rn(g[k], clip);
+      m[k] = __fadd_rn(__fmul_rn(a.mu, m[k]), g[k]);
+      x[k] = a.nesterov ? __fadd_rn(g[k], __fmul_rn(a.mu, m[k])) : m[k];
+      sq += x[k] * x[k];
+    }
+    float* mom = a.mom + base + e;
+    float* upd = a.update + mat * a.numel + e;
+    if constexpr (kVecOk) {
+      reinterpret_cast<float4*>(mom)[0] = make_float4(m[0], m[1], m[2], m[3]);
+      reinterpret_cast<float4*>(mom)[1] = make_float4(m[4], m[5], m[6], m[7]);
+      reinterpret_cast<float4*>(upd)[0] = make_float4(x[0], x[1], x[2], x[3]);
+      reinterpret_cast<float4*>(upd)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kVec; ++k) {
+        if (k < count) {
+          mom[k] = m[k];
+          upd[k] = x[k];
+        }
+      }
+    }
+  }
+  flush_nonfinite(a.nonfinite, nf);
+  const double s = block_sum(static_cast<double>(sq));
+  if (threadIdx.x == 0) a.partials[mat * a.chunks + blockIdx.x] = s;
+}
+
+// Eight consecutive elements of the stack in logical (row-major) order.
+template <bool kFp32, bool kVecOk>
+__device__ __forceinline__ void load_logical(const MatSource& s, int mat, long long cols, long long e, int count,
+                                             float* x) {
+  const long long row = e / cols, col = e - row * cols;
+  if (col + count <= cols) {
+    load8<kFp32, kVecOk>(s.data, mat * s.mat_stride + row * s.row_stride + col, count, x);
+  } else {
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      x[k] = 0.0f;
+      if (k < count) {
+        const long long r = (e + k) / cols, c = (e + k) - r * cols;
+        float one[8];
+        load8<kFp32, false>(s.data, mat * s.mat_stride + r * s.row_stride + c, 1, one);
+        x[k] = one[0];
+      }
+    }
+  }
+}
+
+template <bool kFp32, bool kVecOk>
+__global__ void __launch_bounds__(kThreads)
+    ns_norm_kernel(const MatSource s, long long cols, long long numel, long long chunks, double* partials) {
+  const int mat = blockIdx.y;
+  float sq = 0.0f;
+#pragma unroll 2
+  for (int i = 0; i < kPerThread / kVec; ++i) {
+    const long long e = blockIdx.x * kNsChunk + (static_cast<long long>(i) * kThreads + threadIdx.x) * kVec;
+    if (e >= numel) continue;
+    const int count = static_cast<int>(numel - e < kVec ? numel - e : kVec);
+    float x[kVec];
+    load_logical<kFp32, kVecOk>(s, mat, cols, e, count, x);
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) sq += x[k] * x[k];
+  }
+  const double sum = block_sum(static_cast<double>(sq));
+  if (threadIdx.x == 0) partials[mat * chunks + blockIdx.x] = sum;
+}
+
+// X0 = source / (norm + eps), stored as hi + lo: hi the nearest fp16 of the
+// scaled value, lo the nearest fp16 of what hi leaves (22 bits together).
+// Pads up to the pitch are zero.  Grid: (blocks over rows x pitch / 8, matrix).
+template <bool kFp32, bool kVecOk>
+__global__ void __launch_bounds__(kThreads) ns_scale_kernel(const __grid_constant__ ScaleArgs a) {
+  __shared__ float inv_shared;
+  const int mat = blockIdx.y;
+  // every CTA sums the matrix's partials, in the same order
+  double s = 0.0;
+  for (long long k = threadIdx.x; k < a.chunks; k += kThreads) s += a.partials[mat * a.chunks + k];
+  s = block_sum(s);
+  if (threadIdx.x == 0) inv_shared = static_cast<float>(1.0 / (sqrt(s) + a.eps));
+  __syncthreads();
+  const float inv = inv_shared;
+  const long long vecs_per_row = a.ldx / kVec, total = a.rows * vecs_per_row;
+  for (long long v = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; v < total;
+       v += static_cast<long long>(gridDim.x) * kThreads) {
+    const long long row = v / vecs_per_row, col = (v - row * vecs_per_row) * kVec;
+    const long long left = a.cols - col;
+    const int count = static_cast<int>(left < 0 ? 0 : left < kVec ? left : kVec);
+    float x[kVec];
+    const long long at = mat * a.src.mat_stride + row * a.src.row_stride + col;
+    if (kVecOk && count == kVec) {
+      load8<kFp32, kVecOk>(a.src.data, at, count, x);
+    } else {
+      load8<kFp32, false>(a.src.data, at, count, x);
+    }
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float u = x[2 * k] * inv * a.scale, w = x[2 * k + 1] * inv * a.scale;
+      const __half2 h = __floats2half2_rn(u, w);
+      const __half2 l = __floats2half2_rn(u - __low2float(h), w - __high2float(h));
+      hi[k] = *reinterpret_cast<const uint32_t*>(&h);
+      lo[k] = *reinterpret_cast<const uint32_t*>(&l);
+    }
+    const long long to = (mat * a.rows + row) * a.ldx + col;
+    *reinterpret_cast<uint4*>(a.hi + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    if (a.lo) *reinterpret_cast<uint4*>(a.lo + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_momentum(const MomentumArgs& a, bool vec, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.mats));
+  if (a.grad_fp32) {
+    if (vec) momentum_kernel<true, true><<<grid, kThreads, 0, stream>>>(a);
+    else momentum_kernel<true, false><<<grid, kThreads, 0, stream>>>(a);
+  } else {
+    if (vec) momentum_kernel<false, true><<<grid, kThreads, 0, stream>>>(a);
+    else momentum_kernel<false, false><<<grid, kThreads, 0, stream>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_ns_norm(const MatSource& s, const NsPlan& p, int mats, double* partials, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(p.chunks), static_cast<unsigned>(mats));
+  const long long numel = p.rows * p.cols;
+  if (s.fp32) {
+    if (s.vec_ok) ns_norm_kernel<true, true><<<grid, kThreads, 0, stream>>>(s, p.cols, numel, p.chunks, partials);
+    else ns_norm_kernel<true, false><<<grid, kThreads, 0, stream>>>(s, p.cols, numel, p.chunks, partials);
+  } else {
+    if (s.vec_ok) ns_norm_kernel<false, true><<<grid, kThreads, 0, stream>>>(s, p.cols, numel, p.chunks, partials);
+    else ns_norm_kernel<false, false><<<grid, kThreads, 0, stream>>>(s, p.cols, numel, p.chunks, partials);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_ns_scale(const ScaleArgs& a, cudaStream_t stream) {
+  const long long work = a.rows * (a.ldx / kVec);
+  const long long want = (work + kThreads - 1) / kThreads, most = 8LL * sm_count() / a.mats + 1;
+  const dim3 grid(static_cast<unsigned>(want < most ? want : most), static_cast<unsigned>(a.mats));
+  if (a.src.fp32) {
+    if (a.src.vec_ok) ns_scale_kernel<true, true><<<grid, kThreads, 0, stream>>>(a);
+    else ns_scale_kernel<true, false><<<grid, kThreads, 0, stream>>>(a);
+  } else {
+    if (a.src.vec_ok) ns_scale_kernel<false, true><<<grid, kThreads, 0, stream>>>(a);
+    else ns_scale_kernel<false, false><<<grid, kThreads, 0, stream>>>(a);
+  }
+  return cudaGetLastError();
+}
+
+unsigned int muon_debug_failures() {
+#ifdef ZFS_DEBUG_CHECKS
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_debug_failures, sizeof v) != cudaSuccess) return 0xFFFFFFFFu;
+  return v;
+#else
+  return 0;
+#endif
+}
+
+}  // namespace zfs

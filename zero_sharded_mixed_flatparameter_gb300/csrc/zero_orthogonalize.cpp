@@ -1,0 +1,344 @@
+// Newton-Schulz orthogonalisation of a stack of matrices: the host side.  It
+// lays out the workspace, chooses the power-of-two scales of the fp16
+// operands and enqueues the products; zero_orthogonalize is the public call,
+// ns_run is shared with the Muon step (zero_runtime.cpp).
+//
+//   X0 = G / (|G|_F + eps)
+//   A = X X^T,  P = a I + b A + c A A,  X <- P X      (steps times)
+//
+// with the products over the smaller side of G (X^T X and X P for a tall G):
+// an odd polynomial of the singular values, whose vectors stay.  With the
+// customary (3.4445, -4.7750, 2.0315) five steps bring every singular value
+// that is not tiny to about 1.
+
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+
+#include <cuda_runtime.h>
+
+#include "zero_flatstep.h"
+#include "zero_muon_internal.h"
+
+namespace zfs {
+namespace {
+
+long long round_up(long long x, long long to) { return (x + to - 1) / to * to; }
+
+// Largest |p(s)| = |a s + b s^3 + c s^5| over 0 <= s <= top: at the end or
+// where the derivative, a quadratic in s^2, vanishes.
+double largest_value(double a, double b, double c, double top) {
+  auto p = [&](double s) { return std::fabs(s * (a + s * s * (b + s * s * c))); };
+  double best = p(top);
+  const double disc = 9.0 * b * b - 20.0 * a * c;
+  double roots[2] = {-1.0, -1.0};
+  if (c != 0.0) {
+    if (disc >= 0.0) {
+      roots[0] = (-3.0 * b + std::sqrt(disc)) / (10.0 * c);
+      roots[1] = (-3.0 * b - std::sqrt(disc)) / (10.0 * c);
+    }
+  } else if (b != 0.0) {
+    roots[0] = -a / (3.0 * b);
+  }
+  for (double t : roots)
+    if (t > 0.0 && t < top * top) best = std::max(best, p(std::sqrt(t)));
+  return best;
+}
+
+// Largest |a + b t + c t^2| over 0 <= t <= top.
+double largest_factor(double a, double b, double c, double top) {
+  auto q = [&](double t) { return std::fabs(a + t * (b + t * c)); };
+  double best = std::max(q(0.0), q(top));
+  if (c != 0.0) {
+    const double t = -b / (2.0 * c);
+    if (t > 0.0 && t < top) best = std::max(best, q(t));
+  }
+  return best;
+}
+
+// The power of two that brings entries of a matrix of spectral norm `bound`
+// (no entry is larger) to 2^14..2^15, half of what fp16 holds: 11 bits for
+// every entry down to 2^-29 of the bound.
+int scale_exponent(double bound) { return 15 - static_cast<int>(std::ceil(std::log2(std::max(bound, 1e-6) * 1.05))); }
+
+constexpr double kLargestIterate = 1024.0;
+
+// Steps whose X keeps its low half.  Noise that rounding puts into X at step k
+// passes steps - k further polynomials, each of which multiplies the small
+// singular values by up to a (3.4): with fp16 alone a rank-1 matrix ends
+// 1.5e-1 off after five steps (bf16: 1.2), with the low half kept until two
+// polynomials are left 3.4e-3, and a Gaussian one 1.1e-3 either way.
+int low_steps(int steps) { return std::max(steps - 2, 0); }
+
+}  // namespace
+
+bool ns_config_ok(const zero_ns_config& cfg, const char** why) {
+  if (cfg.steps < 1 || cfg.steps > 32) {
+    *why = "steps not in 1..32";
+    return false;
+  }
+  if (!std::isfinite(cfg.a) || !std::isfinite(cfg.b) || !std::isfinite(cfg.c)) {
+    *why = "coefficients must be finite";
+    return false;
+  }
+  if (!std::isfinite(cfg.eps) || cfg.eps < 0.0f) {
+    *why = "eps must be finite and >= 0";
+    return false;
+  }
+  double top = 1.0;
+  for (int k = 0; k < cfg.steps; ++k) {
+    top = largest_value(cfg.a, cfg.b, cfg.c, top);
+    if (!(top <= kLargestIterate)) {
+      *why = "the coefficients let the iterates grow beyond 1024";
+      return false;
+    }
+  }
+  return true;
+}
+
+int ns_mats(long long rows, long long cols, long long batch) {
+  const long long room = (1LL << 27) / std::max<long long>(rows * cols, 1);
+  return static_cast<int>(std::max<long long>(1, std::min<long long>({batch, room, kMaxMats})));
+}
+
+NsPlan ns_plan(long long rows, long long cols, int mats, bool keep_update) {
+  NsPlan p;
+  p.rows = rows;
+  p.cols = cols;
+  p.tall = rows > cols;
+  p.m = std::min(rows, cols);
+  p.n = std::max(rows, cols);
+  p.mats = mats;
+  p.ldx = round_up(cols, kVec);
+  p.ldm = round_up(p.m, kVec);
+  p.chunks = (rows * cols + kNsChunk - 1) / kNsChunk;
+  long long at = 0;
+  auto take = [&](long long bytes) {
+    const long long here = at;
+    at = round_up(at + bytes, 256);
+    return here;
+  };
+  p.partials = take(8 * p.chunks * mats);
+  for (int k = 0; k < 2; ++k) {
+    p.x_hi[k] = take(2 * p.ldx * rows * mats);
+    p.x_lo[k] = take(2 * p.ldx * rows * mats);
+  }
+  p.gram = take(2 * p.ldm * p.m * mats);
+  p.poly = take(2 * p.ldm * p.m * mats);
+  if (keep_update) p.update = take(4 * rows * cols * mats);
+  p.bytes = at;
+  return p;
+}
+
+cudaError_t ns_run(const NsPlan& p, const zero_ns_config& cfg, int mats, const MatSource& src, char* ws,
+                   const NsOut& out, cudaStream_t stream, int* launches) {
+  auto half = [&](long long at) { return reinterpret_cast<uint16_t*>(ws + at); };
+  const int lows = low_steps(cfg.steps);
+  double top = 1.0;  // bound of the spectral norm of X
+  int ex = scale_exponent(top);
+  ScaleArgs s{};
+  s.src = src;
+  s.rows = p.rows;
+  s.cols = p.cols;
+  s.ldx = p.ldx;
+  s.mats = mats;
+  s.chunks = p.chunks;
+  s.partials = reinterpret_cast<const double*>(ws + p.partials);
+  s.eps = cfg.eps;
+  s.scale = std::ldexp(1.0f, ex);
+  s.hi = half(p.x_hi[0]);
+  s.lo = lows > 0 ? half(p.x_lo[0]) : nullptr;
+  cudaError_t e = launch_ns_scale(s, stream);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  const long long x_stride = p.rows * p.ldx, m_stride = p.m * p.ldm;
+  for (int k = 0; k < cfg.steps; ++k) {
+    const int from = k % 2, to = 1 - from;
+    const bool low = k < lows, last = k + 1 == cfg.steps;
+    const int ea = scale_exponent(top * top);
+    const int ep = scale_exponent(largest_factor(cfg.a, cfg.b, cfg.c, top * top));
+    const double next = largest_value(cfg.a, cfg.b, cfg.c, top);
+    const int en = scale_exponent(next);
+    GemmOperand x;
+    x.part[0] = half(p.x_hi[from]);
+    x.part[1] = low ? half(p.x_lo[from]) : nullptr;
+    x.ld = p.ldx;
+    x.mat_stride = x_stride;
+    GemmOperand sq;
+    sq.ld = p.ldm;
+    sq.mat_stride = m_stride;
+    sq.k_major = true;
+
+    GemmArgs gram{};
+    gram.M = gram.N = p.m;
+    gram.K = p.n;
+    gram.mats = mats;
+    gram.a = gram.b = x;
+    gram.a.k_major = gram.b.k_major = !p.tall;
+    gram.epilogue = kNsGram;
+    gram.alpha = std::ldexp(1.0f, -2 * ex);
+    gram.out_scale = std::ldexp(1.0f, ea);
+    gram.d = half(p.gram);
+    gram.ldd = p.ldm;
+    gram.d_mat_stride = m_stride;
+    e = launch_ns_gemm(gram, stream, launches);
+    if (e != cudaSuccess) return e;
+
+    GemmArgs poly{};
+    poly.M = poly.N = poly.K = p.m;
+    poly.mats = mats;
+    poly.a = poly.b = sq;
+    poly.a.part[0] = poly.b.part[0] = half(p.gram);
+    poly.epilogue = kNsPoly;
+    poly.alpha = std::ldexp(1.0f, -2 * ea);
+    poly.out_scale = std::ldexp(1.0f, ep);
+    poly.ca = cfg.a;
+    poly.cb = cfg.b * std::ldexp(1.0f, -ea);
+    poly.cc = cfg.c;
+    poly.c = half(p.gram);
+    poly.d = half(p.poly);
+    poly.ldd = p.ldm;
+    poly.d_mat_stride = m_stride;
+    e = launch_ns_gemm(poly, stream, launches);
+    if (e != cudaSuccess) return e;
+
+    GemmArgs apply{};
+    apply.M = p.rows;
+    apply.N = p.cols;
+    apply.K = p.m;
+    apply.mats = mats;
+    apply.parts = low ? 2 : 1;
+    sq.part[0] = sq.part[1] = half(p.poly);
+    if (p.tall) {  // X' = X P, P symmetric
+      apply.a = x;
+      apply.a.k_major = true;
+      apply.b = sq;
+    } else {       // X' = P X
+      apply.a = sq;
+      apply.b = x;
+      apply.b.k_major = false;
+    }
+    apply.alpha = std::ldexp(1.0f, -ex - ep);
+    if (last) {
+      apply.epilogue = out.out ? kNsOut : kNsMuon;
+      apply.out = out;
+    } else {
+      apply.epilogue = kNsApply;
+      apply.out_scale = std::ldexp(1.0f, en);
+      apply.d = half(p.x_hi[to]);
+      apply.d_lo = k + 1 < lows ? half(p.x_lo[to]) : nullptr;
+      apply.ldd = p.ldx;
+      apply.d_mat_stride = x_stride;
+    }
+    e = launch_ns_gemm(apply, stream, launches);
+    if (e != cudaSuccess) return e;
+    top = next;
+    ex = en;
+  }
+  return cudaSuccess;
+}
+
+namespace {
+
+zero_status report(zero_status st, const char* fmt, long long x = 0, long long y = 0) {
+  char buf[256];
+  std::snprintf(buf, sizeof buf, fmt, x, y);
+  zfs_report_error(nullptr, st, buf);
+  return st;
+}
+
+zero_status check_shape(const zero_ns_config* cfg, int64_t rows, int64_t cols, int64_t batch) {
+  if (!cfg) return report(ZERO_EINVAL, "config is NULL");
+  const char* why = nullptr;
+  if (!ns_config_ok(*cfg, &why)) return report(ZERO_EINVAL, why);
+  if (rows < 0 || cols < 0 || batch < 0) return report(ZERO_EINVAL, "rows, cols and batch must not be negative");
+  if (rows > (1LL << 30) || cols > (1LL << 30) || (cols > 0 && rows > (1LL << 40) / cols))
+    return report(ZERO_EINVAL, "a matrix of %lld x %lld is too large", rows, cols);
+  return ZERO_OK;
+}
+
+bool on_device(const void* p, int device) {
+  cudaPointerAttributes attr{};
+  if (cudaPointerGetAttributes(&attr, p) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return (attr.type == cudaMemoryTypeDevice || attr.type == cudaMemoryTypeManaged) && attr.device == device;
+}
+
+bool misaligned(const void* p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a != 0; }
+
+}  // namespace
+}  // namespace zfs
+
+extern "C" {
+
+zero_status zero_orthogonalize_workspace_bytes(const zero_ns_config* cfg, int64_t rows, int64_t cols, int64_t batch,
+                                               int64_t* bytes) {
+  if (!bytes) return zfs::report(ZERO_EINVAL, "bytes is NULL");
+  const zero_status st = zfs::check_shape(cfg, rows, cols, batch);
+  if (st != ZERO_OK) return st;
+  *bytes = rows == 0 || cols == 0 || batch == 0
+               ? 0
+               : zfs::ns_plan(rows, cols, zfs::ns_mats(rows, cols, batch), false).bytes;
+  return ZERO_OK;
+}
+
+zero_status zero_orthogonalize(const zero_ns_config* cfg, int64_t rows, int64_t cols, int64_t batch, const void* in,
+                               int32_t in_dtype, int64_t in_row_stride, int64_t in_batch_stride, void* out,
+                               int64_t out_row_stride, int64_t out_batch_stride, void* workspace,
+                               int64_t workspace_bytes, void* stream) {
+  zero_status st = zfs::check_shape(cfg, rows, cols, batch);
+  if (st != ZERO_OK) return st;
+  if (in_dtype != ZERO_GRAD_BF16 && in_dtype != ZERO_GRAD_FP32)
+    return zfs::report(ZERO_EINVAL, "in_dtype %lld is neither bf16 (0) nor fp32 (1)", in_dtype);
+  if (rows == 0 || cols == 0 || batch == 0) return ZERO_OK;
+  if (in_row_stride < cols || out_row_stride < cols)
+    return zfs::report(ZERO_EINVAL, "a row stride is below the %lld columns", cols);
+  if (in_batch_stride < 0 || out_batch_stride < 0) return zfs::report(ZERO_EINVAL, "a batch stride is negative");
+  if (batch > 1 && out_batch_stride < (rows - 1) * out_row_stride + cols)
+    return zfs::report(ZERO_EINVAL, "out's batch stride makes its matrices overlap");
+  const int esz = in_dtype == ZERO_GRAD_FP32 ? 4 : 2;
+  int dev = -1;
+  const cudaError_t got = cudaGetDevice(&dev);
+  if (got != cudaSuccess) return zfs::report(ZERO_ECUDA, "no CUDA device");
+  if (!in || zfs::misaligned(in, esz) || !zfs::on_device(in, dev))
+    return zfs::report(ZERO_EINVAL, "in must be aligned memory of the current device");
+  if (!out || zfs::misaligned(out, 2) || !zfs::on_device(out, dev))
+    return zfs::report(ZERO_EINVAL, "out must be aligned memory of the current device");
+  const int mats = zfs::ns_mats(rows, cols, batch);
+  const zfs::NsPlan p = zfs::ns_plan(rows, cols, mats, false);
+  if (!workspace || zfs::misaligned(workspace, 256) || !zfs::on_device(workspace, dev))
+    return zfs::report(ZERO_EINVAL, "workspace must be 256-byte aligned memory of the current device");
+  if (workspace_bytes < p.bytes)
+    return zfs::report(ZERO_EINVAL, "workspace has %lld bytes, %lld needed", workspace_bytes, p.bytes);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  int launches = 0;
+  for (int64_t first = 0; first < batch; first += mats) {
+    const int count = static_cast<int>(std::min<int64_t>(mats, batch - first));
+    zfs::MatSource src{};
+    src.data = static_cast<const char*>(in) + first * in_batch_stride * esz;
+    src.fp32 = in_dtype == ZERO_GRAD_FP32 ? 1 : 0;
+    src.row_stride = in_row_stride;
+    src.mat_stride = in_batch_stride;
+    src.vec_ok = cols % zfs::kVec == 0 && in_row_stride % zfs::kVec == 0 && in_batch_stride % zfs::kVec == 0 &&
+                 !zfs::misaligned(src.data, 16);
+    zfs::NsOut o;
+    o.out = static_cast<uint16_t*>(out) + first * out_batch_stride;
+    o.row_stride = out_row_stride;
+    o.mat_stride = out_batch_stride;
+    cudaError_t e = zfs::launch_ns_norm(src, p, count, reinterpret_cast<double*>(ws + p.partials), s);
+    if (e == cudaSuccess) e = zfs::ns_run(p, *cfg, count, src, ws, o, s, &launches);
+    if (e != cudaSuccess) {
+      char buf[256];
+      std::snprintf(buf, sizeof buf, "orthogonalize launch: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
+      zfs_report_error(nullptr, ZERO_ECUDA, buf);
+      return ZERO_ECUDA;
+    }
+  }
+  return ZERO_OK;
+}
+
+}  // extern "C"

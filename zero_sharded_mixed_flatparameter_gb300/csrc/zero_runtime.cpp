@@ -21,6 +21,7 @@
 #include <memory>
 #include <mutex>
 #include <thread>
+#include <utility>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -36,6 +37,8 @@
 #include "zero_aux_internal.h"
 #include "zero_host.h"
 #include "zero_internal.h"
+#include "zero_muon_internal.h"
+#include "zero_qk_internal.h"
 
 namespace {
 
@@ -50,7 +53,8 @@ struct zero_ctx {
   int32_t n_units = 0;
   int32_t n_params = 0;
   int64_t shards = 1;  // F
-  std::vector<int64_t> unit_numel, unit_padded, unit_shard, unit_base, param_offset;
+  std::vector<int64_t> unit_numel, unit_padded, unit_shard, unit_base, param_offset, param_numel;
+  std::vector<int32_t> param_unit;
   int64_t padded_total = 0;
   int64_t numel_total = 0;
 
@@ -88,6 +92,18 @@ struct zero_ctx {
   long long* cap_t = nullptr;
   float* cap_bias = nullptr;
   int64_t cap_steps = 0;
+
+  // Muon: matrices of equal shape together, and the flat ranges that the Adam
+  // step leaves out, in flat order.
+  struct MuonGroup {
+    int64_t rows, cols;
+    std::vector<int32_t> params;
+  };
+  bool muon = false;
+  zero_muon_config muon_cfg{};
+  std::vector<MuonGroup> muon_groups;
+  std::vector<std::pair<int64_t, int64_t>> muon_ranges;  // (offset, elements)
+  char* muon_ws = nullptr;
 
   std::string error;
 
@@ -161,6 +177,8 @@ zero_status plan_layout(zero_ctx* ctx, const int64_t* param_numel, const int32_t
   ctx->unit_shard.assign(n_units, 0);
   ctx->unit_base.assign(n_units, 0);
   ctx->param_offset.assign(n_params, 0);
+  ctx->param_numel.assign(param_numel, param_numel + n_params);
+  ctx->param_unit.assign(param_unit, param_unit + n_params);
   for (int32_t p = 0; p < n_params; ++p) {
     const int64_t before = ctx->unit_numel[param_unit[p]];
     if (before > INT64_MAX / 4 - param_numel[p]) return fail(nullptr, ZERO_EINVAL, "parameter sizes overflow");
@@ -293,6 +311,33 @@ std::vector<PlannedSeg> build_segments(const zero_ctx* ctx) {
   return out;
 }
 
+// What is left of the segments without `ranges` (sorted, disjoint).
+std::vector<PlannedSeg> cut_segments(const std::vector<PlannedSeg>& segs,
+                                     const std::vector<std::pair<int64_t, int64_t>>& ranges, int readers, size_t esz) {
+  std::vector<PlannedSeg> out;
+  size_t k = 0;
+  for (const PlannedSeg& s : segs) {
+    const int64_t end = s.base + s.len;
+    int64_t at = s.base;
+    auto keep = [&](int64_t to) {
+      if (to <= at) return;
+      PlannedSeg piece = s;
+      piece.base = at;
+      piece.len = to - at;
+      for (int r = 0; r < readers; ++r)
+        piece.g[r] = static_cast<const char*>(s.g[r]) + (at - s.base) * static_cast<int64_t>(esz);
+      out.push_back(piece);
+    };
+    while (k < ranges.size() && ranges[k].first + ranges[k].second <= at) ++k;
+    for (size_t i = k; i < ranges.size() && ranges[i].first < end; ++i) {
+      keep(std::min(ranges[i].first, end));
+      at = std::max(at, ranges[i].first + ranges[i].second);
+    }
+    keep(end);
+  }
+  return out;
+}
+
 bool vector_ok(const PlannedSeg& s, int N) {
   if (s.base % zfs::kVec != 0) return false;
   for (int r = 0; r < N; ++r)
@@ -317,10 +362,12 @@ PlannedSeg peel(const PlannedSeg& s, int N, size_t esz) {
   return out;
 }
 
-// Launch one kernel per batch of up to kMaxSegs segments of one kind.
-zero_status launch_batches(zero_ctx* ctx, const std::vector<PlannedSeg>& segs, bool vec, int64_t t,
+// Launch one kernel per batch of up to kMaxSegs segments of one kind.  `kept`:
+// the segments read the reduced gradient a clip kept, one fp32 "replica" that
+// is already scaled by 1/N (x 1 below is exact).
+zero_status launch_batches(zero_ctx* ctx, const std::vector<PlannedSeg>& segs, bool vec, bool kept, int64_t t,
                            cudaStream_t stream, int32_t* launches) {
-  const int N = ctx->cfg.n_ranks;
+  const int N = kept ? 1 : ctx->cfg.n_ranks;
   size_t i = 0;
   while (i < segs.size()) {
     zfs::StepArgs a;
@@ -332,11 +379,16 @@ zero_status launch_batches(zero_ctx* ctx, const std::vector<PlannedSeg>& segs, b
     a.clip = ctx->clip_ws ? reinterpret_cast<const float*>(ctx->clip_ws + 8) : nullptr;
     a.nonfinite = ctx->nonfinite;
     fill_scalars(ctx, t, &a);
+    if (kept) {
+      a.inv_n = 1.0f;
+      a.n_ranks = 1;
+      a.grad_fp32 = 1;
+    }
     a.total_padded = ctx->padded_total;
     a.dev_t = ctx->cap_t;
     a.dev_bias = ctx->cap_bias;
     a.dev_steps = ctx->cap_steps;
-    if (ctx->inject == ZERO_INJECT_MISSING_COPY && vec) {
+    if (ctx->inject == ZERO_INJECT_MISSING_COPY && vec && !kept) {
       a.inject_missing_copy = 1;
       ctx->inject = 0;
     }
@@ -377,6 +429,83 @@ int64_t total_chunks(const zero_ctx* ctx) {
   int64_t n = 0;
   for (int32_t i = 0; i < ctx->n_units; ++i) n += unit_chunks(ctx, i);
   return n;
+}
+
+// The Muon part of a step: per shape, momentum and update, then the
+// orthogonalisation whose last product updates master and param16.
+zero_status muon_update(zero_ctx* ctx, cudaStream_t stream, int32_t* launches) {
+  const zero_muon_config& mc = ctx->muon_cfg;
+  const bool kept = ctx->clip_keep != nullptr;
+  const int N = kept ? 1 : ctx->cfg.n_ranks;
+  const int64_t esz = kept ? 4 : static_cast<int64_t>(grad_bytes(ctx->cfg));
+  const int64_t bound = ctx->padded_total - (ctx->inject == ZERO_INJECT_SHORT_BOUNDS ? zfs::kVec : 0);
+  for (const zero_ctx::MuonGroup& group : ctx->muon_groups) {
+    const int64_t numel = group.rows * group.cols;
+    const int most = zfs::ns_mats(group.rows, group.cols, static_cast<long long>(group.params.size()));
+    const zfs::NsPlan p = zfs::ns_plan(group.rows, group.cols, most, true);
+    double scale = 1.0;
+    if (mc.scale == ZERO_MUON_SCALE_RMS) {
+      scale = 0.2 * std::sqrt(static_cast<double>(std::max(group.rows, group.cols)));
+    } else {
+      scale = std::sqrt(std::max(1.0, static_cast<double>(group.rows) / static_cast<double>(group.cols)));
+    }
+    for (size_t first = 0; first < group.params.size(); first += most) {
+      const int mats = static_cast<int>(std::min<size_t>(most, group.params.size() - first));
+      zfs::MomentumArgs a;
+      std::memset(&a, 0, sizeof a);
+      zfs::NsOut out;
+      a.n_ranks = N;
+      a.grad_fp32 = kept || ctx->cfg.grad_dtype == ZERO_GRAD_FP32 ? 1 : 0;
+      a.nesterov = mc.nesterov;
+      a.mats = mats;
+      a.inv_n = 1.0f / static_cast<float>(N);
+      a.mu = mc.momentum;
+      a.clip = ctx->clip_ws ? reinterpret_cast<const float*>(ctx->clip_ws + 8) : nullptr;
+      a.nonfinite = ctx->nonfinite;
+      a.dev_t = ctx->cap_t;
+      a.dev_steps = ctx->cap_steps;
+      a.numel = numel;
+      a.chunks = p.chunks;
+      a.total_padded = bound;
+      a.mom = ctx->bufs.exp_avg;
+      a.update = reinterpret_cast<float*>(ctx->muon_ws + p.update);
+      a.partials = reinterpret_cast<double*>(ctx->muon_ws + p.partials);
+      bool vec = numel % zfs::kVec == 0;
+      for (int k = 0; k < mats; ++k) {
+        const int32_t param = group.params[first + k];
+        const int64_t off = ctx->param_offset[param];
+        const int32_t unit = ctx->param_unit[param];
+        a.offset[k] = out.offset[k] = off;
+        vec = vec && off % zfs::kVec == 0;
+        for (int r = 0; r < N; ++r) {
+          const char* base = kept ? reinterpret_cast<const char*>(ctx->clip_keep) + off * esz
+                                  : static_cast<const char*>(ctx->grads[static_cast<size_t>(unit) * zfs::kMaxRanks + r]) +
+                                        (off - ctx->unit_base[unit]) * esz;
+          a.g[k][r] = base;
+          vec = vec && aligned(base, 16);
+        }
+      }
+      cudaError_t e = zfs::launch_momentum(a, vec, stream);
+      if (e != cudaSuccess) return fail_cuda(ctx, "momentum kernel launch", e);
+      ++*launches;
+      zfs::MatSource src{};
+      src.data = a.update;
+      src.fp32 = 1;
+      src.row_stride = group.cols;
+      src.mat_stride = numel;
+      src.vec_ok = group.cols % zfs::kVec == 0 ? 1 : 0;
+      out.master = ctx->bufs.master;
+      out.p16 = static_cast<uint16_t*>(ctx->bufs.param16);
+      out.decay = static_cast<float>(1.0 - static_cast<double>(mc.lr) * static_cast<double>(mc.weight_decay));
+      out.step = static_cast<float>(static_cast<double>(mc.lr) * scale);
+      out.total_padded = bound;
+      out.dev_t = ctx->cap_t;
+      out.dev_steps = ctx->cap_steps;
+      e = zfs::ns_run(p, mc.ns, mats, src, ctx->muon_ws, out, stream, launches);
+      if (e != cudaSuccess) return fail_cuda(ctx, "orthogonalisation launch", e);
+    }
+  }
+  return ZERO_OK;
 }
 
 bool all_registered(const zero_ctx* ctx, int32_t* missing) {
@@ -736,53 +865,40 @@ zero_status zero_step(zero_ctx* ctx, void* stream) {
   const int64_t t = ctx->t + 1;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   int32_t launches = 0;
-  if (ctx->clip_keep) {
-    // The clip kept the reduced gradient: one fp32 "replica" over the whole
-    // padded buffer, already scaled by 1/N (x 1 below is exact).
-    if (ctx->padded_total > 0) {
-      zfs::StepArgs a;
-      std::memset(&a, 0, sizeof a);
-      a.master = ctx->bufs.master;
-      a.m = ctx->bufs.exp_avg;
-      a.v = ctx->bufs.exp_avg_sq;
-      a.p16 = static_cast<uint16_t*>(ctx->bufs.param16);
-      a.clip = reinterpret_cast<const float*>(ctx->clip_ws + 8);
-      a.nonfinite = ctx->nonfinite;
-      fill_scalars(ctx, t, &a);
-      a.total_padded = ctx->padded_total - (ctx->inject == ZERO_INJECT_SHORT_BOUNDS ? zfs::kVec : 0);
-      a.dev_t = ctx->cap_t;
-      a.dev_bias = ctx->cap_bias;
-      a.dev_steps = ctx->cap_steps;
-      a.inv_n = 1.0f;
-      a.n_ranks = 1;
-      a.grad_fp32 = 1;
-      a.nseg = 1;
-      a.seg[0].base = 0;
-      a.seg[0].len = ctx->padded_total;
-      a.seg[0].vec_start = 0;
-      a.seg[0].g[0] = ctx->clip_keep;
-      a.total_vec = ctx->padded_total / zfs::kVec;
-      a.total_elems = ctx->padded_total;
-      const cudaError_t e = zfs::launch_step_vec(a, s);
-      if (e != cudaSuccess) return fail_cuda(ctx, "step kernel launch", e);
-      launches = 1;
+  // With ZERO_CLIP_KEEP_REDUCED the clip kept the reduced gradient: one fp32
+  // segment over the whole padded buffer.  The matrices of a Muon context are
+  // cut out of the segments.
+  const bool kept = ctx->clip_keep != nullptr;
+  const int readers = kept ? 1 : ctx->cfg.n_ranks;
+  const size_t esz = kept ? 4 : grad_bytes(ctx->cfg);
+  std::vector<PlannedSeg> vec_segs, shift_segs;
+  try {
+    std::vector<PlannedSeg> segs;
+    if (!kept) {
+      segs = build_segments(ctx);
+    } else if (ctx->padded_total > 0) {
+      PlannedSeg whole{};
+      whole.len = ctx->padded_total;
+      whole.g[0] = ctx->clip_keep;
+      segs.push_back(whole);
     }
-  } else {
-    std::vector<PlannedSeg> vec_segs, shift_segs;
-    try {
-      for (const PlannedSeg& sg : build_segments(ctx)) {
-        if (vector_ok(sg, ctx->cfg.n_ranks)) {
-          vec_segs.push_back(sg);
-        } else {
-          shift_segs.push_back(peel(sg, ctx->cfg.n_ranks, grad_bytes(ctx->cfg)));
-        }
+    if (ctx->muon) segs = cut_segments(segs, ctx->muon_ranges, readers, esz);
+    for (const PlannedSeg& sg : segs) {
+      if (vector_ok(sg, readers)) {
+        vec_segs.push_back(sg);
+      } else {
+        shift_segs.push_back(peel(sg, readers, esz));
       }
-    } catch (const std::bad_alloc&) {
-      return fail(ctx, ZERO_ENOMEM, "cannot allocate segment list");
     }
-    st = launch_batches(ctx, vec_segs, true, t, s, &launches);
-    if (st != ZERO_OK) return st;
-    st = launch_batches(ctx, shift_segs, false, t, s, &launches);
+  } catch (const std::bad_alloc&) {
+    return fail(ctx, ZERO_ENOMEM, "cannot allocate segment list");
+  }
+  st = launch_batches(ctx, vec_segs, true, kept, t, s, &launches);
+  if (st != ZERO_OK) return st;
+  st = launch_batches(ctx, shift_segs, false, kept, t, s, &launches);
+  if (st != ZERO_OK) return st;
+  if (ctx->muon) {
+    st = muon_update(ctx, s, &launches);
     if (st != ZERO_OK) return st;
   }
   if (ctx->inject == ZERO_INJECT_SHORT_BOUNDS) ctx->inject = 0;
@@ -1338,9 +1454,14 @@ zero_status zero_import_state(zero_ctx* ctx, const float* master_in, const float
 zero_status zero_debug_check_failures(uint32_t* count) {
   if (!count) return fail(nullptr, ZERO_EINVAL, "count is NULL");
 #ifdef ZFS_DEBUG_CHECKS
-  const unsigned int a = zfs::step_debug_failures(), b = zfs::aux_debug_failures();
-  if (a == 0xFFFFFFFFu || b == 0xFFFFFFFFu) return fail(nullptr, ZERO_ECUDA, "cannot read the check counters");
-  *count = a + b;
+  const unsigned int counts[] = {zfs::step_debug_failures(), zfs::aux_debug_failures(), zfs::muon_debug_failures(),
+                                 zfs::ns_gemm_debug_failures(), zfs::qk_debug_failures()};
+  unsigned int sum = 0;
+  for (unsigned int c : counts) {
+    if (c == 0xFFFFFFFFu) return fail(nullptr, ZERO_ECUDA, "cannot read the check counters");
+    sum += c;
+  }
+  *count = sum;
   return ZERO_OK;
 #else
   *count = 0;
@@ -1493,6 +1614,119 @@ zero_status zero_set_lr(zero_ctx* ctx, float lr) {
   if (!ctx) return fail(nullptr, ZERO_EINVAL, "ctx is NULL");
   if (!std::isfinite(lr)) return fail(ctx, ZERO_EINVAL, "lr is not finite");
   ctx->cfg.lr = lr;
+  return ZERO_OK;
+}
+
+namespace {
+
+// The shapes of a Muon configuration as groups of equal matrices; ENOMEM by exception.
+zero_status muon_plan(zero_ctx* ctx, const zero_muon_config* cfg, const int64_t* rows, const int64_t* cols,
+                      int32_t n_params, std::vector<zero_ctx::MuonGroup>* groups,
+                      std::vector<std::pair<int64_t, int64_t>>* ranges, int64_t* bytes) {
+  if (!cfg) return fail(ctx, ZERO_EINVAL, "config is NULL");
+  if (n_params != ctx->n_params)
+    return fail(ctx, ZERO_EINVAL, "%d shapes for %d parameters", n_params, ctx->n_params);
+  if (n_params > 0 && (!rows || !cols)) return fail(ctx, ZERO_EINVAL, "rows / cols is NULL");
+  if (!std::isfinite(cfg->lr)) return fail(ctx, ZERO_EINVAL, "lr is not finite");
+  if (!(cfg->momentum >= 0.0f && cfg->momentum < 1.0f)) return fail(ctx, ZERO_EINVAL, "momentum not in [0, 1)");
+  if (!std::isfinite(cfg->weight_decay) || cfg->weight_decay < 0.0f)
+    return fail(ctx, ZERO_EINVAL, "weight_decay must be finite and >= 0");
+  if (cfg->nesterov != 0 && cfg->nesterov != 1) return fail(ctx, ZERO_EINVAL, "nesterov must be 0 or 1");
+  if (cfg->scale != ZERO_MUON_SCALE_RMS && cfg->scale != ZERO_MUON_SCALE_ASPECT)
+    return fail(ctx, ZERO_EINVAL, "unknown scale %d", cfg->scale);
+  const char* why = nullptr;
+  if (!zfs::ns_config_ok(cfg->ns, &why)) return fail(ctx, ZERO_EINVAL, "%s", why);
+  for (int32_t p = 0; p < n_params; ++p) {
+    const int64_t r = rows[p], c = cols[p];
+    if (r == 0 && c == 0) continue;  // stays with Adam
+    if (r < 0 || c < 0 || (c > 0 && r > INT64_MAX / c) || r * c != ctx->param_numel[p])
+      return fail(ctx, ZERO_EINVAL, "param %d: %lld x %lld is not its %lld elements", p, static_cast<long long>(r),
+                  static_cast<long long>(c), static_cast<long long>(ctx->param_numel[p]));
+    if (r * c == 0) continue;
+    if (r > (1LL << 30) || c > (1LL << 30) || r * c > (1LL << 40))
+      return fail(ctx, ZERO_EINVAL, "param %d is too large for a matrix", p);
+    auto same = std::find_if(groups->begin(), groups->end(),
+                             [&](const zero_ctx::MuonGroup& g) { return g.rows == r && g.cols == c; });
+    if (same == groups->end()) {
+      groups->push_back({r, c, {}});
+      same = groups->end() - 1;
+    }
+    same->params.push_back(p);
+    ranges->push_back({ctx->param_offset[p], r * c});
+  }
+  *bytes = 0;
+  for (const zero_ctx::MuonGroup& g : *groups) {
+    const int mats = zfs::ns_mats(g.rows, g.cols, static_cast<long long>(g.params.size()));
+    *bytes = std::max<int64_t>(*bytes, zfs::ns_plan(g.rows, g.cols, mats, true).bytes);
+  }
+  return ZERO_OK;
+}
+
+}  // namespace
+
+zero_status zero_muon_workspace_bytes(const zero_ctx* ctx, const zero_muon_config* cfg, const int64_t* rows,
+                                      const int64_t* cols, int32_t n_params, int64_t* bytes) {
+  if (!ctx || !bytes) return fail(const_cast<zero_ctx*>(ctx), ZERO_EINVAL, "NULL argument");
+  zero_ctx* c = const_cast<zero_ctx*>(ctx);
+  try {
+    std::vector<zero_ctx::MuonGroup> groups;
+    std::vector<std::pair<int64_t, int64_t>> ranges;
+    return muon_plan(c, cfg, rows, cols, n_params, &groups, &ranges, bytes);
+  } catch (const std::bad_alloc&) {
+    return fail(c, ZERO_ENOMEM, "cannot allocate the shape tables");
+  }
+}
+
+zero_status zero_enable_muon(zero_ctx* ctx, const zero_muon_config* cfg, const int64_t* rows, const int64_t* cols,
+                             int32_t n_params, void* workspace, int64_t workspace_bytes) {
+  if (!ctx) return fail(nullptr, ZERO_EINVAL, "ctx is NULL");
+  zero_status st = require_bound(ctx);
+  if (st != ZERO_OK) return st;
+  if (ctx->offload) return fail(ctx, ZERO_ENOTSUP, "Muon is not available in an offload context");
+  if (ctx->phase == Phase::kStepped) return fail(ctx, ZERO_ESTATE, "a step awaits post_step");
+  try {
+    std::vector<zero_ctx::MuonGroup> groups;
+    std::vector<std::pair<int64_t, int64_t>> ranges;
+    int64_t need = 0;
+    st = muon_plan(ctx, cfg, rows, cols, n_params, &groups, &ranges, &need);
+    if (st != ZERO_OK) return st;
+    if (need > 0) {
+      int wdev = -1;
+      if (!workspace || !aligned(workspace, 256))
+        return fail(ctx, ZERO_EINVAL, "workspace NULL or not 256-byte aligned");
+      if (workspace_bytes < need)
+        return fail(ctx, ZERO_EINVAL, "workspace has %lld bytes, %lld needed", static_cast<long long>(workspace_bytes),
+                    static_cast<long long>(need));
+      if (!is_device_pointer(workspace, &wdev) || wdev != ctx->device)
+        return fail(ctx, ZERO_EINVAL, "workspace is not memory of the context's device");
+    }
+    ctx->muon_groups.swap(groups);
+    ctx->muon_ranges.swap(ranges);
+  } catch (const std::bad_alloc&) {
+    return fail(ctx, ZERO_ENOMEM, "cannot allocate the shape tables");
+  }
+  ctx->muon_cfg = *cfg;
+  ctx->muon_ws = static_cast<char*>(workspace);
+  ctx->muon = true;
+  return ZERO_OK;
+}
+
+zero_status zero_disable_muon(zero_ctx* ctx) {
+  if (!ctx) return fail(nullptr, ZERO_EINVAL, "ctx is NULL");
+  if (!ctx->muon) return fail(ctx, ZERO_ESTATE, "Muon is not on");
+  if (ctx->phase == Phase::kStepped) return fail(ctx, ZERO_ESTATE, "a step awaits post_step");
+  ctx->muon = false;
+  ctx->muon_groups.clear();
+  ctx->muon_ranges.clear();
+  ctx->muon_ws = nullptr;
+  return ZERO_OK;
+}
+
+zero_status zero_set_muon_lr(zero_ctx* ctx, float lr) {
+  if (!ctx) return fail(nullptr, ZERO_EINVAL, "ctx is NULL");
+  if (!ctx->muon) return fail(ctx, ZERO_ESTATE, "Muon is not on");
+  if (!std::isfinite(lr)) return fail(ctx, ZERO_EINVAL, "lr is not finite");
+  ctx->muon_cfg.lr = lr;
   return ZERO_OK;
 }
 

@@ -1,0 +1,173 @@
+"""Operators on torch tensors around the Muon step: :func:`orthogonalize`,
+:func:`qk_norm_rope` and its gradients.
+
+Each is a thin call of the C function of the same name: checks, the output and
+workspace tensors, the current stream.  Tensors stay on one CUDA device; there
+is no CPU path.
+"""
+
+from __future__ import annotations
+
+from typing import Optional, Sequence, Tuple
+
+import torch
+
+from . import binding as B
+
+_DTYPES = {torch.bfloat16: B.ZERO_GRAD_BF16, torch.float32: B.ZERO_GRAD_FP32}
+
+
+def _stream(device: torch.device) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients: Sequence[float] = (3.4445, -4.7750, 2.0315),
+                  eps: float = 1e-7, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Newton-Schulz orthogonalisation of a matrix or a stack of matrices.
+
+    ``x``: bf16 or fp32, (rows, cols) or (batch, rows, cols), columns
+    contiguous.  Returns (or fills ``out``) bf16 of the same shape.
+    """
+    if x.dim() not in (2, 3) or x.dtype not in _DTYPES or not x.is_cuda:
+        raise ValueError("x must be a bf16 or fp32 CUDA matrix or a stack of them")
+    if x.size(-1) > 1 and x.stride(-1) != 1:
+        raise ValueError("the columns of x must be contiguous")
+    if out is None:
+        out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    elif out.shape != x.shape or out.dtype != torch.bfloat16 or out.device != x.device or (
+            out.size(-1) > 1 and out.stride(-1) != 1):
+        raise ValueError("out must be a bf16 tensor of x's shape and device with contiguous columns")
+    batch, rows, cols = (1, *x.shape) if x.dim() == 2 else x.shape
+    cfg = B.make_ns_config(steps, coefficients, eps)
+    with torch.cuda.device(x.device):
+        need = B.zero_orthogonalize_workspace_bytes(cfg, rows, cols, batch)
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        B.zero_orthogonalize(cfg, rows, cols, batch, x.data_ptr(), _DTYPES[x.dtype],
+                             x.stride(-2) if rows > 1 else max(cols, 1), x.stride(0) if batch > 1 else 0,
+                             out.data_ptr(), out.stride(-2) if rows > 1 else max(cols, 1),
+                             out.stride(0) if batch > 1 else 0, workspace.data_ptr(), need, _stream(x.device))
+    return out
+
+
+def _heads(x: torch.Tensor) -> B.zero_heads:
+    return B.zero_heads(x.data_ptr(), x.stride(0), x.stride(1))
+
+
+def _qk_config(q, k, q_gain, k_gain, table, positions, eps, interleaved) -> B.zero_qk_config:
+    for name, x in (("q", q), ("k", k)):
+        if x.dim() != 3 or x.dtype not in _DTYPES or not x.is_cuda or (x.size(2) > 1 and x.stride(2) != 1):
+            raise ValueError(f"{name} must be a bf16 or fp32 CUDA tensor (tokens, heads, head_dim) with contiguous "
+                             "head vectors")
+    if k.dtype != q.dtype or k.device != q.device or k.size(0) != q.size(0) or k.size(2) != q.size(2):
+        raise ValueError("q and k must agree in type, device, tokens and head_dim")
+    dim = q.size(2)
+    gain_dtype = torch.float32
+    for g in (q_gain, k_gain):
+        if g is None:
+            continue
+        gain_dtype = g.dtype
+        if g.dtype not in _DTYPES or g.shape != (dim,) or g.device != q.device or not g.is_contiguous():
+            raise ValueError("a gain must be a contiguous bf16 or fp32 vector of head_dim elements")
+    if q_gain is not None and k_gain is not None and q_gain.dtype != k_gain.dtype:
+        raise ValueError("the gains must have one type")
+    if table.dim() != 2 or table.dtype != torch.float32 or table.device != q.device or not table.is_contiguous():
+        raise ValueError("table must be a contiguous fp32 tensor (positions, rotary_dim)")
+    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (q.size(0),)
+                                  or positions.device != q.device or not positions.is_contiguous()):
+        raise ValueError("positions must be a contiguous int32 vector with one entry per token")
+    return B.zero_qk_config(q.size(1), k.size(1), dim, table.size(1), 1 if interleaved else 0, _DTYPES[q.dtype],
+                            _DTYPES[gain_dtype], eps, table.size(0))
+
+
+def _ptr(x: Optional[torch.Tensor]) -> int:
+    return x.data_ptr() if x is not None else 0
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_gain: Optional[torch.Tensor], k_gain: Optional[torch.Tensor],
+                 table: torch.Tensor, positions: Optional[torch.Tensor] = None, *, eps: float = 1e-6,
+                 interleaved: bool = False, out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None
+                 ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """RMS norm of every head of q and k (with its gain), then the rotation of
+    the token's position, in one pass.
+
+    ``q`` (tokens, heads, head_dim) and ``k`` (tokens, kv_heads, head_dim) may
+    be strided views of one projection's output.  ``table`` holds per position
+    the rotary_dim/2 cosines, then the sines; rotary_dim is its width.  A
+    position outside the table marks padding: zeros.  ``out`` may be (q, k).
+    """
+    cfg = _qk_config(q, k, q_gain, k_gain, table, positions, eps, interleaved)
+    if out is None:
+        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+               torch.empty(k.shape, dtype=k.dtype, device=k.device))
+    else:
+        _check_like(out, (q, k))
+    with torch.cuda.device(q.device):
+        B.zero_qk_norm_rope(cfg, q.size(0), _heads(q), _heads(k), _ptr(q_gain), _ptr(k_gain), table.data_ptr(),
+                            _ptr(positions), _heads(out[0]), _heads(out[1]), _stream(q.device))
+    return out
+
+
+def _check_like(got, want):
+    for g, w in zip(got, want):
+        if g.shape != w.shape or g.dtype != w.dtype or g.device != w.device or (g.size(2) > 1 and g.stride(2) != 1):
+            raise ValueError("an output or output gradient must match its input in shape, type and device")
+
+
+def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor, k: torch.Tensor,
+                          q_gain: Optional[torch.Tensor], k_gain: Optional[torch.Tensor], table: torch.Tensor,
+                          positions: Optional[torch.Tensor] = None, *, eps: float = 1e-6, interleaved: bool = False,
+                          out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None,
+                          gain_out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
+    """Gradients (dq, dk, dq_gain, dk_gain) of :func:`qk_norm_rope`'s inputs.
+
+    ``gain_out``: two vectors of head_dim elements, bf16 or fp32, to write the
+    gain gradients to, such as slices of a replica's flat gradient; new fp32
+    vectors otherwise.
+    """
+    cfg = _qk_config(q, k, q_gain, k_gain, table, positions, eps, interleaved)
+    _check_like((dq_out, dk_out), (q, k))
+    if out is None:
+        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+               torch.empty(k.shape, dtype=k.dtype, device=k.device))
+    else:
+        _check_like(out, (q, k))
+    dim = q.size(2)
+    if gain_out is None:
+        both = torch.empty((2, dim), dtype=torch.float32, device=q.device)
+        gain_out = (both[0], both[1])
+    else:
+        for g in gain_out:
+            if g.dtype not in _DTYPES or g.dtype != gain_out[0].dtype or g.shape != (dim,) or g.device != q.device \
+                    or not g.is_contiguous():
+                raise ValueError("gain_out must be two contiguous vectors of head_dim elements and one type")
+    with torch.cuda.device(q.device):
+        need = B.zero_qk_backward_workspace_bytes(cfg, q.size(0))
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        B.zero_qk_norm_rope_backward(cfg, q.size(0), _heads(dq_out), _heads(dk_out), _heads(q), _heads(k),
+                                     _ptr(q_gain), _ptr(k_gain), table.data_ptr(), _ptr(positions), _heads(out[0]),
+                                     _heads(out[1]), gain_out[0].data_ptr(), gain_out[1].data_ptr(),
+                                     _DTYPES[gain_out[0].dtype], workspace.data_ptr(), need, _stream(q.device))
+    return (*out, *gain_out)
+
+
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_gain, k_gain, table, positions, eps, interleaved):
+        ctx.save_for_backward(q, k, q_gain, k_gain, table, positions)
+        ctx.eps, ctx.interleaved = eps, interleaved
+        return qk_norm_rope(q, k, q_gain, k_gain, table, positions, eps=eps, interleaved=interleaved)
+
+    @staticmethod
+    def backward(ctx, dq_out, dk_out):
+        q, k, q_gain, k_gain, table, positions = ctx.saved_tensors
+        dq_out, dk_out = (d if d.stride(2) == 1 or d.size(2) == 1 else d.contiguous() for d in (dq_out, dk_out))
+        dq, dk, dq_gain, dk_gain = qk_norm_rope_backward(dq_out, dk_out, q, k, q_gain, k_gain, table, positions,
+                                                         eps=ctx.eps, interleaved=ctx.interleaved)
+        return (dq, dk, dq_gain.to(q_gain.dtype) if q_gain is not None else None,
+                dk_gain.to(k_gain.dtype) if k_gain is not None else None, None, None, None, None)
+
+
+def qk_norm_rope_autograd(q, k, q_gain, k_gain, table, positions=None, *, eps: float = 1e-6,
+                          interleaved: bool = False):
+    """:func:`qk_norm_rope` that records its gradients for torch.autograd."""
+    return _QkNormRope.apply(q, k, q_gain, k_gain, table, positions, eps, interleaved)

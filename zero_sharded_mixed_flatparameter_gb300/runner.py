@@ -250,6 +250,29 @@ class FlatStep:
         B.zero_disable_capturable(self.ctx, self.stream_handle(stream))
         self._cap_ws = None
 
+    def enable_muon(self, shapes: Sequence[Optional[Sequence[int]]], *, lr: float, momentum: float = 0.95,
+                    weight_decay: float = 0.0, nesterov: bool = True, scale: str = "rms", steps: int = 5,
+                    coefficients: Sequence[float] = (3.4445, -4.7750, 2.0315), eps: float = 1e-7) -> None:
+        """Orthogonalised (Muon) updates for the parameters with a (rows,
+        cols) shape in `shapes` (one entry per parameter, None: stays with
+        Adam) in every later step; their momentum lives in exp_avg.  The
+        workspace is allocated by torch."""
+        cfg = B.make_muon_config(lr, momentum, weight_decay, nesterov, scale, steps, coefficients, eps)
+        rows = [0 if s is None else int(s[0]) for s in shapes]
+        cols = [0 if s is None else int(s[1]) for s in shapes]
+        need = B.zero_muon_workspace_bytes(self.ctx, cfg, rows, cols)
+        # 512-byte aligned by torch's allocator
+        workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        B.zero_enable_muon(self.ctx, cfg, rows, cols, workspace.data_ptr(), need)
+        self._muon_ws = workspace
+
+    def disable_muon(self) -> None:
+        B.zero_disable_muon(self.ctx)
+        self._muon_ws = None
+
+    def set_muon_lr(self, lr: float) -> None:
+        B.zero_set_muon_lr(self.ctx, lr)
+
     def count_nonfinite(self, counter: Optional[torch.Tensor]) -> None:
         """Every later step adds its number of non-finite reduced gradients to
         `counter` (a one-element int64 device tensor, zeroed by the caller);
