@@ -141,5 +141,7 @@ struct GemmArgs {
 };
 cudaError_t launch_ns_gemm(const GemmArgs& g, cudaStream_t stream, int* launches);
 unsigned int ns_gemm_debug_failures();
+// Bounded waits of the products that gave up (0xFFFFFFFF if it cannot be read).
+unsigned int ns_gemm_timeouts();
 
 }  // namespace zfs

@@ -1,12 +1,25 @@
-// The matrix products of the Newton-Schulz steps.
+// The matrix products of the Newton-Schulz steps, on the tensor cores.
 //
 // A step on X (m x n over its smaller side m) is three products:
-//   A = X X^T            symmetric: only tiles on and below the diagonal
+//   A = X X^T              symmetric: only tiles on and below the diagonal
 //   P = a I + b A + c A A  symmetric likewise
-//   X' = P X             X = hi + lo while the early steps amplify rounding
-// Operands are fp16 with a power-of-two scale, sums are fp32.
+//   X' = P X               X = hi + lo while later steps amplify its rounding
+// Operands are fp16 with a power-of-two scale, sums are fp32 in TMEM.  A tall
+// G takes X^T X and X P instead, so that X keeps its orientation: operands
+// whose inner (contiguous) index is the summed one are K-major, the others
+// MN-major, and both are what the tensor cores read from shared memory.
+//
+// One persistent CTA (or pair of CTAs on one tile, kCtas = 2) per SM.  Warp
+// roles: 0-7 epilogue (TMEM quadrant warp % 4, column half warp / 4), 8 TMA
+// loads, 9 issues the MMAs.  kStages stages of a 128 x 64 block of A and of B
+// per CTA; two accumulators, so that the epilogue of a tile runs under the
+// next one's products.  In a pair each CTA holds 128 of the 256 rows of A and
+// half of B's columns, and the first CTA issues for both.
 
+#include <cuda.h>
 #include <cuda_fp16.h>
+
+#include <mutex>
 
 #include "zero_device.cuh"
 #include "zero_muon_internal.h"
@@ -14,110 +27,575 @@
 namespace zfs {
 namespace {
 
-constexpr int kTile = 64, kDepth = 16, kGemmThreads = 256;
+constexpr int kBlockK = 64;            // fp16 elements of one 128-byte swizzled row
+constexpr int kBlockM = 128;           // rows per CTA
+constexpr int kStages = 6;
+constexpr int kEpilogueWarps = 8;
+constexpr int kGemmThreads = (kEpilogueWarps + 2) * 32;
+constexpr uint32_t kOperandBytes = kBlockM * kBlockK * 2;
+constexpr uint32_t kStageBytes = 2 * kOperandBytes;
+constexpr uint32_t kSmemBytes = kStages * kStageBytes + 1024;  // + alignment
 
-__device__ __forceinline__ float half_bits(uint16_t b) {
-  __half_raw r;
-  r.x = b;
-  return __half2float(__half(r));
+__device__ unsigned int g_gemm_timeouts = 0;
+
+// What one launch needs; the tensor maps of (hi, lo) of both operands.
+struct GemmKernelArgs {
+  CUtensorMap a[2], b[2];
+  GemmArgs g;
+  long long tiles_m, tiles_n, tiles;  // tiles of one matrix / of all
+  int k_blocks;                       // per part
+  int vec_out;                        // kNsOut / kNsMuon: 16-byte accesses allowed
+};
+
+// ---- mbarriers, TMA, tcgen05 -------------------------------------------------
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-__device__ __forceinline__ uint16_t to_half_bits(float x) {
+__device__ __forceinline__ unsigned long long global_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// Address of `bar` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_rank(uint32_t bar, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(bar), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+}
+
+// A wait for a barrier's phase, bounded: products and copies take microseconds,
+// after kWaitNs they never will.  False: gave up (or another role did).
+constexpr unsigned long long kWaitNs = 1000000000ull;
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+  const unsigned long long t0 = global_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*gave_up) return false;
+    if (global_ns() - t0 > kWaitNs) {
+      *gave_up = 1;
+      atomicAdd(&g_gemm_timeouts, 1u);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* gave_up) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return wait_slow(bar, parity, gave_up);
+}
+
+template <int kCtas>
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  if constexpr (kCtas == 2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  }
+}
+
+// Shared-memory matrix descriptor of a 128-byte swizzled block.  K-major: rows
+// of 64 elements, 8-row groups 1024 bytes apart.  MN-major: 64 (MN) x 64 (K)
+// boxes, the 8-deep groups along K 1024 bytes apart, the boxes along MN 8192.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, bool k_major) {
+  const uint64_t lead = k_major ? 1 : 8192 >> 4, stride = 1024 >> 4;
+  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (lead << 16) | (stride << 32) | (1ull << 46) | (2ull << 61);
+}
+
+template <int kCtas>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kCtas == 2) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+// Arrives on `bar` (of both CTAs of a pair) when the MMAs issued so far are done.
+template <int kCtas>
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  if constexpr (kCtas == 2) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  } else {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+  }
+}
+template <int kCtas>
+__device__ __forceinline__ void tmem_alloc(uint32_t to, uint32_t columns) {
+  if constexpr (kCtas == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to), "r"(columns) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+}
+template <int kCtas>
+__device__ __forceinline__ void tmem_free(uint32_t at, uint32_t columns) {
+  if constexpr (kCtas == 2) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+  else asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns));
+}
+// 32 accumulator columns of this warp's 32 rows (one row per lane).
+__device__ __forceinline__ void tmem_load32(uint32_t at, float* x) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15,"
+      " %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(at));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ---- epilogue ----------------------------------------------------------------
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint16_t half_bits(float x) {
   const __half h = __float2half_rn(x);
   return *reinterpret_cast<const uint16_t*>(&h);
 }
+__device__ __forceinline__ float2 half2_values(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
 
-// One element of the finished product at (i, j) of matrix `mat`.
-__device__ __forceinline__ void store_one(const GemmArgs& g, int mat, long long i, long long j, float acc) {
-  const float v = acc * g.alpha;
-  if (g.epilogue == kNsGram || g.epilogue == kNsPoly) {
+// 32 columns j .. j+31 of row i: x holds the sums.  `mirror`: an off-diagonal
+// tile of a symmetric result, stored transposed as well (lanes are consecutive
+// rows, so every column is one contiguous store of the warp).
+template <int kEpi>
+__device__ __forceinline__ void store_columns(const GemmKernelArgs& ka, int mat, long long i, long long j, bool mirror,
+                                              float* x) {
+  const GemmArgs& g = ka.g;
+  if (i >= g.M || j >= g.N) return;
+  if constexpr (kEpi == kNsGram || kEpi == kNsPoly || kEpi == kNsApply) {
     uint16_t* d = g.d + mat * g.d_mat_stride;
-    float x = v;
-    if (g.epilogue == kNsPoly) {
-      x = g.cc * v + g.cb * half_bits(g.c[mat * g.d_mat_stride + i * g.ldd + j]) + (i == j ? g.ca : 0.0f);
+    const float f = g.alpha * (kEpi == kNsPoly ? g.cc : 1.0f) * g.out_scale;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {  // 8 columns at a time; the pitch is a multiple of 8
+      if (j + 8 * v >= g.ldd) break;
+      const long long at = i * g.ldd + j + 8 * v;
+      float* y = x + 8 * v;
+      if constexpr (kEpi == kNsPoly) {
+        const uint4 c = *reinterpret_cast<const uint4*>(g.c + mat * g.d_mat_stride + at);
+        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+        const float cb = g.cb * g.out_scale, ca = g.ca * g.out_scale;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 cv = half2_values(cw[k]);
+          y[2 * k] = f * y[2 * k] + cb * cv.x + (i == j + 8 * v + 2 * k ? ca : 0.0f);
+          y[2 * k + 1] = f * y[2 * k + 1] + cb * cv.y + (i == j + 8 * v + 2 * k + 1 ? ca : 0.0f);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) y[k] *= f;
+      }
+      uint32_t h[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) h[k] = half2_bits(y[2 * k], y[2 * k + 1]);
+      *reinterpret_cast<uint4*>(d + at) = make_uint4(h[0], h[1], h[2], h[3]);
+      if constexpr (kEpi == kNsApply) {
+        if (g.d_lo) {
+          uint32_t l[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 hv = half2_values(h[k]);
+            l[k] = half2_bits(y[2 * k] - hv.x, y[2 * k + 1] - hv.y);
+          }
+          *reinterpret_cast<uint4*>(g.d_lo + mat * g.d_mat_stride + at) = make_uint4(l[0], l[1], l[2], l[3]);
+        }
+      } else if (mirror) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const long long c = j + 8 * v + k;
+          if (c < g.N) d[c * g.ldd + i] = half_bits(y[k]);
+        }
+      }
     }
-    const uint16_t h = to_half_bits(x * g.out_scale);
-    d[i * g.ldd + j] = h;
-    d[j * g.ldd + i] = h;
-  } else if (g.epilogue == kNsApply) {
-    const float x = v * g.out_scale;
-    const uint16_t h = to_half_bits(x);
-    g.d[mat * g.d_mat_stride + i * g.ldd + j] = h;
-    if (g.d_lo) g.d_lo[mat * g.d_mat_stride + i * g.ldd + j] = to_half_bits(x - half_bits(h));
-  } else if (g.epilogue == kNsOut) {
-    g.out.out[mat * g.out.mat_stride + i * g.out.row_stride + j] = to_bf16_bits(v);
+  } else if constexpr (kEpi == kNsOut) {
+    uint16_t* d = g.out.out + mat * g.out.mat_stride + i * g.out.row_stride + j;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const float* y = x + 8 * v;
+      if (ka.vec_out && j + 8 * v + 8 <= g.N) {
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = pack_bf16x2(y[2 * k] * g.alpha, y[2 * k + 1] * g.alpha);
+        *reinterpret_cast<uint4*>(d + 8 * v) = make_uint4(h[0], h[1], h[2], h[3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (j + 8 * v + k < g.N) d[8 * v + k] = to_bf16_bits(y[k] * g.alpha);
+      }
+    }
   } else {
     const long long at = g.out.offset[mat] + i * g.N + j;
-    if (!ZFS_CHECK(at >= 0 && at < g.out.total_padded)) return;
-    const float w = __fadd_rn(__fmul_rn(g.out.master[at], g.out.decay), __fmul_rn(-g.out.step, v));
-    g.out.master[at] = w;
-    g.out.p16[at] = to_bf16_bits(w);
+    float* w = g.out.master + at;
+    uint16_t* p = g.out.p16 + at;
+    const float step = -g.out.step * g.alpha;  // alpha is a power of two: exact
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      if (ka.vec_out && j + 8 * v + 8 <= g.N) {
+        if (!ZFS_CHECK(at >= 0 && at + 8 * v + 8 <= g.out.total_padded)) continue;
+        float y[8];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float4 old = *reinterpret_cast<const float4*>(w + 8 * v + 4 * q);
+          const float o[4] = {old.x, old.y, old.z, old.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            y[4 * q + k] = __fadd_rn(__fmul_rn(o[k], g.out.decay), __fmul_rn(step, x[8 * v + 4 * q + k]));
+          *reinterpret_cast<float4*>(w + 8 * v + 4 * q) = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+        }
+        *reinterpret_cast<uint4*>(p + 8 * v) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                                          pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int e = 8 * v + k;
+          if (j + e >= g.N || !ZFS_CHECK(at >= 0 && at + e < g.out.total_padded)) continue;
+          const float y = __fadd_rn(__fmul_rn(w[e], g.out.decay), __fmul_rn(step, x[e]));
+          w[e] = y;
+          p[e] = to_bf16_bits(y);
+        }
+      }
+    }
   }
 }
 
-template <bool kAK, bool kBK>
-__global__ void __launch_bounds__(kGemmThreads) ns_gemm_kernel(const __grid_constant__ GemmArgs g) {
-  __shared__ float as[kDepth][kTile + 1], bs[kDepth][kTile + 1];
-  if (g.epilogue == kNsMuon && g.out.dev_t && *g.out.dev_t >= g.out.dev_steps) return;
-  const long long tiles_n = (g.N + kTile - 1) / kTile;
-  const long long i0 = blockIdx.x / tiles_n * kTile, j0 = blockIdx.x % tiles_n * kTile;
-  const bool symmetric = g.epilogue == kNsGram || g.epilogue == kNsPoly;
-  if (symmetric && j0 > i0) return;
-  const int mat = blockIdx.y, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-  float acc[4][4] = {};
-  for (int part = 0; part < g.parts; ++part) {
-    const uint16_t* pa = g.a.part[part] + mat * g.a.mat_stride;
-    const uint16_t* pb = g.b.part[part] + mat * g.b.mat_stride;
-    for (long long k0 = 0; k0 < g.K; k0 += kDepth) {
-      for (int e = threadIdx.x; e < kTile * kDepth; e += kGemmThreads) {
-        {
-          const int i = kAK ? e / kDepth : e % kTile, k = kAK ? e % kDepth : e / kTile;
-          const bool in = i0 + i < g.M && k0 + k < g.K;
-          as[k][i] = in ? half_bits(kAK ? pa[(i0 + i) * g.a.ld + k0 + k] : pa[(k0 + k) * g.a.ld + i0 + i]) : 0.0f;
+// Tile t of all matrices: (matrix, tile row, tile column).
+template <int kEpi>
+__device__ __forceinline__ void locate(const GemmKernelArgs& ka, long long t, int* mat, long long* ti, long long* tj) {
+  *mat = static_cast<int>(t / ka.tiles);
+  long long r = t - *mat * ka.tiles;
+  if constexpr (kEpi == kNsGram || kEpi == kNsPoly) {  // rows of the lower triangle, one after another
+    long long i = static_cast<long long>((sqrt(8.0 * static_cast<double>(r) + 1.0) - 1.0) * 0.5);
+    while (i * (i + 1) / 2 > r) --i;
+    while ((i + 1) * (i + 2) / 2 <= r) ++i;
+    *ti = i;
+    *tj = r - i * (i + 1) / 2;
+  } else {  // bands of 8 tile rows, so that tiles in flight share operands in L2
+    constexpr long long kBand = 8;
+    const long long band = r / (kBand * ka.tiles_n), first = band * kBand;
+    const long long high = ka.tiles_m - first < kBand ? ka.tiles_m - first : kBand;
+    r -= band * kBand * ka.tiles_n;
+    *ti = first + r % high;
+    *tj = r / high;
+  }
+}
+
+template <int kCtas, int kEpi>
+__global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_constant__ GemmKernelArgs ka) {
+  constexpr int kBlockN = 128 * kCtas;  // columns of a tile; rows: kBlockM * kCtas
+  constexpr uint32_t kTmemColumns = 2 * kBlockN;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
+  __shared__ uint32_t tmem_base;
+  __shared__ int gave_up;
+  const GemmArgs& g = ka.g;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t stages = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const uint32_t rank = kCtas == 2 ? blockIdx.x % 2 : 0;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tmem_full = empty + 8 * kStages,
+                 tmem_empty = tmem_full + 16;
+  if (threadIdx.x == 0) {
+    gave_up = 0;
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(tmem_full + 8 * s, 1);
+      mbar_init(tmem_empty + 8 * s, kEpilogueWarps * kCtas);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 9) tmem_alloc<kCtas>(smem_u32(&tmem_base), kTmemColumns);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if constexpr (kCtas == 2) cluster_sync();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_base;
+  const long long first = blockIdx.x / kCtas, step = gridDim.x / kCtas, total = ka.tiles * g.mats;
+  const int k_steps = ka.k_blocks * g.parts;
+  bool skip = false;
+  if constexpr (kEpi == kNsMuon) skip = g.out.dev_t && *g.out.dev_t >= g.out.dev_steps;
+
+  if (warp == 8 && lane == 0 && !skip) {
+    // ---- loads: both CTAs of a pair count on the first one's barrier ---------
+    uint32_t stage = 0, parity = 0;
+    long long issued = 0;
+    bool ok = true;
+    for (long long t = first; t < total && ok; t += step) {
+      int mat;
+      long long ti, tj;
+      locate<kEpi>(ka, t, &mat, &ti, &tj);
+      const int i0 = static_cast<int>(ti * kBlockM * kCtas + rank * kBlockM);
+      const int j0 = static_cast<int>(tj * kBlockN + rank * 128);
+      for (int s = 0; s < k_steps; ++s) {
+        const int part = s / ka.k_blocks, k0 = (s - part * ka.k_blocks) * kBlockK;
+        if (!wait_phase(empty + 8 * stage, parity ^ 1, &gave_up)) {
+          ok = false;
+          break;
         }
-        {
-          const int j = kBK ? e / kDepth : e % kTile, k = kBK ? e % kDepth : e / kTile;
-          const bool in = j0 + j < g.N && k0 + k < g.K;
-          bs[k][j] = in ? half_bits(kBK ? pb[(j0 + j) * g.b.ld + k0 + k] : pb[(k0 + k) * g.b.ld + j0 + j]) : 0.0f;
+        const uint32_t at = stages + stage * kStageBytes;
+        const uint32_t bar = kCtas == 2 ? map_rank(full + 8 * stage, 0) : full + 8 * stage;
+        if (rank == 0) mbar_expect_tx(full + 8 * stage, kStageBytes * kCtas);
+        if (g.a.k_major) {
+          tma_load<kCtas>(at, &ka.a[part], k0, i0, mat, bar);
+        } else {
+          tma_load<kCtas>(at, &ka.a[part], i0, k0, mat, bar);
+          tma_load<kCtas>(at + kOperandBytes / 2, &ka.a[part], i0 + 64, k0, mat, bar);
+        }
+        if (g.b.k_major) {
+          tma_load<kCtas>(at + kOperandBytes, &ka.b[part], k0, j0, mat, bar);
+        } else {
+          tma_load<kCtas>(at + kOperandBytes, &ka.b[part], j0, k0, mat, bar);
+          tma_load<kCtas>(at + kOperandBytes + kOperandBytes / 2, &ka.b[part], j0 + 64, k0, mat, bar);
+        }
+        ++issued;
+        if (++stage == kStages) {
+          stage = 0;
+          parity ^= 1;
         }
       }
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < kDepth; ++k) {
-        float x[4], y[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          x[r] = as[k][ty + 16 * r];
-          y[r] = bs[k][tx + 16 * r];
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) acc[r][c] = fmaf(x[r], y[c], acc[r][c]);
+    }
+    // The MMAs' last arrivals reach this CTA's barriers before it may leave.
+    for (int s = 0; s < kStages && ok && issued >= kStages; ++s) {
+      ok = wait_phase(empty + 8 * stage, parity ^ 1, &gave_up);
+      if (++stage == kStages) {
+        stage = 0;
+        parity ^= 1;
       }
-      __syncthreads();
+    }
+    for (int s = 0; s < issued && ok && issued < kStages; ++s) ok = wait_phase(empty + 8 * s, 0, &gave_up);
+    if (!ok) {
+      // a role gave up: the copies in flight land (bounded) before this CTA leaves
+      const unsigned long long t0 = global_ns();
+      while (global_ns() - t0 < 50000000ull) {
+        bool landed = true;
+        if (rank == 0) {
+          for (int s = 0; s < kStages; ++s) {
+            // the phase of the last issue to this stage
+            const long long uses = (issued + kStages - 1 - s) / kStages;
+            if (uses > 0 && !mbar_try_wait(full + 8 * s, static_cast<uint32_t>((uses - 1) & 1))) landed = false;
+          }
+        } else {
+          landed = false;  // the peer's copies count on the first CTA's barrier: wait the time out
+        }
+        if (landed) break;
+      }
+    }
+  } else if (warp == 9 && lane == 0 && rank == 0 && !skip) {
+    // ---- MMAs ---------------------------------------------------------------
+    const uint32_t idesc = (1u << 4) | (g.a.k_major ? 0u : 1u << 15) | (g.b.k_major ? 0u : 1u << 16) |
+                           (static_cast<uint32_t>(kBlockN >> 3) << 17) |
+                           (static_cast<uint32_t>((kBlockM * kCtas) >> 4) << 24);
+    const uint64_t step_a = g.a.k_major ? 32 >> 4 : 2048 >> 4, step_b = g.b.k_major ? 32 >> 4 : 2048 >> 4;
+    uint32_t stage = 0, parity = 0, acc = 0, acc_parity = 0;
+    bool ok = true;
+    for (long long t = first; t < total && ok; t += step) {
+      ok = wait_phase(tmem_empty + 8 * acc, acc_parity ^ 1, &gave_up);
+      if (!ok) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t d = tmem + acc * kBlockN;
+      for (int s = 0; s < k_steps; ++s) {
+        ok = wait_phase(full + 8 * stage, parity, &gave_up);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t at = stages + stage * kStageBytes;
+        const uint64_t da = smem_desc(at, g.a.k_major), db = smem_desc(at + kOperandBytes, g.b.k_major);
+#pragma unroll
+        for (int k = 0; k < kBlockK / 16; ++k)
+          mma<kCtas>(d, da + k * step_a, db + k * step_b, idesc, s > 0 || k > 0 ? 1 : 0);
+        mma_commit<kCtas>(empty + 8 * stage);
+        if (++stage == kStages) {
+          stage = 0;
+          parity ^= 1;
+        }
+      }
+      if (!ok) break;
+      mma_commit<kCtas>(tmem_full + 8 * acc);
+      acc ^= 1;
+      if (acc == 0) acc_parity ^= 1;
+    }
+  } else if (warp < kEpilogueWarps && !skip) {
+    // ---- epilogue -------------------------------------------------------------
+    const uint32_t quadrant = warp % 4, half = warp / 4;
+    uint32_t acc = 0, acc_parity = 0;
+    for (long long t = first; t < total; t += step) {
+      int mat;
+      long long ti, tj;
+      locate<kEpi>(ka, t, &mat, &ti, &tj);
+      if (!__all_sync(0xffffffffu, wait_phase(tmem_full + 8 * acc, acc_parity, &gave_up))) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const long long i = ti * kBlockM * kCtas + rank * kBlockM + quadrant * 32 + lane;
+      const bool mirror = (kEpi == kNsGram || kEpi == kNsPoly) && ti != tj;
+#pragma unroll 1
+      for (int c = half * kBlockN / 2; c < static_cast<int>(half + 1) * kBlockN / 2; c += 32) {
+        float x[32];
+        __syncwarp();
+        tmem_load32(tmem + acc * kBlockN + ((quadrant * 32) << 16) + c, x);
+        store_columns<kEpi>(ka, mat, i, tj * kBlockN + c, mirror, x);
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(kCtas == 2 ? map_rank(tmem_empty + 8 * acc, 0) : tmem_empty + 8 * acc);
+      acc ^= 1;
+      if (acc == 0) acc_parity ^= 1;
     }
   }
-#pragma unroll
-  for (int r = 0; r < 4; ++r) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const long long i = i0 + ty + 16 * r, j = j0 + tx + 16 * c;
-      if (i >= g.M || j >= g.N || (symmetric && j > i)) continue;
-      store_one(g, mat, i, j, acc[r][c]);
-    }
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if constexpr (kCtas == 2) cluster_sync();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (warp == 9) tmem_free<kCtas>(tmem, kTmemColumns);
+}
+
+// ---- host --------------------------------------------------------------------
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+std::once_flag g_encode_once;
+EncodeFn g_encode = nullptr;
+
+void load_encode() {
+  void* fn = nullptr;
+  cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+  if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+      q == cudaDriverEntryPointSuccess && fn) {
+    g_encode = reinterpret_cast<EncodeFn>(fn);
   }
+}
+
+// Map of one part of an operand with `mn` rows (columns) and `k` summed
+// elements, read in boxes of 64 x 128 (K-major) or 64 x 64; what lies outside
+// reads as zero.
+bool encode(CUtensorMap* map, const GemmOperand& o, int part, long long mn, long long k, int mats) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(o.k_major ? k : mn), static_cast<cuuint64_t>(o.k_major ? mn : k),
+                              static_cast<cuuint64_t>(mats)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.ld) * 2, static_cast<cuuint64_t>(o.mat_stride) * 2};
+  const cuuint32_t box[3] = {64, o.k_major ? 128u : 64u, 1};
+  const cuuint32_t unit[3] = {1, 1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(o.part[part]), dims, strides, box, unit,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int kCtas, int kEpi>
+cudaError_t launch(GemmKernelArgs& ka, cudaStream_t stream) {
+  const GemmArgs& g = ka.g;
+  const long long tile = 128 * kCtas;
+  ka.tiles_m = (g.M + tile - 1) / tile;
+  ka.tiles_n = (g.N + tile - 1) / tile;
+  ka.tiles = kEpi == kNsGram || kEpi == kNsPoly ? ka.tiles_m * (ka.tiles_m + 1) / 2 : ka.tiles_m * ka.tiles_n;
+  const cudaError_t e =
+      cudaFuncSetAttribute(ns_gemm_kernel<kCtas, kEpi>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  const long long tiles = ka.tiles * g.mats, room = sm_count() / kCtas;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((tiles < room ? tiles : room) * kCtas));
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kCtas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, ns_gemm_kernel<kCtas, kEpi>, ka);
+}
+
+template <int kEpi>
+cudaError_t launch_tile(GemmKernelArgs& ka, cudaStream_t stream) {
+  // A pair of SMs works on 256 x 256, one alone on 128 x 128: pairs once their
+  // tiles fill the GPU.
+  const long long t = 256;
+  const long long m = (ka.g.M + t - 1) / t, n = (ka.g.N + t - 1) / t;
+  const long long pairs = (kEpi == kNsGram || kEpi == kNsPoly ? m * (m + 1) / 2 : m * n) * ka.g.mats;
+  return pairs >= sm_count() / 2 ? launch<2, kEpi>(ka, stream) : launch<1, kEpi>(ka, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_ns_gemm(const GemmArgs& g, cudaStream_t stream, int* launches) {
-  const dim3 grid(static_cast<unsigned>((g.N + kTile - 1) / kTile * ((g.M + kTile - 1) / kTile)),
-                  static_cast<unsigned>(g.mats));
-  if (g.a.k_major && g.b.k_major) ns_gemm_kernel<true, true><<<grid, kGemmThreads, 0, stream>>>(g);
-  else if (g.a.k_major) ns_gemm_kernel<true, false><<<grid, kGemmThreads, 0, stream>>>(g);
-  else ns_gemm_kernel<false, false><<<grid, kGemmThreads, 0, stream>>>(g);
+  std::call_once(g_encode_once, load_encode);
+  if (!g_encode) return cudaErrorNotSupported;
+  GemmKernelArgs ka;
+  ka.g = g;
+  ka.k_blocks = static_cast<int>((g.K + kBlockK - 1) / kBlockK);
+  for (int p = 0; p < g.parts; ++p) {
+    if (!encode(&ka.a[p], g.a, p, g.M, g.K, g.mats) || !encode(&ka.b[p], g.b, p, g.N, g.K, g.mats))
+      return cudaErrorInvalidValue;
+  }
+  ka.vec_out = 0;
+  if (g.epilogue == kNsOut) {
+    ka.vec_out = g.out.row_stride % kVec == 0 && g.out.mat_stride % kVec == 0 &&
+                 reinterpret_cast<uintptr_t>(g.out.out) % 16 == 0;
+  } else if (g.epilogue == kNsMuon) {
+    ka.vec_out = g.N % kVec == 0;
+    for (int m = 0; m < g.mats; ++m) ka.vec_out = ka.vec_out && g.out.offset[m] % kVec == 0;
+  }
   ++*launches;
-  return cudaGetLastError();
+  switch (g.epilogue) {
+    case kNsGram: return launch_tile<kNsGram>(ka, stream);
+    case kNsPoly: return launch_tile<kNsPoly>(ka, stream);
+    case kNsApply: return launch_tile<kNsApply>(ka, stream);
+    case kNsOut: return launch_tile<kNsOut>(ka, stream);
+    default: return launch_tile<kNsMuon>(ka, stream);
+  }
+}
+
+unsigned int ns_gemm_timeouts() {
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_gemm_timeouts, sizeof v) != cudaSuccess) return 0xFFFFFFFFu;
+  return v;
 }
 
 unsigned int ns_gemm_debug_failures() {

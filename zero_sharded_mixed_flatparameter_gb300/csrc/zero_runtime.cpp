@@ -1504,9 +1504,10 @@ zero_status zero_read_nonfinite(zero_ctx* ctx, uint64_t* count, void* stream) {
 
 zero_status zero_kernel_timeouts(const zero_ctx* ctx, uint32_t* count) {
   if (!count) return fail(const_cast<zero_ctx*>(ctx), ZERO_EINVAL, "count is NULL");
-  const unsigned int v = zfs::step_timeouts();
-  if (v == 0xFFFFFFFFu) return fail(const_cast<zero_ctx*>(ctx), ZERO_ECUDA, "cannot read the timeout counter");
-  *count = v;
+  const unsigned int v = zfs::step_timeouts(), w = zfs::ns_gemm_timeouts();
+  if (v == 0xFFFFFFFFu || w == 0xFFFFFFFFu)
+    return fail(const_cast<zero_ctx*>(ctx), ZERO_ECUDA, "cannot read the timeout counter");
+  *count = v + w;
   return ZERO_OK;
 }
 
