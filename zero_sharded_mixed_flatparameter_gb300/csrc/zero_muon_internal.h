@@ -111,29 +111,29 @@ unsigned int muon_debug_failures();
 
 // ---- the products (zero_ns_gemm.cu) ----------------------------------------
 enum NsEpilogue {
-  kNsGram = 0,   // D symmetric: only tiles on and below the diagonal are computed, both halves stored
-  kNsPoly = 1,   // as kNsGram, D = a I + b C + c acc
-  kNsApply = 2,  // X' as a scaled fp16 pair (lo may be absent)
-  kNsOut = 3,    // the finished bf16 matrices
-  kNsMuon = 4    // the update of master and param16
+  kNsGram = 0,   // D = alpha acc, symmetric: only tiles on and below the diagonal are computed, both halves stored
+  kNsPoly = 1,   // as kNsGram, D = alpha acc + cfactor C
+  kNsApply = 2,  // D = alpha acc + cfactor (C + C_lo) as a pair (d_lo may be absent)
+  kNsOut = 3,    // the finished matrices, likewise, as bf16
+  kNsMuon = 4    // likewise, into the update of master and param16
 };
 
 struct GemmOperand {
-  const uint16_t* part[2] = {nullptr, nullptr};  // fp16 bits; the second part is added (hi + lo)
-  long long ld = 0, mat_stride = 0;              // elements
+  const uint16_t* data = nullptr;    // fp16 bits
+  long long ld = 0, mat_stride = 0;  // elements
   bool k_major = true;  // element (i, k) at i * ld + k; else at k * ld + i
 };
 
+// C, C_lo, D and D_lo are fp16 with one layout (ldd, d_mat_stride); the powers
+// of two of their scales are part of alpha and cfactor.
 struct GemmArgs {
   long long M = 0, N = 0, K = 0;
   int mats = 0;
   GemmOperand a, b;
-  int parts = 1;             // 2: sum over (a.part[p], b.part[p])
   int epilogue = kNsGram;
-  float alpha = 1.0f;        // power of two that undoes the operands' scales
-  float out_scale = 1.0f;    // power of two of the stored values
-  float ca = 0.0f, cb = 0.0f, cc = 0.0f;  // kNsPoly (cb already undoes C's scale)
-  const uint16_t* c = nullptr;            // kNsPoly: the Gram matrix, laid out as d
+  float alpha = 1.0f, cfactor = 0.0f;
+  const uint16_t* c = nullptr;
+  const uint16_t* c_lo = nullptr;
   uint16_t* d = nullptr;
   uint16_t* d_lo = nullptr;
   long long ldd = 0, d_mat_stride = 0;

@@ -2,12 +2,16 @@
 //
 // A step on X (m x n over its smaller side m) is three products:
 //   A = X X^T              symmetric: only tiles on and below the diagonal
-//   P = a I + b A + c A A  symmetric likewise
-//   X' = P X               X = hi + lo while later steps amplify its rounding
-// Operands are fp16 with a power-of-two scale, sums are fp32 in TMEM.  A tall
-// G takes X^T X and X P instead, so that X keeps its orientation: operands
-// whose inner (contiguous) index is the summed one are K-major, the others
-// MN-major, and both are what the tensor cores read from shared memory.
+//   P = b A + c A A        symmetric likewise
+//   X' = a X + P X         the first term from X = hi + lo in the epilogue
+// Operands are fp16 with a power-of-two scale, sums are fp32 in TMEM.  The
+// identity stays out of P: its rounding on P's diagonal would dominate, and
+// the low half of X, which matters for what the identity carries (directions
+// that X all but lacks and later steps multiply by up to a), then needs no
+// product of its own.  A tall G takes X^T X and X P instead, so that X keeps
+// its orientation: operands whose inner (contiguous) index is the summed one
+// are K-major, the others MN-major, and both are what the tensor cores read
+// from shared memory.
 //
 // One persistent CTA (or pair of CTAs on one tile, kCtas = 2) per SM.  Warp
 // roles: 0-7 epilogue (TMEM quadrant warp % 4, column half warp / 4), 8 TMA
@@ -38,12 +42,12 @@ constexpr uint32_t kSmemBytes = kStages * kStageBytes + 1024;  // + alignment
 
 __device__ unsigned int g_gemm_timeouts = 0;
 
-// What one launch needs; the tensor maps of (hi, lo) of both operands.
+// What one launch needs.
 struct GemmKernelArgs {
-  CUtensorMap a[2], b[2];
+  CUtensorMap a, b;
   GemmArgs g;
   long long tiles_m, tiles_n, tiles;  // tiles of one matrix / of all
-  int k_blocks;                       // per part
+  int k_blocks;
   int vec_out;                        // kNsOut / kNsMuon: 16-byte accesses allowed
 };
 
@@ -203,6 +207,28 @@ __device__ __forceinline__ float2 half2_values(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+// x[0..7] += factor * the old iterate's 8 elements at `at`.
+__device__ __forceinline__ void add_old(const GemmArgs& g, long long at, float* x) {
+  const uint4 h = *reinterpret_cast<const uint4*>(g.c + at);
+  const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 v = half2_values(hw[k]);
+    x[2 * k] = fmaf(g.cfactor, v.x, x[2 * k]);
+    x[2 * k + 1] = fmaf(g.cfactor, v.y, x[2 * k + 1]);
+  }
+  if (g.c_lo) {
+    const uint4 l = *reinterpret_cast<const uint4*>(g.c_lo + at);
+    const uint32_t lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 v = half2_values(lw[k]);
+      x[2 * k] = fmaf(g.cfactor, v.x, x[2 * k]);
+      x[2 * k + 1] = fmaf(g.cfactor, v.y, x[2 * k + 1]);
+    }
+  }
+}
+
 // 32 columns j .. j+31 of row i: x holds the sums.  `mirror`: an off-diagonal
 // tile of a symmetric result, stored transposed as well (lanes are consecutive
 // rows, so every column is one contiguous store of the warp).
@@ -211,32 +237,20 @@ __device__ __forceinline__ void store_columns(const GemmKernelArgs& ka, int mat,
                                               float* x) {
   const GemmArgs& g = ka.g;
   if (i >= g.M || j >= g.N) return;
-  if constexpr (kEpi == kNsGram || kEpi == kNsPoly || kEpi == kNsApply) {
-    uint16_t* d = g.d + mat * g.d_mat_stride;
-    const float f = g.alpha * (kEpi == kNsPoly ? g.cc : 1.0f) * g.out_scale;
+  // 8 columns at a time; the pitch of C and D is a multiple of 8
+  const long long row = mat * g.d_mat_stride + i * g.ldd + j;
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {  // 8 columns at a time; the pitch is a multiple of 8
-      if (j + 8 * v >= g.ldd) break;
-      const long long at = i * g.ldd + j + 8 * v;
-      float* y = x + 8 * v;
-      if constexpr (kEpi == kNsPoly) {
-        const uint4 c = *reinterpret_cast<const uint4*>(g.c + mat * g.d_mat_stride + at);
-        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-        const float cb = g.cb * g.out_scale, ca = g.ca * g.out_scale;
+  for (int v = 0; v < 4; ++v) {
+    if (j + 8 * v >= g.N) break;
+    float* y = x + 8 * v;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 cv = half2_values(cw[k]);
-          y[2 * k] = f * y[2 * k] + cb * cv.x + (i == j + 8 * v + 2 * k ? ca : 0.0f);
-          y[2 * k + 1] = f * y[2 * k + 1] + cb * cv.y + (i == j + 8 * v + 2 * k + 1 ? ca : 0.0f);
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y[k] *= f;
-      }
+    for (int k = 0; k < 8; ++k) y[k] *= g.alpha;
+    if constexpr (kEpi != kNsGram) add_old(g, row + 8 * v, y);
+    if constexpr (kEpi == kNsGram || kEpi == kNsPoly || kEpi == kNsApply) {
       uint32_t h[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) h[k] = half2_bits(y[2 * k], y[2 * k + 1]);
-      *reinterpret_cast<uint4*>(d + at) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(g.d + row + 8 * v) = make_uint4(h[0], h[1], h[2], h[3]);
       if constexpr (kEpi == kNsApply) {
         if (g.d_lo) {
           uint32_t l[4];
@@ -245,61 +259,50 @@ __device__ __forceinline__ void store_columns(const GemmKernelArgs& ka, int mat,
             const float2 hv = half2_values(h[k]);
             l[k] = half2_bits(y[2 * k] - hv.x, y[2 * k + 1] - hv.y);
           }
-          *reinterpret_cast<uint4*>(g.d_lo + mat * g.d_mat_stride + at) = make_uint4(l[0], l[1], l[2], l[3]);
+          *reinterpret_cast<uint4*>(g.d_lo + row + 8 * v) = make_uint4(l[0], l[1], l[2], l[3]);
         }
       } else if (mirror) {
+        uint16_t* d = g.d + mat * g.d_mat_stride;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const long long c = j + 8 * v + k;
           if (c < g.N) d[c * g.ldd + i] = half_bits(y[k]);
         }
       }
-    }
-  } else if constexpr (kEpi == kNsOut) {
-    uint16_t* d = g.out.out + mat * g.out.mat_stride + i * g.out.row_stride + j;
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const float* y = x + 8 * v;
+    } else if constexpr (kEpi == kNsOut) {
+      uint16_t* d = g.out.out + mat * g.out.mat_stride + i * g.out.row_stride + j + 8 * v;
       if (ka.vec_out && j + 8 * v + 8 <= g.N) {
-        uint32_t h[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) h[k] = pack_bf16x2(y[2 * k] * g.alpha, y[2 * k + 1] * g.alpha);
-        *reinterpret_cast<uint4*>(d + 8 * v) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(d) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                                  pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
       } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (j + 8 * v + k < g.N) d[8 * v + k] = to_bf16_bits(y[k] * g.alpha);
+          if (j + 8 * v + k < g.N) d[k] = to_bf16_bits(y[k]);
       }
-    }
-  } else {
-    const long long at = g.out.offset[mat] + i * g.N + j;
-    float* w = g.out.master + at;
-    uint16_t* p = g.out.p16 + at;
-    const float step = -g.out.step * g.alpha;  // alpha is a power of two: exact
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
+    } else {
+      const long long at = g.out.offset[mat] + i * g.N + j + 8 * v;
+      float* w = g.out.master + at;
+      uint16_t* p = g.out.p16 + at;
       if (ka.vec_out && j + 8 * v + 8 <= g.N) {
-        if (!ZFS_CHECK(at >= 0 && at + 8 * v + 8 <= g.out.total_padded)) continue;
-        float y[8];
+        if (!ZFS_CHECK(at >= 0 && at + 8 <= g.out.total_padded)) continue;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const float4 old = *reinterpret_cast<const float4*>(w + 8 * v + 4 * q);
+          const float4 old = *reinterpret_cast<const float4*>(w + 4 * q);
           const float o[4] = {old.x, old.y, old.z, old.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            y[4 * q + k] = __fadd_rn(__fmul_rn(o[k], g.out.decay), __fmul_rn(step, x[8 * v + 4 * q + k]));
-          *reinterpret_cast<float4*>(w + 8 * v + 4 * q) = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+            y[4 * q + k] = __fadd_rn(__fmul_rn(o[k], g.out.decay), __fmul_rn(-g.out.step, y[4 * q + k]));
+          *reinterpret_cast<float4*>(w + 4 * q) = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
         }
-        *reinterpret_cast<uint4*>(p + 8 * v) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                                          pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                                                  pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
       } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const int e = 8 * v + k;
-          if (j + e >= g.N || !ZFS_CHECK(at >= 0 && at + e < g.out.total_padded)) continue;
-          const float y = __fadd_rn(__fmul_rn(w[e], g.out.decay), __fmul_rn(step, x[e]));
-          w[e] = y;
-          p[e] = to_bf16_bits(y);
+          if (j + 8 * v + k >= g.N || !ZFS_CHECK(at >= 0 && at + k < g.out.total_padded)) continue;
+          const float z = __fadd_rn(__fmul_rn(w[k], g.out.decay), __fmul_rn(-g.out.step, y[k]));
+          w[k] = z;
+          p[k] = to_bf16_bits(z);
         }
       }
     }
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
   const long long first = blockIdx.x / kCtas, step = gridDim.x / kCtas, total = ka.tiles * g.mats;
-  const int k_steps = ka.k_blocks * g.parts;
+  const int k_steps = ka.k_blocks;
   bool skip = false;
   if constexpr (kEpi == kNsMuon) skip = g.out.dev_t && *g.out.dev_t >= g.out.dev_steps;
 
@@ -376,7 +379,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
       const int i0 = static_cast<int>(ti * kBlockM * kCtas + rank * kBlockM);
       const int j0 = static_cast<int>(tj * kBlockN + rank * 128);
       for (int s = 0; s < k_steps; ++s) {
-        const int part = s / ka.k_blocks, k0 = (s - part * ka.k_blocks) * kBlockK;
+        const int k0 = s * kBlockK;
         if (!wait_phase(empty + 8 * stage, parity ^ 1, &gave_up)) {
           ok = false;
           break;
@@ -385,16 +388,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
         const uint32_t bar = kCtas == 2 ? map_rank(full + 8 * stage, 0) : full + 8 * stage;
         if (rank == 0) mbar_expect_tx(full + 8 * stage, kStageBytes * kCtas);
         if (g.a.k_major) {
-          tma_load<kCtas>(at, &ka.a[part], k0, i0, mat, bar);
+          tma_load<kCtas>(at, &ka.a, k0, i0, mat, bar);
         } else {
-          tma_load<kCtas>(at, &ka.a[part], i0, k0, mat, bar);
-          tma_load<kCtas>(at + kOperandBytes / 2, &ka.a[part], i0 + 64, k0, mat, bar);
+          tma_load<kCtas>(at, &ka.a, i0, k0, mat, bar);
+          tma_load<kCtas>(at + kOperandBytes / 2, &ka.a, i0 + 64, k0, mat, bar);
         }
         if (g.b.k_major) {
-          tma_load<kCtas>(at + kOperandBytes, &ka.b[part], k0, j0, mat, bar);
+          tma_load<kCtas>(at + kOperandBytes, &ka.b, k0, j0, mat, bar);
         } else {
-          tma_load<kCtas>(at + kOperandBytes, &ka.b[part], j0, k0, mat, bar);
-          tma_load<kCtas>(at + kOperandBytes + kOperandBytes / 2, &ka.b[part], j0 + 64, k0, mat, bar);
+          tma_load<kCtas>(at + kOperandBytes, &ka.b, j0, k0, mat, bar);
+          tma_load<kCtas>(at + kOperandBytes + kOperandBytes / 2, &ka.b, j0 + 64, k0, mat, bar);
         }
         ++issued;
         if (++stage == kStages) {
@@ -512,16 +515,16 @@ void load_encode() {
   }
 }
 
-// Map of one part of an operand with `mn` rows (columns) and `k` summed
+// Map of an operand with `mn` rows (columns) and `k` summed
 // elements, read in boxes of 64 x 128 (K-major) or 64 x 64; what lies outside
 // reads as zero.
-bool encode(CUtensorMap* map, const GemmOperand& o, int part, long long mn, long long k, int mats) {
+bool encode(CUtensorMap* map, const GemmOperand& o, long long mn, long long k, int mats) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(o.k_major ? k : mn), static_cast<cuuint64_t>(o.k_major ? mn : k),
                               static_cast<cuuint64_t>(mats)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(o.ld) * 2, static_cast<cuuint64_t>(o.mat_stride) * 2};
   const cuuint32_t box[3] = {64, o.k_major ? 128u : 64u, 1};
   const cuuint32_t unit[3] = {1, 1, 1};
-  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(o.part[part]), dims, strides, box, unit,
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(o.data), dims, strides, box, unit,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -570,10 +573,7 @@ cudaError_t launch_ns_gemm(const GemmArgs& g, cudaStream_t stream, int* launches
   GemmKernelArgs ka;
   ka.g = g;
   ka.k_blocks = static_cast<int>((g.K + kBlockK - 1) / kBlockK);
-  for (int p = 0; p < g.parts; ++p) {
-    if (!encode(&ka.a[p], g.a, p, g.M, g.K, g.mats) || !encode(&ka.b[p], g.b, p, g.N, g.K, g.mats))
-      return cudaErrorInvalidValue;
-  }
+  if (!encode(&ka.a, g.a, g.M, g.K, g.mats) || !encode(&ka.b, g.b, g.N, g.K, g.mats)) return cudaErrorInvalidValue;
   ka.vec_out = 0;
   if (g.epilogue == kNsOut) {
     ka.vec_out = g.out.row_stride % kVec == 0 && g.out.mat_stride % kVec == 0 &&

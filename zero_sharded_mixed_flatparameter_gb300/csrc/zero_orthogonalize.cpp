@@ -46,10 +46,10 @@ double largest_value(double a, double b, double c, double top) {
   return best;
 }
 
-// Largest |a + b t + c t^2| over 0 <= t <= top.
-double largest_factor(double a, double b, double c, double top) {
-  auto q = [&](double t) { return std::fabs(a + t * (b + t * c)); };
-  double best = std::max(q(0.0), q(top));
+// Largest |b t + c t^2| over 0 <= t <= top: the spectral norm of P = b A + c A A.
+double largest_factor(double b, double c, double top) {
+  auto q = [&](double t) { return std::fabs(t * (b + t * c)); };
+  double best = q(top);
   if (c != 0.0) {
     const double t = -b / (2.0 * c);
     if (t > 0.0 && t < top) best = std::max(best, q(t));
@@ -66,9 +66,9 @@ constexpr double kLargestIterate = 1024.0;
 
 // Steps whose X keeps its low half.  Noise that rounding puts into X at step k
 // passes steps - k further polynomials, each of which multiplies the small
-// singular values by up to a (3.4): with fp16 alone a rank-1 matrix ends
+// singular values by up to a (3.4): with 11 bits alone a rank-1 matrix ends
 // 1.5e-1 off after five steps (bf16: 1.2), with the low half kept until two
-// polynomials are left 3.4e-3, and a Gaussian one 1.1e-3 either way.
+// polynomials are left 2.8e-3, and a Gaussian one 1.1e-3 either way.
 int low_steps(int steps) { return std::max(steps - 2, 0); }
 
 }  // namespace
@@ -157,18 +157,16 @@ cudaError_t ns_run(const NsPlan& p, const zero_ns_config& cfg, int mats, const M
     const int from = k % 2, to = 1 - from;
     const bool low = k < lows, last = k + 1 == cfg.steps;
     const int ea = scale_exponent(top * top);
-    const int ep = scale_exponent(largest_factor(cfg.a, cfg.b, cfg.c, top * top));
+    const int ep = scale_exponent(largest_factor(cfg.b, cfg.c, top * top));
     const double next = largest_value(cfg.a, cfg.b, cfg.c, top);
     const int en = scale_exponent(next);
     GemmOperand x;
-    x.part[0] = half(p.x_hi[from]);
-    x.part[1] = low ? half(p.x_lo[from]) : nullptr;
+    x.data = half(p.x_hi[from]);
     x.ld = p.ldx;
     x.mat_stride = x_stride;
-    GemmOperand sq;
-    sq.ld = p.ldm;
-    sq.mat_stride = m_stride;
-    sq.k_major = true;
+    GemmOperand square;
+    square.ld = p.ldm;
+    square.mat_stride = m_stride;
 
     GemmArgs gram{};
     gram.M = gram.N = p.m;
@@ -177,8 +175,7 @@ cudaError_t ns_run(const NsPlan& p, const zero_ns_config& cfg, int mats, const M
     gram.a = gram.b = x;
     gram.a.k_major = gram.b.k_major = !p.tall;
     gram.epilogue = kNsGram;
-    gram.alpha = std::ldexp(1.0f, -2 * ex);
-    gram.out_scale = std::ldexp(1.0f, ea);
+    gram.alpha = std::ldexp(1.0f, ea - 2 * ex);
     gram.d = half(p.gram);
     gram.ldd = p.ldm;
     gram.d_mat_stride = m_stride;
@@ -188,14 +185,11 @@ cudaError_t ns_run(const NsPlan& p, const zero_ns_config& cfg, int mats, const M
     GemmArgs poly{};
     poly.M = poly.N = poly.K = p.m;
     poly.mats = mats;
-    poly.a = poly.b = sq;
-    poly.a.part[0] = poly.b.part[0] = half(p.gram);
+    poly.a = poly.b = square;
+    poly.a.data = poly.b.data = half(p.gram);
     poly.epilogue = kNsPoly;
-    poly.alpha = std::ldexp(1.0f, -2 * ea);
-    poly.out_scale = std::ldexp(1.0f, ep);
-    poly.ca = cfg.a;
-    poly.cb = cfg.b * std::ldexp(1.0f, -ea);
-    poly.cc = cfg.c;
+    poly.alpha = cfg.c * std::ldexp(1.0f, ep - 2 * ea);
+    poly.cfactor = cfg.b * std::ldexp(1.0f, ep - ea);
     poly.c = half(p.gram);
     poly.d = half(p.poly);
     poly.ldd = p.ldm;
@@ -208,28 +202,29 @@ cudaError_t ns_run(const NsPlan& p, const zero_ns_config& cfg, int mats, const M
     apply.N = p.cols;
     apply.K = p.m;
     apply.mats = mats;
-    apply.parts = low ? 2 : 1;
-    sq.part[0] = sq.part[1] = half(p.poly);
-    if (p.tall) {  // X' = X P, P symmetric
+    square.data = half(p.poly);
+    if (p.tall) {  // X' = a X + X P, P symmetric
       apply.a = x;
-      apply.a.k_major = true;
-      apply.b = sq;
-    } else {       // X' = P X
-      apply.a = sq;
+      apply.b = square;
+    } else {       // X' = a X + P X
+      apply.a = square;
       apply.b = x;
       apply.b.k_major = false;
     }
-    apply.alpha = std::ldexp(1.0f, -ex - ep);
+    const int eo = last ? 0 : en;
+    apply.alpha = std::ldexp(1.0f, eo - ex - ep);
+    apply.cfactor = cfg.a * std::ldexp(1.0f, eo - ex);
+    apply.c = x.data;
+    apply.c_lo = low ? half(p.x_lo[from]) : nullptr;
+    apply.ldd = p.ldx;
+    apply.d_mat_stride = x_stride;
     if (last) {
       apply.epilogue = out.out ? kNsOut : kNsMuon;
       apply.out = out;
     } else {
       apply.epilogue = kNsApply;
-      apply.out_scale = std::ldexp(1.0f, en);
       apply.d = half(p.x_hi[to]);
       apply.d_lo = k + 1 < lows ? half(p.x_lo[to]) : nullptr;
-      apply.ldd = p.ldx;
-      apply.d_mat_stride = x_stride;
     }
     e = launch_ns_gemm(apply, stream, launches);
     if (e != cudaSuccess) return e;
