@@ -175,6 +175,20 @@ def test_all_padding_and_no_tokens():
     assert (back[2] == 0).all() and (back[3] == 0).all()
 
 
+@pytest.mark.parametrize("dim,rotary", [(64, 64), (72, 24), (80, 32)])
+def test_no_eps(dim, rotary):
+    # with eps 0 nothing that is not a real head (padding, lanes without one) may reach a sum
+    q, k, dq, dk, gains, table, positions = inputs(37, 5, 3, dim, rotary, torch.float32, 15)
+    dev = [x.cuda() for x in (q, k, *gains, table, positions)]
+    out = ops.qk_norm_rope(*dev, eps=0.0)
+    back = ops.qk_norm_rope_backward(dq.cuda(), dk.cuda(), *dev, eps=0.0)
+    x, gain = k.double().requires_grad_(), gains[1].double().requires_grad_()
+    want = qk64(x, gain, table, positions, 0.0, False)
+    assert relative(out[1], want.detach()) <= 2e-6
+    dx, dgain = torch.autograd.grad(want, (x, gain), dk.double())
+    assert relative(back[1], dx) <= 2e-6 and relative(back[3], dgain) <= GAIN_TOL
+
+
 def test_zero_rows_and_large_values():
     q, k, dq, dk, gains, table, positions = inputs(6, 2, 1, 64, 64, torch.float32, 11, padded=False)
     q[0] = 0

@@ -6,8 +6,12 @@
 // backward, with xn = x * rstd and h = R^T dout:
 //   dx = rstd * (gain h - xn * mean(gain h xn)),  dgain = sum h xn
 //
-// A head is read once and written once; everything between is fp32 in
-// registers and shared memory.  One warp per head of a token.
+// A head is read once and written once; everything between is fp32.  Bound by
+// memory, so the kernel for heads of whole vectors keeps enough bytes in
+// flight: a group of lanes holds a head, 8 elements (16 or 32 bytes) a lane, a
+// warp takes a token's heads kUnroll groups at a time, and the token's cosines
+// and sines stay in registers over its heads.  Other head sizes take one warp
+// per head with the head in shared memory.
 
 #include <cmath>
 #include <cstdio>
@@ -41,6 +45,8 @@ struct QkArgs {
   const int32_t* positions;
   float* partials;             // [CTA][2][dim] gain sums of the backward pass
   void* dgain[2];
+  int group;                   // lanes per head (power of two)
+  int chunks, chunk_heads;     // a token's heads in parts for separate warps
 };
 
 template <bool kFp32>
@@ -155,21 +161,304 @@ __global__ void __launch_bounds__(kQkThreads) qk_kernel(const __grid_constant__ 
   }
 }
 
-// The gain gradients from the CTAs' sums, in CTA order.
-__global__ void __launch_bounds__(kQkThreads) qk_gain_kernel(const __grid_constant__ QkArgs a, int ctas) {
-  const int d = blockIdx.x * kQkThreads + threadIdx.x;
-  if (d >= 2 * a.dim) return;
-  const int which = d / a.dim;
-  if (!a.dgain[which]) return;
-  double s = 0.0;
-  for (int c = 0; c < ctas; ++c) s += a.partials[static_cast<long long>(c) * 2 * a.dim + d];
-  if (a.dgain_fp32) store_one<true>(a.dgain[which], d % a.dim, static_cast<float>(s));
-  else store_one<false>(a.dgain[which], d % a.dim, static_cast<float>(s));
+// ---- heads of whole vectors -----------------------------------------------------------
+template <bool kFp32>
+struct Vec8 {
+  uint4 lo, hi;  // hi: fp32 only
+};
+template <bool kFp32, bool kAligned>
+__device__ __forceinline__ Vec8<kFp32> load_vec(const void* p, long long at) {
+  Vec8<kFp32> v;
+  if constexpr (!kAligned) {
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < (kFp32 ? 8 : 4); ++k) {
+      if constexpr (kFp32) {
+        w[k] = static_cast<const uint32_t*>(p)[at + k];
+      } else {
+        const uint16_t* q = static_cast<const uint16_t*>(p) + at + 2 * k;
+        w[k] = static_cast<uint32_t>(q[0]) | static_cast<uint32_t>(q[1]) << 16;
+      }
+    }
+    v.lo = make_uint4(w[0], w[1], w[2], w[3]);
+    if constexpr (kFp32) v.hi = make_uint4(w[4], w[5], w[6], w[7]);
+  } else if constexpr (kFp32) {
+    const float* q = static_cast<const float*>(p) + at;
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v.lo.x), "=r"(v.lo.y), "=r"(v.lo.z), "=r"(v.lo.w), "=r"(v.hi.x), "=r"(v.hi.y), "=r"(v.hi.z),
+                   "=r"(v.hi.w)
+                 : "l"(q));
+  } else {
+    v.lo = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+  }
+  return v;
+}
+template <bool kFp32>
+__device__ __forceinline__ void widen(const Vec8<kFp32>& v, float* x) {
+  const uint32_t l[4] = {v.lo.x, v.lo.y, v.lo.z, v.lo.w};
+  if constexpr (kFp32) {
+    const uint32_t h[4] = {v.hi.x, v.hi.y, v.hi.z, v.hi.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[k] = __uint_as_float(l[k]);
+      x[4 + k] = __uint_as_float(h[k]);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[2 * k] = bf16_lo(l[k]);
+      x[2 * k + 1] = bf16_hi(l[k]);
+    }
+  }
+}
+template <bool kFp32, bool kAligned>
+__device__ __forceinline__ void store_vec(void* p, long long at, const float* x) {
+  if constexpr (!kAligned) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) store_one<kFp32>(p, at + k, x[k]);
+  } else if constexpr (kFp32) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<float*>(p) + at),
+                 "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) =
+        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  }
 }
 
+// A lane's 8 elements turned: its partner's 8 come from the lane `partner`
+// (halves), or the pairs lie in the lane (interleaved).  sn carries the sign.
+__device__ __forceinline__ void turn(bool interleaved, int partner, const float* cs, const float* sn, float* y) {
+  if (interleaved) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float one = y[2 * k], two = y[2 * k + 1];
+      y[2 * k] = fmaf(one, cs[k], -two * sn[k]);
+      y[2 * k + 1] = fmaf(two, cs[k], one * sn[k]);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float other = __shfl_sync(0xffffffffu, y[k], partner);
+      y[k] = fmaf(y[k], cs[k], other * sn[k]);
+    }
+  }
+}
+
+template <bool kFp32, bool kBackward, bool kAligned>
+__global__ void __launch_bounds__(kQkThreads, 2) qk_vec_kernel(const __grid_constant__ QkArgs a) {
+  constexpr int kUnroll = kBackward ? 2 : 4;  // heads in flight per group of lanes
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int in_group = lane % a.group, groups = 32 / a.group, my_group = lane / a.group;
+  const int d0 = in_group * 8, half = a.rotary / 2;
+  const bool active = d0 < a.dim, turned = d0 < a.rotary, first = d0 < half;
+  const bool interleaved = a.interleaved != 0;
+  const int partner = !turned ? lane : first ? lane + half / 8 : lane - half / 8;
+  const float inv_dim = 1.0f / static_cast<float>(a.dim);
+  float dgain[2][8] = {};
+  const long long units = a.tokens * a.chunks;
+  for (long long u = static_cast<long long>(blockIdx.x) * kQkWarps + warp; u < units;
+       u += static_cast<long long>(gridDim.x) * kQkWarps) {
+    const long long token = u / a.chunks;
+    const int begin = static_cast<int>(u - token * a.chunks) * a.chunk_heads;
+    const long long position = a.positions ? a.positions[token] : token;
+    const bool live = position >= 0 && position < a.n_positions;
+    float cs[8], sn[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      cs[k] = 1.0f;
+      sn[k] = 0.0f;
+    }
+    if (live && turned) {
+      const float* row = a.table + position * a.rotary;
+      const float sign = kBackward ? -1.0f : 1.0f;
+      if (interleaved) {
+        const float4 c = *reinterpret_cast<const float4*>(row + d0 / 2);
+        const float4 s = *reinterpret_cast<const float4*>(row + half + d0 / 2);
+        cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
+        sn[0] = sign * s.x; sn[1] = sign * s.y; sn[2] = sign * s.z; sn[3] = sign * s.w;
+      } else {
+        const int pair = first ? d0 : d0 - half;
+        const float own = first ? -sign : sign;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float4 c = *reinterpret_cast<const float4*>(row + pair + 4 * q);
+          const float4 s = *reinterpret_cast<const float4*>(row + half + pair + 4 * q);
+          cs[4 * q] = c.x; cs[4 * q + 1] = c.y; cs[4 * q + 2] = c.z; cs[4 * q + 3] = c.w;
+          sn[4 * q] = own * s.x; sn[4 * q + 1] = own * s.y; sn[4 * q + 2] = own * s.z; sn[4 * q + 3] = own * s.w;
+        }
+      }
+    }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      // the part of this unit's heads that are queries (keys)
+      const int shift = which ? a.q_heads : 0, count = which ? a.k_heads : a.q_heads;
+      const int lo = begin - shift > 0 ? begin - shift : 0;
+      const int end = begin + a.chunk_heads - shift < count ? begin + a.chunk_heads - shift : count;
+      if (lo >= end) continue;
+      const Heads &hx = a.x[which], &hy = a.dy[which], &ho = a.out[which];
+      const long long from = token * hx.token + d0, grad = token * hy.token + d0, to = token * ho.token + d0;
+      float gain[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) gain[k] = active ? load_gain(a, which, d0 + k) : 0.0f;
+      for (int h0 = lo; h0 < end; h0 += groups * kUnroll) {
+        Vec8<kFp32> vx[kUnroll], vy[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+          const int h = h0 + i * groups + my_group;
+          vx[i].lo = vx[i].hi = vy[i].lo = vy[i].hi = make_uint4(0, 0, 0, 0);
+          if (live && active && h < end) {
+            vx[i] = load_vec<kFp32, kAligned>(hx.p, from + h * hx.head);
+            if constexpr (kBackward) vy[i] = load_vec<kFp32, kAligned>(hy.p, grad + h * hy.head);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+          const int h = h0 + i * groups + my_group;
+          float x[8], y[8];
+          widen<kFp32>(vx[i], x);
+          float sq = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sq = fmaf(x[k], x[k], sq);
+          if constexpr (!kBackward) {
+            for (int o = a.group / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+            const float rstd = rsqrtf(fmaf(sq, inv_dim, a.eps));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) y[k] = x[k] * rstd * gain[k];
+            turn(interleaved, partner, cs, sn, y);
+          } else {
+            widen<kFp32>(vy[i], y);
+            turn(interleaved, partner, cs, sn, y);  // h: the gradient turned back
+            float dot = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) dot = fmaf(y[k] * gain[k], x[k], dot);
+            for (int o = a.group / 2; o > 0; o >>= 1) {
+              sq += __shfl_xor_sync(0xffffffffu, sq, o);
+              dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            }
+            const float rstd = rsqrtf(fmaf(sq, inv_dim, a.eps));
+            const float mean = dot * rstd * inv_dim;  // mean(gain h xn)
+            const bool real = live && h < end;        // else 0 * inf for eps 0
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float xn = x[k] * rstd;
+              if (real) dgain[which][k] = fmaf(y[k], xn, dgain[which][k]);
+              y[k] = rstd * fmaf(-xn, mean, y[k] * gain[k]);
+            }
+          }
+          if (active && h < end) {
+            if (!live) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) y[k] = 0.0f;
+            }
+            store_vec<kFp32, kAligned>(ho.p, to + h * ho.head, y);
+          }
+        }
+      }
+    }
+  }
+  if constexpr (kBackward) {
+    // the CTA's gain sums: over the groups of a warp, then over the warps
+    __shared__ float sums[kQkWarps][kMaxHeadDim];
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        for (int o = a.group; o < 32; o <<= 1) dgain[which][k] += __shfl_xor_sync(0xffffffffu, dgain[which][k], o);
+      }
+      __syncthreads();
+      if (my_group == 0 && active) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sums[warp][d0 + k] = dgain[which][k];
+      }
+      __syncthreads();
+      for (int d = threadIdx.x; d < a.dim; d += kQkThreads) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kQkWarps; ++w) s += sums[w][d];
+        a.partials[(static_cast<long long>(blockIdx.x) * 2 + which) * a.dim + d] = s;
+      }
+    }
+  }
+}
+
+// The gain gradients from the CTAs' sums: 32 columns per CTA, every warp a
+// contiguous share of the CTAs, then warp after warp.
+__global__ void __launch_bounds__(kQkThreads) qk_gain_kernel(const __grid_constant__ QkArgs a, int ctas) {
+  __shared__ float sums[kQkWarps][32];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, column = blockIdx.x * 32 + lane;
+  const int share = (ctas + kQkWarps - 1) / kQkWarps, begin = warp * share;
+  const int end = begin + share < ctas ? begin + share : ctas;
+  float s = 0.0f;
+  if (column < 2 * a.dim) {
+#pragma unroll 8
+    for (int c = begin; c < end; ++c) s += a.partials[static_cast<long long>(c) * 2 * a.dim + column];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || column >= 2 * a.dim) return;
+  s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kQkWarps; ++w) s += sums[w][lane];
+  const int which = column / a.dim;
+  if (!a.dgain[which]) return;
+  if (a.dgain_fp32) store_one<true>(a.dgain[which], column % a.dim, s);
+  else store_one<false>(a.dgain[which], column % a.dim, s);
+}
+
+int next_power(int x) {
+  int p = 1;
+  while (p < x) p *= 2;
+  return p;
+}
+
+// Whether heads fall into whole vectors of 8 for a lane.
+bool lanes_ok(const QkArgs& a) {
+  if (a.dim % 8) return false;
+  if (a.interleaved ? a.rotary % 8 : a.rotary % 16) return false;
+  return !a.rotary || reinterpret_cast<uintptr_t>(a.table) % 16 == 0;
+}
+
+// Whether all heads can then be read and written in one access a lane; the
+// others go element by element with the same arithmetic.
+bool vectors_ok(const QkArgs& a, bool fp32, bool backward) {
+  const uintptr_t align = fp32 ? 32 : 16;
+  for (int w = 0; w < 2; ++w) {
+    if ((w ? a.k_heads : a.q_heads) == 0) continue;
+    const Heads* all[3] = {&a.x[w], &a.out[w], backward ? &a.dy[w] : &a.x[w]};
+    for (const Heads* h : all)
+      if (reinterpret_cast<uintptr_t>(h->p) % align || h->token % 8 || h->head % 8) return false;
+  }
+  return true;
+}
+
+// CTAs of a launch over `rows` heads; the backward workspace has room for any.
 int qk_ctas(long long rows) {
   const long long want = (rows + kQkWarps - 1) / kQkWarps, most = 4LL * sm_count();
   return static_cast<int>(want < 1 ? 0 : want < most ? want : most);
+}
+
+template <bool kFp32, bool kBackward>
+int launch_qk(QkArgs& a, cudaStream_t s) {
+  const long long rows = a.tokens * (a.q_heads + a.k_heads);
+  int ctas = qk_ctas(rows);
+  if (lanes_ok(a)) {
+    // A warp takes a whole token while that gives every SM 16 warps (the
+    // token's cosines are read once); fewer tokens are cut into parts.
+    a.group = next_power(a.dim / 8);
+    const int heads = a.q_heads + a.k_heads, groups = 32 / a.group;
+    const long long most = (heads + groups - 1) / groups, wanted = 16LL * sm_count() / a.tokens;
+    const long long parts = wanted < 1 ? 1 : wanted < most ? wanted : most;
+    a.chunk_heads = static_cast<int>(((heads + parts - 1) / parts + groups - 1) / groups * groups);
+    a.chunks = (heads + a.chunk_heads - 1) / a.chunk_heads;
+    const long long want = (a.tokens * a.chunks + kQkWarps - 1) / kQkWarps, resident = 2LL * sm_count();
+    ctas = static_cast<int>(want < resident ? want : resident);
+    if (vectors_ok(a, kFp32, kBackward)) qk_vec_kernel<kFp32, kBackward, true><<<ctas, kQkThreads, 0, s>>>(a);
+    else qk_vec_kernel<kFp32, kBackward, false><<<ctas, kQkThreads, 0, s>>>(a);
+  } else {
+    qk_kernel<kFp32, kBackward><<<ctas, kQkThreads, 0, s>>>(a);
+  }
+  return ctas;
 }
 
 zero_status report(zero_status st, const char* text) {
@@ -277,10 +566,9 @@ zero_status zero_qk_norm_rope(const zero_qk_config* cfg, int64_t tokens, const z
   zfs::QkArgs a{};
   st = zfs::fill(cfg, tokens, q, k, q_gain, k_gain, table, positions, q_out, k_out, &a);
   if (st != ZERO_OK) return st;
-  const int ctas = zfs::qk_ctas(tokens * (cfg->q_heads + cfg->k_heads));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cfg->dtype == ZERO_GRAD_FP32) zfs::qk_kernel<true, false><<<ctas, zfs::kQkThreads, 0, s>>>(a);
-  else zfs::qk_kernel<false, false><<<ctas, zfs::kQkThreads, 0, s>>>(a);
+  if (cfg->dtype == ZERO_GRAD_FP32) zfs::launch_qk<true, false>(a, s);
+  else zfs::launch_qk<false, false>(a, s);
   return zfs::launched("norm and rotation launch");
 }
 
@@ -309,7 +597,7 @@ zero_status zero_qk_norm_rope_backward(const zero_qk_config* cfg, int64_t tokens
     return zfs::report(ZERO_EINVAL, "a gain gradient must be aligned device memory");
   zfs::QkArgs a{};
   const long long rows = tokens * (cfg->q_heads + cfg->k_heads);
-  const int ctas = zfs::qk_ctas(rows);
+  int ctas = 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (rows > 0) {
     st = zfs::fill(cfg, tokens, q, k, q_gain, k_gain, table, positions, dq, dk, &a);
@@ -328,8 +616,7 @@ zero_status zero_qk_norm_rope_backward(const zero_qk_config* cfg, int64_t tokens
     if (zfs::bad(workspace, 16, dev)) return zfs::report(ZERO_EINVAL, "workspace must be 16-byte aligned device memory");
     if (workspace_bytes < need) return zfs::report(ZERO_EINVAL, "workspace is too small");
     a.partials = static_cast<float*>(workspace);
-    if (cfg->dtype == ZERO_GRAD_FP32) zfs::qk_kernel<true, true><<<ctas, zfs::kQkThreads, 0, s>>>(a);
-    else zfs::qk_kernel<false, true><<<ctas, zfs::kQkThreads, 0, s>>>(a);
+    ctas = cfg->dtype == ZERO_GRAD_FP32 ? zfs::launch_qk<true, true>(a, s) : zfs::launch_qk<false, true>(a, s);
     st = zfs::launched("norm and rotation backward launch");
     if (st != ZERO_OK) return st;
   }
@@ -338,7 +625,7 @@ zero_status zero_qk_norm_rope_backward(const zero_qk_config* cfg, int64_t tokens
   a.dgain[0] = dq_gain;
   a.dgain[1] = dk_gain;
   a.dgain_fp32 = dgain_dtype == ZERO_GRAD_FP32;
-  zfs::qk_gain_kernel<<<(2 * a.dim + zfs::kQkThreads - 1) / zfs::kQkThreads, zfs::kQkThreads, 0, s>>>(a, ctas);
+  zfs::qk_gain_kernel<<<(2 * a.dim + 31) / 32, zfs::kQkThreads, 0, s>>>(a, ctas);
   return zfs::launched("gain gradient launch");
 }
 
