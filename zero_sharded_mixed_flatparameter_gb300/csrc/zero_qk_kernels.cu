@@ -8,10 +8,11 @@
 //
 // A head is read once and written once; everything between is fp32.  Bound by
 // memory, so the kernel for heads of whole vectors keeps enough bytes in
-// flight: a group of lanes holds a head, 8 elements (16 or 32 bytes) a lane, a
-// warp takes a token's heads kUnroll groups at a time, and the token's cosines
-// and sines stay in registers over its heads.  Other head sizes take one warp
-// per head with the head in shared memory.
+// flight: a group of lanes holds a head, two runs of 4 elements a lane placed so
+// that every rotated pair lies in one lane, a warp takes a token's heads
+// kUnroll groups at a time, and the token's cosines and sines stay in
+// registers over its heads.  Other head sizes take one warp per head with the
+// head in shared memory.
 
 #include <cmath>
 #include <cstdio>
@@ -161,74 +162,59 @@ __global__ void __launch_bounds__(kQkThreads) qk_kernel(const __grid_constant__ 
   }
 }
 
-// ---- heads of whole vectors -----------------------------------------------------------
+// ---- heads of whole vectors --------------------------------------------------
+// Four elements as loaded.
 template <bool kFp32>
-struct Vec8 {
-  uint4 lo, hi;  // hi: fp32 only
+struct Raw4 {
+  uint32_t w[kFp32 ? 4 : 2];
 };
 template <bool kFp32, bool kAligned>
-__device__ __forceinline__ Vec8<kFp32> load_vec(const void* p, long long at) {
-  Vec8<kFp32> v;
-  if constexpr (!kAligned) {
-    uint32_t w[8];
-#pragma unroll
-    for (int k = 0; k < (kFp32 ? 8 : 4); ++k) {
-      if constexpr (kFp32) {
-        w[k] = static_cast<const uint32_t*>(p)[at + k];
-      } else {
-        const uint16_t* q = static_cast<const uint16_t*>(p) + at + 2 * k;
-        w[k] = static_cast<uint32_t>(q[0]) | static_cast<uint32_t>(q[1]) << 16;
-      }
-    }
-    v.lo = make_uint4(w[0], w[1], w[2], w[3]);
-    if constexpr (kFp32) v.hi = make_uint4(w[4], w[5], w[6], w[7]);
+__device__ __forceinline__ Raw4<kFp32> load4(const void* p, long long at) {
+  Raw4<kFp32> v;
+  if constexpr (kFp32 && kAligned) {
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
+    v.w[0] = u.x; v.w[1] = u.y; v.w[2] = u.z; v.w[3] = u.w;
   } else if constexpr (kFp32) {
-    const float* q = static_cast<const float*>(p) + at;
-    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(v.lo.x), "=r"(v.lo.y), "=r"(v.lo.z), "=r"(v.lo.w), "=r"(v.hi.x), "=r"(v.hi.y), "=r"(v.hi.z),
-                   "=r"(v.hi.w)
-                 : "l"(q));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v.w[k] = static_cast<const uint32_t*>(p)[at + k];
+  } else if constexpr (kAligned) {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
+    v.w[0] = u.x; v.w[1] = u.y;
   } else {
-    v.lo = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) v.w[k] = static_cast<uint32_t>(q[2 * k]) | static_cast<uint32_t>(q[2 * k + 1]) << 16;
   }
   return v;
 }
 template <bool kFp32>
-__device__ __forceinline__ void widen(const Vec8<kFp32>& v, float* x) {
-  const uint32_t l[4] = {v.lo.x, v.lo.y, v.lo.z, v.lo.w};
+__device__ __forceinline__ void widen(const Raw4<kFp32>& v, float* x) {
   if constexpr (kFp32) {
-    const uint32_t h[4] = {v.hi.x, v.hi.y, v.hi.z, v.hi.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x[k] = __uint_as_float(l[k]);
-      x[4 + k] = __uint_as_float(h[k]);
-    }
+    for (int k = 0; k < 4; ++k) x[k] = __uint_as_float(v.w[k]);
   } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      x[2 * k] = bf16_lo(l[k]);
-      x[2 * k + 1] = bf16_hi(l[k]);
+    for (int k = 0; k < 2; ++k) {
+      x[2 * k] = bf16_lo(v.w[k]);
+      x[2 * k + 1] = bf16_hi(v.w[k]);
     }
   }
 }
 template <bool kFp32, bool kAligned>
-__device__ __forceinline__ void store_vec(void* p, long long at, const float* x) {
-  if constexpr (!kAligned) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) store_one<kFp32>(p, at + k, x[k]);
-  } else if constexpr (kFp32) {
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<float*>(p) + at),
-                 "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
-                 : "memory");
+__device__ __forceinline__ void store4(void* p, long long at, const float* x) {
+  if constexpr (kFp32 && kAligned) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(x[0], x[1], x[2], x[3]);
+  } else if constexpr (kAligned) {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
   } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) =
-        make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) store_one<kFp32>(p, at + k, x[k]);
   }
 }
 
-// A lane's 8 elements turned: its partner's 8 come from the lane `partner`
-// (halves), or the pairs lie in the lane (interleaved).  sn carries the sign.
-__device__ __forceinline__ void turn(bool interleaved, int partner, const float* cs, const float* sn, float* y) {
+// The lane's four pairs turned; sn carries the sign.  Halves: element k pairs
+// with 4 + k; interleaved: 2k with 2k + 1.
+__device__ __forceinline__ void turn(bool interleaved, const float* cs, const float* sn, float* y) {
   if (interleaved) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -238,56 +224,49 @@ __device__ __forceinline__ void turn(bool interleaved, int partner, const float*
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float other = __shfl_sync(0xffffffffu, y[k], partner);
-      y[k] = fmaf(y[k], cs[k], other * sn[k]);
+    for (int k = 0; k < 4; ++k) {
+      const float one = y[k], two = y[4 + k];
+      y[k] = fmaf(one, cs[k], -two * sn[k]);
+      y[4 + k] = fmaf(two, cs[k], one * sn[k]);
     }
   }
 }
 
 template <bool kFp32, bool kBackward, bool kAligned>
 __global__ void __launch_bounds__(kQkThreads, 2) qk_vec_kernel(const __grid_constant__ QkArgs a) {
-  constexpr int kUnroll = kBackward ? 2 : 4;  // heads in flight per group of lanes
+  // heads in flight per group of lanes: 16 registers of queries or keys, with
+  // as many of gradients in the backward pass
+  constexpr int kUnroll = (kFp32 ? 4 : 8) / (kBackward ? 2 : 1);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int in_group = lane % a.group, groups = 32 / a.group, my_group = lane / a.group;
-  const int d0 = in_group * 8, half = a.rotary / 2;
-  const bool active = d0 < a.dim, turned = d0 < a.rotary, first = d0 < half;
+  const int half = a.rotary / 2;
   const bool interleaved = a.interleaved != 0;
-  const int partner = !turned ? lane : first ? lane + half / 8 : lane - half / 8;
+  const bool active = in_group * 8 < a.dim, turned = in_group * 8 < a.rotary;
+  // the lane's two runs of 4 elements, and its first pair
+  const int d0 = turned && !interleaved ? in_group * 4 : in_group * 8;
+  const int d1 = turned && !interleaved ? half + in_group * 4 : in_group * 8 + 4;
+  const int pair = in_group * 4;
   const float inv_dim = 1.0f / static_cast<float>(a.dim);
-  float dgain[2][8] = {};
-  const long long units = a.tokens * a.chunks;
-  for (long long u = static_cast<long long>(blockIdx.x) * kQkWarps + warp; u < units;
-       u += static_cast<long long>(gridDim.x) * kQkWarps) {
-    const long long token = u / a.chunks;
+  float gain[2][8], dgain[2][8] = {};
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) gain[which][k] = active ? load_gain(a, which, k < 4 ? d0 + k : d1 + k - 4) : 0.0f;
+  }
+  const long long units = a.tokens * a.chunks, stride = static_cast<long long>(gridDim.x) * kQkWarps;
+  for (long long u = static_cast<long long>(blockIdx.x) * kQkWarps + warp; u < units; u += stride) {
+    const long long token = a.chunks == 1 ? u : u / a.chunks;
     const int begin = static_cast<int>(u - token * a.chunks) * a.chunk_heads;
     const long long position = a.positions ? a.positions[token] : token;
     const bool live = position >= 0 && position < a.n_positions;
-    float cs[8], sn[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      cs[k] = 1.0f;
-      sn[k] = 0.0f;
-    }
+    float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {};
     if (live && turned) {
-      const float* row = a.table + position * a.rotary;
+      const float* row = a.table + position * a.rotary + pair;
+      const float4 c = *reinterpret_cast<const float4*>(row);
+      const float4 s = *reinterpret_cast<const float4*>(row + half);
       const float sign = kBackward ? -1.0f : 1.0f;
-      if (interleaved) {
-        const float4 c = *reinterpret_cast<const float4*>(row + d0 / 2);
-        const float4 s = *reinterpret_cast<const float4*>(row + half + d0 / 2);
-        cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
-        sn[0] = sign * s.x; sn[1] = sign * s.y; sn[2] = sign * s.z; sn[3] = sign * s.w;
-      } else {
-        const int pair = first ? d0 : d0 - half;
-        const float own = first ? -sign : sign;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float4 c = *reinterpret_cast<const float4*>(row + pair + 4 * q);
-          const float4 s = *reinterpret_cast<const float4*>(row + half + pair + 4 * q);
-          cs[4 * q] = c.x; cs[4 * q + 1] = c.y; cs[4 * q + 2] = c.z; cs[4 * q + 3] = c.w;
-          sn[4 * q] = own * s.x; sn[4 * q + 1] = own * s.y; sn[4 * q + 2] = own * s.z; sn[4 * q + 3] = own * s.w;
-        }
-      }
+      cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
+      sn[0] = sign * s.x; sn[1] = sign * s.y; sn[2] = sign * s.z; sn[3] = sign * s.w;
     }
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
@@ -295,28 +274,32 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_vec_kernel(const __grid_cons
       const int shift = which ? a.q_heads : 0, count = which ? a.k_heads : a.q_heads;
       const int lo = begin - shift > 0 ? begin - shift : 0;
       const int end = begin + a.chunk_heads - shift < count ? begin + a.chunk_heads - shift : count;
-      if (lo >= end) continue;
       const Heads &hx = a.x[which], &hy = a.dy[which], &ho = a.out[which];
-      const long long from = token * hx.token + d0, grad = token * hy.token + d0, to = token * ho.token + d0;
-      float gain[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) gain[k] = active ? load_gain(a, which, d0 + k) : 0.0f;
       for (int h0 = lo; h0 < end; h0 += groups * kUnroll) {
-        Vec8<kFp32> vx[kUnroll], vy[kUnroll];
+        Raw4<kFp32> vx[kUnroll][2], vy[kBackward ? kUnroll : 1][2];
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
           const int h = h0 + i * groups + my_group;
-          vx[i].lo = vx[i].hi = vy[i].lo = vy[i].hi = make_uint4(0, 0, 0, 0);
+          vx[i][0] = vx[i][1] = Raw4<kFp32>{};
+          if constexpr (kBackward) vy[i][0] = vy[i][1] = Raw4<kFp32>{};
           if (live && active && h < end) {
-            vx[i] = load_vec<kFp32, kAligned>(hx.p, from + h * hx.head);
-            if constexpr (kBackward) vy[i] = load_vec<kFp32, kAligned>(hy.p, grad + h * hy.head);
+            const long long from = token * hx.token + h * hx.head;
+            vx[i][0] = load4<kFp32, kAligned>(hx.p, from + d0);
+            vx[i][1] = load4<kFp32, kAligned>(hx.p, from + d1);
+            if constexpr (kBackward) {
+              const long long grad = token * hy.token + h * hy.head;
+              vy[i][0] = load4<kFp32, kAligned>(hy.p, grad + d0);
+              vy[i][1] = load4<kFp32, kAligned>(hy.p, grad + d1);
+            }
           }
         }
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
+          if (h0 + i * groups >= end) break;  // the same for the whole warp
           const int h = h0 + i * groups + my_group;
           float x[8], y[8];
-          widen<kFp32>(vx[i], x);
+          widen<kFp32>(vx[i][0], x);
+          widen<kFp32>(vx[i][1], x + 4);
           float sq = 0.0f;
 #pragma unroll
           for (int k = 0; k < 8; ++k) sq = fmaf(x[k], x[k], sq);
@@ -324,14 +307,18 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_vec_kernel(const __grid_cons
             for (int o = a.group / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
             const float rstd = rsqrtf(fmaf(sq, inv_dim, a.eps));
 #pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = x[k] * rstd * gain[k];
-            turn(interleaved, partner, cs, sn, y);
+            for (int k = 0; k < 8; ++k) y[k] = x[k] * rstd * gain[which][k];
+            turn(interleaved, cs, sn, y);
           } else {
-            widen<kFp32>(vy[i], y);
-            turn(interleaved, partner, cs, sn, y);  // h: the gradient turned back
-            float dot = 0.0f;
+            widen<kFp32>(vy[i][0], y);
+            widen<kFp32>(vy[i][1], y + 4);
+            turn(interleaved, cs, sn, y);  // h: the gradient turned back
+            float dot = 0.0f, g[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) dot = fmaf(y[k] * gain[k], x[k], dot);
+            for (int k = 0; k < 8; ++k) {
+              g[k] = y[k] * gain[which][k];
+              dot = fmaf(g[k], x[k], dot);
+            }
             for (int o = a.group / 2; o > 0; o >>= 1) {
               sq += __shfl_xor_sync(0xffffffffu, sq, o);
               dot += __shfl_xor_sync(0xffffffffu, dot, o);
@@ -343,7 +330,7 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_vec_kernel(const __grid_cons
             for (int k = 0; k < 8; ++k) {
               const float xn = x[k] * rstd;
               if (real) dgain[which][k] = fmaf(y[k], xn, dgain[which][k]);
-              y[k] = rstd * fmaf(-xn, mean, y[k] * gain[k]);
+              y[k] = rstd * fmaf(-xn, mean, g[k]);
             }
           }
           if (active && h < end) {
@@ -351,7 +338,9 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_vec_kernel(const __grid_cons
 #pragma unroll
               for (int k = 0; k < 8; ++k) y[k] = 0.0f;
             }
-            store_vec<kFp32, kAligned>(ho.p, to + h * ho.head, y);
+            const long long to = token * ho.token + h * ho.head;
+            store4<kFp32, kAligned>(ho.p, to + d0, y);
+            store4<kFp32, kAligned>(ho.p, to + d1, y + 4);
           }
         }
       }
@@ -369,7 +358,7 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_vec_kernel(const __grid_cons
       __syncthreads();
       if (my_group == 0 && active) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sums[warp][d0 + k] = dgain[which][k];
+        for (int k = 0; k < 8; ++k) sums[warp][k < 4 ? d0 + k : d1 + k - 4] = dgain[which][k];
       }
       __syncthreads();
       for (int d = threadIdx.x; d < a.dim; d += kQkThreads) {
@@ -383,13 +372,16 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_vec_kernel(const __grid_cons
 }
 
 // The gain gradients from the CTAs' sums: 32 columns per CTA, every warp a
-// contiguous share of the CTAs, then warp after warp.
-__global__ void __launch_bounds__(kQkThreads) qk_gain_kernel(const __grid_constant__ QkArgs a, int ctas) {
-  __shared__ float sums[kQkWarps][32];
+// contiguous share of the CTAs, then warp after warp.  Launched so that it may
+// become resident while the pass before it finishes; it waits for that pass.
+constexpr int kGainThreads = 1024, kGainWarps = kGainThreads / 32;
+__global__ void __launch_bounds__(kGainThreads) qk_gain_kernel(const __grid_constant__ QkArgs a, int ctas) {
+  __shared__ float sums[kGainWarps][32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, column = blockIdx.x * 32 + lane;
-  const int share = (ctas + kQkWarps - 1) / kQkWarps, begin = warp * share;
+  const int share = (ctas + kGainWarps - 1) / kGainWarps, begin = warp * share;
   const int end = begin + share < ctas ? begin + share : ctas;
   float s = 0.0f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (column < 2 * a.dim) {
 #pragma unroll 8
     for (int c = begin; c < end; ++c) s += a.partials[static_cast<long long>(c) * 2 * a.dim + column];
@@ -399,7 +391,7 @@ __global__ void __launch_bounds__(kQkThreads) qk_gain_kernel(const __grid_consta
   if (warp != 0 || column >= 2 * a.dim) return;
   s = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kQkWarps; ++w) s += sums[w][lane];
+  for (int w = 0; w < kGainWarps; ++w) s += sums[w][lane];
   const int which = column / a.dim;
   if (!a.dgain[which]) return;
   if (a.dgain_fp32) store_one<true>(a.dgain[which], column % a.dim, s);
@@ -415,19 +407,19 @@ int next_power(int x) {
 // Whether heads fall into whole vectors of 8 for a lane.
 bool lanes_ok(const QkArgs& a) {
   if (a.dim % 8) return false;
-  if (a.interleaved ? a.rotary % 8 : a.rotary % 16) return false;
+  if (a.rotary % 8) return false;
   return !a.rotary || reinterpret_cast<uintptr_t>(a.table) % 16 == 0;
 }
 
 // Whether all heads can then be read and written in one access a lane; the
 // others go element by element with the same arithmetic.
 bool vectors_ok(const QkArgs& a, bool fp32, bool backward) {
-  const uintptr_t align = fp32 ? 32 : 16;
+  const uintptr_t align = fp32 ? 16 : 8;
   for (int w = 0; w < 2; ++w) {
     if ((w ? a.k_heads : a.q_heads) == 0) continue;
     const Heads* all[3] = {&a.x[w], &a.out[w], backward ? &a.dy[w] : &a.x[w]};
     for (const Heads* h : all)
-      if (reinterpret_cast<uintptr_t>(h->p) % align || h->token % 8 || h->head % 8) return false;
+      if (reinterpret_cast<uintptr_t>(h->p) % align || h->token % 4 || h->head % 4) return false;
   }
   return true;
 }
@@ -625,7 +617,16 @@ zero_status zero_qk_norm_rope_backward(const zero_qk_config* cfg, int64_t tokens
   a.dgain[0] = dq_gain;
   a.dgain[1] = dk_gain;
   a.dgain_fp32 = dgain_dtype == ZERO_GRAD_FP32;
-  zfs::qk_gain_kernel<<<(2 * a.dim + 31) / 32, zfs::kQkThreads, 0, s>>>(a, ctas);
+  cudaLaunchConfig_t launch = {};
+  launch.gridDim = dim3((2 * a.dim + 31) / 32);
+  launch.blockDim = dim3(zfs::kGainThreads);
+  launch.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  launch.attrs = attr;
+  launch.numAttrs = 1;
+  cudaLaunchKernelEx(&launch, zfs::qk_gain_kernel, a, ctas);
   return zfs::launched("gain gradient launch");
 }
 
