@@ -8,10 +8,11 @@
 //
 // A head is read once and written once; everything between is fp32.  Bound by
 // memory, so the kernel for heads of whole vectors keeps enough bytes in
-// flight: a group of lanes holds a head, two runs of 4 elements a lane placed so
-// that every rotated pair lies in one lane, a warp takes a token's heads
-// kUnroll groups at a time, and the token's cosines and sines stay in
-// registers over its heads.  Other head sizes take one warp per head with the
+// flight and instructions few: a group of lanes holds a head, two runs of 4
+// elements a lane placed so that every rotated pair lies in one lane, a warp
+// takes a token's heads kUnroll groups at a time, the token's cosines and sines
+// stay in registers over its heads, the gains in shared memory, and addresses
+// move by constant steps.  Other head sizes take one warp per head with the
 // head in shared memory.
 
 #include <cmath>
@@ -163,169 +164,232 @@ __global__ void __launch_bounds__(kQkThreads) qk_kernel(const __grid_constant__ 
 }
 
 // ---- heads of whole vectors --------------------------------------------------
-// Four elements as loaded.
+// A lane's eight elements as loaded: two runs of 4.
 template <bool kFp32>
-struct Raw4 {
-  uint32_t w[kFp32 ? 4 : 2];
+struct Raw8 {
+  uint32_t w[kFp32 ? 8 : 4];
 };
 template <bool kFp32, bool kAligned>
-__device__ __forceinline__ Raw4<kFp32> load4(const void* p, long long at) {
-  Raw4<kFp32> v;
+__device__ __forceinline__ void load4(const char* p, uint32_t* w) {
   if constexpr (kFp32 && kAligned) {
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
-    v.w[0] = u.x; v.w[1] = u.y; v.w[2] = u.z; v.w[3] = u.w;
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
   } else if constexpr (kFp32) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v.w[k] = static_cast<const uint32_t*>(p)[at + k];
+    for (int k = 0; k < 4; ++k) w[k] = reinterpret_cast<const uint32_t*>(p)[k];
   } else if constexpr (kAligned) {
-    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at);
-    v.w[0] = u.x; v.w[1] = u.y;
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x; w[1] = u.y;
   } else {
-    const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+    const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) v.w[k] = static_cast<uint32_t>(q[2 * k]) | static_cast<uint32_t>(q[2 * k + 1]) << 16;
+    for (int k = 0; k < 2; ++k) w[k] = static_cast<uint32_t>(q[2 * k]) | static_cast<uint32_t>(q[2 * k + 1]) << 16;
   }
-  return v;
+}
+// The lane's pairs: x[k] and x[4 + k] turn together.  Halves: elements k of
+// the two runs; interleaved: neighbours.
+template <bool kFp32>
+__device__ __forceinline__ void widen(const Raw8<kFp32>& v, bool interleaved, float* x) {
+  if constexpr (kFp32) {
+    if (interleaved) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[k] = __uint_as_float(v.w[2 * k]);
+        x[4 + k] = __uint_as_float(v.w[2 * k + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = __uint_as_float(v.w[k]);
+    }
+  } else {
+    if (interleaved) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[k] = bf16_lo(v.w[k]);
+        x[4 + k] = bf16_hi(v.w[k]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[2 * k] = bf16_lo(v.w[k]);
+        x[2 * k + 1] = bf16_hi(v.w[k]);
+      }
+    }
+  }
 }
 template <bool kFp32>
-__device__ __forceinline__ void widen(const Raw4<kFp32>& v, float* x) {
+__device__ __forceinline__ void narrow(const float* x, bool interleaved, Raw8<kFp32>* v) {
   if constexpr (kFp32) {
+    if (interleaved) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) x[k] = __uint_as_float(v.w[k]);
+      for (int k = 0; k < 4; ++k) {
+        v->w[2 * k] = __float_as_uint(x[k]);
+        v->w[2 * k + 1] = __float_as_uint(x[4 + k]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v->w[k] = __float_as_uint(x[k]);
+    }
   } else {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      x[2 * k] = bf16_lo(v.w[k]);
-      x[2 * k + 1] = bf16_hi(v.w[k]);
-    }
+    for (int k = 0; k < 4; ++k)
+      v->w[k] = interleaved ? pack_bf16x2(x[k], x[4 + k]) : pack_bf16x2(x[2 * k], x[2 * k + 1]);
   }
 }
 template <bool kFp32, bool kAligned>
-__device__ __forceinline__ void store4(void* p, long long at, const float* x) {
+__device__ __forceinline__ void store4(char* p, const uint32_t* w) {
   if constexpr (kFp32 && kAligned) {
-    *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  } else if constexpr (kFp32) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) reinterpret_cast<uint32_t*>(p)[k] = w[k];
   } else if constexpr (kAligned) {
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
   } else {
+    uint16_t* q = reinterpret_cast<uint16_t*>(p);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) store_one<kFp32>(p, at + k, x[k]);
-  }
-}
-
-// The lane's four pairs turned; sn carries the sign.  Halves: element k pairs
-// with 4 + k; interleaved: 2k with 2k + 1.
-__device__ __forceinline__ void turn(bool interleaved, const float* cs, const float* sn, float* y) {
-  if (interleaved) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float one = y[2 * k], two = y[2 * k + 1];
-      y[2 * k] = fmaf(one, cs[k], -two * sn[k]);
-      y[2 * k + 1] = fmaf(two, cs[k], one * sn[k]);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float one = y[k], two = y[4 + k];
-      y[k] = fmaf(one, cs[k], -two * sn[k]);
-      y[4 + k] = fmaf(two, cs[k], one * sn[k]);
+    for (int k = 0; k < 2; ++k) {
+      q[2 * k] = static_cast<uint16_t>(w[k]);
+      q[2 * k + 1] = static_cast<uint16_t>(w[k] >> 16);
     }
   }
 }
 
-template <bool kFp32, bool kBackward, bool kAligned>
-__global__ void __launch_bounds__(kQkThreads, 2) qk_vec_kernel(const __grid_constant__ QkArgs a) {
-  // heads in flight per group of lanes: 16 registers of queries or keys, with
-  // as many of gradients in the backward pass
-  constexpr int kUnroll = (kFp32 ? 4 : 8) / (kBackward ? 2 : 1);
+// The lane's four pairs turned (kBack: turned back).
+template <bool kBack>
+__device__ __forceinline__ void turn(const float* cs, const float* sn, float* y) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float one = y[k], two = y[4 + k], a = two * sn[k], b = one * sn[k];
+    y[k] = fmaf(one, cs[k], kBack ? a : -a);
+    y[4 + k] = fmaf(two, cs[k], kBack ? -b : b);
+  }
+}
+
+// kGroup: lanes per head, and aligned heads; 0: a.group lanes, any alignment.
+template <bool kFp32, bool kBackward, int kGroup>
+__global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 4) qk_vec_kernel(const __grid_constant__ QkArgs a) {
+  constexpr bool kAligned = kGroup != 0;
+  constexpr int kUnroll = kFp32 ? 2 : 4;  // heads in flight per group of lanes
+  constexpr long long kSize = kFp32 ? 4 : 2;
+  // in the order of a lane's pairs: [query, key][lane of the group][8]
+  __shared__ __align__(16) float gains[2][kMaxHeadDim];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int in_group = lane % a.group, groups = 32 / a.group, my_group = lane / a.group;
+  const int group = kGroup ? kGroup : a.group;
+  const int in_group = lane % group, groups = 32 / group, my_group = lane / group;
   const int half = a.rotary / 2;
   const bool interleaved = a.interleaved != 0;
   const bool active = in_group * 8 < a.dim, turned = in_group * 8 < a.rotary;
-  // the lane's two runs of 4 elements, and its first pair
+  // the lane's two runs of 4 elements
   const int d0 = turned && !interleaved ? in_group * 4 : in_group * 8;
   const int d1 = turned && !interleaved ? half + in_group * 4 : in_group * 8 + 4;
-  const int pair = in_group * 4;
-  const float inv_dim = 1.0f / static_cast<float>(a.dim);
-  float gain[2][8], dgain[2][8] = {};
+  auto element = [&](int k) {  // of the lane's k-th value in pair order
+    const int e = interleaved ? (k < 4 ? 2 * k : 2 * (k - 4) + 1) : k;
+    return e < 4 ? d0 + e : d1 + e - 4;
+  };
+  if (warp == 0 && my_group == 0 && active) {
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
+    for (int which = 0; which < 2; ++which) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) gain[which][k] = active ? load_gain(a, which, k < 4 ? d0 + k : d1 + k - 4) : 0.0f;
+      for (int k = 0; k < 8; ++k) gains[which][in_group * 8 + k] = load_gain(a, which, element(k));
+    }
   }
+  __syncthreads();
+  const float inv_dim = 1.0f / static_cast<float>(a.dim);
+  float dgain[2][8] = {};
   const long long units = a.tokens * a.chunks, stride = static_cast<long long>(gridDim.x) * kQkWarps;
-  for (long long u = static_cast<long long>(blockIdx.x) * kQkWarps + warp; u < units; u += stride) {
+  long long u = static_cast<long long>(blockIdx.x) * kQkWarps + warp;
+  auto position_of = [&](long long unit) -> long long {
+    if (unit >= units) return -1;
+    const long long token = a.chunks == 1 ? unit : unit / a.chunks;
+    return a.positions ? a.positions[token] : token;
+  };
+  long long position = position_of(u);
+  for (; u < units; u += stride) {
     const long long token = a.chunks == 1 ? u : u / a.chunks;
-    const int begin = static_cast<int>(u - token * a.chunks) * a.chunk_heads;
-    const long long position = a.positions ? a.positions[token] : token;
+    const int begin = a.chunks == 1 ? 0 : static_cast<int>(u - token * a.chunks) * a.chunk_heads;
     const bool live = position >= 0 && position < a.n_positions;
     float cs[4] = {1.0f, 1.0f, 1.0f, 1.0f}, sn[4] = {};
     if (live && turned) {
-      const float* row = a.table + position * a.rotary + pair;
+      const float* row = a.table + position * a.rotary + in_group * 4;
       const float4 c = *reinterpret_cast<const float4*>(row);
       const float4 s = *reinterpret_cast<const float4*>(row + half);
-      const float sign = kBackward ? -1.0f : 1.0f;
       cs[0] = c.x; cs[1] = c.y; cs[2] = c.z; cs[3] = c.w;
-      sn[0] = sign * s.x; sn[1] = sign * s.y; sn[2] = sign * s.z; sn[3] = sign * s.w;
+      sn[0] = s.x; sn[1] = s.y; sn[2] = s.z; sn[3] = s.w;
     }
+    position = position_of(u + stride);  // of the next token, while this one is worked on
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       // the part of this unit's heads that are queries (keys)
       const int shift = which ? a.q_heads : 0, count = which ? a.k_heads : a.q_heads;
-      const int lo = begin - shift > 0 ? begin - shift : 0;
+      const int lo = begin > shift ? begin - shift : 0;
       const int end = begin + a.chunk_heads - shift < count ? begin + a.chunk_heads - shift : count;
+      if (lo >= end) continue;
       const Heads &hx = a.x[which], &hy = a.dy[which], &ho = a.out[which];
-      for (int h0 = lo; h0 < end; h0 += groups * kUnroll) {
-        Raw4<kFp32> vx[kUnroll][2], vy[kBackward ? kUnroll : 1][2];
+      const int mine = lo + my_group;
+      const long long run = (d1 - d0) * kSize;
+      const char* px = static_cast<const char*>(hx.p) + (token * hx.token + mine * hx.head + d0) * kSize;
+      const char* py = kBackward ? static_cast<const char*>(hy.p) + (token * hy.token + mine * hy.head + d0) * kSize : nullptr;
+      char* po = static_cast<char*>(ho.p) + (token * ho.token + mine * ho.head + d0) * kSize;
+      const long long step_x = hx.head * groups * kSize, step_y = hy.head * groups * kSize, step_o = ho.head * groups * kSize;
+      float gain[8];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float4 g = *reinterpret_cast<const float4*>(&gains[which][(active ? in_group * 8 : 0) + 4 * q]);
+        gain[4 * q] = g.x; gain[4 * q + 1] = g.y; gain[4 * q + 2] = g.z; gain[4 * q + 3] = g.w;
+      }
+      int left = active ? end - mine : 0;  // heads from the lane's own on; > 0: it has one
+#pragma unroll 1
+      for (int h0 = lo; h0 < end; h0 += groups * kUnroll, left -= groups * kUnroll) {
+        Raw8<kFp32> vx[kUnroll], vy[kUnroll];
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
-          const int h = h0 + i * groups + my_group;
-          vx[i][0] = vx[i][1] = Raw4<kFp32>{};
-          if constexpr (kBackward) vy[i][0] = vy[i][1] = Raw4<kFp32>{};
-          if (live && active && h < end) {
-            const long long from = token * hx.token + h * hx.head;
-            vx[i][0] = load4<kFp32, kAligned>(hx.p, from + d0);
-            vx[i][1] = load4<kFp32, kAligned>(hx.p, from + d1);
+          vx[i] = Raw8<kFp32>{};
+          if constexpr (kBackward) vy[i] = Raw8<kFp32>{};
+          if (left > i * groups) {
+            load4<kFp32, kAligned>(px, vx[i].w);
+            load4<kFp32, kAligned>(px + run, vx[i].w + (kFp32 ? 4 : 2));
             if constexpr (kBackward) {
-              const long long grad = token * hy.token + h * hy.head;
-              vy[i][0] = load4<kFp32, kAligned>(hy.p, grad + d0);
-              vy[i][1] = load4<kFp32, kAligned>(hy.p, grad + d1);
+              load4<kFp32, kAligned>(py, vy[i].w);
+              load4<kFp32, kAligned>(py + run, vy[i].w + (kFp32 ? 4 : 2));
             }
           }
+          px += step_x;
+          if constexpr (kBackward) py += step_y;
         }
 #pragma unroll
         for (int i = 0; i < kUnroll; ++i) {
           if (h0 + i * groups >= end) break;  // the same for the whole warp
-          const int h = h0 + i * groups + my_group;
+          const bool mine_too = left > i * groups;
           float x[8], y[8];
-          widen<kFp32>(vx[i][0], x);
-          widen<kFp32>(vx[i][1], x + 4);
+          widen<kFp32>(vx[i], interleaved, x);
           float sq = 0.0f;
 #pragma unroll
           for (int k = 0; k < 8; ++k) sq = fmaf(x[k], x[k], sq);
           if constexpr (!kBackward) {
-            for (int o = a.group / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+#pragma unroll
+            for (int o = group / 2; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
             const float rstd = rsqrtf(fmaf(sq, inv_dim, a.eps));
 #pragma unroll
-            for (int k = 0; k < 8; ++k) y[k] = x[k] * rstd * gain[which][k];
-            turn(interleaved, cs, sn, y);
+            for (int k = 0; k < 8; ++k) y[k] = x[k] * rstd * gain[k];
+            turn<false>(cs, sn, y);
           } else {
-            widen<kFp32>(vy[i][0], y);
-            widen<kFp32>(vy[i][1], y + 4);
-            turn(interleaved, cs, sn, y);  // h: the gradient turned back
+            widen<kFp32>(vy[i], interleaved, y);
+            turn<true>(cs, sn, y);  // h: the gradient turned back
             float dot = 0.0f, g[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              g[k] = y[k] * gain[which][k];
+              g[k] = y[k] * gain[k];
               dot = fmaf(g[k], x[k], dot);
             }
-            for (int o = a.group / 2; o > 0; o >>= 1) {
+#pragma unroll
+            for (int o = group / 2; o > 0; o >>= 1) {
               sq += __shfl_xor_sync(0xffffffffu, sq, o);
               dot += __shfl_xor_sync(0xffffffffu, dot, o);
             }
             const float rstd = rsqrtf(fmaf(sq, inv_dim, a.eps));
             const float mean = dot * rstd * inv_dim;  // mean(gain h xn)
-            const bool real = live && h < end;        // else 0 * inf for eps 0
+            const bool real = live && mine_too;       // else 0 * inf for eps 0, or what is behind padding
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const float xn = x[k] * rstd;
@@ -333,15 +397,14 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_vec_kernel(const __grid_cons
               y[k] = rstd * fmaf(-xn, mean, g[k]);
             }
           }
-          if (active && h < end) {
-            if (!live) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k) y[k] = 0.0f;
-            }
-            const long long to = token * ho.token + h * ho.head;
-            store4<kFp32, kAligned>(ho.p, to + d0, y);
-            store4<kFp32, kAligned>(ho.p, to + d1, y + 4);
+          if (mine_too) {
+            Raw8<kFp32> out;
+            narrow<kFp32>(y, interleaved, &out);
+            if (!live) out = Raw8<kFp32>{};
+            store4<kFp32, kAligned>(po, out.w);
+            store4<kFp32, kAligned>(po + run, out.w + (kFp32 ? 4 : 2));
           }
+          po += step_o;
         }
       }
     }
@@ -353,12 +416,12 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_vec_kernel(const __grid_cons
     for (int which = 0; which < 2; ++which) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        for (int o = a.group; o < 32; o <<= 1) dgain[which][k] += __shfl_xor_sync(0xffffffffu, dgain[which][k], o);
+        for (int o = group; o < 32; o <<= 1) dgain[which][k] += __shfl_xor_sync(0xffffffffu, dgain[which][k], o);
       }
       __syncthreads();
       if (my_group == 0 && active) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sums[warp][k < 4 ? d0 + k : d1 + k - 4] = dgain[which][k];
+        for (int k = 0; k < 8; ++k) sums[warp][element(k)] = dgain[which][k];
       }
       __syncthreads();
       for (int d = threadIdx.x; d < a.dim; d += kQkThreads) {
@@ -443,10 +506,16 @@ int launch_qk(QkArgs& a, cudaStream_t s) {
     const long long parts = wanted < 1 ? 1 : wanted < most ? wanted : most;
     a.chunk_heads = static_cast<int>(((heads + parts - 1) / parts + groups - 1) / groups * groups);
     a.chunks = (heads + a.chunk_heads - 1) / a.chunk_heads;
-    const long long want = (a.tokens * a.chunks + kQkWarps - 1) / kQkWarps, resident = 2LL * sm_count();
+    const long long want = (a.tokens * a.chunks + kQkWarps - 1) / kQkWarps, resident = (kBackward ? 2LL : 4LL) * sm_count();
     ctas = static_cast<int>(want < resident ? want : resident);
-    if (vectors_ok(a, kFp32, kBackward)) qk_vec_kernel<kFp32, kBackward, true><<<ctas, kQkThreads, 0, s>>>(a);
-    else qk_vec_kernel<kFp32, kBackward, false><<<ctas, kQkThreads, 0, s>>>(a);
+    const int group = vectors_ok(a, kFp32, kBackward) ? a.group : 0;
+    switch (group) {
+      case 4: qk_vec_kernel<kFp32, kBackward, 4><<<ctas, kQkThreads, 0, s>>>(a); break;
+      case 8: qk_vec_kernel<kFp32, kBackward, 8><<<ctas, kQkThreads, 0, s>>>(a); break;
+      case 16: qk_vec_kernel<kFp32, kBackward, 16><<<ctas, kQkThreads, 0, s>>>(a); break;
+      case 32: qk_vec_kernel<kFp32, kBackward, 32><<<ctas, kQkThreads, 0, s>>>(a); break;
+      default: qk_vec_kernel<kFp32, kBackward, 0><<<ctas, kQkThreads, 0, s>>>(a);
+    }
   } else {
     qk_kernel<kFp32, kBackward><<<ctas, kQkThreads, 0, s>>>(a);
   }
