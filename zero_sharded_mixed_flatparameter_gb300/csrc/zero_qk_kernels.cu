@@ -266,11 +266,19 @@ __device__ __forceinline__ void turn(const float* cs, const float* sn, float* y)
   }
 }
 
+// CTAs of the vector kernel on an SM: 32 warps forward (64 registers), 20
+// backward (96).
+constexpr int kVecThreads = 128, kVecWarps = kVecThreads / 32;
+template <bool kBackward>
+constexpr int kVecCtas = kBackward ? 5 : 8;
+
 // kGroup: lanes per head, and aligned heads; 0: a.group lanes, any alignment.
 template <bool kFp32, bool kBackward, int kGroup>
-__global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 4) qk_vec_kernel(const __grid_constant__ QkArgs a) {
+__global__ void __launch_bounds__(kVecThreads, kVecCtas<kBackward>)
+    qk_vec_kernel(const __grid_constant__ QkArgs a) {
+  constexpr int kThreads = kVecThreads, kWarps = kVecWarps;
   constexpr bool kAligned = kGroup != 0;
-  constexpr int kUnroll = kFp32 ? 2 : 4;  // heads in flight per group of lanes
+  constexpr int kUnroll = kBackward ? (kFp32 ? 1 : 2) : kFp32 ? 2 : 4;  // heads in flight per group of lanes
   constexpr long long kSize = kFp32 ? 4 : 2;
   // in the order of a lane's pairs: [query, key][lane of the group][8]
   __shared__ __align__(16) float gains[2][kMaxHeadDim];
@@ -296,14 +304,18 @@ __global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 4) qk_vec_kernel(c
   }
   __syncthreads();
   const float inv_dim = 1.0f / static_cast<float>(a.dim);
-  float dgain[2][8] = {};
-  const long long units = a.tokens * a.chunks, stride = static_cast<long long>(gridDim.x) * kQkWarps;
-  long long u = static_cast<long long>(blockIdx.x) * kQkWarps + warp;
+  const long long units = a.tokens * a.chunks, stride = static_cast<long long>(gridDim.x) * kWarps;
   auto position_of = [&](long long unit) -> long long {
     if (unit >= units) return -1;
     const long long token = a.chunks == 1 ? unit : unit / a.chunks;
     return a.positions ? a.positions[token] : token;
   };
+  // Forward: a token's queries, then its keys.  Backward: all queries, then all
+  // keys, so that one set of gain sums is live at a time.
+#pragma unroll 1
+  for (int pass = 0; pass < (kBackward ? 2 : 1); ++pass) {
+  float dgain[8] = {};
+  long long u = static_cast<long long>(blockIdx.x) * kWarps + warp;
   long long position = position_of(u);
   for (; u < units; u += stride) {
     const long long token = a.chunks == 1 ? u : u / a.chunks;
@@ -319,7 +331,8 @@ __global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 4) qk_vec_kernel(c
     }
     position = position_of(u + stride);  // of the next token, while this one is worked on
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
+    for (int part = 0; part < (kBackward ? 1 : 2); ++part) {
+      const int which = kBackward ? pass : part;
       // the part of this unit's heads that are queries (keys)
       const int shift = which ? a.q_heads : 0, count = which ? a.k_heads : a.q_heads;
       const int lo = begin > shift ? begin - shift : 0;
@@ -393,7 +406,7 @@ __global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 4) qk_vec_kernel(c
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const float xn = x[k] * rstd;
-              if (real) dgain[which][k] = fmaf(y[k], xn, dgain[which][k]);
+              if (real) dgain[k] = fmaf(y[k], xn, dgain[k]);
               y[k] = rstd * fmaf(-xn, mean, g[k]);
             }
           }
@@ -411,26 +424,24 @@ __global__ void __launch_bounds__(kQkThreads, kBackward ? 2 : 4) qk_vec_kernel(c
   }
   if constexpr (kBackward) {
     // the CTA's gain sums: over the groups of a warp, then over the warps
-    __shared__ float sums[kQkWarps][kMaxHeadDim];
+    __shared__ float sums[kWarps][kMaxHeadDim];
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        for (int o = group; o < 32; o <<= 1) dgain[which][k] += __shfl_xor_sync(0xffffffffu, dgain[which][k], o);
-      }
-      __syncthreads();
-      if (my_group == 0 && active) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sums[warp][element(k)] = dgain[which][k];
-      }
-      __syncthreads();
-      for (int d = threadIdx.x; d < a.dim; d += kQkThreads) {
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kQkWarps; ++w) s += sums[w][d];
-        a.partials[(static_cast<long long>(blockIdx.x) * 2 + which) * a.dim + d] = s;
-      }
+    for (int k = 0; k < 8; ++k) {
+      for (int o = group; o < 32; o <<= 1) dgain[k] += __shfl_xor_sync(0xffffffffu, dgain[k], o);
     }
+    __syncthreads();
+    if (my_group == 0 && active) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sums[warp][element(k)] = dgain[k];
+    }
+    __syncthreads();
+    for (int d = threadIdx.x; d < a.dim; d += kThreads) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += sums[w][d];
+      a.partials[(static_cast<long long>(blockIdx.x) * 2 + pass) * a.dim + d] = s;
+    }
+  }
   }
 }
 
@@ -487,16 +498,21 @@ bool vectors_ok(const QkArgs& a, bool fp32, bool backward) {
   return true;
 }
 
-// CTAs of a launch over `rows` heads; the backward workspace has room for any.
-int qk_ctas(long long rows) {
-  const long long want = (rows + kQkWarps - 1) / kQkWarps, most = 4LL * sm_count();
-  return static_cast<int>(want < 1 ? 0 : want < most ? want : most);
+// CTAs of `warps` warps for `units` units of a warp's work, at most `per_sm` on an SM.
+int qk_ctas(long long units, int warps, int per_sm) {
+  const long long want = (units + warps - 1) / warps, most = static_cast<long long>(per_sm) * sm_count();
+  return static_cast<int>(want < most ? want : most);
+}
+// The most that a backward launch over `rows` heads takes.
+int backward_ctas(long long rows) {
+  const int a = qk_ctas(rows, kQkWarps, 4), b = qk_ctas(rows, kVecWarps, kVecCtas<true>);
+  return a > b ? a : b;
 }
 
 template <bool kFp32, bool kBackward>
 int launch_qk(QkArgs& a, cudaStream_t s) {
   const long long rows = a.tokens * (a.q_heads + a.k_heads);
-  int ctas = qk_ctas(rows);
+  int ctas = qk_ctas(rows, kQkWarps, 4);
   if (lanes_ok(a)) {
     // A warp takes a whole token while that gives every SM 16 warps (the
     // token's cosines are read once); fewer tokens are cut into parts.
@@ -506,15 +522,14 @@ int launch_qk(QkArgs& a, cudaStream_t s) {
     const long long parts = wanted < 1 ? 1 : wanted < most ? wanted : most;
     a.chunk_heads = static_cast<int>(((heads + parts - 1) / parts + groups - 1) / groups * groups);
     a.chunks = (heads + a.chunk_heads - 1) / a.chunk_heads;
-    const long long want = (a.tokens * a.chunks + kQkWarps - 1) / kQkWarps, resident = (kBackward ? 2LL : 4LL) * sm_count();
-    ctas = static_cast<int>(want < resident ? want : resident);
+    ctas = qk_ctas(a.tokens * a.chunks, kVecWarps, kVecCtas<kBackward>);
     const int group = vectors_ok(a, kFp32, kBackward) ? a.group : 0;
     switch (group) {
-      case 4: qk_vec_kernel<kFp32, kBackward, 4><<<ctas, kQkThreads, 0, s>>>(a); break;
-      case 8: qk_vec_kernel<kFp32, kBackward, 8><<<ctas, kQkThreads, 0, s>>>(a); break;
-      case 16: qk_vec_kernel<kFp32, kBackward, 16><<<ctas, kQkThreads, 0, s>>>(a); break;
-      case 32: qk_vec_kernel<kFp32, kBackward, 32><<<ctas, kQkThreads, 0, s>>>(a); break;
-      default: qk_vec_kernel<kFp32, kBackward, 0><<<ctas, kQkThreads, 0, s>>>(a);
+      case 4: qk_vec_kernel<kFp32, kBackward, 4><<<ctas, kVecThreads, 0, s>>>(a); break;
+      case 8: qk_vec_kernel<kFp32, kBackward, 8><<<ctas, kVecThreads, 0, s>>>(a); break;
+      case 16: qk_vec_kernel<kFp32, kBackward, 16><<<ctas, kVecThreads, 0, s>>>(a); break;
+      case 32: qk_vec_kernel<kFp32, kBackward, 32><<<ctas, kVecThreads, 0, s>>>(a); break;
+      default: qk_vec_kernel<kFp32, kBackward, 0><<<ctas, kVecThreads, 0, s>>>(a);
     }
   } else {
     qk_kernel<kFp32, kBackward><<<ctas, kQkThreads, 0, s>>>(a);
@@ -527,15 +542,10 @@ zero_status report(zero_status st, const char* text) {
   return st;
 }
 
-bool bad(const void* p, int esz, int device) {
-  if (!p || reinterpret_cast<uintptr_t>(p) % esz) return true;
-  cudaPointerAttributes attr{};
-  if (cudaPointerGetAttributes(&attr, p) != cudaSuccess) {
-    cudaGetLastError();
-    return true;
-  }
-  return (attr.type != cudaMemoryTypeDevice && attr.type != cudaMemoryTypeManaged) || attr.device != device;
-}
+// As the other calls of every step: NULL and alignment are checked, not where
+// the memory lies (a query of the driver per pointer costs more than the
+// launch of a single token's pass).
+bool bad(const void* p, int esz) { return !p || reinterpret_cast<uintptr_t>(p) % esz != 0; }
 
 zero_status check_config(const zero_qk_config* c, int64_t tokens) {
   if (!c) return report(ZERO_EINVAL, "config is NULL");
@@ -558,8 +568,6 @@ zero_status check_config(const zero_qk_config* c, int64_t tokens) {
 zero_status fill(const zero_qk_config* c, int64_t tokens, const zero_heads* q, const zero_heads* k, const void* q_gain,
                  const void* k_gain, const float* table, const int32_t* positions, const zero_heads* q_out,
                  const zero_heads* k_out, QkArgs* a) {
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return report(ZERO_ECUDA, "no CUDA device");
   const int esz = c->dtype == ZERO_GRAD_FP32 ? 4 : 2, gsz = c->gain_dtype == ZERO_GRAD_FP32 ? 4 : 2;
   const zero_heads* in[2] = {q, k};
   const zero_heads* out[2] = {q_out, k_out};
@@ -567,19 +575,19 @@ zero_status fill(const zero_qk_config* c, int64_t tokens, const zero_heads* q, c
   const int heads[2] = {c->q_heads, c->k_heads};
   for (int w = 0; w < 2; ++w) {
     if (heads[w] == 0) continue;
-    if (!in[w] || bad(in[w]->data, esz, dev)) return report(ZERO_EINVAL, w ? "k must be aligned device memory" : "q must be aligned device memory");
-    if (!out[w] || bad(out[w]->data, esz, dev))
-      return report(ZERO_EINVAL, w ? "k's output must be aligned device memory" : "q's output must be aligned device memory");
+    if (!in[w] || bad(in[w]->data, esz)) return report(ZERO_EINVAL, w ? "k is NULL or misaligned" : "q is NULL or misaligned");
+    if (!out[w] || bad(out[w]->data, esz))
+      return report(ZERO_EINVAL, w ? "k's output is NULL or misaligned" : "q's output is NULL or misaligned");
     if (in[w]->token_stride < 0 || in[w]->head_stride < 0 || out[w]->token_stride < 0 || out[w]->head_stride < 0)
       return report(ZERO_EINVAL, "a stride is negative");
-    if (gain[w] && bad(gain[w], gsz, dev)) return report(ZERO_EINVAL, "a gain must be aligned device memory");
+    if (gain[w] && bad(gain[w], gsz)) return report(ZERO_EINVAL, "a gain is misaligned");
     a->x[w] = {in[w]->data, in[w]->token_stride, in[w]->head_stride};
     a->out[w] = {out[w]->data, out[w]->token_stride, out[w]->head_stride};
     a->gain[w] = gain[w];
   }
-  if (c->rotary_dim > 0 && c->n_positions > 0 && bad(table, 4, dev))
-    return report(ZERO_EINVAL, "table must be aligned device memory");
-  if (positions && bad(positions, 4, dev)) return report(ZERO_EINVAL, "positions must be aligned device memory");
+  if (c->rotary_dim > 0 && c->n_positions > 0 && bad(table, 4))
+    return report(ZERO_EINVAL, "table is NULL or misaligned");
+  if (positions && bad(positions, 4)) return report(ZERO_EINVAL, "positions is misaligned");
   a->tokens = tokens;
   a->q_heads = c->q_heads;
   a->k_heads = c->k_heads;
@@ -637,7 +645,7 @@ zero_status zero_qk_backward_workspace_bytes(const zero_qk_config* cfg, int64_t 
   if (!bytes) return zfs::report(ZERO_EINVAL, "bytes is NULL");
   const zero_status st = zfs::check_config(cfg, tokens);
   if (st != ZERO_OK) return st;
-  *bytes = static_cast<int64_t>(zfs::qk_ctas(tokens * (cfg->q_heads + cfg->k_heads))) * 2 * cfg->head_dim * 4;
+  *bytes = static_cast<int64_t>(zfs::backward_ctas(tokens * (cfg->q_heads + cfg->k_heads))) * 2 * cfg->head_dim * 4;
   return ZERO_OK;
 }
 
@@ -651,11 +659,9 @@ zero_status zero_qk_norm_rope_backward(const zero_qk_config* cfg, int64_t tokens
   if (st != ZERO_OK) return st;
   if (dgain_dtype != ZERO_GRAD_BF16 && dgain_dtype != ZERO_GRAD_FP32)
     return zfs::report(ZERO_EINVAL, "dgain_dtype is neither bf16 (0) nor fp32 (1)");
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return zfs::report(ZERO_ECUDA, "no CUDA device");
   const int dsz = dgain_dtype == ZERO_GRAD_FP32 ? 4 : 2;
-  if ((dq_gain && zfs::bad(dq_gain, dsz, dev)) || (dk_gain && zfs::bad(dk_gain, dsz, dev)))
-    return zfs::report(ZERO_EINVAL, "a gain gradient must be aligned device memory");
+  if ((dq_gain && zfs::bad(dq_gain, dsz)) || (dk_gain && zfs::bad(dk_gain, dsz)))
+    return zfs::report(ZERO_EINVAL, "a gain gradient is misaligned");
   zfs::QkArgs a{};
   const long long rows = tokens * (cfg->q_heads + cfg->k_heads);
   int ctas = 0;
@@ -667,14 +673,14 @@ zero_status zero_qk_norm_rope_backward(const zero_qk_config* cfg, int64_t tokens
     const int heads[2] = {cfg->q_heads, cfg->k_heads};
     for (int w = 0; w < 2; ++w) {
       if (heads[w] == 0) continue;
-      if (!dy[w] || zfs::bad(dy[w]->data, cfg->dtype == ZERO_GRAD_FP32 ? 4 : 2, dev))
-        return zfs::report(ZERO_EINVAL, "an output gradient must be aligned device memory");
+      if (!dy[w] || zfs::bad(dy[w]->data, cfg->dtype == ZERO_GRAD_FP32 ? 4 : 2))
+        return zfs::report(ZERO_EINVAL, "an output gradient is NULL or misaligned");
       if (dy[w]->token_stride < 0 || dy[w]->head_stride < 0) return zfs::report(ZERO_EINVAL, "a stride is negative");
       a.dy[w] = {dy[w]->data, dy[w]->token_stride, dy[w]->head_stride};
     }
     int64_t need = 0;
     zero_qk_backward_workspace_bytes(cfg, tokens, &need);
-    if (zfs::bad(workspace, 16, dev)) return zfs::report(ZERO_EINVAL, "workspace must be 16-byte aligned device memory");
+    if (zfs::bad(workspace, 16)) return zfs::report(ZERO_EINVAL, "workspace is NULL or not 16-byte aligned");
     if (workspace_bytes < need) return zfs::report(ZERO_EINVAL, "workspace is too small");
     a.partials = static_cast<float*>(workspace);
     ctas = cfg->dtype == ZERO_GRAD_FP32 ? zfs::launch_qk<true, true>(a, s) : zfs::launch_qk<false, true>(a, s);

@@ -8,6 +8,8 @@ is no CPU path.
 
 from __future__ import annotations
 
+import contextlib
+import functools
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -15,10 +17,19 @@ import torch
 from . import binding as B
 
 _DTYPES = {torch.bfloat16: B.ZERO_GRAD_BF16, torch.float32: B.ZERO_GRAD_FP32}
+_CURRENT = contextlib.nullcontext()
+# read-only configuration structs by their values
+_ns_config = functools.lru_cache(maxsize=64)(B.make_ns_config)
+_qk_config = functools.lru_cache(maxsize=64)(B.zero_qk_config)
+
+
+def _on(device: torch.device):
+    """Makes `device` current for a C call; the usual case costs nothing."""
+    return _CURRENT if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
 
 
 def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients: Sequence[float] = (3.4445, -4.7750, 2.0315),
@@ -38,8 +49,8 @@ def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients: Sequence[flo
             out.size(-1) > 1 and out.stride(-1) != 1):
         raise ValueError("out must be a bf16 tensor of x's shape and device with contiguous columns")
     batch, rows, cols = (1, *x.shape) if x.dim() == 2 else x.shape
-    cfg = B.make_ns_config(steps, coefficients, eps)
-    with torch.cuda.device(x.device):
+    cfg = _ns_config(steps, tuple(coefficients), eps)
+    with _on(x.device):
         need = B.zero_orthogonalize_workspace_bytes(cfg, rows, cols, batch)
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
         B.zero_orthogonalize(cfg, rows, cols, batch, x.data_ptr(), _DTYPES[x.dtype],
@@ -50,33 +61,36 @@ def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients: Sequence[flo
 
 
 def _heads(x: torch.Tensor) -> B.zero_heads:
-    return B.zero_heads(x.data_ptr(), x.stride(0), x.stride(1))
+    token, head, one = x.stride()
+    if one != 1 and x.size(2) > 1:
+        raise ValueError("the vector of a head must be contiguous")
+    return B.zero_heads(x.data_ptr(), token, head)
 
 
-def _qk_config(q, k, q_gain, k_gain, table, positions, eps, interleaved) -> B.zero_qk_config:
-    for name, x in (("q", q), ("k", k)):
-        if x.dim() != 3 or x.dtype not in _DTYPES or not x.is_cuda or (x.size(2) > 1 and x.stride(2) != 1):
-            raise ValueError(f"{name} must be a bf16 or fp32 CUDA tensor (tokens, heads, head_dim) with contiguous "
-                             "head vectors")
-    if k.dtype != q.dtype or k.device != q.device or k.size(0) != q.size(0) or k.size(2) != q.size(2):
+def _check_qk(q, k, q_gain, k_gain, table, positions, eps, interleaved) -> B.zero_qk_config:
+    device, dtype = q.device, q.dtype
+    if q.dim() != 3 or k.dim() != 3 or dtype not in _DTYPES or not q.is_cuda:
+        raise ValueError("q and k must be bf16 or fp32 CUDA tensors (tokens, heads, head_dim)")
+    (tokens, q_heads, dim), (k_tokens, k_heads, k_dim) = q.shape, k.shape
+    if k.dtype != dtype or k.device != device or k_tokens != tokens or k_dim != dim:
         raise ValueError("q and k must agree in type, device, tokens and head_dim")
-    dim = q.size(2)
-    gain_dtype = torch.float32
+    gain_dtype = None
     for g in (q_gain, k_gain):
         if g is None:
             continue
-        gain_dtype = g.dtype
-        if g.dtype not in _DTYPES or g.shape != (dim,) or g.device != q.device or not g.is_contiguous():
+        if g.dtype not in _DTYPES or g.shape != (dim,) or g.device != device or not g.is_contiguous():
             raise ValueError("a gain must be a contiguous bf16 or fp32 vector of head_dim elements")
-    if q_gain is not None and k_gain is not None and q_gain.dtype != k_gain.dtype:
-        raise ValueError("the gains must have one type")
-    if table.dim() != 2 or table.dtype != torch.float32 or table.device != q.device or not table.is_contiguous():
+        if gain_dtype not in (None, g.dtype):
+            raise ValueError("the gains must have one type")
+        gain_dtype = g.dtype
+    if table.dim() != 2 or table.dtype != torch.float32 or table.device != device or not table.is_contiguous():
         raise ValueError("table must be a contiguous fp32 tensor (positions, rotary_dim)")
-    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (q.size(0),)
-                                  or positions.device != q.device or not positions.is_contiguous()):
+    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (tokens,)
+                                  or positions.device != device or not positions.is_contiguous()):
         raise ValueError("positions must be a contiguous int32 vector with one entry per token")
-    return B.zero_qk_config(q.size(1), k.size(1), dim, table.size(1), 1 if interleaved else 0, _DTYPES[q.dtype],
-                            _DTYPES[gain_dtype], eps, table.size(0))
+    n_positions, rotary = table.shape
+    return _qk_config(q_heads, k_heads, dim, rotary, 1 if interleaved else 0, _DTYPES[dtype],
+                      _DTYPES[gain_dtype or torch.float32], eps, n_positions)
 
 
 def _ptr(x: Optional[torch.Tensor]) -> int:
@@ -95,13 +109,12 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_gain: Optional[torch.Tensor
     the rotary_dim/2 cosines, then the sines; rotary_dim is its width.  A
     position outside the table marks padding: zeros.  ``out`` may be (q, k).
     """
-    cfg = _qk_config(q, k, q_gain, k_gain, table, positions, eps, interleaved)
+    cfg = _check_qk(q, k, q_gain, k_gain, table, positions, eps, interleaved)
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
-               torch.empty(k.shape, dtype=k.dtype, device=k.device))
+        out = (q.new_empty(q.shape), q.new_empty(k.shape))
     else:
         _check_like(out, (q, k))
-    with torch.cuda.device(q.device):
+    with _on(q.device):
         B.zero_qk_norm_rope(cfg, q.size(0), _heads(q), _heads(k), _ptr(q_gain), _ptr(k_gain), table.data_ptr(),
                             _ptr(positions), _heads(out[0]), _heads(out[1]), _stream(q.device))
     return out
@@ -109,7 +122,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_gain: Optional[torch.Tensor
 
 def _check_like(got, want):
     for g, w in zip(got, want):
-        if g.shape != w.shape or g.dtype != w.dtype or g.device != w.device or (g.size(2) > 1 and g.stride(2) != 1):
+        if g.shape != w.shape or g.dtype != w.dtype or g.device != w.device:
             raise ValueError("an output or output gradient must match its input in shape, type and device")
 
 
@@ -124,23 +137,21 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
     gain gradients to, such as slices of a replica's flat gradient; new fp32
     vectors otherwise.
     """
-    cfg = _qk_config(q, k, q_gain, k_gain, table, positions, eps, interleaved)
+    cfg = _check_qk(q, k, q_gain, k_gain, table, positions, eps, interleaved)
     _check_like((dq_out, dk_out), (q, k))
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
-               torch.empty(k.shape, dtype=k.dtype, device=k.device))
+        out = (q.new_empty(q.shape), q.new_empty(k.shape))
     else:
         _check_like(out, (q, k))
     dim = q.size(2)
     if gain_out is None:
-        both = torch.empty((2, dim), dtype=torch.float32, device=q.device)
-        gain_out = (both[0], both[1])
+        gain_out = torch.empty((2, dim), dtype=torch.float32, device=q.device).unbind()
     else:
         for g in gain_out:
             if g.dtype not in _DTYPES or g.dtype != gain_out[0].dtype or g.shape != (dim,) or g.device != q.device \
                     or not g.is_contiguous():
                 raise ValueError("gain_out must be two contiguous vectors of head_dim elements and one type")
-    with torch.cuda.device(q.device):
+    with _on(q.device):
         need = B.zero_qk_backward_workspace_bytes(cfg, q.size(0))
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
         B.zero_qk_norm_rope_backward(cfg, q.size(0), _heads(dq_out), _heads(dk_out), _heads(q), _heads(k),

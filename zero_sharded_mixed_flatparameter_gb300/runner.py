@@ -122,8 +122,9 @@ class FlatStep:
 
     @staticmethod
     def stream_handle(stream: Optional[torch.cuda.Stream] = None) -> int:
-        s = stream if stream is not None else torch.cuda.current_stream()
-        return int(s.cuda_stream)
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return int(stream.cuda_stream)
 
     def grad_dtype_torch(self):
         return torch.bfloat16 if self.grad_dtype == "bf16" else torch.float32
