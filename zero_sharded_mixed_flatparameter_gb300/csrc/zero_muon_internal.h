@@ -109,6 +109,53 @@ struct MomentumArgs {
 cudaError_t launch_momentum(const MomentumArgs& a, bool vec, cudaStream_t stream);
 unsigned int muon_debug_failures();
 
+// ---- thin matrices (zero_ns_thin.cu) ---------------------------------------
+// A smaller side of at most kThin: one launch for the whole orthogonalisation
+// (and, in a Muon step, for its momentum pass and update), matrices of several
+// shapes together.
+constexpr int kThin = 128;
+constexpr int kMaxSteps = 32;
+constexpr int kThinChain = 2;  // steps per Gram matrix
+// Elements of the fp32 workspace of one launch (more only for a single matrix
+// that is larger).
+constexpr long long kThinWork = 1LL << 22;
+struct ThinArgs {
+  int steps;
+  float a, b, c, eps;
+  // powers of two of the stored X0, A, P, Q and A P
+  int ex[kMaxSteps], ea[kMaxSteps], ep[kMaxSteps], eq[kMaxSteps], ew[kMaxSteps];
+  int rows[kMaxMats], cols[kMaxMats];  // a stack uses entry 0
+  // fp32, as many elements as the matrix (a multiple of 8 apart): the Muon
+  // step's update and the iterate between two Gram matrices
+  float* work;
+  long long work_mat_stride;           // of a stack
+  // A stack: input and bf16 output.
+  MatSource src;
+  uint16_t* out;
+  long long out_row_stride, out_mat_stride;
+  int vec_out;
+  // The Muon step: see MomentumArgs and NsOut.
+  int n_ranks, grad_fp32, nesterov;
+  float inv_n, mu, decay;
+  const float* clip;
+  unsigned long long* nonfinite;
+  const long long* dev_t;
+  long long dev_steps, total_padded;
+  float *mom, *master;
+  uint16_t* p16;
+  uint32_t vec[(kMaxMats + 31) / 32];  // bit per matrix: 8-element vectors are aligned everywhere
+  float step[kMaxMats];
+  long long offset[kMaxMats], work_offset[kMaxMats];
+  const void* g[kMaxMats][kMaxRanks];
+};
+// CTAs (a cluster) per matrix of this shape.
+int thin_ctas(long long rows, long long cols);
+// Fills the scales and coefficients of `cfg`.
+void thin_scales(const zero_ns_config& cfg, ThinArgs* a);
+cudaError_t launch_ns_thin(const ThinArgs& a, bool muon, int ctas, long long mats, cudaStream_t stream, int* launches);
+unsigned int thin_debug_failures();
+unsigned int thin_timeouts();
+
 // ---- the products (zero_ns_gemm.cu) ----------------------------------------
 enum NsEpilogue {
   kNsGram = 0,   // D = alpha acc, symmetric: only tiles on and below the diagonal are computed, both halves stored

@@ -33,40 +33,6 @@ __device__ __forceinline__ double block_sum(double x) {
   return s;
 }
 
-// Eight consecutive values from element `at` of a bf16 or fp32 array; kVecOk:
-// the address is 16-byte aligned and all eight exist.
-template <bool kFp32, bool kVecOk>
-__device__ __forceinline__ void load8(const void* base, long long at, int count, float* x) {
-  if constexpr (kVecOk) {
-    if constexpr (kFp32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
-      const float4 u = p[0], v = p[1];
-      x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-      x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
-    } else {
-      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[2 * k] = bf16_lo(w[k]);
-        x[2 * k + 1] = bf16_hi(w[k]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      x[k] = 0.0f;
-      if (k < count) {
-        if constexpr (kFp32) {
-          x[k] = static_cast<const float*>(base)[at + k];
-        } else {
-          x[k] = __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(base)[at + k]) << 16);
-        }
-      }
-    }
-  }
-}
-
 // One chunk of one matrix per CTA (grid: chunk, matrix).  A thread's vectors
 // are kThreads vectors apart, so a warp reads contiguous runs.
 template <bool kFp32, bool kVecOk>

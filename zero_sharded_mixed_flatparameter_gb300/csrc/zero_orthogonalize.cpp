@@ -131,6 +131,35 @@ NsPlan ns_plan(long long rows, long long cols, int mats, bool keep_update) {
   return p;
 }
 
+void thin_scales(const zero_ns_config& cfg, ThinArgs* a) {
+  a->steps = cfg.steps;
+  a->a = cfg.a;
+  a->b = cfg.b;
+  a->c = cfg.c;
+  a->eps = cfg.eps;
+  double top = 1.0, chain = 1.0;  // spectral norms of X and of Q
+  for (int k = 0; k < cfg.steps; ++k) {
+    // P = a I + b A + c A A with its identity
+    auto q = [&](double t) { return std::fabs(cfg.a + t * (cfg.b + t * cfg.c)); };
+    double p = std::max(q(0.0), q(top * top));
+    const double turn = cfg.c != 0.0f ? -cfg.b / (2.0 * cfg.c) : -1.0;
+    if (turn > 0.0 && turn < top * top) p = std::max(p, q(turn));
+    chain = k % kThinChain == 0 ? p : chain * p;
+    a->ex[k] = scale_exponent(top);
+    a->ea[k] = scale_exponent(top * top);
+    a->ep[k] = scale_exponent(p);
+    a->eq[k] = scale_exponent(chain);
+    a->ew[k] = scale_exponent(top * top * p);
+    top = largest_value(cfg.a, cfg.b, cfg.c, top);
+  }
+}
+
+// Matrices of a stack that one thin launch takes, and its workspace.
+long long thin_stride(long long rows, long long cols) { return round_up(rows * cols, kVec); }
+long long thin_mats(long long rows, long long cols, long long batch) {
+  return std::max<long long>(1, std::min<long long>(batch, kThinWork / thin_stride(rows, cols)));
+}
+
 cudaError_t ns_run(const NsPlan& p, const zero_ns_config& cfg, int mats, const MatSource& src, char* ws,
                    const NsOut& out, cudaStream_t stream, int* launches) {
   auto half = [&](long long at) { return reinterpret_cast<uint16_t*>(ws + at); };
@@ -274,8 +303,9 @@ zero_status zero_orthogonalize_workspace_bytes(const zero_ns_config* cfg, int64_
   if (!bytes) return zfs::report(ZERO_EINVAL, "bytes is NULL");
   const zero_status st = zfs::check_shape(cfg, rows, cols, batch);
   if (st != ZERO_OK) return st;
-  *bytes = rows == 0 || cols == 0 || batch == 0
-               ? 0
+  *bytes = rows == 0 || cols == 0 || batch == 0 ? 0
+           : std::min(rows, cols) <= zfs::kThin
+               ? 4 * zfs::thin_stride(rows, cols) * zfs::thin_mats(rows, cols, batch)
                : zfs::ns_plan(rows, cols, zfs::ns_mats(rows, cols, batch), false).bytes;
   return ZERO_OK;
 }
@@ -302,17 +332,14 @@ zero_status zero_orthogonalize(const zero_ns_config* cfg, int64_t rows, int64_t 
     return zfs::report(ZERO_EINVAL, "in must be aligned memory of the current device");
   if (!out || zfs::misaligned(out, 2) || !zfs::on_device(out, dev))
     return zfs::report(ZERO_EINVAL, "out must be aligned memory of the current device");
-  const int mats = zfs::ns_mats(rows, cols, batch);
-  const zfs::NsPlan p = zfs::ns_plan(rows, cols, mats, false);
-  if (!workspace || zfs::misaligned(workspace, 256) || !zfs::on_device(workspace, dev))
-    return zfs::report(ZERO_EINVAL, "workspace must be 256-byte aligned memory of the current device");
-  if (workspace_bytes < p.bytes)
-    return zfs::report(ZERO_EINVAL, "workspace has %lld bytes, %lld needed", workspace_bytes, p.bytes);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  char* ws = static_cast<char*>(workspace);
-  int launches = 0;
-  for (int64_t first = 0; first < batch; first += mats) {
-    const int count = static_cast<int>(std::min<int64_t>(mats, batch - first));
+  auto failed = [](cudaError_t e) {
+    char buf[256];
+    std::snprintf(buf, sizeof buf, "orthogonalize launch: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
+    zfs_report_error(nullptr, ZERO_ECUDA, buf);
+    return ZERO_ECUDA;
+  };
+  auto source = [&](int64_t first) {
     zfs::MatSource src{};
     src.data = static_cast<const char*>(in) + first * in_batch_stride * esz;
     src.fp32 = in_dtype == ZERO_GRAD_FP32 ? 1 : 0;
@@ -320,18 +347,48 @@ zero_status zero_orthogonalize(const zero_ns_config* cfg, int64_t rows, int64_t 
     src.mat_stride = in_batch_stride;
     src.vec_ok = cols % zfs::kVec == 0 && in_row_stride % zfs::kVec == 0 && in_batch_stride % zfs::kVec == 0 &&
                  !zfs::misaligned(src.data, 16);
+    return src;
+  };
+  int launches = 0;
+  int64_t need = 0;
+  zero_orthogonalize_workspace_bytes(cfg, rows, cols, batch, &need);
+  if (!workspace || zfs::misaligned(workspace, 256) || !zfs::on_device(workspace, dev))
+    return zfs::report(ZERO_EINVAL, "workspace must be 256-byte aligned memory of the current device");
+  if (workspace_bytes < need)
+    return zfs::report(ZERO_EINVAL, "workspace has %lld bytes, %lld needed", workspace_bytes, need);
+  if (std::min(rows, cols) <= zfs::kThin) {
+    zfs::ThinArgs a{};
+    a.work = static_cast<float*>(workspace);
+    a.work_mat_stride = zfs::thin_stride(rows, cols);
+    zfs::thin_scales(*cfg, &a);
+    a.rows[0] = static_cast<int>(rows);
+    a.cols[0] = static_cast<int>(cols);
+    a.out_row_stride = out_row_stride;
+    a.out_mat_stride = out_batch_stride;
+    a.vec_out = out_row_stride % zfs::kVec == 0 && out_batch_stride % zfs::kVec == 0 && !zfs::misaligned(out, 16);
+    const int64_t most = zfs::thin_mats(rows, cols, batch);
+    for (int64_t first = 0; first < batch; first += most) {
+      a.src = source(first);
+      a.out = static_cast<uint16_t*>(out) + first * out_batch_stride;
+      const cudaError_t e = zfs::launch_ns_thin(a, false, zfs::thin_ctas(rows, cols), std::min(most, batch - first), s,
+                                                &launches);
+      if (e != cudaSuccess) return failed(e);
+    }
+    return ZERO_OK;
+  }
+  const int mats = zfs::ns_mats(rows, cols, batch);
+  const zfs::NsPlan p = zfs::ns_plan(rows, cols, mats, false);
+  char* ws = static_cast<char*>(workspace);
+  for (int64_t first = 0; first < batch; first += mats) {
+    const int count = static_cast<int>(std::min<int64_t>(mats, batch - first));
+    const zfs::MatSource src = source(first);
     zfs::NsOut o;
     o.out = static_cast<uint16_t*>(out) + first * out_batch_stride;
     o.row_stride = out_row_stride;
     o.mat_stride = out_batch_stride;
     cudaError_t e = zfs::launch_ns_norm(src, p, count, reinterpret_cast<double*>(ws + p.partials), s);
     if (e == cudaSuccess) e = zfs::ns_run(p, *cfg, count, src, ws, o, s, &launches);
-    if (e != cudaSuccess) {
-      char buf[256];
-      std::snprintf(buf, sizeof buf, "orthogonalize launch: %s (%s)", cudaGetErrorName(e), cudaGetErrorString(e));
-      zfs_report_error(nullptr, ZERO_ECUDA, buf);
-      return ZERO_ECUDA;
-    }
+    if (e != cudaSuccess) return failed(e);
   }
   return ZERO_OK;
 }

@@ -431,36 +431,110 @@ int64_t total_chunks(const zero_ctx* ctx) {
   return n;
 }
 
-// The Muon part of a step: per shape, momentum and update, then the
+// Where parameter p's gradients lie, replica after replica (or the reduced
+// gradient that a clip kept); whether all are 16-byte aligned.
+bool param_grads(const zero_ctx* ctx, int32_t p, const void** g) {
+  const int64_t off = ctx->param_offset[p];
+  if (ctx->clip_keep) {
+    g[0] = ctx->clip_keep + off;
+    return aligned(g[0], 16);
+  }
+  const int32_t unit = ctx->param_unit[p];
+  const int64_t bytes = (off - ctx->unit_base[unit]) * static_cast<int64_t>(grad_bytes(ctx->cfg));
+  bool ok = true;
+  for (int r = 0; r < ctx->cfg.n_ranks; ++r) {
+    g[r] = static_cast<const char*>(ctx->grads[static_cast<size_t>(unit) * zfs::kMaxRanks + r]) + bytes;
+    ok = ok && aligned(g[r], 16);
+  }
+  return ok;
+}
+
+double muon_scale(const zero_muon_config& c, int64_t rows, int64_t cols) {
+  if (c.scale == ZERO_MUON_SCALE_RMS) return 0.2 * std::sqrt(static_cast<double>(std::max(rows, cols)));
+  return std::sqrt(std::max(1.0, static_cast<double>(rows) / static_cast<double>(cols)));
+}
+
+// The Muon part of a step: thin matrices of all shapes in one launch per
+// cluster size, the others shape by shape — momentum and update, then the
 // orthogonalisation whose last product updates master and param16.
 zero_status muon_update(zero_ctx* ctx, cudaStream_t stream, int32_t* launches) {
   const zero_muon_config& mc = ctx->muon_cfg;
-  const bool kept = ctx->clip_keep != nullptr;
-  const int N = kept ? 1 : ctx->cfg.n_ranks;
-  const int64_t esz = kept ? 4 : static_cast<int64_t>(grad_bytes(ctx->cfg));
+  const int N = ctx->clip_keep ? 1 : ctx->cfg.n_ranks;
+  const int grad_fp32 = ctx->clip_keep || ctx->cfg.grad_dtype == ZERO_GRAD_FP32 ? 1 : 0;
+  const float* clip = ctx->clip_ws ? reinterpret_cast<const float*>(ctx->clip_ws + 8) : nullptr;
   const int64_t bound = ctx->padded_total - (ctx->inject == ZERO_INJECT_SHORT_BOUNDS ? zfs::kVec : 0);
+  const float decay = static_cast<float>(1.0 - static_cast<double>(mc.lr) * static_cast<double>(mc.weight_decay));
+  uint16_t* p16 = static_cast<uint16_t*>(ctx->bufs.param16);
+
+  for (int ctas = 1; ctas <= 8; ctas *= 2) {
+    zfs::ThinArgs a;
+    std::memset(&a, 0, sizeof a);
+    zfs::thin_scales(mc.ns, &a);
+    a.n_ranks = N;
+    a.grad_fp32 = grad_fp32;
+    a.nesterov = mc.nesterov;
+    a.inv_n = 1.0f / static_cast<float>(N);
+    a.mu = mc.momentum;
+    a.decay = decay;
+    a.clip = clip;
+    a.nonfinite = ctx->nonfinite;
+    a.dev_t = ctx->cap_t;
+    a.dev_steps = ctx->cap_steps;
+    a.total_padded = bound;
+    a.mom = ctx->bufs.exp_avg;
+    a.work = reinterpret_cast<float*>(ctx->muon_ws);
+    a.master = ctx->bufs.master;
+    a.p16 = p16;
+    int mats = 0;
+    int64_t at = 0;
+    auto flush = [&]() {
+      if (mats == 0) return cudaSuccess;
+      const cudaError_t e = zfs::launch_ns_thin(a, true, ctas, mats, stream, launches);
+      mats = 0;
+      at = 0;
+      std::memset(a.vec, 0, sizeof a.vec);
+      return e;
+    };
+    for (const zero_ctx::MuonGroup& group : ctx->muon_groups) {
+      if (std::min(group.rows, group.cols) > zfs::kThin || zfs::thin_ctas(group.rows, group.cols) != ctas) continue;
+      const int64_t numel = group.rows * group.cols;
+      for (int32_t p : group.params) {
+        if (mats == zfs::kMaxMats || (mats > 0 && at + numel > zfs::kThinWork)) {
+          const cudaError_t e = flush();
+          if (e != cudaSuccess) return fail_cuda(ctx, "thin orthogonalisation launch", e);
+        }
+        a.rows[mats] = static_cast<int32_t>(group.rows);
+        a.cols[mats] = static_cast<int32_t>(group.cols);
+        a.offset[mats] = ctx->param_offset[p];
+        a.work_offset[mats] = at;
+        a.step[mats] = static_cast<float>(static_cast<double>(mc.lr) * muon_scale(mc, group.rows, group.cols));
+        const bool vec = param_grads(ctx, p, a.g[mats]) && group.cols % zfs::kVec == 0 && a.offset[mats] % zfs::kVec == 0;
+        if (vec) a.vec[mats / 32] |= 1u << (mats % 32);
+        at += (numel + zfs::kVec - 1) / zfs::kVec * zfs::kVec;
+        ++mats;
+      }
+    }
+    const cudaError_t e = flush();
+    if (e != cudaSuccess) return fail_cuda(ctx, "thin orthogonalisation launch", e);
+  }
+
   for (const zero_ctx::MuonGroup& group : ctx->muon_groups) {
+    if (std::min(group.rows, group.cols) <= zfs::kThin) continue;
     const int64_t numel = group.rows * group.cols;
     const int most = zfs::ns_mats(group.rows, group.cols, static_cast<long long>(group.params.size()));
     const zfs::NsPlan p = zfs::ns_plan(group.rows, group.cols, most, true);
-    double scale = 1.0;
-    if (mc.scale == ZERO_MUON_SCALE_RMS) {
-      scale = 0.2 * std::sqrt(static_cast<double>(std::max(group.rows, group.cols)));
-    } else {
-      scale = std::sqrt(std::max(1.0, static_cast<double>(group.rows) / static_cast<double>(group.cols)));
-    }
     for (size_t first = 0; first < group.params.size(); first += most) {
       const int mats = static_cast<int>(std::min<size_t>(most, group.params.size() - first));
       zfs::MomentumArgs a;
       std::memset(&a, 0, sizeof a);
       zfs::NsOut out;
       a.n_ranks = N;
-      a.grad_fp32 = kept || ctx->cfg.grad_dtype == ZERO_GRAD_FP32 ? 1 : 0;
+      a.grad_fp32 = grad_fp32;
       a.nesterov = mc.nesterov;
       a.mats = mats;
       a.inv_n = 1.0f / static_cast<float>(N);
       a.mu = mc.momentum;
-      a.clip = ctx->clip_ws ? reinterpret_cast<const float*>(ctx->clip_ws + 8) : nullptr;
+      a.clip = clip;
       a.nonfinite = ctx->nonfinite;
       a.dev_t = ctx->cap_t;
       a.dev_steps = ctx->cap_steps;
@@ -473,17 +547,8 @@ zero_status muon_update(zero_ctx* ctx, cudaStream_t stream, int32_t* launches) {
       bool vec = numel % zfs::kVec == 0;
       for (int k = 0; k < mats; ++k) {
         const int32_t param = group.params[first + k];
-        const int64_t off = ctx->param_offset[param];
-        const int32_t unit = ctx->param_unit[param];
-        a.offset[k] = out.offset[k] = off;
-        vec = vec && off % zfs::kVec == 0;
-        for (int r = 0; r < N; ++r) {
-          const char* base = kept ? reinterpret_cast<const char*>(ctx->clip_keep) + off * esz
-                                  : static_cast<const char*>(ctx->grads[static_cast<size_t>(unit) * zfs::kMaxRanks + r]) +
-                                        (off - ctx->unit_base[unit]) * esz;
-          a.g[k][r] = base;
-          vec = vec && aligned(base, 16);
-        }
+        a.offset[k] = out.offset[k] = ctx->param_offset[param];
+        vec = param_grads(ctx, param, a.g[k]) && vec && a.offset[k] % zfs::kVec == 0;
       }
       cudaError_t e = zfs::launch_momentum(a, vec, stream);
       if (e != cudaSuccess) return fail_cuda(ctx, "momentum kernel launch", e);
@@ -495,9 +560,9 @@ zero_status muon_update(zero_ctx* ctx, cudaStream_t stream, int32_t* launches) {
       src.mat_stride = numel;
       src.vec_ok = group.cols % zfs::kVec == 0 ? 1 : 0;
       out.master = ctx->bufs.master;
-      out.p16 = static_cast<uint16_t*>(ctx->bufs.param16);
-      out.decay = static_cast<float>(1.0 - static_cast<double>(mc.lr) * static_cast<double>(mc.weight_decay));
-      out.step = static_cast<float>(static_cast<double>(mc.lr) * scale);
+      out.p16 = p16;
+      out.decay = decay;
+      out.step = static_cast<float>(static_cast<double>(mc.lr) * muon_scale(mc, group.rows, group.cols));
       out.total_padded = bound;
       out.dev_t = ctx->cap_t;
       out.dev_steps = ctx->cap_steps;
@@ -1455,7 +1520,7 @@ zero_status zero_debug_check_failures(uint32_t* count) {
   if (!count) return fail(nullptr, ZERO_EINVAL, "count is NULL");
 #ifdef ZFS_DEBUG_CHECKS
   const unsigned int counts[] = {zfs::step_debug_failures(), zfs::aux_debug_failures(), zfs::muon_debug_failures(),
-                                 zfs::ns_gemm_debug_failures(), zfs::qk_debug_failures()};
+                                 zfs::ns_gemm_debug_failures(), zfs::thin_debug_failures(), zfs::qk_debug_failures()};
   unsigned int sum = 0;
   for (unsigned int c : counts) {
     if (c == 0xFFFFFFFFu) return fail(nullptr, ZERO_ECUDA, "cannot read the check counters");
@@ -1504,10 +1569,13 @@ zero_status zero_read_nonfinite(zero_ctx* ctx, uint64_t* count, void* stream) {
 
 zero_status zero_kernel_timeouts(const zero_ctx* ctx, uint32_t* count) {
   if (!count) return fail(const_cast<zero_ctx*>(ctx), ZERO_EINVAL, "count is NULL");
-  const unsigned int v = zfs::step_timeouts(), w = zfs::ns_gemm_timeouts();
-  if (v == 0xFFFFFFFFu || w == 0xFFFFFFFFu)
-    return fail(const_cast<zero_ctx*>(ctx), ZERO_ECUDA, "cannot read the timeout counter");
-  *count = v + w;
+  const unsigned int counts[] = {zfs::step_timeouts(), zfs::ns_gemm_timeouts(), zfs::thin_timeouts()};
+  unsigned int sum = 0;
+  for (unsigned int c : counts) {
+    if (c == 0xFFFFFFFFu) return fail(const_cast<zero_ctx*>(ctx), ZERO_ECUDA, "cannot read the timeout counter");
+    sum += c;
+  }
+  *count = sum;
   return ZERO_OK;
 }
 
@@ -1657,6 +1725,11 @@ zero_status muon_plan(zero_ctx* ctx, const zero_muon_config* cfg, const int64_t*
   }
   *bytes = 0;
   for (const zero_ctx::MuonGroup& g : *groups) {
+    if (std::min(g.rows, g.cols) <= zfs::kThin) {
+      // what one thin launch holds: at most kThinWork elements unless one matrix is larger
+      *bytes = std::max<int64_t>(*bytes, 4 * (std::max<int64_t>(g.rows * g.cols, zfs::kThinWork) + zfs::kVec));
+      continue;
+    }
     const int mats = zfs::ns_mats(g.rows, g.cols, static_cast<long long>(g.params.size()));
     *bytes = std::max<int64_t>(*bytes, zfs::ns_plan(g.rows, g.cols, mats, true).bytes);
   }
