@@ -136,6 +136,10 @@ template <bool kFp32, bool kVecOk>
 __global__ void __launch_bounds__(kThreads) ns_scale_kernel(const __grid_constant__ ScaleArgs a) {
   __shared__ float inv_shared;
   const int mat = blockIdx.y;
+  // The first product may take its place already; the partials and the source
+  // are read once the pass before has finished.
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   // every CTA sums the matrix's partials, in the same order
   double s = 0.0;
   for (long long k = threadIdx.x; k < a.chunks; k += kThreads) s += a.partials[mat * a.chunks + k];
@@ -201,15 +205,21 @@ cudaError_t launch_ns_norm(const MatSource& s, const NsPlan& p, int mats, double
 cudaError_t launch_ns_scale(const ScaleArgs& a, cudaStream_t stream) {
   const long long work = a.rows * (a.ldx / kVec);
   const long long want = (work + kThreads - 1) / kThreads, most = 8LL * sm_count() / a.mats + 1;
-  const dim3 grid(static_cast<unsigned>(want < most ? want : most), static_cast<unsigned>(a.mats));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(want < most ? want : most), static_cast<unsigned>(a.mats));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
   if (a.src.fp32) {
-    if (a.src.vec_ok) ns_scale_kernel<true, true><<<grid, kThreads, 0, stream>>>(a);
-    else ns_scale_kernel<true, false><<<grid, kThreads, 0, stream>>>(a);
-  } else {
-    if (a.src.vec_ok) ns_scale_kernel<false, true><<<grid, kThreads, 0, stream>>>(a);
-    else ns_scale_kernel<false, false><<<grid, kThreads, 0, stream>>>(a);
+    return a.src.vec_ok ? cudaLaunchKernelEx(&cfg, ns_scale_kernel<true, true>, a)
+                        : cudaLaunchKernelEx(&cfg, ns_scale_kernel<true, false>, a);
   }
-  return cudaGetLastError();
+  return a.src.vec_ok ? cudaLaunchKernelEx(&cfg, ns_scale_kernel<false, true>, a)
+                      : cudaLaunchKernelEx(&cfg, ns_scale_kernel<false, false>, a);
 }
 
 unsigned int muon_debug_failures() {

@@ -19,6 +19,13 @@
 // per CTA; two accumulators, so that the epilogue of a tile runs under the
 // next one's products.  In a pair each CTA holds 128 of the 256 rows of A and
 // half of B's columns, and the first CTA issues for both.
+//
+// The epilogue moves 64 columns at a time through two 32 KB buffers: C (hi and
+// lo) comes in by TMA a chunk ahead, D goes out by TMA, both in whole 128-byte
+// rows; the final update crosses the buffer so that master and param16 are
+// read and written in whole rows too.  (Rows read and written by a thread each
+// cost the L1 a line per lane: an update of 1024 x 2048 matrices took 170 us
+// where its products take 60.)
 
 #include <cuda.h>
 
@@ -33,120 +40,128 @@ namespace {
 
 constexpr int kBlockK = 64;            // fp16 elements of one 128-byte swizzled row
 constexpr int kBlockM = 128;           // rows per CTA
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kEpilogueWarps = 8;
-constexpr int kGemmThreads = (kEpilogueWarps + 2) * 32;
+constexpr int kEpilogueThreads = kEpilogueWarps * 32;
+constexpr int kGemmThreads = kEpilogueThreads + 64;
 constexpr uint32_t kOperandBytes = kBlockM * kBlockK * 2;
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
-constexpr uint32_t kSmemBytes = kStages * kStageBytes + 1024;  // + alignment
+constexpr int kChunk = 64;             // columns of a step of the epilogue
+constexpr uint32_t kHalfBytes = kBlockM * kChunk * 2;  // a chunk of hi (or of lo, or transposed)
+constexpr uint32_t kBufferBytes = 2 * kHalfBytes;
+constexpr uint32_t kSmemBytes = kStages * kStageBytes + 2 * kBufferBytes + 1024;  // + alignment
 
 // What one launch needs.
 struct GemmKernelArgs {
   CUtensorMap a, b;
+  CUtensorMap c, c_lo, d, d_lo;  // boxes of 64 x 64
   GemmArgs g;
-  long long tiles_m, tiles_n, tiles;  // tiles of one matrix / of all
+  int tiles_m, tiles_n, tiles;   // tiles of one matrix / of all
   int k_blocks;
-  int vec_out;                        // kNsOut / kNsMuon: 16-byte accesses allowed
+  int vec_out;                   // kNsOut / kNsMuon: four elements of a row are aligned
 };
 
+__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
+               "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+// A barrier of the epilogue's warps that tells whether any thread says `x`.
+__device__ __forceinline__ bool epilogue_any(bool x) {
+  uint32_t any;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(any)
+      : "r"(x ? 1u : 0u), "n"(kEpilogueThreads)
+      : "memory");
+  return any != 0;
+}
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueThreads) : "memory"); }
+
 // ---- epilogue ----------------------------------------------------------------
-// x[0..7] += factor * the old iterate's 8 elements at `at`.
-__device__ __forceinline__ void add_old(const GemmArgs& g, long long at, float* x) {
-  const uint4 h = *reinterpret_cast<const uint4*>(g.c + at);
-  const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+// Address of the 16-byte piece `piece` (of 8) of row r in a 128 x 64 half.
+__device__ __forceinline__ uint32_t piece_at(uint32_t half, int r, int piece) {
+  return half + r * 128 + ((piece ^ (r & 7)) << 4);
+}
+
+// y[0..31] += factor * 32 fp16 of row r, from piece `first`.
+__device__ __forceinline__ void add_pieces(uint32_t half, int r, int first, float factor, float* y) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 v = half2_values(hw[k]);
-    x[2 * k] = fmaf(g.cfactor, v.x, x[2 * k]);
-    x[2 * k + 1] = fmaf(g.cfactor, v.y, x[2 * k + 1]);
-  }
-  if (g.c_lo) {
-    const uint4 l = *reinterpret_cast<const uint4*>(g.c_lo + at);
-    const uint32_t lw[4] = {l.x, l.y, l.z, l.w};
+  for (int v = 0; v < 4; ++v) {
+    const uint4 h = lds16(piece_at(half, r, first + v));
+    const uint32_t w[4] = {h.x, h.y, h.z, h.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float2 v = half2_values(lw[k]);
-      x[2 * k] = fmaf(g.cfactor, v.x, x[2 * k]);
-      x[2 * k + 1] = fmaf(g.cfactor, v.y, x[2 * k + 1]);
+      const float2 u = half2_values(w[k]);
+      y[8 * v + 2 * k] = fmaf(factor, u.x, y[8 * v + 2 * k]);
+      y[8 * v + 2 * k + 1] = fmaf(factor, u.y, y[8 * v + 2 * k + 1]);
     }
   }
 }
 
-// 32 columns j .. j+31 of row i: x holds the sums.  `mirror`: an off-diagonal
-// tile of a symmetric result, stored transposed as well (lanes are consecutive
-// rows, so every column is one contiguous store of the warp).
+// Whole rows of a finished chunk (fp32 in `buffer`, 16-byte pieces swizzled by
+// row) to their place: rows i0 .. i0+127 of the matrix, columns j0 .. j0+63.
 template <int kEpi>
-__device__ __forceinline__ void store_columns(const GemmKernelArgs& ka, int mat, long long i, long long j, bool mirror,
-                                              float* x) {
+__device__ __forceinline__ void store_rows(const GemmKernelArgs& ka, int mat, uint32_t buffer, long long i0, long long j0,
+                                           int warp, int lane) {
   const GemmArgs& g = ka.g;
-  if (i >= g.M || j >= g.N) return;
-  // 8 columns at a time; the pitch of C and D is a multiple of 8
-  const long long row = mat * g.d_mat_stride + i * g.ldd + j;
+  auto value4 = [&](int r, int piece) {
+    const uint4 v = lds16(buffer + r * 256 + ((piece ^ (r & 7)) << 4));
+    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+  };
+  const long long base = kEpi == kNsMuon ? g.out.offset[mat] : mat * g.out.mat_stride;
+  const long long pitch = kEpi == kNsMuon ? g.N : g.out.row_stride;
+  if (ka.vec_out && j0 + kChunk <= g.N) {  // two rows per warp and access
+    const int piece = lane % 16;
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    if (j + 8 * v >= g.N) break;
-    float* y = x + 8 * v;
+    for (int q = 0; q < 2; ++q) {
+      float4 old[4];
+      if constexpr (kEpi == kNsMuon) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] *= g.alpha;
-    if constexpr (kEpi != kNsGram) add_old(g, row + 8 * v, y);
-    if constexpr (kEpi == kNsGram || kEpi == kNsPoly || kEpi == kNsApply) {
-      uint32_t h[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = half2_bits(y[2 * k], y[2 * k + 1]);
-      *reinterpret_cast<uint4*>(g.d + row + 8 * v) = make_uint4(h[0], h[1], h[2], h[3]);
-      if constexpr (kEpi == kNsApply) {
-        if (g.d_lo) {
-          uint32_t l[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 hv = half2_values(h[k]);
-            l[k] = half2_bits(y[2 * k] - hv.x, y[2 * k + 1] - hv.y);
-          }
-          *reinterpret_cast<uint4*>(g.d_lo + row + 8 * v) = make_uint4(l[0], l[1], l[2], l[3]);
-        }
-      } else if (mirror) {
-        uint16_t* d = g.d + mat * g.d_mat_stride;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const long long c = j + 8 * v + k;
-          if (c < g.N) d[c * g.ldd + i] = half_bits(y[k]);
+        for (int k = 0; k < 4; ++k) {
+          const int r = warp * 16 + (q * 4 + k) * 2 + lane / 16;
+          const long long at = base + (i0 + r) * pitch + j0 + 4 * piece;
+          if (i0 + r < g.M && ZFS_CHECK(at >= 0 && at + 4 <= g.out.total_padded))
+            old[k] = *reinterpret_cast<const float4*>(g.out.master + at);
         }
       }
-    } else if constexpr (kEpi == kNsOut) {
-      uint16_t* d = g.out.out + mat * g.out.mat_stride + i * g.out.row_stride + j + 8 * v;
-      if (ka.vec_out && j + 8 * v + 8 <= g.N) {
-        *reinterpret_cast<uint4*>(d) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                                  pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-      } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (j + 8 * v + k < g.N) d[k] = to_bf16_bits(y[k]);
+      for (int k = 0; k < 4; ++k) {
+        const int r = warp * 16 + (q * 4 + k) * 2 + lane / 16;
+        const long long at = base + (i0 + r) * pitch + j0 + 4 * piece;
+        if (i0 + r >= g.M) continue;
+        float4 y = value4(r, piece);
+        if constexpr (kEpi == kNsMuon) {
+          if (!ZFS_CHECK(at >= 0 && at + 4 <= g.out.total_padded)) continue;
+          y.x = __fadd_rn(__fmul_rn(old[k].x, g.out.decay), __fmul_rn(-g.out.step, y.x));
+          y.y = __fadd_rn(__fmul_rn(old[k].y, g.out.decay), __fmul_rn(-g.out.step, y.y));
+          y.z = __fadd_rn(__fmul_rn(old[k].z, g.out.decay), __fmul_rn(-g.out.step, y.z));
+          y.w = __fadd_rn(__fmul_rn(old[k].w, g.out.decay), __fmul_rn(-g.out.step, y.w));
+          *reinterpret_cast<float4*>(g.out.master + at) = y;
+          *reinterpret_cast<uint2*>(g.out.p16 + at) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+        } else {
+          *reinterpret_cast<uint2*>(g.out.out + at) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+        }
       }
-    } else {
-      const long long at = g.out.offset[mat] + i * g.N + j + 8 * v;
-      float* w = g.out.master + at;
-      uint16_t* p = g.out.p16 + at;
-      if (ka.vec_out && j + 8 * v + 8 <= g.N) {
-        if (!ZFS_CHECK(at >= 0 && at + 8 <= g.out.total_padded)) continue;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float4 old = *reinterpret_cast<const float4*>(w + 4 * q);
-          const float o[4] = {old.x, old.y, old.z, old.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            y[4 * q + k] = __fadd_rn(__fmul_rn(o[k], g.out.decay), __fmul_rn(-g.out.step, y[4 * q + k]));
-          *reinterpret_cast<float4*>(w + 4 * q) = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
-        }
-        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                                  pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+    }
+  } else {  // a row per warp, columns lane and lane + 32
+#pragma unroll 4
+    for (int k = 0; k < 32; ++k) {
+      const int r = warp * 16 + k / 2, c = lane + 32 * (k % 2);
+      if (i0 + r >= g.M || j0 + c >= g.N) continue;
+      const long long at = base + (i0 + r) * pitch + j0 + c;
+      float y;
+      asm volatile("ld.shared.f32 %0, [%1];"
+                   : "=f"(y)
+                   : "r"(buffer + r * 256 + (((c / 4) ^ (r & 7)) << 4) + c % 4 * 4)
+                   : "memory");
+      if constexpr (kEpi == kNsMuon) {
+        if (!ZFS_CHECK(at >= 0 && at < g.out.total_padded)) continue;
+        y = __fadd_rn(__fmul_rn(g.out.master[at], g.out.decay), __fmul_rn(-g.out.step, y));
+        g.out.master[at] = y;
+        g.out.p16[at] = to_bf16_bits(y);
       } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (j + 8 * v + k >= g.N || !ZFS_CHECK(at >= 0 && at + k < g.out.total_padded)) continue;
-          const float z = __fadd_rn(__fmul_rn(w[k], g.out.decay), __fmul_rn(-g.out.step, y[k]));
-          w[k] = z;
-          p[k] = to_bf16_bits(z);
-        }
+        g.out.out[at] = to_bf16_bits(y);
       }
     }
   }
@@ -154,19 +169,19 @@ __device__ __forceinline__ void store_columns(const GemmKernelArgs& ka, int mat,
 
 // Tile t of all matrices: (matrix, tile row, tile column).
 template <int kEpi>
-__device__ __forceinline__ void locate(const GemmKernelArgs& ka, long long t, int* mat, long long* ti, long long* tj) {
-  *mat = static_cast<int>(t / ka.tiles);
-  long long r = t - *mat * ka.tiles;
+__device__ __forceinline__ void locate(const GemmKernelArgs& ka, int t, int* mat, int* ti, int* tj) {
+  *mat = t / ka.tiles;
+  int r = t - *mat * ka.tiles;
   if constexpr (kEpi == kNsGram || kEpi == kNsPoly) {  // rows of the lower triangle, one after another
-    long long i = static_cast<long long>((sqrt(8.0 * static_cast<double>(r) + 1.0) - 1.0) * 0.5);
-    while (i * (i + 1) / 2 > r) --i;
-    while ((i + 1) * (i + 2) / 2 <= r) ++i;
+    int i = static_cast<int>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
+    while (static_cast<long long>(i) * (i + 1) / 2 > r) --i;
+    while (static_cast<long long>(i + 1) * (i + 2) / 2 <= r) ++i;
     *ti = i;
-    *tj = r - i * (i + 1) / 2;
+    *tj = r - static_cast<int>(static_cast<long long>(i) * (i + 1) / 2);
   } else {  // bands of 8 tile rows, so that tiles in flight share operands in L2
-    constexpr long long kBand = 8;
-    const long long band = r / (kBand * ka.tiles_n), first = band * kBand;
-    const long long high = ka.tiles_m - first < kBand ? ka.tiles_m - first : kBand;
+    constexpr int kBand = 8;
+    const int band = r / (kBand * ka.tiles_n), first = band * kBand;
+    const int high = ka.tiles_m - first < kBand ? ka.tiles_m - first : kBand;
     r -= band * kBand * ka.tiles_n;
     *ti = first + r % high;
     *tj = r / high;
@@ -178,15 +193,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
   constexpr int kBlockN = 128 * kCtas;  // columns of a tile; rows: kBlockM * kCtas
   constexpr uint32_t kTmemColumns = 2 * kBlockN;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 6];
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
   const GemmArgs& g = ka.g;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t stages = (smem_u32(smem_raw) + 1023) & ~1023u;
+  const uint32_t stages = (smem_u32(smem_raw) + 1023) & ~1023u, buffers = stages + kStages * kStageBytes;
   const uint32_t rank = kCtas == 2 ? blockIdx.x % 2 : 0;
   const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tmem_full = empty + 8 * kStages,
-                 tmem_empty = tmem_full + 16;
+                 tmem_empty = tmem_full + 16, c_full = tmem_empty + 16;
   if (threadIdx.x == 0) {
     gave_up = 0;
     for (int s = 0; s < kStages; ++s) {
@@ -196,6 +211,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
     for (int s = 0; s < 2; ++s) {
       mbar_init(tmem_full + 8 * s, 1);
       mbar_init(tmem_empty + 8 * s, kEpilogueWarps * kCtas);
+      mbar_init(c_full + 8 * s, 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -205,8 +221,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
   if constexpr (kCtas == 2) cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
-  const long long first = blockIdx.x / kCtas, step = gridDim.x / kCtas, total = ka.tiles * g.mats;
+  const int first = blockIdx.x / kCtas, step = gridDim.x / kCtas, total = ka.tiles * g.mats;
   const int k_steps = ka.k_blocks;
+  // The next kernel may take free SMs from here on; what the one before wrote
+  // is read only after it has finished.
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   bool skip = false;
   if constexpr (kEpi == kNsMuon) skip = g.out.dev_t && *g.out.dev_t >= g.out.dev_steps;
 
@@ -215,12 +235,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
     uint32_t stage = 0, parity = 0;
     long long issued = 0;
     bool ok = true;
-    for (long long t = first; t < total && ok; t += step) {
-      int mat;
-      long long ti, tj;
+    for (int t = first; t < total && ok; t += step) {
+      int mat, ti, tj;
       locate<kEpi>(ka, t, &mat, &ti, &tj);
-      const int i0 = static_cast<int>(ti * kBlockM * kCtas + rank * kBlockM);
-      const int j0 = static_cast<int>(tj * kBlockN + rank * 128);
+      const int i0 = ti * kBlockM * kCtas + rank * kBlockM;
+      const int j0 = tj * kBlockN + rank * 128;
       for (int s = 0; s < k_steps; ++s) {
         const int k0 = s * kBlockK;
         if (!wait_phase(empty + 8 * stage, parity ^ 1, &gave_up)) {
@@ -283,7 +302,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
     const uint64_t step_a = g.a.k_major ? 32 >> 4 : 2048 >> 4, step_b = g.b.k_major ? 32 >> 4 : 2048 >> 4;
     uint32_t stage = 0, parity = 0, acc = 0, acc_parity = 0;
     bool ok = true;
-    for (long long t = first; t < total && ok; t += step) {
+    for (int t = first; t < total && ok; t += step) {
       ok = wait_phase(tmem_empty + 8 * acc, acc_parity ^ 1, &gave_up);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -310,28 +329,139 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
     }
   } else if (warp < kEpilogueWarps && !skip) {
     // ---- epilogue -------------------------------------------------------------
-    const uint32_t quadrant = warp % 4, half = warp / 4;
-    uint32_t acc = 0, acc_parity = 0;
-    for (long long t = first; t < total; t += step) {
-      int mat;
-      long long ti, tj;
+    constexpr bool kHasC = kEpi != kNsGram;
+    constexpr bool kRows = kEpi == kNsOut || kEpi == kNsMuon;  // finished rows, not a TMA store
+    constexpr bool kSymmetric = kEpi == kNsGram || kEpi == kNsPoly;
+    constexpr int kChunks = kBlockN / kChunk;
+    const bool leader = threadIdx.x == 0;
+    const int quadrant = warp % 4, half = warp / 4, r = quadrant * 32 + lane;
+    const uint32_t c_bytes = kHalfBytes * (g.c_lo ? 2 : 1);
+    // C of the n-th chunk of this CTA (its tile and column) into buffer n % 2.
+    auto load_c = [&](int t, int chunk, int n) {
+      int mat, ti, tj;
       locate<kEpi>(ka, t, &mat, &ti, &tj);
-      if (!__all_sync(0xffffffffu, wait_phase(tmem_full + 8 * acc, acc_parity, &gave_up))) break;
-      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      const long long i = ti * kBlockM * kCtas + rank * kBlockM + quadrant * 32 + lane;
-      const bool mirror = (kEpi == kNsGram || kEpi == kNsPoly) && ti != tj;
-#pragma unroll 1
-      for (int c = half * kBlockN / 2; c < static_cast<int>(half + 1) * kBlockN / 2; c += 32) {
-        float x[32];
-        __syncwarp();
-        tmem_load32(tmem + acc * kBlockN + ((quadrant * 32) << 16) + c, x);
-        store_columns<kEpi>(ka, mat, i, tj * kBlockN + c, mirror, x);
+      const int i0 = ti * kBlockM * kCtas + rank * kBlockM, j0 = tj * kBlockN + chunk * kChunk;
+      const uint32_t to = buffers + (n & 1) * kBufferBytes, bar = c_full + 8 * (n & 1);
+      mbar_expect_tx(bar, c_bytes);
+      tma_load<1>(to, &ka.c, j0, i0, mat, bar);
+      tma_load<1>(to + kHalfBytes / 2, &ka.c, j0, i0 + 64, mat, bar);
+      if (g.c_lo) {
+        tma_load<1>(to + kHalfBytes, &ka.c_lo, j0, i0, mat, bar);
+        tma_load<1>(to + kHalfBytes + kHalfBytes / 2, &ka.c_lo, j0, i0 + 64, mat, bar);
       }
-      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(kCtas == 2 ? map_rank(tmem_empty + 8 * acc, 0) : tmem_empty + 8 * acc);
+    };
+    uint32_t acc = 0, acc_parity = 0;
+    int n = 0, loads = 0;  // chunks so far, and C's on their way or here
+    if (kHasC && leader && first < total) {
+      load_c(first, 0, 0);
+      ++loads;
+    }
+    bool ok = true;
+    for (int t = first; t < total; t += step) {
+      int mat, ti, tj;
+      locate<kEpi>(ka, t, &mat, &ti, &tj);
+      const int i0 = ti * kBlockM * kCtas + rank * kBlockM;
+      const bool mirror = kSymmetric && ti != tj;
+      ok = wait_phase(tmem_full + 8 * acc, acc_parity, &gave_up) && ok;
+      if (epilogue_any(!ok)) break;  // all or none, so that the barriers below stay matched
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+#pragma unroll 1
+      for (int chunk = 0; chunk < kChunks; ++chunk, ++n) {
+        const uint32_t buffer = buffers + (n & 1) * kBufferBytes;
+        const int j0 = tj * kBlockN + chunk * kChunk;
+        if (leader) {
+          // the other buffer's store (the chunk before) has been read: its next C may come
+          if constexpr (!kRows) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          const bool more = chunk + 1 < kChunks;
+          if (kHasC && (more || t + step < total)) {
+            load_c(more ? t : t + step, more ? chunk + 1 : 0, n + 1);
+            ++loads;
+          }
+        }
+        float y[32];
+        __syncwarp();
+        tmem_load32(tmem + acc * kBlockN + ((quadrant * 32) << 16) + chunk * kChunk + half * 32, y);
+        if (chunk + 1 == kChunks) {  // the accumulator is drained
+          asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(kCtas == 2 ? map_rank(tmem_empty + 8 * acc, 0) : tmem_empty + 8 * acc);
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) y[k] *= g.alpha;
+        if constexpr (kHasC) {
+          if (!wait_phase(c_full + 8 * (n & 1), (n >> 1) & 1, &gave_up)) ok = false;
+          add_pieces(buffer, r, half * 4, g.cfactor, y);
+          if (g.c_lo) add_pieces(buffer + kHalfBytes, r, half * 4, g.cfactor, y);
+        }
+        if constexpr (kRows) {
+          epilogue_sync();  // every thread has its C
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            sts16(buffer + r * 256 + (((half * 8 + v) ^ (r & 7)) << 4),
+                  make_uint4(__float_as_uint(y[4 * v]), __float_as_uint(y[4 * v + 1]), __float_as_uint(y[4 * v + 2]),
+                             __float_as_uint(y[4 * v + 3])));
+          epilogue_sync();
+          if (ok && j0 < g.N) store_rows<kEpi>(ka, mat, buffer, i0, j0, warp, lane);
+          asm volatile("fence.proxy.async;" ::: "memory");
+          epilogue_sync();  // the buffer is free again
+        } else {
+          // Without C, that this buffer's store has been read is known to the leader alone.
+          if constexpr (!kHasC) epilogue_sync();
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h[k] = half2_bits(y[8 * v + 2 * k], y[8 * v + 2 * k + 1]);
+            sts16(piece_at(buffer, r, half * 4 + v), make_uint4(h[0], h[1], h[2], h[3]));
+            if constexpr (kEpi == kNsApply) {
+              if (g.d_lo) {
+                uint32_t l[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float2 hv = half2_values(h[k]);
+                  l[k] = half2_bits(y[8 * v + 2 * k] - hv.x, y[8 * v + 2 * k + 1] - hv.y);
+                }
+                sts16(piece_at(buffer + kHalfBytes, r, half * 4 + v), make_uint4(l[0], l[1], l[2], l[3]));
+              }
+            } else if (mirror) {
+              // transposed: row c of the two 64 x 64 boxes, column r
+              const uint32_t box = buffer + kHalfBytes + (r / 64) * (kHalfBytes / 2);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int c = half * 32 + 8 * v + k;
+                sts2(box + c * 128 + (((r % 64 / 8) ^ (c & 7)) << 4) + r % 8 * 2,
+                     static_cast<uint16_t>(h[k / 2] >> (16 * (k % 2))));
+              }
+            }
+          }
+          asm volatile("fence.proxy.async;" ::: "memory");
+          epilogue_sync();
+          if (leader && j0 < g.N) {
+            // boxes that reach over the matrix's end are cut there by the copy
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const int i = i0 + 64 * b;
+              const uint32_t one = buffer + b * (kHalfBytes / 2), two = one + kHalfBytes;
+              if (i >= g.M) break;
+              tma_store(&ka.d, one, j0, i, mat);
+              if (mirror) tma_store(&ka.d, two, i, j0, mat);
+              if (kEpi == kNsApply && g.d_lo) tma_store(&ka.d_lo, two, j0, i, mat);
+            }
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        }
+      }
       acc ^= 1;
       if (acc == 0) acc_parity ^= 1;
+    }
+    if (leader) {
+      // nothing is in flight when this CTA leaves (a C that is not used only if a role gave up)
+      if (kHasC && loads > n) {
+        const unsigned long long t0 = global_ns();
+        while (!mbar_try_wait(c_full + 8 * ((loads - 1) & 1), ((loads - 1) >> 1) & 1) && global_ns() - t0 < 50000000ull) {
+        }
+      }
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   }
   __syncwarp();
@@ -372,29 +502,45 @@ bool encode(CUtensorMap* map, const GemmOperand& o, long long mn, long long k, i
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Map of C or D, M x N, in boxes of 64 x 64.
+bool encode_result(CUtensorMap* map, const uint16_t* data, const GemmArgs& g) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(g.N), static_cast<cuuint64_t>(g.M),
+                              static_cast<cuuint64_t>(g.mats)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(g.ldd) * 2, static_cast<cuuint64_t>(g.d_mat_stride) * 2};
+  const cuuint32_t box[3] = {64, 64, 1};
+  const cuuint32_t unit[3] = {1, 1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(data), dims, strides, box, unit,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int kCtas, int kEpi>
 cudaError_t launch(GemmKernelArgs& ka, cudaStream_t stream) {
   const GemmArgs& g = ka.g;
-  const long long tile = 128 * kCtas;
-  ka.tiles_m = (g.M + tile - 1) / tile;
-  ka.tiles_n = (g.N + tile - 1) / tile;
-  ka.tiles = kEpi == kNsGram || kEpi == kNsPoly ? ka.tiles_m * (ka.tiles_m + 1) / 2 : ka.tiles_m * ka.tiles_n;
+  const long long tile = 128 * kCtas, tiles_m = (g.M + tile - 1) / tile, tiles_n = (g.N + tile - 1) / tile;
+  const long long all = kEpi == kNsGram || kEpi == kNsPoly ? tiles_m * (tiles_m + 1) / 2 : tiles_m * tiles_n;
+  if (all * g.mats > 0x3fffffffLL) return cudaErrorInvalidValue;
+  ka.tiles_m = static_cast<int>(tiles_m);
+  ka.tiles_n = static_cast<int>(tiles_n);
+  ka.tiles = static_cast<int>(all);
   const cudaError_t e =
       cudaFuncSetAttribute(ns_gemm_kernel<kCtas, kEpi>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  const long long tiles = ka.tiles * g.mats, room = sm_count() / kCtas;
+  const long long tiles = all * g.mats, room = sm_count() / kCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((tiles < room ? tiles : room) * kCtas));
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kCtas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, ns_gemm_kernel<kCtas, kEpi>, ka);
 }
 
@@ -417,13 +563,15 @@ cudaError_t launch_ns_gemm(const GemmArgs& g, cudaStream_t stream, int* launches
   ka.g = g;
   ka.k_blocks = static_cast<int>((g.K + kBlockK - 1) / kBlockK);
   if (!encode(&ka.a, g.a, g.M, g.K, g.mats) || !encode(&ka.b, g.b, g.N, g.K, g.mats)) return cudaErrorInvalidValue;
+  if ((g.c && !encode_result(&ka.c, g.c, g)) || (g.c_lo && !encode_result(&ka.c_lo, g.c_lo, g)) ||
+      (g.d && !encode_result(&ka.d, g.d, g)) || (g.d_lo && !encode_result(&ka.d_lo, g.d_lo, g)))
+    return cudaErrorInvalidValue;
   ka.vec_out = 0;
   if (g.epilogue == kNsOut) {
-    ka.vec_out = g.out.row_stride % kVec == 0 && g.out.mat_stride % kVec == 0 &&
-                 reinterpret_cast<uintptr_t>(g.out.out) % 16 == 0;
+    ka.vec_out = g.out.row_stride % 4 == 0 && g.out.mat_stride % 4 == 0 && reinterpret_cast<uintptr_t>(g.out.out) % 8 == 0;
   } else if (g.epilogue == kNsMuon) {
-    ka.vec_out = g.N % kVec == 0;
-    for (int m = 0; m < g.mats; ++m) ka.vec_out = ka.vec_out && g.out.offset[m] % kVec == 0;
+    ka.vec_out = g.N % 4 == 0;
+    for (int m = 0; m < g.mats; ++m) ka.vec_out = ka.vec_out && g.out.offset[m] % 4 == 0;
   }
   ++*launches;
   switch (g.epilogue) {

@@ -47,17 +47,6 @@ struct Shared {
 __device__ __forceinline__ uint32_t chunk_at(uint32_t half, int r, int chunk) {
   return half + (chunk / 8) * kBlockBytes + r * 128 + (((chunk % 8) ^ (r & 7)) << 4);
 }
-__device__ __forceinline__ void sts16(uint32_t at, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ uint4 lds16(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-  return v;
-}
-__device__ __forceinline__ void sts2(uint32_t at, uint16_t v) {
-  asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(v) : "memory");
-}
 // The nearest fp16 pair of eight values.
 __device__ __forceinline__ void split8(const float* x, uint32_t* hi, uint32_t* lo) {
 #pragma unroll
