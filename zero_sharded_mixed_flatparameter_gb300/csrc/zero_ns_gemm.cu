@@ -20,12 +20,14 @@
 // next one's products.  In a pair each CTA holds 128 of the 256 rows of A and
 // half of B's columns, and the first CTA issues for both.
 //
-// The epilogue moves 64 columns at a time through two 32 KB buffers: C (hi and
-// lo) comes in by TMA a chunk ahead, D goes out by TMA, both in whole 128-byte
-// rows; the final update crosses the buffer so that master and param16 are
-// read and written in whole rows too.  (Rows read and written by a thread each
-// cost the L1 a line per lane: an update of 1024 x 2048 matrices took 170 us
-// where its products take 60.)
+// Each epilogue warp works by itself, 32 rows by 64 columns at a time through
+// its own 8 KB of shared memory: C (hi and lo) comes in by TMA while the
+// products still run, D goes out by TMA, both in whole 128-byte rows; the final
+// update crosses the buffer so that master and param16 are read and written in
+// whole rows too.  (Rows read and written by a thread each cost the L1 a line
+// per lane, 170 us for an update of 16 1024 x 2048 matrices whose products take
+// 60; one buffer for all warps costs a barrier and a store's latency per 64
+// columns: 16 products of 1024 took 61 us, 33 without any epilogue.)
 
 #include <cuda.h>
 
@@ -42,19 +44,19 @@ constexpr int kBlockK = 64;            // fp16 elements of one 128-byte swizzled
 constexpr int kBlockM = 128;           // rows per CTA
 constexpr int kStages = 5;
 constexpr int kEpilogueWarps = 8;
-constexpr int kEpilogueThreads = kEpilogueWarps * 32;
-constexpr int kGemmThreads = kEpilogueThreads + 64;
+constexpr int kGemmThreads = (kEpilogueWarps + 2) * 32;
 constexpr uint32_t kOperandBytes = kBlockM * kBlockK * 2;
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
 constexpr int kChunk = 64;             // columns of a step of the epilogue
-constexpr uint32_t kHalfBytes = kBlockM * kChunk * 2;  // a chunk of hi (or of lo, or transposed)
+constexpr uint32_t kHalfBytes = 32 * kChunk * 2;  // a warp's chunk of hi (or of lo, or transposed)
 constexpr uint32_t kBufferBytes = 2 * kHalfBytes;
-constexpr uint32_t kSmemBytes = kStages * kStageBytes + 2 * kBufferBytes + 1024;  // + alignment
+constexpr uint32_t kSmemBytes = kStages * kStageBytes + kEpilogueWarps * kBufferBytes + 1024;  // + alignment
 
 // What one launch needs.
 struct GemmKernelArgs {
   CUtensorMap a, b;
-  CUtensorMap c, c_lo, d, d_lo;  // boxes of 64 x 64
+  CUtensorMap c, c_lo, d, d_lo;  // boxes of 64 x 32
+  CUtensorMap d_mirror;          // boxes of 32 x 64
   GemmArgs g;
   int tiles_m, tiles_n, tiles;   // tiles of one matrix / of all
   int k_blocks;
@@ -66,20 +68,8 @@ __device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, 
                "r"(y), "r"(z), "r"(src)
                : "memory");
 }
-// A barrier of the epilogue's warps that tells whether any thread says `x`.
-__device__ __forceinline__ bool epilogue_any(bool x) {
-  uint32_t any;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(any)
-      : "r"(x ? 1u : 0u), "n"(kEpilogueThreads)
-      : "memory");
-  return any != 0;
-}
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueThreads) : "memory"); }
-
 // ---- epilogue ----------------------------------------------------------------
-// Address of the 16-byte piece `piece` (of 8) of row r in a 128 x 64 half.
+// Address of the 16-byte piece `piece` (of 8) of row r in a 32 x 64 half.
 __device__ __forceinline__ uint32_t piece_at(uint32_t half, int r, int piece) {
   return half + r * 128 + ((piece ^ (r & 7)) << 4);
 }
@@ -99,27 +89,23 @@ __device__ __forceinline__ void add_pieces(uint32_t half, int r, int first, floa
   }
 }
 
-// Whole rows of a finished chunk (fp32 in `buffer`, 16-byte pieces swizzled by
-// row) to their place: rows i0 .. i0+127 of the matrix, columns j0 .. j0+63.
+// Whole rows of a warp's finished chunk (32 x 64 fp32 in `buffer`, 16-byte
+// pieces swizzled by row) to their place, from row i0 and column j0.
 template <int kEpi>
 __device__ __forceinline__ void store_rows(const GemmKernelArgs& ka, int mat, uint32_t buffer, long long i0, long long j0,
-                                           int warp, int lane) {
+                                           int lane) {
   const GemmArgs& g = ka.g;
-  auto value4 = [&](int r, int piece) {
-    const uint4 v = lds16(buffer + r * 256 + ((piece ^ (r & 7)) << 4));
-    return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
-  };
   const long long base = kEpi == kNsMuon ? g.out.offset[mat] : mat * g.out.mat_stride;
   const long long pitch = kEpi == kNsMuon ? g.N : g.out.row_stride;
-  if (ka.vec_out && j0 + kChunk <= g.N) {  // two rows per warp and access
+  if (ka.vec_out && j0 + kChunk <= g.N) {  // two rows per access
     const int piece = lane % 16;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q) {
       float4 old[4];
       if constexpr (kEpi == kNsMuon) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int r = warp * 16 + (q * 4 + k) * 2 + lane / 16;
+          const int r = (q * 4 + k) * 2 + lane / 16;
           const long long at = base + (i0 + r) * pitch + j0 + 4 * piece;
           if (i0 + r < g.M && ZFS_CHECK(at >= 0 && at + 4 <= g.out.total_padded))
             old[k] = *reinterpret_cast<const float4*>(g.out.master + at);
@@ -127,10 +113,11 @@ __device__ __forceinline__ void store_rows(const GemmKernelArgs& ka, int mat, ui
       }
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int r = warp * 16 + (q * 4 + k) * 2 + lane / 16;
+        const int r = (q * 4 + k) * 2 + lane / 16;
         const long long at = base + (i0 + r) * pitch + j0 + 4 * piece;
         if (i0 + r >= g.M) continue;
-        float4 y = value4(r, piece);
+        const uint4 v = lds16(buffer + r * 256 + ((piece ^ (r & 7)) << 4));
+        float4 y = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
         if constexpr (kEpi == kNsMuon) {
           if (!ZFS_CHECK(at >= 0 && at + 4 <= g.out.total_padded)) continue;
           y.x = __fadd_rn(__fmul_rn(old[k].x, g.out.decay), __fmul_rn(-g.out.step, y.x));
@@ -144,10 +131,10 @@ __device__ __forceinline__ void store_rows(const GemmKernelArgs& ka, int mat, ui
         }
       }
     }
-  } else {  // a row per warp, columns lane and lane + 32
+  } else {  // columns lane and lane + 32
 #pragma unroll 4
-    for (int k = 0; k < 32; ++k) {
-      const int r = warp * 16 + k / 2, c = lane + 32 * (k % 2);
+    for (int k = 0; k < 64; ++k) {
+      const int r = k / 2, c = lane + 32 * (k % 2);
       if (i0 + r >= g.M || j0 + c >= g.N) continue;
       const long long at = base + (i0 + r) * pitch + j0 + c;
       float y;
@@ -193,7 +180,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
   constexpr int kBlockN = 128 * kCtas;  // columns of a tile; rows: kBlockM * kCtas
   constexpr uint32_t kTmemColumns = 2 * kBlockN;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kStages + 6];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 4 + kEpilogueWarps];
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
   const GemmArgs& g = ka.g;
@@ -211,8 +198,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
     for (int s = 0; s < 2; ++s) {
       mbar_init(tmem_full + 8 * s, 1);
       mbar_init(tmem_empty + 8 * s, kEpilogueWarps * kCtas);
-      mbar_init(c_full + 8 * s, 1);
     }
+    for (int w = 0; w < kEpilogueWarps; ++w) mbar_init(c_full + 8 * w, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 9) tmem_alloc<kCtas>(smem_u32(&tmem_base), kTmemColumns);
@@ -332,133 +319,132 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
     constexpr bool kHasC = kEpi != kNsGram;
     constexpr bool kRows = kEpi == kNsOut || kEpi == kNsMuon;  // finished rows, not a TMA store
     constexpr bool kSymmetric = kEpi == kNsGram || kEpi == kNsPoly;
-    constexpr int kChunks = kBlockN / kChunk;
-    const bool leader = threadIdx.x == 0;
-    const int quadrant = warp % 4, half = warp / 4, r = quadrant * 32 + lane;
+    constexpr int kChunks = kBlockN / kChunk / 2;  // per warp and tile
+    const int quadrant = warp % 4, half = warp / 4;
+    const uint32_t buffer = buffers + warp * kBufferBytes, bar = c_full + 8 * warp;
     const uint32_t c_bytes = kHalfBytes * (g.c_lo ? 2 : 1);
-    // C of the n-th chunk of this CTA (its tile and column) into buffer n % 2.
-    auto load_c = [&](int t, int chunk, int n) {
+    // This warp's C of a tile's chunk into its buffer; one lane.
+    auto load_c = [&](int t, int chunk) {
       int mat, ti, tj;
       locate<kEpi>(ka, t, &mat, &ti, &tj);
-      const int i0 = ti * kBlockM * kCtas + rank * kBlockM, j0 = tj * kBlockN + chunk * kChunk;
-      const uint32_t to = buffers + (n & 1) * kBufferBytes, bar = c_full + 8 * (n & 1);
+      const int i0 = ti * kBlockM * kCtas + rank * kBlockM + quadrant * 32, j0 = tj * kBlockN + (2 * chunk + half) * kChunk;
       mbar_expect_tx(bar, c_bytes);
-      tma_load<1>(to, &ka.c, j0, i0, mat, bar);
-      tma_load<1>(to + kHalfBytes / 2, &ka.c, j0, i0 + 64, mat, bar);
-      if (g.c_lo) {
-        tma_load<1>(to + kHalfBytes, &ka.c_lo, j0, i0, mat, bar);
-        tma_load<1>(to + kHalfBytes + kHalfBytes / 2, &ka.c_lo, j0, i0 + 64, mat, bar);
-      }
+      tma_load<1>(buffer, &ka.c, j0, i0, mat, bar);
+      if (g.c_lo) tma_load<1>(buffer + kHalfBytes, &ka.c_lo, j0, i0, mat, bar);
     };
-    uint32_t acc = 0, acc_parity = 0;
-    int n = 0, loads = 0;  // chunks so far, and C's on their way or here
-    if (kHasC && leader && first < total) {
-      load_c(first, 0, 0);
-      ++loads;
+    uint32_t acc = 0, acc_parity = 0, c_parity = 0;
+    bool loaded = false;  // a C is on its way or here
+    if (kHasC && lane == 0 && first < total) {
+      load_c(first, 0);
+      loaded = true;
     }
     bool ok = true;
-    for (int t = first; t < total; t += step) {
+    for (int t = first; t < total && ok; t += step) {
       int mat, ti, tj;
       locate<kEpi>(ka, t, &mat, &ti, &tj);
-      const int i0 = ti * kBlockM * kCtas + rank * kBlockM;
+      const int i0 = ti * kBlockM * kCtas + rank * kBlockM + quadrant * 32;
       const bool mirror = kSymmetric && ti != tj;
-      ok = wait_phase(tmem_full + 8 * acc, acc_parity, &gave_up) && ok;
-      if (epilogue_any(!ok)) break;  // all or none, so that the barriers below stay matched
+      ok = __all_sync(0xffffffffu, wait_phase(tmem_full + 8 * acc, acc_parity, &gave_up));
+      if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 #pragma unroll 1
-      for (int chunk = 0; chunk < kChunks; ++chunk, ++n) {
-        const uint32_t buffer = buffers + (n & 1) * kBufferBytes;
-        const int j0 = tj * kBlockN + chunk * kChunk;
-        if (leader) {
-          // the other buffer's store (the chunk before) has been read: its next C may come
-          if constexpr (!kRows) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          const bool more = chunk + 1 < kChunks;
-          if (kHasC && (more || t + step < total)) {
-            load_c(more ? t : t + step, more ? chunk + 1 : 0, n + 1);
-            ++loads;
+      for (int chunk = 0; chunk < kChunks; ++chunk) {
+        const int j0 = tj * kBlockN + (2 * chunk + half) * kChunk;
+        const uint32_t from = tmem + acc * kBlockN + ((quadrant * 32) << 16) + (2 * chunk + half) * kChunk;
+        if constexpr (kHasC) {
+          ok = __all_sync(0xffffffffu, wait_phase(bar, c_parity, &gave_up));
+          if (!ok) break;
+          c_parity ^= 1;
+          loaded = false;
+        } else {
+          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          __syncwarp();
+        }
+        float y[2][32];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          tmem_load32(from + 32 * q, y[q]);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) y[q][k] *= g.alpha;
+          if constexpr (kHasC) {
+            add_pieces(buffer, lane, 4 * q, g.cfactor, y[q]);
+            if (g.c_lo) add_pieces(buffer + kHalfBytes, lane, 4 * q, g.cfactor, y[q]);
+          }
+          if constexpr (!kRows) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const float* z = y[q] + 8 * v;
+              uint32_t h[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) h[k] = half2_bits(z[2 * k], z[2 * k + 1]);
+              sts16(piece_at(buffer, lane, 4 * q + v), make_uint4(h[0], h[1], h[2], h[3]));
+              if constexpr (kEpi == kNsApply) {
+                if (g.d_lo) {
+                  uint32_t l[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    const float2 hv = half2_values(h[k]);
+                    l[k] = half2_bits(z[2 * k] - hv.x, z[2 * k + 1] - hv.y);
+                  }
+                  sts16(piece_at(buffer + kHalfBytes, lane, 4 * q + v), make_uint4(l[0], l[1], l[2], l[3]));
+                }
+              } else if (mirror) {
+                // transposed, rows of 64 bytes: row c, column `lane`
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const int c = 32 * q + 8 * v + k;
+                  sts2(buffer + kHalfBytes + c * 64 + (((lane / 8) ^ ((c >> 1) & 3)) << 4) + lane % 8 * 2,
+                       static_cast<uint16_t>(h[k / 2] >> (16 * (k % 2))));
+                }
+              }
+            }
           }
         }
-        float y[32];
-        __syncwarp();
-        tmem_load32(tmem + acc * kBlockN + ((quadrant * 32) << 16) + chunk * kChunk + half * 32, y);
-        if (chunk + 1 == kChunks) {  // the accumulator is drained
+        if (chunk + 1 == kChunks) {  // this warp's part of the accumulator is drained
           asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(kCtas == 2 ? map_rank(tmem_empty + 8 * acc, 0) : tmem_empty + 8 * acc);
         }
-#pragma unroll
-        for (int k = 0; k < 32; ++k) y[k] *= g.alpha;
-        if constexpr (kHasC) {
-          if (!wait_phase(c_full + 8 * (n & 1), (n >> 1) & 1, &gave_up)) ok = false;
-          add_pieces(buffer, r, half * 4, g.cfactor, y);
-          if (g.c_lo) add_pieces(buffer + kHalfBytes, r, half * 4, g.cfactor, y);
-        }
         if constexpr (kRows) {
-          epilogue_sync();  // every thread has its C
+          __syncwarp();  // every lane has its C
 #pragma unroll
-          for (int v = 0; v < 8; ++v)
-            sts16(buffer + r * 256 + (((half * 8 + v) ^ (r & 7)) << 4),
-                  make_uint4(__float_as_uint(y[4 * v]), __float_as_uint(y[4 * v + 1]), __float_as_uint(y[4 * v + 2]),
-                             __float_as_uint(y[4 * v + 3])));
-          epilogue_sync();
-          if (ok && j0 < g.N) store_rows<kEpi>(ka, mat, buffer, i0, j0, warp, lane);
-          asm volatile("fence.proxy.async;" ::: "memory");
-          epilogue_sync();  // the buffer is free again
-        } else {
-          // Without C, that this buffer's store has been read is known to the leader alone.
-          if constexpr (!kHasC) epilogue_sync();
+          for (int q = 0; q < 2; ++q) {
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint32_t h[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) h[k] = half2_bits(y[8 * v + 2 * k], y[8 * v + 2 * k + 1]);
-            sts16(piece_at(buffer, r, half * 4 + v), make_uint4(h[0], h[1], h[2], h[3]));
-            if constexpr (kEpi == kNsApply) {
-              if (g.d_lo) {
-                uint32_t l[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float2 hv = half2_values(h[k]);
-                  l[k] = half2_bits(y[8 * v + 2 * k] - hv.x, y[8 * v + 2 * k + 1] - hv.y);
-                }
-                sts16(piece_at(buffer + kHalfBytes, r, half * 4 + v), make_uint4(l[0], l[1], l[2], l[3]));
-              }
-            } else if (mirror) {
-              // transposed: row c of the two 64 x 64 boxes, column r
-              const uint32_t box = buffer + kHalfBytes + (r / 64) * (kHalfBytes / 2);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const int c = half * 32 + 8 * v + k;
-                sts2(box + c * 128 + (((r % 64 / 8) ^ (c & 7)) << 4) + r % 8 * 2,
-                     static_cast<uint16_t>(h[k / 2] >> (16 * (k % 2))));
-              }
-            }
+            for (int v = 0; v < 8; ++v)
+              sts16(buffer + lane * 256 + (((8 * q + v) ^ (lane & 7)) << 4),
+                    make_uint4(__float_as_uint(y[q][4 * v]), __float_as_uint(y[q][4 * v + 1]),
+                               __float_as_uint(y[q][4 * v + 2]), __float_as_uint(y[q][4 * v + 3])));
           }
-          asm volatile("fence.proxy.async;" ::: "memory");
-          epilogue_sync();
-          if (leader && j0 < g.N) {
-            // boxes that reach over the matrix's end are cut there by the copy
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const int i = i0 + 64 * b;
-              const uint32_t one = buffer + b * (kHalfBytes / 2), two = one + kHalfBytes;
-              if (i >= g.M) break;
-              tma_store(&ka.d, one, j0, i, mat);
-              if (mirror) tma_store(&ka.d, two, i, j0, mat);
-              if (kEpi == kNsApply && g.d_lo) tma_store(&ka.d_lo, two, j0, i, mat);
+          __syncwarp();
+          if (i0 < g.M && j0 < g.N) store_rows<kEpi>(ka, mat, buffer, i0, j0, lane);
+        }
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (!kRows) {
+            if (i0 < g.M && j0 < g.N) {  // what reaches over the matrix's end is cut by the copy
+              tma_store(&ka.d, buffer, j0, i0, mat);
+              if (mirror) tma_store(&ka.d_mirror, buffer + kHalfBytes, i0, j0, mat);
+              if (kEpi == kNsApply && g.d_lo) tma_store(&ka.d_lo, buffer + kHalfBytes, j0, i0, mat);
             }
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+          const bool more = chunk + 1 < kChunks;
+          if (kHasC && (more || t + step < total)) {
+            if constexpr (!kRows) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            load_c(more ? t : t + step, more ? chunk + 1 : 0);
+            loaded = true;
           }
         }
       }
       acc ^= 1;
       if (acc == 0) acc_parity ^= 1;
     }
-    if (leader) {
+    if (lane == 0) {
       // nothing is in flight when this CTA leaves (a C that is not used only if a role gave up)
-      if (kHasC && loads > n) {
+      if (loaded) {
         const unsigned long long t0 = global_ns();
-        while (!mbar_try_wait(c_full + 8 * ((loads - 1) & 1), ((loads - 1) >> 1) & 1) && global_ns() - t0 < 50000000ull) {
+        while (!mbar_try_wait(bar, c_parity) && global_ns() - t0 < 50000000ull) {
         }
       }
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -502,16 +488,16 @@ bool encode(CUtensorMap* map, const GemmOperand& o, long long mn, long long k, i
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Map of C or D, M x N, in boxes of 64 x 64.
-bool encode_result(CUtensorMap* map, const uint16_t* data, const GemmArgs& g) {
+// Map of C or D, M x N, in boxes of `columns` x `rows`.
+bool encode_result(CUtensorMap* map, const uint16_t* data, const GemmArgs& g, cuuint32_t columns, cuuint32_t rows) {
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(g.N), static_cast<cuuint64_t>(g.M),
                               static_cast<cuuint64_t>(g.mats)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(g.ldd) * 2, static_cast<cuuint64_t>(g.d_mat_stride) * 2};
-  const cuuint32_t box[3] = {64, 64, 1};
+  const cuuint32_t box[3] = {columns, rows, 1};
   const cuuint32_t unit[3] = {1, 1, 1};
   return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(data), dims, strides, box, unit,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, columns == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int kCtas, int kEpi>
@@ -563,8 +549,10 @@ cudaError_t launch_ns_gemm(const GemmArgs& g, cudaStream_t stream, int* launches
   ka.g = g;
   ka.k_blocks = static_cast<int>((g.K + kBlockK - 1) / kBlockK);
   if (!encode(&ka.a, g.a, g.M, g.K, g.mats) || !encode(&ka.b, g.b, g.N, g.K, g.mats)) return cudaErrorInvalidValue;
-  if ((g.c && !encode_result(&ka.c, g.c, g)) || (g.c_lo && !encode_result(&ka.c_lo, g.c_lo, g)) ||
-      (g.d && !encode_result(&ka.d, g.d, g)) || (g.d_lo && !encode_result(&ka.d_lo, g.d_lo, g)))
+  const bool mirrored = g.epilogue == kNsGram || g.epilogue == kNsPoly;
+  if ((g.c && !encode_result(&ka.c, g.c, g, 64, 32)) || (g.c_lo && !encode_result(&ka.c_lo, g.c_lo, g, 64, 32)) ||
+      (g.d && !encode_result(&ka.d, g.d, g, 64, 32)) || (g.d_lo && !encode_result(&ka.d_lo, g.d_lo, g, 64, 32)) ||
+      (mirrored && !encode_result(&ka.d_mirror, g.d, g, 32, 64)))
     return cudaErrorInvalidValue;
   ka.vec_out = 0;
   if (g.epilogue == kNsOut) {
