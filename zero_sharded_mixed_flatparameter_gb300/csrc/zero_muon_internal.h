@@ -119,11 +119,21 @@ constexpr int kThinChain = 2;  // steps per Gram matrix
 // Elements of the fp32 workspace of one launch (more only for a single matrix
 // that is larger).
 constexpr long long kThinWork = 1LL << 22;
+// Factors of a step: the coefficients, and the powers of two between the
+// stored (fp16) X, A, P, Q and A P.
+struct ThinStep {
+  float x;          // X as stored
+  float gram;       // A from X X^T
+  float square, gram_term, identity;  // P from A A, from A and on its diagonal
+  float chain;      // Q from P Q
+  float inner;      // A P
+  float next;       // the next A from P (A P)
+  float result;     // Q X to its value
+};
 struct ThinArgs {
   int steps;
-  float a, b, c, eps;
-  // powers of two of the stored X0, A, P, Q and A P
-  int ex[kMaxSteps], ea[kMaxSteps], ep[kMaxSteps], eq[kMaxSteps], ew[kMaxSteps];
+  float eps;
+  ThinStep step_factors[kMaxSteps];
   int rows[kMaxMats], cols[kMaxMats];  // a stack uses entry 0
   // fp32, as many elements as the matrix (a multiple of 8 apart): the Muon
   // step's update and the iterate between two Gram matrices

@@ -3,8 +3,8 @@
 // matrices, and its normalisation into scaled fp16 pairs.
 //
 // All are one pass over memory-resident data and bound by it; the norm is
-// summed per chunk of kNsChunk elements of a matrix, in fp32 over the 64
-// elements of one thread and in fp64 above, each in a fixed order.
+// summed per chunk of kNsChunk elements of a matrix, in fp32 over the elements
+// of a warp and in fp64 above, each in a fixed order.
 
 #include <cuda_fp16.h>
 
@@ -18,9 +18,10 @@ constexpr int kThreads = 256;
 constexpr int kPerThread = static_cast<int>(kNsChunk) / kThreads;  // elements per thread and chunk
 static_assert(kPerThread % kVec == 0, "whole vectors per thread");
 
-// Sum over the CTA in a fixed order; valid in thread 0.
-__device__ __forceinline__ double block_sum(double x) {
-  __shared__ double warp_sum[kThreads / 32];
+// Sum over the CTA in a fixed order, fp32 within a warp and fp64 above (by one
+// thread: the GPU has few fp64 units); valid in thread 0.
+__device__ __forceinline__ double block_sum(float x) {
+  __shared__ float warp_sum[kThreads / 32];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_down_sync(0xffffffffu, x, o);
   if (threadIdx.x % 32 == 0) warp_sum[threadIdx.x / 32] = x;
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) momentum_kernel(const __grid_constan
     }
   }
   flush_nonfinite(a.nonfinite, nf);
-  const double s = block_sum(static_cast<double>(sq));
+  const double s = block_sum(sq);
   if (threadIdx.x == 0) a.partials[mat * a.chunks + blockIdx.x] = s;
 }
 
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int k = 0; k < kVec; ++k) sq += x[k] * x[k];
   }
-  const double sum = block_sum(static_cast<double>(sq));
+  const double sum = block_sum(sq);
   if (threadIdx.x == 0) partials[mat * chunks + blockIdx.x] = sum;
 }
 
@@ -142,8 +143,11 @@ __global__ void __launch_bounds__(kThreads) ns_scale_kernel(const __grid_constan
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // every CTA sums the matrix's partials, in the same order
   double s = 0.0;
-  for (long long k = threadIdx.x; k < a.chunks; k += kThreads) s += a.partials[mat * a.chunks + k];
-  s = block_sum(s);
+  if (threadIdx.x < 32) {
+    for (long long k = threadIdx.x; k < a.chunks; k += 32) s += a.partials[mat * a.chunks + k];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_down_sync(0xffffffffu, s, o);
+  }
   if (threadIdx.x == 0) inv_shared = static_cast<float>(1.0 / (sqrt(s) + a.eps));
   __syncthreads();
   const float inv = inv_shared;

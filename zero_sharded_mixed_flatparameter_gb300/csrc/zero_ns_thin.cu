@@ -36,8 +36,9 @@ constexpr uint32_t kTmemColumns = 256;
 
 struct Shared {
   uint64_t bar[3];
-  double warp_sum[kWarps];
   double sum;  // of this CTA's columns, read by the cluster
+  float warp_sum[kWarps];
+  float norm_scale;
   uint32_t tmem;
   int gave_up;
 };
@@ -363,25 +364,28 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
     }
   }
   if constexpr (kMuon) flush_nonfinite(a.nonfinite, nf);
-  double s = sq;
+  // fp32 over a warp, fp64 above, by one thread (the GPU has few fp64 units)
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) sh.warp_sum[warp] = s;
+  for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+  if (lane == 0) sh.warp_sum[warp] = sq;
   __syncthreads();
   if (tid == 0) {
     double t = 0.0;
     for (int w = 0; w < kWarps; ++w) t += sh.warp_sum[w];
     sh.sum = t;
   }
-  if constexpr (kCtas > 1) {
-    cluster_sync();
-    s = 0.0;
-    for (int r = 0; r < kCtas; ++r) s += ld_cluster_f64(map_rank(smem_u32(&sh.sum), r));
-  } else {
-    __syncthreads();
-    s = sh.sum;
+  if constexpr (kCtas > 1) cluster_sync();
+  if (tid == 0) {
+    double t = 0.0;
+    if constexpr (kCtas > 1) {
+      for (int r = 0; r < kCtas; ++r) t += ld_cluster_f64(map_rank(smem_u32(&sh.sum), r));
+    } else {
+      t = sh.sum;
+    }
+    sh.norm_scale = static_cast<float>(1.0 / (sqrt(t) + static_cast<double>(a.eps)));
   }
-  const float norm_scale = static_cast<float>(1.0 / (sqrt(s) + static_cast<double>(a.eps)));
+  __syncthreads();
+  const float norm_scale = sh.norm_scale;
   const int mk = x.mk;
   // the epilogue's share of a thread: row `row`, a quarter of the columns
   const int row = (warp % 4) * 32 + lane, quarter = warp / 4;
@@ -392,10 +396,10 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
 
   for (int begin = 0; begin < a.steps; begin += kThinChain) {
   const int end = min(begin + kThinChain, a.steps);
-  const int ex = a.ex[begin];
+  const ThinStep& f0 = a.step_factors[begin];
   auto fetch = [&](int j0, uint32_t buffer) {
-    if (begin == 0) load_slice<kFp32>(x, source, vec, j0, norm_scale * ldexpf(1.0f, ex), buffer);
-    else load_slice<true>(xw, work, vec_work, j0, ldexpf(1.0f, ex), buffer);
+    if (begin == 0) load_slice<kFp32>(x, source, vec, j0, norm_scale * f0.x, buffer);
+    else load_slice<true>(xw, work, vec_work, j0, f0.x, buffer);
   };
 
   // ---- Gram matrix: slices of X through the two buffers -------------------------
@@ -415,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
   ok = alive;
   if (used >= 2) ok = wait(used & 1) && ok;
   if (used >= 1) ok = wait((used + 1) & 1) && ok;
-  const float from_x = ldexpf(1.0f, -2 * ex);
+  const float from_x = f0.gram;
   if constexpr (kCtas == 1) {
     // A straight from the accumulator
     if (ok && in_rows) {
@@ -423,9 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
         float y[16];
         __syncwarp();
         tmem_load16(tmem_row + c, y);
-        const float f = from_x * ldexpf(1.0f, a.ea[begin]);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) y[k] *= f;
+        for (int k = 0; k < 16; ++k) y[k] *= from_x;
         store_pair(b0, row, c / 8, y);
         store_pair(b0, row, c / 8 + 1, y + 8);
       }
@@ -448,7 +451,6 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
     }
     cluster_sync();
     const int columns = mk / kCtas, first = rank * columns;
-    const float f = ldexpf(1.0f, a.ea[begin]);
     for (int e = tid; e < columns * (mk / 2); e += kThreads) {
       const int c = first + e / (mk / 2), r = e % (mk / 2) * 2;
       float u = 0.0f, v = 0.0f;
@@ -458,8 +460,6 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
         u += ld_cluster(at);
         v += ld_cluster(at + 4);
       }
-      u *= f;
-      v *= f;
       const uint32_t hi = half2_bits(u, v);
       const float2 h = half2_values(hi);
       const uint32_t lo = half2_bits(u - h.x, v - h.y);
@@ -479,14 +479,14 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
   // A in b0, P in b1, Q in b2; every matrix commutes with every other.
   for (int k = begin; k < end; ++k) {
     const bool first = k == begin, last = k + 1 == end;
+    const ThinStep& f = a.step_factors[k];
     if (tid == 0 && alive) {
       product(tmem, b0, b0);  // A A
       go(0);
     }
     ok = wait(0);
     if (ok && in_rows) {
-      const float fc = a.c * ldexpf(1.0f, a.ep[k] - 2 * a.ea[k]), fb = a.b * ldexpf(1.0f, a.ep[k] - a.ea[k]);
-      const float fa = a.a * ldexpf(1.0f, a.ep[k]);
+      const float fc = f.square, fb = f.gram_term, fa = f.identity;
       for (int c = quarter * 32; c < min(mk, quarter * 32 + 32); c += 16) {
         float y[16];
         __syncwarp();
@@ -514,8 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
     }
     ok = wait(0);
     if (ok && in_rows) {
-      const float fq = !first ? ldexpf(1.0f, a.eq[k] - a.ep[k] - a.eq[k - 1]) : 0.0f;
-      const float fw = ldexpf(1.0f, a.ew[k] - a.ea[k] - a.ep[k]);
+      const float fq = f.chain, fw = f.inner;
       for (int c = quarter * 32; c < min(mk, quarter * 32 + 32); c += 16) {
         float y[16];
         if (!first) {
@@ -544,13 +543,12 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
     }
     ok = wait(0);
     if (ok && in_rows) {
-      const float f = ldexpf(1.0f, a.ea[k + 1] - a.ep[k] - a.ew[k]);
       for (int c = quarter * 32; c < min(mk, quarter * 32 + 32); c += 16) {
         float y[16];
         __syncwarp();
         tmem_load16(tmem_row + c, y);
 #pragma unroll
-        for (int q = 0; q < 16; ++q) y[q] *= f;
+        for (int q = 0; q < 16; ++q) y[q] *= f.next;
         store_pair(b0, row, c / 8, y);
         store_pair(b0, row, c / 8 + 1, y + 8);
       }
@@ -559,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
   }
 
   // ---- Q X, slice after slice, the epilogue one slice behind the products -------
-  const float to_result = ldexpf(1.0f, -ex - a.eq[end - 1]);
+  const float to_result = a.step_factors[end - 1].result;
   used = 0;
   for (int j0 = rank * kSlice;; j0 += kCtas * kSlice, ++used) {
     const int i = used & 1;

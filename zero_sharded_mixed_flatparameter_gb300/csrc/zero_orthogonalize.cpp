@@ -133,24 +133,33 @@ NsPlan ns_plan(long long rows, long long cols, int mats, bool keep_update) {
 
 void thin_scales(const zero_ns_config& cfg, ThinArgs* a) {
   a->steps = cfg.steps;
-  a->a = cfg.a;
-  a->b = cfg.b;
-  a->c = cfg.c;
   a->eps = cfg.eps;
   double top = 1.0, chain = 1.0;  // spectral norms of X and of Q
+  int eq = 0, ex0 = 0;            // of the chain's last step, of its X
   for (int k = 0; k < cfg.steps; ++k) {
+    ThinStep& f = a->step_factors[k];
     // P = a I + b A + c A A with its identity
     auto q = [&](double t) { return std::fabs(cfg.a + t * (cfg.b + t * cfg.c)); };
     double p = std::max(q(0.0), q(top * top));
     const double turn = cfg.c != 0.0f ? -cfg.b / (2.0 * cfg.c) : -1.0;
     if (turn > 0.0 && turn < top * top) p = std::max(p, q(turn));
-    chain = k % kThinChain == 0 ? p : chain * p;
-    a->ex[k] = scale_exponent(top);
-    a->ea[k] = scale_exponent(top * top);
-    a->ep[k] = scale_exponent(p);
-    a->eq[k] = scale_exponent(chain);
-    a->ew[k] = scale_exponent(top * top * p);
-    top = largest_value(cfg.a, cfg.b, cfg.c, top);
+    const bool first = k % kThinChain == 0;
+    const double next = largest_value(cfg.a, cfg.b, cfg.c, top);
+    const int ex = scale_exponent(top), ea = scale_exponent(top * top), ep = scale_exponent(p);
+    const int ew = scale_exponent(top * top * p), before = eq;
+    chain = first ? p : chain * p;
+    eq = scale_exponent(chain);
+    if (first) ex0 = ex;
+    f.x = std::ldexp(1.0f, ex);
+    f.gram = std::ldexp(1.0f, ea - 2 * ex);
+    f.square = cfg.c * std::ldexp(1.0f, ep - 2 * ea);
+    f.gram_term = cfg.b * std::ldexp(1.0f, ep - ea);
+    f.identity = cfg.a * std::ldexp(1.0f, ep);
+    f.chain = std::ldexp(1.0f, eq - ep - before);
+    f.inner = std::ldexp(1.0f, ew - ea - ep);
+    f.next = std::ldexp(1.0f, scale_exponent(next * next) - ep - ew);
+    f.result = std::ldexp(1.0f, -ex0 - eq);
+    top = next;
   }
 }
 
