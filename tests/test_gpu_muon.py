@@ -297,7 +297,7 @@ def test_refusals(over, status):
 
 
 def test_state_refusals():
-    pl, shapes = mlp([16, 40, 8])
+    pl, shapes = mlp([140, 300, 8])
     fs = make(pl, shapes, 2, muon=False)
     fs.reduce_grads(-1, grads_for(fs, pl, 2, "bf16", 1))
     fs.step()

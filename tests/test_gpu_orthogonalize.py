@@ -173,8 +173,7 @@ def call(rows=8, cols=8, batch=1, cfg=None, **over):
 
 @pytest.mark.parametrize("over", [
     dict(src=0), dict(out=0), dict(in_row_stride=7),
-    dict(workspace=0), dict(workspace_bytes=100), dict(rows=136, cols=136, workspace=0),
-    dict(rows=136, cols=136, workspace_bytes=1000),
+    dict(rows=136, cols=136, workspace=0), dict(rows=136, cols=136, workspace_bytes=1000),
     dict(out_row_stride=7), dict(in_dtype=2), dict(rows=-1), dict(batch=-1), dict(in_batch_stride=-1),
     dict(batch=2, out_batch_stride=63), dict(cfg=B.zero_ns_config(0, 1.5, -0.5, 0.0, 0.0)),
     dict(cfg=B.zero_ns_config(5, float("nan"), 0.0, 0.0, 0.0)), dict(cfg=B.zero_ns_config(5, 1.5, -0.5, 0.0, -1.0)),
@@ -189,7 +188,7 @@ def test_refusals(over):
 
 def test_misaligned_pointers():
     x = torch.zeros(4096, device="cuda").data_ptr()
-    for over in (dict(src=x + 2), dict(out=x + 1), dict(workspace=x + 16)):
+    for over in (dict(src=x + 2), dict(out=x + 1), dict(rows=136, cols=136, workspace=x + 16)):
         with pytest.raises(B.ZeroError) as e:
             call(**over)
         assert e.value.status == B.ZERO_EINVAL

@@ -115,29 +115,23 @@ unsigned int muon_debug_failures();
 // shapes together.
 constexpr int kThin = 128;
 constexpr int kMaxSteps = 32;
-constexpr int kThinChain = 2;  // steps per Gram matrix
-// Elements of the fp32 workspace of one launch (more only for a single matrix
-// that is larger).
-constexpr long long kThinWork = 1LL << 22;
+// Bytes of the workspace that one launch may take (more only for a single
+// matrix that needs more).
+constexpr long long kThinWork = 1LL << 26;
 // Factors of a step: the coefficients, and the powers of two between the
-// stored (fp16) X, A, P, Q and A P.
+// stored (fp16) X, A and P.
 struct ThinStep {
   float x;          // X as stored
   float gram;       // A from X X^T
   float square, gram_term, identity;  // P from A A, from A and on its diagonal
-  float chain;      // Q from P Q
-  float inner;      // A P
-  float next;       // the next A from P (A P)
-  float result;     // Q X to its value
+  float result;     // P X to the next X as stored (the last step: to its value)
 };
 struct ThinArgs {
   int steps;
   float eps;
   ThinStep step_factors[kMaxSteps];
   int rows[kMaxMats], cols[kMaxMats];  // a stack uses entry 0
-  // fp32, as many elements as the matrix (a multiple of 8 apart): the Muon
-  // step's update and the iterate between two Gram matrices
-  float* work;
+  char* work;                          // thin_work() bytes per matrix
   long long work_mat_stride;           // of a stack
   // A stack: input and bf16 output.
   MatSource src;
@@ -160,6 +154,8 @@ struct ThinArgs {
 };
 // CTAs (a cluster) per matrix of this shape.
 int thin_ctas(long long rows, long long cols);
+// Bytes of workspace that a matrix of this shape needs (a multiple of 256).
+long long thin_work(long long rows, long long cols, bool muon);
 // Fills the scales and coefficients of `cfg`.
 void thin_scales(const zero_ns_config& cfg, ThinArgs* a);
 cudaError_t launch_ns_thin(const ThinArgs& a, bool muon, int ctas, long long mats, cudaStream_t stream, int* launches);

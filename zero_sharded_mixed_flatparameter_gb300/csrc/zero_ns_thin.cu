@@ -1,23 +1,21 @@
 // Newton-Schulz orthogonalisation of thin matrices, smaller side m <= kThin:
 // the whole chain in one launch, a cluster of CTAs per matrix.
 //
-// Every step's factor is a polynomial of the same Gram matrix, so a few steps
-// can run on m x m matrices alone and touch X twice:
-//   A = X X^T;  per step P = a I + b A + c A A,  Q <- P Q,  A <- P (A P)
-//   X <- Q X
-// The rounding of A then grows by up to a^2 (11.9) a step instead of a: the
-// products keep 22 bits (every operand is an fp16 pair hi + lo, a product is
-// lo hi + hi lo + hi hi with fp32 sums that the tensor cores truncate: 1e-6)
-// and two steps share a Gram matrix.  A rank-1 128 x 128 matrix is then 1.2e-5
-// off after two steps, 1.4e-4 after three and 5.5e-2 after all five from one
-// Gram matrix; restarted every two, 5e-4 after five.
+//   A = X X^T,  P = a I + b A + c A A,  X <- P X      (steps times)
 //
-// What bounds it is latency: each product of 128 takes under a microsecond,
-// and the next one waits for it.  Hence one launch, operands that stay in
-// shared memory (A, P, Q: 3 x 64 KB), and the columns of X split over up to 8
-// CTAs whose partial Gram matrices are joined in distributed shared memory;
-// every CTA then solves the chain by itself rather than wait for another.
-// In the Muon step the momentum pass is the first thing the kernel does.
+// What bounds it is latency: a product of 128 takes under half a microsecond,
+// and the next one waits for it.  Hence one launch; A, P and X stay in shared
+// memory, the columns of X split over up to 8 CTAs in slices of 128 whose
+// partial Gram matrices are joined in distributed shared memory; every CTA
+// forms P by itself rather than wait for another.  More than one slice per CTA
+// (n > 1024) pass through global memory as ready images, once per step: a
+// slice's new columns go straight into the next step's Gram matrix.  In the
+// Muon step the momentum pass is the first thing the kernel does.
+//
+// With tiny m the roundings of a step do not average out, and latency leaves
+// room, so products keep 22 bits here: every operand is an fp16 pair (hi + lo)
+// and a product is hi lo + lo hi + hi hi with fp32 sums (which the tensor cores
+// truncate: 1e-6): 1e-5 off after five steps where 11 bits leave 5e-3.
 
 #include "zero_device.cuh"
 #include "zero_muon_internal.h"
@@ -36,9 +34,8 @@ constexpr uint32_t kTmemColumns = 256;
 
 struct Shared {
   uint64_t bar[3];
-  double sum;  // of this CTA's columns, read by the cluster
+  float sum;  // of this CTA's columns, read by the cluster
   float warp_sum[kWarps];
-  float norm_scale;
   uint32_t tmem;
   int gave_up;
 };
@@ -75,20 +72,29 @@ __device__ __forceinline__ void load_pair(uint32_t buffer, int r, int chunk, flo
 }
 
 // acc (128 rows, `n` columns) = sum over k < depth of the pair product of two
-// buffers, A K-major and B K-major or MN-major.  One thread.
+// buffers, A K-major and B K-major or MN-major; n and depth multiples of 16.
+// One thread: descriptors move by constants, as what this thread does between
+// two MMAs is what a short product takes.
 __device__ __forceinline__ void issue_pair(uint32_t acc, uint32_t a, uint32_t b, bool b_k_major, int n, int depth,
                                            bool accumulate) {
   const uint32_t idesc = (1u << 4) | (b_k_major ? 0u : 1u << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+  const uint64_t da = smem_desc(a, true, 0), db = smem_desc(b, b_k_major, kBlockBytes);
+  const uint32_t b_step = b_k_major ? 2 : 128, b_block = b_k_major ? kBlockBytes >> 4 : 512;  // units of 16 bytes
   uint32_t on = accumulate ? 1 : 0;
-#pragma unroll 1
+#pragma unroll
   for (int part = 0; part < 3; ++part) {  // hi lo, lo hi, hi hi: the small terms first, as sums are truncated
-    const uint32_t pa = a + (part == 1 ? kHalfBytes : 0), pb = b + (part == 0 ? kHalfBytes : 0);
-#pragma unroll 1
-    for (int k = 0; k < depth; k += 16) {
-      const uint32_t ka = pa + (k / 64) * kBlockBytes + (k % 64) * 2;
-      const uint32_t kb = b_k_major ? pb + (k / 64) * kBlockBytes + (k % 64) * 2 : pb + k * 128;
-      mma<1>(acc, smem_desc(ka, true, 0), smem_desc(kb, b_k_major, kBlockBytes), idesc, on);
-      on = 1;
+    uint64_t pa = da + (part == 1 ? kHalfBytes >> 4 : 0), pb = db + (part == 0 ? kHalfBytes >> 4 : 0);
+#pragma unroll
+    for (int block = 0; block < 2; ++block) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (block * 64 + k * 16 < depth) {
+          mma<1>(acc, pa + 2 * k, pb + b_step * k, idesc, on);
+          on = 1;
+        }
+      }
+      pa += kBlockBytes >> 4;
+      pb += b_block;
     }
   }
 }
@@ -101,11 +107,6 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ float ld_cluster(uint32_t at) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-  return v;
-}
-__device__ __forceinline__ double ld_cluster_f64(uint32_t at) {
-  double v;
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(at) : "memory");
   return v;
 }
 __device__ __forceinline__ void st_cluster(uint32_t at, uint32_t v) {
@@ -152,141 +153,149 @@ __device__ __forceinline__ void load_run(const void* base, const Run& r, bool ve
   else load8<kFp32, false>(base, r.at, r.count, x);
 }
 
-// A slice of X0 as pairs in `buffer`; what does not exist is zero.
-template <bool kFp32>
-__device__ __forceinline__ void load_slice(const Matrix& x, const void* base, bool vec, int j0, float scale,
-                                           uint32_t buffer) {
-#pragma unroll 2
-  for (int i = threadIdx.x; i < slice_runs(x); i += kThreads) {
-    const Run r = slice_run(x, j0, i);
-    float v[8];
-    load_run<kFp32>(base, r, vec, v);
+// A run of the slice from column j0, scaled, as pairs in `buffer`.
+__device__ __forceinline__ void put_run(const Matrix& x, const Run& r, int j0, float scale, float* v, uint32_t buffer) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] *= scale;
-    if (!x.tall) {
-      store_pair(buffer, r.row, (r.col - j0) / 8, v);
-    } else {
-      uint32_t hi[4], lo[4];
-      split8(v, hi, lo);
-      const int c = r.col - j0;
+  for (int k = 0; k < 8; ++k) v[k] *= scale;
+  if (!x.tall) {
+    store_pair(buffer, r.row, (r.col - j0) / 8, v);
+  } else {
+    uint32_t hi[4], lo[4];
+    split8(v, hi, lo);
+    const int c = r.col - j0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t at = chunk_at(buffer, r.row + k, c / 8) + c % 8 * 2;
-        sts2(at, static_cast<uint16_t>(hi[k / 2] >> (16 * (k % 2))));
-        sts2(at + kHalfBytes, static_cast<uint16_t>(lo[k / 2] >> (16 * (k % 2))));
-      }
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t at = chunk_at(buffer, r.row + k, c / 8) + c % 8 * 2;
+      sts2(at, static_cast<uint16_t>(hi[k / 2] >> (16 * (k % 2))));
+      sts2(at + kHalfBytes, static_cast<uint16_t>(lo[k / 2] >> (16 * (k % 2))));
     }
   }
 }
 
-// The momentum pass over a slice: returns the thread's sum of squares.
+// The momentum pass of a run: y becomes the update (the squares' sum is the caller's).
 template <bool kFp32>
-__device__ __forceinline__ float momentum_slice(const ThinArgs& a, int mat, const Matrix& x, bool vec, int j0,
-                                                float* update, unsigned* nf) {
-  const float clip = a.clip ? *a.clip : 1.0f;
+__device__ __forceinline__ void momentum_run(const ThinArgs& a, int mat, const Run& r, bool vec, float clip, float* y,
+                                             unsigned* nf) {
   const long long base = a.offset[mat];
-  float sq = 0.0f;
-  for (int i = threadIdx.x; i < slice_runs(x); i += kThreads) {
-    const Run r = slice_run(x, j0, i);
-    if (r.count == 0 || !ZFS_CHECK(base >= 0 && base + r.at + r.count <= a.total_padded)) continue;
-    float g[8], y[8], m[8];
-    load_run<kFp32>(a.g[mat][0], r, vec, g);
+  float g[8], m[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) y[k] = 0.0f;
+  if (r.count == 0 || !ZFS_CHECK(base >= 0 && base + r.at + r.count <= a.total_padded)) return;
+  load_run<true>(a.mom + base, r, vec, m);
+  load_run<kFp32>(a.g[mat][0], r, vec, g);
 #pragma unroll 4
-    for (int q = 1; q < a.n_ranks; ++q) {
-      load_run<kFp32>(a.g[mat][q], r, vec, y);
+  for (int q = 1; q < a.n_ranks; ++q) {
+    load_run<kFp32>(a.g[mat][q], r, vec, y);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) g[k] = __fadd_rn(g[k], y[k]);
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) g[k] = __fmul_rn(g[k], a.inv_n);
-    *nf += tally_nonfinite<8>(g);
-    load_run<true>(a.mom + base, r, vec, m);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (a.clip) g[k] = __fmul_rn(g[k], clip);
-      m[k] = __fadd_rn(__fmul_rn(a.mu, m[k]), g[k]);
-      y[k] = a.nesterov ? __fadd_rn(g[k], __fmul_rn(a.mu, m[k])) : m[k];
-      sq += y[k] * y[k];
-    }
-    float* mom = a.mom + base + r.at;
-    if (vec && r.count == 8) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        reinterpret_cast<float4*>(mom)[q] = make_float4(m[4 * q], m[4 * q + 1], m[4 * q + 2], m[4 * q + 3]);
-        reinterpret_cast<float4*>(update + r.at)[q] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (k < r.count) {
-          mom[k] = m[k];
-          update[r.at + k] = y[k];
-        }
-      }
-    }
+    for (int k = 0; k < 8; ++k) g[k] = __fadd_rn(g[k], y[k]);
   }
-  return sq;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) g[k] = __fmul_rn(g[k], a.inv_n);
+  *nf += tally_nonfinite<8>(g);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (a.clip) g[k] = __fmul_rn(g[k], clip);
+    m[k] = __fadd_rn(__fmul_rn(a.mu, m[k]), g[k]);
+    y[k] = a.nesterov ? __fadd_rn(g[k], __fmul_rn(a.mu, m[k])) : m[k];
+  }
+  float* mom = a.mom + base + r.at;
+  if (vec && r.count == 8) {
+    reinterpret_cast<float4*>(mom)[0] = make_float4(m[0], m[1], m[2], m[3]);
+    reinterpret_cast<float4*>(mom)[1] = make_float4(m[4], m[5], m[6], m[7]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (k < r.count) mom[k] = m[k];
+  }
 }
 
 // ---- the output --------------------------------------------------------------
-// Eight consecutive X columns j .. j+7 of row i, finished values.
+// One finished value at `at` of the matrix's storage.
 template <bool kMuon>
-__device__ __forceinline__ void store_result(const ThinArgs& a, int mat, const Matrix& x, bool vec, int i, int j,
-                                             float* y) {
-  if (i >= x.m || j >= x.n) return;
-  const int count = min(8, x.n - j);
-  const long long ld = kMuon ? x.ld : a.out_row_stride;
-  const long long at = x.tall ? j * ld + i : i * ld + j, next = x.tall ? ld : 1;
+__device__ __forceinline__ void put_value(const ThinArgs& a, int mat, long long at, float y, float old) {
   if constexpr (kMuon) {
-    const long long base = a.offset[mat] + at;
-    if (!ZFS_CHECK(base >= 0 && base + (count - 1) * next < a.total_padded)) return;
-    float* w = a.master + base;
-    uint16_t* p = a.p16 + base;
-    const float step = a.step[mat];
-    if (vec && !x.tall && count == 8) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const float4 old = reinterpret_cast<const float4*>(w)[q];
-        const float o[4] = {old.x, old.y, old.z, old.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          y[4 * q + k] = __fadd_rn(__fmul_rn(o[k], a.decay), __fmul_rn(-step, y[4 * q + k]));
-        reinterpret_cast<float4*>(w)[q] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
-      }
-      *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                                pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-    } else {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (k < count) {
-          const float z = __fadd_rn(__fmul_rn(w[k * next], a.decay), __fmul_rn(-step, y[k]));
-          w[k * next] = z;
-          p[k * next] = to_bf16_bits(z);
-        }
+    const float z = __fadd_rn(__fmul_rn(old, a.decay), __fmul_rn(-a.step[mat], y));
+    a.master[a.offset[mat] + at] = z;
+    a.p16[a.offset[mat] + at] = to_bf16_bits(z);
+  } else {
+    a.out[mat * a.out_mat_stride + at] = to_bf16_bits(y);
+  }
+}
+template <bool kMuon>
+__device__ __forceinline__ float old_value(const ThinArgs& a, int mat, long long at, bool* ok) {
+  if constexpr (kMuon) {
+    *ok = ZFS_CHECK(a.offset[mat] + at >= 0 && a.offset[mat] + at < a.total_padded);
+    return *ok ? a.master[a.offset[mat] + at] : 0.0f;
+  } else {
+    *ok = true;
+    return 0.0f;
+  }
+}
+
+// A slice of a wide matrix from `rows` (fp32, 128 x 128, 16-byte pieces
+// swizzled by row): a row per warp, so that accesses are contiguous.
+template <bool kMuon>
+__device__ __forceinline__ void write_rows(const ThinArgs& a, int mat, const Matrix& x, bool vec, uint32_t rows, int j0,
+                                           int warp, int lane) {
+  const long long ld = kMuon ? x.ld : a.out_row_stride;
+  const int width = min(kSlice, x.n - j0);
+  if ((kMuon ? vec : a.vec_out != 0) && width == kSlice) {
+#pragma unroll 2
+    for (int i = warp; i < x.m; i += kWarps) {
+      const long long at = i * ld + j0 + 4 * lane;
+      const uint4 v = lds16(rows + i * 512 + ((lane ^ (i & 7)) << 4));
+      float4 y = make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z), __uint_as_float(v.w));
+      if constexpr (kMuon) {
+        const long long to = a.offset[mat] + at;
+        if (!ZFS_CHECK(to >= 0 && to + 4 <= a.total_padded)) continue;
+        const float4 old = *reinterpret_cast<const float4*>(a.master + to);
+        const float step = -a.step[mat];
+        y.x = __fadd_rn(__fmul_rn(old.x, a.decay), __fmul_rn(step, y.x));
+        y.y = __fadd_rn(__fmul_rn(old.y, a.decay), __fmul_rn(step, y.y));
+        y.z = __fadd_rn(__fmul_rn(old.z, a.decay), __fmul_rn(step, y.z));
+        y.w = __fadd_rn(__fmul_rn(old.w, a.decay), __fmul_rn(step, y.w));
+        *reinterpret_cast<float4*>(a.master + to) = y;
+        *reinterpret_cast<uint2*>(a.p16 + to) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+      } else {
+        *reinterpret_cast<uint2*>(a.out + mat * a.out_mat_stride + at) =
+            make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
       }
     }
   } else {
-    uint16_t* d = a.out + mat * a.out_mat_stride + at;
-    if (a.vec_out && !x.tall && count == 8) {
-      *reinterpret_cast<uint4*>(d) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                                pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
-    } else {
+    for (int i = warp; i < x.m; i += kWarps) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (k < count) d[k * next] = to_bf16_bits(y[k]);
+      for (int q = 0; q < kSlice / 32; ++q) {
+        const int c = lane + 32 * q;
+        if (c >= width) continue;
+        float y;
+        asm volatile("ld.shared.f32 %0, [%1];"
+                     : "=f"(y)
+                     : "r"(rows + i * 512 + (((c / 4) ^ (i & 7)) << 4) + c % 4 * 4)
+                     : "memory");
+        bool ok;
+        const float old = old_value<kMuon>(a, mat, i * ld + j0 + c, &ok);
+        if (ok) put_value<kMuon>(a, mat, i * ld + j0 + c, y, old);
+      }
     }
   }
 }
 
-// The same of an iterate between two Gram matrices, to the fp32 buffer.
-__device__ __forceinline__ void store_iterate(const Matrix& x, float* to, int i, int j, const float* y) {
-  if (i >= x.m || j >= x.n) return;
-  const int count = min(8, x.n - j);
-  float* d = to + (x.tall ? j * x.ld + i : i * x.ld + j);
-  const long long next = x.tall ? x.ld : 1;
+// Sixteen columns from j of X row i of a tall matrix: lanes are consecutive
+// elements of its rows.
+template <bool kMuon>
+__device__ __forceinline__ void write_columns(const ThinArgs& a, int mat, const Matrix& x, int i, int j, const float* y) {
+  if (i >= x.m) return;
+  const long long ld = kMuon ? x.ld : a.out_row_stride;
+  float old[16];
+  bool ok[16];
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    if (k < count) d[k * next] = y[k];
+  for (int k = 0; k < 16; ++k) {
+    ok[k] = false;
+    if (j + k < x.n) old[k] = old_value<kMuon>(a, mat, (j + k) * ld + i, &ok[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    if (ok[k]) put_value<kMuon>(a, mat, (j + k) * ld + i, y[k], old[k]);
 }
 
 // ---- the kernel --------------------------------------------------------------
@@ -302,7 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const uint32_t rank = kCtas > 1 ? cluster_rank() : 0;
   const int mat = blockIdx.x / kCtas;
-  const uint32_t b0 = (smem_u32(smem_raw) + 1023) & ~1023u, b1 = b0 + kPairBytes, b2 = b1 + kPairBytes;
+  // A, then P, in square; slices of X in turn in the other two
+  const uint32_t square = (smem_u32(smem_raw) + 1023) & ~1023u, slices = square + kPairBytes;
   Matrix x;
   {
     const int at = kMuon ? mat : 0, rows = a.rows[at], cols = a.cols[at];
@@ -312,13 +322,15 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
     x.mk = (x.m + 15) / 16 * 16;
     x.ld = kMuon ? cols : a.src.row_stride;
   }
+  const int mk = x.mk, all = (x.n + kSlice - 1) / kSlice;
+  const int mine = (all - static_cast<int>(rank) + kCtas - 1) / kCtas;  // slices rank, rank + kCtas, ...
+  const bool many = all > kCtas;  // some CTA has more than one: the images pass through global memory
   const bool vec = kMuon ? (a.vec[mat / 32] >> (mat % 32)) & 1 : a.src.vec_ok != 0;
-  // the Muon step's update, and the iterate between Gram matrices, row after row
-  float* work = a.work + (kMuon ? a.work_offset[mat] : mat * a.work_mat_stride);
-  Matrix xw = x;
-  xw.ld = x.tall ? x.m : x.n;
-  const bool vec_work = xw.ld % 8 == 0;
-  const void* source = kMuon ? static_cast<const void*>(work)
+  // of this matrix: the Muon step's update (fp32, only with many slices), then the images
+  char* work = a.work + (kMuon ? a.work_offset[mat] : mat * a.work_mat_stride);
+  float* update = reinterpret_cast<float*>(work);
+  char* images = work + (kMuon ? (static_cast<long long>(x.m) * x.n * 4 + 255) / 256 * 256 : 0);
+  const void* source = kMuon ? static_cast<const void*>(update)
                              : static_cast<const char*>(a.src.data) + mat * a.src.mat_stride * (kFp32 ? 4 : 2);
   if (tid == 0) {
     sh.gave_up = 0;
@@ -329,279 +341,291 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = sh.tmem;
+  const uint32_t tmem = sh.tmem, gram = tmem, other = tmem + 128;
   bool alive = true;
+  // Barriers: products that a buffer of slices (0, 1) waits for, all others (2).
   uint32_t phase[3] = {0, 0, 0};
-  // Waits for the products committed to barrier `i`; all threads.
-  auto wait = [&](int i) {
+  bool pending[2] = {false, false};
+  auto wait = [&](int i) {  // all threads
     const bool ok = alive && wait_phase(smem_u32(&sh.bar[i]), phase[i], &sh.gave_up);
     phase[i] ^= 1;
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     return ok;
   };
+  auto drained = [&](int i) {  // the Gram products of slice buffer i
+    const bool ok = !pending[i] || wait(i);
+    pending[i] = false;
+    return ok;
+  };
   // Makes shared-memory operands and drained accumulators ready for products.
   auto ready = [&](bool ok) {
-    asm volatile("fence.proxy.async;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     alive = __syncthreads_and(ok ? 1 : 0) != 0;
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   };
+  auto first_column = [&](int s) { return (static_cast<int>(rank) + s * kCtas) * kSlice; };
+  auto depth_of = [&](int s) { return (min(kSlice, x.n - first_column(s)) + 15) / 16 * 16; };
+  auto image = [&](int s) { return images + (static_cast<long long>(rank) + s * kCtas) * (512LL * mk); };
+  // A slice's image between shared and global memory: mk rows of the four blocks.
+  auto store_image = [&](int s, uint32_t from) {  // one thread
+    for (int b = 0; b < 4; ++b)
+      asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(image(s) + b * 128LL * mk),
+                   "r"(from + b * kBlockBytes), "r"(128 * mk)
+                   : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  };
+  auto load_image = [&](int s, uint32_t to) {  // one thread
+    const uint32_t bar = smem_u32(&sh.bar[2]);
+    mbar_expect_tx(bar, 512 * mk);
+    for (int b = 0; b < 4; ++b)
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                       to + b * kBlockBytes),
+                   "l"(image(s) + b * 128LL * mk), "r"(128 * mk), "r"(bar)
+                   : "memory");
+  };
+  // the share of a thread in an epilogue: row `row`, columns from `begin`
+  const int row = (warp % 4) * 32 + lane, quarter = warp / 4;
+  const bool in_rows = (warp % 4) * 32 < mk;  // the same for the whole warp
+  const uint32_t lanes = ((warp % 4) * 32) << 16;
+  const int share = (mk / 16 + 3) / 4 * 16;   // columns of a quarter of an m x m matrix
+  auto add_to_gram = [&](int s, uint32_t buffer) {  // one thread
+    issue_pair(gram, buffer, buffer, true, mk, depth_of(s), s > 0);
+    mma_commit<1>(smem_u32(&sh.bar[s & 1]));
+  };
 
-  // ---- norm (and momentum) over this CTA's slices ------------------------------
+  // ---- norm (and momentum) ------------------------------------------------------
+  // A single slice stays in registers until the norm is known.
+  const float clip = kMuon && a.clip ? *a.clip : 1.0f;
+  const int runs = slice_runs(x);
+  constexpr int kHeld = kThin * (kSlice / 8) / kThreads;
+  float held[kHeld][8];
   float sq = 0.0f;
   unsigned nf = 0;
-  for (int j0 = rank * kSlice; j0 < x.n; j0 += kCtas * kSlice) {
-    if constexpr (kMuon) {
-      sq += a.grad_fp32 ? momentum_slice<true>(a, mat, x, vec, j0, work, &nf)
-                        : momentum_slice<false>(a, mat, x, vec, j0, work, &nf);
-    } else {
-      for (int i = tid; i < slice_runs(x); i += kThreads) {
-        float v[8];
-        load_run<kFp32>(source, slice_run(x, j0, i), vec, v);
+  for (int s = 0; s < mine; ++s) {
+    const int j0 = first_column(s);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sq += v[k] * v[k];
+    for (int q = 0; q < kHeld; ++q) {
+      const int i = tid + q * kThreads;
+      if (i < runs) {
+        const Run r = slice_run(x, j0, i);
+        if constexpr (kMuon) {
+          if (a.grad_fp32) momentum_run<true>(a, mat, r, vec, clip, held[q], &nf);
+          else momentum_run<false>(a, mat, r, vec, clip, held[q], &nf);
+          if (many) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              if (k < r.count) update[r.at + k] = held[q][k];
+          }
+        } else {
+          load_run<kFp32>(source, r, vec, held[q]);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sq += held[q][k] * held[q][k];
       }
     }
   }
   if constexpr (kMuon) flush_nonfinite(a.nonfinite, nf);
-  // fp32 over a warp, fp64 above, by one thread (the GPU has few fp64 units)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
   if (lane == 0) sh.warp_sum[warp] = sq;
   __syncthreads();
-  if (tid == 0) {
-    double t = 0.0;
-    for (int w = 0; w < kWarps; ++w) t += sh.warp_sum[w];
-    sh.sum = t;
+  sq = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) sq += sh.warp_sum[w];
+  if constexpr (kCtas > 1) {
+    if (tid == 0) sh.sum = sq;
+    cluster_sync();
+    sq = 0.0f;
+    for (int r = 0; r < kCtas; ++r) sq += ld_cluster(map_rank(smem_u32(&sh.sum), r));
   }
-  if constexpr (kCtas > 1) cluster_sync();
-  if (tid == 0) {
-    double t = 0.0;
-    if constexpr (kCtas > 1) {
-      for (int r = 0; r < kCtas; ++r) t += ld_cluster_f64(map_rank(smem_u32(&sh.sum), r));
-    } else {
-      t = sh.sum;
-    }
-    sh.norm_scale = static_cast<float>(1.0 / (sqrt(t) + static_cast<double>(a.eps)));
-  }
-  __syncthreads();
-  const float norm_scale = sh.norm_scale;
-  const int mk = x.mk;
-  // the epilogue's share of a thread: row `row`, a quarter of the columns
-  const int row = (warp % 4) * 32 + lane, quarter = warp / 4;
-  const bool in_rows = (warp % 4) * 32 < mk;  // the same for the whole warp
-  const uint32_t tmem_row = tmem + (((warp % 4) * 32) << 16);
-  auto product = [&](uint32_t acc, uint32_t p, uint32_t q) { issue_pair(acc, p, q, true, mk, mk, false); };
-  auto go = [&](int i) { mma_commit<1>(smem_u32(&sh.bar[i])); };
+  const float scale = 1.0f / (sqrtf(sq) + a.eps) * a.step_factors[0].x;
 
-  for (int begin = 0; begin < a.steps; begin += kThinChain) {
-  const int end = min(begin + kThinChain, a.steps);
-  const ThinStep& f0 = a.step_factors[begin];
-  auto fetch = [&](int j0, uint32_t buffer) {
-    if (begin == 0) load_slice<kFp32>(x, source, vec, j0, norm_scale * f0.x, buffer);
-    else load_slice<true>(xw, work, vec_work, j0, f0.x, buffer);
-  };
-
-  // ---- Gram matrix: slices of X through the two buffers -------------------------
-  int used = 0;
+  // ---- X0 and its Gram matrix ---------------------------------------------------
   bool ok = alive;
-  for (int j0 = rank * kSlice; j0 < x.n; j0 += kCtas * kSlice, ++used) {
-    const int i = used & 1;
-    ok = alive;
-    if (used >= 2) ok = wait(i);
-    fetch(j0, i ? b1 : b0);
+  for (int s = 0; s < mine; ++s) {
+    const int j0 = first_column(s), i = s & 1;
+    const uint32_t buffer = slices + i * kPairBytes;
+    if (many) {
+      ok = drained(i);
+      if (tid == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncthreads();
+    }
+#pragma unroll
+    for (int q = 0; q < kHeld; ++q) {
+      const int e = tid + q * kThreads;
+      if (e < runs) {
+        const Run r = slice_run(x, j0, e);
+        if (many) {
+          if constexpr (kMuon) load_run<true>(update, r, false, held[q]);
+          else load_run<kFp32>(source, r, vec, held[q]);
+        }
+        put_run(x, r, j0, scale, held[q], buffer);
+      }
+    }
     ready(ok);
     if (tid == 0 && alive) {
-      issue_pair(tmem, i ? b1 : b0, i ? b1 : b0, true, mk, kSlice, used > 0);
-      mma_commit<1>(smem_u32(&sh.bar[i]));
+      if (many) store_image(s, buffer);
+      add_to_gram(s, buffer);
     }
+    pending[i] = true;
   }
-  ok = alive;
-  if (used >= 2) ok = wait(used & 1) && ok;
-  if (used >= 1) ok = wait((used + 1) & 1) && ok;
-  const float from_x = f0.gram;
-  if constexpr (kCtas == 1) {
-    // A straight from the accumulator
-    if (ok && in_rows) {
-      for (int c = quarter * 32; c < min(mk, quarter * 32 + 32); c += 16) {
-        float y[16];
-        __syncwarp();
-        tmem_load16(tmem_row + c, y);
-#pragma unroll
-        for (int k = 0; k < 16; ++k) y[k] *= from_x;
-        store_pair(b0, row, c / 8, y);
-        store_pair(b0, row, c / 8 + 1, y + 8);
-      }
-    }
-  } else {
-    // Partial sums to this CTA's b2 (column after column: A is symmetric, and
-    // lanes are rows); each CTA joins mk / kCtas columns in rank order and
-    // gives them to all.
-    if (ok && in_rows) {
-      for (int c = quarter * 32; c < min(mk, quarter * 32 + 32); c += 16) {
-        float y[16];
-        __syncwarp();
-        tmem_load16(tmem_row + c, y);
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(b2 + ((c + k) * 128 + row) * 4),
-                       "f"(used > 0 ? y[k] * from_x : 0.0f)
-                       : "memory");
-      }
-    }
-    cluster_sync();
-    const int columns = mk / kCtas, first = rank * columns;
-    for (int e = tid; e < columns * (mk / 2); e += kThreads) {
-      const int c = first + e / (mk / 2), r = e % (mk / 2) * 2;
-      float u = 0.0f, v = 0.0f;
-#pragma unroll
-      for (int q = 0; q < kCtas; ++q) {
-        const uint32_t at = map_rank(b2 + (c * 128 + r) * 4, q);
-        u += ld_cluster(at);
-        v += ld_cluster(at + 4);
-      }
-      const uint32_t hi = half2_bits(u, v);
-      const float2 h = half2_values(hi);
-      const uint32_t lo = half2_bits(u - h.x, v - h.y);
-      const uint32_t at = chunk_at(b0, c, r / 8) + r % 8 * 2;  // row c of A, columns r and r + 1
-#pragma unroll
-      for (int q = 0; q < kCtas; ++q) {
-        st_cluster(map_rank(at, q), hi);
-        st_cluster(map_rank(at + kHalfBytes, q), lo);
-      }
-    }
-    asm volatile("fence.proxy.async;" ::: "memory");
-    cluster_sync();
-  }
-  ready(ok);
 
-  // ---- the chain on m x m matrices ----------------------------------------------
-  // A in b0, P in b1, Q in b2; every matrix commutes with every other.
-  for (int k = begin; k < end; ++k) {
-    const bool first = k == begin, last = k + 1 == end;
+  for (int k = 0; k < a.steps; ++k) {
     const ThinStep& f = a.step_factors[k];
-    if (tid == 0 && alive) {
-      product(tmem, b0, b0);  // A A
-      go(0);
+    const bool last = k + 1 == a.steps;
+    ok = drained(0);
+    ok = drained(1) && ok;
+    if (many && tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+
+    // ---- A, joined over the cluster -----------------------------------------------
+    if constexpr (kCtas == 1) {
+      if (ok && in_rows) {
+        for (int c = quarter * share; c < min(mk, (quarter + 1) * share); c += 16) {
+          float y[16];
+          __syncwarp();
+          tmem_load16(gram + lanes + c, y);
+#pragma unroll
+          for (int q = 0; q < 16; ++q) y[q] *= f.gram;
+          store_pair(square, row, c / 8, y);
+          store_pair(square, row, c / 8 + 1, y + 8);
+        }
+      }
+    } else {
+      // Partial sums to this CTA's second slice buffer (column after column: A
+      // is symmetric, and lanes are rows); each CTA joins mk / kCtas columns
+      // in rank order and gives them to all.
+      const uint32_t partial = slices + kPairBytes;
+      __syncthreads();  // (with many slices: the last image has been stored)
+      if (ok && in_rows) {
+        for (int c = quarter * share; c < min(mk, (quarter + 1) * share); c += 16) {
+          float y[16];
+          __syncwarp();
+          tmem_load16(gram + lanes + c, y);
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(partial + ((c + q) * 128 + row) * 4),
+                         "f"(mine > 0 ? y[q] * f.gram : 0.0f)
+                         : "memory");
+        }
+      }
+      cluster_sync();
+      const int columns = mk / kCtas, from = rank * columns;
+      for (int e = tid; e < columns * (mk / 2); e += kThreads) {
+        const int c = from + e / (mk / 2), r = e % (mk / 2) * 2;
+        float u = 0.0f, v = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kCtas; ++q) {
+          const uint32_t at = map_rank(partial + (c * 128 + r) * 4, q);
+          u += ld_cluster(at);
+          v += ld_cluster(at + 4);
+        }
+        const uint32_t hi = half2_bits(u, v);
+        const float2 h = half2_values(hi);
+        const uint32_t lo = half2_bits(u - h.x, v - h.y);
+        const uint32_t at = chunk_at(square, c, r / 8) + r % 8 * 2;  // row c of A, columns r and r + 1
+#pragma unroll
+        for (int q = 0; q < kCtas; ++q) {
+          st_cluster(map_rank(at, q), hi);
+          st_cluster(map_rank(at + kHalfBytes, q), lo);
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
+      cluster_sync();
     }
-    ok = wait(0);
+    ready(ok);
+
+    // ---- P over A -----------------------------------------------------------------
+    if (tid == 0 && alive) {
+      issue_pair(other, square, square, true, mk, mk, false);
+      mma_commit<1>(smem_u32(&sh.bar[2]));
+    }
+    ok = wait(2);
     if (ok && in_rows) {
-      const float fc = f.square, fb = f.gram_term, fa = f.identity;
-      for (int c = quarter * 32; c < min(mk, quarter * 32 + 32); c += 16) {
+      for (int c = quarter * share; c < min(mk, (quarter + 1) * share); c += 16) {
         float y[16];
         __syncwarp();
-        tmem_load16(tmem_row + c, y);
+        tmem_load16(other + lanes + c, y);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          float old[8], z[8];
-          load_pair(b0, row, c / 8 + h, old);
+          float old[8];
+          load_pair(square, row, c / 8 + h, old);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             const int col = c + 8 * h + q;
-            z[q] = fmaf(fc, y[8 * h + q], fb * old[q]) + (col == row && row < x.m ? fa : 0.0f);
+            y[8 * h + q] = fmaf(f.square, y[8 * h + q], f.gram_term * old[q]) +
+                           (col == row && row < x.m ? f.identity : 0.0f);
           }
-          store_pair(b1, row, c / 8 + h, z);
-          if (first) store_pair(b2, row, c / 8 + h, z);
+          store_pair(square, row, c / 8 + h, y + 8 * h);
         }
       }
     }
     ready(ok);
-    if (first && last) break;
-    if (tid == 0 && alive) {
-      if (!first) product(tmem, b1, b2);       // P Q
-      if (!last) product(tmem + 128, b0, b1);   // A P
-      go(0);
-    }
-    ok = wait(0);
-    if (ok && in_rows) {
-      const float fq = f.chain, fw = f.inner;
-      for (int c = quarter * 32; c < min(mk, quarter * 32 + 32); c += 16) {
-        float y[16];
-        if (!first) {
-          __syncwarp();
-          tmem_load16(tmem_row + c, y);
-#pragma unroll
-          for (int q = 0; q < 16; ++q) y[q] *= fq;
-          store_pair(b2, row, c / 8, y);
-          store_pair(b2, row, c / 8 + 1, y + 8);
-        }
-        if (!last) {
-          __syncwarp();
-          tmem_load16(tmem_row + 128 + c, y);
-#pragma unroll
-          for (int q = 0; q < 16; ++q) y[q] *= fw;
-          store_pair(b0, row, c / 8, y);
-          store_pair(b0, row, c / 8 + 1, y + 8);
-        }
-      }
-    }
-    ready(ok);
-    if (last) break;
-    if (tid == 0 && alive) {
-      product(tmem, b1, b0);  // P (A P)
-      go(0);
-    }
-    ok = wait(0);
-    if (ok && in_rows) {
-      for (int c = quarter * 32; c < min(mk, quarter * 32 + 32); c += 16) {
-        float y[16];
-        __syncwarp();
-        tmem_load16(tmem_row + c, y);
-#pragma unroll
-        for (int q = 0; q < 16; ++q) y[q] *= f.next;
-        store_pair(b0, row, c / 8, y);
-        store_pair(b0, row, c / 8 + 1, y + 8);
-      }
-    }
-    ready(ok);
-  }
 
-  // ---- Q X, slice after slice, the epilogue one slice behind the products -------
-  const float to_result = a.step_factors[end - 1].result;
-  used = 0;
-  for (int j0 = rank * kSlice;; j0 += kCtas * kSlice, ++used) {
-    const int i = used & 1;
-    const bool more = j0 < x.n;
-    if (!more && used == 0) break;
-    if (more) {
-      fetch(j0, i ? b1 : b0);
-      ready(alive);
-      if (tid == 0 && alive) {
-        issue_pair(tmem + i * 128, b2, i ? b1 : b0, false, kSlice, mk, false);
-        mma_commit<1>(smem_u32(&sh.bar[1 + i]));
+    // ---- P X, slice after slice ------------------------------------------------------
+    for (int s = 0; s < mine; ++s) {
+      const int j0 = first_column(s), i = s & 1, width = depth_of(s);
+      const uint32_t buffer = slices + i * kPairBytes, beside = slices + (1 - i) * kPairBytes;
+      if (many) {
+        ok = drained(i);
+        if (tid == 0) {
+          // the buffer's image has been stored; a load's bytes count on barrier 2
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          if (ok && alive) load_image(s, buffer);
+        }
+        ok = wait(2) && ok;
+        ready(ok);
       }
-    }
-    if (used > 0) {
-      const int before = j0 - kCtas * kSlice;
-      ok = wait(2 - i);
+      if (tid == 0 && alive) {
+        issue_pair(other, square, buffer, false, width, mk, false);
+        mma_commit<1>(smem_u32(&sh.bar[2]));
+      }
+      ok = wait(2);
+      if (last && !x.tall && many) {  // the buffer beside takes the finished rows
+        ok = drained(1 - i) && ok;
+        __syncthreads();
+      }
       if (ok && in_rows) {
-#pragma unroll 1
-        for (int c = quarter * 32; c < quarter * 32 + 32; c += 16) {
+        for (int c = quarter * 32; c < min(width, quarter * 32 + 32); c += 16) {
           float y[16];
           __syncwarp();
-          tmem_load16(tmem_row + (1 - i) * 128 + c, y);
+          tmem_load16(other + lanes + c, y);
 #pragma unroll
-          for (int q = 0; q < 16; ++q) y[q] *= to_result;
-          if (end == a.steps) {
-            store_result<kMuon>(a, mat, x, vec, row, before + c, y);
-            store_result<kMuon>(a, mat, x, vec, row, before + c + 8, y + 8);
+          for (int q = 0; q < 16; ++q) y[q] *= f.result;
+          if (!last) {
+            store_pair(buffer, row, c / 8, y);
+            store_pair(buffer, row, c / 8 + 1, y + 8);
+          } else if (x.tall) {
+            write_columns<kMuon>(a, mat, x, row, j0 + c, y);
           } else {
-            store_iterate(xw, work, row, before + c, y);
-            store_iterate(xw, work, row, before + c + 8, y + 8);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              sts16(beside + row * 512 + (((c / 4 + q) ^ (row & 7)) << 4),
+                    make_uint4(__float_as_uint(y[4 * q]), __float_as_uint(y[4 * q + 1]), __float_as_uint(y[4 * q + 2]),
+                               __float_as_uint(y[4 * q + 3])));
           }
         }
       }
       ready(ok);
+      if (!last) {
+        if (tid == 0 && alive) {
+          if (many) store_image(s, buffer);
+          add_to_gram(s, buffer);
+        }
+        pending[i] = true;
+      } else if (!x.tall) {
+        if (alive) write_rows<kMuon>(a, mat, x, vec, beside, j0, warp, lane);
+        if (many) ready(alive);
+      }
     }
-    if (!more) break;
-  }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   if (warp == 0) tmem_free<1>(tmem, kTmemColumns);
-  // no CTA leaves while another may read its shared memory (the last such read
-  // lies before the barrier behind the joined Gram matrix)
+  if (many && tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  // No CTA leaves while another may read its shared memory: the last such read
+  // lies before the barrier behind the last joined Gram matrix.
 }
 
 template <int kCtas, bool kMuon, bool kFp32>
@@ -641,6 +665,15 @@ cudaError_t launch_ctas(const ThinArgs& a, int ctas, long long mats, cudaStream_
 int thin_ctas(long long rows, long long cols) {
   const long long slices = ((rows > cols ? rows : cols) + kSlice - 1) / kSlice;
   return slices <= 1 ? 1 : slices <= 2 ? 2 : slices <= 4 ? 4 : 8;
+}
+
+// What a matrix needs of the workspace: nothing while every CTA has one slice;
+// else the images of the slices and, in a Muon step, the update.
+long long thin_work(long long rows, long long cols, bool muon) {
+  const long long m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
+  const long long all = (n + kSlice - 1) / kSlice, mk = (m + 15) / 16 * 16;
+  if (all <= thin_ctas(rows, cols)) return 0;
+  return all * 512 * mk + (muon ? (m * n * 4 + 255) / 256 * 256 : 0);
 }
 
 cudaError_t launch_ns_thin(const ThinArgs& a, bool muon, int ctas, long long mats, cudaStream_t stream, int* launches) {

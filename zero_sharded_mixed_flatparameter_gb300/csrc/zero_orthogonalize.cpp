@@ -134,8 +134,7 @@ NsPlan ns_plan(long long rows, long long cols, int mats, bool keep_update) {
 void thin_scales(const zero_ns_config& cfg, ThinArgs* a) {
   a->steps = cfg.steps;
   a->eps = cfg.eps;
-  double top = 1.0, chain = 1.0;  // spectral norms of X and of Q
-  int eq = 0, ex0 = 0;            // of the chain's last step, of its X
+  double top = 1.0;  // spectral norm of X
   for (int k = 0; k < cfg.steps; ++k) {
     ThinStep& f = a->step_factors[k];
     // P = a I + b A + c A A with its identity
@@ -143,30 +142,22 @@ void thin_scales(const zero_ns_config& cfg, ThinArgs* a) {
     double p = std::max(q(0.0), q(top * top));
     const double turn = cfg.c != 0.0f ? -cfg.b / (2.0 * cfg.c) : -1.0;
     if (turn > 0.0 && turn < top * top) p = std::max(p, q(turn));
-    const bool first = k % kThinChain == 0;
     const double next = largest_value(cfg.a, cfg.b, cfg.c, top);
     const int ex = scale_exponent(top), ea = scale_exponent(top * top), ep = scale_exponent(p);
-    const int ew = scale_exponent(top * top * p), before = eq;
-    chain = first ? p : chain * p;
-    eq = scale_exponent(chain);
-    if (first) ex0 = ex;
     f.x = std::ldexp(1.0f, ex);
     f.gram = std::ldexp(1.0f, ea - 2 * ex);
     f.square = cfg.c * std::ldexp(1.0f, ep - 2 * ea);
     f.gram_term = cfg.b * std::ldexp(1.0f, ep - ea);
     f.identity = cfg.a * std::ldexp(1.0f, ep);
-    f.chain = std::ldexp(1.0f, eq - ep - before);
-    f.inner = std::ldexp(1.0f, ew - ea - ep);
-    f.next = std::ldexp(1.0f, scale_exponent(next * next) - ep - ew);
-    f.result = std::ldexp(1.0f, -ex0 - eq);
+    f.result = std::ldexp(1.0f, (k + 1 < cfg.steps ? scale_exponent(next) : 0) - ep - ex);
     top = next;
   }
 }
 
-// Matrices of a stack that one thin launch takes, and its workspace.
-long long thin_stride(long long rows, long long cols) { return round_up(rows * cols, kVec); }
+// Matrices of a stack that one thin launch takes.
 long long thin_mats(long long rows, long long cols, long long batch) {
-  return std::max<long long>(1, std::min<long long>(batch, kThinWork / thin_stride(rows, cols)));
+  const long long each = thin_work(rows, cols, false);
+  return std::max<long long>(1, std::min<long long>(batch, each > 0 ? kThinWork / each : 1 << 24));
 }
 
 cudaError_t ns_run(const NsPlan& p, const zero_ns_config& cfg, int mats, const MatSource& src, char* ws,
@@ -314,7 +305,7 @@ zero_status zero_orthogonalize_workspace_bytes(const zero_ns_config* cfg, int64_
   if (st != ZERO_OK) return st;
   *bytes = rows == 0 || cols == 0 || batch == 0 ? 0
            : std::min(rows, cols) <= zfs::kThin
-               ? 4 * zfs::thin_stride(rows, cols) * zfs::thin_mats(rows, cols, batch)
+               ? zfs::thin_work(rows, cols, false) * zfs::thin_mats(rows, cols, batch)
                : zfs::ns_plan(rows, cols, zfs::ns_mats(rows, cols, batch), false).bytes;
   return ZERO_OK;
 }
@@ -361,14 +352,14 @@ zero_status zero_orthogonalize(const zero_ns_config* cfg, int64_t rows, int64_t 
   int launches = 0;
   int64_t need = 0;
   zero_orthogonalize_workspace_bytes(cfg, rows, cols, batch, &need);
-  if (!workspace || zfs::misaligned(workspace, 256) || !zfs::on_device(workspace, dev))
+  if (need > 0 && (!workspace || zfs::misaligned(workspace, 256) || !zfs::on_device(workspace, dev)))
     return zfs::report(ZERO_EINVAL, "workspace must be 256-byte aligned memory of the current device");
   if (workspace_bytes < need)
     return zfs::report(ZERO_EINVAL, "workspace has %lld bytes, %lld needed", workspace_bytes, need);
   if (std::min(rows, cols) <= zfs::kThin) {
     zfs::ThinArgs a{};
-    a.work = static_cast<float*>(workspace);
-    a.work_mat_stride = zfs::thin_stride(rows, cols);
+    a.work = static_cast<char*>(workspace);
+    a.work_mat_stride = zfs::thin_work(rows, cols, false);
     zfs::thin_scales(*cfg, &a);
     a.rows[0] = static_cast<int>(rows);
     a.cols[0] = static_cast<int>(cols);

@@ -482,7 +482,7 @@ zero_status muon_update(zero_ctx* ctx, cudaStream_t stream, int32_t* launches) {
     a.dev_steps = ctx->cap_steps;
     a.total_padded = bound;
     a.mom = ctx->bufs.exp_avg;
-    a.work = reinterpret_cast<float*>(ctx->muon_ws);
+    a.work = ctx->muon_ws;
     a.master = ctx->bufs.master;
     a.p16 = p16;
     int mats = 0;
@@ -497,9 +497,9 @@ zero_status muon_update(zero_ctx* ctx, cudaStream_t stream, int32_t* launches) {
     };
     for (const zero_ctx::MuonGroup& group : ctx->muon_groups) {
       if (std::min(group.rows, group.cols) > zfs::kThin || zfs::thin_ctas(group.rows, group.cols) != ctas) continue;
-      const int64_t numel = group.rows * group.cols;
+      const int64_t each = zfs::thin_work(group.rows, group.cols, true);
       for (int32_t p : group.params) {
-        if (mats == zfs::kMaxMats || (mats > 0 && at + numel > zfs::kThinWork)) {
+        if (mats == zfs::kMaxMats || (mats > 0 && at + each > zfs::kThinWork)) {
           const cudaError_t e = flush();
           if (e != cudaSuccess) return fail_cuda(ctx, "thin orthogonalisation launch", e);
         }
@@ -510,7 +510,7 @@ zero_status muon_update(zero_ctx* ctx, cudaStream_t stream, int32_t* launches) {
         a.step[mats] = static_cast<float>(static_cast<double>(mc.lr) * muon_scale(mc, group.rows, group.cols));
         const bool vec = param_grads(ctx, p, a.g[mats]) && group.cols % zfs::kVec == 0 && a.offset[mats] % zfs::kVec == 0;
         if (vec) a.vec[mats / 32] |= 1u << (mats % 32);
-        at += (numel + zfs::kVec - 1) / zfs::kVec * zfs::kVec;
+        at += each;
         ++mats;
       }
     }
@@ -1724,15 +1724,19 @@ zero_status muon_plan(zero_ctx* ctx, const zero_muon_config* cfg, const int64_t*
     ranges->push_back({ctx->param_offset[p], r * c});
   }
   *bytes = 0;
+  int64_t thin = 0;
   for (const zero_ctx::MuonGroup& g : *groups) {
     if (std::min(g.rows, g.cols) <= zfs::kThin) {
-      // what one thin launch holds: at most kThinWork elements unless one matrix is larger
-      *bytes = std::max<int64_t>(*bytes, 4 * (std::max<int64_t>(g.rows * g.cols, zfs::kThinWork) + zfs::kVec));
+      // what one thin launch takes: matrices up to kThinWork, or one that needs more
+      const int64_t each = zfs::thin_work(g.rows, g.cols, true);
+      thin += each * static_cast<int64_t>(g.params.size());
+      *bytes = std::max<int64_t>(*bytes, each);
       continue;
     }
     const int mats = zfs::ns_mats(g.rows, g.cols, static_cast<long long>(g.params.size()));
     *bytes = std::max<int64_t>(*bytes, zfs::ns_plan(g.rows, g.cols, mats, true).bytes);
   }
+  *bytes = std::max<int64_t>(*bytes, std::min<int64_t>(thin, zfs::kThinWork));
   return ZERO_OK;
 }
 
