@@ -36,7 +36,7 @@ def test_against_64_bits(rows, cols, dtype):
 
 
 @pytest.mark.parametrize("rows,cols", [(8, 300), (128, 129), (129, 128), (100, 3000), (3000, 100), (120, 257), (17, 520),
-                                       (1025, 33), (2, 20000)])
+                                       (1025, 33), (2, 20000), (70, 2100), (2100, 70), (9, 4000), (128, 5000)])
 @pytest.mark.parametrize("rank", [0, 1, 3])
 def test_thin_matrices_are_nearly_exact(rows, cols, rank):
     # Thin matrices keep 22 bits throughout: what is left is the bf16 result,

@@ -71,32 +71,36 @@ __device__ __forceinline__ void load_pair(uint32_t buffer, int r, int chunk, flo
   }
 }
 
-// acc (128 rows, `n` columns) = sum over k < depth of the pair product of two
-// buffers, A K-major and B K-major or MN-major; n and depth multiples of 16.
-// One thread: descriptors move by constants, as what this thread does between
-// two MMAs is what a short product takes.
-__device__ __forceinline__ void issue_pair(uint32_t acc, uint32_t a, uint32_t b, bool b_k_major, int n, int depth,
+// acc (128 rows, `n` columns, a multiple of 16) = sum over k < 64 kBlocks of the
+// pair product of two buffers, A K-major and B K-major or MN-major.  One
+// thread, straight-line code with descriptors that move by constants: what this
+// thread does between two MMAs is what a short product takes (predicated
+// pieces of 16 took 1550 cycles whatever the depth).
+template <int kBlocks>
+__device__ __forceinline__ void issue_blocks(uint32_t acc, uint64_t da, uint64_t db, uint32_t b_step, uint32_t b_block,
+                                             uint32_t idesc, uint32_t accumulate) {
+#pragma unroll
+  for (int part = 0; part < 3; ++part) {  // hi lo, lo hi, hi hi: the small terms first, as sums are truncated
+    const uint64_t pa = da + (part == 1 ? kHalfBytes >> 4 : 0), pb = db + (part == 0 ? kHalfBytes >> 4 : 0);
+#pragma unroll
+    for (int block = 0; block < kBlocks; ++block) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint64_t ka = pa + block * (kBlockBytes >> 4) + 2 * k, kb = pb + block * b_block + k * b_step;
+        if (part == 0 && block == 0 && k == 0) mma<1>(acc, ka, kb, idesc, accumulate);
+        else mma_add<1>(acc, ka, kb, idesc);
+      }
+    }
+  }
+}
+// `deep`: more than 64 of k; what the operands hold beyond their size is zero.
+__device__ __forceinline__ void issue_pair(uint32_t acc, uint32_t a, uint32_t b, bool b_k_major, int n, bool deep,
                                            bool accumulate) {
   const uint32_t idesc = (1u << 4) | (b_k_major ? 0u : 1u << 16) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
   const uint64_t da = smem_desc(a, true, 0), db = smem_desc(b, b_k_major, kBlockBytes);
   const uint32_t b_step = b_k_major ? 2 : 128, b_block = b_k_major ? kBlockBytes >> 4 : 512;  // units of 16 bytes
-  uint32_t on = accumulate ? 1 : 0;
-#pragma unroll
-  for (int part = 0; part < 3; ++part) {  // hi lo, lo hi, hi hi: the small terms first, as sums are truncated
-    uint64_t pa = da + (part == 1 ? kHalfBytes >> 4 : 0), pb = db + (part == 0 ? kHalfBytes >> 4 : 0);
-#pragma unroll
-    for (int block = 0; block < 2; ++block) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (block * 64 + k * 16 < depth) {
-          mma<1>(acc, pa + 2 * k, pb + b_step * k, idesc, on);
-          on = 1;
-        }
-      }
-      pa += kBlockBytes >> 4;
-      pb += b_block;
-    }
-  }
+  if (deep) issue_blocks<2>(acc, da, db, b_step, b_block, idesc, accumulate);
+  else issue_blocks<1>(acc, da, db, b_step, b_block, idesc, accumulate);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -338,6 +342,12 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) tmem_alloc<1>(smem_u32(&sh.tmem), kTmemColumns);
+  // Products run over 64 or 128 of k: what lies beyond mk (columns of A and P,
+  // rows of X) is zero.  Later writes stay within mk; a slice buffer that took
+  // other data is cleared again (clear_rest).
+  if (mk % 64 != 0) {
+    for (uint32_t i = tid; i < 3 * kPairBytes / 16; i += kThreads) sts16(square + 16 * i, make_uint4(0, 0, 0, 0));
+  }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -384,13 +394,19 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
                    "l"(image(s) + b * 128LL * mk), "r"(128 * mk), "r"(bar)
                    : "memory");
   };
+  // Zero from row mk on in the blocks of a slice buffer, as far as products read.
+  auto clear_rest = [&](uint32_t buffer) {
+    const int top = mk > 64 ? 128 : 64, pieces = (top - mk) * 8;
+    for (int e = tid; e < 4 * pieces; e += kThreads)
+      sts16(buffer + e / pieces * kBlockBytes + mk * 128 + e % pieces * 16, make_uint4(0, 0, 0, 0));
+  };
   // the share of a thread in an epilogue: row `row`, columns from `begin`
   const int row = (warp % 4) * 32 + lane, quarter = warp / 4;
   const bool in_rows = (warp % 4) * 32 < mk;  // the same for the whole warp
   const uint32_t lanes = ((warp % 4) * 32) << 16;
   const int share = (mk / 16 + 3) / 4 * 16;   // columns of a quarter of an m x m matrix
   auto add_to_gram = [&](int s, uint32_t buffer) {  // one thread
-    issue_pair(gram, buffer, buffer, true, mk, depth_of(s), s > 0);
+    issue_pair(gram, buffer, buffer, true, mk, depth_of(s) > 64, s > 0);
     mma_commit<1>(smem_u32(&sh.bar[s & 1]));
   };
 
@@ -532,12 +548,13 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
       }
       asm volatile("fence.proxy.async.shared::cluster;" ::: "memory");
       cluster_sync();
+      if (many) clear_rest(partial);
     }
     ready(ok);
 
     // ---- P over A -----------------------------------------------------------------
     if (tid == 0 && alive) {
-      issue_pair(other, square, square, true, mk, mk, false);
+      issue_pair(other, square, square, true, mk, mk > 64, false);
       mma_commit<1>(smem_u32(&sh.bar[2]));
     }
     ok = wait(2);
@@ -577,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
         ready(ok);
       }
       if (tid == 0 && alive) {
-        issue_pair(other, square, buffer, false, width, mk, false);
+        issue_pair(other, square, buffer, false, width, mk > 64, false);
         mma_commit<1>(smem_u32(&sh.bar[2]));
       }
       ok = wait(2);
@@ -615,7 +632,11 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
         pending[i] = true;
       } else if (!x.tall) {
         if (alive) write_rows<kMuon>(a, mat, x, vec, beside, j0, warp, lane);
-        if (many) ready(alive);
+        if (many) {
+          __syncthreads();
+          clear_rest(beside);
+          ready(alive);
+        }
       }
     }
   }

@@ -111,6 +111,23 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
         : "memory");
   }
 }
+// The same, always onto what the accumulator holds.
+template <int kCtas>
+__device__ __forceinline__ void mma_add(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  if constexpr (kCtas == 2) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.eq.u32 p, 0, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.eq.u32 p, 0, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc)
+        : "memory");
+  }
+}
 // Arrives on `bar` (of both CTAs of a pair) when the MMAs issued so far are done.
 template <int kCtas>
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
