@@ -202,6 +202,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
     for (int w = 0; w < kEpilogueWarps; ++w) mbar_init(c_full + 8 * w, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  if (warp == 8 && lane < 6) {  // the maps are there before the first copy asks for them
+    const CUtensorMap* maps[6] = {&ka.a, &ka.b, &ka.c, &ka.c_lo, &ka.d, &ka.d_lo};
+    const bool used[6] = {true, true, g.c != nullptr, g.c_lo != nullptr, g.d != nullptr, g.d_lo != nullptr};
+    if (used[lane]) asm volatile("prefetch.tensormap [%0];" ::"l"(maps[lane]) : "memory");
+  }
   if (warp == 9) tmem_alloc<kCtas>(smem_u32(&tmem_base), kTmemColumns);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
@@ -532,12 +537,18 @@ cudaError_t launch(GemmKernelArgs& ka, cudaStream_t stream) {
 
 template <int kEpi>
 cudaError_t launch_tile(GemmKernelArgs& ka, cudaStream_t stream) {
-  // A pair of SMs works on 256 x 256, one alone on 128 x 128: pairs once their
-  // tiles fill the GPU.
-  const long long t = 256;
-  const long long m = (ka.g.M + t - 1) / t, n = (ka.g.N + t - 1) / t;
-  const long long pairs = (kEpi == kNsGram || kEpi == kNsPoly ? m * (m + 1) / 2 : m * n) * ka.g.mats;
-  return pairs >= sm_count() / 2 ? launch<2, kEpi>(ka, stream) : launch<1, kEpi>(ka, stream);
+  // A pair of SMs works on 256 x 256, one alone on 128 x 128.  A 64-deep block
+  // takes both about as long (0.28 us: the pair's products, the single's
+  // operands at 64 bytes a cycle), so the form that needs fewer rounds over the
+  // GPU wins; at a tie the single's shorter epilogue does.  Two Gram matrices of
+  // 2048 x 8192: 97 us in singles (two rounds), 52 in pairs (one).
+  auto rounds = [&](long long tile, long long room) {
+    const long long m = (ka.g.M + tile - 1) / tile, n = (ka.g.N + tile - 1) / tile;
+    const long long tiles = (kEpi == kNsGram || kEpi == kNsPoly ? m * (m + 1) / 2 : m * n) * ka.g.mats;
+    return (tiles + room - 1) / room;
+  };
+  const int sms = sm_count();
+  return rounds(256, sms / 2) < rounds(128, sms) ? launch<2, kEpi>(ka, stream) : launch<1, kEpi>(ka, stream);
 }
 
 }  // namespace
