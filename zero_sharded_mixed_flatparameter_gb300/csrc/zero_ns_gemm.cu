@@ -100,20 +100,20 @@ __device__ __forceinline__ void store_rows(const GemmKernelArgs& ka, int mat, ui
   if (ka.vec_out && j0 + kChunk <= g.N) {  // two rows per access
     const int piece = lane % 16;
 #pragma unroll 1
-    for (int q = 0; q < 4; ++q) {
-      float4 old[4];
+    for (int q = 0; q < 2; ++q) {
+      float4 old[8];
       if constexpr (kEpi == kNsMuon) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = (q * 4 + k) * 2 + lane / 16;
+        for (int k = 0; k < 8; ++k) {
+          const int r = (q * 8 + k) * 2 + lane / 16;
           const long long at = base + (i0 + r) * pitch + j0 + 4 * piece;
           if (i0 + r < g.M && ZFS_CHECK(at >= 0 && at + 4 <= g.out.total_padded))
             old[k] = *reinterpret_cast<const float4*>(g.out.master + at);
         }
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = (q * 4 + k) * 2 + lane / 16;
+      for (int k = 0; k < 8; ++k) {
+        const int r = (q * 8 + k) * 2 + lane / 16;
         const long long at = base + (i0 + r) * pitch + j0 + 4 * piece;
         if (i0 + r >= g.M) continue;
         const uint4 v = lds16(buffer + r * 256 + ((piece ^ (r & 7)) << 4));
@@ -349,6 +349,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
       locate<kEpi>(ka, t, &mat, &ti, &tj);
       const int i0 = ti * kBlockM * kCtas + rank * kBlockM + quadrant * 32;
       const bool mirror = kSymmetric && ti != tj;
+      if constexpr (kEpi == kNsMuon) {
+        // the tile's master rows on their way into L2 while the products run
+        for (int chunk = 0; chunk < kChunks; ++chunk) {
+          const long long j = static_cast<long long>(tj) * kBlockN + (2 * chunk + half) * kChunk;
+          if (i0 + lane < g.M && j < g.N) {
+            const float* w = g.out.master + g.out.offset[mat] + (i0 + lane) * g.N + j;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(w) : "memory");
+            if (j + 32 < g.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(w + 32) : "memory");
+          }
+        }
+      }
       ok = __all_sync(0xffffffffu, wait_phase(tmem_full + 8 * acc, acc_parity, &gave_up));
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
