@@ -21,6 +21,7 @@ _CURRENT = contextlib.nullcontext()
 # read-only configuration structs by their values
 _ns_config = functools.lru_cache(maxsize=64)(B.make_ns_config)
 _qk_config = functools.lru_cache(maxsize=64)(B.zero_qk_config)
+_CONTIGUOUS = torch.contiguous_format
 
 
 def _on(device: torch.device):
@@ -52,7 +53,7 @@ def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients: Sequence[flo
     cfg = _ns_config(steps, tuple(coefficients), eps)
     with _on(x.device):
         need = B.zero_orthogonalize_workspace_bytes(cfg, rows, cols, batch)
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)  # 512-byte aligned
         B.zero_orthogonalize(cfg, rows, cols, batch, x.data_ptr(), _DTYPES[x.dtype],
                              x.stride(-2) if rows > 1 else max(cols, 1), x.stride(0) if batch > 1 else 0,
                              out.data_ptr(), out.stride(-2) if rows > 1 else max(cols, 1),
@@ -67,7 +68,7 @@ def _heads(x: torch.Tensor) -> B.zero_heads:
     return B.zero_heads(x.data_ptr(), token, head)
 
 
-def _check_qk(q, k, q_gain, k_gain, table, positions, eps, interleaved) -> B.zero_qk_config:
+def _check_qk(q, k, q_gain, k_gain, table, positions, eps, interleaved):
     device, dtype = q.device, q.dtype
     if q.dim() != 3 or k.dim() != 3 or dtype not in _DTYPES or not q.is_cuda:
         raise ValueError("q and k must be bf16 or fp32 CUDA tensors (tokens, heads, head_dim)")
@@ -89,8 +90,13 @@ def _check_qk(q, k, q_gain, k_gain, table, positions, eps, interleaved) -> B.zer
                                   or positions.device != device or not positions.is_contiguous()):
         raise ValueError("positions must be a contiguous int32 vector with one entry per token")
     n_positions, rotary = table.shape
-    return _qk_config(q_heads, k_heads, dim, rotary, 1 if interleaved else 0, _DTYPES[dtype],
-                      _DTYPES[gain_dtype or torch.float32], eps, n_positions)
+    return tokens, _qk_config(q_heads, k_heads, dim, rotary, 1 if interleaved else 0, _DTYPES[dtype],
+                              _DTYPES[gain_dtype or torch.float32], eps, n_positions)
+
+
+@functools.lru_cache(maxsize=256)
+def _backward_workspace(q_heads: int, k_heads: int, dim: int, tokens: int, device: int) -> int:
+    return B.zero_qk_backward_workspace_bytes(B.zero_qk_config(q_heads, k_heads, dim, 0, 0, 0, 0, 0.0, 0), tokens)
 
 
 def _ptr(x: Optional[torch.Tensor]) -> int:
@@ -109,14 +115,15 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_gain: Optional[torch.Tensor
     the rotary_dim/2 cosines, then the sines; rotary_dim is its width.  A
     position outside the table marks padding: zeros.  ``out`` may be (q, k).
     """
-    cfg = _check_qk(q, k, q_gain, k_gain, table, positions, eps, interleaved)
+    tokens, cfg = _check_qk(q, k, q_gain, k_gain, table, positions, eps, interleaved)
     if out is None:
-        out = (q.new_empty(q.shape), q.new_empty(k.shape))
+        out = (torch.empty_like(q, memory_format=_CONTIGUOUS), torch.empty_like(k, memory_format=_CONTIGUOUS))
     else:
         _check_like(out, (q, k))
-    with _on(q.device):
-        B.zero_qk_norm_rope(cfg, q.size(0), _heads(q), _heads(k), _ptr(q_gain), _ptr(k_gain), table.data_ptr(),
-                            _ptr(positions), _heads(out[0]), _heads(out[1]), _stream(q.device))
+    device = q.device
+    with _on(device):
+        B.zero_qk_norm_rope(cfg, tokens, _heads(q), _heads(k), _ptr(q_gain), _ptr(k_gain), table.data_ptr(),
+                            _ptr(positions), _heads(out[0]), _heads(out[1]), _stream(device))
     return out
 
 
@@ -137,27 +144,28 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
     gain gradients to, such as slices of a replica's flat gradient; new fp32
     vectors otherwise.
     """
-    cfg = _check_qk(q, k, q_gain, k_gain, table, positions, eps, interleaved)
+    tokens, cfg = _check_qk(q, k, q_gain, k_gain, table, positions, eps, interleaved)
     _check_like((dq_out, dk_out), (q, k))
     if out is None:
-        out = (q.new_empty(q.shape), q.new_empty(k.shape))
+        out = (torch.empty_like(q, memory_format=_CONTIGUOUS), torch.empty_like(k, memory_format=_CONTIGUOUS))
     else:
         _check_like(out, (q, k))
-    dim = q.size(2)
+    device, dim = q.device, cfg.head_dim
     if gain_out is None:
-        gain_out = torch.empty((2, dim), dtype=torch.float32, device=q.device).unbind()
+        gain_out = (torch.empty(dim, dtype=torch.float32, device=device),
+                    torch.empty(dim, dtype=torch.float32, device=device))
     else:
         for g in gain_out:
-            if g.dtype not in _DTYPES or g.dtype != gain_out[0].dtype or g.shape != (dim,) or g.device != q.device \
+            if g.dtype not in _DTYPES or g.dtype != gain_out[0].dtype or g.shape != (dim,) or g.device != device \
                     or not g.is_contiguous():
                 raise ValueError("gain_out must be two contiguous vectors of head_dim elements and one type")
-    with _on(q.device):
-        need = B.zero_qk_backward_workspace_bytes(cfg, q.size(0))
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-        B.zero_qk_norm_rope_backward(cfg, q.size(0), _heads(dq_out), _heads(dk_out), _heads(q), _heads(k),
+    with _on(device):
+        need = max(_backward_workspace(cfg.q_heads, cfg.k_heads, dim, tokens, device.index), 16)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        B.zero_qk_norm_rope_backward(cfg, tokens, _heads(dq_out), _heads(dk_out), _heads(q), _heads(k),
                                      _ptr(q_gain), _ptr(k_gain), table.data_ptr(), _ptr(positions), _heads(out[0]),
                                      _heads(out[1]), gain_out[0].data_ptr(), gain_out[1].data_ptr(),
-                                     _DTYPES[gain_out[0].dtype], workspace.data_ptr(), need, _stream(q.device))
+                                     _DTYPES[gain_out[0].dtype], workspace.data_ptr(), need, _stream(device))
     return (*out, *gain_out)
 
 
