@@ -59,10 +59,14 @@ NsPlan ns_plan(long long rows, long long cols, int mats, bool keep_update);
 int ns_mats(long long rows, long long cols, long long batch);
 // Checks steps, coefficients and eps; the reason in `why`.
 bool ns_config_ok(const zero_ns_config& cfg, const char** why);
-// From `src` with its norm partials in the workspace to `out`: normalise, then the steps.
-struct MatSource;
-cudaError_t ns_run(const NsPlan& p, const zero_ns_config& cfg, int mats, const MatSource& src, char* ws,
-                   const NsOut& out, cudaStream_t stream, int* launches);
+// Stacks that go through the steps together.
+constexpr int kMaxProblems = 12;
+// Elements of X that are worked on at once.
+constexpr long long kNsBatch = 1LL << 27;
+struct NsProblem;
+// From every problem's source, with its norm partials in the workspace, to its
+// `out`: normalise, then the steps.
+cudaError_t ns_run(const NsProblem* problems, int count, const zero_ns_config& cfg, cudaStream_t stream, int* launches);
 
 // ---- elementwise passes (zero_muon_kernels.cu) -----------------------------
 // A stack of strided matrices as the orthogonalisation's input.
@@ -71,6 +75,13 @@ struct MatSource {
   int fp32;                 // else bf16
   long long row_stride, mat_stride;
   int vec_ok;               // 8-element vectors of a row are aligned
+};
+struct NsProblem {
+  NsPlan plan;
+  int mats;
+  MatSource src;
+  char* ws;
+  NsOut out;
 };
 // Partial sums of squares, [mat][chunk].
 cudaError_t launch_ns_norm(const MatSource& s, const NsPlan& p, int mats, double* partials, cudaStream_t stream);
@@ -192,7 +203,8 @@ struct GemmArgs {
   long long ldd = 0, d_mat_stride = 0;
   NsOut out;
 };
-cudaError_t launch_ns_gemm(const GemmArgs& g, cudaStream_t stream, int* launches);
+// One launch for `count` (up to kMaxProblems) stacks with one epilogue.
+cudaError_t launch_ns_gemm(const GemmArgs* g, int count, cudaStream_t stream, int* launches);
 unsigned int ns_gemm_debug_failures();
 // Bounded waits of the products that gave up (0xFFFFFFFF if it cannot be read).
 unsigned int ns_gemm_timeouts();

@@ -31,6 +31,7 @@
 
 #include <cuda.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "zero_device.cuh"
@@ -52,15 +53,24 @@ constexpr uint32_t kHalfBytes = 32 * kChunk * 2;  // a warp's chunk of hi (or of
 constexpr uint32_t kBufferBytes = 2 * kHalfBytes;
 constexpr uint32_t kSmemBytes = kStages * kStageBytes + kEpilogueWarps * kBufferBytes + 1024;  // + alignment
 
-// What one launch needs.
-struct GemmKernelArgs {
+// One stack of equal matrices.
+struct Problem {
   CUtensorMap a, b;
   CUtensorMap c, c_lo, d, d_lo;  // boxes of 64 x 32
   CUtensorMap d_mirror;          // boxes of 32 x 64
   GemmArgs g;
-  int tiles_m, tiles_n, tiles;   // tiles of one matrix / of all
+  int first;                     // tile of the launch
+  int tiles_m, tiles_n, tiles;   // tiles of one matrix
   int k_blocks;
   int vec_out;                   // kNsOut / kNsMuon: four elements of a row are aligned
+};
+
+// What one launch needs: stacks of several shapes share it, so that small ones
+// do not leave the GPU to a few tiles at a time.
+template <int kProblems>
+struct GemmKernelArgs {
+  Problem p[kProblems];
+  int problems, total;           // tiles of all
 };
 
 __device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
@@ -92,12 +102,12 @@ __device__ __forceinline__ void add_pieces(uint32_t half, int r, int first, floa
 // Whole rows of a warp's finished chunk (32 x 64 fp32 in `buffer`, 16-byte
 // pieces swizzled by row) to their place, from row i0 and column j0.
 template <int kEpi>
-__device__ __forceinline__ void store_rows(const GemmKernelArgs& ka, int mat, uint32_t buffer, long long i0, long long j0,
+__device__ __forceinline__ void store_rows(const Problem& p, int mat, uint32_t buffer, long long i0, long long j0,
                                            int lane) {
-  const GemmArgs& g = ka.g;
+  const GemmArgs& g = p.g;
   const long long base = kEpi == kNsMuon ? g.out.offset[mat] : mat * g.out.mat_stride;
   const long long pitch = kEpi == kNsMuon ? g.N : g.out.row_stride;
-  if (ka.vec_out && j0 + kChunk <= g.N) {  // two rows per access
+  if (p.vec_out && j0 + kChunk <= g.N) {  // two rows per access
     const int piece = lane % 16;
 #pragma unroll 1
     for (int q = 0; q < 2; ++q) {
@@ -154,36 +164,46 @@ __device__ __forceinline__ void store_rows(const GemmKernelArgs& ka, int mat, ui
   }
 }
 
-// Tile t of all matrices: (matrix, tile row, tile column).
-template <int kEpi>
-__device__ __forceinline__ void locate(const GemmKernelArgs& ka, int t, int* mat, int* ti, int* tj) {
-  *mat = t / ka.tiles;
-  int r = t - *mat * ka.tiles;
+// Tile t of the launch: its stack, matrix, tile row and column.
+struct Tile {
+  int problem, mat, ti, tj;
+};
+template <int kEpi, int kProblems>
+__device__ __forceinline__ Tile locate(const GemmKernelArgs<kProblems>& ka, int t) {
+  Tile at;
+  at.problem = 0;
+  if constexpr (kProblems > 1) {
+    while (at.problem + 1 < ka.problems && t >= ka.p[at.problem + 1].first) ++at.problem;
+  }
+  const Problem& p = ka.p[at.problem];
+  t -= p.first;
+  at.mat = t / p.tiles;
+  int r = t - at.mat * p.tiles;
   if constexpr (kEpi == kNsGram || kEpi == kNsPoly) {  // rows of the lower triangle, one after another
     int i = static_cast<int>((sqrtf(8.0f * static_cast<float>(r) + 1.0f) - 1.0f) * 0.5f);
     while (static_cast<long long>(i) * (i + 1) / 2 > r) --i;
     while (static_cast<long long>(i + 1) * (i + 2) / 2 <= r) ++i;
-    *ti = i;
-    *tj = r - static_cast<int>(static_cast<long long>(i) * (i + 1) / 2);
+    at.ti = i;
+    at.tj = r - static_cast<int>(static_cast<long long>(i) * (i + 1) / 2);
   } else {  // bands of 8 tile rows, so that tiles in flight share operands in L2
     constexpr int kBand = 8;
-    const int band = r / (kBand * ka.tiles_n), first = band * kBand;
-    const int high = ka.tiles_m - first < kBand ? ka.tiles_m - first : kBand;
-    r -= band * kBand * ka.tiles_n;
-    *ti = first + r % high;
-    *tj = r / high;
+    const int band = r / (kBand * p.tiles_n), first = band * kBand;
+    const int high = p.tiles_m - first < kBand ? p.tiles_m - first : kBand;
+    r -= band * kBand * p.tiles_n;
+    at.ti = first + r % high;
+    at.tj = r / high;
   }
+  return at;
 }
 
-template <int kCtas, int kEpi>
-__global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_constant__ GemmKernelArgs ka) {
+template <int kCtas, int kEpi, int kProblems>
+__global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_constant__ GemmKernelArgs<kProblems> ka) {
   constexpr int kBlockN = 128 * kCtas;  // columns of a tile; rows: kBlockM * kCtas
   constexpr uint32_t kTmemColumns = 2 * kBlockN;
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(8) uint64_t bars[2 * kStages + 4 + kEpilogueWarps];
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
-  const GemmArgs& g = ka.g;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t stages = (smem_u32(smem_raw) + 1023) & ~1023u, buffers = stages + kStages * kStageBytes;
   const uint32_t rank = kCtas == 2 ? blockIdx.x % 2 : 0;
@@ -202,10 +222,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
     for (int w = 0; w < kEpilogueWarps; ++w) mbar_init(c_full + 8 * w, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 8 && lane < 6) {  // the maps are there before the first copy asks for them
-    const CUtensorMap* maps[6] = {&ka.a, &ka.b, &ka.c, &ka.c_lo, &ka.d, &ka.d_lo};
-    const bool used[6] = {true, true, g.c != nullptr, g.c_lo != nullptr, g.d != nullptr, g.d_lo != nullptr};
-    if (used[lane]) asm volatile("prefetch.tensormap [%0];" ::"l"(maps[lane]) : "memory");
+  if (warp == 8) {  // the maps are there before the first copy asks for them
+    for (int i = lane; i < 2 * ka.problems; i += 32)
+      asm volatile("prefetch.tensormap [%0];" ::"l"(i % 2 ? &ka.p[i / 2].b : &ka.p[i / 2].a) : "memory");
   }
   if (warp == 9) tmem_alloc<kCtas>(smem_u32(&tmem_base), kTmemColumns);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -213,14 +232,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
   if constexpr (kCtas == 2) cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
-  const int first = blockIdx.x / kCtas, step = gridDim.x / kCtas, total = ka.tiles * g.mats;
-  const int k_steps = ka.k_blocks;
+  const int first = blockIdx.x / kCtas, step = gridDim.x / kCtas, total = ka.total;
   // The next kernel may take free SMs from here on; what the one before wrote
   // is read only after it has finished.
   asm volatile("griddepcontrol.launch_dependents;");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   bool skip = false;
-  if constexpr (kEpi == kNsMuon) skip = g.out.dev_t && *g.out.dev_t >= g.out.dev_steps;
+  if constexpr (kEpi == kNsMuon) skip = ka.p[0].g.out.dev_t && *ka.p[0].g.out.dev_t >= ka.p[0].g.out.dev_steps;
 
   if (warp == 8 && lane == 0 && !skip) {
     // ---- loads: both CTAs of a pair count on the first one's barrier ---------
@@ -228,10 +246,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
     long long issued = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
-      int mat, ti, tj;
-      locate<kEpi>(ka, t, &mat, &ti, &tj);
-      const int i0 = ti * kBlockM * kCtas + rank * kBlockM;
-      const int j0 = tj * kBlockN + rank * 128;
+      const Tile at_tile = locate<kEpi>(ka, t);
+      const Problem& p = ka.p[at_tile.problem];
+      const int i0 = at_tile.ti * kBlockM * kCtas + rank * kBlockM, j0 = at_tile.tj * kBlockN + rank * 128;
+      const int mat = at_tile.mat, k_steps = p.k_blocks;
+      const bool a_k = p.g.a.k_major, b_k = p.g.b.k_major;
       for (int s = 0; s < k_steps; ++s) {
         const int k0 = s * kBlockK;
         if (!wait_phase(empty + 8 * stage, parity ^ 1, &gave_up)) {
@@ -241,17 +260,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
         const uint32_t at = stages + stage * kStageBytes;
         const uint32_t bar = kCtas == 2 ? map_rank(full + 8 * stage, 0) : full + 8 * stage;
         if (rank == 0) mbar_expect_tx(full + 8 * stage, kStageBytes * kCtas);
-        if (g.a.k_major) {
-          tma_load<kCtas>(at, &ka.a, k0, i0, mat, bar);
+        if (a_k) {
+          tma_load<kCtas>(at, &p.a, k0, i0, mat, bar);
         } else {
-          tma_load<kCtas>(at, &ka.a, i0, k0, mat, bar);
-          tma_load<kCtas>(at + kOperandBytes / 2, &ka.a, i0 + 64, k0, mat, bar);
+          tma_load<kCtas>(at, &p.a, i0, k0, mat, bar);
+          tma_load<kCtas>(at + kOperandBytes / 2, &p.a, i0 + 64, k0, mat, bar);
         }
-        if (g.b.k_major) {
-          tma_load<kCtas>(at + kOperandBytes, &ka.b, k0, j0, mat, bar);
+        if (b_k) {
+          tma_load<kCtas>(at + kOperandBytes, &p.b, k0, j0, mat, bar);
         } else {
-          tma_load<kCtas>(at + kOperandBytes, &ka.b, j0, k0, mat, bar);
-          tma_load<kCtas>(at + kOperandBytes + kOperandBytes / 2, &ka.b, j0 + 64, k0, mat, bar);
+          tma_load<kCtas>(at + kOperandBytes, &p.b, j0, k0, mat, bar);
+          tma_load<kCtas>(at + kOperandBytes + kOperandBytes / 2, &p.b, j0 + 64, k0, mat, bar);
         }
         ++issued;
         if (++stage == kStages) {
@@ -288,13 +307,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
     }
   } else if (warp == 9 && lane == 0 && rank == 0 && !skip) {
     // ---- MMAs ---------------------------------------------------------------
-    const uint32_t idesc = (1u << 4) | (g.a.k_major ? 0u : 1u << 15) | (g.b.k_major ? 0u : 1u << 16) |
-                           (static_cast<uint32_t>(kBlockN >> 3) << 17) |
-                           (static_cast<uint32_t>((kBlockM * kCtas) >> 4) << 24);
-    const uint64_t step_a = g.a.k_major ? 32 >> 4 : 2048 >> 4, step_b = g.b.k_major ? 32 >> 4 : 2048 >> 4;
     uint32_t stage = 0, parity = 0, acc = 0, acc_parity = 0;
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
+      const Problem& p = ka.p[locate<kEpi>(ka, t).problem];
+      const bool a_k = p.g.a.k_major, b_k = p.g.b.k_major;
+      const int k_steps = p.k_blocks;
+      const uint32_t idesc = (1u << 4) | (a_k ? 0u : 1u << 15) | (b_k ? 0u : 1u << 16) |
+                             (static_cast<uint32_t>(kBlockN >> 3) << 17) |
+                             (static_cast<uint32_t>((kBlockM * kCtas) >> 4) << 24);
+      const uint64_t step_a = a_k ? 32 >> 4 : 2048 >> 4, step_b = b_k ? 32 >> 4 : 2048 >> 4;
       ok = wait_phase(tmem_empty + 8 * acc, acc_parity ^ 1, &gave_up);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -304,7 +326,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t at = stages + stage * kStageBytes;
-        const uint64_t da = smem_desc(at, g.a.k_major, 8192), db = smem_desc(at + kOperandBytes, g.b.k_major, 8192);
+        const uint64_t da = smem_desc(at, a_k, 8192), db = smem_desc(at + kOperandBytes, b_k, 8192);
 #pragma unroll
         for (int k = 0; k < kBlockK / 16; ++k)
           mma<kCtas>(d, da + k * step_a, db + k * step_b, idesc, s > 0 || k > 0 ? 1 : 0);
@@ -327,15 +349,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
     constexpr int kChunks = kBlockN / kChunk / 2;  // per warp and tile
     const int quadrant = warp % 4, half = warp / 4;
     const uint32_t buffer = buffers + warp * kBufferBytes, bar = c_full + 8 * warp;
-    const uint32_t c_bytes = kHalfBytes * (g.c_lo ? 2 : 1);
+    const bool has_lo = ka.p[0].g.c_lo != nullptr, makes_lo = ka.p[0].g.d_lo != nullptr;  // as of every stack
+    const uint32_t c_bytes = kHalfBytes * (has_lo ? 2 : 1);
     // This warp's C of a tile's chunk into its buffer; one lane.
     auto load_c = [&](int t, int chunk) {
-      int mat, ti, tj;
-      locate<kEpi>(ka, t, &mat, &ti, &tj);
-      const int i0 = ti * kBlockM * kCtas + rank * kBlockM + quadrant * 32, j0 = tj * kBlockN + (2 * chunk + half) * kChunk;
+      const Tile at = locate<kEpi>(ka, t);
+      const Problem& p = ka.p[at.problem];
+      const int i0 = at.ti * kBlockM * kCtas + rank * kBlockM + quadrant * 32;
+      const int j0 = at.tj * kBlockN + (2 * chunk + half) * kChunk;
       mbar_expect_tx(bar, c_bytes);
-      tma_load<1>(buffer, &ka.c, j0, i0, mat, bar);
-      if (g.c_lo) tma_load<1>(buffer + kHalfBytes, &ka.c_lo, j0, i0, mat, bar);
+      tma_load<1>(buffer, &p.c, j0, i0, at.mat, bar);
+      if (has_lo) tma_load<1>(buffer + kHalfBytes, &p.c_lo, j0, i0, at.mat, bar);
     };
     uint32_t acc = 0, acc_parity = 0, c_parity = 0;
     bool loaded = false;  // a C is on its way or here
@@ -345,8 +369,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
     }
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
-      int mat, ti, tj;
-      locate<kEpi>(ka, t, &mat, &ti, &tj);
+      const Tile at = locate<kEpi>(ka, t);
+      const Problem& p = ka.p[at.problem];
+      const GemmArgs& g = p.g;
+      const int mat = at.mat, ti = at.ti, tj = at.tj;
       const int i0 = ti * kBlockM * kCtas + rank * kBlockM + quadrant * 32;
       const bool mirror = kSymmetric && ti != tj;
       if constexpr (kEpi == kNsMuon) {
@@ -384,7 +410,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
           for (int k = 0; k < 32; ++k) y[q][k] *= g.alpha;
           if constexpr (kHasC) {
             add_pieces(buffer, lane, 4 * q, g.cfactor, y[q]);
-            if (g.c_lo) add_pieces(buffer + kHalfBytes, lane, 4 * q, g.cfactor, y[q]);
+            if (has_lo) add_pieces(buffer + kHalfBytes, lane, 4 * q, g.cfactor, y[q]);
           }
           if constexpr (!kRows) {
 #pragma unroll
@@ -395,7 +421,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
               for (int k = 0; k < 4; ++k) h[k] = half2_bits(z[2 * k], z[2 * k + 1]);
               sts16(piece_at(buffer, lane, 4 * q + v), make_uint4(h[0], h[1], h[2], h[3]));
               if constexpr (kEpi == kNsApply) {
-                if (g.d_lo) {
+                if (makes_lo) {
                   uint32_t l[4];
 #pragma unroll
                   for (int k = 0; k < 4; ++k) {
@@ -432,16 +458,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
                                __float_as_uint(y[q][4 * v + 2]), __float_as_uint(y[q][4 * v + 3])));
           }
           __syncwarp();
-          if (i0 < g.M && j0 < g.N) store_rows<kEpi>(ka, mat, buffer, i0, j0, lane);
+          if (i0 < g.M && j0 < g.N) store_rows<kEpi>(p, mat, buffer, i0, j0, lane);
         }
         asm volatile("fence.proxy.async;" ::: "memory");
         __syncwarp();
         if (lane == 0) {
           if constexpr (!kRows) {
             if (i0 < g.M && j0 < g.N) {  // what reaches over the matrix's end is cut by the copy
-              tma_store(&ka.d, buffer, j0, i0, mat);
-              if (mirror) tma_store(&ka.d_mirror, buffer + kHalfBytes, i0, j0, mat);
-              if (kEpi == kNsApply && g.d_lo) tma_store(&ka.d_lo, buffer + kHalfBytes, j0, i0, mat);
+              tma_store(&p.d, buffer, j0, i0, mat);
+              if (mirror) tma_store(&p.d_mirror, buffer + kHalfBytes, i0, j0, mat);
+              if (kEpi == kNsApply && makes_lo) tma_store(&p.d_lo, buffer + kHalfBytes, j0, i0, mat);
             }
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
@@ -516,21 +542,28 @@ bool encode_result(CUtensorMap* map, const uint16_t* data, const GemmArgs& g, cu
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int kCtas, int kEpi>
-cudaError_t launch(GemmKernelArgs& ka, cudaStream_t stream) {
-  const GemmArgs& g = ka.g;
-  const long long tile = 128 * kCtas, tiles_m = (g.M + tile - 1) / tile, tiles_n = (g.N + tile - 1) / tile;
-  const long long all = kEpi == kNsGram || kEpi == kNsPoly ? tiles_m * (tiles_m + 1) / 2 : tiles_m * tiles_n;
-  if (all * g.mats > 0x3fffffffLL) return cudaErrorInvalidValue;
-  ka.tiles_m = static_cast<int>(tiles_m);
-  ka.tiles_n = static_cast<int>(tiles_n);
-  ka.tiles = static_cast<int>(all);
-  const cudaError_t e =
-      cudaFuncSetAttribute(ns_gemm_kernel<kCtas, kEpi>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+template <int kCtas, int kEpi, int kProblems>
+cudaError_t launch(GemmKernelArgs<kProblems>& ka, cudaStream_t stream) {
+  const long long tile = 128 * kCtas;
+  long long total = 0;
+  for (int i = 0; i < ka.problems; ++i) {
+    Problem& p = ka.p[i];
+    const long long tiles_m = (p.g.M + tile - 1) / tile, tiles_n = (p.g.N + tile - 1) / tile;
+    const long long all = kEpi == kNsGram || kEpi == kNsPoly ? tiles_m * (tiles_m + 1) / 2 : tiles_m * tiles_n;
+    if (total + all * p.g.mats > 0x3fffffffLL) return cudaErrorInvalidValue;
+    p.first = static_cast<int>(total);
+    p.tiles_m = static_cast<int>(tiles_m);
+    p.tiles_n = static_cast<int>(tiles_n);
+    p.tiles = static_cast<int>(all);
+    total += all * p.g.mats;
+  }
+  ka.total = static_cast<int>(total);
+  const auto kernel = ns_gemm_kernel<kCtas, kEpi, kProblems>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
-  const long long tiles = all * g.mats, room = sm_count() / kCtas;
+  const long long room = sm_count() / kCtas;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((tiles < room ? tiles : room) * kCtas));
+  cfg.gridDim = dim3(static_cast<unsigned>((total < room ? total : room) * kCtas));
   cfg.blockDim = dim3(kGemmThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
@@ -543,54 +576,79 @@ cudaError_t launch(GemmKernelArgs& ka, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, ns_gemm_kernel<kCtas, kEpi>, ka);
+  return cudaLaunchKernelEx(&cfg, kernel, ka);
 }
 
-template <int kEpi>
-cudaError_t launch_tile(GemmKernelArgs& ka, cudaStream_t stream) {
+template <int kEpi, int kProblems>
+cudaError_t launch_tile(GemmKernelArgs<kProblems>& ka, cudaStream_t stream) {
   // A pair of SMs works on 256 x 256, one alone on 128 x 128.  A 64-deep block
   // takes both about as long (0.28 us: the pair's products, the single's
   // operands at 64 bytes a cycle), so the form that needs fewer rounds over the
-  // GPU wins; at a tie the single's shorter epilogue does.  Two Gram matrices of
-  // 2048 x 8192: 97 us in singles (two rounds), 52 in pairs (one).
-  auto rounds = [&](long long tile, long long room) {
-    const long long m = (ka.g.M + tile - 1) / tile, n = (ka.g.N + tile - 1) / tile;
-    const long long tiles = (kEpi == kNsGram || kEpi == kNsPoly ? m * (m + 1) / 2 : m * n) * ka.g.mats;
-    return (tiles + room - 1) / room;
+  // GPU wins, give or take the longer epilogue of a pair (4 blocks).  Two Gram
+  // matrices of 2048 x 8192: 97 us in singles (two rounds), 52 in pairs (one).
+  auto cost = [&](long long tile, long long room) {
+    long long tiles = 0, blocks = 0;
+    for (int i = 0; i < ka.problems; ++i) {
+      const Problem& p = ka.p[i];
+      const long long m = (p.g.M + tile - 1) / tile, n = (p.g.N + tile - 1) / tile;
+      const long long t = (kEpi == kNsGram || kEpi == kNsPoly ? m * (m + 1) / 2 : m * n) * p.g.mats;
+      tiles += t;
+      blocks += t * p.k_blocks;
+    }
+    const double mean = static_cast<double>(blocks) / static_cast<double>(tiles);
+    return mean * static_cast<double>((tiles + room - 1) / room);
   };
   const int sms = sm_count();
-  return rounds(256, sms / 2) < rounds(128, sms) ? launch<2, kEpi>(ka, stream) : launch<1, kEpi>(ka, stream);
+  return cost(256, sms / 2) + 4.0 < cost(128, sms) ? launch<2, kEpi, kProblems>(ka, stream)
+                                                   : launch<1, kEpi, kProblems>(ka, stream);
 }
 
-}  // namespace
-
-cudaError_t launch_ns_gemm(const GemmArgs& g, cudaStream_t stream, int* launches) {
-  std::call_once(g_encode_once, load_encode);
-  if (!g_encode) return cudaErrorNotSupported;
-  GemmKernelArgs ka;
-  ka.g = g;
-  ka.k_blocks = static_cast<int>((g.K + kBlockK - 1) / kBlockK);
-  if (!encode(&ka.a, g.a, g.M, g.K, g.mats) || !encode(&ka.b, g.b, g.N, g.K, g.mats)) return cudaErrorInvalidValue;
+bool fill(const GemmArgs& g, Problem* p) {
+  p->g = g;
+  p->k_blocks = static_cast<int>((g.K + kBlockK - 1) / kBlockK);
   const bool mirrored = g.epilogue == kNsGram || g.epilogue == kNsPoly;
-  if ((g.c && !encode_result(&ka.c, g.c, g, 64, 32)) || (g.c_lo && !encode_result(&ka.c_lo, g.c_lo, g, 64, 32)) ||
-      (g.d && !encode_result(&ka.d, g.d, g, 64, 32)) || (g.d_lo && !encode_result(&ka.d_lo, g.d_lo, g, 64, 32)) ||
-      (mirrored && !encode_result(&ka.d_mirror, g.d, g, 32, 64)))
-    return cudaErrorInvalidValue;
-  ka.vec_out = 0;
+  if (!encode(&p->a, g.a, g.M, g.K, g.mats) || !encode(&p->b, g.b, g.N, g.K, g.mats) ||
+      (g.c && !encode_result(&p->c, g.c, g, 64, 32)) || (g.c_lo && !encode_result(&p->c_lo, g.c_lo, g, 64, 32)) ||
+      (g.d && !encode_result(&p->d, g.d, g, 64, 32)) || (g.d_lo && !encode_result(&p->d_lo, g.d_lo, g, 64, 32)) ||
+      (mirrored && !encode_result(&p->d_mirror, g.d, g, 32, 64)))
+    return false;
+  p->vec_out = 0;
   if (g.epilogue == kNsOut) {
-    ka.vec_out = g.out.row_stride % 4 == 0 && g.out.mat_stride % 4 == 0 && reinterpret_cast<uintptr_t>(g.out.out) % 8 == 0;
+    p->vec_out = g.out.row_stride % 4 == 0 && g.out.mat_stride % 4 == 0 && reinterpret_cast<uintptr_t>(g.out.out) % 8 == 0;
   } else if (g.epilogue == kNsMuon) {
-    ka.vec_out = g.N % 4 == 0;
-    for (int m = 0; m < g.mats; ++m) ka.vec_out = ka.vec_out && g.out.offset[m] % 4 == 0;
+    p->vec_out = g.N % 4 == 0;
+    for (int m = 0; m < g.mats; ++m) p->vec_out = p->vec_out && g.out.offset[m] % 4 == 0;
   }
-  ++*launches;
-  switch (g.epilogue) {
+  return true;
+}
+
+template <int kProblems>
+cudaError_t launch_problems(const GemmArgs* g, int count, cudaStream_t stream) {
+  GemmKernelArgs<kProblems> ka;
+  ka.problems = count;
+  // the deepest tiles first, so that the last round is of short ones
+  int order[kProblems];
+  for (int i = 0; i < count; ++i) order[i] = i;
+  std::stable_sort(order, order + count, [&](int x, int y) { return g[x].K > g[y].K; });
+  for (int i = 0; i < count; ++i)
+    if (!fill(g[order[i]], &ka.p[i])) return cudaErrorInvalidValue;
+  switch (g[0].epilogue) {
     case kNsGram: return launch_tile<kNsGram>(ka, stream);
     case kNsPoly: return launch_tile<kNsPoly>(ka, stream);
     case kNsApply: return launch_tile<kNsApply>(ka, stream);
     case kNsOut: return launch_tile<kNsOut>(ka, stream);
     default: return launch_tile<kNsMuon>(ka, stream);
   }
+}
+
+}  // namespace
+
+cudaError_t launch_ns_gemm(const GemmArgs* g, int count, cudaStream_t stream, int* launches) {
+  std::call_once(g_encode_once, load_encode);
+  if (!g_encode) return cudaErrorNotSupported;
+  ++*launches;
+  // (a stack by itself spares the launch 20 KB of arguments)
+  return count == 1 ? launch_problems<1>(g, count, stream) : launch_problems<kMaxProblems>(g, count, stream);
 }
 
 unsigned int ns_gemm_timeouts() {

@@ -98,7 +98,7 @@ bool ns_config_ok(const zero_ns_config& cfg, const char** why) {
 }
 
 int ns_mats(long long rows, long long cols, long long batch) {
-  const long long room = (1LL << 27) / std::max<long long>(rows * cols, 1);
+  const long long room = kNsBatch / std::max<long long>(rows * cols, 1);
   return static_cast<int>(std::max<long long>(1, std::min<long long>({batch, room, kMaxMats})));
 }
 
@@ -160,28 +160,29 @@ long long thin_mats(long long rows, long long cols, long long batch) {
   return std::max<long long>(1, std::min<long long>(batch, each > 0 ? kThinWork / each : 1 << 24));
 }
 
-cudaError_t ns_run(const NsPlan& p, const zero_ns_config& cfg, int mats, const MatSource& src, char* ws,
-                   const NsOut& out, cudaStream_t stream, int* launches) {
-  auto half = [&](long long at) { return reinterpret_cast<uint16_t*>(ws + at); };
+cudaError_t ns_run(const NsProblem* problems, int count, const zero_ns_config& cfg, cudaStream_t stream,
+                   int* launches) {
   const int lows = low_steps(cfg.steps);
   double top = 1.0;  // bound of the spectral norm of X
   int ex = scale_exponent(top);
-  ScaleArgs s{};
-  s.src = src;
-  s.rows = p.rows;
-  s.cols = p.cols;
-  s.ldx = p.ldx;
-  s.mats = mats;
-  s.chunks = p.chunks;
-  s.partials = reinterpret_cast<const double*>(ws + p.partials);
-  s.eps = cfg.eps;
-  s.scale = std::ldexp(1.0f, ex);
-  s.hi = half(p.x_hi[0]);
-  s.lo = lows > 0 ? half(p.x_lo[0]) : nullptr;
-  cudaError_t e = launch_ns_scale(s, stream);
-  if (e != cudaSuccess) return e;
-  ++*launches;
-  const long long x_stride = p.rows * p.ldx, m_stride = p.m * p.ldm;
+  for (int i = 0; i < count; ++i) {
+    const NsProblem& q = problems[i];
+    ScaleArgs s{};
+    s.src = q.src;
+    s.rows = q.plan.rows;
+    s.cols = q.plan.cols;
+    s.ldx = q.plan.ldx;
+    s.mats = q.mats;
+    s.chunks = q.plan.chunks;
+    s.partials = reinterpret_cast<const double*>(q.ws + q.plan.partials);
+    s.eps = cfg.eps;
+    s.scale = std::ldexp(1.0f, ex);
+    s.hi = reinterpret_cast<uint16_t*>(q.ws + q.plan.x_hi[0]);
+    s.lo = lows > 0 ? reinterpret_cast<uint16_t*>(q.ws + q.plan.x_lo[0]) : nullptr;
+    const cudaError_t e = launch_ns_scale(s, stream);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+  }
   for (int k = 0; k < cfg.steps; ++k) {
     const int from = k % 2, to = 1 - from;
     const bool low = k < lows, last = k + 1 == cfg.steps;
@@ -189,74 +190,78 @@ cudaError_t ns_run(const NsPlan& p, const zero_ns_config& cfg, int mats, const M
     const int ep = scale_exponent(largest_factor(cfg.b, cfg.c, top * top));
     const double next = largest_value(cfg.a, cfg.b, cfg.c, top);
     const int en = scale_exponent(next);
-    GemmOperand x;
-    x.data = half(p.x_hi[from]);
-    x.ld = p.ldx;
-    x.mat_stride = x_stride;
-    GemmOperand square;
-    square.ld = p.ldm;
-    square.mat_stride = m_stride;
+    GemmArgs gram[kMaxProblems], poly[kMaxProblems], apply[kMaxProblems];
+    for (int i = 0; i < count; ++i) {
+      const NsProblem& q = problems[i];
+      const NsPlan& p = q.plan;
+      auto half = [&](long long at) { return reinterpret_cast<uint16_t*>(q.ws + at); };
+      GemmOperand x;
+      x.data = half(p.x_hi[from]);
+      x.ld = p.ldx;
+      x.mat_stride = p.rows * p.ldx;
+      GemmOperand square;
+      square.ld = p.ldm;
+      square.mat_stride = p.m * p.ldm;
 
-    GemmArgs gram{};
-    gram.M = gram.N = p.m;
-    gram.K = p.n;
-    gram.mats = mats;
-    gram.a = gram.b = x;
-    gram.a.k_major = gram.b.k_major = !p.tall;
-    gram.epilogue = kNsGram;
-    gram.alpha = std::ldexp(1.0f, ea - 2 * ex);
-    gram.d = half(p.gram);
-    gram.ldd = p.ldm;
-    gram.d_mat_stride = m_stride;
-    e = launch_ns_gemm(gram, stream, launches);
-    if (e != cudaSuccess) return e;
+      GemmArgs& g = gram[i];
+      g.M = g.N = p.m;
+      g.K = p.n;
+      g.mats = q.mats;
+      g.a = g.b = x;
+      g.a.k_major = g.b.k_major = !p.tall;
+      g.epilogue = kNsGram;
+      g.alpha = std::ldexp(1.0f, ea - 2 * ex);
+      g.d = half(p.gram);
+      g.ldd = p.ldm;
+      g.d_mat_stride = square.mat_stride;
 
-    GemmArgs poly{};
-    poly.M = poly.N = poly.K = p.m;
-    poly.mats = mats;
-    poly.a = poly.b = square;
-    poly.a.data = poly.b.data = half(p.gram);
-    poly.epilogue = kNsPoly;
-    poly.alpha = cfg.c * std::ldexp(1.0f, ep - 2 * ea);
-    poly.cfactor = cfg.b * std::ldexp(1.0f, ep - ea);
-    poly.c = half(p.gram);
-    poly.d = half(p.poly);
-    poly.ldd = p.ldm;
-    poly.d_mat_stride = m_stride;
-    e = launch_ns_gemm(poly, stream, launches);
-    if (e != cudaSuccess) return e;
+      GemmArgs& s = poly[i];
+      s.M = s.N = s.K = p.m;
+      s.mats = q.mats;
+      s.a = s.b = square;
+      s.a.data = s.b.data = half(p.gram);
+      s.epilogue = kNsPoly;
+      s.alpha = cfg.c * std::ldexp(1.0f, ep - 2 * ea);
+      s.cfactor = cfg.b * std::ldexp(1.0f, ep - ea);
+      s.c = half(p.gram);
+      s.d = half(p.poly);
+      s.ldd = p.ldm;
+      s.d_mat_stride = square.mat_stride;
 
-    GemmArgs apply{};
-    apply.M = p.rows;
-    apply.N = p.cols;
-    apply.K = p.m;
-    apply.mats = mats;
-    square.data = half(p.poly);
-    if (p.tall) {  // X' = a X + X P, P symmetric
-      apply.a = x;
-      apply.b = square;
-    } else {       // X' = a X + P X
-      apply.a = square;
-      apply.b = x;
-      apply.b.k_major = false;
+      GemmArgs& u = apply[i];
+      u.M = p.rows;
+      u.N = p.cols;
+      u.K = p.m;
+      u.mats = q.mats;
+      square.data = half(p.poly);
+      if (p.tall) {  // X' = a X + X P, P symmetric
+        u.a = x;
+        u.b = square;
+      } else {       // X' = a X + P X
+        u.a = square;
+        u.b = x;
+        u.b.k_major = false;
+      }
+      const int eo = last ? 0 : en;
+      u.alpha = std::ldexp(1.0f, eo - ex - ep);
+      u.cfactor = cfg.a * std::ldexp(1.0f, eo - ex);
+      u.c = x.data;
+      u.c_lo = low ? half(p.x_lo[from]) : nullptr;
+      u.ldd = p.ldx;
+      u.d_mat_stride = x.mat_stride;
+      if (last) {
+        u.epilogue = q.out.out ? kNsOut : kNsMuon;
+        u.out = q.out;
+      } else {
+        u.epilogue = kNsApply;
+        u.d = half(p.x_hi[to]);
+        u.d_lo = k + 1 < lows ? half(p.x_lo[to]) : nullptr;
+      }
     }
-    const int eo = last ? 0 : en;
-    apply.alpha = std::ldexp(1.0f, eo - ex - ep);
-    apply.cfactor = cfg.a * std::ldexp(1.0f, eo - ex);
-    apply.c = x.data;
-    apply.c_lo = low ? half(p.x_lo[from]) : nullptr;
-    apply.ldd = p.ldx;
-    apply.d_mat_stride = x_stride;
-    if (last) {
-      apply.epilogue = out.out ? kNsOut : kNsMuon;
-      apply.out = out;
-    } else {
-      apply.epilogue = kNsApply;
-      apply.d = half(p.x_hi[to]);
-      apply.d_lo = k + 1 < lows ? half(p.x_lo[to]) : nullptr;
+    for (const GemmArgs* phase : {gram, poly, apply}) {
+      const cudaError_t e = launch_ns_gemm(phase, count, stream, launches);
+      if (e != cudaSuccess) return e;
     }
-    e = launch_ns_gemm(apply, stream, launches);
-    if (e != cudaSuccess) return e;
     top = next;
     ex = en;
   }
@@ -380,14 +385,16 @@ zero_status zero_orthogonalize(const zero_ns_config* cfg, int64_t rows, int64_t 
   const zfs::NsPlan p = zfs::ns_plan(rows, cols, mats, false);
   char* ws = static_cast<char*>(workspace);
   for (int64_t first = 0; first < batch; first += mats) {
-    const int count = static_cast<int>(std::min<int64_t>(mats, batch - first));
-    const zfs::MatSource src = source(first);
-    zfs::NsOut o;
-    o.out = static_cast<uint16_t*>(out) + first * out_batch_stride;
-    o.row_stride = out_row_stride;
-    o.mat_stride = out_batch_stride;
-    cudaError_t e = zfs::launch_ns_norm(src, p, count, reinterpret_cast<double*>(ws + p.partials), s);
-    if (e == cudaSuccess) e = zfs::ns_run(p, *cfg, count, src, ws, o, s, &launches);
+    zfs::NsProblem q{};
+    q.plan = p;
+    q.mats = static_cast<int>(std::min<int64_t>(mats, batch - first));
+    q.src = source(first);
+    q.ws = ws;
+    q.out.out = static_cast<uint16_t*>(out) + first * out_batch_stride;
+    q.out.row_stride = out_row_stride;
+    q.out.mat_stride = out_batch_stride;
+    cudaError_t e = zfs::launch_ns_norm(q.src, p, q.mats, reinterpret_cast<double*>(ws + p.partials), s);
+    if (e == cudaSuccess) e = zfs::ns_run(&q, 1, *cfg, s, &launches);
     if (e != cudaSuccess) return failed(e);
   }
   return ZERO_OK;

@@ -99,9 +99,17 @@ struct zero_ctx {
     int64_t rows, cols;
     std::vector<int32_t> params;
   };
+  // Matrices of one shape that are worked on together, and the batch they
+  // belong to (thin ones have no batch).
+  struct MuonPart {
+    int32_t group, batch;
+    size_t first;
+    int mats;
+  };
   bool muon = false;
   zero_muon_config muon_cfg{};
   std::vector<MuonGroup> muon_groups;
+  std::vector<MuonPart> muon_parts;
   std::vector<std::pair<int64_t, int64_t>> muon_ranges;  // (offset, elements)
   char* muon_ws = nullptr;
 
@@ -455,7 +463,7 @@ double muon_scale(const zero_muon_config& c, int64_t rows, int64_t cols) {
 }
 
 // The Muon part of a step: thin matrices of all shapes in one launch per
-// cluster size, the others shape by shape — momentum and update, then the
+// cluster size, the others batch by batch — momentum and update, then the
 // orthogonalisation whose last product updates master and param16.
 zero_status muon_update(zero_ctx* ctx, cudaStream_t stream, int32_t* launches) {
   const zero_muon_config& mc = ctx->muon_cfg;
@@ -518,20 +526,25 @@ zero_status muon_update(zero_ctx* ctx, cudaStream_t stream, int32_t* launches) {
     if (e != cudaSuccess) return fail_cuda(ctx, "thin orthogonalisation launch", e);
   }
 
-  for (const zero_ctx::MuonGroup& group : ctx->muon_groups) {
-    if (std::min(group.rows, group.cols) <= zfs::kThin) continue;
-    const int64_t numel = group.rows * group.cols;
-    const int most = zfs::ns_mats(group.rows, group.cols, static_cast<long long>(group.params.size()));
-    const zfs::NsPlan p = zfs::ns_plan(group.rows, group.cols, most, true);
-    for (size_t first = 0; first < group.params.size(); first += most) {
-      const int mats = static_cast<int>(std::min<size_t>(most, group.params.size() - first));
+  for (size_t begin = 0, end = 0; begin < ctx->muon_parts.size(); begin = end) {
+    while (end < ctx->muon_parts.size() && ctx->muon_parts[end].batch == ctx->muon_parts[begin].batch) ++end;
+    zfs::NsProblem problems[zfs::kMaxProblems];
+    char* ws = ctx->muon_ws;
+    for (size_t i = begin; i < end; ++i) {
+      const zero_ctx::MuonPart& part = ctx->muon_parts[i];
+      const zero_ctx::MuonGroup& group = ctx->muon_groups[part.group];
+      const int64_t numel = group.rows * group.cols;
+      zfs::NsProblem& q = problems[i - begin];
+      q.plan = zfs::ns_plan(group.rows, group.cols, part.mats, true);
+      q.mats = part.mats;
+      q.ws = ws;
+      ws += q.plan.bytes;
       zfs::MomentumArgs a;
       std::memset(&a, 0, sizeof a);
-      zfs::NsOut out;
       a.n_ranks = N;
       a.grad_fp32 = grad_fp32;
       a.nesterov = mc.nesterov;
-      a.mats = mats;
+      a.mats = part.mats;
       a.inv_n = 1.0f / static_cast<float>(N);
       a.mu = mc.momentum;
       a.clip = clip;
@@ -539,36 +552,36 @@ zero_status muon_update(zero_ctx* ctx, cudaStream_t stream, int32_t* launches) {
       a.dev_t = ctx->cap_t;
       a.dev_steps = ctx->cap_steps;
       a.numel = numel;
-      a.chunks = p.chunks;
+      a.chunks = q.plan.chunks;
       a.total_padded = bound;
       a.mom = ctx->bufs.exp_avg;
-      a.update = reinterpret_cast<float*>(ctx->muon_ws + p.update);
-      a.partials = reinterpret_cast<double*>(ctx->muon_ws + p.partials);
+      a.update = reinterpret_cast<float*>(q.ws + q.plan.update);
+      a.partials = reinterpret_cast<double*>(q.ws + q.plan.partials);
       bool vec = numel % zfs::kVec == 0;
-      for (int k = 0; k < mats; ++k) {
-        const int32_t param = group.params[first + k];
-        a.offset[k] = out.offset[k] = ctx->param_offset[param];
+      for (int k = 0; k < part.mats; ++k) {
+        const int32_t param = group.params[part.first + k];
+        a.offset[k] = q.out.offset[k] = ctx->param_offset[param];
         vec = param_grads(ctx, param, a.g[k]) && vec && a.offset[k] % zfs::kVec == 0;
       }
-      cudaError_t e = zfs::launch_momentum(a, vec, stream);
+      const cudaError_t e = zfs::launch_momentum(a, vec, stream);
       if (e != cudaSuccess) return fail_cuda(ctx, "momentum kernel launch", e);
       ++*launches;
-      zfs::MatSource src{};
-      src.data = a.update;
-      src.fp32 = 1;
-      src.row_stride = group.cols;
-      src.mat_stride = numel;
-      src.vec_ok = group.cols % zfs::kVec == 0 ? 1 : 0;
-      out.master = ctx->bufs.master;
-      out.p16 = p16;
-      out.decay = decay;
-      out.step = static_cast<float>(static_cast<double>(mc.lr) * muon_scale(mc, group.rows, group.cols));
-      out.total_padded = bound;
-      out.dev_t = ctx->cap_t;
-      out.dev_steps = ctx->cap_steps;
-      e = zfs::ns_run(p, mc.ns, mats, src, ctx->muon_ws, out, stream, launches);
-      if (e != cudaSuccess) return fail_cuda(ctx, "orthogonalisation launch", e);
+      q.src = zfs::MatSource{};
+      q.src.data = a.update;
+      q.src.fp32 = 1;
+      q.src.row_stride = group.cols;
+      q.src.mat_stride = numel;
+      q.src.vec_ok = group.cols % zfs::kVec == 0 ? 1 : 0;
+      q.out.master = ctx->bufs.master;
+      q.out.p16 = p16;
+      q.out.decay = decay;
+      q.out.step = static_cast<float>(static_cast<double>(mc.lr) * muon_scale(mc, group.rows, group.cols));
+      q.out.total_padded = bound;
+      q.out.dev_t = ctx->cap_t;
+      q.out.dev_steps = ctx->cap_steps;
     }
+    const cudaError_t e = zfs::ns_run(problems, static_cast<int>(end - begin), mc.ns, stream, launches);
+    if (e != cudaSuccess) return fail_cuda(ctx, "orthogonalisation launch", e);
   }
   return ZERO_OK;
 }
@@ -1691,7 +1704,8 @@ namespace {
 // The shapes of a Muon configuration as groups of equal matrices; ENOMEM by exception.
 zero_status muon_plan(zero_ctx* ctx, const zero_muon_config* cfg, const int64_t* rows, const int64_t* cols,
                       int32_t n_params, std::vector<zero_ctx::MuonGroup>* groups,
-                      std::vector<std::pair<int64_t, int64_t>>* ranges, int64_t* bytes) {
+                      std::vector<zero_ctx::MuonPart>* parts, std::vector<std::pair<int64_t, int64_t>>* ranges,
+                      int64_t* bytes) {
   if (!cfg) return fail(ctx, ZERO_EINVAL, "config is NULL");
   if (n_params != ctx->n_params)
     return fail(ctx, ZERO_EINVAL, "%d shapes for %d parameters", n_params, ctx->n_params);
@@ -1724,7 +1738,8 @@ zero_status muon_plan(zero_ctx* ctx, const zero_muon_config* cfg, const int64_t*
     ranges->push_back({ctx->param_offset[p], r * c});
   }
   *bytes = 0;
-  int64_t thin = 0;
+  int64_t thin = 0, elements = 0, batch_bytes = 0;
+  int32_t batch = 0, shapes = 0;
   for (const zero_ctx::MuonGroup& g : *groups) {
     if (std::min(g.rows, g.cols) <= zfs::kThin) {
       // what one thin launch takes: matrices up to kThinWork, or one that needs more
@@ -1733,8 +1748,26 @@ zero_status muon_plan(zero_ctx* ctx, const zero_muon_config* cfg, const int64_t*
       *bytes = std::max<int64_t>(*bytes, each);
       continue;
     }
-    const int mats = zfs::ns_mats(g.rows, g.cols, static_cast<long long>(g.params.size()));
-    *bytes = std::max<int64_t>(*bytes, zfs::ns_plan(g.rows, g.cols, mats, true).bytes);
+    // batches of up to kNsBatch elements and kMaxProblems shapes
+    const int32_t index = static_cast<int32_t>(&g - groups->data());
+    for (size_t first = 0; first < g.params.size();) {
+      const int64_t numel = g.rows * g.cols;
+      int64_t room = (zfs::kNsBatch - elements) / numel;
+      if (room < 1 || shapes == zfs::kMaxProblems) {
+        if (shapes > 0) ++batch;
+        shapes = 0;
+        elements = 0;
+        batch_bytes = 0;
+        room = std::max<int64_t>(zfs::kNsBatch / numel, 1);
+      }
+      const int mats = static_cast<int>(std::min<int64_t>({room, zfs::kMaxMats, static_cast<int64_t>(g.params.size() - first)}));
+      parts->push_back({index, batch, first, mats});
+      first += mats;
+      ++shapes;
+      elements += mats * numel;
+      batch_bytes += zfs::ns_plan(g.rows, g.cols, mats, true).bytes;
+      *bytes = std::max(*bytes, batch_bytes);
+    }
   }
   *bytes = std::max<int64_t>(*bytes, std::min<int64_t>(thin, zfs::kThinWork));
   return ZERO_OK;
@@ -1748,8 +1781,9 @@ zero_status zero_muon_workspace_bytes(const zero_ctx* ctx, const zero_muon_confi
   zero_ctx* c = const_cast<zero_ctx*>(ctx);
   try {
     std::vector<zero_ctx::MuonGroup> groups;
+    std::vector<zero_ctx::MuonPart> parts;
     std::vector<std::pair<int64_t, int64_t>> ranges;
-    return muon_plan(c, cfg, rows, cols, n_params, &groups, &ranges, bytes);
+    return muon_plan(c, cfg, rows, cols, n_params, &groups, &parts, &ranges, bytes);
   } catch (const std::bad_alloc&) {
     return fail(c, ZERO_ENOMEM, "cannot allocate the shape tables");
   }
@@ -1764,9 +1798,10 @@ zero_status zero_enable_muon(zero_ctx* ctx, const zero_muon_config* cfg, const i
   if (ctx->phase == Phase::kStepped) return fail(ctx, ZERO_ESTATE, "a step awaits post_step");
   try {
     std::vector<zero_ctx::MuonGroup> groups;
+    std::vector<zero_ctx::MuonPart> parts;
     std::vector<std::pair<int64_t, int64_t>> ranges;
     int64_t need = 0;
-    st = muon_plan(ctx, cfg, rows, cols, n_params, &groups, &ranges, &need);
+    st = muon_plan(ctx, cfg, rows, cols, n_params, &groups, &parts, &ranges, &need);
     if (st != ZERO_OK) return st;
     if (need > 0) {
       int wdev = -1;
@@ -1779,6 +1814,7 @@ zero_status zero_enable_muon(zero_ctx* ctx, const zero_muon_config* cfg, const i
         return fail(ctx, ZERO_EINVAL, "workspace is not memory of the context's device");
     }
     ctx->muon_groups.swap(groups);
+    ctx->muon_parts.swap(parts);
     ctx->muon_ranges.swap(ranges);
   } catch (const std::bad_alloc&) {
     return fail(ctx, ZERO_ENOMEM, "cannot allocate the shape tables");
@@ -1795,6 +1831,7 @@ zero_status zero_disable_muon(zero_ctx* ctx) {
   if (ctx->phase == Phase::kStepped) return fail(ctx, ZERO_ESTATE, "a step awaits post_step");
   ctx->muon = false;
   ctx->muon_groups.clear();
+  ctx->muon_parts.clear();
   ctx->muon_ranges.clear();
   ctx->muon_ws = nullptr;
   return ZERO_OK;
