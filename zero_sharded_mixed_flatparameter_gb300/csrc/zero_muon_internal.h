@@ -63,6 +63,11 @@ bool ns_config_ok(const zero_ns_config& cfg, const char** why);
 constexpr int kMaxProblems = 12;
 // Elements of X that are worked on at once.
 constexpr long long kNsBatch = 1LL << 27;
+// A stack of as many is not put together with others: it fills the GPU (8 or
+// more rounds of tiles), and a launch of several stacks looks up each tile's
+// (the hidden-2048 model: 16.7 ms together, 16.2 apart; the hidden-1024 model,
+// whose stacks are smaller: 1.94 and 2.29).
+constexpr long long kNsAlone = 1LL << 26;
 struct NsProblem;
 // From every problem's source, with its norm partials in the workspace, to its
 // `out`: normalise, then the steps.

@@ -309,14 +309,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
     // ---- MMAs ---------------------------------------------------------------
     uint32_t stage = 0, parity = 0, acc = 0, acc_parity = 0;
     bool ok = true;
-    for (int t = first; t < total && ok; t += step) {
+    // What differs between stacks, looked up a tile ahead.
+    bool a_k = true, b_k = true;
+    int k_steps = 0;
+    auto look_up = [&](int t, bool& a, bool& b, int& steps) {
+      if (t >= total) return;
       const Problem& p = ka.p[locate<kEpi>(ka, t).problem];
-      const bool a_k = p.g.a.k_major, b_k = p.g.b.k_major;
-      const int k_steps = p.k_blocks;
+      a = p.g.a.k_major;
+      b = p.g.b.k_major;
+      steps = p.k_blocks;
+    };
+    look_up(first, a_k, b_k, k_steps);
+    for (int t = first; t < total && ok; t += step) {
       const uint32_t idesc = (1u << 4) | (a_k ? 0u : 1u << 15) | (b_k ? 0u : 1u << 16) |
                              (static_cast<uint32_t>(kBlockN >> 3) << 17) |
                              (static_cast<uint32_t>((kBlockM * kCtas) >> 4) << 24);
       const uint64_t step_a = a_k ? 32 >> 4 : 2048 >> 4, step_b = b_k ? 32 >> 4 : 2048 >> 4;
+      bool next_a = true, next_b = true;
+      int next_steps = 0;
       ok = wait_phase(tmem_empty + 8 * acc, acc_parity ^ 1, &gave_up);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -331,6 +341,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
         for (int k = 0; k < kBlockK / 16; ++k)
           mma<kCtas>(d, da + k * step_a, db + k * step_b, idesc, s > 0 || k > 0 ? 1 : 0);
         mma_commit<kCtas>(empty + 8 * stage);
+        if (s == 0) look_up(t + step, next_a, next_b, next_steps);
         if (++stage == kStages) {
           stage = 0;
           parity ^= 1;
@@ -338,6 +349,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
       }
       if (!ok) break;
       mma_commit<kCtas>(tmem_full + 8 * acc);
+      a_k = next_a;
+      b_k = next_b;
+      k_steps = next_steps;
       acc ^= 1;
       if (acc == 0) acc_parity ^= 1;
     }

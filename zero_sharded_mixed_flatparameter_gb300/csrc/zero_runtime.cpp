@@ -1740,6 +1740,7 @@ zero_status muon_plan(zero_ctx* ctx, const zero_muon_config* cfg, const int64_t*
   *bytes = 0;
   int64_t thin = 0, elements = 0, batch_bytes = 0;
   int32_t batch = 0, shapes = 0;
+  bool alone = false;
   for (const zero_ctx::MuonGroup& g : *groups) {
     if (std::min(g.rows, g.cols) <= zfs::kThin) {
       // what one thin launch takes: matrices up to kThinWork, or one that needs more
@@ -1748,12 +1749,13 @@ zero_status muon_plan(zero_ctx* ctx, const zero_muon_config* cfg, const int64_t*
       *bytes = std::max<int64_t>(*bytes, each);
       continue;
     }
-    // batches of up to kNsBatch elements and kMaxProblems shapes
+    // batches of up to kNsBatch elements and kMaxProblems shapes; kNsAlone by themselves
     const int32_t index = static_cast<int32_t>(&g - groups->data());
     for (size_t first = 0; first < g.params.size();) {
       const int64_t numel = g.rows * g.cols;
       int64_t room = (zfs::kNsBatch - elements) / numel;
-      if (room < 1 || shapes == zfs::kMaxProblems) {
+      const int64_t left = static_cast<int64_t>(g.params.size() - first) * numel;
+      if (room < 1 || shapes == zfs::kMaxProblems || left >= zfs::kNsAlone || alone) {
         if (shapes > 0) ++batch;
         shapes = 0;
         elements = 0;
@@ -1765,6 +1767,7 @@ zero_status muon_plan(zero_ctx* ctx, const zero_muon_config* cfg, const int64_t*
       first += mats;
       ++shapes;
       elements += mats * numel;
+      alone = mats * numel >= zfs::kNsAlone;
       batch_bytes += zfs::ns_plan(g.rows, g.cols, mats, true).bytes;
       *bytes = std::max(*bytes, batch_bytes);
     }
