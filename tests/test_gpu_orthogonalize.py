@@ -23,7 +23,8 @@ def normal(shape, seed, std=1e-3):
 
 SHAPES = [(1, 1), (1, 7), (7, 1), (2, 3), (16, 16), (33, 17), (64, 64), (64, 130), (127, 129), (128, 128), (130, 64),
           (128, 1024), (129, 257), (257, 129), (255, 640), (640, 255), (256, 2000), (2000, 256), (384, 384),
-          (513, 777), (777, 513), (1, 5000), (5000, 1), (8, 4096), (300, 4100)]
+          (513, 777), (777, 513), (1, 5000), (5000, 1), (8, 4096), (300, 4100), (150, 6000), (6000, 150), (130, 1100),
+          (400, 2100), (2100, 400), (640, 1500)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])

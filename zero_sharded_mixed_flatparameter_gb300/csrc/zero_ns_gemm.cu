@@ -514,6 +514,166 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
   if (warp == 9) tmem_free<kCtas>(tmem, kTmemColumns);
 }
 
+// ---- few tiles, many k ---------------------------------------------------------
+// A Gram matrix with so few tiles that most SMs would idle: a cluster of kSplit
+// CTAs per tile, each over its share of k.  Every CTA leaves its sums (fp32) in
+// its shared memory, and each joins a part of the tile from all of them, in
+// rank order.  One 512 x 2048 matrix: the product over 32 blocks of k takes 9.4
+// us in one CTA at the rate its operands come in; in eight, 2.3 us for 4 blocks
+// each, 0.7 to put the sums down and meet, 2.3 to join them.
+template <int kSplit>
+__global__ void __launch_bounds__(kGemmThreads, 1) ns_gram_split_kernel(const __grid_constant__ GemmKernelArgs<1> ka) {
+  constexpr int kUnits = 8 / kSplit;  // 32 x 64 parts of the tile that a CTA joins
+  constexpr uint32_t kTmemColumns = 128;
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 1];
+  __shared__ uint32_t tmem_base;
+  __shared__ int gave_up;
+  const Problem& p = ka.p[0];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t stages = (smem_u32(smem_raw) + 1023) & ~1023u, buffers = stages + kStages * kStageBytes;
+  const int rank = blockIdx.x % kSplit;
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tmem_full = empty + 8 * kStages;
+  if (threadIdx.x == 0) {
+    gave_up = 0;
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full + 8 * s, 1);
+      mbar_init(empty + 8 * s, 1);
+    }
+    mbar_init(tmem_full, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 8 && lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.a) : "memory");
+  if (warp == 9) tmem_alloc<1>(smem_u32(&tmem_base), kTmemColumns);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Tile at = locate<kNsGram>(ka, blockIdx.x / kSplit);
+  const int i0 = at.ti * kBlockM, j0 = at.tj * kBlockM;
+  const int begin = static_cast<int>(static_cast<long long>(p.k_blocks) * rank / kSplit);
+  const int end = static_cast<int>(static_cast<long long>(p.k_blocks) * (rank + 1) / kSplit);
+  const bool k_major = p.g.a.k_major;
+  if (warp == 8 && lane == 0) {
+    int issued = 0;
+    bool ok = true;
+    for (int s = begin; s < end && ok; ++s) {
+      const int stage = issued % kStages;
+      ok = wait_phase(empty + 8 * stage, issued / kStages & 1 ^ 1, &gave_up);
+      if (!ok) break;
+      const uint32_t to = stages + stage * kStageBytes, bar = full + 8 * stage;
+      mbar_expect_tx(bar, kStageBytes);
+      for (int operand = 0; operand < 2; ++operand) {
+        const int x = operand ? j0 : i0;
+        const uint32_t half = to + operand * kOperandBytes;
+        if (k_major) {
+          tma_load<1>(half, &p.a, s * kBlockK, x, at.mat, bar);
+        } else {
+          tma_load<1>(half, &p.a, x, s * kBlockK, at.mat, bar);
+          tma_load<1>(half + kOperandBytes / 2, &p.a, x + 64, s * kBlockK, at.mat, bar);
+        }
+      }
+      ++issued;
+    }
+    if (!ok) {  // a role gave up: the copies in flight land (bounded) before this CTA leaves
+      const unsigned long long t0 = global_ns();
+      for (bool landed = false; !landed && global_ns() - t0 < 50000000ull;) {
+        landed = true;
+        for (int s = 0; s < kStages; ++s) {
+          const int uses = (issued + kStages - 1 - s) / kStages;
+          if (uses > 0 && !mbar_try_wait(full + 8 * s, (uses - 1) & 1)) landed = false;
+        }
+      }
+    }
+  } else if (warp == 9 && lane == 0) {
+    const uint32_t idesc = (1u << 4) | (k_major ? 0u : 3u << 15) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+    const uint64_t step = k_major ? 32 >> 4 : 2048 >> 4;
+    bool ok = true;
+    for (int s = begin, n = 0; s < end; ++s, ++n) {
+      const int stage = n % kStages;
+      ok = wait_phase(full + 8 * stage, n / kStages & 1, &gave_up);
+      if (!ok) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t from = stages + stage * kStageBytes;
+      const uint64_t da = smem_desc(from, k_major, 8192), db = smem_desc(from + kOperandBytes, k_major, 8192);
+#pragma unroll
+      for (int k = 0; k < kBlockK / 16; ++k) mma<1>(tmem, da + k * step, db + k * step, idesc, n > 0 || k > 0 ? 1 : 0);
+      mma_commit<1>(empty + 8 * stage);
+    }
+    if (ok) mma_commit<1>(tmem_full);
+  } else if (warp < kEpilogueWarps) {
+    // the sums to shared memory, where no stage is in use any more
+    if (__all_sync(0xffffffffu, wait_phase(tmem_full, 0, &gave_up))) {
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t unit = stages + warp * 8192;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        float y[32];
+        tmem_load32(tmem + (((warp % 4) * 32) << 16) + warp / 4 * kChunk + 32 * q, y);
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+          sts16(unit + lane * 256 + (((8 * q + v) ^ (lane & 7)) << 4),
+                make_uint4(__float_as_uint(y[4 * v]), __float_as_uint(y[4 * v + 1]), __float_as_uint(y[4 * v + 2]),
+                           __float_as_uint(y[4 * v + 3])));
+      }
+    }
+  }
+  cluster_sync();
+  if (warp < kEpilogueWarps) {
+    const int mine = warp / kSplit, part = warp % kSplit, unit = rank * kUnits + mine;
+    const uint32_t buffer = buffers + mine * kBufferBytes;
+    const bool mirror = at.ti != at.tj;
+#pragma unroll
+    for (int q = 0; q < 16 / kSplit; ++q) {
+      // a load takes two whole rows, 512 bytes in a line: the lanes' 16 bytes from
+      // 32 rows took 6.6 us for the 64 KB
+      const int row = 2 * (part * (16 / kSplit) + q) + lane / 16, piece = lane % 16;
+      float y[4] = {};
+#pragma unroll
+      for (int r = 0; r < kSplit; ++r) {
+        const float4 v = lds16_cluster(map_rank(stages + unit * 8192 + row * 256 + ((piece ^ (row & 7)) << 4), r));
+        y[0] += v.x;
+        y[1] += v.y;
+        y[2] += v.z;
+        y[3] += v.w;
+      }
+      uint32_t h[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) h[k] = half2_bits(y[2 * k] * p.g.alpha, y[2 * k + 1] * p.g.alpha);
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(piece_at(buffer, row, piece / 2) + piece % 2 * 8), "r"(h[0]),
+                   "r"(h[1])
+                   : "memory");
+      if (mirror) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int c = 4 * piece + k;
+          sts2(buffer + kHalfBytes + c * 64 + (((row / 8) ^ ((c >> 1) & 3)) << 4) + row % 8 * 2,
+               static_cast<uint16_t>(h[k / 2] >> (16 * (k % 2))));
+        }
+      }
+    }
+    asm volatile("fence.proxy.async;" ::: "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
+    if (part == 0 && lane == 0) {
+      const int i = i0 + unit % 4 * 32, j = j0 + unit / 4 * kChunk;
+      if (i < p.g.M && j < p.g.N) {
+        tma_store(&p.d, buffer, j, i, at.mat);
+        if (mirror) tma_store(&p.d_mirror, buffer + kHalfBytes, i, j, at.mat);
+      }
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+  }
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while another reads its sums
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  if (warp == 9) tmem_free<1>(tmem, kTmemColumns);
+}
+
 // ---- host --------------------------------------------------------------------
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -556,6 +716,29 @@ bool encode_result(CUtensorMap* map, const uint16_t* data, const GemmArgs& g, cu
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Launches `kernel` in clusters of `cluster` CTAs, after the kernel before it
+// by programmatic serialization.
+template <typename Args>
+cudaError_t launch_clusters(void (*kernel)(const Args), const Args& ka, long long ctas, int cluster, cudaStream_t stream) {
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+  cfg.blockDim = dim3(kGemmThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, ka);
+}
+
 template <int kCtas, int kEpi, int kProblems>
 cudaError_t launch(GemmKernelArgs<kProblems>& ka, cudaStream_t stream) {
   const long long tile = 128 * kCtas;
@@ -572,25 +755,21 @@ cudaError_t launch(GemmKernelArgs<kProblems>& ka, cudaStream_t stream) {
     total += all * p.g.mats;
   }
   ka.total = static_cast<int>(total);
-  const auto kernel = ns_gemm_kernel<kCtas, kEpi, kProblems>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e != cudaSuccess) return e;
   const long long room = sm_count() / kCtas;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((total < room ? total : room) * kCtas));
-  cfg.blockDim = dim3(kGemmThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kCtas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, ka);
+  if constexpr (kCtas == 1 && kEpi == kNsGram && kProblems == 1) {
+    // Clusters that the GPU holds at once, each CTA with at least 4 blocks of k.
+    // (A cluster lies in one GPC: of 152 SMs, clusters of 8 reach 120 and of 4
+    // reach 144.)  The five steps without and with it, us: 512 x 8192 325, 173;
+    // 512 x 2048 165, 131; by four 896 x 2048 188, 156 and 512 x 1024 144, 127; by
+    // two 1280 x 5120 342, 292 and 1100 x 1200 181, 173.
+    const long long k_blocks = ka.p[0].k_blocks;
+    if (total * 8 <= room * 3 / 4 && k_blocks >= 32)
+      return launch_clusters(ns_gram_split_kernel<8>, ka, total * 8, 8, stream);
+    if (total * 4 <= room * 15 / 16 && k_blocks >= 16)
+      return launch_clusters(ns_gram_split_kernel<4>, ka, total * 4, 4, stream);
+    if (total * 2 <= room && k_blocks >= 16) return launch_clusters(ns_gram_split_kernel<2>, ka, total * 2, 2, stream);
+  }
+  return launch_clusters(ns_gemm_kernel<kCtas, kEpi, kProblems>, ka, (total < room ? total : room) * kCtas, kCtas, stream);
 }
 
 template <int kEpi, int kProblems>

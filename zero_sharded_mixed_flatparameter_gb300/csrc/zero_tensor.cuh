@@ -195,6 +195,15 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
   return v;
 }
+// From the shared memory of any CTA of the cluster.
+__device__ __forceinline__ float4 lds16_cluster(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ void sts2(uint32_t at, uint16_t v) {
   asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(v) : "memory");
 }
