@@ -725,7 +725,8 @@ zero_status zero_qk_norm_rope_backward(const zero_qk_config* cfg, int64_t tokens
                                        int64_t workspace_bytes, void* stream);
 
 /*
- * zero_kernel_timeouts — how many bounded waits of the tile-staged step
+ * zero_kernel_timeouts — how many bounded waits of the Newton-Schulz
+ * products (zero_orthogonalize, the Muon step) and of the tile-staged step
  * kernels (used for N = 1..4 or N >= 11 bf16 and N >= 7 fp32 replicas when a
  * launch covers at least 2^23 elements) gave up on the current device since
  * the library was loaded.  A wait gives up only if a

@@ -334,3 +334,13 @@ def test_llama_layer_shapes():
     step(fs, grads)
     check_matrices(fs, pl, shapes, before, reduced(grads))
     assert fs.kernel_timeouts() == timeouts
+
+
+def test_nothing_outside_the_buffers_is_written():
+    for widths in ([13, 57, 131, 9], [260, 300, 140], [30, 2000]):
+        pl, shapes = mlp(widths)
+        init = [si.normal_fp32(k, 0.02, 100 + p).cuda() for p, k in enumerate(pl.numel)]
+        fs = FlatStep(pl.numel, pl.unit, stage=1, n_ranks=3, init_params=init, guard=256, guard_value=7.0)
+        fs.enable_muon(shapes, lr=LR)
+        step(fs, grads_for(fs, pl, 3, "bf16", 1))
+        assert all((g == 7.0).all() for g in fs.guards())
