@@ -20,13 +20,19 @@
 // next one's products.  In a pair each CTA holds 128 of the 256 rows of A and
 // half of B's columns, and the first CTA issues for both.
 //
-// Each epilogue warp works by itself, 32 rows by 64 columns at a time through
-// its own 8 KB of shared memory: C (hi and lo) comes in by TMA while the
-// products still run, D goes out by TMA, both in whole 128-byte rows; the final
-// update crosses the buffer so that master and param16 are read and written in
-// whole rows too.  (Rows read and written by a thread each cost the L1 a line
-// per lane, 170 us for an update of 16 1024 x 2048 matrices whose products take
-// 60; one buffer for all warps costs a barrier and a store's latency per 64
+// Each epilogue warp works by itself, 32 rows by 64 columns at a time with its
+// own 8 KB of shared memory.  The products leave little of shared memory's
+// bandwidth (of 128 bytes a cycle, 64 go to loads and 64 to the MMAs at their
+// peak), so the epilogue spares it: C (hi and lo) comes in by cp.async while
+// the products still run, D goes out from registers, a 32-byte sector per lane
+// and access, and only the transposed half of a symmetric tile crosses the
+// buffer.  24 matrices of 1024 x 2048, five steps: 1054 us with C and D both by
+// TMA through the buffer (their copies queue behind the operands'), 1010 so,
+// 1152 with C read into registers as D is written.  The final update crosses
+// the buffer so that master and param16 are read and written in whole rows.
+// (Rows read and written by a thread each, 16 bytes at a time, cost the L1 a
+// line per lane: 170 us for an update of 16 1024 x 2048 matrices whose products
+// take 60; one buffer for all warps costs a barrier and a store's latency per 64
 // columns: 16 products of 1024 took 61 us, 33 without any epilogue.)
 
 #include <cuda.h>
@@ -56,8 +62,6 @@ constexpr uint32_t kSmemBytes = kStages * kStageBytes + kEpilogueWarps * kBuffer
 // One stack of equal matrices.
 struct Problem {
   CUtensorMap a, b;
-  CUtensorMap c, c_lo, d, d_lo;  // boxes of 64 x 32
-  CUtensorMap d_mirror;          // boxes of 32 x 64
   GemmArgs g;
   int first;                     // tile of the launch
   int tiles_m, tiles_n, tiles;   // tiles of one matrix
@@ -73,15 +77,45 @@ struct GemmKernelArgs {
   int problems, total;           // tiles of all
 };
 
-__device__ __forceinline__ void tma_store(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x),
-               "r"(y), "r"(z), "r"(src)
-               : "memory");
-}
 // ---- epilogue ----------------------------------------------------------------
 // Address of the 16-byte piece `piece` (of 8) of row r in a 32 x 64 half.
 __device__ __forceinline__ uint32_t piece_at(uint32_t half, int r, int piece) {
   return half + r * 128 + ((piece ^ (r & 7)) << 4);
+}
+
+// A 32 x 64 half from global memory: 16 bytes per lane, four whole rows of 128
+// bytes per access.  `rows` x `columns` of it lie inside the matrix, the rest
+// reads as zero; whole pieces are read, up to the pitch.
+__device__ __forceinline__ void load_half(uint32_t half, const uint16_t* from, long long pitch, long long rows,
+                                          long long columns, int lane) {
+  const int piece = lane % 8;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int r = 4 * k + lane / 8;
+    const bool inside = r < rows && 8 * piece < columns;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(piece_at(half, r, piece)),
+                 "l"(from + (inside ? r * pitch + 8 * piece : 0)), "r"(inside ? 16 : 0)
+                 : "memory");
+  }
+}
+
+// 16 fp16 of a row to global memory, a whole 32-byte sector per lane.
+__device__ __forceinline__ void store_sector(uint16_t* to, const uint32_t* h) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(h[0]), "r"(h[1]), "r"(h[2]),
+               "r"(h[3]), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7])
+               : "memory");
+}
+
+// Where column `lane` of row c of a transposed half (64 x 32, rows of 64 bytes)
+// lies, and rows 8 k to 8 k + 7 of it to global memory.
+__device__ __forceinline__ uint32_t mirror_at(uint32_t half, int c, int column) {
+  return half + c * 64 + (((column / 8) ^ ((c >> 1) & 3)) << 4) + column % 8 * 2;
+}
+__device__ __forceinline__ void store_mirror(uint32_t half, int k, uint16_t* to, long long pitch, long long rows,
+                                             long long columns, int lane) {
+  const int r = 8 * k + lane / 4, piece = lane % 4;
+  const uint4 v = lds16(mirror_at(half, r, 8 * piece));
+  if (r < rows && 8 * piece < columns) *reinterpret_cast<uint4*>(to + r * pitch + 8 * piece) = v;
 }
 
 // y[0..31] += factor * 32 fp16 of row r, from piece `first`.
@@ -201,14 +235,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
   constexpr int kBlockN = 128 * kCtas;  // columns of a tile; rows: kBlockM * kCtas
   constexpr uint32_t kTmemColumns = 2 * kBlockN;
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kStages + 4 + kEpilogueWarps];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
   __shared__ uint32_t tmem_base;
   __shared__ int gave_up;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const uint32_t stages = (smem_u32(smem_raw) + 1023) & ~1023u, buffers = stages + kStages * kStageBytes;
   const uint32_t rank = kCtas == 2 ? blockIdx.x % 2 : 0;
   const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tmem_full = empty + 8 * kStages,
-                 tmem_empty = tmem_full + 16, c_full = tmem_empty + 16;
+                 tmem_empty = tmem_full + 16;
   if (threadIdx.x == 0) {
     gave_up = 0;
     for (int s = 0; s < kStages; ++s) {
@@ -219,7 +253,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
       mbar_init(tmem_full + 8 * s, 1);
       mbar_init(tmem_empty + 8 * s, kEpilogueWarps * kCtas);
     }
-    for (int w = 0; w < kEpilogueWarps; ++w) mbar_init(c_full + 8 * w, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 8) {  // the maps are there before the first copy asks for them
@@ -242,6 +275,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
 
   if (warp == 8 && lane == 0 && !skip) {
     // ---- loads: both CTAs of a pair count on the first one's barrier ---------
+    asm volatile("fence.proxy.async;" ::: "memory");  // what plain stores of the kernel before wrote
     uint32_t stage = 0, parity = 0;
     long long issued = 0;
     bool ok = true;
@@ -358,29 +392,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
   } else if (warp < kEpilogueWarps && !skip) {
     // ---- epilogue -------------------------------------------------------------
     constexpr bool kHasC = kEpi != kNsGram;
-    constexpr bool kRows = kEpi == kNsOut || kEpi == kNsMuon;  // finished rows, not a TMA store
+    constexpr bool kRows = kEpi == kNsOut || kEpi == kNsMuon;  // finished rows
     constexpr bool kSymmetric = kEpi == kNsGram || kEpi == kNsPoly;
     constexpr int kChunks = kBlockN / kChunk / 2;  // per warp and tile
     const int quadrant = warp % 4, half = warp / 4;
-    const uint32_t buffer = buffers + warp * kBufferBytes, bar = c_full + 8 * warp;
+    const uint32_t buffer = buffers + warp * kBufferBytes;
     const bool has_lo = ka.p[0].g.c_lo != nullptr, makes_lo = ka.p[0].g.d_lo != nullptr;  // as of every stack
-    const uint32_t c_bytes = kHalfBytes * (has_lo ? 2 : 1);
-    // This warp's C of a tile's chunk into its buffer; one lane.
+    // This warp's C of a tile's chunk into its buffer.
     auto load_c = [&](int t, int chunk) {
       const Tile at = locate<kEpi>(ka, t);
-      const Problem& p = ka.p[at.problem];
-      const int i0 = at.ti * kBlockM * kCtas + rank * kBlockM + quadrant * 32;
-      const int j0 = at.tj * kBlockN + (2 * chunk + half) * kChunk;
-      mbar_expect_tx(bar, c_bytes);
-      tma_load<1>(buffer, &p.c, j0, i0, at.mat, bar);
-      if (has_lo) tma_load<1>(buffer + kHalfBytes, &p.c_lo, j0, i0, at.mat, bar);
+      const GemmArgs& g = ka.p[at.problem].g;
+      const long long i0 = at.ti * kBlockM * kCtas + rank * kBlockM + quadrant * 32;
+      const long long j0 = static_cast<long long>(at.tj) * kBlockN + (2 * chunk + half) * kChunk;
+      const bool some = i0 < g.M && j0 < g.N;
+      const long long from = some ? at.mat * g.d_mat_stride + i0 * g.ldd + j0 : 0, rows = some ? g.M - i0 : 0;
+      load_half(buffer, g.c + from, g.ldd, rows, g.N - j0, lane);
+      if (has_lo) load_half(buffer + kHalfBytes, g.c_lo + from, g.ldd, rows, g.N - j0, lane);
     };
-    uint32_t acc = 0, acc_parity = 0, c_parity = 0;
-    bool loaded = false;  // a C is on its way or here
-    if (kHasC && lane == 0 && first < total) {
-      load_c(first, 0);
-      loaded = true;
-    }
+    uint32_t acc = 0, acc_parity = 0;
+    if (kHasC && first < total) load_c(first, 0);
     bool ok = true;
     for (int t = first; t < total && ok; t += step) {
       const Tile at = locate<kEpi>(ka, t);
@@ -408,12 +438,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
         const int j0 = tj * kBlockN + (2 * chunk + half) * kChunk;
         const uint32_t from = tmem + acc * kBlockN + ((quadrant * 32) << 16) + (2 * chunk + half) * kChunk;
         if constexpr (kHasC) {
-          ok = __all_sync(0xffffffffu, wait_phase(bar, c_parity, &gave_up));
-          if (!ok) break;
-          c_parity ^= 1;
-          loaded = false;
-        } else {
-          if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          asm volatile("cp.async.wait_all;" ::: "memory");
           __syncwarp();
         }
         float y[2][32];
@@ -428,30 +453,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
           }
           if constexpr (!kRows) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const float* z = y[q] + 8 * v;
-              uint32_t h[4];
+            for (int v = 0; v < 2; ++v) {
+              const float* z = y[q] + 16 * v;
+              const int c0 = 32 * q + 16 * v;
+              const bool inside = i0 + lane < g.M && j0 + c0 < g.N;
+              const long long to = mat * g.d_mat_stride + (i0 + lane) * g.ldd + j0 + c0;
+              uint32_t h[8];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) h[k] = half2_bits(z[2 * k], z[2 * k + 1]);
-              sts16(piece_at(buffer, lane, 4 * q + v), make_uint4(h[0], h[1], h[2], h[3]));
+              for (int k = 0; k < 8; ++k) h[k] = half2_bits(z[2 * k], z[2 * k + 1]);
+              if (inside) store_sector(g.d + to, h);
               if constexpr (kEpi == kNsApply) {
                 if (makes_lo) {
-                  uint32_t l[4];
+                  uint32_t l[8];
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
+                  for (int k = 0; k < 8; ++k) {
                     const float2 hv = half2_values(h[k]);
                     l[k] = half2_bits(z[2 * k] - hv.x, z[2 * k + 1] - hv.y);
                   }
-                  sts16(piece_at(buffer + kHalfBytes, lane, 4 * q + v), make_uint4(l[0], l[1], l[2], l[3]));
+                  if (inside) store_sector(g.d_lo + to, l);
                 }
               } else if (mirror) {
                 // transposed, rows of 64 bytes: row c, column `lane`
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  const int c = 32 * q + 8 * v + k;
-                  sts2(buffer + kHalfBytes + c * 64 + (((lane / 8) ^ ((c >> 1) & 3)) << 4) + lane % 8 * 2,
-                       static_cast<uint16_t>(h[k / 2] >> (16 * (k % 2))));
-                }
+                for (int k = 0; k < 16; ++k)
+                  sts2(mirror_at(buffer + kHalfBytes, c0 + k, lane), static_cast<uint16_t>(h[k / 2] >> (16 * (k % 2))));
               }
             }
           }
@@ -473,38 +498,24 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
           }
           __syncwarp();
           if (i0 < g.M && j0 < g.N) store_rows<kEpi>(p, mat, buffer, i0, j0, lane);
+        } else {
+          __syncwarp();
+          if (mirror && i0 < g.M && j0 < g.N) {
+            uint16_t* to = g.d + mat * g.d_mat_stride + j0 * g.ldd + i0;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) store_mirror(buffer + kHalfBytes, k, to, g.ldd, g.M - j0, g.N - i0, lane);
+          }
         }
-        asm volatile("fence.proxy.async;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          if constexpr (!kRows) {
-            if (i0 < g.M && j0 < g.N) {  // what reaches over the matrix's end is cut by the copy
-              tma_store(&p.d, buffer, j0, i0, mat);
-              if (mirror) tma_store(&p.d_mirror, buffer + kHalfBytes, i0, j0, mat);
-              if (kEpi == kNsApply && makes_lo) tma_store(&p.d_lo, buffer + kHalfBytes, j0, i0, mat);
-            }
-            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-          }
-          const bool more = chunk + 1 < kChunks;
-          if (kHasC && (more || t + step < total)) {
-            if constexpr (!kRows) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            load_c(more ? t : t + step, more ? chunk + 1 : 0);
-            loaded = true;
-          }
+        __syncwarp();  // the buffer is free
+        if constexpr (kHasC) {
+          if (chunk + 1 < kChunks) load_c(t, chunk + 1);
+          else if (t + step < total) load_c(t + step, 0);
         }
       }
       acc ^= 1;
       if (acc == 0) acc_parity ^= 1;
     }
-    if (lane == 0) {
-      // nothing is in flight when this CTA leaves (a C that is not used only if a role gave up)
-      if (loaded) {
-        const unsigned long long t0 = global_ns();
-        while (!mbar_try_wait(bar, c_parity) && global_ns() - t0 < 50000000ull) {
-        }
-      }
-      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    }
+    asm volatile("cp.async.wait_all;" ::: "memory");  // (in flight only if a role gave up)
   }
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -557,6 +568,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gram_split_kernel(const __
   const int end = static_cast<int>(static_cast<long long>(p.k_blocks) * (rank + 1) / kSplit);
   const bool k_major = p.g.a.k_major;
   if (warp == 8 && lane == 0) {
+    asm volatile("fence.proxy.async;" ::: "memory");  // what plain stores of the kernel before wrote
     int issued = 0;
     bool ok = true;
     for (int s = begin; s < end && ok; ++s) {
@@ -625,6 +637,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gram_split_kernel(const __
     const int mine = warp / kSplit, part = warp % kSplit, unit = rank * kUnits + mine;
     const uint32_t buffer = buffers + mine * kBufferBytes;
     const bool mirror = at.ti != at.tj;
+    const long long i0 = at.ti * kBlockM + unit % 4 * 32, j0 = at.tj * kBlockM + unit / 4 * kChunk;
+    uint16_t* d = p.g.d + at.mat * p.g.d_mat_stride;
 #pragma unroll
     for (int q = 0; q < 16 / kSplit; ++q) {
       // a load takes two whole rows, 512 bytes in a line: the lanes' 16 bytes from
@@ -642,28 +656,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gram_split_kernel(const __
       uint32_t h[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) h[k] = half2_bits(y[2 * k] * p.g.alpha, y[2 * k + 1] * p.g.alpha);
-      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(piece_at(buffer, row, piece / 2) + piece % 2 * 8), "r"(h[0]),
-                   "r"(h[1])
-                   : "memory");
+      if (i0 + row < p.g.M && j0 + 4 * piece < p.g.N)
+        *reinterpret_cast<uint2*>(d + (i0 + row) * p.g.ldd + j0 + 4 * piece) = make_uint2(h[0], h[1]);
       if (mirror) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int c = 4 * piece + k;
-          sts2(buffer + kHalfBytes + c * 64 + (((row / 8) ^ ((c >> 1) & 3)) << 4) + row % 8 * 2,
-               static_cast<uint16_t>(h[k / 2] >> (16 * (k % 2))));
+          sts2(mirror_at(buffer, c, row), static_cast<uint16_t>(h[k / 2] >> (16 * (k % 2))));
         }
       }
     }
-    asm volatile("fence.proxy.async;" ::: "memory");
-    asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
-    if (part == 0 && lane == 0) {
-      const int i = i0 + unit % 4 * 32, j = j0 + unit / 4 * kChunk;
-      if (i < p.g.M && j < p.g.N) {
-        tma_store(&p.d, buffer, j, i, at.mat);
-        if (mirror) tma_store(&p.d_mirror, buffer + kHalfBytes, i, j, at.mat);
-      }
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (mirror) {
+      asm volatile("bar.sync 1, %0;" ::"n"(kEpilogueWarps * 32) : "memory");
+#pragma unroll
+      for (int k = part; k < 8; k += kSplit)
+        store_mirror(buffer, k, d + j0 * p.g.ldd + i0, p.g.ldd, p.g.M - j0, p.g.N - i0, lane);
     }
   }
   __syncwarp();
@@ -702,18 +709,6 @@ bool encode(CUtensorMap* map, const GemmOperand& o, long long mn, long long k, i
   return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(o.data), dims, strides, box, unit,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Map of C or D, M x N, in boxes of `columns` x `rows`.
-bool encode_result(CUtensorMap* map, const uint16_t* data, const GemmArgs& g, cuuint32_t columns, cuuint32_t rows) {
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(g.N), static_cast<cuuint64_t>(g.M),
-                              static_cast<cuuint64_t>(g.mats)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(g.ldd) * 2, static_cast<cuuint64_t>(g.d_mat_stride) * 2};
-  const cuuint32_t box[3] = {columns, rows, 1};
-  const cuuint32_t unit[3] = {1, 1, 1};
-  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<uint16_t*>(data), dims, strides, box, unit,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, columns == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Launches `kernel` in clusters of `cluster` CTAs, after the kernel before it
@@ -799,12 +794,7 @@ cudaError_t launch_tile(GemmKernelArgs<kProblems>& ka, cudaStream_t stream) {
 bool fill(const GemmArgs& g, Problem* p) {
   p->g = g;
   p->k_blocks = static_cast<int>((g.K + kBlockK - 1) / kBlockK);
-  const bool mirrored = g.epilogue == kNsGram || g.epilogue == kNsPoly;
-  if (!encode(&p->a, g.a, g.M, g.K, g.mats) || !encode(&p->b, g.b, g.N, g.K, g.mats) ||
-      (g.c && !encode_result(&p->c, g.c, g, 64, 32)) || (g.c_lo && !encode_result(&p->c_lo, g.c_lo, g, 64, 32)) ||
-      (g.d && !encode_result(&p->d, g.d, g, 64, 32)) || (g.d_lo && !encode_result(&p->d_lo, g.d_lo, g, 64, 32)) ||
-      (mirrored && !encode_result(&p->d_mirror, g.d, g, 32, 64)))
-    return false;
+  if (!encode(&p->a, g.a, g.M, g.K, g.mats) || !encode(&p->b, g.b, g.N, g.K, g.mats)) return false;
   p->vec_out = 0;
   if (g.epilogue == kNsOut) {
     p->vec_out = g.out.row_stride % 4 == 0 && g.out.mat_stride % 4 == 0 && reinterpret_cast<uintptr_t>(g.out.out) % 8 == 0;
@@ -840,7 +830,7 @@ cudaError_t launch_ns_gemm(const GemmArgs* g, int count, cudaStream_t stream, in
   std::call_once(g_encode_once, load_encode);
   if (!g_encode) return cudaErrorNotSupported;
   ++*launches;
-  // (a stack by itself spares the launch 20 KB of arguments)
+  // (a stack by itself spares the launch 12 KB of arguments)
   return count == 1 ? launch_problems<1>(g, count, stream) : launch_problems<kMaxProblems>(g, count, stream);
 }
 

@@ -110,8 +110,8 @@ NsPlan ns_plan(long long rows, long long cols, int mats, bool keep_update) {
   p.m = std::min(rows, cols);
   p.n = std::max(rows, cols);
   p.mats = mats;
-  p.ldx = round_up(cols, kVec);
-  p.ldm = round_up(p.m, kVec);
+  p.ldx = round_up(cols, 16);  // rows of whole 32-byte sectors
+  p.ldm = round_up(p.m, 16);
   p.chunks = (rows * cols + kNsChunk - 1) / kNsChunk;
   long long at = 0;
   auto take = [&](long long bytes) {
