@@ -13,6 +13,12 @@
 // are K-major, the others MN-major, and both are what the tensor cores read
 // from shared memory.
 //
+// Bound by the tensor cores where the matrices are large: eight 2048-wide
+// decoder layers run the last product of a step at 1.5 PFLOP/s (a 64-deep block
+// of a pair's tile in 666 cycles, 512 at the nominal rate); by latency where
+// they are small (a launch of one 512 x 2048 matrix takes 7.5 us, its products
+// 2.3).
+//
 // One persistent CTA (or pair of CTAs on one tile, kCtas = 2) per SM.  Warp
 // roles: 0-7 epilogue (TMEM quadrant warp % 4, column half warp / 4), 8 TMA
 // loads, 9 issues the MMAs.  kStages stages of a 128 x 64 block of A and of B

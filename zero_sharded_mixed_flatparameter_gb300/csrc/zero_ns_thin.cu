@@ -10,7 +10,10 @@
 // forms P by itself rather than wait for another.  More than one slice per CTA
 // (n > 1024) pass through global memory as ready images, once per step: a
 // slice's new columns go straight into the next step's Gram matrix.  In the
-// Muon step the momentum pass is the first thing the kernel does.
+// Muon step the momentum pass is the first thing the kernel does.  Five steps on
+// one 64 x 64 matrix take 20.6 us with the call, and a whole step of an MLP of
+// five layers up to 128 wide 51 us; with a launch per product one 128 x 512
+// matrix would be 17 of them at some 7 us.
 //
 // With tiny m the roundings of a step do not average out, and latency leaves
 // room, so products keep 22 bits here: every operand is an fp16 pair (hi + lo)

