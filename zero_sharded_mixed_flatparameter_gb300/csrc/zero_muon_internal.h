@@ -69,8 +69,9 @@ constexpr long long kNsBatch = 1LL << 27;
 // whose stacks are smaller: 1.94 and 2.29).
 constexpr long long kNsAlone = 1LL << 26;
 struct NsProblem;
-// From every problem's source, with its norm partials in the workspace, to its
-// `out`: normalise, then the steps.
+// A problem's source, with its norm partials in the workspace, normalised.
+cudaError_t ns_start(const NsProblem& q, const zero_ns_config& cfg, cudaStream_t stream, int* launches);
+// The steps of all problems, from there to their `out`.
 cudaError_t ns_run(const NsProblem* problems, int count, const zero_ns_config& cfg, cudaStream_t stream, int* launches);
 
 // ---- elementwise passes (zero_muon_kernels.cu) -----------------------------
@@ -95,6 +96,7 @@ struct ScaleArgs {
   MatSource src;
   long long rows, cols, ldx;
   int mats;
+  int per_thread;           // vectors
   long long chunks;
   const double* partials;
   double eps;
@@ -102,7 +104,7 @@ struct ScaleArgs {
   uint16_t* hi;             // fp16 bits, [mat][row][ldx]
   uint16_t* lo;             // or nullptr
 };
-cudaError_t launch_ns_scale(const ScaleArgs& a, cudaStream_t stream);
+cudaError_t launch_ns_scale(ScaleArgs a, cudaStream_t stream);
 
 // The Muon step's momentum pass over up to kMaxMats equal matrices of the flat
 // buffer: g = rank-order sum x 1/N x clip, mom = mu mom + g, update = nesterov
@@ -122,7 +124,9 @@ struct MomentumArgs {
   long long offset[kMaxMats];
   const void* g[kMaxMats][kMaxRanks];  // the matrix's gradients, replica by replica
 };
-cudaError_t launch_momentum(const MomentumArgs& a, bool vec, cudaStream_t stream);
+// `follows`: the launch before it on the stream is a normalisation that this
+// pass neither reads from nor writes to; the two may overlap.
+cudaError_t launch_momentum(const MomentumArgs& a, bool vec, bool follows, cudaStream_t stream);
 unsigned int muon_debug_failures();
 
 // ---- thin matrices (zero_ns_thin.cu) ---------------------------------------

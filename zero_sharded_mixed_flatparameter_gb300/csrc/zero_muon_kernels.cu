@@ -42,7 +42,10 @@ __device__ __forceinline__ double block_sum(float x) {
 // are kThreads vectors apart, so a warp reads contiguous runs.
 template <bool kFp32, bool kVecOk>
 __global__ void __launch_bounds__(kThreads) momentum_kernel(const __grid_constant__ MomentumArgs a) {
-  if (a.dev_t && *a.dev_t >= a.dev_steps) return;  // capturable: past the captured steps' table
+  if (a.dev_t && *a.dev_t >= a.dev_steps) {  // capturable: past the captured steps' table
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
   const int mat = blockIdx.y;
   const float clip = a.clip ? *a.clip : 1.0f;
   const long long base = a.offset[mat];
@@ -92,6 +95,9 @@ __global__ void __launch_bounds__(kThreads) momentum_kernel(const __grid_constan
   flush_nonfinite(a.nonfinite, nf);
   const double s = block_sum(sq);
   if (threadIdx.x == 0) a.partials[mat * a.chunks + blockIdx.x] = s;
+  // Launched beside the normalisation of another stack: what waits for this
+  // kernel may rely on that one too.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Eight consecutive elements of the stack in logical (row-major) order.
@@ -136,15 +142,19 @@ __global__ void __launch_bounds__(kThreads)
 
 // X0 = source / (norm + eps), stored as hi + lo: hi the nearest fp16 of the
 // scaled value, lo the nearest fp16 of what hi leaves (22 bits together).
-// Pads up to the pitch are zero.  Grid: (blocks over rows x pitch / 8, matrix).
+// Pads up to the pitch are zero.  Grid: (blocks over rows x pitch / 8, matrix),
+// from the end to the start: the update that the pass before wrote last is still
+// in L2.
 template <bool kFp32, bool kVecOk>
 __global__ void __launch_bounds__(kThreads) ns_scale_kernel(const __grid_constant__ ScaleArgs a) {
   __shared__ float inv_shared;
-  const int mat = blockIdx.y;
-  // The first product may take its place already; the partials and the source
-  // are read once the pass before has finished.
-  asm volatile("griddepcontrol.launch_dependents;");
+  const int mat = static_cast<int>(gridDim.y - 1 - blockIdx.y);
+  const long long block = gridDim.x - 1 - blockIdx.x;
+  // The partials and the source are read once the pass before has finished; the
+  // next kernel, another stack's momentum pass or the first product, may begin
+  // once the last of these CTAs has got here.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
   // every CTA sums the matrix's partials, in the same order
   double s = 0.0;
   if (threadIdx.x < 32) {
@@ -156,9 +166,12 @@ __global__ void __launch_bounds__(kThreads) ns_scale_kernel(const __grid_constan
   __syncthreads();
   const float inv = inv_shared;
   const long long vecs_per_row = a.ldx / kVec, total = a.rows * vecs_per_row;
-  for (long long v = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; v < total;
-       v += static_cast<long long>(gridDim.x) * kThreads) {
-    const long long row = v / vecs_per_row, col = (v - row * vecs_per_row) * kVec;
+  const bool small = total <= 0xffffffffLL;  // 32-bit divisions
+  for (int i = 0; i < a.per_thread; ++i) {
+    const long long v = (block * a.per_thread + i) * kThreads + threadIdx.x;
+    if (v >= total) break;
+    const long long row = small ? static_cast<uint32_t>(v) / static_cast<uint32_t>(vecs_per_row) : v / vecs_per_row;
+    const long long col = (v - row * vecs_per_row) * kVec;
     const long long left = a.cols - col;
     const int count = static_cast<int>(left < 0 ? 0 : left < kVec ? left : kVec);
     float x[kVec];
@@ -185,16 +198,22 @@ __global__ void __launch_bounds__(kThreads) ns_scale_kernel(const __grid_constan
 
 }  // namespace
 
-cudaError_t launch_momentum(const MomentumArgs& a, bool vec, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.mats));
+cudaError_t launch_momentum(const MomentumArgs& a, bool vec, bool follows, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.chunks), static_cast<unsigned>(a.mats));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = follows ? 1 : 0;
   if (a.grad_fp32) {
-    if (vec) momentum_kernel<true, true><<<grid, kThreads, 0, stream>>>(a);
-    else momentum_kernel<true, false><<<grid, kThreads, 0, stream>>>(a);
-  } else {
-    if (vec) momentum_kernel<false, true><<<grid, kThreads, 0, stream>>>(a);
-    else momentum_kernel<false, false><<<grid, kThreads, 0, stream>>>(a);
+    return vec ? cudaLaunchKernelEx(&cfg, momentum_kernel<true, true>, a)
+               : cudaLaunchKernelEx(&cfg, momentum_kernel<true, false>, a);
   }
-  return cudaGetLastError();
+  return vec ? cudaLaunchKernelEx(&cfg, momentum_kernel<false, true>, a)
+             : cudaLaunchKernelEx(&cfg, momentum_kernel<false, false>, a);
 }
 
 cudaError_t launch_ns_norm(const MatSource& s, const NsPlan& p, int mats, double* partials, cudaStream_t stream) {
@@ -210,11 +229,15 @@ cudaError_t launch_ns_norm(const MatSource& s, const NsPlan& p, int mats, double
   return cudaGetLastError();
 }
 
-cudaError_t launch_ns_scale(const ScaleArgs& a, cudaStream_t stream) {
-  const long long work = a.rows * (a.ldx / kVec);
-  const long long want = (work + kThreads - 1) / kThreads, most = 8LL * sm_count() / a.mats + 1;
+cudaError_t launch_ns_scale(ScaleArgs a, cudaStream_t stream) {
+  // What the GPU holds at once (8 CTAs per SM), or up to 16 vectors per thread,
+  // so that the sum of the partials counts little.
+  const long long work = a.rows * (a.ldx / kVec), room = 8LL * sm_count() * kThreads;
+  const long long per = (work * a.mats + room - 1) / room;
+  a.per_thread = static_cast<int>(per < 1 ? 1 : per < 16 ? per : 16);
+  const long long block = static_cast<long long>(kThreads) * a.per_thread;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(want < most ? want : most), static_cast<unsigned>(a.mats));
+  cfg.gridDim = dim3(static_cast<unsigned>((work + block - 1) / block), static_cast<unsigned>(a.mats));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

@@ -160,29 +160,28 @@ long long thin_mats(long long rows, long long cols, long long batch) {
   return std::max<long long>(1, std::min<long long>(batch, each > 0 ? kThinWork / each : 1 << 24));
 }
 
+cudaError_t ns_start(const NsProblem& q, const zero_ns_config& cfg, cudaStream_t stream, int* launches) {
+  ScaleArgs s{};
+  s.src = q.src;
+  s.rows = q.plan.rows;
+  s.cols = q.plan.cols;
+  s.ldx = q.plan.ldx;
+  s.mats = q.mats;
+  s.chunks = q.plan.chunks;
+  s.partials = reinterpret_cast<const double*>(q.ws + q.plan.partials);
+  s.eps = cfg.eps;
+  s.scale = std::ldexp(1.0f, scale_exponent(1.0));
+  s.hi = reinterpret_cast<uint16_t*>(q.ws + q.plan.x_hi[0]);
+  s.lo = low_steps(cfg.steps) > 0 ? reinterpret_cast<uint16_t*>(q.ws + q.plan.x_lo[0]) : nullptr;
+  ++*launches;
+  return launch_ns_scale(s, stream);
+}
+
 cudaError_t ns_run(const NsProblem* problems, int count, const zero_ns_config& cfg, cudaStream_t stream,
                    int* launches) {
   const int lows = low_steps(cfg.steps);
   double top = 1.0;  // bound of the spectral norm of X
   int ex = scale_exponent(top);
-  for (int i = 0; i < count; ++i) {
-    const NsProblem& q = problems[i];
-    ScaleArgs s{};
-    s.src = q.src;
-    s.rows = q.plan.rows;
-    s.cols = q.plan.cols;
-    s.ldx = q.plan.ldx;
-    s.mats = q.mats;
-    s.chunks = q.plan.chunks;
-    s.partials = reinterpret_cast<const double*>(q.ws + q.plan.partials);
-    s.eps = cfg.eps;
-    s.scale = std::ldexp(1.0f, ex);
-    s.hi = reinterpret_cast<uint16_t*>(q.ws + q.plan.x_hi[0]);
-    s.lo = lows > 0 ? reinterpret_cast<uint16_t*>(q.ws + q.plan.x_lo[0]) : nullptr;
-    const cudaError_t e = launch_ns_scale(s, stream);
-    if (e != cudaSuccess) return e;
-    ++*launches;
-  }
   for (int k = 0; k < cfg.steps; ++k) {
     const int from = k % 2, to = 1 - from;
     const bool low = k < lows, last = k + 1 == cfg.steps;
@@ -394,6 +393,7 @@ zero_status zero_orthogonalize(const zero_ns_config* cfg, int64_t rows, int64_t 
     q.out.row_stride = out_row_stride;
     q.out.mat_stride = out_batch_stride;
     cudaError_t e = zfs::launch_ns_norm(q.src, p, q.mats, reinterpret_cast<double*>(ws + p.partials), s);
+    if (e == cudaSuccess) e = zfs::ns_start(q, *cfg, s, &launches);
     if (e == cudaSuccess) e = zfs::ns_run(&q, 1, *cfg, s, &launches);
     if (e != cudaSuccess) return failed(e);
   }

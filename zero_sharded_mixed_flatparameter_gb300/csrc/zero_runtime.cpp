@@ -563,7 +563,7 @@ zero_status muon_update(zero_ctx* ctx, cudaStream_t stream, int32_t* launches) {
         a.offset[k] = q.out.offset[k] = ctx->param_offset[param];
         vec = param_grads(ctx, param, a.g[k]) && vec && a.offset[k] % zfs::kVec == 0;
       }
-      const cudaError_t e = zfs::launch_momentum(a, vec, stream);
+      cudaError_t e = zfs::launch_momentum(a, vec, i > begin, stream);
       if (e != cudaSuccess) return fail_cuda(ctx, "momentum kernel launch", e);
       ++*launches;
       q.src = zfs::MatSource{};
@@ -579,6 +579,8 @@ zero_status muon_update(zero_ctx* ctx, cudaStream_t stream, int32_t* launches) {
       q.out.total_padded = bound;
       q.out.dev_t = ctx->cap_t;
       q.out.dev_steps = ctx->cap_steps;
+      e = zfs::ns_start(q, mc.ns, stream, launches);
+      if (e != cudaSuccess) return fail_cuda(ctx, "normalisation launch", e);
     }
     const cudaError_t e = zfs::ns_run(problems, static_cast<int>(end - begin), mc.ns, stream, launches);
     if (e != cudaSuccess) return fail_cuda(ctx, "orthogonalisation launch", e);
