@@ -344,3 +344,31 @@ def test_nothing_outside_the_buffers_is_written():
         fs.enable_muon(shapes, lr=LR)
         step(fs, grads_for(fs, pl, 3, "bf16", 1))
         assert all((g == 7.0).all() for g in fs.guards())
+
+
+def test_offsets_beyond_32_bits():
+    # matrices of every path behind 2^31 elements of another parameter
+    head, mats = 2 ** 31 + 40, [(64, 48), (300, 200), (200, 320), (1, 9)]
+    numel = [head] + [r * c for r, c in mats]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    init = [torch.zeros(head, device="cuda")]
+    init += [torch.empty(k, device="cuda").normal_(0.0, 0.02, generator=g) for k in numel[1:]]
+    fs = FlatStep(numel, [0] * len(numel), stage=1, n_ranks=1, lr=1e-3, adamw=True, init_params=init)
+    del init
+    fs.enable_muon([None] + mats, lr=LR, momentum=MU, weight_decay=WD)
+    grad = torch.zeros(fs.padded, dtype=torch.bfloat16, device="cuda")
+    grad[head:].normal_(0.0, 1e-2, generator=g)
+    w0 = fs.master[head:].cpu()
+    step(fs, [grad])
+    w1, p16 = fs.master[head:].cpu(), fs.param16[head:].cpu()
+    assert not fs.master[:head].any() and not fs.exp_avg[:head].any()
+    for p, s in enumerate(mats):
+        o = fs.param_offset(1 + p)
+        at = slice(o - head, o - head + numel[1 + p])
+        mine = grad[o:o + numel[1 + p]].float().cpu()
+        assert torch.equal(fs.exp_avg[o:o + numel[1 + p]].cpu(), mine)
+        want = orthogonalized64(mine.view(s))
+        update = (w0[at].double() * (1 - LR * WD) - w1[at].double()) / (LR * muon_scale(*s, "rms"))
+        slack = float(w0[at].abs().max()) * 2.0 ** -22 / (LR * muon_scale(*s, "rms")) * np.sqrt(want.numel()) / float(want.norm())
+        assert relative(update.view(s), want) <= NS_TOL + slack, s
+        assert torch.equal(p16[at], w1[at].bfloat16())

@@ -50,6 +50,15 @@ def test_thin_matrices_are_nearly_exact(rows, cols, rank):
     assert relative(ops.orthogonalize(x.cuda()), want) <= 2.5e-3
 
 
+@pytest.mark.parametrize("batch,rows,cols", [(2112, 1040, 1010), (250000, 64, 136)])
+def test_stack_of_more_than_2_to_the_31_elements(batch, rows, cols):
+    x = normal((rows, cols), batch).cuda()
+    got = ops.orthogonalize(x.expand(batch, rows, cols))
+    assert got.numel() > 2 ** 31
+    assert relative(got[batch - 1], orthogonalized64(x.cpu())) <= NS_TOL
+    assert all(torch.equal(part, got[:1].expand_as(part)) for part in got.split(batch // 16 + 1))
+
+
 @pytest.mark.parametrize("batch,rows,cols", [(3, 65, 40), (5, 40, 65), (2, 300, 520), (9, 128, 128), (70, 24, 9),
                                              (70, 130, 140)])
 def test_stack(batch, rows, cols):
