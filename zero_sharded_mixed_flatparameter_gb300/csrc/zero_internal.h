@@ -63,6 +63,7 @@ struct StepArgs {
   long long dev_steps;
   unsigned long long* nonfinite;  // caller's counter of non-finite reduced
                                   // gradients, or nullptr (not counted)
+  int overlap;             // the Muon part follows: its first launch may begin at once (vector kernel)
   int inject_missing_copy; // test hook: the tile-staged kernel announces the
                            // launch's first tile but issues none of its copies
   Seg seg[kMaxSegs];

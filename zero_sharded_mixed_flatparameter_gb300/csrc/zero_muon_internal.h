@@ -124,8 +124,7 @@ struct MomentumArgs {
   long long offset[kMaxMats];
   const void* g[kMaxMats][kMaxRanks];  // the matrix's gradients, replica by replica
 };
-// `follows`: the launch before it on the stream is a normalisation that this
-// pass neither reads from nor writes to; the two may overlap.
+// `follows`: as with launch_ns_thin.
 cudaError_t launch_momentum(const MomentumArgs& a, bool vec, bool follows, cudaStream_t stream);
 unsigned int muon_debug_failures();
 
@@ -178,7 +177,10 @@ int thin_ctas(long long rows, long long cols);
 long long thin_work(long long rows, long long cols, bool muon);
 // Fills the scales and coefficients of `cfg`.
 void thin_scales(const zero_ns_config& cfg, ThinArgs* a);
-cudaError_t launch_ns_thin(const ThinArgs& a, bool muon, int ctas, long long mats, cudaStream_t stream, int* launches);
+// `follows` (Muon): the launch before it belongs to the same step, and this one
+// neither reads what that one writes nor writes what it uses; they may overlap.
+cudaError_t launch_ns_thin(const ThinArgs& a, bool muon, bool follows, int ctas, long long mats, cudaStream_t stream,
+                           int* launches);
 unsigned int thin_debug_failures();
 unsigned int thin_timeouts();
 

@@ -8,7 +8,8 @@
 // two vectors of every replica in flight per thread.  Over 486 M elements of 8
 // bf16 replicas the momentum pass (28 bytes per element) takes 1.95 ms, 7.0
 // TB/s, and the normalisation (8 bytes) 0.66 ms, 5.9 TB/s; 71 M elements in
-// four launches 346 us (5.7 TB/s) and 102 us (5.5).
+// four launches each, one after another, 346 us (5.7 TB/s) and 102 us (5.5); they
+// overlap in a step (zero_runtime.cpp), which takes 40 us less for it.
 
 #include <cuda_fp16.h>
 

@@ -11,8 +11,8 @@
 // (n > 1024) pass through global memory as ready images, once per step: a
 // slice's new columns go straight into the next step's Gram matrix.  In the
 // Muon step the momentum pass is the first thing the kernel does.  Five steps on
-// one 64 x 64 matrix take 20.6 us with the call, and a whole step of an MLP of
-// five layers up to 128 wide 51 us; with a launch per product one 128 x 512
+// one 64 x 64 matrix take 21 us with the call, and a whole step of an MLP of
+// five layers up to 128 wide 43 us; with a launch per product one 128 x 512
 // matrix would be 17 of them at some 7 us.
 //
 // With tiny m the roundings of a step do not average out, and latency leaves
@@ -313,7 +313,11 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
   extern __shared__ unsigned char smem_raw[];
   __shared__ Shared sh;
   if constexpr (kMuon) {
-    if (a.dev_t && *a.dev_t >= a.dev_steps) return;  // the same for the whole grid
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (a.dev_t && *a.dev_t >= a.dev_steps) {  // the same for the whole grid
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      return;
+    }
   }
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const uint32_t rank = kCtas > 1 ? cluster_rank() : 0;
@@ -650,10 +654,13 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
   if (many && tid == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   // No CTA leaves while another may read its shared memory: the last such read
   // lies before the barrier behind the last joined Gram matrix.
+  // Launched beside a kernel of the same step: what waits for this one may rely
+  // on that one too.
+  if constexpr (kMuon) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int kCtas, bool kMuon, bool kFp32>
-cudaError_t launch(const ThinArgs& a, long long mats, cudaStream_t stream) {
+cudaError_t launch(const ThinArgs& a, long long mats, bool follows, cudaStream_t stream) {
   const cudaError_t e = cudaFuncSetAttribute(ns_thin_kernel<kCtas, kMuon, kFp32>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -662,23 +669,25 @@ cudaError_t launch(const ThinArgs& a, long long mats, cudaStream_t stream) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = kCtas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = follows ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, ns_thin_kernel<kCtas, kMuon, kFp32>, a);
 }
 
 template <bool kMuon, bool kFp32>
-cudaError_t launch_ctas(const ThinArgs& a, int ctas, long long mats, cudaStream_t stream) {
+cudaError_t launch_ctas(const ThinArgs& a, int ctas, long long mats, bool follows, cudaStream_t stream) {
   switch (ctas) {
-    case 1: return launch<1, kMuon, kFp32>(a, mats, stream);
-    case 2: return launch<2, kMuon, kFp32>(a, mats, stream);
-    case 4: return launch<4, kMuon, kFp32>(a, mats, stream);
-    default: return launch<8, kMuon, kFp32>(a, mats, stream);
+    case 1: return launch<1, kMuon, kFp32>(a, mats, follows, stream);
+    case 2: return launch<2, kMuon, kFp32>(a, mats, follows, stream);
+    case 4: return launch<4, kMuon, kFp32>(a, mats, follows, stream);
+    default: return launch<8, kMuon, kFp32>(a, mats, follows, stream);
   }
 }
 
@@ -700,10 +709,12 @@ long long thin_work(long long rows, long long cols, bool muon) {
   return all * 512 * mk + (muon ? (m * n * 4 + 255) / 256 * 256 : 0);
 }
 
-cudaError_t launch_ns_thin(const ThinArgs& a, bool muon, int ctas, long long mats, cudaStream_t stream, int* launches) {
+cudaError_t launch_ns_thin(const ThinArgs& a, bool muon, bool follows, int ctas, long long mats, cudaStream_t stream,
+                           int* launches) {
   ++*launches;
-  if (muon) return launch_ctas<true, true>(a, ctas, mats, stream);
-  return a.src.fp32 ? launch_ctas<false, true>(a, ctas, mats, stream) : launch_ctas<false, false>(a, ctas, mats, stream);
+  if (muon) return launch_ctas<true, true>(a, ctas, mats, follows, stream);
+  return a.src.fp32 ? launch_ctas<false, true>(a, ctas, mats, false, stream)
+                    : launch_ctas<false, false>(a, ctas, mats, false, stream);
 }
 
 unsigned int thin_timeouts() {

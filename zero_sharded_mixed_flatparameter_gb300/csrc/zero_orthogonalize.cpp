@@ -374,7 +374,7 @@ zero_status zero_orthogonalize(const zero_ns_config* cfg, int64_t rows, int64_t 
     for (int64_t first = 0; first < batch; first += most) {
       a.src = source(first);
       a.out = static_cast<uint16_t*>(out) + first * out_batch_stride;
-      const cudaError_t e = zfs::launch_ns_thin(a, false, zfs::thin_ctas(rows, cols), std::min(most, batch - first), s,
+      const cudaError_t e = zfs::launch_ns_thin(a, false, false, zfs::thin_ctas(rows, cols), std::min(most, batch - first), s,
                                                 &launches);
       if (e != cudaSuccess) return failed(e);
     }

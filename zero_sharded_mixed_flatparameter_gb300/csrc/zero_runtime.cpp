@@ -396,6 +396,7 @@ zero_status launch_batches(zero_ctx* ctx, const std::vector<PlannedSeg>& segs, b
     a.dev_t = ctx->cap_t;
     a.dev_bias = ctx->cap_bias;
     a.dev_steps = ctx->cap_steps;
+    a.overlap = ctx->muon ? 1 : 0;
     if (ctx->inject == ZERO_INJECT_MISSING_COPY && vec && !kept) {
       a.inject_missing_copy = 1;
       ctx->inject = 0;
@@ -474,6 +475,12 @@ zero_status muon_update(zero_ctx* ctx, cudaStream_t stream, int32_t* launches) {
   const float decay = static_cast<float>(1.0 - static_cast<double>(mc.lr) * static_cast<double>(mc.weight_decay));
   uint16_t* p16 = static_cast<uint16_t*>(ctx->bufs.param16);
 
+  // Each launch of a step works on elements of its own, so it may begin beside
+  // the one before (AdamW's, or another cluster size's) unless both need the
+  // workspace.  Each waits for that one at its end, and the first of a step is an
+  // ordinary launch: all that came before the step is done.  (Toy MLP, cold
+  // caches: 65 us one after another, 57 so.)
+  bool workspace_used = false;
   for (int ctas = 1; ctas <= 8; ctas *= 2) {
     zfs::ThinArgs a;
     std::memset(&a, 0, sizeof a);
@@ -497,7 +504,9 @@ zero_status muon_update(zero_ctx* ctx, cudaStream_t stream, int32_t* launches) {
     int64_t at = 0;
     auto flush = [&]() {
       if (mats == 0) return cudaSuccess;
-      const cudaError_t e = zfs::launch_ns_thin(a, true, ctas, mats, stream, launches);
+      const bool follows = *launches > 0 && !(at > 0 && workspace_used);
+      const cudaError_t e = zfs::launch_ns_thin(a, true, follows, ctas, mats, stream, launches);
+      workspace_used = workspace_used || at > 0;
       mats = 0;
       at = 0;
       std::memset(a.vec, 0, sizeof a.vec);
@@ -563,7 +572,8 @@ zero_status muon_update(zero_ctx* ctx, cudaStream_t stream, int32_t* launches) {
         a.offset[k] = q.out.offset[k] = ctx->param_offset[param];
         vec = param_grads(ctx, param, a.g[k]) && vec && a.offset[k] % zfs::kVec == 0;
       }
-      cudaError_t e = zfs::launch_momentum(a, vec, i > begin, stream);
+      const bool follows = i > begin || (begin == 0 && *launches > 0 && !workspace_used);
+      cudaError_t e = zfs::launch_momentum(a, vec, follows, stream);
       if (e != cudaSuccess) return fail_cuda(ctx, "momentum kernel launch", e);
       ++*launches;
       q.src = zfs::MatSource{};

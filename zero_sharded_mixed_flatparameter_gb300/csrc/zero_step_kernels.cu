@@ -157,6 +157,7 @@ template <int N, bool kFp32, bool kDevBias>
 __global__ void __launch_bounds__(kStepThreads, 1) step_vec_kernel(const __grid_constant__ StepArgs a) {
   const long long tid = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  if (a.overlap) asm volatile("griddepcontrol.launch_dependents;");
   float bc1, bc2;
   if (!step_bias<kDevBias>(a, &bc1, &bc2)) return;
   // Clip coefficient of the global norm (x 1 is exact when not clipping).
