@@ -65,7 +65,7 @@ constexpr int kMaxProblems = 12;
 constexpr long long kNsBatch = 1LL << 27;
 // A stack of as many is not put together with others: it fills the GPU (8 or
 // more rounds of tiles), and a launch of several stacks looks up each tile's
-// (the hidden-2048 model: 16.7 ms together, 16.2 apart; the hidden-1024 model,
+// (the hidden-2048 model: 15.9 ms together, 15.5 apart; the hidden-1024 model,
 // whose stacks are smaller: 1.94 and 2.29).
 constexpr long long kNsAlone = 1LL << 26;
 struct NsProblem;
