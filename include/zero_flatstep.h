@@ -575,7 +575,8 @@ zero_status zero_orthogonalize_workspace_bytes(const zero_ns_config* cfg, int64_
  *  out        device bf16 matrices, likewise; must not overlap `in`
  *  workspace  device scratch, 256-byte aligned, kept until the work on
  *             `stream` has completed
- * An all-zero matrix gives zeros; one with an inf or NaN gives NaN.
+ * An all-zero matrix gives zeros (with eps = 0, too); one with an inf or NaN
+ * gives NaN.
  * rows, cols or batch of 0: ZERO_OK without device work.
  * Errors: ZERO_EINVAL (config, sizes, strides, pointers, workspace);
  * ZERO_ECUDA.

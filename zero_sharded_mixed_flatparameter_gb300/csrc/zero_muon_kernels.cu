@@ -163,7 +163,10 @@ __global__ void __launch_bounds__(kThreads) ns_scale_kernel(const __grid_constan
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_down_sync(0xffffffffu, s, o);
   }
-  if (threadIdx.x == 0) inv_shared = static_cast<float>(1.0 / (sqrt(s) + a.eps));
+  if (threadIdx.x == 0) {
+    const double d = sqrt(s) + a.eps;
+    inv_shared = d == 0.0 ? 0.0f : static_cast<float>(1.0 / d);  // a zero matrix stays one without eps, too
+  }
   __syncthreads();
   const float inv = inv_shared;
   const long long vecs_per_row = a.ldx / kVec, total = a.rows * vecs_per_row;

@@ -462,7 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
     sq = 0.0f;
     for (int r = 0; r < kCtas; ++r) sq += ld_cluster(map_rank(smem_u32(&sh.sum), r));
   }
-  const float scale = 1.0f / (sqrtf(sq) + a.eps) * a.step_factors[0].x;
+  const float norm = sqrtf(sq) + a.eps;
+  const float scale = norm == 0.0f ? 0.0f : 1.0f / norm * a.step_factors[0].x;  // a zero matrix stays one
 
   // ---- X0 and its Gram matrix ---------------------------------------------------
   bool ok = alive;
