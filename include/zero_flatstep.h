@@ -575,8 +575,9 @@ zero_status zero_orthogonalize_workspace_bytes(const zero_ns_config* cfg, int64_
  *  out        device bf16 matrices, likewise; must not overlap `in`
  *  workspace  device scratch, 256-byte aligned, kept until the work on
  *             `stream` has completed
- * An all-zero matrix gives zeros (with eps = 0, too); one with an inf or NaN
- * gives NaN.
+ * Entries may have any finite size: the norm is summed so that their squares
+ * stay in range.  An all-zero matrix gives zeros (with eps = 0, too); one with
+ * an inf or NaN gives NaN.
  * rows, cols or batch of 0: ZERO_OK without device work.
  * Errors: ZERO_EINVAL (config, sizes, strides, pointers, workspace);
  * ZERO_ECUDA.

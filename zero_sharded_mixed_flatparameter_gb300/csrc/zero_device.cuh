@@ -44,6 +44,12 @@ __device__ __forceinline__ float4 ld_stream_f4(const float* p) { return __ldcs(r
 __device__ __forceinline__ void st_stream_f4(float* p, float4 x) { __stcs(reinterpret_cast<float4*>(p), x); }
 __device__ __forceinline__ void st_stream(void* p, uint4 x) { __stcs(reinterpret_cast<uint4*>(p), x); }
 
+// A sum of squares in fp32 is taken as it is within these bounds.  Outside, or
+// when it is NaN, the squares of finite entries may have over- or underflowed,
+// and it is formed again from the entries times a power of two, kNormDown or
+// kNormUp (every finite fp32 value, up to 2^37 of them, then stays in range).
+constexpr float kNormLow = 0x1p-80f, kNormHigh = 0x1p100f, kNormUp = 0x1p90f, kNormDown = 0x1p-90f;
+
 // Eight consecutive values from element `at` of a bf16 or fp32 array; kVecOk:
 // the address is 16-byte aligned and all eight exist.
 template <bool kFp32, bool kVecOk>

@@ -4,7 +4,7 @@
 //
 // All are one pass over memory-resident data and bound by it; the norm is
 // summed per chunk of kNsChunk elements of a matrix, in fp32 over the elements
-// of a warp and in fp64 above, each in a fixed order.  A CTA per chunk keeps
+// of a warp and in fp64 above, each in a fixed order, whatever the entries' size.  A CTA per chunk keeps
 // two vectors of every replica in flight per thread.  Over 486 M elements of 8
 // bf16 replicas the momentum pass (28 bytes per element) takes 1.95 ms, 7.0
 // TB/s, and the normalisation (8 bytes) 0.66 ms, 5.9 TB/s; 71 M elements in
@@ -23,18 +23,53 @@ constexpr int kThreads = 256;
 constexpr int kPerThread = static_cast<int>(kNsChunk) / kThreads;  // elements per thread and chunk
 static_assert(kPerThread % kVec == 0, "whole vectors per thread");
 
-// Sum over the CTA in a fixed order, fp32 within a warp and fp64 above (by one
-// thread: the GPU has few fp64 units); valid in thread 0.
-__device__ __forceinline__ double block_sum(float x) {
+// A thread's sum of squares.  Vectors whose squares leave fp32's range are summed
+// times a power of two, of which one sum is enough: beside large ones (odd < 0:
+// minus the sum of (x kNormDown)^2) small ones (odd > 0: (x kNormUp)^2) are nothing.
+struct Squares {
+  float sum = 0.0f, odd = 0.0f;
+  __device__ __forceinline__ void add(const float* x) {
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) s += x[k] * x[k];
+    if (s >= kNormLow && s <= kNormHigh) {
+      sum += s;
+      return;
+    }
+    const bool small = s < kNormLow;
+    const float f = small ? kNormUp : kNormDown;
+    s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) s += x[k] * f * (x[k] * f);
+    if (!small) odd = (odd > 0.0f ? 0.0f : odd) - s;
+    else if (odd >= 0.0f) odd += s;
+  }
+};
+
+// The CTA's sum of squares in a fixed order, fp32 within a warp and fp64 above
+// (by one thread: the GPU has few fp64 units); valid in thread 0.
+__device__ __forceinline__ double block_sum(const Squares& q) {
   __shared__ float warp_sum[kThreads / 32];
+  float x = q.sum;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_down_sync(0xffffffffu, x, o);
   if (threadIdx.x % 32 == 0) warp_sum[threadIdx.x / 32] = x;
-  __syncthreads();
+  const bool odd = __syncthreads_or(q.odd != 0.0f) != 0;
   double s = 0.0;
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) s += warp_sum[w];
+  }
+  if (__builtin_expect(odd, 0)) {
+    __shared__ double odd_sum[kThreads / 32];
+    constexpr double kUp = static_cast<double>(kNormUp) * kNormUp, kDown = static_cast<double>(kNormDown) * kNormDown;
+    double y = q.odd >= 0.0f ? q.odd / kUp : -q.odd / kDown;
+    for (int o = 16; o > 0; o >>= 1) y += __shfl_down_sync(0xffffffffu, y, o);
+    if (threadIdx.x % 32 == 0) odd_sum[threadIdx.x / 32] = y;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int w = 0; w < kThreads / 32; ++w) s += odd_sum[w];
+    }
   }
   return s;
 }
@@ -42,7 +77,7 @@ __device__ __forceinline__ double block_sum(float x) {
 // One chunk of one matrix per CTA (grid: chunk, matrix).  A thread's vectors
 // are kThreads vectors apart, so a warp reads contiguous runs.
 template <bool kFp32, bool kVecOk>
-__global__ void __launch_bounds__(kThreads) momentum_kernel(const __grid_constant__ MomentumArgs a) {
+__global__ void __launch_bounds__(kThreads, kVecOk && !kFp32 ? 6 : 5) momentum_kernel(const __grid_constant__ MomentumArgs a) {
   if (a.dev_t && *a.dev_t >= a.dev_steps) {  // capturable: past the captured steps' table
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
@@ -51,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) momentum_kernel(const __grid_constan
   const float clip = a.clip ? *a.clip : 1.0f;
   const long long base = a.offset[mat];
   unsigned nf = 0;
-  float sq = 0.0f;
+  Squares sq;
 #pragma unroll 2
   for (int i = 0; i < kPerThread / kVec; ++i) {
     const long long e = blockIdx.x * kNsChunk + (static_cast<long long>(i) * kThreads + threadIdx.x) * kVec;
@@ -74,8 +109,8 @@ __global__ void __launch_bounds__(kThreads) momentum_kernel(const __grid_constan
       if (a.clip) g[k] = __fmul_rn(g[k], clip);
       m[k] = __fadd_rn(__fmul_rn(a.mu, m[k]), g[k]);
       x[k] = a.nesterov ? __fadd_rn(g[k], __fmul_rn(a.mu, m[k])) : m[k];
-      sq += x[k] * x[k];
     }
+    sq.add(x);
     float* mom = a.mom + base + e;
     float* upd = a.update + mat * a.numel + e;
     if constexpr (kVecOk) {
@@ -123,10 +158,10 @@ __device__ __forceinline__ void load_logical(const MatSource& s, int mat, long l
 }
 
 template <bool kFp32, bool kVecOk>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 8)
     ns_norm_kernel(const MatSource s, long long cols, long long numel, long long chunks, double* partials) {
   const int mat = blockIdx.y;
-  float sq = 0.0f;
+  Squares sq;
 #pragma unroll 2
   for (int i = 0; i < kPerThread / kVec; ++i) {
     const long long e = blockIdx.x * kNsChunk + (static_cast<long long>(i) * kThreads + threadIdx.x) * kVec;
@@ -134,8 +169,7 @@ __global__ void __launch_bounds__(kThreads)
     const int count = static_cast<int>(numel - e < kVec ? numel - e : kVec);
     float x[kVec];
     load_logical<kFp32, kVecOk>(s, mat, cols, e, count, x);
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) sq += x[k] * x[k];
+    sq.add(x);
   }
   const double sum = block_sum(sq);
   if (threadIdx.x == 0) partials[mat * chunks + blockIdx.x] = sum;
@@ -148,7 +182,7 @@ __global__ void __launch_bounds__(kThreads)
 // in L2.
 template <bool kFp32, bool kVecOk>
 __global__ void __launch_bounds__(kThreads) ns_scale_kernel(const __grid_constant__ ScaleArgs a) {
-  __shared__ float inv_shared;
+  __shared__ float power_shared, rest_shared;
   const int mat = static_cast<int>(gridDim.y - 1 - blockIdx.y);
   const long long block = gridDim.x - 1 - blockIdx.x;
   // The partials and the source are read once the pass before has finished; the
@@ -164,11 +198,22 @@ __global__ void __launch_bounds__(kThreads) ns_scale_kernel(const __grid_constan
     for (int o = 16; o > 0; o >>= 1) s += __shfl_down_sync(0xffffffffu, s, o);
   }
   if (threadIdx.x == 0) {
+    // x scale / d.  Where 1 / d leaves fp32's range, by a power of two first, 2^100
+    // or 2^-100: sqrt(s) reaches from 2^-149 to 2^148.
     const double d = sqrt(s) + a.eps;
-    inv_shared = d == 0.0 ? 0.0f : static_cast<float>(1.0 / d);  // a zero matrix stays one without eps, too
+    const float rough = static_cast<float>(d);
+    if (rough >= 0x1p-60f && rough <= 0x1p60f) {
+      power_shared = 1.0f;
+      rest_shared = static_cast<float>(a.scale / d);
+    } else {
+      const float power = rough < 1.0f ? 0x1p100f : 0x1p-100f;
+      power_shared = power;
+      rest_shared = d == 0.0 ? 0.0f  // a zero matrix stays one without eps, too
+                    : d <= 1e300 ? static_cast<float>(a.scale / (d * power)) : __int_as_float(0x7fffffff);
+    }
   }
   __syncthreads();
-  const float inv = inv_shared;
+  const float power = power_shared, rest = rest_shared;
   const long long vecs_per_row = a.ldx / kVec, total = a.rows * vecs_per_row;
   const bool small = total <= 0xffffffffLL;  // 32-bit divisions
   for (int i = 0; i < a.per_thread; ++i) {
@@ -188,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) ns_scale_kernel(const __grid_constan
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float u = x[2 * k] * inv * a.scale, w = x[2 * k + 1] * inv * a.scale;
+      const float u = x[2 * k] * power * rest, w = x[2 * k + 1] * power * rest;
       const __half2 h = __floats2half2_rn(u, w);
       const __half2 l = __floats2half2_rn(u - __low2float(h), w - __high2float(h));
       hi[k] = *reinterpret_cast<const uint32_t*>(&h);

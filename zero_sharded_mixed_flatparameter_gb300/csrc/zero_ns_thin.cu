@@ -160,10 +160,12 @@ __device__ __forceinline__ void load_run(const void* base, const Run& r, bool ve
   else load8<kFp32, false>(base, r.at, r.count, x);
 }
 
-// A run of the slice from column j0, scaled, as pairs in `buffer`.
-__device__ __forceinline__ void put_run(const Matrix& x, const Run& r, int j0, float scale, float* v, uint32_t buffer) {
+// A run of the slice from column j0, scaled (by a power of two first), as pairs
+// in `buffer`.
+__device__ __forceinline__ void put_run(const Matrix& x, const Run& r, int j0, float power, float scale, float* v,
+                                        uint32_t buffer) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) v[k] *= scale;
+  for (int k = 0; k < 8; ++k) v[k] = v[k] * power * scale;
   if (!x.tall) {
     store_pair(buffer, r.row, (r.col - j0) / 8, v);
   } else {
@@ -423,10 +425,35 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
   const int runs = slice_runs(x);
   constexpr int kHeld = kThin * (kSlice / 8) / kThreads;
   float held[kHeld][8];
-  float sq = 0.0f;
   unsigned nf = 0;
+  // Sums of a thread go slice by slice, with what the additions round off kept
+  // beside them: many slices are long runs.
+  float sq = 0.0f, rounded = 0.0f;
+  auto add_slice = [&](float part) {
+    const float sum = __fadd_rn(sq, part), added = __fsub_rn(sum, sq);
+    rounded += __fadd_rn(__fsub_rn(sq, __fsub_rn(sum, added)), __fsub_rn(part, added));
+    sq = sum;
+  };
+  // The sum over the cluster, in one order for every thread of it.
+  auto joined = [&](float part) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+    if (lane == 0) sh.warp_sum[warp] = part;
+    __syncthreads();
+    part = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) part += sh.warp_sum[w];
+    if constexpr (kCtas > 1) {
+      if (tid == 0) sh.sum = part;
+      cluster_sync();
+      part = 0.0f;
+      for (int r = 0; r < kCtas; ++r) part += ld_cluster(map_rank(smem_u32(&sh.sum), r));
+    }
+    return part;
+  };
   for (int s = 0; s < mine; ++s) {
     const int j0 = first_column(s);
+    float part = 0.0f;
 #pragma unroll
     for (int q = 0; q < kHeld; ++q) {
       const int i = tid + q * kThreads;
@@ -444,25 +471,39 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
           load_run<kFp32>(source, r, vec, held[q]);
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sq += held[q][k] * held[q][k];
+        for (int k = 0; k < 8; ++k) part += held[q][k] * held[q][k];
       }
     }
+    add_slice(part);
   }
   if constexpr (kMuon) flush_nonfinite(a.nonfinite, nf);
+  float power = 1.0f, total = joined(sq + rounded);
+  if (__builtin_expect(!(total >= kNormLow && total <= kNormHigh), 0)) {  // the same for the whole cluster
+    power = total < kNormLow ? kNormUp : kNormDown;
+    sq = rounded = 0.0f;
+    for (int s = 0; s < mine; ++s) {
+      float part = 0.0f;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-  if (lane == 0) sh.warp_sum[warp] = sq;
-  __syncthreads();
-  sq = 0.0f;
+      for (int q = 0; q < kHeld; ++q) {
+        const int i = tid + q * kThreads;
+        if (i < runs) {
+          if (many) {
+            const Run r = slice_run(x, first_column(s), i);
+            if constexpr (kMuon) load_run<true>(update, r, false, held[q]);
+            else load_run<kFp32>(source, r, vec, held[q]);
+          }
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) sq += sh.warp_sum[w];
-  if constexpr (kCtas > 1) {
-    if (tid == 0) sh.sum = sq;
-    cluster_sync();
-    sq = 0.0f;
-    for (int r = 0; r < kCtas; ++r) sq += ld_cluster(map_rank(smem_u32(&sh.sum), r));
+          for (int k = 0; k < 8; ++k) part += held[q][k] * power * (held[q][k] * power);
+        }
+      }
+      add_slice(part);
+    }
+    if constexpr (kCtas > 1) cluster_sync();  // the first sums have been read
+    else __syncthreads();
+    total = joined(sq + rounded);
   }
-  const float norm = sqrtf(sq) + a.eps;
+  // x / (norm + eps), both times `power`
+  const float norm = sqrtf(total) + a.eps * power;
   const float scale = norm == 0.0f ? 0.0f : 1.0f / norm * a.step_factors[0].x;  // a zero matrix stays one
 
   // ---- X0 and its Gram matrix ---------------------------------------------------
@@ -484,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
           if constexpr (kMuon) load_run<true>(update, r, false, held[q]);
           else load_run<kFp32>(source, r, vec, held[q]);
         }
-        put_run(x, r, j0, scale, held[q], buffer);
+        put_run(x, r, j0, power, scale, held[q], buffer);
       }
     }
     ready(ok);
