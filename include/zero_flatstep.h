@@ -625,7 +625,11 @@ zero_status zero_muon_workspace_bytes(const zero_ctx* ctx, const zero_muon_confi
  *  rows, cols  per parameter: its row-major shape, rows * cols elements; 0, 0
  *              leaves the parameter with Adam
  *  workspace   device scratch of zero_muon_workspace_bytes, 256-byte aligned,
- *              caller-owned, in use by every step until zero_disable_muon
+ *              caller-owned: every later step uses it, and it must outlive the
+ *              last of them on its stream, also after this call was repeated or
+ *              zero_disable_muon called.  A captured step keeps the
+ *              configuration and the workspace it was captured with, for as
+ *              long as it is replayed
  * Errors: ZERO_EINVAL (config, shapes, workspace); ZERO_ESTATE (no buffers, a
  * step awaits post_step); ZERO_ENOTSUP (offload context); ZERO_ENOMEM.  A
  * zero_step that then fails with ZERO_ECUDA may have updated what was launched

@@ -81,6 +81,7 @@ class FlatStep:
         torch.cuda.current_stream(self.device).synchronize()
         self._init = []
         self._registered: List[List[torch.Tensor]] = []
+        self._muon_ws: List[torch.Tensor] = []  # the last one is the current one
 
     # -- buffers ---------------------------------------------------------------
     def _ptr(self, t: torch.Tensor) -> int:
@@ -256,20 +257,29 @@ class FlatStep:
                     coefficients: Sequence[float] = (3.4445, -4.7750, 2.0315), eps: float = 1e-7) -> None:
         """Orthogonalised (Muon) updates for the parameters with a (rows,
         cols) shape in `shapes` (one entry per parameter, None: stays with
-        Adam) in every later step; their momentum lives in exp_avg.  The
-        workspace is allocated by torch."""
+        Adam) in every later step; their momentum lives in exp_avg.  Called
+        again, it replaces the configuration (another momentum or decay, say).
+
+        The workspace is allocated by torch: up to 12 bytes per matrix element
+        of the 2^27 that are worked on at once, next to their Gram matrices.
+        It is used again where it is large enough, and none is released before
+        the FlatStep is: steps in flight on any stream and captured steps keep
+        theirs."""
         cfg = B.make_muon_config(lr, momentum, weight_decay, nesterov, scale, steps, coefficients, eps)
         rows = [0 if s is None else int(s[0]) for s in shapes]
         cols = [0 if s is None else int(s[1]) for s in shapes]
         need = B.zero_muon_workspace_bytes(self.ctx, cfg, rows, cols)
-        # 512-byte aligned by torch's allocator
-        workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-        B.zero_enable_muon(self.ctx, cfg, rows, cols, workspace.data_ptr(), need)
-        self._muon_ws = workspace
+        workspace = self._muon_ws[-1] if self._muon_ws else None
+        if workspace is None or workspace.numel() < need:
+            # 512-byte aligned by torch's allocator
+            workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        B.zero_enable_muon(self.ctx, cfg, rows, cols, workspace.data_ptr(), workspace.numel())
+        if not self._muon_ws or workspace is not self._muon_ws[-1]:
+            self._muon_ws.append(workspace)
 
     def disable_muon(self) -> None:
+        """All parameters back to Adam (the workspace stays, see enable_muon)."""
         B.zero_disable_muon(self.ctx)
-        self._muon_ws = None
 
     def set_muon_lr(self, lr: float) -> None:
         B.zero_set_muon_lr(self.ctx, lr)
