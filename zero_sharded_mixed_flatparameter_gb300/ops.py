@@ -13,6 +13,7 @@ import functools
 from typing import Optional, Sequence, Tuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import binding as B
 
@@ -177,6 +178,7 @@ class _QkNormRope(torch.autograd.Function):
         return qk_norm_rope(q, k, q_gain, k_gain, table, positions, eps=eps, interleaved=interleaved)
 
     @staticmethod
+    @once_differentiable  # a second derivative raises: the kernels record no graph
     def backward(ctx, dq_out, dk_out):
         q, k, q_gain, k_gain, table, positions = ctx.saved_tensors
         dq_out, dk_out = (d if d.stride(2) == 1 or d.size(2) == 1 else d.contiguous() for d in (dq_out, dk_out))
@@ -188,5 +190,6 @@ class _QkNormRope(torch.autograd.Function):
 
 def qk_norm_rope_autograd(q, k, q_gain, k_gain, table, positions=None, *, eps: float = 1e-6,
                           interleaved: bool = False):
-    """:func:`qk_norm_rope` that records its gradients for torch.autograd."""
+    """:func:`qk_norm_rope` that records its gradients for torch.autograd (first
+    derivatives; differentiating them again raises an error)."""
     return _QkNormRope.apply(q, k, q_gain, k_gain, table, positions, eps, interleaved)
