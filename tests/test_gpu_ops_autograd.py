@@ -48,3 +48,28 @@ def test_first_derivatives_repeat():
     (q.square().sum() + k.sum()).backward()
     for x, g in zip(leaves, once):
         assert torch.equal(x.grad, g)
+
+
+def test_inputs_that_require_gradients():
+    # a result cut from the graph would train nothing, silently
+    leaves, table = inputs()
+    plain = [x.detach() for x in leaves]
+    x = torch.randn(8, 8, device="cuda", requires_grad=True)
+    dq, dk = torch.randn_like(plain[0]), torch.randn_like(plain[1])
+    with pytest.raises(ValueError):
+        ops.orthogonalize(x)
+    for i in range(4):
+        args = list(plain)
+        args[i] = leaves[i]
+        with pytest.raises(ValueError):
+            ops.qk_norm_rope(*args, table)
+        with pytest.raises(ValueError):
+            ops.qk_norm_rope_backward(dq, dk, *args, table)
+    with pytest.raises(ValueError):
+        ops.qk_norm_rope_backward(dq.requires_grad_(), dk, *plain, table)
+    want = [*ops.qk_norm_rope(*plain, table), *ops.qk_norm_rope_backward(dq.detach(), dk, *plain, table)]
+    with torch.no_grad():
+        assert torch.equal(ops.orthogonalize(x), ops.orthogonalize(x.detach()))
+        got = [*ops.qk_norm_rope(*leaves, table), *ops.qk_norm_rope_backward(dq, dk, *leaves, table)]
+    for a, b in zip(got, want):
+        assert torch.equal(a, b) and not a.requires_grad

@@ -34,13 +34,21 @@ def _stream(device: torch.device) -> int:
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
+def _no_graph(what: str, *tensors: Optional[torch.Tensor]) -> None:
+    """A result that torch.autograd would take for a constant is refused."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"{what} records no gradient: detach its inputs or call it under torch.no_grad()")
+
+
 def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients: Sequence[float] = (3.4445, -4.7750, 2.0315),
                   eps: float = 1e-7, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Newton-Schulz orthogonalisation of a matrix or a stack of matrices.
 
     ``x``: bf16 or fp32, (rows, cols) or (batch, rows, cols), columns
-    contiguous.  Returns (or fills ``out``) bf16 of the same shape.
+    contiguous.  Returns (or fills ``out``) bf16 of the same shape.  Not
+    differentiable: an ``x`` that requires a gradient is refused.
     """
+    _no_graph("orthogonalize", x)
     if x.dim() not in (2, 3) or x.dtype not in _DTYPES or not x.is_cuda:
         raise ValueError("x must be a bf16 or fp32 CUDA matrix or a stack of them")
     if x.size(-1) > 1 and x.stride(-1) != 1:
@@ -115,7 +123,10 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_gain: Optional[torch.Tensor
     be strided views of one projection's output.  ``table`` holds per position
     the rotary_dim/2 cosines, then the sines; rotary_dim is its width.  A
     position outside the table marks padding: zeros.  ``out`` may be (q, k).
+    Inputs that require gradients are refused: :func:`qk_norm_rope_autograd`
+    records them.
     """
+    _no_graph("qk_norm_rope (qk_norm_rope_autograd does)", q, k, q_gain, k_gain)
     tokens, cfg = _check_qk(q, k, q_gain, k_gain, table, positions, eps, interleaved)
     if out is None:
         out = (torch.empty_like(q, memory_format=_CONTIGUOUS), torch.empty_like(k, memory_format=_CONTIGUOUS))
@@ -143,8 +154,10 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
 
     ``gain_out``: two vectors of head_dim elements, bf16 or fp32, to write the
     gain gradients to, such as slices of a replica's flat gradient; new fp32
-    vectors otherwise.
+    vectors otherwise.  Inputs that require gradients are refused, as in
+    :func:`qk_norm_rope`.
     """
+    _no_graph("qk_norm_rope_backward", dq_out, dk_out, q, k, q_gain, k_gain)
     tokens, cfg = _check_qk(q, k, q_gain, k_gain, table, positions, eps, interleaved)
     _check_like((dq_out, dk_out), (q, k))
     if out is None:
