@@ -40,13 +40,61 @@ def _no_graph(what: str, *tensors: Optional[torch.Tensor]) -> None:
         raise ValueError(f"{what} records no gradient: detach its inputs or call it under torch.no_grad()")
 
 
+def _layout(x: torch.Tensor) -> Tuple[int, int, list]:
+    """Byte address, bytes of a contiguous run and the (stride, size) of the other dimensions, largest stride first."""
+    size = x.element_size()
+    dims = sorted(((st * size, n) for n, st in zip(x.shape, x.stride()) if n > 1), reverse=True)
+    run = size
+    while dims and dims[-1][0] == run:
+        run *= dims.pop()[1]
+    return x.data_ptr(), run, dims
+
+
+def _span(run: int, dims) -> int:
+    return run + sum(stride * (n - 1) for stride, n in dims)
+
+
+def _apart(at: int, run: int, dims, other_run: int, other_dims) -> bool:
+    """Whether a layout at 0 and another `at` bytes further (or before) share no byte; False where this cannot tell."""
+    if at >= _span(run, dims) or -at >= _span(other_run, other_dims):
+        return True
+    if not dims or not other_dims or dims[0][0] != other_dims[0][0]:
+        return False
+    pitch, inner, other = dims[0][0], dims[1:], other_dims[1:]  # rows of one pitch, such as columns of one buffer
+    if _span(run, inner) > pitch or _span(other_run, other) > pitch:
+        return False
+    at %= pitch
+    return _apart(at, run, inner, other_run, other) and _apart(at - pitch, run, inner, other_run, other)
+
+
+def _same(a: torch.Tensor, b: torch.Tensor) -> bool:
+    return a.data_ptr() == b.data_ptr() and a.shape == b.shape and all(
+        n == 1 or s == t for n, s, t in zip(a.shape, a.stride(), b.stride()))
+
+
+def _check_memory(outs, ins) -> None:
+    """Refuses outputs that overlap themselves, one another or an input; output
+    i may be one of ins[i] itself (each element is read before it is written)."""
+    for i, out in enumerate(outs):
+        if out.numel() == 0:
+            continue
+        at, run, dims = _layout(out)
+        if any(stride < _span(run, dims[d + 1:]) for d, (stride, _) in enumerate(dims)):
+            raise ValueError("an output's elements overlap one another")
+        others = [*outs[:i], *(t for j, some in enumerate(ins) for t in some if j != i or not _same(t, out))]
+        for there, other_run, other_dims in (_layout(t) for t in others if t.numel()):
+            if not _apart(there - at, run, dims, other_run, other_dims):
+                raise ValueError("an output overlaps another tensor of the call")
+
+
 def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients: Sequence[float] = (3.4445, -4.7750, 2.0315),
                   eps: float = 1e-7, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Newton-Schulz orthogonalisation of a matrix or a stack of matrices.
 
     ``x``: bf16 or fp32, (rows, cols) or (batch, rows, cols), columns
-    contiguous.  Returns (or fills ``out``) bf16 of the same shape.  Not
-    differentiable: an ``x`` that requires a gradient is refused.
+    contiguous.  Returns (or fills ``out``, which must not overlap ``x``) bf16
+    of the same shape.  Not differentiable: an ``x`` that requires a gradient is
+    refused.
     """
     _no_graph("orthogonalize", x)
     if x.dim() not in (2, 3) or x.dtype not in _DTYPES or not x.is_cuda:
@@ -58,6 +106,8 @@ def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients: Sequence[flo
     elif out.shape != x.shape or out.dtype != torch.bfloat16 or out.device != x.device or (
             out.size(-1) > 1 and out.stride(-1) != 1):
         raise ValueError("out must be a bf16 tensor of x's shape and device with contiguous columns")
+    else:
+        _check_memory((out,), ((), (x,)))
     batch, rows, cols = (1, *x.shape) if x.dim() == 2 else x.shape
     cfg = _ns_config(steps, tuple(coefficients), eps)
     with _on(x.device):
@@ -122,7 +172,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_gain: Optional[torch.Tensor
     ``q`` (tokens, heads, head_dim) and ``k`` (tokens, kv_heads, head_dim) may
     be strided views of one projection's output.  ``table`` holds per position
     the rotary_dim/2 cosines, then the sines; rotary_dim is its width.  A
-    position outside the table marks padding: zeros.  ``out`` may be (q, k).
+    position outside the table marks padding: zeros.  ``out`` may be (q, k),
+    and must not overlap them otherwise.
     Inputs that require gradients are refused: :func:`qk_norm_rope_autograd`
     records them.
     """
@@ -132,6 +183,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_gain: Optional[torch.Tensor
         out = (torch.empty_like(q, memory_format=_CONTIGUOUS), torch.empty_like(k, memory_format=_CONTIGUOUS))
     else:
         _check_like(out, (q, k))
+        _check_memory(out, ((q,), (k,)))
     device = q.device
     with _on(device):
         B.zero_qk_norm_rope(cfg, tokens, _heads(q), _heads(k), _ptr(q_gain), _ptr(k_gain), table.data_ptr(),
@@ -152,6 +204,7 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
                           gain_out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
     """Gradients (dq, dk, dq_gain, dk_gain) of :func:`qk_norm_rope`'s inputs.
 
+    ``out`` may be (dq_out, dk_out) or (q, k), and must not overlap them otherwise.
     ``gain_out``: two vectors of head_dim elements, bf16 or fp32, to write the
     gain gradients to, such as slices of a replica's flat gradient; new fp32
     vectors otherwise.  Inputs that require gradients are refused, as in
@@ -164,6 +217,7 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
         out = (torch.empty_like(q, memory_format=_CONTIGUOUS), torch.empty_like(k, memory_format=_CONTIGUOUS))
     else:
         _check_like(out, (q, k))
+        _check_memory(out, ((dq_out, q), (dk_out, k)))
     device, dim = q.device, cfg.head_dim
     if gain_out is None:
         gain_out = (torch.empty(dim, dtype=torch.float32, device=device),
@@ -173,6 +227,7 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
             if g.dtype not in _DTYPES or g.dtype != gain_out[0].dtype or g.shape != (dim,) or g.device != device \
                     or not g.is_contiguous():
                 raise ValueError("gain_out must be two contiguous vectors of head_dim elements and one type")
+        _check_memory(gain_out, ())
     with _on(device):
         need = max(_backward_workspace(cfg.q_heads, cfg.k_heads, dim, tokens, device.index), 16)
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
