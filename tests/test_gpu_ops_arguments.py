@@ -1,0 +1,44 @@
+"""Numbers given as something else than Python numbers."""
+
+import pytest
+import torch
+
+from muon_reference import rotation_table
+from zero_sharded_mixed_flatparameter_gb300 import binding as B
+from zero_sharded_mixed_flatparameter_gb300 import ops
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from zero_sharded_mixed_flatparameter_gb300 import build_lib
+    build_lib.build()
+    B.load()
+
+
+def test_an_eps_that_changes_in_place():
+    q, k = torch.randn(5, 2, 64, device="cuda"), torch.randn(5, 1, 64, device="cuda")
+    table, eps = rotation_table(8, 64).cuda(), torch.tensor(1e-6)
+    for value in (1e-6, 10.0):
+        eps.fill_(value)
+        got = ops.qk_norm_rope(q, k, None, None, table, eps=eps)
+        want = ops.qk_norm_rope(q, k, None, None, table, eps=value)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), value
+
+
+def test_coefficients_that_change_in_place():
+    x = torch.randn(40, 50, device="cuda")
+    coefficients, eps = torch.tensor([3.4445, -4.7750, 2.0315], dtype=torch.float64), torch.tensor(0.0)
+    first = ops.orthogonalize(x, coefficients=coefficients, eps=eps)
+    assert torch.equal(first, ops.orthogonalize(x, eps=0.0))
+    coefficients.copy_(torch.tensor([1.5, -0.5, 0.0]))
+    eps.fill_(5.0)
+    again = ops.orthogonalize(x, coefficients=coefficients, eps=eps)
+    assert torch.equal(again, ops.orthogonalize(x, coefficients=(1.5, -0.5, 0.0), eps=5.0))
+    assert not torch.equal(again, first)
+
+
+def test_steps_are_whole():
+    with pytest.raises(TypeError):
+        ops.orthogonalize(torch.zeros(4, 4, device="cuda"), steps=5.5)

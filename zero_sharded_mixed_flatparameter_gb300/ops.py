@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import functools
+import operator
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -19,7 +20,8 @@ from . import binding as B
 
 _DTYPES = {torch.bfloat16: B.ZERO_GRAD_BF16, torch.float32: B.ZERO_GRAD_FP32}
 _CURRENT = contextlib.nullcontext()
-# read-only configuration structs by their values
+# read-only configuration structs by their values (plain numbers: what hashes by
+# identity, such as a tensor, could change its value under a kept entry)
 _ns_config = functools.lru_cache(maxsize=64)(B.make_ns_config)
 _qk_config = functools.lru_cache(maxsize=64)(B.zero_qk_config)
 _CONTIGUOUS = torch.contiguous_format
@@ -109,7 +111,7 @@ def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients: Sequence[flo
     else:
         _check_memory((out,), ((), (x,)))
     batch, rows, cols = (1, *x.shape) if x.dim() == 2 else x.shape
-    cfg = _ns_config(steps, tuple(coefficients), eps)
+    cfg = _ns_config(operator.index(steps), tuple(map(float, coefficients)), float(eps))
     with _on(x.device):
         need = B.zero_orthogonalize_workspace_bytes(cfg, rows, cols, batch)
         workspace = torch.empty(need, dtype=torch.uint8, device=x.device)  # 512-byte aligned
@@ -150,7 +152,7 @@ def _check_qk(q, k, q_gain, k_gain, table, positions, eps, interleaved):
         raise ValueError("positions must be a contiguous int32 vector with one entry per token")
     n_positions, rotary = table.shape
     return tokens, _qk_config(q_heads, k_heads, dim, rotary, 1 if interleaved else 0, _DTYPES[dtype],
-                              _DTYPES[gain_dtype or torch.float32], eps, n_positions)
+                              _DTYPES[gain_dtype or torch.float32], float(eps), n_positions)
 
 
 @functools.lru_cache(maxsize=256)
