@@ -55,7 +55,7 @@ def _inputs():
     files += [os.path.join(CSRC, "zero_internal.h"), os.path.join(CSRC, "zero_device.cuh"),
               os.path.join(CSRC, "zero_aux_internal.h"), os.path.join(CSRC, "zero_host.h"),
               os.path.join(CSRC, "zero_muon_internal.h"), os.path.join(CSRC, "zero_qk_internal.h"),
-              os.path.join(CSRC, "zero_tensor.cuh"),
+              os.path.join(CSRC, "zero_tensor.cuh"), os.path.join(CSRC, "zero_wait.h"),
               os.path.join(INCLUDE, "zero_flatstep.h")]
     return files
 

@@ -7,6 +7,8 @@
 
 #include <cstdint>
 
+#include "zero_wait.h"
+
 namespace zfs {
 
 // Waits of this file's kernels that gave up.
@@ -47,14 +49,13 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
 
-// A wait for a barrier's phase, bounded: products and copies take microseconds,
-// after kWaitNs they never will.  False: gave up (or another role did).
-constexpr unsigned long long kWaitNs = 1000000000ull;
+// A wait for a barrier's phase, bounded (zero_wait.h).  False: gave up (or
+// another role did).
 static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* gave_up) {
-  const unsigned long long t0 = global_ns();
+  Patience patience(global_ns());
   while (!mbar_try_wait(bar, parity)) {
     if (*gave_up) return false;
-    if (global_ns() - t0 > kWaitNs) {
+    if (patience.spent(global_ns())) {
       *gave_up = 1;
       atomicAdd(&g_wait_timeouts, 1u);
       return false;
