@@ -578,7 +578,8 @@ zero_status zero_orthogonalize_workspace_bytes(const zero_ns_config* cfg, int64_
  * Entries may have any finite size: the norm is summed so that their squares
  * stay in range.  An all-zero matrix gives zeros (with eps = 0, too); one with
  * an inf or NaN gives NaN.
- * rows, cols or batch of 0: ZERO_OK without device work.
+ * rows, cols or batch of 0: ZERO_OK without device work.  Waits of the kernels
+ * are bounded, see zero_kernel_timeouts.
  * Errors: ZERO_EINVAL (config, sizes, strides, pointers, workspace);
  * ZERO_ECUDA.
  */
@@ -737,9 +738,10 @@ zero_status zero_qk_norm_rope_backward(const zero_qk_config* cfg, int64_t tokens
  * kernels (used for N = 1..4 or N >= 11 bf16 and N >= 7 fp32 replicas when a
  * launch covers at least 2^23 elements) gave up on the current device since
  * the library was loaded.  A wait gives up only if a
- * bulk copy never lands; the CTA then leaves the rest of its tiles unchanged,
- * so a non-zero count means some step is incomplete.  Reads a device counter:
- * synchronizes with the device.  ctx may be NULL.
+ * bulk copy or a product never arrives; the CTA then leaves the rest of its
+ * tiles unchanged, so a count that grew means that a step or an
+ * orthogonalisation is incomplete (its call has returned ZERO_OK before).
+ * Reads device counters: synchronizes with the device.  ctx may be NULL.
  */
 zero_status zero_kernel_timeouts(const zero_ctx* ctx, uint32_t* count);
 

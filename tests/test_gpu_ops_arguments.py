@@ -42,3 +42,11 @@ def test_coefficients_that_change_in_place():
 def test_steps_are_whole():
     with pytest.raises(TypeError):
         ops.orthogonalize(torch.zeros(4, 4, device="cuda"), steps=5.5)
+
+
+def test_waits_that_gave_up_are_counted_for_the_operators():
+    before = ops.kernel_timeouts()
+    for shape in ((64, 64), (30, 2000), (300, 200), (512, 2048)):
+        ops.orthogonalize(torch.randn(shape, device="cuda"))
+    assert ops.kernel_timeouts() == before == B.zero_kernel_timeouts()
+    assert ops.kernel_timeouts("cuda:0") == before

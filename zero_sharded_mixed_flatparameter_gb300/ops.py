@@ -122,6 +122,15 @@ def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients: Sequence[flo
     return out
 
 
+def kernel_timeouts(device: Optional[torch.device] = None) -> int:
+    """Bounded waits that gave up on the device since the library was loaded:
+    0, unless the hardware failed to deliver.  A call in whose course the count
+    grew left part of its output unwritten.  Synchronizes."""
+    device = torch.device("cuda" if device is None else device)
+    with torch.cuda.device(device):
+        return B.zero_kernel_timeouts()
+
+
 def _heads(x: torch.Tensor) -> B.zero_heads:
     token, head, one = x.stride()
     if one != 1 and x.size(2) > 1:

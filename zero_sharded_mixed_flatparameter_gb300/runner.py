@@ -294,7 +294,10 @@ class FlatStep:
         self._nonfinite = counter
 
     def kernel_timeouts(self) -> int:
-        """Bounded waits of the tile-staged step kernels that gave up (process-wide count)."""
+        """Bounded waits that gave up, of the tile-staged step kernels and of the
+        Muon step's products (process-wide count; ops.kernel_timeouts is the same).
+        0, unless the hardware failed to deliver: a step in whose course it grew
+        is incomplete."""
         return B.zero_kernel_timeouts(self.ctx)
 
     def step_count(self) -> int:
