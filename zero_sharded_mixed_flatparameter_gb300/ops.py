@@ -96,7 +96,10 @@ def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients: Sequence[flo
     ``x``: bf16 or fp32, (rows, cols) or (batch, rows, cols), columns
     contiguous.  Returns (or fills ``out``, which must not overlap ``x``) bf16
     of the same shape.  Not differentiable: an ``x`` that requires a gradient is
-    refused.
+    refused.  Products run on fp16 operands (22 bits where the smaller side is at
+    most 128): with the default coefficients and up to 8 steps within 4e-3 of the
+    exact result's norm, bf16's rounding included; noise outside a low rank grows
+    with more steps, as it does in fp32.
     """
     _no_graph("orthogonalize", x)
     if x.dim() not in (2, 3) or x.dtype not in _DTYPES or not x.is_cuda:
