@@ -539,7 +539,8 @@ zero_status zero_cpu_adam(const zero_config* cfg, int64_t t, const float* grad, 
  * (embeddings, norms, biases, heads) stays with Adam / AdamW in the same
  * zero_step.  A shard boundary may cut a matrix anywhere, so the update needs
  * the whole matrix; all shards of the simulated ranks live in one buffer, and
- * the result does not depend on the stage.
+ * the result does not depend on the stage (bit for bit: the matrices of a
+ * context, which do count, are the same; see zero_orthogonalize).
  */
 
 /*
@@ -583,6 +584,12 @@ zero_status zero_orthogonalize_workspace_bytes(const zero_ns_config* cfg, int64_
  *  out        device bf16 matrices, likewise; must not overlap `in`
  *  workspace  device scratch, 256-byte aligned, kept until the work on
  *             `stream` has completed
+ * Equal calls give equal bits, and the values of a matrix's neighbours do not
+ * count.  How many there are may: a smaller side of at most 128 gives the same
+ * bits in any stack, for larger ones the order of the sums depends on how many
+ * tiles the stack has (512 x 2048 alone, in a stack of two and of four: sums
+ * over k in eight, four and two parts), and in a Muon step on the shapes that
+ * share its launches.
  * Entries may have any finite size: the norm is summed so that their squares
  * stay in range.  An all-zero matrix gives zeros (with eps = 0, too); one with
  * an inf or NaN gives NaN.

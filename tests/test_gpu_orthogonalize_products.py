@@ -68,3 +68,23 @@ def test_nonfinite(shape):
     alone = normal(shape, 2)
     alone[100, 200] = float("nan")
     assert ops.orthogonalize(alone.cuda()).isnan().all()
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(1, 512, 2048), (2, 512, 2048), (4, 2048, 512), (8, 512, 2048), (3, 777, 1301),
+                                             (2, 2048, 2100), (9, 128, 700)])
+def test_neighbours_values_do_not_count(batch, rows, cols):
+    x = normal((batch, rows, cols), 4).cuda()
+    got = ops.orthogonalize(x)[batch - 1]
+    y = x.clone()
+    y[:batch - 1] = normal((batch - 1, rows, cols), 5).cuda() * 1e5
+    if batch > 1:
+        y[0, 3, 4] = float("nan")
+    assert torch.equal(ops.orthogonalize(y)[batch - 1], got)
+
+
+def test_thin_matrices_are_the_same_in_any_stack():
+    for shape in ((100, 700), (3000, 90), (64, 64)):
+        x = normal((40, *shape), 6).cuda()
+        want = ops.orthogonalize(x)
+        for count in (1, 2, 7):
+            assert torch.equal(ops.orthogonalize(x[:count]), want[:count])
