@@ -50,3 +50,13 @@ def test_waits_that_gave_up_are_counted_for_the_operators():
         ops.orthogonalize(torch.randn(shape, device="cuda"))
     assert ops.kernel_timeouts() == before == B.zero_kernel_timeouts()
     assert ops.kernel_timeouts("cuda:0") == before
+
+
+def test_current_stream_and_device():
+    from zero_sharded_mixed_flatparameter_gb300 import _current
+    from zero_sharded_mixed_flatparameter_gb300.runner import FlatStep
+    assert _current.current_device() == torch.cuda.current_device()
+    for stream in (torch.cuda.current_stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(stream):
+            assert FlatStep.stream_handle() == FlatStep.stream_handle(stream) == stream.cuda_stream
+            assert _current._public_stream(0) == _current.current_stream(0) == stream.cuda_stream

@@ -17,6 +17,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import binding as B
+from ._current import current_device, current_stream
 
 _DTYPES = {torch.bfloat16: B.ZERO_GRAD_BF16, torch.float32: B.ZERO_GRAD_FP32}
 _CURRENT = contextlib.nullcontext()
@@ -29,11 +30,11 @@ _CONTIGUOUS = torch.contiguous_format
 
 def _on(device: torch.device):
     """Makes `device` current for a C call; the usual case costs nothing."""
-    return _CURRENT if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
+    return _CURRENT if current_device() == device.index else torch.cuda.device(device)
 
 
 def _stream(device: torch.device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
+    return current_stream(device.index)
 
 
 def _no_graph(what: str, *tensors: Optional[torch.Tensor]) -> None:

@@ -20,6 +20,7 @@ from typing import List, Optional, Sequence
 import torch
 
 from . import binding as B
+from ._current import current_device, current_stream
 
 
 class FlatStep:
@@ -124,7 +125,7 @@ class FlatStep:
     @staticmethod
     def stream_handle(stream: Optional[torch.cuda.Stream] = None) -> int:
         if stream is None:
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+            return current_stream(current_device())
         return int(stream.cuda_stream)
 
     def grad_dtype_torch(self):
