@@ -23,17 +23,18 @@ constexpr int kThreads = 256;
 constexpr int kPerThread = static_cast<int>(kNsChunk) / kThreads;  // elements per thread and chunk
 static_assert(kPerThread % kVec == 0, "whole vectors per thread");
 
-// A thread's sum of squares.  Vectors whose squares leave fp32's range are summed
-// times a power of two, of which one sum is enough: beside large ones (odd < 0:
-// minus the sum of (x kNormDown)^2) small ones (odd > 0: (x kNormUp)^2) are nothing.
+// A thread's sum of squares, entry after entry.  Vectors that leave it outside
+// kNormLow..kNormHigh are summed apart, from their entries times a power of two, and
+// one such sum is enough: beside large ones (odd < 0: minus the sum of
+// (x kNormDown)^2) small ones (odd > 0: (x kNormUp)^2) are nothing.
 struct Squares {
-  float sum = 0.0f, odd = 0.0f;
+  float sum = 0.0f, odd = 0.0f;  // sum: 0 or in the range
   __device__ __forceinline__ void add(const float* x) {
-    float s = 0.0f;
+    float s = sum;
 #pragma unroll
     for (int k = 0; k < kVec; ++k) s += x[k] * x[k];
     if (s >= kNormLow && s <= kNormHigh) {
-      sum += s;
+      sum = s;
       return;
     }
     const bool small = s < kNormLow;

@@ -181,6 +181,39 @@ __device__ __forceinline__ void put_run(const Matrix& x, const Run& r, int j0, f
   }
 }
 
+// A thread's sum of squares, entry after entry.  Every 32 slices `part` moves to
+// `sum`, with what the additions round off kept beside it: many slices are long runs.
+struct LongSum {
+  float part = 0.0f, sum = 0.0f, rounded = 0.0f;
+  __device__ __forceinline__ void end_slice(int s) {
+    if (s % 32 != 31) return;
+    const float to = __fadd_rn(sum, part), added = __fsub_rn(to, sum);
+    rounded += __fadd_rn(__fsub_rn(sum, __fsub_rn(to, added)), __fsub_rn(part, added));
+    sum = to;
+    part = 0.0f;
+  }
+  __device__ __forceinline__ float value() const { return part + rounded + sum; }
+};
+
+// A thread's sum over its CTA's slices once more, of entries times `power` (not
+// inline: for matrices that hardly ever come).
+template <bool kFp32>
+__device__ __noinline__ float scaled_squares(const void* base, const Matrix x, bool vec, int j0, int step, int slices,
+                                             float power) {
+  LongSum sum;
+  const int runs = slice_runs(x);
+  for (int s = 0; s < slices; ++s) {
+    for (int i = threadIdx.x; i < runs; i += kThreads) {
+      float v[8];
+      load_run<kFp32>(base, slice_run(x, j0 + s * step, i), vec, v);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum.part += v[k] * power * (v[k] * power);
+    }
+    sum.end_slice(s);
+  }
+  return sum.value();
+}
+
 // The momentum pass of a run: y becomes the update (the squares' sum is the caller's).
 template <bool kFp32>
 __device__ __forceinline__ void momentum_run(const ThinArgs& a, int mat, const Run& r, bool vec, float clip, float* y,
@@ -426,34 +459,26 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
   constexpr int kHeld = kThin * (kSlice / 8) / kThreads;
   float held[kHeld][8];
   unsigned nf = 0;
-  // Sums of a thread go slice by slice, with what the additions round off kept
-  // beside them: many slices are long runs.
-  float sq = 0.0f, rounded = 0.0f;
-  auto add_slice = [&](float part) {
-    const float sum = __fadd_rn(sq, part), added = __fsub_rn(sum, sq);
-    rounded += __fadd_rn(__fsub_rn(sq, __fsub_rn(sum, added)), __fsub_rn(part, added));
-    sq = sum;
-  };
+  LongSum sum;
   // The sum over the cluster, in one order for every thread of it.
-  auto joined = [&](float part) {
+  auto joined = [&](float value) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-    if (lane == 0) sh.warp_sum[warp] = part;
+    for (int o = 16; o > 0; o >>= 1) value += __shfl_xor_sync(0xffffffffu, value, o);
+    if (lane == 0) sh.warp_sum[warp] = value;
     __syncthreads();
-    part = 0.0f;
+    value = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) part += sh.warp_sum[w];
+    for (int w = 0; w < kWarps; ++w) value += sh.warp_sum[w];
     if constexpr (kCtas > 1) {
-      if (tid == 0) sh.sum = part;
+      if (tid == 0) sh.sum = value;
       cluster_sync();
-      part = 0.0f;
-      for (int r = 0; r < kCtas; ++r) part += ld_cluster(map_rank(smem_u32(&sh.sum), r));
+      value = 0.0f;
+      for (int r = 0; r < kCtas; ++r) value += ld_cluster(map_rank(smem_u32(&sh.sum), r));
     }
-    return part;
+    return value;
   };
   for (int s = 0; s < mine; ++s) {
     const int j0 = first_column(s);
-    float part = 0.0f;
 #pragma unroll
     for (int q = 0; q < kHeld; ++q) {
       const int i = tid + q * kThreads;
@@ -471,36 +496,31 @@ __global__ void __launch_bounds__(kThreads, 1) ns_thin_kernel(const __grid_const
           load_run<kFp32>(source, r, vec, held[q]);
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) part += held[q][k] * held[q][k];
+        for (int k = 0; k < 8; ++k) sum.part += held[q][k] * held[q][k];
       }
     }
-    add_slice(part);
+    sum.end_slice(s);
   }
   if constexpr (kMuon) flush_nonfinite(a.nonfinite, nf);
-  float power = 1.0f, total = joined(sq + rounded);
-  if (__builtin_expect(!(total >= kNormLow && total <= kNormHigh), 0)) {  // the same for the whole cluster
+  float power = 1.0f, total = joined(sum.value());
+  // The same for the whole cluster; as a vote, so that the compiler knows it to be
+  // the same for a warp (the barriers in the branch cost every call 1.5 us else).
+  if (__any_sync(0xffffffffu, !(total >= kNormLow && total <= kNormHigh))) {
     power = total < kNormLow ? kNormUp : kNormDown;
-    sq = rounded = 0.0f;
-    for (int s = 0; s < mine; ++s) {
-      float part = 0.0f;
+    float again = 0.0f;
+    if (many) {
+      again = scaled_squares<kMuon || kFp32>(kMuon ? update : source, x, vec, first_column(0), kCtas * kSlice, mine, power);
+    } else if (mine > 0) {
 #pragma unroll
       for (int q = 0; q < kHeld; ++q) {
-        const int i = tid + q * kThreads;
-        if (i < runs) {
-          if (many) {
-            const Run r = slice_run(x, first_column(s), i);
-            if constexpr (kMuon) load_run<true>(update, r, false, held[q]);
-            else load_run<kFp32>(source, r, vec, held[q]);
-          }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) part += held[q][k] * power * (held[q][k] * power);
-        }
+        for (int k = 0; k < 8; ++k)
+          if (tid + q * kThreads < runs) again += held[q][k] * power * (held[q][k] * power);
       }
-      add_slice(part);
     }
     if constexpr (kCtas > 1) cluster_sync();  // the first sums have been read
     else __syncthreads();
-    total = joined(sq + rounded);
+    total = joined(again);
   }
   // x / (norm + eps), both times `power`
   const float norm = sqrtf(total) + a.eps * power;
