@@ -571,7 +571,9 @@ typedef struct zero_ns_config {
 } zero_ns_config;
 
 /* Workspace of zero_orthogonalize for a stack of `batch` rows x cols matrices
- * (0 when there is nothing to do).  Errors: ZERO_EINVAL. */
+ * (0 when there is nothing to do): 8 bytes per element of up to 2^27 and 4 per
+ * element of the Gram matrices, so up to 1.6 GB unless one matrix alone is larger.
+ * Errors: ZERO_EINVAL. */
 zero_status zero_orthogonalize_workspace_bytes(const zero_ns_config* cfg, int64_t rows, int64_t cols, int64_t batch,
                                                int64_t* bytes);
 
@@ -623,7 +625,9 @@ typedef struct zero_muon_config {
   zero_ns_config ns;
 } zero_muon_config;
 
-/* Workspace of zero_enable_muon.  rows / cols as there.  Errors: ZERO_EINVAL, ZERO_ENOMEM. */
+/* Workspace of zero_enable_muon: as zero_orthogonalize's, and 4 bytes per element
+ * for the update (1.7 GB for eight 2048-wide decoder layers).  rows / cols as there.
+ * Errors: ZERO_EINVAL, ZERO_ENOMEM. */
 zero_status zero_muon_workspace_bytes(const zero_ctx* ctx, const zero_muon_config* cfg, const int64_t* rows,
                                       const int64_t* cols, int32_t n_params, int64_t* bytes);
 
@@ -665,7 +669,7 @@ zero_status zero_set_muon_lr(zero_ctx* ctx, float lr);
  * Orthogonalised updates move all singular values of the query and key
  * projections at one rate, which lets attention logits grow; training with
  * them norms every head's queries and keys.  The two gains are parameters of
- * the layer's unit (vectors: Adam), and the backward pass writes their
+ * the layer's unit (vectors: Adam), and the backward pass can write their
  * gradient where the replica's flat gradient holds it.
  */
 

@@ -4,12 +4,14 @@
 //
 // All are one pass over memory-resident data and bound by it; the norm is
 // summed per chunk of kNsChunk elements of a matrix, in fp32 over the elements
-// of a warp and in fp64 above, each in a fixed order, whatever the entries' size.  A CTA per chunk keeps
-// two vectors of every replica in flight per thread.  Over 486 M elements of 8
-// bf16 replicas the momentum pass (28 bytes per element) takes 1.95 ms, 7.0
-// TB/s, and the normalisation (8 bytes) 0.66 ms, 5.9 TB/s; 71 M elements in
-// four launches each, one after another, 346 us (5.7 TB/s) and 102 us (5.5); they
-// overlap in a step (zero_runtime.cpp), which takes 40 us less for it.
+// of a warp and in fp64 above, each in a fixed order, whatever the entries' size.
+// A CTA per chunk keeps two vectors of every replica in flight per thread.  Over
+// 486 M elements of 8 bf16 replicas the momentum pass (28 bytes per element) takes
+// 1.96 ms, 6.9 TB/s, and the normalisation (8 bytes) 0.61 ms, 6.4 TB/s; 71 M
+// elements in four launches each, one after another, 348 us (5.7 TB/s) and 104 us
+// (5.5); they overlap in a step (zero_runtime.cpp), which takes 40 us less for it.
+// Matrices that are not 16-byte aligned go element by element (the whole step of the
+// 71 M elements 2.6 ms instead of 1.75).
 
 #include <cuda_fp16.h>
 
@@ -76,7 +78,8 @@ __device__ __forceinline__ double block_sum(const Squares& q) {
 }
 
 // One chunk of one matrix per CTA (grid: chunk, matrix).  A thread's vectors
-// are kThreads vectors apart, so a warp reads contiguous runs.
+// are kThreads vectors apart, so a warp reads contiguous runs.  The CTAs per SM are
+// what keeps the loads in flight (bf16 vectors at five instead of six: 5 % slower).
 template <bool kFp32, bool kVecOk>
 __global__ void __launch_bounds__(kThreads, kVecOk && !kFp32 ? 6 : 5) momentum_kernel(const __grid_constant__ MomentumArgs a) {
   if (a.dev_t && *a.dev_t >= a.dev_steps) {  // capturable: past the captured steps' table
