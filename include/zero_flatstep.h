@@ -751,6 +751,140 @@ zero_status zero_qk_norm_rope_backward(const zero_qk_config* cfg, int64_t tokens
                                        void* dq_gain, void* dk_gain, int32_t dgain_dtype, void* workspace,
                                        int64_t workspace_bytes, void* stream);
 
+/* ---- Activations in 8 bits ---------------------------------------------------
+ * What a training step keeps of its activations for the backward pass, in half
+ * or a quarter of the bytes: 8-bit codes with one scale for every 32 columns of
+ * a row.  A scale is the smallest power of two, from 2^-126 on, under which the
+ * group's largest magnitude is at most the format's (448; 127): an element is
+ * divided by it exactly and rounded once, to nearest, ties to even.  A group
+ * with an inf or NaN in it reads as NaN.
+ */
+#define ZERO_PACK_E4M3 0  /* 4 significant bits: off by at most 2^-4 of itself */
+#define ZERO_PACK_INT8 1  /* whole numbers: off by at most 2^-7 of the group's largest */
+
+/*
+ * The 8-bit form of a matrix (device memory):
+ *  codes   [rows][groups * 32] bytes, 16-byte aligned; groups = ceil(cols / 32).
+ *          Codes of columns that do not exist are zero
+ *  scales  [rows][groups] bytes: the power of two plus 127; 255: not finite
+ *  format  ZERO_PACK_*
+ */
+typedef struct zero_packed {
+  void* codes;
+  void* scales;
+  int32_t format;
+} zero_packed;
+
+/*
+ * zero_pack_activations — codes and scales of a matrix; zero_unpack_activations
+ * — the values they stand for, rounded to dtype (exact, but for bf16
+ * subnormals).
+ *  cols    1..2^24; row r of the matrix begins at r * stride elements
+ * rows of 0: ZERO_OK without device work.  Errors: ZERO_EINVAL; ZERO_ECUDA.
+ */
+zero_status zero_pack_activations(int64_t rows, int64_t cols, const void* x, int32_t dtype, int64_t x_stride,
+                                  const zero_packed* packed, void* stream);
+zero_status zero_unpack_activations(int64_t rows, int64_t cols, const zero_packed* packed, void* out, int32_t dtype,
+                                    int64_t out_stride, void* stream);
+
+/* ---- Layer norm ----------------------------------------------------------------
+ *  cols          1..2^24
+ *  center        1: layer norm; 0: the mean stays (RMS norm)
+ *  dtype         zero_grad_dtype of x, y and their gradients
+ *  weight_dtype  zero_grad_dtype of weight and bias (bf16: as gathered)
+ *  eps           finite, >= 0
+ */
+typedef struct zero_norm_config {
+  int64_t cols;
+  int32_t center;
+  int32_t dtype;
+  int32_t weight_dtype;
+  float eps;
+} zero_norm_config;
+
+/*
+ * zero_layer_norm — for every row x
+ *   mean = sum x / cols (center 0: 0),  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
+ *   y = (x - mean) * rstd * weight + bias
+ * in fp32, rounded once; a row whose squares exceed fp32's range has rstd 0.
+ *  weight, bias   cols elements of weight_dtype, or NULL: none
+ *  y              may be x itself (same stride), else must not overlap it
+ *  stats          fp32 [rows][2]: mean and rstd, which the backward pass reads;
+ *                 8-byte aligned, or NULL: not wanted
+ *  packed         takes the 8-bit form of x in the same pass, or NULL
+ * rows of 0: ZERO_OK without device work.  Errors: ZERO_EINVAL; ZERO_ECUDA.
+ */
+zero_status zero_layer_norm(const zero_norm_config* cfg, int64_t rows, const void* x, int64_t x_stride,
+                            const void* weight, const void* bias, void* y, int64_t y_stride, float* stats,
+                            const zero_packed* packed, void* stream);
+
+/* Workspace of zero_layer_norm_backward.  Errors: ZERO_EINVAL. */
+zero_status zero_layer_norm_backward_workspace_bytes(const zero_norm_config* cfg, int64_t rows, int64_t* bytes);
+
+/*
+ * zero_layer_norm_backward — with xn = (x - mean) * rstd, g = dy * weight:
+ *   dx = rstd * (g - sum g / cols - xn * sum (g xn) / cols)   (center 0: without sum g)
+ *   dweight = sum over the rows of dy xn,  dbias = sum over the rows of dy
+ * The column sums are fp32 in an order that the sizes, types, strides and
+ * alignments fix: the same call gives the same bits.
+ *  x, packed         the forward input, or (x NULL) its 8-bit form; the entries
+ *                    it stands for take the input's place, the statistics stay
+ *  stats             as zero_layer_norm wrote them
+ *  dx                may be dy or x itself (same stride), else must not overlap them
+ *  dweight, dbias    cols elements of dgrad_dtype (zero_grad_dtype), overwritten
+ *                    (zeros for 0 rows); NULL: not wanted
+ *  workspace         device scratch, 16-byte aligned (not read where neither of
+ *                    the two is wanted)
+ * Errors: as zero_layer_norm; ZERO_EINVAL for a small workspace.
+ */
+zero_status zero_layer_norm_backward(const zero_norm_config* cfg, int64_t rows, const void* dy, int64_t dy_stride,
+                                     const void* x, int64_t x_stride, const zero_packed* packed, const void* weight,
+                                     const float* stats, void* dx, int64_t dx_stride, void* dweight, void* dbias,
+                                     int32_t dgrad_dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* ---- Embedding -----------------------------------------------------------------
+ *  rows      of the table, 0..2^30
+ *  dim       1..2^24
+ *  dtype     zero_grad_dtype of the table and of the looked up rows (forward),
+ *            of their gradient (backward)
+ *  id_bytes  4 or 8: int32 or int64 ids
+ *  scale     finite factor of the looked up rows
+ */
+typedef struct zero_embedding_config {
+  int64_t rows;
+  int64_t dim;
+  int32_t dtype;
+  int32_t id_bytes;
+  float scale;
+} zero_embedding_config;
+
+/*
+ * zero_embedding — out[t] = scale * table[ids[t]], rounded once; zeros where the
+ * id is outside [0, rows) (padding).
+ *  tokens   0..2^30 (0: ZERO_OK without device work)
+ *  table, out   rows at multiples of their stride (elements)
+ * Errors: ZERO_EINVAL; ZERO_ECUDA.
+ */
+zero_status zero_embedding(const zero_embedding_config* cfg, int64_t tokens, const void* ids, const void* table,
+                           int64_t table_stride, void* out, int64_t out_stride, void* stream);
+
+/* Workspace of zero_embedding_backward.  Errors: ZERO_EINVAL. */
+zero_status zero_embedding_backward_workspace_bytes(const zero_embedding_config* cfg, int64_t tokens, int64_t* bytes);
+
+/*
+ * zero_embedding_backward — dtable[v] = scale * sum of dout[t] over the tokens t
+ * with ids[t] = v.  The tokens are sorted by row, the sums fp32 in an order that
+ * the ids fix: the same call gives the same bits.
+ *  dtable      dtable_dtype (zero_grad_dtype), must not overlap dout or ids
+ *  accumulate  0: every row is written (zeros without tokens); 1: the sums are
+ *              added to what is there, rows without tokens stay as they are
+ *  workspace   device scratch, 16-byte aligned
+ * Errors: as zero_embedding; ZERO_EINVAL for a small workspace.
+ */
+zero_status zero_embedding_backward(const zero_embedding_config* cfg, int64_t tokens, const void* ids, const void* dout,
+                                    int64_t dout_stride, void* dtable, int32_t dtable_dtype, int64_t dtable_stride,
+                                    int32_t accumulate, void* workspace, int64_t workspace_bytes, void* stream);
+
 /*
  * zero_kernel_timeouts — how many bounded waits of the Newton-Schulz
  * products (zero_orthogonalize, the Muon step) and of the tile-staged step

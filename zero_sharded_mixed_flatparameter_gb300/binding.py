@@ -34,12 +34,15 @@ EXPORTED = (
     "zero_disable_capturable", "zero_count_nonfinite", "zero_read_nonfinite", "zero_gather_units",
     "zero_orthogonalize_workspace_bytes", "zero_orthogonalize", "zero_muon_workspace_bytes", "zero_enable_muon",
     "zero_disable_muon", "zero_set_muon_lr", "zero_qk_norm_rope", "zero_qk_backward_workspace_bytes",
-    "zero_qk_norm_rope_backward",
+    "zero_qk_norm_rope_backward", "zero_pack_activations", "zero_unpack_activations", "zero_layer_norm",
+    "zero_layer_norm_backward_workspace_bytes", "zero_layer_norm_backward", "zero_embedding",
+    "zero_embedding_backward_workspace_bytes", "zero_embedding_backward",
 )
 ZERO_CLIP_KEEP_REDUCED = 1
 ZERO_INJECT_MISSING_COPY = 1
 ZERO_INJECT_SHORT_BOUNDS = 2
 ZERO_MUON_SCALE_RMS, ZERO_MUON_SCALE_ASPECT = 0, 1
+ZERO_PACK_E4M3, ZERO_PACK_INT8 = 0, 1
 
 
 class zero_config(ctypes.Structure):
@@ -71,6 +74,20 @@ class zero_qk_config(ctypes.Structure):
 
 class zero_heads(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class zero_packed(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("format", ctypes.c_int32)]
+
+
+class zero_norm_config(ctypes.Structure):
+    _fields_ = [("cols", ctypes.c_int64), ("center", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class zero_embedding_config(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("id_bytes", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class ZeroError(RuntimeError):
@@ -147,6 +164,15 @@ def load(path: str = LIB_PATH):
             "zero_qk_norm_rope_backward": [P(zero_qk_config), i64, P(zero_heads), P(zero_heads), P(zero_heads),
                                            P(zero_heads), vp, vp, vp, vp, P(zero_heads), P(zero_heads), vp, vp, i32,
                                            vp, i64, vp],
+            "zero_pack_activations": [i64, i64, vp, i32, i64, P(zero_packed), vp],
+            "zero_unpack_activations": [i64, i64, P(zero_packed), vp, i32, i64, vp],
+            "zero_layer_norm": [P(zero_norm_config), i64, vp, i64, vp, vp, vp, i64, vp, P(zero_packed), vp],
+            "zero_layer_norm_backward_workspace_bytes": [P(zero_norm_config), i64, P(i64)],
+            "zero_layer_norm_backward": [P(zero_norm_config), i64, vp, i64, vp, i64, P(zero_packed), vp, vp, vp, i64,
+                                         vp, vp, i32, vp, i64, vp],
+            "zero_embedding": [P(zero_embedding_config), i64, vp, vp, i64, vp, i64, vp],
+            "zero_embedding_backward_workspace_bytes": [P(zero_embedding_config), i64, P(i64)],
+            "zero_embedding_backward": [P(zero_embedding_config), i64, vp, vp, i64, vp, i32, i64, i32, vp, i64, vp],
         }
         for name, args in sig.items():
             fn = getattr(lib, name)
@@ -176,6 +202,10 @@ def _i32(values: Sequence[int]):
 
 def _ptrs(values: Sequence[int]):
     return (ctypes.c_void_p * max(len(values), 1))(*[int(v) if v else None for v in values])
+
+
+def _ref(struct):
+    return ctypes.byref(struct) if struct is not None else None
 
 
 def make_config(stage: int, n_ranks: int, grad_dtype: str = "bf16", lr: float = 1e-3, beta1: float = 0.9,
@@ -486,6 +516,58 @@ def zero_qk_norm_rope_backward(cfg: zero_qk_config, tokens: int, dq_out: zero_he
         ctypes.byref(cfg), tokens, ctypes.byref(dq_out), ctypes.byref(dk_out), ctypes.byref(q), ctypes.byref(k),
         q_gain or None, k_gain or None, table or None, positions or None, ctypes.byref(dq), ctypes.byref(dk),
         dq_gain or None, dk_gain or None, dgain_dtype, workspace or None, workspace_bytes, stream or None))
+
+
+def zero_pack_activations(rows: int, cols: int, x: int, dtype: int, x_stride: int, packed: zero_packed,
+                          stream: int = 0) -> None:
+    _check(load().zero_pack_activations(rows, cols, x or None, dtype, x_stride, _ref(packed), stream or None))
+
+
+def zero_unpack_activations(rows: int, cols: int, packed: zero_packed, out: int, dtype: int, out_stride: int,
+                            stream: int = 0) -> None:
+    _check(load().zero_unpack_activations(rows, cols, _ref(packed), out or None, dtype, out_stride, stream or None))
+
+
+def zero_layer_norm(cfg: zero_norm_config, rows: int, x: int, x_stride: int, weight: int, bias: int, y: int,
+                    y_stride: int, stats: int, packed: zero_packed | None = None, stream: int = 0) -> None:
+    _check(load().zero_layer_norm(ctypes.byref(cfg), rows, x or None, x_stride, weight or None, bias or None, y or None,
+                                  y_stride, stats or None, _ref(packed), stream or None))
+
+
+def zero_layer_norm_backward_workspace_bytes(cfg: zero_norm_config, rows: int) -> int:
+    n = ctypes.c_int64()
+    _check(load().zero_layer_norm_backward_workspace_bytes(ctypes.byref(cfg), rows, ctypes.byref(n)))
+    return n.value
+
+
+def zero_layer_norm_backward(cfg: zero_norm_config, rows: int, dy: int, dy_stride: int, x: int, x_stride: int,
+                             packed: zero_packed | None, weight: int, stats: int, dx: int, dx_stride: int, dweight: int,
+                             dbias: int, dgrad_dtype: int, workspace: int, workspace_bytes: int,
+                             stream: int = 0) -> None:
+    _check(load().zero_layer_norm_backward(
+        ctypes.byref(cfg), rows, dy or None, dy_stride, x or None, x_stride, _ref(packed), weight or None, stats or None,
+        dx or None, dx_stride, dweight or None, dbias or None, dgrad_dtype, workspace or None, workspace_bytes,
+        stream or None))
+
+
+def zero_embedding(cfg: zero_embedding_config, tokens: int, ids: int, table: int, table_stride: int, out: int,
+                   out_stride: int, stream: int = 0) -> None:
+    _check(load().zero_embedding(ctypes.byref(cfg), tokens, ids or None, table or None, table_stride, out or None,
+                                 out_stride, stream or None))
+
+
+def zero_embedding_backward_workspace_bytes(cfg: zero_embedding_config, tokens: int) -> int:
+    n = ctypes.c_int64()
+    _check(load().zero_embedding_backward_workspace_bytes(ctypes.byref(cfg), tokens, ctypes.byref(n)))
+    return n.value
+
+
+def zero_embedding_backward(cfg: zero_embedding_config, tokens: int, ids: int, dout: int, dout_stride: int, dtable: int,
+                            dtable_dtype: int, dtable_stride: int, accumulate: int, workspace: int,
+                            workspace_bytes: int, stream: int = 0) -> None:
+    _check(load().zero_embedding_backward(ctypes.byref(cfg), tokens, ids or None, dout or None, dout_stride,
+                                          dtable or None, dtable_dtype, dtable_stride, accumulate, workspace or None,
+                                          workspace_bytes, stream or None))
 
 
 def zero_destroy(ctx: int) -> None:

@@ -31,7 +31,7 @@ COMMON = ["-std=c++17", "-O3", "-lineinfo", "--fmad=false", "-Xcompiler", "-fPIC
           "-I" + INCLUDE, "-I" + CSRC]
 SOURCES = ["zero_step_kernels.cu", "zero_aux_kernels.cu", "zero_runtime.cpp", "zero_no_alloc.cu",
            "zero_orthogonalize.cpp", "zero_muon_kernels.cu", "zero_ns_gemm.cu", "zero_ns_thin.cu",
-           "zero_qk_kernels.cu"]
+           "zero_qk_kernels.cu", "zero_norm_kernels.cu", "zero_pack_kernels.cu", "zero_embedding_kernels.cu"]
 HOST_SOURCES = ["zero_host_adam.cpp"]
 HOST_FLAGS = ["-std=c++17", "-O3", "-ffp-contract=off", "-fno-math-errno", "-fPIC", "-pthread", "-I" + CSRC]
 
@@ -55,7 +55,8 @@ def _inputs():
     files += [os.path.join(CSRC, "zero_internal.h"), os.path.join(CSRC, "zero_device.cuh"),
               os.path.join(CSRC, "zero_aux_internal.h"), os.path.join(CSRC, "zero_host.h"),
               os.path.join(CSRC, "zero_muon_internal.h"), os.path.join(CSRC, "zero_qk_internal.h"),
-              os.path.join(CSRC, "zero_tensor.cuh"), os.path.join(CSRC, "zero_wait.h"),
+              os.path.join(CSRC, "zero_norm_internal.h"), os.path.join(CSRC, "zero_rows.cuh"),
+              os.path.join(CSRC, "zero_rows_host.h"), os.path.join(CSRC, "zero_tensor.cuh"), os.path.join(CSRC, "zero_wait.h"),
               os.path.join(INCLUDE, "zero_flatstep.h")]
     return files
 

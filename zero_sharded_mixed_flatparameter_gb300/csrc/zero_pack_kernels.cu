@@ -1,0 +1,140 @@
+// Activations to 8 bits, with a power-of-two scale for every 32 columns of a
+// row, and back; and their C calls.  The form itself: zero_rows.cuh.
+
+#include "zero_flatstep.h"
+#include "zero_norm_internal.h"
+#include "zero_rows.cuh"
+#include "zero_rows_host.h"
+
+namespace zfs {
+namespace {
+
+constexpr int kPackThreads = 256;
+
+struct PackArgs {
+  long long rows;
+  int cols, lanes;     // lanes: threads on a row, a power of two up to kPackThreads
+  int groups, form;
+  void* x;             // read by the one, written by the other
+  long long x_stride;
+  uint8_t *codes, *scales;
+};
+
+// A thread takes eight columns of kRows rows at a time, `lanes` threads a row.
+template <bool kFp32, int kVec, bool kPack>
+__global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constant__ PackArgs a) {
+  constexpr int kRows = 4;  // in flight
+  constexpr long long kSize = kFp32 ? 4 : 2;
+  const int lanes = a.lanes, lane = threadIdx.x % lanes, per_cta = kPackThreads / lanes;
+  const long long step = static_cast<long long>(gridDim.x) * per_cta;
+  const long long first = static_cast<long long>(blockIdx.x) * per_cta;
+  for (long long r0 = first; r0 < a.rows; r0 += step * kRows) {
+    const long long mine = r0 + threadIdx.x / lanes;
+    for (int at = 0; at < a.cols; at += lanes * 8) {
+      const int cols = a.cols - at, groups = a.groups - at / kPackGroup;
+      Eight<kFp32, kVec> raw[kRows];
+      EightCodes<kVec> codes[kRows];
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const long long r = mine + step * i;
+        const bool real = r < a.rows;
+        if constexpr (kPack) {
+          load_eight<kFp32, kVec>(static_cast<const char*>(a.x) + (r * a.x_stride + at) * kSize, lane, lanes,
+                                  real ? cols : 0, &raw[i]);
+        } else {
+          load_codes<kVec>(a.codes + r * a.groups * kPackGroup + at, a.scales + r * a.groups + at / kPackGroup, lane,
+                           lanes, real ? groups : 0, &codes[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const long long r = mine + step * i;
+        float x[8];
+        if constexpr (kPack) {
+          widen_eight<kFp32, kVec>(raw[i], x);
+          pack_eight<kVec>(x, lane, lanes, groups, r < a.rows, a.form, a.codes + r * a.groups * kPackGroup + at,
+                           a.scales + r * a.groups + at / kPackGroup);
+        } else {
+          widen_codes<kVec>(codes[i], a.form, x);
+          if (r < a.rows) {
+            store_eight<kFp32, kVec>(static_cast<char*>(a.x) + (r * a.x_stride + at) * kSize, lane, lanes, cols, x);
+          }
+        }
+      }
+    }
+  }
+}
+
+template <bool kPack>
+void launch_pack(const PackArgs& a, bool fp32, bool vec, int ctas, cudaStream_t s) {
+  if (fp32) {
+    if (vec) pack_kernel<true, 8, kPack><<<ctas, kPackThreads, 0, s>>>(a);
+    else pack_kernel<true, 1, kPack><<<ctas, kPackThreads, 0, s>>>(a);
+  } else {
+    if (vec) pack_kernel<false, 8, kPack><<<ctas, kPackThreads, 0, s>>>(a);
+    else pack_kernel<false, 1, kPack><<<ctas, kPackThreads, 0, s>>>(a);
+  }
+}
+
+zero_status convert(int64_t rows, int64_t cols, const void* x, int32_t dtype, int64_t x_stride,
+                    const zero_packed* packed, bool pack, void* stream) {
+  if (rows < 0) return refuse(ZERO_EINVAL, "rows is negative");
+  if (cols < 1 || cols > (1 << 24)) return refuse(ZERO_EINVAL, "cols not in 1..2^24");
+  if (!is_dtype(dtype)) return refuse(ZERO_EINVAL, "dtype is neither bf16 (0) nor fp32 (1)");
+  if (!packed) return refuse(ZERO_EINVAL, "packed is NULL");
+  if (packed->format != ZERO_PACK_E4M3 && packed->format != ZERO_PACK_INT8)
+    return refuse(ZERO_EINVAL, "the 8-bit format is neither e4m3 (0) nor int8 (1)");
+  if (rows == 0) return ZERO_OK;
+  if (misplaced(x, dtype_bytes(dtype)) || x_stride < 0)
+    return refuse(ZERO_EINVAL, "the matrix is NULL or misaligned, or its stride negative");
+  if (misplaced(packed->codes, 16) || !packed->scales)
+    return refuse(ZERO_EINVAL, "codes or scales are NULL or misaligned");
+  PackArgs a{};
+  a.rows = rows;
+  a.cols = static_cast<int>(cols);
+  a.groups = (a.cols + kPackGroup - 1) / kPackGroup;
+  a.form = packed->format == ZERO_PACK_E4M3 ? kPackE4m3 : kPackInt8;
+  a.x = const_cast<void*>(x);
+  a.x_stride = x_stride;
+  a.codes = static_cast<uint8_t*>(packed->codes);
+  a.scales = static_cast<uint8_t*>(packed->scales);
+  const bool vec = cols % 8 == 0 && rows_aligned(x, x_stride, rows, dtype);
+  // whole groups for a warp's lanes where elements are single
+  const int need = (a.cols + 7) / 8, lanes = power_of_two(need < kPackThreads ? need : kPackThreads);
+  a.lanes = vec || lanes >= 32 ? lanes : 32;
+  const long long per_cta = kPackThreads / a.lanes, want = (rows + per_cta - 1) / per_cta;
+  const long long most = static_cast<long long>(sm_count()) * (2048 / kPackThreads);
+  const int ctas = static_cast<int>(want < most ? want : most);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (pack) launch_pack<true>(a, dtype == ZERO_GRAD_FP32, vec, ctas, s);
+  else launch_pack<false>(a, dtype == ZERO_GRAD_FP32, vec, ctas, s);
+  return launch_status(pack ? "pack launch" : "unpack launch");
+}
+
+}  // namespace
+
+unsigned int pack_debug_failures() {
+#ifdef ZFS_DEBUG_CHECKS
+  unsigned int v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_debug_failures, sizeof v) != cudaSuccess) return 0xFFFFFFFFu;
+  return v;
+#else
+  return 0;
+#endif
+}
+
+}  // namespace zfs
+
+extern "C" {
+
+zero_status zero_pack_activations(int64_t rows, int64_t cols, const void* x, int32_t dtype, int64_t x_stride,
+                                  const zero_packed* packed, void* stream) {
+  return zfs::convert(rows, cols, x, dtype, x_stride, packed, true, stream);
+}
+
+zero_status zero_unpack_activations(int64_t rows, int64_t cols, const zero_packed* packed, void* out, int32_t dtype,
+                                    int64_t out_stride, void* stream) {
+  return zfs::convert(rows, cols, out, dtype, out_stride, packed, false, stream);
+}
+
+}  // extern "C"

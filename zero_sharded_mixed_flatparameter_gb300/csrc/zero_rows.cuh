@@ -1,0 +1,246 @@
+// Device helpers of the kernels over rows of activations (layer norm, 8-bit
+// form, embedding): eight elements of a row per thread, and the 8-bit codes.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include <cstdint>
+
+#include "zero_device.cuh"
+
+namespace zfs {
+
+constexpr int kPackGroup = 32;                  // columns that share a scale
+constexpr int kPackE4m3 = 1, kPackInt8 = 2;     // forms (0: none), as the public ones plus 1
+
+// Eight elements of a row as loaded.  kVec 8: eight neighbours from column
+// 8 * lane on, 16-byte aligned; kVec 1: columns lane, lane + lanes, ... (so that
+// neighbouring threads read neighbouring columns whatever the alignment).
+template <bool kFp32, int kVec>
+struct Eight {
+  uint32_t w[kFp32 || kVec == 1 ? 8 : 4];
+};
+
+// The column of element k of thread `lane` of `lanes`, from column `first` on.
+template <int kVec>
+__device__ __forceinline__ int column(int k, int lane, int lanes) {
+  return kVec == 8 ? lane * 8 + k : k * lanes + lane;
+}
+
+// How many of the thread's elements lie within `cols` columns are loaded; the
+// others are zero.  `row`: the row's first element.
+template <bool kFp32, int kVec>
+__device__ __forceinline__ void load_eight(const void* row, int lane, int lanes, int cols, Eight<kFp32, kVec>* v) {
+  if constexpr (kVec == 8) {
+#pragma unroll
+    for (int k = 0; k < (kFp32 ? 8 : 4); ++k) v->w[k] = 0u;
+    if (lane * 8 < cols) {
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(row) + static_cast<long long>(lane) * (kFp32 ? 32 : 16));
+      const uint4 u = __ldcs(p);
+      v->w[0] = u.x; v->w[1] = u.y; v->w[2] = u.z; v->w[3] = u.w;
+      if constexpr (kFp32) {
+        const uint4 t = __ldcs(p + 1);
+        v->w[4] = t.x; v->w[5] = t.y; v->w[6] = t.z; v->w[7] = t.w;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int c = k * lanes + lane;
+      v->w[k] = 0u;
+      if (c < cols) {
+        if constexpr (kFp32) v->w[k] = static_cast<const uint32_t*>(row)[c];
+        else v->w[k] = static_cast<const uint16_t*>(row)[c];
+      }
+    }
+  }
+}
+
+template <bool kFp32, int kVec>
+__device__ __forceinline__ void widen_eight(const Eight<kFp32, kVec>& v, float* x) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if constexpr (kFp32) x[k] = __uint_as_float(v.w[k]);
+    else if constexpr (kVec == 8) x[k] = k % 2 ? bf16_hi(v.w[k / 2]) : bf16_lo(v.w[k / 2]);
+    else x[k] = bf16_lo(v.w[k]);
+  }
+}
+
+template <bool kFp32, int kVec>
+__device__ __forceinline__ void store_eight(void* row, int lane, int lanes, int cols, const float* x) {
+  if constexpr (kVec == 8) {
+    if (lane * 8 < cols) {
+      uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(row) + static_cast<long long>(lane) * (kFp32 ? 32 : 16));
+      if constexpr (kFp32) {
+        p[0] = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+        p[1] = make_uint4(__float_as_uint(x[4]), __float_as_uint(x[5]), __float_as_uint(x[6]), __float_as_uint(x[7]));
+      } else {
+        p[0] = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                          pack_bf16x2(x[6], x[7]));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int c = k * lanes + lane;
+      if (c < cols) {
+        if constexpr (kFp32) static_cast<float*>(row)[c] = x[k];
+        else static_cast<uint16_t*>(row)[c] = to_bf16_bits(x[k]);
+      }
+    }
+  }
+}
+
+// Element `at` of a bf16 or fp32 vector (weights, biases, their gradients).
+__device__ __forceinline__ float load_scalar(const void* p, bool fp32, long long at) {
+  if (fp32) return static_cast<const float*>(p)[at];
+  return bf16_lo(static_cast<const uint16_t*>(p)[at]);
+}
+__device__ __forceinline__ void store_scalar(void* p, bool fp32, long long at, float x) {
+  if (fp32) static_cast<float*>(p)[at] = x;
+  else static_cast<uint16_t*>(p)[at] = to_bf16_bits(x);
+}
+
+// ---- the 8-bit form ---------------------------------------------------------
+// The byte of a group's scale 2^(byte - 127): the smallest power of two under
+// which the group's largest magnitude (its fp32 bits) is at most 448 (e4m3) or
+// 127 (int8).  A power of two scales without rounding, so that an element is
+// rounded once; the e4m3 grid is the same under any of them but for what it
+// underflows, and int8 gives up half a bit on average for it.  255: the group
+// holds an inf or NaN; its codes are zero, and 0 * 2^128 (inf) reads as NaN.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t largest, int form) {
+  const uint32_t e = largest >> 23, m = largest & 0x7FFFFFu;
+  if (e == 255u) return 255u;
+  const int b = form == kPackE4m3 ? static_cast<int>(e) - 8 + (m > 0x600000u) : static_cast<int>(e) - 6 + (m > 0x7E0000u);
+  return b < 1 ? 1u : static_cast<uint32_t>(b);
+}
+// 1 / scale (not for byte 255, whose codes are zero whatever the elements).
+__device__ __forceinline__ float inverse_scale(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+__device__ __forceinline__ float scale_value(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+// Four elements (already times the inverse scale) as four codes, and back.
+__device__ __forceinline__ uint32_t encode4(const float* x, int form) {
+  if (form == kPackE4m3) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
+  }
+  uint32_t w = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) w |= (static_cast<uint32_t>(__float2int_rn(x[k])) & 0xFFu) << (8 * k);
+  return w;
+}
+__device__ __forceinline__ void decode4(uint32_t w, int form, float* x) {
+  if (form == kPackE4m3) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> (16 * k)), __NV_E4M3);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      x[2 * k] = f.x;
+      x[2 * k + 1] = f.y;
+    }
+  } else {
+    // a byte below an fp32 exponent of 2^23: 2^23 + 128 + code, exactly
+    const uint32_t u = w ^ 0x80808080u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7540u + k)) - 8388736.0f;
+  }
+}
+__device__ __forceinline__ uint32_t encode1(float x, int form) {
+  if (form == kPackE4m3) return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+  return static_cast<uint32_t>(__float2int_rn(x)) & 0xFFu;
+}
+__device__ __forceinline__ float decode1(uint32_t code, int form) {
+  if (form == kPackE4m3) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3);
+    return __half2float(*reinterpret_cast<const __half*>(&h));
+  }
+  return static_cast<float>(static_cast<int8_t>(code));
+}
+
+// Writes the 8-bit form of the thread's eight elements; every lane of the warp
+// calls it.  `lanes`: threads that hold the row (a power of two below 32, or a
+// multiple of 32); `write`: the thread's row exists.  Codes past the last column
+// of the last group are zero.
+template <int kVec>
+__device__ __forceinline__ void pack_eight(const float* x, int lane, int lanes, int groups, bool write, int form,
+                                           uint8_t* codes, uint8_t* scales) {
+  if constexpr (kVec == 8) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7FFFFFFFu);
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, m, o);
+      if (o < lanes) m = max(m, other);
+    }
+    const uint32_t byte = scale_byte(m, form);
+    const float inv = inverse_scale(byte);
+    float s[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s[k] = x[k] * inv;
+    uint2 c = make_uint2(encode4(s, form), encode4(s + 4, form));
+    if (byte == 255u) c = make_uint2(0u, 0u);
+    if (write && lane < groups * 4) {
+      *reinterpret_cast<uint2*>(codes + static_cast<long long>(lane) * 8) = c;
+      if (lane % 4 == 0) scales[lane / 4] = static_cast<uint8_t>(byte);
+      // fewer lanes than a group's quarters: the rest of the only group
+      if (lane + 1 == lanes) {
+        for (int q = lanes; q < 4; ++q) *reinterpret_cast<uint2*>(codes + q * 8) = make_uint2(0u, 0u);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if ((k * lanes + (lane & ~31)) / kPackGroup >= groups) break;  // the same for the whole warp
+      const uint32_t byte = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(x[k]) & 0x7FFFFFFFu), form);
+      const uint32_t c = byte == 255u ? 0u : encode1(x[k] * inverse_scale(byte), form);
+      const int at = k * lanes + lane;
+      if (write) {
+        codes[at] = static_cast<uint8_t>(c);
+        if (lane % 32 == 0) scales[at / kPackGroup] = static_cast<uint8_t>(byte);
+      }
+    }
+  }
+}
+
+// The thread's eight elements in 8 bits, as loaded, and as values.
+template <int kVec>
+struct EightCodes {
+  uint32_t w[kVec == 8 ? 3 : 8];  // kVec 8: codes, the scale's byte; kVec 1: code | scale << 8
+};
+template <int kVec>
+__device__ __forceinline__ void load_codes(const uint8_t* codes, const uint8_t* scales, int lane, int lanes, int groups,
+                                           EightCodes<kVec>* v) {
+  if constexpr (kVec == 8) {
+    v->w[0] = v->w[1] = v->w[2] = 0u;
+    if (lane < groups * 4) {
+      const uint2 c = __ldcs(reinterpret_cast<const uint2*>(codes + static_cast<long long>(lane) * 8));
+      v->w[0] = c.x; v->w[1] = c.y;
+      v->w[2] = scales[lane / 4];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int at = k * lanes + lane;
+      v->w[k] = 0u;
+      if (at < groups * kPackGroup)
+        v->w[k] = codes[at] | static_cast<uint32_t>(scales[at / kPackGroup]) << 8;
+    }
+  }
+}
+template <int kVec>
+__device__ __forceinline__ void widen_codes(const EightCodes<kVec>& v, int form, float* x) {
+  if constexpr (kVec == 8) {
+    const float s = scale_value(v.w[2]);
+    decode4(v.w[0], form, x);
+    decode4(v.w[1], form, x + 4);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] *= s;
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = decode1(v.w[k] & 0xFFu, form) * scale_value(v.w[k] >> 8);
+  }
+}
+
+}  // namespace zfs

@@ -38,6 +38,7 @@
 #include "zero_host.h"
 #include "zero_internal.h"
 #include "zero_muon_internal.h"
+#include "zero_norm_internal.h"
 #include "zero_qk_internal.h"
 
 namespace {
@@ -1545,7 +1546,8 @@ zero_status zero_debug_check_failures(uint32_t* count) {
   if (!count) return fail(nullptr, ZERO_EINVAL, "count is NULL");
 #ifdef ZFS_DEBUG_CHECKS
   const unsigned int counts[] = {zfs::step_debug_failures(), zfs::aux_debug_failures(), zfs::muon_debug_failures(),
-                                 zfs::ns_gemm_debug_failures(), zfs::thin_debug_failures(), zfs::qk_debug_failures()};
+                                 zfs::ns_gemm_debug_failures(), zfs::thin_debug_failures(), zfs::qk_debug_failures(),
+                                 zfs::norm_debug_failures(), zfs::pack_debug_failures(), zfs::embedding_debug_failures()};
   unsigned int sum = 0;
   for (unsigned int c : counts) {
     if (c == 0xFFFFFFFFu) return fail(nullptr, ZERO_ECUDA, "cannot read the check counters");

@@ -1,5 +1,6 @@
-"""Operators on torch tensors around the Muon step: :func:`orthogonalize`,
-:func:`qk_norm_rope` and its gradients.
+"""Operators on torch tensors around the optimizer step: :func:`orthogonalize`,
+:func:`qk_norm_rope`, :func:`layer_norm` and :func:`embedding` with their
+gradients, and activations kept in 8 bits (:func:`pack_activations`).
 
 Each is a thin call of the C function of the same name: checks, the output and
 workspace tensors, the current stream.  Tensors stay on one CUDA device; there
@@ -11,7 +12,7 @@ from __future__ import annotations
 import contextlib
 import functools
 import operator
-from typing import Optional, Sequence, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -25,6 +26,8 @@ _CURRENT = contextlib.nullcontext()
 # identity, such as a tensor, could change its value under a kept entry)
 _ns_config = functools.lru_cache(maxsize=64)(B.make_ns_config)
 _qk_config = functools.lru_cache(maxsize=64)(B.zero_qk_config)
+_norm_config = functools.lru_cache(maxsize=64)(B.zero_norm_config)
+_embedding_config = functools.lru_cache(maxsize=64)(B.zero_embedding_config)
 _CONTIGUOUS = torch.contiguous_format
 
 
@@ -276,3 +279,387 @@ def qk_norm_rope_autograd(q, k, q_gain, k_gain, table, positions=None, *, eps: f
     """:func:`qk_norm_rope` that records its gradients for torch.autograd (first
     derivatives; differentiating them again raises an error)."""
     return _QkNormRope.apply(q, k, q_gain, k_gain, table, positions, eps, interleaved)
+
+
+# ---- rows of activations -------------------------------------------------------
+_FORMATS = {torch.float8_e4m3fn: B.ZERO_PACK_E4M3, torch.int8: B.ZERO_PACK_INT8}
+_GROUP = 32  # columns that share a scale
+
+
+def _matrix(x: torch.Tensor, what: str, copy: bool = True) -> torch.Tensor:
+    """`x` as a matrix of its last dimension's rows; a copy where its strides allow no such view (refused unless
+    `copy`)."""
+    if x.dim() == 2:
+        pass
+    elif x.dim() == 0:
+        raise ValueError(f"{what} must have a dimension")
+    elif copy:
+        x = x.reshape(-1, x.size(-1)) if x.numel() else x.new_empty((x.shape[:-1].numel(), x.size(-1)))
+    elif x.numel() == 0:
+        return x.new_empty((x.shape[:-1].numel(), x.size(-1)))
+    else:
+        try:
+            x = x.view(-1, x.size(-1))
+        except RuntimeError:
+            raise ValueError(f"the rows of {what} must have one stride") from None
+    if x.stride(1) != 1 and x.size(1) > 1:
+        raise ValueError(f"the columns of {what} must be contiguous")
+    return x
+
+
+def _check_rows(x: torch.Tensor, what: str) -> None:
+    if x.dtype not in _DTYPES or not x.is_cuda:
+        raise ValueError(f"{what} must be a bf16 or fp32 CUDA tensor")
+    if x.dim() == 0 or x.size(-1) == 0:
+        raise ValueError(f"{what} must have columns")
+
+
+def _check_vectors(cols: int, device: torch.device, what: str, *vectors: Optional[torch.Tensor]) -> Optional[torch.dtype]:
+    """The type that the given vectors share."""
+    dtype = None
+    for v in vectors:
+        if v is None:
+            continue
+        if v.dtype not in _DTYPES or v.shape != (cols,) or v.device != device or not v.is_contiguous() or \
+                dtype not in (None, v.dtype):
+            raise ValueError(f"{what} must be contiguous vectors of one entry per column and one type (bf16 or fp32)")
+        dtype = v.dtype
+    return dtype
+
+
+class PackedActivations(NamedTuple):
+    """A tensor in 8 bits: codes (rows, 32 * groups) of e4m3 or int8, a power of two (its exponent plus 127) per group
+    of 32 columns, the shape and the type of what was packed."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    shape: torch.Size
+    dtype: torch.dtype
+
+
+def _new_packed(rows: int, x: torch.Tensor, dtype: torch.dtype) -> PackedActivations:
+    if dtype not in _FORMATS:
+        raise ValueError("activations are packed to torch.float8_e4m3fn or torch.int8")
+    groups = -(-x.size(-1) // _GROUP)
+    return PackedActivations(torch.empty((rows, groups * _GROUP), dtype=dtype, device=x.device),
+                             torch.empty((rows, groups), dtype=torch.uint8, device=x.device), x.shape, x.dtype)
+
+
+def _check_packed(packed: PackedActivations) -> Tuple[int, int]:
+    """Rows and columns of what was packed."""
+    codes, scales, shape, dtype = packed
+    if len(shape) == 0 or shape[-1] == 0 or dtype not in _DTYPES or codes.dtype not in _FORMATS or not codes.is_cuda:
+        raise ValueError("packed must be what pack_activations returns")
+    rows, cols = shape[:-1].numel(), shape[-1]
+    groups = -(-cols // _GROUP)
+    if codes.shape != (rows, groups * _GROUP) or scales.shape != (rows, groups) or scales.dtype != torch.uint8 or \
+            scales.device != codes.device or not codes.is_contiguous() or not scales.is_contiguous():
+        raise ValueError("the codes and scales of packed must be contiguous and fit its shape")
+    return rows, cols
+
+
+def _packed_struct(packed: PackedActivations) -> B.zero_packed:
+    return B.zero_packed(packed.codes.data_ptr(), packed.scales.data_ptr(), _FORMATS[packed.codes.dtype])
+
+
+def pack_activations(x: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, *,
+                     out: Optional[PackedActivations] = None) -> PackedActivations:
+    """``x`` (bf16 or fp32, any shape, columns contiguous) in 8 bits, with a
+    power-of-two scale for every 32 columns of a row.
+
+    ``dtype``: torch.float8_e4m3fn (each entry within 2^-4 of itself) or
+    torch.int8 (within 2^-7 of its group's largest).  A group with an inf or NaN
+    reads as NaN.  ``out``: an earlier result of the same shape and types to
+    write to.  What ``x`` requires a gradient for is not recorded: this keeps a
+    tensor for the backward pass, as saving it would.
+    """
+    _check_rows(x, "x")
+    m = _matrix(x.detach(), "x")
+    if out is None:
+        out = _new_packed(m.size(0), x, dtype)
+    else:
+        _check_packed(out)
+        if out.shape != x.shape or out.dtype != x.dtype or out.codes.dtype != dtype or out.codes.device != x.device:
+            raise ValueError("out must have x's shape, type and device, and codes of dtype")
+        _check_memory((out.codes, out.scales), ((), (), (m,)))
+    with _on(x.device):
+        B.zero_pack_activations(m.size(0), m.size(1), m.data_ptr(), _DTYPES[x.dtype], m.stride(0), _packed_struct(out),
+                                _stream(x.device))
+    return out
+
+
+def unpack_activations(packed: PackedActivations, dtype: Optional[torch.dtype] = None, *,
+                       out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The values that ``packed`` stands for, in the type of what was packed or
+    ``dtype`` (bf16 or fp32; both hold them exactly, but for bf16 subnormals)."""
+    rows, cols = _check_packed(packed)
+    device = packed.codes.device
+    if out is None:
+        out = torch.empty(packed.shape, dtype=packed.dtype if dtype is None else dtype, device=device)
+        if out.dtype not in _DTYPES:
+            raise ValueError("dtype must be bf16 or fp32")
+        m = out
+        stride = cols
+    else:
+        _no_graph("unpack_activations", out)
+        if out.shape != packed.shape or out.device != device or out.dtype not in _DTYPES or dtype not in (None, out.dtype):
+            raise ValueError("out must be a bf16 or fp32 tensor of packed's shape and device")
+        m = _matrix(out, "out", copy=False)
+        _check_memory((m,), ((), (packed.codes, packed.scales)))
+        stride = m.stride(0)
+    with _on(device):
+        B.zero_unpack_activations(rows, cols, _packed_struct(packed), m.data_ptr(), _DTYPES[out.dtype], stride,
+                                  _stream(device))
+    return out
+
+
+def _check_norm(x, weight, bias):
+    _check_rows(x, "x")
+    return _check_vectors(x.size(-1), x.device, "weight and bias", weight, bias) or torch.float32
+
+
+def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, *,
+               eps: float = 1e-5, center: bool = True, pack: Optional[torch.dtype] = None,
+               out: Optional[torch.Tensor] = None):
+    """Layer norm over the last dimension, or, with ``center=False``, the norm
+    without the mean (RMS norm).
+
+    ``x``: bf16 or fp32, any leading dimensions, columns contiguous; ``weight``
+    and ``bias`` bf16 or fp32 vectors of one type.  Returns y and the rows'
+    statistics (fp32, rows x 2: mean and 1 / deviation), which the backward pass
+    reads; with ``pack`` (torch.float8_e4m3fn or torch.int8) also ``x`` in 8 bits
+    (:class:`PackedActivations`), written in the same pass, which it can read in
+    place of ``x``.  ``out`` may be ``x``, and must not overlap it otherwise.
+    Inputs that require gradients are refused: :func:`layer_norm_autograd`
+    records them.
+    """
+    _no_graph("layer_norm (layer_norm_autograd does)", x, weight, bias)
+    vector_dtype = _check_norm(x, weight, bias)
+    m, device = _matrix(x, "x"), x.device
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        y, y_stride = out, x.size(-1)
+    else:
+        _check_like((out,), (x,))
+        y = _matrix(out, "out", copy=False)
+        y_stride = y.stride(0)
+        _check_memory((y,), ((m,),))
+    rows, cols = m.shape
+    stats = torch.empty((rows, 2), dtype=torch.float32, device=device)
+    packed = None if pack is None else _new_packed(rows, x, pack)
+    with _on(device):
+        B.zero_layer_norm(_norm_config(cols, 1 if center else 0, _DTYPES[x.dtype], _DTYPES[vector_dtype], float(eps)),
+                          rows, m.data_ptr(), m.stride(0), _ptr(weight), _ptr(bias), y.data_ptr(), y_stride,
+                          stats.data_ptr(), None if packed is None else _packed_struct(packed), _stream(device))
+    return (out, stats) if packed is None else (out, stats, packed)
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace(cols: int, rows: int, device: int) -> int:
+    return B.zero_layer_norm_backward_workspace_bytes(B.zero_norm_config(cols, 1, 0, 0, 0.0), rows)
+
+
+def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivations], weight: Optional[torch.Tensor],
+                        stats: torch.Tensor, *, center: bool = True, bias: bool = True,
+                        out: Optional[torch.Tensor] = None, weight_out: Optional[torch.Tensor] = None,
+                        bias_out: Optional[torch.Tensor] = None):
+    """Gradients (dx, dweight, dbias) of :func:`layer_norm`'s inputs.
+
+    ``x``: the forward input, or its 8-bit form, whose values then take the
+    input's place.  ``stats``, ``center``: as in the forward pass; dweight is None
+    without a weight, dbias with ``bias=False``.  ``out`` may be ``dy`` or ``x``,
+    and must not overlap them otherwise.  ``weight_out``, ``bias_out``: vectors of
+    one type, bf16 or fp32, to write those gradients to, such as slices of a
+    replica's flat gradient; new fp32 vectors otherwise.  Inputs that require
+    gradients are refused.
+    """
+    kept = isinstance(x, PackedActivations)
+    _no_graph("layer_norm_backward", dy, None if kept else x, weight)
+    _check_rows(dy, "dy")
+    device, cols = dy.device, dy.size(-1)
+    vector_dtype = _check_vectors(cols, device, "weight", weight) or torch.float32
+    g = _matrix(dy, "dy")
+    rows = g.size(0)
+    if kept:
+        _check_packed(x)
+        if x.shape != dy.shape or x.codes.device != device:
+            raise ValueError("x and dy must agree in shape and device")
+        m = None
+    else:
+        _check_like((dy,), (x,))
+        m = _matrix(x, "x")
+    if stats.shape != (rows, 2) or stats.dtype != torch.float32 or stats.device != device or not stats.is_contiguous():
+        raise ValueError("stats must be the contiguous fp32 tensor (rows, 2) of the forward pass")
+    if out is None:
+        out = torch.empty(dy.shape, dtype=dy.dtype, device=device)
+        d, d_stride = out, cols
+    else:
+        _check_like((out,), (dy,))
+        d = _matrix(out, "out", copy=False)
+        d_stride = d.stride(0)
+        _check_memory((d,), ((g,) if m is None else (g, m),))
+        if kept:
+            _check_memory((d,), ((), (x.codes, x.scales)))
+    given = _check_vectors(cols, device, "weight_out and bias_out", weight_out, bias_out)
+    if given is not None:
+        _check_memory([v for v in (weight_out, bias_out) if v is not None], ())
+    if weight is not None and weight_out is None:
+        weight_out = torch.empty(cols, dtype=given or torch.float32, device=device)
+    if not bias:
+        if bias_out is not None:
+            raise ValueError("bias_out without a bias")
+    elif bias_out is None:
+        bias_out = torch.empty(cols, dtype=given or torch.float32, device=device)
+    wanted = weight_out if weight_out is not None else bias_out
+    with _on(device):
+        need = 0 if wanted is None else _norm_workspace(cols, rows, device.index)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        B.zero_layer_norm_backward(
+            _norm_config(cols, 1 if center else 0, _DTYPES[dy.dtype], _DTYPES[vector_dtype], 0.0), rows, g.data_ptr(),
+            g.stride(0), _ptr(m), 0 if m is None else m.stride(0), _packed_struct(x) if kept else None, _ptr(weight),
+            stats.data_ptr(), d.data_ptr(), d_stride, _ptr(weight_out), _ptr(bias_out),
+            _DTYPES[torch.float32 if wanted is None else wanted.dtype], workspace.data_ptr(), need, _stream(device))
+    return out, weight_out, bias_out
+
+
+def _with_rows(d: torch.Tensor) -> torch.Tensor:
+    """A gradient as the kernels take it (autograd hands over broadcast ones)."""
+    return d if d.dim() and (d.stride(-1) == 1 or d.size(-1) == 1) else d.contiguous()
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, center, pack):
+        x = _with_rows(x)
+        y, stats, *packed = layer_norm(x, weight, bias, eps=eps, center=center, pack=pack)
+        if packed:
+            codes, scales, ctx.shape, ctx.dtype = packed[0]
+            ctx.save_for_backward(weight, bias, stats, codes, scales)
+        else:
+            ctx.save_for_backward(weight, bias, stats, x)
+        ctx.center = center
+        return y
+
+    @staticmethod
+    @once_differentiable  # a second derivative raises: the kernels record no graph
+    def backward(ctx, dy):
+        weight, bias, stats, x, *scales = ctx.saved_tensors
+        if scales:
+            x = PackedActivations(x, scales[0], ctx.shape, ctx.dtype)
+        dx, dweight, dbias = layer_norm_backward(_with_rows(dy), x, weight, stats, center=ctx.center,
+                                                 bias=bias is not None)
+        return (dx, dweight.to(weight.dtype) if weight is not None else None,
+                dbias.to(bias.dtype) if bias is not None else None, None, None, None)
+
+
+def layer_norm_autograd(x, weight=None, bias=None, *, eps: float = 1e-5, center: bool = True,
+                        pack: Optional[torch.dtype] = None) -> torch.Tensor:
+    """:func:`layer_norm`'s y, recording its gradients for torch.autograd (first
+    derivatives; differentiating them again raises an error).  With ``pack`` the
+    8-bit form of ``x`` is kept for the backward pass in place of ``x``: a half or
+    a quarter of the memory, for gradients of weight and ``x`` through the rounded
+    entries."""
+    return _LayerNorm.apply(x, weight, bias, eps, center, pack)
+
+
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
+
+
+def _check_ids(ids: torch.Tensor) -> torch.Tensor:
+    if ids.dtype not in _ID_BYTES or not ids.is_cuda:
+        raise ValueError("ids must be an int32 or int64 CUDA tensor")
+    return ids if ids.is_contiguous() else ids.contiguous()
+
+
+def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0,
+              out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``scale`` times the rows ``ids`` of ``table``, rounded once; zeros where an
+    id is outside the table (padding).
+
+    ``ids``: int32 or int64, any shape; ``table`` (rows, dim) bf16 or fp32 with
+    contiguous columns, such as a slice of the gathered unit buffer.  Returns (or
+    fills ``out``) ids.shape + (dim,).  A ``table`` that requires a gradient is
+    refused: :func:`embedding_autograd` records it.
+    """
+    _no_graph("embedding (embedding_autograd does)", table)
+    if table.dim() != 2:
+        raise ValueError("table must be a matrix")
+    _check_rows(table, "table")
+    device, (rows, dim) = table.device, table.shape
+    ids = _check_ids(ids)
+    if ids.device != device:
+        raise ValueError("ids and table must be on one device")
+    if table.stride(1) != 1 and dim > 1:
+        raise ValueError("the columns of table must be contiguous")
+    if out is None:
+        out = torch.empty((*ids.shape, dim), dtype=table.dtype, device=device)
+        y, stride = out, dim
+    else:
+        if out.shape != (*ids.shape, dim) or out.dtype != table.dtype or out.device != device:
+            raise ValueError("out must have the shape of ids and dim, and table's type and device")
+        y = _matrix(out, "out", copy=False)
+        stride = y.stride(0)
+        _check_memory((y,), ((), (table, ids)))
+    with _on(device):
+        B.zero_embedding(_embedding_config(rows, dim, _DTYPES[table.dtype], _ID_BYTES[ids.dtype], float(scale)),
+                         ids.numel(), ids.data_ptr(), table.data_ptr(), table.stride(0), y.data_ptr(), stride,
+                         _stream(device))
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def _embedding_workspace(rows: int, dim: int, tokens: int) -> int:
+    return B.zero_embedding_backward_workspace_bytes(B.zero_embedding_config(rows, dim, 0, 4, 1.0), tokens)
+
+
+def embedding_backward(dy: torch.Tensor, ids: torch.Tensor, rows: int, *, scale: float = 1.0,
+                       out: Optional[torch.Tensor] = None, accumulate: bool = False) -> torch.Tensor:
+    """Gradient (rows, dim) of :func:`embedding`'s table from that of its result:
+    every row ``scale`` times the sum over its tokens, in fp32 and in a fixed order.
+
+    ``out``: a bf16 or fp32 matrix to write it to, such as a slice of a replica's
+    flat gradient; a new one of ``dy``'s type otherwise.  Rows without tokens are
+    zeroed; with ``accumulate`` the sums are added to ``out`` instead, and those
+    rows stay as they are.
+    """
+    _no_graph("embedding_backward", dy, out)
+    _check_rows(dy, "dy")
+    ids, rows, device, dim = _check_ids(ids), operator.index(rows), dy.device, dy.size(-1)
+    if dy.shape != (*ids.shape, dim) or ids.device != device:
+        raise ValueError("dy must have the shape of ids and one more dimension, on one device")
+    g = _matrix(dy, "dy")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs an out to add to")
+        out = torch.empty((rows, dim), dtype=dy.dtype, device=device)
+    else:
+        if out.shape != (rows, dim) or out.dtype not in _DTYPES or out.device != device or (
+                out.stride(1) != 1 and dim > 1):
+            raise ValueError("out must be a bf16 or fp32 matrix (rows, dim) with contiguous columns")
+        _check_memory((out,), ((), (g, ids)))
+    with _on(device):
+        need = _embedding_workspace(rows, dim, ids.numel())
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        B.zero_embedding_backward(_embedding_config(rows, dim, _DTYPES[dy.dtype], _ID_BYTES[ids.dtype], float(scale)),
+                                  ids.numel(), ids.data_ptr(), g.data_ptr(), g.stride(0), out.data_ptr(),
+                                  _DTYPES[out.dtype], out.stride(0), 1 if accumulate else 0, workspace.data_ptr(),
+                                  need, _stream(device))
+    return out
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ids, table, scale):
+        ctx.save_for_backward(ids)
+        ctx.rows, ctx.scale = table.size(0), scale
+        return embedding(ids, table, scale=scale)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        return None, embedding_backward(_with_rows(dy), ctx.saved_tensors[0], ctx.rows, scale=ctx.scale), None
+
+
+def embedding_autograd(ids, table, *, scale: float = 1.0) -> torch.Tensor:
+    """:func:`embedding` that records the table's gradient for torch.autograd
+    (first derivatives; differentiating it again raises an error)."""
+    return _Embedding.apply(ids, table, scale)
