@@ -18,9 +18,12 @@
 namespace zfs {
 namespace {
 
-constexpr int kNormThreads = 256;   // threads of a CTA that holds several rows
-constexpr int kNormWidest = 8192;   // columns that a CTA of 1024 threads holds
-constexpr int kWideThreads = 512;   // threads of a CTA that walks over a row
+constexpr int kLaneThreads = 256, kLaneCtas = 3;  // of the kernels that hold several rows in a warp, CTAs an SM
+constexpr int kLaneCols = 128;                    // columns of a row of theirs, at most
+// Warps of a CTA, one an SM: 80 registers a thread forward, 128 backward.
+constexpr int kForwardWarps = 24, kBackwardWarps = 16, kNormWarps = 24;
+constexpr int kNormWidest = 8192;                 // columns that warps hold in registers
+constexpr int kWideThreads = 512;                 // threads of a CTA that walks over a row
 
 struct NormArgs {
   long long rows;
@@ -40,160 +43,121 @@ struct NormArgs {
   int dgrad_fp32, parts;
 };
 
-// Sums of kN values over the lanes that hold a row: by shuffles within a group
-// of lanes of a warp, or over the CTA through `shared` (two alternating
-// buffers, so that one barrier a sum is enough).
-template <bool kLanes, int kN>
-struct RowSum {
-  float (*buffer)[32][kN];
-  int turn = 0;
-  __device__ __forceinline__ void operator()(float (&v)[kN], int lanes) {
-    const int width = kLanes ? lanes : 32;
+// ---- rows of up to kLaneCols columns: a power of two of a warp's lanes each ------
+template <int kN>
+__device__ __forceinline__ void lanes_sum(float (&v)[kN], int lanes) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      if (o < width) {
+  for (int o = 8; o > 0; o >>= 1) {
+    if (o < lanes) {
 #pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-      }
-    }
-    if constexpr (!kLanes) {
-      if (threadIdx.x % 32 == 0) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) buffer[turn][threadIdx.x / 32][i] = v[i];
-      }
-      __syncthreads();
-      const int warps = lanes / 32;
-#pragma unroll
-      for (int i = 0; i < kN; ++i) v[i] = 0.0f;
-      for (int w = 0; w < warps; ++w) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] += buffer[turn][w][i];
-      }
-      turn ^= 1;
+      for (int i = 0; i < kN; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     }
   }
-};
+}
 
-template <int kVec>
-__device__ __forceinline__ void load_vector(const void* p, bool fp32, int lane, int lanes, int cols, float other, float* w) {
+__device__ __forceinline__ void load_vector(const void* p, bool fp32, int lane, int cols, float other, float* w) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const int c = column<kVec>(k, lane, lanes);
+    const int c = lane * 8 + k;
     w[k] = p && c < cols ? load_scalar(p, fp32, c) : other;
   }
 }
 
-// kLanes: a.lanes lanes of a warp hold a row, else the CTA does.
-template <bool kFp32, int kVec, bool kLanes, int kThreads>
-__global__ void __launch_bounds__(kThreads) norm_forward_kernel(const __grid_constant__ NormArgs a) {
+template <bool kFp32>
+__global__ void __launch_bounds__(kLaneThreads, kLaneCtas) norm_lanes_forward_kernel(const __grid_constant__ NormArgs a) {
   constexpr int kRows = 2;  // in flight
   constexpr long long kSize = kFp32 ? 4 : 2;
-  __shared__ float buffer[2][32][kRows];
-  RowSum<kLanes, kRows> sum{buffer};
-  const int lanes = a.lanes, lane = kLanes ? threadIdx.x % lanes : threadIdx.x;
-  const int per_cta = kLanes ? kThreads / lanes : 1;
+  const int lanes = a.lanes, lane = threadIdx.x % lanes, per_cta = kLaneThreads / lanes;
   float w[8], b[8];
-  load_vector<kVec>(a.weight, a.weight_fp32, lane, lanes, a.cols, 1.0f, w);
-  load_vector<kVec>(a.bias, a.weight_fp32, lane, lanes, a.cols, 0.0f, b);
-  const long long step = static_cast<long long>(gridDim.x) * per_cta;
-  const long long mine = static_cast<long long>(blockIdx.x) * per_cta + (kLanes ? threadIdx.x / lanes : 0);
+  load_vector(a.weight, a.weight_fp32, lane, a.cols, 1.0f, w);
+  load_vector(a.bias, a.weight_fp32, lane, a.cols, 0.0f, b);
+  const long long step = static_cast<long long>(gridDim.x) * per_cta, first = static_cast<long long>(blockIdx.x) * per_cta;
   // all threads take the same number of turns
-  for (long long r0 = 0; static_cast<long long>(blockIdx.x) * per_cta + r0 < a.rows; r0 += step * kRows) {
-    Eight<kFp32, kVec> raw[kRows];
+  for (long long r0 = first; r0 < a.rows; r0 += step * kRows) {
+    const long long mine = r0 + threadIdx.x / lanes;
+    Eight<kFp32, 8> raw[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const long long r = mine + r0 + step * i;
-      load_eight<kFp32, kVec>(static_cast<const char*>(a.x) + r * a.x_stride * kSize, lane, lanes,
-                              r < a.rows ? a.cols : 0, &raw[i]);
+      const long long r = mine + step * i;
+      load_eight<kFp32, 8>(static_cast<const char*>(a.x) + r * a.x_stride * kSize, lane, lanes, r < a.rows ? a.cols : 0,
+                           &raw[i]);
     }
-    float x[kRows][8], mean[kRows], total[kRows];
+    float x[kRows][8], mean[kRows] = {}, total[kRows] = {};
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      widen_eight<kFp32, kVec>(raw[i], x[i]);
-      mean[i] = 0.0f;
-    }
-    if (a.center) {
+      widen_eight<kFp32, 8>(raw[i], x[i]);
 #pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) mean[i] += x[i][k];
-      }
-      sum(mean, lanes);
+      for (int k = 0; k < 8; ++k) mean[i] += x[i][k];
     }
+    if (a.center) lanes_sum(mean, lanes);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      mean[i] *= a.inv_cols;
-      total[i] = 0.0f;
+      mean[i] = a.center ? mean[i] * a.inv_cols : 0.0f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float d = column<kVec>(k, lane, lanes) < a.cols ? x[i][k] - mean[i] : 0.0f;
+        const float d = x[i][k] - mean[i];
         total[i] = fmaf(d, d, total[i]);
       }
+      if (lane * 8 >= a.cols) total[i] = 0.0f;
     }
-    sum(total, lanes);
+    lanes_sum(total, lanes);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const long long r = mine + r0 + step * i;
+      const long long r = mine + step * i;
       const bool real = r < a.rows;
       if (a.form != 0) {
-        pack_eight<kVec>(x[i], lane, lanes, a.groups, real, a.form, a.codes + r * a.groups * kPackGroup,
-                         a.scales + r * a.groups);
+        pack_eight<8>(x[i], lane, lanes, a.groups, real, a.form, a.codes + r * a.groups * kPackGroup,
+                      a.scales + r * a.groups);
       }
       const float rstd = rsqrtf(fmaf(total[i], a.inv_cols, a.eps));
       if (a.stats && real && lane == 0) a.stats[r] = make_float2(mean[i], rstd);
-      float y[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) y[k] = fmaf((x[i][k] - mean[i]) * rstd, w[k], b[k]);
+      for (int k = 0; k < 8; ++k) x[i][k] = fmaf((x[i][k] - mean[i]) * rstd, w[k], b[k]);
       if (real) {
-        store_eight<kFp32, kVec>(static_cast<char*>(a.out) + r * a.out_stride * kSize, lane, lanes, a.cols, y);
+        store_eight<kFp32, 8>(static_cast<char*>(a.out) + r * a.out_stride * kSize, lane, lanes, a.cols, x[i]);
       }
     }
   }
 }
 
 // kPacked: x comes from its 8-bit form.
-template <bool kFp32, int kVec, bool kLanes, int kThreads, bool kPacked>
-__global__ void __launch_bounds__(kThreads) norm_backward_kernel(const __grid_constant__ NormArgs a) {
-  constexpr int kRows = kThreads > 256 ? 1 : 2;
+template <bool kFp32, bool kPacked>
+__global__ void __launch_bounds__(kLaneThreads, kLaneCtas) norm_lanes_backward_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int kRows = 2;
   constexpr long long kSize = kFp32 ? 4 : 2;
-  __shared__ float buffer[2][32][2 * kRows];
-  RowSum<kLanes, 2 * kRows> sum{buffer};
-  const int lanes = a.lanes, lane = kLanes ? threadIdx.x % lanes : threadIdx.x;
-  const int per_cta = kLanes ? kThreads / lanes : 1;
+  const int lanes = a.lanes, lane = threadIdx.x % lanes, per_cta = kLaneThreads / lanes;
   float w[8], dw[8] = {}, db[8] = {};
-  load_vector<kVec>(a.weight, a.weight_fp32, lane, lanes, a.cols, 1.0f, w);
-  const long long step = static_cast<long long>(gridDim.x) * per_cta;
-  const long long mine = static_cast<long long>(blockIdx.x) * per_cta + (kLanes ? threadIdx.x / lanes : 0);
-  for (long long r0 = 0; static_cast<long long>(blockIdx.x) * per_cta + r0 < a.rows; r0 += step * kRows) {
-    Eight<kFp32, kVec> raw[kRows], grad[kRows];
-    EightCodes<kVec> codes[kRows];
+  load_vector(a.weight, a.weight_fp32, lane, a.cols, 1.0f, w);
+  const long long step = static_cast<long long>(gridDim.x) * per_cta, first = static_cast<long long>(blockIdx.x) * per_cta;
+  const bool column = lane * 8 < a.cols;
+  for (long long r0 = first; r0 < a.rows; r0 += step * kRows) {
+    const long long mine = r0 + threadIdx.x / lanes;
+    Eight<kFp32, 8> raw[kRows], grad[kRows];
+    EightCodes<8> codes[kRows];
     float2 stats[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const long long r = mine + r0 + step * i;
+      const long long r = mine + step * i;
       const bool real = r < a.rows;
       stats[i] = real ? a.stats[r] : make_float2(0.0f, 0.0f);
       if constexpr (kPacked) {
-        load_codes<kVec>(a.codes + r * a.groups * kPackGroup, a.scales + r * a.groups, lane, lanes,
-                         real ? a.groups : 0, &codes[i]);
+        load_codes<8>(a.codes + r * a.groups * kPackGroup, a.scales + r * a.groups, lane, lanes, real ? a.groups : 0, &codes[i]);
       } else {
-        load_eight<kFp32, kVec>(static_cast<const char*>(a.x) + r * a.x_stride * kSize, lane, lanes,
-                                real ? a.cols : 0, &raw[i]);
+        load_eight<kFp32, 8>(static_cast<const char*>(a.x) + r * a.x_stride * kSize, lane, lanes, real ? a.cols : 0, &raw[i]);
       }
-      load_eight<kFp32, kVec>(static_cast<const char*>(a.dy) + r * a.dy_stride * kSize, lane, lanes,
-                              real ? a.cols : 0, &grad[i]);
+      load_eight<kFp32, 8>(static_cast<const char*>(a.dy) + r * a.dy_stride * kSize, lane, lanes, real ? a.cols : 0, &grad[i]);
     }
     float xn[kRows][8], g[kRows][8], total[2 * kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      if constexpr (kPacked) widen_codes<kVec>(codes[i], a.form, xn[i]);
-      else widen_eight<kFp32, kVec>(raw[i], xn[i]);
-      widen_eight<kFp32, kVec>(grad[i], g[i]);
+      if constexpr (kPacked) widen_codes<8>(codes[i], a.form, xn[i]);
+      else widen_eight<kFp32, 8>(raw[i], xn[i]);
+      widen_eight<kFp32, 8>(grad[i], g[i]);
       total[2 * i] = total[2 * i + 1] = 0.0f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         // columns past the last: nothing of the mean, of the row's inf or NaN
-        xn[i][k] = column<kVec>(k, lane, lanes) < a.cols ? (xn[i][k] - stats[i].x) * stats[i].y : 0.0f;
+        xn[i][k] = column ? (xn[i][k] - stats[i].x) * stats[i].y : 0.0f;
         dw[k] = fmaf(g[i][k], xn[i][k], dw[k]);
         db[k] += g[i][k];
         g[i][k] *= w[k];
@@ -201,53 +165,326 @@ __global__ void __launch_bounds__(kThreads) norm_backward_kernel(const __grid_co
         total[2 * i + 1] = fmaf(g[i][k], xn[i][k], total[2 * i + 1]);
       }
     }
-    sum(total, lanes);
+    lanes_sum(total, lanes);
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const long long r = mine + r0 + step * i;
+      const long long r = mine + step * i;
       if (r >= a.rows) continue;
       const float m1 = a.center ? total[2 * i] * a.inv_cols : 0.0f, m2 = total[2 * i + 1] * a.inv_cols;
-      float d[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) d[k] = stats[i].y * fmaf(-xn[i][k], m2, g[i][k] - m1);
-      store_eight<kFp32, kVec>(static_cast<char*>(a.out) + r * a.out_stride * kSize, lane, lanes, a.cols, d);
+      for (int k = 0; k < 8; ++k) g[i][k] = stats[i].y * fmaf(-xn[i][k], m2, g[i][k] - m1);
+      store_eight<kFp32, 8>(static_cast<char*>(a.out) + r * a.out_stride * kSize, lane, lanes, a.cols, g[i]);
     }
   }
   if (!a.partials) return;
+  // over the groups of a warp, then over the warps
+  __shared__ float sums[2][kLaneThreads / 32][kLaneCols];
   float* part = a.partials + static_cast<long long>(blockIdx.x) * 2 * a.cols;
-  if constexpr (kLanes) {
-    // over the groups of a warp, then over the warps
-    __shared__ float sums[2][kThreads / 32][256];
-    const int warp = threadIdx.x / 32;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      for (int o = lanes; o < 32; o <<= 1) {
-        dw[k] += __shfl_xor_sync(0xffffffffu, dw[k], o);
-        db[k] += __shfl_xor_sync(0xffffffffu, db[k], o);
+  for (int k = 0; k < 8; ++k) {
+    for (int o = lanes; o < 32; o <<= 1) {
+      dw[k] += __shfl_xor_sync(0xffffffffu, dw[k], o);
+      db[k] += __shfl_xor_sync(0xffffffffu, db[k], o);
+    }
+    if (threadIdx.x % 32 < lanes) {
+      sums[0][threadIdx.x / 32][lane * 8 + k] = dw[k];
+      sums[1][threadIdx.x / 32][lane * 8 + k] = db[k];
+    }
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.cols; c += kLaneThreads) {
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      float s = 0.0f;
+      for (int v = 0; v < kLaneThreads / 32; ++v) s += sums[which][v][c];
+      part[which * a.cols + c] = s;
+    }
+  }
+}
+
+// ---- rows of up to kNormWidest columns: whole warps each -------------------------
+// A CTA's warps form groups of a.lanes threads, a group takes kRows rows at a
+// time, a thread kN times eight columns of each.  The weights stand in shared
+// memory in the order in which a thread reads them.
+template <int kVec, int kN>
+struct Slots {
+  int lanes, lane;  // of the group
+  // The n-th eight columns: from column `at`, as thread `lane_of` of the group.
+  __device__ __forceinline__ int at(int n) const { return kVec == 8 ? 0 : n * 8 * lanes; }
+  __device__ __forceinline__ int lane_of(int n) const { return kVec == 8 ? n * lanes + lane : lane; }
+  __device__ __forceinline__ int column_of(int n, int k) const {
+    return kVec == 8 ? (n * lanes + lane) * 8 + k : (n * 8 + k) * lanes + lane;
+  }
+  // Where a column's weight stands: the lower and the upper four of a thread's
+  // eight apart, for 16-byte reads without conflicts.
+  __device__ __forceinline__ int slot(int c) const {
+    return kVec == 8 ? ((c % 8 / 4) * kN * lanes + c / 8) * 4 + c % 4 : c;
+  }
+  __device__ __forceinline__ void read(const float* table, int n, float* w) const {
+    if constexpr (kVec == 8) {
+      const float4* t = reinterpret_cast<const float4*>(table) + n * lanes + lane;
+      const float4 u = t[0], v = t[kN * lanes];
+      w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+      w[4] = v.x; w[5] = v.y; w[6] = v.z; w[7] = v.w;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = table[(n * 8 + k) * lanes + lane];
+    }
+  }
+  // All the CTA's threads; columns that do not exist get zero.
+  __device__ __forceinline__ void stage(const void* p, bool fp32, int cols, float other, float* table) const {
+    for (int c = threadIdx.x; c < kN * 8 * lanes; c += blockDim.x)
+      table[slot(c)] = c >= cols ? 0.0f : p ? load_scalar(p, fp32, c) : other;
+  }
+};
+
+// Sums of kV values over the group's threads.
+template <int kV>
+struct GroupSum {
+  float (*buffer)[kNormWarps][kV];  // [turn][warp of the CTA]
+  int first, warps, barrier, turn;  // the group's first warp, how many, its barrier
+  __device__ __forceinline__ GroupSum(float (*b)[kNormWarps][kV], int lanes)
+      : buffer(b), first(threadIdx.x / lanes * (lanes / 32)), warps(lanes / 32), barrier(1 + threadIdx.x / lanes), turn(0) {}
+  __device__ __forceinline__ void operator()(float (&v)[kV]) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+    }
+    if (warps == 1) return;
+    if (threadIdx.x % 32 == 0) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) buffer[turn][threadIdx.x / 32][i] = v[i];
+    }
+    // two alternating buffers: one barrier a sum is enough
+    asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(warps * 32) : "memory");
+#pragma unroll
+    for (int i = 0; i < kV; ++i) v[i] = 0.0f;
+    for (int w = first; w < first + warps; ++w) {
+#pragma unroll
+      for (int i = 0; i < kV; ++i) v[i] += buffer[turn][w][i];
+    }
+    turn ^= 1;
+  }
+};
+
+// Rows in flight, by the registers that a thread's part of one takes.
+template <bool kFp32, int kVec, int kN>
+constexpr int kForwardRows = kN * (kFp32 || kVec == 1 ? 2 : 1) >= 8 ? 1 : kN * (kFp32 || kVec == 1 ? 2 : 1) >= 4 ? 2 : 4;
+
+template <bool kFp32, int kVec, int kN, bool kPack>
+__global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int kRows = kForwardRows<kFp32, kVec, kN>;  // in flight
+  constexpr long long kSize = kFp32 ? 4 : 2;
+  extern __shared__ __align__(16) float tables[];
+  __shared__ float buffer[2][kNormWarps][kRows];
+  GroupSum<kRows> sum(buffer, a.lanes);
+  const Slots<kVec, kN> own{a.lanes, static_cast<int>(threadIdx.x) % a.lanes};
+  float *weight = tables, *bias = tables + kN * 8 * a.lanes;
+  const int groups = blockDim.x / a.lanes, group = threadIdx.x / a.lanes;
+  const long long step = static_cast<long long>(gridDim.x) * groups;
+  // the first rows of the CTAs before their second ones
+  const long long mine = blockIdx.x + static_cast<long long>(gridDim.x) * group;
+  bool staged = false;
+  for (long long r0 = mine; r0 < a.rows || !staged; r0 += step * kRows) {
+    Eight<kFp32, kVec> raw[kRows][kN];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const long long r = r0 + step * i;
+      const char* row = static_cast<const char*>(a.x) + r * a.x_stride * kSize;
+#pragma unroll
+      for (int n = 0; n < kN; ++n)
+        load_eight<kFp32, kVec>(row + own.at(n) * kSize, own.lane_of(n), own.lanes, r < a.rows ? a.cols - own.at(n) : 0,
+                                &raw[i][n]);
+    }
+    if (!staged) {  // while the first rows are on their way
+      own.stage(a.weight, a.weight_fp32, a.cols, 1.0f, weight);
+      own.stage(a.bias, a.weight_fp32, a.cols, 0.0f, bias);
+      __syncthreads();
+      staged = true;
+      if (r0 >= a.rows) break;
+    }
+    float mean[kRows] = {}, total[kRows] = {};
+    if (a.center) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          float x[8];
+          widen_eight<kFp32, kVec>(raw[i][n], x);
+          mean[i] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+        }
       }
-      if (threadIdx.x % 32 < lanes) {
-        sums[0][warp][column<kVec>(k, lane, lanes)] = dw[k];
-        sums[1][warp][column<kVec>(k, lane, lanes)] = db[k];
+      sum(mean);
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      mean[i] *= a.inv_cols;
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        float x[8], part = 0.0f;
+        forget_widened(raw[i][n]);
+        widen_eight<kFp32, kVec>(raw[i][n], x);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float d = x[k] - mean[i];
+          if (kVec == 1 && own.column_of(n, k) >= a.cols) d = 0.0f;
+          part = fmaf(d, d, part);
+        }
+        if (kVec == 8 && own.column_of(n, 0) >= a.cols) part = 0.0f;
+        total[i] += part;
+      }
+    }
+    sum(total);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const long long r = r0 + step * i;
+      const bool real = r < a.rows;
+      const float rstd = rsqrtf(fmaf(total[i], a.inv_cols, a.eps));
+      if (a.stats && real && own.lane == 0) a.stats[r] = make_float2(mean[i], rstd);
+      total[i] = rstd;
+    }
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      float w[8], b[8];
+      own.read(weight, n, w);
+      own.read(bias, n, b);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const long long r = r0 + step * i;
+        const bool real = r < a.rows;
+        float x[8];
+        forget_widened(raw[i][n]);
+        widen_eight<kFp32, kVec>(raw[i][n], x);
+        if constexpr (kPack) {
+          pack_eight<kVec>(x, own.lane_of(n), own.lanes, a.groups - own.at(n) / kPackGroup, real, a.form,
+                           a.codes + r * a.groups * kPackGroup + own.at(n), a.scales + r * a.groups + own.at(n) / kPackGroup);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = fmaf((x[k] - mean[i]) * total[i], w[k], b[k]);
+        if (real) {
+          store_eight<kFp32, kVec>(static_cast<char*>(a.out) + (r * a.out_stride + own.at(n)) * kSize, own.lane_of(n),
+                                   own.lanes, a.cols - own.at(n), x);
+        }
+      }
+    }
+  }
+}
+
+template <bool kFp32, int kVec, int kN>
+constexpr int kBackwardRows = kN * (kFp32 || kVec == 1 ? 2 : 1) >= 4 ? 1 : 2;
+
+template <bool kFp32, int kVec, int kN, bool kPacked>
+__global__ void __launch_bounds__(kBackwardWarps * 32, 1) norm_backward_kernel(const __grid_constant__ NormArgs a) {
+  constexpr int kRows = kBackwardRows<kFp32, kVec, kN>;
+  constexpr long long kSize = kFp32 ? 4 : 2;
+  extern __shared__ __align__(16) float tables[];
+  __shared__ float buffer[2][kNormWarps][2 * kRows];
+  GroupSum<2 * kRows> sum(buffer, a.lanes);
+  const Slots<kVec, kN> own{a.lanes, static_cast<int>(threadIdx.x) % a.lanes};
+  const int groups = blockDim.x / a.lanes, group = threadIdx.x / a.lanes;
+  const long long step = static_cast<long long>(gridDim.x) * groups;
+  const long long mine = blockIdx.x + static_cast<long long>(gridDim.x) * group;
+  float dw[kN][8] = {}, db[kN][8] = {};
+  own.stage(a.weight, a.weight_fp32, a.cols, 1.0f, tables);
+  __syncthreads();
+  for (long long r0 = mine; r0 < a.rows; r0 += step * kRows) {
+    Eight<kFp32, kVec> raw[kRows][kN], grad[kRows][kN];
+    EightCodes<kVec> codes[kRows][kN];
+    float2 stats[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const long long r = r0 + step * i;
+      const bool real = r < a.rows;
+      stats[i] = real ? a.stats[r] : make_float2(0.0f, 0.0f);
+      const char* row = static_cast<const char*>(a.x) + r * a.x_stride * kSize;
+      const char* drow = static_cast<const char*>(a.dy) + r * a.dy_stride * kSize;
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+        if constexpr (kPacked) {
+          load_codes<kVec>(a.codes + r * a.groups * kPackGroup + own.at(n), a.scales + r * a.groups + own.at(n) / kPackGroup,
+                           own.lane_of(n), own.lanes, real ? a.groups - own.at(n) / kPackGroup : 0, &codes[i][n]);
+        } else {
+          load_eight<kFp32, kVec>(row + own.at(n) * kSize, own.lane_of(n), own.lanes, real ? a.cols - own.at(n) : 0,
+                                  &raw[i][n]);
+        }
+        load_eight<kFp32, kVec>(drow + own.at(n) * kSize, own.lane_of(n), own.lanes, real ? a.cols - own.at(n) : 0,
+                                &grad[i][n]);
+      }
+    }
+    // xn, and dy; columns past the last: nothing of the mean, of the row's inf or NaN
+    auto values = [&](int i, int n, float* xn, float* g) {
+      if constexpr (kPacked) widen_codes<kVec>(codes[i][n], a.form, xn);
+      else widen_eight<kFp32, kVec>(raw[i][n], xn);
+      widen_eight<kFp32, kVec>(grad[i][n], g);
+      const bool some = kVec == 8 && own.column_of(n, 0) < a.cols;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        xn[k] = (kVec == 8 ? some : own.column_of(n, k) < a.cols) ? (xn[k] - stats[i].x) * stats[i].y : 0.0f;
+    };
+    float total[2 * kRows] = {};
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      float w[8];
+      own.read(tables, n, w);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        float xn[8], g[8];
+        values(i, n, xn, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          dw[n][k] = fmaf(g[k], xn[k], dw[n][k]);
+          db[n][k] += g[k];
+          g[k] *= w[k];
+          total[2 * i] += g[k];
+          total[2 * i + 1] = fmaf(g[k], xn[k], total[2 * i + 1]);
+        }
+      }
+    }
+    sum(total);
+#pragma unroll
+    for (int n = 0; n < kN; ++n) {
+      float w[8];
+      own.read(tables, n, w);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const long long r = r0 + step * i;
+        if (r >= a.rows) continue;
+        const float m1 = a.center ? total[2 * i] * a.inv_cols : 0.0f, m2 = total[2 * i + 1] * a.inv_cols;
+        float xn[8], g[8];
+        if constexpr (kPacked) forget_widened(codes[i][n]);
+        else forget_widened(raw[i][n]);
+        forget_widened(grad[i][n]);
+        values(i, n, xn, g);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[k] = stats[i].y * fmaf(-xn[k], m2, fmaf(g[k], w[k], -m1));
+        store_eight<kFp32, kVec>(static_cast<char*>(a.out) + (r * a.out_stride + own.at(n)) * kSize, own.lane_of(n),
+                                 own.lanes, a.cols - own.at(n), g);
+      }
+    }
+  }
+  if (!a.partials) return;
+  // the CTA's sums: one group after another adds its own, in the weights' place
+  float* part = a.partials + static_cast<long long>(blockIdx.x) * 2 * a.cols;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    if (which && !a.want_bias) break;
+    for (int turn = 0; turn < groups; ++turn) {
+      __syncthreads();
+      if (turn != group) continue;
+#pragma unroll
+      for (int n = 0; n < kN; ++n) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int at = own.slot(own.column_of(n, k));
+          const float s = which ? db[n][k] : dw[n][k];
+          tables[at] = turn ? tables[at] + s : s;
+        }
       }
     }
     __syncthreads();
-    for (int c = threadIdx.x; c < a.cols; c += kThreads) {
-#pragma unroll
-      for (int which = 0; which < 2; ++which) {
-        float s = 0.0f;
-        for (int v = 0; v < kThreads / 32; ++v) s += sums[which][v][c];
-        part[which * a.cols + c] = s;
-      }
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int c = column<kVec>(k, lane, lanes);
-      if (c < a.cols) {
-        part[c] = dw[k];
-        if (a.want_bias) part[a.cols + c] = db[k];
-      }
-    }
+    for (int c = threadIdx.x; c < a.cols; c += blockDim.x) part[which * a.cols + c] = tables[own.slot(c)];
+    __syncthreads();
   }
 }
 
@@ -380,47 +617,77 @@ __global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(const __grid_co
 }
 
 // ---- host ----------------------------------------------------------------------
-// How a row is held: by `lanes` lanes of a warp, by a CTA of `lanes` threads, or
-// (0) by none.
+// How a row is held: by `lanes` lanes of a warp (up to 16), by a group of `lanes`
+// threads of a CTA of `threads`, kN times eight columns each, or (0) by none.
 struct Shape {
-  int lanes, threads;
+  int lanes, threads, n;
   bool vec;
 };
-Shape shape_of(int cols, bool vec) {
-  if (cols > kNormWidest) return {0, kWideThreads, false};
-  const int need = vec ? cols / 8 : (cols + 7) / 8;
-  if (need <= 32) return {vec ? power_of_two(need) : 32, kNormThreads, vec};
-  const int threads = (need + 31) / 32 * 32;
-  return {threads, threads, vec};
+// most: the largest kN that the pass has registers for (single elements: 2).
+Shape shape_of(int cols, bool vec, int most, int cta_warps) {
+  if (cols > kNormWidest) return {0, kWideThreads, 0, false};
+  const int eights = (cols + 7) / 8;
+  if (vec && cols <= kLaneCols) return {power_of_two(eights), kLaneThreads, 1, true};
+  if (!vec && most > 2) most = 2;
+  const int warps = (eights + 31) / 32;
+  int n = 1;
+  while (n < most && n < warps) n *= 2;
+  const int lanes = (warps + n - 1) / n * 32, groups = cta_warps * 32 / lanes;
+  return {lanes, groups * lanes, n, vec};
 }
+Shape forward_shape(int cols, bool vec, bool fp32) { return shape_of(cols, vec, fp32 ? 4 : 8, kForwardWarps); }
+Shape backward_shape(int cols, bool vec) { return shape_of(cols, vec, 2, kBackwardWarps); }
 
-// CTAs for all rows, at most 2048 threads an SM.
+// CTAs for all rows: what is resident at once, at most.
 int norm_ctas(const Shape& s, long long rows) {
-  const long long per_cta = s.lanes && s.lanes <= 32 ? s.threads / s.lanes : 1;
-  const long long want = (rows + per_cta - 1) / per_cta, most = static_cast<long long>(sm_count()) * (2048 / s.threads);
+  const bool small = s.lanes > 0 && s.lanes < 32;
+  const long long per_cta = small ? s.threads / s.lanes : 1;
+  const long long want = (rows + per_cta - 1) / per_cta, per_sm = s.lanes == 0 ? 2048 / kWideThreads : small ? kLaneCtas : 1;
+  const long long most = per_sm * sm_count();
   return static_cast<int>(want < most ? want : most);
 }
-// Parts of the rows whose column sums are joined; the same whether or not the
-// tensors turn out to be aligned, for the workspace.
+// Parts of the rows whose column sums are joined.
 int wide_parts(long long rows) { return static_cast<int>(rows < 32 ? (rows ? rows : 1) : 32); }
+int parts_of(const Shape& s, long long rows) { return s.lanes ? norm_ctas(s, rows) : wide_parts(rows); }
+// ... whether or not the tensors turn out to be aligned, for the workspace.
 int most_parts(int cols, long long rows) {
-  if (cols > kNormWidest) return wide_parts(rows);
-  const int a = norm_ctas(shape_of(cols, false), rows);
-  const int b = cols % 8 ? a : norm_ctas(shape_of(cols, true), rows);
+  const int a = parts_of(backward_shape(cols, false), rows), b = parts_of(backward_shape(cols, true), rows);
   return a > b ? a : b;
 }
 
+// Dynamic shared memory beyond what every kernel may have; set anew each time, as
+// it belongs to the current context.
+template <typename Kernel>
+void launch_with(Kernel kernel, const NormArgs& a, const Shape& s, int ctas, int tables, cudaStream_t st) {
+  const int bytes = tables * s.n * 8 * s.lanes * static_cast<int>(sizeof(float));
+  if (bytes > 40 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  kernel<<<ctas, s.threads, bytes, st>>>(a);
+}
+
+template <bool kFp32, int kVec, int kN>
+void launch_forward_n(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st) {
+  if (a.form) launch_with(norm_forward_kernel<kFp32, kVec, kN, true>, a, s, ctas, 2, st);
+  else launch_with(norm_forward_kernel<kFp32, kVec, kN, false>, a, s, ctas, 2, st);
+}
 template <bool kFp32, int kVec>
 void launch_forward(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st) {
-  if (s.lanes <= 32) norm_forward_kernel<kFp32, kVec, true, kNormThreads><<<ctas, s.threads, 0, st>>>(a);
-  else if (s.threads <= 256) norm_forward_kernel<kFp32, kVec, false, 256><<<ctas, s.threads, 0, st>>>(a);
-  else norm_forward_kernel<kFp32, kVec, false, 1024><<<ctas, s.threads, 0, st>>>(a);
+  if constexpr (kVec == 8) {
+    if (s.lanes < 32) return norm_lanes_forward_kernel<kFp32><<<ctas, s.threads, 0, st>>>(a);
+    if (s.n == 4) return launch_forward_n<kFp32, kVec, 4>(a, s, ctas, st);
+    if constexpr (!kFp32) {
+      if (s.n == 8) return launch_forward_n<kFp32, kVec, 8>(a, s, ctas, st);
+    }
+  }
+  if (s.n == 2) launch_forward_n<kFp32, kVec, 2>(a, s, ctas, st);
+  else launch_forward_n<kFp32, kVec, 1>(a, s, ctas, st);
 }
 template <bool kFp32, int kVec, bool kPacked>
 void launch_backward(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st) {
-  if (s.lanes <= 32) norm_backward_kernel<kFp32, kVec, true, kNormThreads, kPacked><<<ctas, s.threads, 0, st>>>(a);
-  else if (s.threads <= 256) norm_backward_kernel<kFp32, kVec, false, 256, kPacked><<<ctas, s.threads, 0, st>>>(a);
-  else norm_backward_kernel<kFp32, kVec, false, 1024, kPacked><<<ctas, s.threads, 0, st>>>(a);
+  if constexpr (kVec == 8) {
+    if (s.lanes < 32) return norm_lanes_backward_kernel<kFp32, kPacked><<<ctas, s.threads, 0, st>>>(a);
+  }
+  if (s.n == 2) launch_with(norm_backward_kernel<kFp32, kVec, 2, kPacked>, a, s, ctas, 1, st);
+  else launch_with(norm_backward_kernel<kFp32, kVec, 1, kPacked>, a, s, ctas, 1, st);
 }
 template <bool kFp32, bool kPacked>
 void launch_wide_backward(const NormArgs& a, int ctas, cudaStream_t st) {
@@ -507,10 +774,10 @@ zero_status zero_layer_norm(const zero_norm_config* cfg, int64_t rows, const voi
   a.bias = bias;
   a.stats = reinterpret_cast<float2*>(stats);
   const bool vec = a.cols % 8 == 0 && rows_aligned(x, x_stride, rows, cfg->dtype) && rows_aligned(y, y_stride, rows, cfg->dtype);
-  const Shape s = shape_of(a.cols, vec);
+  const bool fp32 = cfg->dtype == ZERO_GRAD_FP32;
+  const Shape s = forward_shape(a.cols, vec, fp32);
   const int ctas = norm_ctas(s, rows);
   a.lanes = s.lanes;
-  const bool fp32 = cfg->dtype == ZERO_GRAD_FP32;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (s.lanes == 0) {
     if (fp32) norm_wide_forward_kernel<true><<<ctas, kWideThreads, 0, cs>>>(a);
@@ -578,10 +845,10 @@ zero_status zero_layer_norm_backward(const zero_norm_config* cfg, int64_t rows, 
     a.stats = const_cast<float2*>(reinterpret_cast<const float2*>(stats));
     const bool vec = a.cols % 8 == 0 && (packed || rows_aligned(x, x_stride, rows, cfg->dtype)) &&
                      rows_aligned(dy, dy_stride, rows, cfg->dtype) && rows_aligned(dx, dx_stride, rows, cfg->dtype);
-    const Shape s = shape_of(a.cols, vec);
+    const Shape s = backward_shape(a.cols, vec);
     const int ctas = norm_ctas(s, rows);
     a.lanes = s.lanes;
-    a.parts = s.lanes ? ctas : wide_parts(rows);
+    a.parts = parts_of(s, rows);
     const bool fp32 = cfg->dtype == ZERO_GRAD_FP32;
     if (s.lanes == 0) {
       if (fp32) packed ? launch_wide_backward<true, true>(a, ctas, cs) : launch_wide_backward<true, false>(a, ctas, cs);

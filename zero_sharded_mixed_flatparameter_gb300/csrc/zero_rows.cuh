@@ -66,6 +66,14 @@ __device__ __forceinline__ void widen_eight(const Eight<kFp32, kVec>& v, float* 
   }
 }
 
+// Widened anew where it is used again: eight fp32 values kept instead take twice
+// the registers of the loaded words (bf16), four times those of codes.
+template <typename T>
+__device__ __forceinline__ void forget_widened(T& v) {
+#pragma unroll
+  for (uint32_t& w : v.w) asm volatile("" : "+r"(w));
+}
+
 template <bool kFp32, int kVec>
 __device__ __forceinline__ void store_eight(void* row, int lane, int lanes, int cols, const float* x) {
   if constexpr (kVec == 8) {
