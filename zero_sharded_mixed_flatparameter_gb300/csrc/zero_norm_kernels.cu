@@ -106,7 +106,9 @@ __global__ void __launch_bounds__(kLaneThreads, kLaneCtas) norm_lanes_forward_ke
       const long long r = mine + step * i;
       const bool real = r < a.rows;
       if (a.form != 0) {
-        pack_eight<8>(x[i], lane, lanes, a.groups, real, a.form, a.codes + r * a.groups * kPackGroup,
+        F2 pairs[4];
+        to_pairs(x[i], pairs);
+        pack_eight<8>(pairs, lane, lanes, a.groups, real, a.form, a.codes + r * a.groups * kPackGroup,
                       a.scales + r * a.groups);
       }
       const float rstd = rsqrtf(fmaf(total[i], a.inv_cols, a.eps));
@@ -150,8 +152,13 @@ __global__ void __launch_bounds__(kLaneThreads, kLaneCtas) norm_lanes_backward_k
     float xn[kRows][8], g[kRows][8], total[2 * kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      if constexpr (kPacked) widen_codes<8>(codes[i], a.form, xn[i]);
-      else widen_eight<kFp32, 8>(raw[i], xn[i]);
+      if constexpr (kPacked) {
+        F2 pairs[4];
+        widen_codes<8>(codes[i], a.form, pairs);
+        from_pairs(pairs, xn[i]);
+      } else {
+        widen_eight<kFp32, 8>(raw[i], xn[i]);
+      }
       widen_eight<kFp32, 8>(grad[i], g[i]);
       total[2 * i] = total[2 * i + 1] = 0.0f;
 #pragma unroll
@@ -220,21 +227,33 @@ struct Slots {
   __device__ __forceinline__ int slot(int c) const {
     return kVec == 8 ? ((c % 8 / 4) * kN * lanes + c / 8) * 4 + c % 4 : c;
   }
-  __device__ __forceinline__ void read(const float* table, int n, float* w) const {
+  __device__ __forceinline__ void read(const float* table, int n, F2* w) const {
     if constexpr (kVec == 8) {
-      const float4* t = reinterpret_cast<const float4*>(table) + n * lanes + lane;
-      const float4 u = t[0], v = t[kN * lanes];
-      w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-      w[4] = v.x; w[5] = v.y; w[6] = v.z; w[7] = v.w;
+      const ulonglong2* t = reinterpret_cast<const ulonglong2*>(table) + n * lanes + lane;
+      const ulonglong2 u = t[0], v = t[kN * lanes];
+      w[0] = u.x; w[1] = u.y; w[2] = v.x; w[3] = v.y;
     } else {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = table[(n * 8 + k) * lanes + lane];
+      for (int k = 0; k < 4; ++k)
+        w[k] = pair(table[(n * 8 + 2 * k) * lanes + lane], table[(n * 8 + 2 * k + 1) * lanes + lane]);
     }
   }
-  // All the CTA's threads; columns that do not exist get zero.
-  __device__ __forceinline__ void stage(const void* p, bool fp32, int cols, float other, float* table) const {
-    for (int c = threadIdx.x; c < kN * 8 * lanes; c += blockDim.x)
-      table[slot(c)] = c >= cols ? 0.0f : p ? load_scalar(p, fp32, c) : other;
+  // Columns 4 * four .. 4 * four + 3 of a vector; those that do not exist: zero.
+  __device__ __forceinline__ float4 load_four(const void* p, bool fp32, int four, int cols, float other) const {
+    const int c = four * 4;
+    float v[4];
+    if (p && c + 4 <= cols && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+      if (fp32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + c);
+      const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + c);
+      return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = c + k >= cols ? 0.0f : p ? load_scalar(p, fp32, c + k) : other;
+    return make_float4(v[0], v[1], v[2], v[3]);
+  }
+  // All the CTA's threads.
+  __device__ __forceinline__ void store_four(float* table, int four, float4 v) const {
+    *reinterpret_cast<float4*>(table + slot(four * 4)) = v;  // four neighbours in either order
   }
 };
 
@@ -298,8 +317,12 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(con
                                 &raw[i][n]);
     }
     if (!staged) {  // while the first rows are on their way
-      own.stage(a.weight, a.weight_fp32, a.cols, 1.0f, weight);
-      own.stage(a.bias, a.weight_fp32, a.cols, 0.0f, bias);
+      for (int four = threadIdx.x; four < kN * 2 * a.lanes; four += blockDim.x) {
+        const float4 w = own.load_four(a.weight, a.weight_fp32, four, a.cols, 1.0f);
+        const float4 b = own.load_four(a.bias, a.weight_fp32, four, a.cols, 0.0f);
+        own.store_four(weight, four, w);
+        own.store_four(bias, four, b);
+      }
       __syncthreads();
       staged = true;
       if (r0 >= a.rows) break;
@@ -308,32 +331,42 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(con
     if (a.center) {
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
+        F2 s = 0;
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
-          float x[8];
-          widen_eight<kFp32, kVec>(raw[i][n], x);
-          mean[i] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+          F2 x[4];
+          widen_pairs<kFp32, kVec>(raw[i][n], x);
+          s = add2(s, add2(add2(x[0], x[1]), add2(x[2], x[3])));
         }
+        mean[i] = sum_of(s);
       }
       sum(mean);
     }
+    F2 less[kRows];  // minus the mean
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       mean[i] *= a.inv_cols;
+      less[i] = both(-mean[i]);
+      F2 s = 0;
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
-        float x[8], part = 0.0f;
+        F2 x[4], part = 0;
         forget_widened(raw[i][n]);
-        widen_eight<kFp32, kVec>(raw[i][n], x);
+        widen_pairs<kFp32, kVec>(raw[i][n], x);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float d = x[k] - mean[i];
-          if (kVec == 1 && own.column_of(n, k) >= a.cols) d = 0.0f;
-          part = fmaf(d, d, part);
+        for (int k = 0; k < 4; ++k) {
+          F2 d = add2(x[k], less[i]);
+          if constexpr (kVec == 1) {
+            float lo, hi;
+            split(d, &lo, &hi);
+            d = pair(own.column_of(n, 2 * k) < a.cols ? lo : 0.0f, own.column_of(n, 2 * k + 1) < a.cols ? hi : 0.0f);
+          }
+          part = fma2(d, d, part);
         }
-        if (kVec == 8 && own.column_of(n, 0) >= a.cols) part = 0.0f;
-        total[i] += part;
+        if (kVec == 8 && own.column_of(n, 0) >= a.cols) part = 0;
+        s = add2(s, part);
       }
+      total[i] = sum_of(s);
     }
     sum(total);
 #pragma unroll
@@ -346,24 +379,25 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(con
     }
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
-      float w[8], b[8];
+      F2 w[4], b[4];
       own.read(weight, n, w);
       own.read(bias, n, b);
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const long long r = r0 + step * i;
         const bool real = r < a.rows;
-        float x[8];
+        F2 x[4];
         forget_widened(raw[i][n]);
-        widen_eight<kFp32, kVec>(raw[i][n], x);
+        widen_pairs<kFp32, kVec>(raw[i][n], x);
         if constexpr (kPack) {
           pack_eight<kVec>(x, own.lane_of(n), own.lanes, a.groups - own.at(n) / kPackGroup, real, a.form,
                            a.codes + r * a.groups * kPackGroup + own.at(n), a.scales + r * a.groups + own.at(n) / kPackGroup);
         }
+        const F2 rstd = both(total[i]);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = fmaf((x[k] - mean[i]) * total[i], w[k], b[k]);
+        for (int k = 0; k < 4; ++k) x[k] = fma2(mul2(add2(x[k], less[i]), rstd), w[k], b[k]);
         if (real) {
-          store_eight<kFp32, kVec>(static_cast<char*>(a.out) + (r * a.out_stride + own.at(n)) * kSize, own.lane_of(n),
+          store_pairs<kFp32, kVec>(static_cast<char*>(a.out) + (r * a.out_stride + own.at(n)) * kSize, own.lane_of(n),
                                    own.lanes, a.cols - own.at(n), x);
         }
       }
@@ -374,95 +408,196 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(con
 template <bool kFp32, int kVec, int kN>
 constexpr int kBackwardRows = kN * (kFp32 || kVec == 1 ? 2 : 1) >= 4 ? 1 : 2;
 
+// Rows of whole vectors come through shared memory: a thread's copies of its own
+// columns run kStages - 1 turns ahead of it, whatever the barriers of a turn
+// make it wait for.  Bytes of a thread's turn:
+constexpr int kStages = 3;
+template <bool kFp32, int kN, bool kPacked>
+constexpr int kTurnBytes = kBackwardRows<kFp32, 8, kN> * kN * (16 * (kFp32 ? 2 : 1) + (kPacked ? 8 : 16 * (kFp32 ? 2 : 1)));
+
 template <bool kFp32, int kVec, int kN, bool kPacked>
 __global__ void __launch_bounds__(kBackwardWarps * 32, 1) norm_backward_kernel(const __grid_constant__ NormArgs a) {
   constexpr int kRows = kBackwardRows<kFp32, kVec, kN>;
   constexpr long long kSize = kFp32 ? 4 : 2;
+  constexpr bool kAhead = kVec == 8;
+  constexpr int kWords = kFp32 ? 2 : 1;  // 16-byte words of eight elements
   extern __shared__ __align__(16) float tables[];
   __shared__ float buffer[2][kNormWarps][2 * kRows];
   GroupSum<2 * kRows> sum(buffer, a.lanes);
   const Slots<kVec, kN> own{a.lanes, static_cast<int>(threadIdx.x) % a.lanes};
   const int groups = blockDim.x / a.lanes, group = threadIdx.x / a.lanes;
-  const long long step = static_cast<long long>(gridDim.x) * groups;
+  const long long step = static_cast<long long>(gridDim.x) * groups * kRows;
   const long long mine = blockIdx.x + static_cast<long long>(gridDim.x) * group;
-  float dw[kN][8] = {}, db[kN][8] = {};
-  own.stage(a.weight, a.weight_fp32, a.cols, 1.0f, tables);
-  __syncthreads();
-  for (long long r0 = mine; r0 < a.rows; r0 += step * kRows) {
-    Eight<kFp32, kVec> raw[kRows][kN], grad[kRows][kN];
-    EightCodes<kVec> codes[kRows][kN];
-    float2 stats[kRows];
+  F2 dw[kN][4] = {}, db[kN][4] = {};
+  // the copies' places: [stage][row][n][dy's words, then x's][thread]
+  constexpr int kTurn = kAhead ? kTurnBytes<kFp32, kN, kPacked> : 0;
+  char* const ring = reinterpret_cast<char*>(tables + kN * 8 * a.lanes);
+  auto place = [&](int stage, int i, int n, int word) {  // of dy's words, x's words and x's codes
+    const int at = kRows * kN * 16 * word + (i * kN + n) * (word < 2 * kWords && !(kPacked && word >= kWords) ? 16 : 8);
+    return ring + (static_cast<size_t>(stage) * kTurn + at) * blockDim.x +
+           threadIdx.x * (kPacked && word >= kWords ? 8 : 16);
+  };
+  auto copy = [&](long long r0, int stage) {
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const long long r = r0 + static_cast<long long>(gridDim.x) * groups * i;
+        if (r < a.rows) {
+          const char* row = static_cast<const char*>(a.x) + r * a.x_stride * kSize;
+          const char* drow = static_cast<const char*>(a.dy) + r * a.dy_stride * kSize;
+#pragma unroll
+          for (int n = 0; n < kN; ++n) {
+            const int v = own.lane_of(n);
+            if (v * 8 >= a.cols) continue;
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+              copy_async<16>(place(stage, i, n, w), drow + (v * kWords + w) * 16LL);
+              if constexpr (!kPacked) copy_async<16>(place(stage, i, n, kWords + w), row + (v * kWords + w) * 16LL);
+            }
+            if constexpr (kPacked) copy_async<8>(place(stage, i, n, kWords), a.codes + r * a.groups * kPackGroup + v * 8LL);
+          }
+        }
+      }
+      copy_commit();
+    }
+  };
+  // what a turn needs beside: the rows' statistics and scales, a turn ahead
+  float2 stats[kRows], next_stats[kRows];
+  uint32_t scales[kRows][kN], next_scales[kRows][kN];
+  auto look_ahead = [&](long long r0) {
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const long long r = r0 + step * i;
-      const bool real = r < a.rows;
-      stats[i] = real ? a.stats[r] : make_float2(0.0f, 0.0f);
-      const char* row = static_cast<const char*>(a.x) + r * a.x_stride * kSize;
-      const char* drow = static_cast<const char*>(a.dy) + r * a.dy_stride * kSize;
+      const long long r = r0 + static_cast<long long>(gridDim.x) * groups * i;
+      next_stats[i] = r < a.rows ? a.stats[r] : make_float2(0.0f, 0.0f);
+      if constexpr (kPacked && kAhead) {
 #pragma unroll
-      for (int n = 0; n < kN; ++n) {
-        if constexpr (kPacked) {
-          load_codes<kVec>(a.codes + r * a.groups * kPackGroup + own.at(n), a.scales + r * a.groups + own.at(n) / kPackGroup,
-                           own.lane_of(n), own.lanes, real ? a.groups - own.at(n) / kPackGroup : 0, &codes[i][n]);
-        } else {
-          load_eight<kFp32, kVec>(row + own.at(n) * kSize, own.lane_of(n), own.lanes, real ? a.cols - own.at(n) : 0,
-                                  &raw[i][n]);
-        }
-        load_eight<kFp32, kVec>(drow + own.at(n) * kSize, own.lane_of(n), own.lanes, real ? a.cols - own.at(n) : 0,
-                                &grad[i][n]);
+        for (int n = 0; n < kN; ++n)
+          next_scales[i][n] = r < a.rows && own.lane_of(n) * 8 < a.cols ? a.scales[r * a.groups + own.lane_of(n) / 4] : 0u;
       }
     }
-    // xn, and dy; columns past the last: nothing of the mean, of the row's inf or NaN
-    auto values = [&](int i, int n, float* xn, float* g) {
-      if constexpr (kPacked) widen_codes<kVec>(codes[i][n], a.form, xn);
-      else widen_eight<kFp32, kVec>(raw[i][n], xn);
-      widen_eight<kFp32, kVec>(grad[i][n], g);
-      const bool some = kVec == 8 && own.column_of(n, 0) < a.cols;
+  };
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        xn[k] = (kVec == 8 ? some : own.column_of(n, k) < a.cols) ? (xn[k] - stats[i].x) * stats[i].y : 0.0f;
+  for (int s = 0; s < kStages - 1; ++s) copy(mine + step * s, s);
+  look_ahead(mine);
+  for (int four = threadIdx.x; four < kN * 2 * a.lanes; four += blockDim.x)
+    own.store_four(tables, four, own.load_four(a.weight, a.weight_fp32, four, a.cols, 1.0f));
+  __syncthreads();
+  int stage = 0;
+  for (long long r0 = mine; r0 < a.rows; r0 += step) {
+    Eight<kFp32, kVec> raw[kRows][kN], grad[kRows][kN];
+    EightCodes<kVec> codes[kRows][kN];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      stats[i] = next_stats[i];
+#pragma unroll
+      for (int n = 0; n < kN; ++n) scales[i][n] = kPacked && kAhead ? next_scales[i][n] : 0u;
+    }
+    look_ahead(r0 + step);
+    if constexpr (kAhead) {
+      copy(r0 + step * (kStages - 1), (stage + kStages - 1) % kStages);  // where the turn before this one was
+      copy_wait<kStages - 1>();
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const bool real = r0 + static_cast<long long>(gridDim.x) * groups * i < a.rows;
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          const bool some = real && own.lane_of(n) * 8 < a.cols;
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) {
+            uint4 u = make_uint4(0u, 0u, 0u, 0u), v = u;
+            if (some) {
+              u = *reinterpret_cast<const uint4*>(place(stage, i, n, w));
+              if constexpr (!kPacked) v = *reinterpret_cast<const uint4*>(place(stage, i, n, kWords + w));
+            }
+            grad[i][n].w[4 * w] = u.x; grad[i][n].w[4 * w + 1] = u.y; grad[i][n].w[4 * w + 2] = u.z; grad[i][n].w[4 * w + 3] = u.w;
+            raw[i][n].w[4 * w] = v.x; raw[i][n].w[4 * w + 1] = v.y; raw[i][n].w[4 * w + 2] = v.z; raw[i][n].w[4 * w + 3] = v.w;
+          }
+          if constexpr (kPacked) {
+            const uint2 u = some ? *reinterpret_cast<const uint2*>(place(stage, i, n, kWords)) : make_uint2(0u, 0u);
+            codes[i][n].w[0] = u.x; codes[i][n].w[1] = u.y; codes[i][n].w[2] = scales[i][n];
+          }
+        }
+      }
+      stage = (stage + 1) % kStages;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const long long r = r0 + static_cast<long long>(gridDim.x) * groups * i;
+        const bool real = r < a.rows;
+        const char* row = static_cast<const char*>(a.x) + r * a.x_stride * kSize;
+        const char* drow = static_cast<const char*>(a.dy) + r * a.dy_stride * kSize;
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+          if constexpr (kPacked) {
+            load_codes<kVec>(a.codes + r * a.groups * kPackGroup + own.at(n), a.scales + r * a.groups + own.at(n) / kPackGroup,
+                             own.lane_of(n), own.lanes, real ? a.groups - own.at(n) / kPackGroup : 0, &codes[i][n]);
+          } else {
+            load_eight<kFp32, kVec>(row + own.at(n) * kSize, own.lane_of(n), own.lanes, real ? a.cols - own.at(n) : 0,
+                                    &raw[i][n]);
+          }
+          load_eight<kFp32, kVec>(drow + own.at(n) * kSize, own.lane_of(n), own.lanes, real ? a.cols - own.at(n) : 0,
+                                  &grad[i][n]);
+        }
+      }
+    }
+    // xn, and dy (columns past the last: dy is zero, and what they add to sums, too)
+    auto values = [&](int i, int n, F2* xn, F2* g) {
+      if constexpr (kPacked) widen_codes<kVec>(codes[i][n], a.form, xn);
+      else widen_pairs<kFp32, kVec>(raw[i][n], xn);
+      widen_pairs<kFp32, kVec>(grad[i][n], g);
+      const F2 less = both(-stats[i].x), rstd = both(stats[i].y);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) xn[k] = mul2(add2(xn[k], less), rstd);
     };
-    float total[2 * kRows] = {};
+    F2 one[kRows] = {}, two[kRows] = {};
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
-      float w[8];
+      F2 w[4];
       own.read(tables, n, w);
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        float xn[8], g[8];
+        F2 xn[4], g[4];
         values(i, n, xn, g);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          dw[n][k] = fmaf(g[k], xn[k], dw[n][k]);
-          db[n][k] += g[k];
-          g[k] *= w[k];
-          total[2 * i] += g[k];
-          total[2 * i + 1] = fmaf(g[k], xn[k], total[2 * i + 1]);
+        for (int k = 0; k < 4; ++k) {
+          dw[n][k] = fma2(g[k], xn[k], dw[n][k]);
+          db[n][k] = add2(db[n][k], g[k]);
+          g[k] = mul2(g[k], w[k]);
+          one[i] = add2(one[i], g[k]);
+          two[i] = fma2(g[k], xn[k], two[i]);
         }
       }
+    }
+    float total[2 * kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      total[2 * i] = sum_of(one[i]);
+      total[2 * i + 1] = sum_of(two[i]);
     }
     sum(total);
 #pragma unroll
     for (int n = 0; n < kN; ++n) {
-      float w[8];
+      F2 w[4];
       own.read(tables, n, w);
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        const long long r = r0 + step * i;
+        const long long r = r0 + static_cast<long long>(gridDim.x) * groups * i;
         if (r >= a.rows) continue;
-        const float m1 = a.center ? total[2 * i] * a.inv_cols : 0.0f, m2 = total[2 * i + 1] * a.inv_cols;
-        float xn[8], g[8];
+        const F2 m1 = both(a.center ? -total[2 * i] * a.inv_cols : 0.0f), m2 = both(-total[2 * i + 1] * a.inv_cols);
+        const F2 rstd = both(stats[i].y);
+        F2 xn[4], g[4];
         if constexpr (kPacked) forget_widened(codes[i][n]);
         else forget_widened(raw[i][n]);
         forget_widened(grad[i][n]);
         values(i, n, xn, g);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) g[k] = stats[i].y * fmaf(-xn[k], m2, fmaf(g[k], w[k], -m1));
-        store_eight<kFp32, kVec>(static_cast<char*>(a.out) + (r * a.out_stride + own.at(n)) * kSize, own.lane_of(n),
+        for (int k = 0; k < 4; ++k) g[k] = mul2(rstd, fma2(xn[k], m2, fma2(g[k], w[k], m1)));
+        store_pairs<kFp32, kVec>(static_cast<char*>(a.out) + (r * a.out_stride + own.at(n)) * kSize, own.lane_of(n),
                                  own.lanes, a.cols - own.at(n), g);
       }
     }
   }
+  if constexpr (kAhead) copy_wait<0>();
   if (!a.partials) return;
   // the CTA's sums: one group after another adds its own, in the weights' place
   float* part = a.partials + static_cast<long long>(blockIdx.x) * 2 * a.cols;
@@ -474,10 +609,12 @@ __global__ void __launch_bounds__(kBackwardWarps * 32, 1) norm_backward_kernel(c
       if (turn != group) continue;
 #pragma unroll
       for (int n = 0; n < kN; ++n) {
+        float mine[8];
+        from_pairs(which ? db[n] : dw[n], mine);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           const int at = own.slot(own.column_of(n, k));
-          const float s = which ? db[n][k] : dw[n][k];
+          const float s = mine[k];
           tables[at] = turn ? tables[at] + s : s;
         }
       }
@@ -624,19 +761,24 @@ struct Shape {
   bool vec;
 };
 // most: the largest kN that the pass has registers for (single elements: 2).
-Shape shape_of(int cols, bool vec, int most, int cta_warps) {
+// Where every row can have an SM to itself, it is spread over as many warps as
+// there are (1 row of 2048: 2.0 us of device time, 3.7 us as one warp of many).
+Shape shape_of(int cols, long long rows, bool vec, int most, int cta_warps) {
   if (cols > kNormWidest) return {0, kWideThreads, 0, false};
   const int eights = (cols + 7) / 8;
   if (vec && cols <= kLaneCols) return {power_of_two(eights), kLaneThreads, 1, true};
   if (!vec && most > 2) most = 2;
+  const bool alone = rows <= sm_count();
   const int warps = (eights + 31) / 32;
   int n = 1;
-  while (n < most && n < warps) n *= 2;
-  const int lanes = (warps + n - 1) / n * 32, groups = cta_warps * 32 / lanes;
+  while (n < most && (alone ? n * cta_warps < warps : n < warps)) n *= 2;
+  const int lanes = (warps + n - 1) / n * 32, groups = alone ? 1 : cta_warps * 32 / lanes;
   return {lanes, groups * lanes, n, vec};
 }
-Shape forward_shape(int cols, bool vec, bool fp32) { return shape_of(cols, vec, fp32 ? 4 : 8, kForwardWarps); }
-Shape backward_shape(int cols, bool vec) { return shape_of(cols, vec, 2, kBackwardWarps); }
+Shape forward_shape(int cols, long long rows, bool vec, bool fp32) {
+  return shape_of(cols, rows, vec, fp32 ? 4 : 8, kForwardWarps);
+}
+Shape backward_shape(int cols, long long rows, bool vec) { return shape_of(cols, rows, vec, 2, kBackwardWarps); }
 
 // CTAs for all rows: what is resident at once, at most.
 int norm_ctas(const Shape& s, long long rows) {
@@ -651,23 +793,21 @@ int wide_parts(long long rows) { return static_cast<int>(rows < 32 ? (rows ? row
 int parts_of(const Shape& s, long long rows) { return s.lanes ? norm_ctas(s, rows) : wide_parts(rows); }
 // ... whether or not the tensors turn out to be aligned, for the workspace.
 int most_parts(int cols, long long rows) {
-  const int a = parts_of(backward_shape(cols, false), rows), b = parts_of(backward_shape(cols, true), rows);
+  const int a = parts_of(backward_shape(cols, rows, false), rows), b = parts_of(backward_shape(cols, rows, true), rows);
   return a > b ? a : b;
 }
 
-// Dynamic shared memory beyond what every kernel may have; set anew each time, as
-// it belongs to the current context.
-template <typename Kernel>
-void launch_with(Kernel kernel, const NormArgs& a, const Shape& s, int ctas, int tables, cudaStream_t st) {
-  const int bytes = tables * s.n * 8 * s.lanes * static_cast<int>(sizeof(float));
-  if (bytes > 40 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  kernel<<<ctas, s.threads, bytes, st>>>(a);
+template <auto kKernel>
+void launch_with(const NormArgs& a, const Shape& s, int ctas, int bytes, cudaStream_t st) {
+  if (bytes > 40 * 1024 && allow_shared<kKernel>() != cudaSuccess) return;  // reported as the launch's error
+  kKernel<<<ctas, s.threads, bytes, st>>>(a);
 }
 
 template <bool kFp32, int kVec, int kN>
 void launch_forward_n(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st) {
-  if (a.form) launch_with(norm_forward_kernel<kFp32, kVec, kN, true>, a, s, ctas, 2, st);
-  else launch_with(norm_forward_kernel<kFp32, kVec, kN, false>, a, s, ctas, 2, st);
+  const int bytes = 2 * kN * 8 * s.lanes * static_cast<int>(sizeof(float));
+  if (a.form) launch_with<norm_forward_kernel<kFp32, kVec, kN, true>>(a, s, ctas, bytes, st);
+  else launch_with<norm_forward_kernel<kFp32, kVec, kN, false>>(a, s, ctas, bytes, st);
 }
 template <bool kFp32, int kVec>
 void launch_forward(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st) {
@@ -681,13 +821,19 @@ void launch_forward(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st
   if (s.n == 2) launch_forward_n<kFp32, kVec, 2>(a, s, ctas, st);
   else launch_forward_n<kFp32, kVec, 1>(a, s, ctas, st);
 }
+template <bool kFp32, int kVec, int kN, bool kPacked>
+void launch_backward_n(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st) {
+  const int bytes = kN * 8 * s.lanes * static_cast<int>(sizeof(float)) +
+                    (kVec == 8 ? kStages * kTurnBytes<kFp32, kN, kPacked> * s.threads : 0);
+  launch_with<norm_backward_kernel<kFp32, kVec, kN, kPacked>>(a, s, ctas, bytes, st);
+}
 template <bool kFp32, int kVec, bool kPacked>
 void launch_backward(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st) {
   if constexpr (kVec == 8) {
     if (s.lanes < 32) return norm_lanes_backward_kernel<kFp32, kPacked><<<ctas, s.threads, 0, st>>>(a);
   }
-  if (s.n == 2) launch_with(norm_backward_kernel<kFp32, kVec, 2, kPacked>, a, s, ctas, 1, st);
-  else launch_with(norm_backward_kernel<kFp32, kVec, 1, kPacked>, a, s, ctas, 1, st);
+  if (s.n == 2) launch_backward_n<kFp32, kVec, 2, kPacked>(a, s, ctas, st);
+  else launch_backward_n<kFp32, kVec, 1, kPacked>(a, s, ctas, st);
 }
 template <bool kFp32, bool kPacked>
 void launch_wide_backward(const NormArgs& a, int ctas, cudaStream_t st) {
@@ -775,7 +921,7 @@ zero_status zero_layer_norm(const zero_norm_config* cfg, int64_t rows, const voi
   a.stats = reinterpret_cast<float2*>(stats);
   const bool vec = a.cols % 8 == 0 && rows_aligned(x, x_stride, rows, cfg->dtype) && rows_aligned(y, y_stride, rows, cfg->dtype);
   const bool fp32 = cfg->dtype == ZERO_GRAD_FP32;
-  const Shape s = forward_shape(a.cols, vec, fp32);
+  const Shape s = forward_shape(a.cols, rows, vec, fp32);
   const int ctas = norm_ctas(s, rows);
   a.lanes = s.lanes;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
@@ -845,7 +991,7 @@ zero_status zero_layer_norm_backward(const zero_norm_config* cfg, int64_t rows, 
     a.stats = const_cast<float2*>(reinterpret_cast<const float2*>(stats));
     const bool vec = a.cols % 8 == 0 && (packed || rows_aligned(x, x_stride, rows, cfg->dtype)) &&
                      rows_aligned(dy, dy_stride, rows, cfg->dtype) && rows_aligned(dx, dx_stride, rows, cfg->dtype);
-    const Shape s = backward_shape(a.cols, vec);
+    const Shape s = backward_shape(a.cols, rows, vec);
     const int ctas = norm_ctas(s, rows);
     a.lanes = s.lanes;
     a.parts = parts_of(s, rows);

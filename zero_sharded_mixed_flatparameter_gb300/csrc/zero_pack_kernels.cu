@@ -10,6 +10,10 @@ namespace zfs {
 namespace {
 
 constexpr int kPackThreads = 256;
+template <int kVec>
+constexpr int kPackRows = kVec == 8 ? 4 : 1;  // in flight
+template <int kVec>
+constexpr int kPackCtas = kVec == 8 ? 5 : 4;  // of an SM (48, 64 registers)
 
 struct PackArgs {
   long long rows;
@@ -22,8 +26,8 @@ struct PackArgs {
 
 // A thread takes eight columns of kRows rows at a time, `lanes` threads a row.
 template <bool kFp32, int kVec, bool kPack>
-__global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constant__ PackArgs a) {
-  constexpr int kRows = 4;  // in flight
+__global__ void __launch_bounds__(kPackThreads, kPackCtas<kVec>) pack_kernel(const __grid_constant__ PackArgs a) {
+  constexpr int kRows = kPackRows<kVec>;
   constexpr long long kSize = kFp32 ? 4 : 2;
   const int lanes = a.lanes, lane = threadIdx.x % lanes, per_cta = kPackThreads / lanes;
   const long long step = static_cast<long long>(gridDim.x) * per_cta;
@@ -49,15 +53,15 @@ __global__ void __launch_bounds__(kPackThreads) pack_kernel(const __grid_constan
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const long long r = mine + step * i;
-        float x[8];
+        F2 x[4];
         if constexpr (kPack) {
-          widen_eight<kFp32, kVec>(raw[i], x);
+          widen_pairs<kFp32, kVec>(raw[i], x);
           pack_eight<kVec>(x, lane, lanes, groups, r < a.rows, a.form, a.codes + r * a.groups * kPackGroup + at,
                            a.scales + r * a.groups + at / kPackGroup);
         } else {
           widen_codes<kVec>(codes[i], a.form, x);
           if (r < a.rows) {
-            store_eight<kFp32, kVec>(static_cast<char*>(a.x) + (r * a.x_stride + at) * kSize, lane, lanes, cols, x);
+            store_pairs<kFp32, kVec>(static_cast<char*>(a.x) + (r * a.x_stride + at) * kSize, lane, lanes, cols, x);
           }
         }
       }
@@ -103,7 +107,7 @@ zero_status convert(int64_t rows, int64_t cols, const void* x, int32_t dtype, in
   const int need = (a.cols + 7) / 8, lanes = power_of_two(need < kPackThreads ? need : kPackThreads);
   a.lanes = vec || lanes >= 32 ? lanes : 32;
   const long long per_cta = kPackThreads / a.lanes, want = (rows + per_cta - 1) / per_cta;
-  const long long most = static_cast<long long>(sm_count()) * (2048 / kPackThreads);
+  const long long most = static_cast<long long>(sm_count()) * (vec ? kPackCtas<8> : kPackCtas<1>);
   const int ctas = static_cast<int>(want < most ? want : most);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (pack) launch_pack<true>(a, dtype == ZERO_GRAD_FP32, vec, ctas, s);

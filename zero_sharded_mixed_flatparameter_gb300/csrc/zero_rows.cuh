@@ -66,6 +66,20 @@ __device__ __forceinline__ void widen_eight(const Eight<kFp32, kVec>& v, float* 
   }
 }
 
+// Asynchronous copies of a thread's own bytes to its own place in shared memory:
+// it waits for its own groups of copies, with no barrier and nothing to poll.
+template <int kBytes>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+  if constexpr (kBytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(kBytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kPending>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
 // Widened anew where it is used again: eight fp32 values kept instead take twice
 // the registers of the loaded words (bf16), four times those of codes.
 template <typename T>
@@ -97,6 +111,58 @@ __device__ __forceinline__ void store_eight(void* row, int lane, int lanes, int 
       }
     }
   }
+}
+
+// Two fp32 values in one register pair: the packed instructions round each like
+// the single ones, at half the instructions.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 both(float x) { return pair(x, x); }
+__device__ __forceinline__ void split(F2 v, float* lo, float* hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v)); }
+__device__ __forceinline__ float sum_of(F2 v) {
+  float lo, hi;
+  split(v, &lo, &hi);
+  return lo + hi;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ void to_pairs(const float* x, F2* p) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) p[k] = pair(x[2 * k], x[2 * k + 1]);
+}
+__device__ __forceinline__ void from_pairs(const F2* p, float* x) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) split(p[k], &x[2 * k], &x[2 * k + 1]);
+}
+
+template <bool kFp32, int kVec>
+__device__ __forceinline__ void widen_pairs(const Eight<kFp32, kVec>& v, F2* p) {
+  float x[8];
+  widen_eight<kFp32, kVec>(v, x);
+  to_pairs(x, p);
+}
+template <bool kFp32, int kVec>
+__device__ __forceinline__ void store_pairs(void* row, int lane, int lanes, int cols, const F2* p) {
+  float x[8];
+  from_pairs(p, x);
+  store_eight<kFp32, kVec>(row, lane, lanes, cols, x);
 }
 
 // Element `at` of a bf16 or fp32 vector (weights, biases, their gradients).
@@ -171,8 +237,10 @@ __device__ __forceinline__ float decode1(uint32_t code, int form) {
 // multiple of 32); `write`: the thread's row exists.  Codes past the last column
 // of the last group are zero.
 template <int kVec>
-__device__ __forceinline__ void pack_eight(const float* x, int lane, int lanes, int groups, bool write, int form,
+__device__ __forceinline__ void pack_eight(const F2* p, int lane, int lanes, int groups, bool write, int form,
                                            uint8_t* codes, uint8_t* scales) {
+  float x[8];
+  from_pairs(p, x);
   if constexpr (kVec == 8) {
     uint32_t m = 0;
 #pragma unroll
@@ -183,10 +251,12 @@ __device__ __forceinline__ void pack_eight(const float* x, int lane, int lanes, 
       if (o < lanes) m = max(m, other);
     }
     const uint32_t byte = scale_byte(m, form);
-    const float inv = inverse_scale(byte);
-    float s[8];
+    const F2 inv = both(inverse_scale(byte));
+    F2 q[4];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s[k] = x[k] * inv;
+    for (int k = 0; k < 4; ++k) q[k] = mul2(p[k], inv);
+    float s[8];
+    from_pairs(q, s);
     uint2 c = make_uint2(encode4(s, form), encode4(s + 4, form));
     if (byte == 255u) c = make_uint2(0u, 0u);
     if (write && lane < groups * 4) {
@@ -194,19 +264,21 @@ __device__ __forceinline__ void pack_eight(const float* x, int lane, int lanes, 
       if (lane % 4 == 0) scales[lane / 4] = static_cast<uint8_t>(byte);
       // fewer lanes than a group's quarters: the rest of the only group
       if (lane + 1 == lanes) {
-        for (int q = lanes; q < 4; ++q) *reinterpret_cast<uint2*>(codes + q * 8) = make_uint2(0u, 0u);
+        for (int q4 = lanes; q4 < 4; ++q4) *reinterpret_cast<uint2*>(codes + q4 * 8) = make_uint2(0u, 0u);
       }
     }
   } else {
+    // every element's group is a warp's: eight independent ones
+    uint32_t byte[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      byte[k] = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(x[k]) & 0x7FFFFFFFu), form);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      if ((k * lanes + (lane & ~31)) / kPackGroup >= groups) break;  // the same for the whole warp
-      const uint32_t byte = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(x[k]) & 0x7FFFFFFFu), form);
-      const uint32_t c = byte == 255u ? 0u : encode1(x[k] * inverse_scale(byte), form);
       const int at = k * lanes + lane;
-      if (write) {
-        codes[at] = static_cast<uint8_t>(c);
-        if (lane % 32 == 0) scales[at / kPackGroup] = static_cast<uint8_t>(byte);
+      if (write && at / kPackGroup < groups) {
+        codes[at] = static_cast<uint8_t>(byte[k] == 255u ? 0u : encode1(x[k] * inverse_scale(byte[k]), form));
+        if (lane % 32 == 0) scales[at / kPackGroup] = static_cast<uint8_t>(byte[k]);
       }
     }
   }
@@ -238,16 +310,19 @@ __device__ __forceinline__ void load_codes(const uint8_t* codes, const uint8_t* 
   }
 }
 template <int kVec>
-__device__ __forceinline__ void widen_codes(const EightCodes<kVec>& v, int form, float* x) {
+__device__ __forceinline__ void widen_codes(const EightCodes<kVec>& v, int form, F2* p) {
+  float x[8];
   if constexpr (kVec == 8) {
-    const float s = scale_value(v.w[2]);
+    const F2 s = both(scale_value(v.w[2]));
     decode4(v.w[0], form, x);
     decode4(v.w[1], form, x + 4);
+    to_pairs(x, p);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] *= s;
+    for (int k = 0; k < 4; ++k) p[k] = mul2(p[k], s);
   } else {
 #pragma unroll
     for (int k = 0; k < 8; ++k) x[k] = decode1(v.w[k] & 0xFFu, form) * scale_value(v.w[k] >> 8);
+    to_pairs(x, p);
   }
 }
 

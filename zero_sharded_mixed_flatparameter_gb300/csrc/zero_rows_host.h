@@ -2,6 +2,7 @@
 // error texts.  Not part of the public ABI.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cstdio>
 
@@ -41,6 +42,20 @@ inline int power_of_two(int x) {
   int p = 1;
   while (p < x) p *= 2;
   return p;
+}
+
+// Lets a kernel have kMostShared bytes of dynamic shared memory, once a context
+// (the limit belongs to it).
+constexpr int kMostShared = 225 * 1024;
+template <auto kKernel>
+cudaError_t allow_shared() {
+  static std::atomic<unsigned long long> done{~0ull};
+  unsigned long long id = 0;
+  const bool known = current_context_id(&id);
+  if (known && done.load(std::memory_order_relaxed) == id) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+  if (e == cudaSuccess && known) done.store(id, std::memory_order_relaxed);
+  return e;
 }
 
 // Launches that may become resident while the kernel before them finishes (the
