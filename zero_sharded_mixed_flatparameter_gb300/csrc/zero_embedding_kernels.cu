@@ -4,14 +4,14 @@
 //   out[t] = scale * table[id[t]]         (zeros where id[t] is no row)
 //   dtable[v] = scale * sum of dout[t] over the tokens t with id[t] = v
 //
-// The gradient takes three launches.  The first sorts: every CTA owns a range
-// of rows, reads all ids (they stay in L2), counts those before its range (so
-// that it knows where its tokens go without asking another CTA) and places its
-// own in the order of (row, token).  The second sums: a run of kChunk sorted
-// tokens at a time, rows that lie in one run whole, the run's first and last
-// row in part, and zeros for the rows without tokens.  The third joins the
-// parts of a row in order.  Each sum has one order: the same call gives the
-// same bits.
+// The gradient takes three launches.  The first sorts: every CTA owns the rows of
+// one remainder (frequent tokens often have neighbouring ids), reads all ids (they
+// stay in L2), counts those of lower remainders (so that it knows where its tokens
+// go without asking another CTA) and places its own in the order of (row, token).
+// The second sums: a run of sorted tokens at a time, with the rest of its
+// last row, and writes zeros to the rows without tokens; a row of more than twice
+// as many tokens is summed in parts, one a run.  The third joins the parts in order.
+// Each sum has one order: the same call gives the same bits.
 
 #include <cmath>
 
@@ -24,11 +24,13 @@ namespace zfs {
 namespace {
 
 constexpr int kEmbThreads = 256;
+constexpr int kLookupCtas = 4;    // of an SM
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
-constexpr int kSortRows = 1536;   // of a CTA at most: a counter for each and every warp, 192 KB
+constexpr int kSortCtas = 128;    // a power of two
+constexpr int kSortRows = 1024;   // of a CTA at most: a counter for each and every warp, 128 KB
 constexpr int kSortLoads = 8;     // ids in flight per lane
-constexpr int kChunk = 32;        // sorted tokens of a run
-constexpr int kZeroRows = 16;     // table rows of a CTA that writes zeros
+constexpr int kSortList = 128;    // tokens that a warp keeps, else it reads its ids again
+constexpr int kLeastChunk = 8, kMostChunk = 32;  // sorted tokens of a run
 constexpr int kJoinWarps = 8;
 
 struct EmbArgs {
@@ -42,37 +44,45 @@ struct EmbArgs {
   float scale;
   int accumulate;
   // gradient
-  int2* sorted;                // (token, row) in the order of (row, token)
-  int* begin;                  // [vocab + 1] where a row's tokens begin in it
-  int* crossing;               // how many runs end in the middle of a row's first part, then which
-  float* parts;                // [run][part of the row before, of the last row][pitch]
-  int pitch, per_cta;          // pitch: columns of a part, per_cta: table rows of a sorting CTA
-  int runs, slabs;
+  int4* sorted;                // token, row, where the row's tokens begin and end, in the order of the rows
+  int* counts;                 // [vocab] tokens of a row
+  int* live;                   // tokens that have a row; then how many rows are in parts
+  int4* heavy;                 // the rows in parts: first run, row, how many runs
+  float* parts;                // [run][of a row that began before it, of its last row][pitch]
+  int pitch, slabs;            // pitch: columns of a part, slabs: of 128 columns
+  int remainders, per_cta;     // sorting CTAs, rows of each
+  int runs, chunk;             // runs of `chunk` sorted tokens
+  int columns;                 // warps for the columns of a run
 };
 
-// The row of token t, -1 if it has none.
-__device__ __forceinline__ int row_of(const EmbArgs& a, long long t) {
-  if (a.wide_ids) {
-    const long long id = static_cast<const long long*>(a.ids)[t];
-    return id >= 0 && id < a.vocab ? static_cast<int>(id) : -1;
-  }
-  const int id = static_cast<const int*>(a.ids)[t];
-  return id >= 0 && id < a.vocab ? id : -1;
+// The row of an id, -1 if it has none.
+template <typename Id>
+__device__ __forceinline__ int row_of(Id id, int vocab) {
+  return id >= 0 && id < vocab ? static_cast<int>(id) : -1;
 }
 
-template <bool kFp32, int kVec>
-__global__ void __launch_bounds__(kEmbThreads) embedding_kernel(const __grid_constant__ EmbArgs a) {
+template <bool kFp32, int kVec, typename Id>
+__global__ void __launch_bounds__(kEmbThreads, kLookupCtas) embedding_kernel(const __grid_constant__ EmbArgs a) {
   constexpr int kRows = 4;  // in flight
   constexpr long long kSize = kFp32 ? 4 : 2;
+  const Id* ids = static_cast<const Id*>(a.ids);
   const int lanes = a.lanes, lane = threadIdx.x % lanes, per_cta = kEmbThreads / lanes;
   const long long step = static_cast<long long>(gridDim.x) * per_cta;
   const int at = blockIdx.y * lanes * 8, cols = a.dim - at;
-  for (long long t0 = static_cast<long long>(blockIdx.x) * per_cta + threadIdx.x / lanes; t0 < a.tokens;
-       t0 += step * kRows) {
+  const long long first = static_cast<long long>(blockIdx.x) * per_cta + threadIdx.x / lanes;
+  // the next ids are read while the rows of these are on their way
+  Id next[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) next[i] = first + step * i < a.tokens ? ids[first + step * i] : -1;
+  for (long long t0 = first; t0 < a.tokens; t0 += step * kRows) {
     int row[kRows];
     Eight<kFp32, kVec> raw[kRows];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) row[i] = t0 + step * i < a.tokens ? row_of(a, t0 + step * i) : -1;
+    for (int i = 0; i < kRows; ++i) {
+      row[i] = row_of(next[i], a.vocab);
+      const long long after = t0 + step * (kRows + i);
+      next[i] = after < a.tokens ? ids[after] : -1;
+    }
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
       load_eight<kFp32, kVec>(static_cast<const char*>(a.rows) + (row[i] * a.row_stride + at) * kSize, lane, lanes,
@@ -96,54 +106,84 @@ __device__ __forceinline__ int warp_total(int x) {
   return x;
 }
 
-// Calls f(token, row - first, lanes of the warp that call it now, those of them
-// with the same row) for every token of the warp's share whose row lies in
-// [first, first + count), in the order of the tokens; returns how many of this
-// lane's tokens have a row before `first`.
+// Calls f(token, row, the lanes that call it now, those of them with the same
+// row) for every token of a warp's list, in order.
 template <typename F>
-__device__ __forceinline__ int walk_tokens(const EmbArgs& a, int first, int count, F f) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const long long share = (a.tokens + kSortThreads - 1) / kSortThreads * 32;
-  const long long end = (warp + 1) * share < a.tokens ? (warp + 1) * share : a.tokens;
-  int before = 0;
-  for (long long t0 = warp * share; t0 < end; t0 += 32 * kSortLoads) {
-    int row[kSortLoads];
-#pragma unroll
-    for (int u = 0; u < kSortLoads; ++u) row[u] = t0 + 32 * u + lane < end ? row_of(a, t0 + 32 * u + lane) : -1;
-#pragma unroll
-    for (int u = 0; u < kSortLoads; ++u) {
-      const int r = row[u] - first;
-      before += row[u] >= 0 && r < 0;
-      const bool in = row[u] >= 0 && r >= 0 && r < count;
-      const unsigned some = __ballot_sync(0xffffffffu, in);
-      if (some == 0u) continue;
-      if (in) {
-        f(static_cast<int>(t0 + 32 * u + lane), r, some, __match_any_sync(some, r));
-      }
-      __syncwarp();
+__device__ __forceinline__ void walk_list(const int2* list, int count, F f) {
+  const int lane = threadIdx.x % 32;
+  for (int i = 0; i < count; i += 32) {
+    const bool in = i + lane < count;
+    const unsigned some = __ballot_sync(0xffffffffu, in);
+    if (in) {
+      const int2 e = list[i + lane];
+      f(e.x, e.y, some, __match_any_sync(some, e.y));
     }
+    __syncwarp();
   }
-  return before;
+}
+// The same from the ids, for a warp whose tokens do not fit its list.  rows_of: a
+// CTA's rows have the remainder blockIdx.x, `row` is their quotient.
+struct Share {
+  long long begin, end;  // the warp's tokens
+  int mask, shift;       // remainder, quotient
+};
+template <typename Id, typename F>
+__device__ __forceinline__ void walk_ids(const EmbArgs& a, const Share& own, F f) {
+  const int lane = threadIdx.x % 32;
+  for (long long t = own.begin; t < own.end; t += 32) {
+    const int v = t + lane < own.end ? row_of(static_cast<const Id*>(a.ids)[t + lane], a.vocab) : -1;
+    const bool in = v >= 0 && (v & own.mask) == static_cast<int>(blockIdx.x);
+    const unsigned some = __ballot_sync(0xffffffffu, in);
+    if (in) f(static_cast<int>(t) + lane, v >> own.shift, some, __match_any_sync(some, v));
+    __syncwarp();
+  }
 }
 
+template <typename Id>
 __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __grid_constant__ EmbArgs a) {
-  extern __shared__ int counters[];  // [warp][row]
+  extern __shared__ int shared[];
+  const Id* ids = static_cast<const Id*>(a.ids);
+  __shared__ int2 lists[kSortWarps][kSortList];
   __shared__ int sums[kSortWarps];
   __shared__ int base;
+  int* const counters = shared;                               // [warp][row]
+  int* const begins = counters + kSortWarps * a.per_cta;      // [row], then the end of the last
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const unsigned lower = (1u << lane) - 1u;  // the lanes before this one
-  const int first = blockIdx.x * a.per_cta;
-  const int count = a.vocab - first < a.per_cta ? a.vocab - first : a.per_cta;
+  const int b = blockIdx.x, shift = __ffs(a.remainders) - 1;
+  const long long per_warp = (a.tokens + kSortThreads - 1) / kSortThreads * 32;
+  const long long end = (warp + 1) * per_warp < a.tokens ? (warp + 1) * per_warp : a.tokens;
+  const Share own{warp * per_warp, end, a.remainders - 1, shift};
   int* mine = counters + warp * a.per_cta;
   for (int i = threadIdx.x; i < kSortWarps * a.per_cta; i += kSortThreads) counters[i] = 0;
-  if (blockIdx.x == 0 && threadIdx.x == 0) a.crossing[0] = 0;
-  __syncthreads();
-  int before = walk_tokens(a, first, count, [&](int, int r, unsigned, unsigned same) {
-    if ((same & lower) == 0u) mine[r] += __popc(same);
-  });
+  if (b == 0 && threadIdx.x == 0) a.live[1] = 0;
+  // the warp's tokens of this CTA's rows to its list; those of CTAs before it counted
+  int before = 0, listed = 0;
+  for (long long t0 = own.begin; t0 < end; t0 += 32 * kSortLoads) {
+    Id id[kSortLoads];
+#pragma unroll
+    for (int u = 0; u < kSortLoads; ++u) id[u] = t0 + 32 * u + lane < end ? ids[t0 + 32 * u + lane] : -1;
+#pragma unroll
+    for (int u = 0; u < kSortLoads; ++u) {
+      const int row = row_of(id[u], a.vocab), rest = row & own.mask;
+      before += row >= 0 && rest < b;
+      const bool in = row >= 0 && rest == b;
+      const unsigned some = __ballot_sync(0xffffffffu, in);
+      if (some == 0u) continue;
+      const int at = listed + __popc(some & lower);
+      if (in && at < kSortList) lists[warp][at] = make_int2(static_cast<int>(t0) + 32 * u + lane, row >> shift);
+      listed += __popc(some);
+    }
+  }
   before = warp_total(before);
   if (lane == 0) sums[warp] = before;
   __syncthreads();
+  const bool fits = listed <= kSortList;
+  auto count = [&](int, int r, unsigned, unsigned same) {
+    if ((same & lower) == 0u) mine[r] += __popc(same);
+  };
+  if (fits) walk_list(lists[warp], listed, count);
+  else walk_ids<Id>(a, own, count);
   if (warp == 0) {
     before = warp_total(sums[lane]);
     if (lane == 0) base = before;
@@ -151,10 +191,10 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
   __syncthreads();
   // where every (row, warp) begins: over the rows kSortThreads at a time
   int running = base;
-  for (int r0 = 0; r0 < count; r0 += kSortThreads) {
+  for (int r0 = 0; r0 < a.per_cta; r0 += kSortThreads) {
     const int r = r0 + threadIdx.x;
     int total = 0;
-    if (r < count) {
+    if (r < a.per_cta) {
       for (int w = 0; w < kSortWarps; ++w) {
         const int c = counters[w * a.per_cta + r];
         counters[w * a.per_cta + r] = total;
@@ -167,7 +207,6 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
       const int x = __shfl_up_sync(0xffffffffu, scan, o);
       if (lane >= o) scan += x;
     }
-    __syncthreads();
     if (lane == 31) sums[warp] = scan;
     __syncthreads();
     int before_mine = 0, all = 0;
@@ -175,132 +214,159 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
       if (w < warp) before_mine += sums[w];
       all += sums[w];
     }
-    if (r < count) {
-      const int at = running + before_mine + scan - total;
-      a.begin[first + r] = at;
-      for (int w = 0; w < kSortWarps; ++w) counters[w * a.per_cta + r] += at;
+    if (r < a.per_cta) {
+      begins[r] = running + before_mine + scan - total;
+      const long long v = (static_cast<long long>(r) << shift) + b;
+      if (v < a.vocab) a.counts[v] = total;
     }
     running += all;
+    __syncthreads();
   }
-  if (first + count == a.vocab && threadIdx.x == 0) a.begin[a.vocab] = running;
-  if (running == base) return;
+  if (threadIdx.x == 0) {
+    begins[a.per_cta] = running;
+    if (b + 1 == a.remainders) a.live[0] = running;
+  }
   __syncthreads();
-  walk_tokens(a, first, count, [&](int t, int r, unsigned some, unsigned same) {
+  auto place = [&](int t, int r, unsigned some, unsigned same) {
     const int at = mine[r];
     __syncwarp(some);
     if ((same & lower) == 0u) mine[r] = at + __popc(same);
-    const int to = at + __popc(same & lower);
-    if (ZFS_CHECK(to >= 0 && to < a.tokens)) a.sorted[to] = make_int2(t, first + r);
-  });
+    const int begin = begins[r], to = begin + at + __popc(same & lower);
+    if (ZFS_CHECK(to >= 0 && to < a.tokens)) a.sorted[to] = make_int4(t, (r << shift) + b, begin, begins[r + 1]);
+  };
+  if (fits) walk_list(lists[warp], listed, place);
+  else walk_ids<Id>(a, own, place);
 }
 
-// A thread's eight columns of the table's gradient.
+// A warp sums kSumCount elements a lane: eight of a vector, or two single ones,
+// so that narrow tables have warps enough.
+template <int kVec>
+constexpr int kSumCount = kVec == 8 ? 8 : 2;
+
+// The warp's columns, from `at` on, of a row of the table's gradient.
 template <bool kFp32, int kVec>
-__device__ __forceinline__ void put_row(const EmbArgs& a, int row, int at, int lane, int lanes, const float* sum) {
+__device__ __forceinline__ void put_row(const EmbArgs& a, int row, int at, int lane, const float* sum) {
   constexpr long long kSize = kFp32 ? 4 : 2;
+  constexpr int kCount = kSumCount<kVec>;
   char* to = static_cast<char*>(a.out) + (row * a.out_stride + at) * kSize;
-  float x[8];
+  float x[kCount];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) x[k] = sum[k] * a.scale;
+  for (int k = 0; k < kCount; ++k) x[k] = sum[k] * a.scale;
   if (a.accumulate) {
-    Eight<kFp32, kVec> old;
-    float y[8];
-    load_eight<kFp32, kVec>(to, lane, lanes, a.dim - at, &old);
-    widen_eight<kFp32, kVec>(old, y);
+    Eight<kFp32, kVec, kCount> old;
+    float y[kCount];
+    load_eight<kFp32, kVec, kCount>(to, lane, 32, a.dim - at, &old);
+    widen_eight<kFp32, kVec, kCount>(old, y);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] += y[k];
+    for (int k = 0; k < kCount; ++k) x[k] += y[k];
   }
-  store_eight<kFp32, kVec>(to, lane, lanes, a.dim - at, x);
+  store_eight<kFp32, kVec, kCount>(to, lane, 32, a.dim - at, x);
 }
 
+// A warp takes 32 * kSumCount columns of a run, or of 32 rows that may have no
+// token.
 template <bool kFp32, bool kOutFp32, int kVec>
-__global__ void __launch_bounds__(kEmbThreads) embedding_sum_kernel(const __grid_constant__ EmbArgs a, int run_ctas) {
-  constexpr int kRows = 8;  // in flight
-  constexpr long long kSize = kFp32 ? 4 : 2;
-  const int lanes = a.lanes, lane = threadIdx.x % lanes, per_cta = kEmbThreads / lanes;
-  const int at = blockIdx.y * lanes * 8, cols = a.dim - at;
+__global__ void __launch_bounds__(kEmbThreads, 3) embedding_sum_kernel(const __grid_constant__ EmbArgs a) {
+  constexpr int kRows = kFp32 && kVec == 8 ? 4 : 8;  // in flight
+  constexpr int kCount = kSumCount<kVec>;
+  constexpr long long kSize = kFp32 ? 4 : 2, kOutSize = kOutFp32 ? 4 : 2;
+  const int lane = threadIdx.x % 32;
+  const long long unit = static_cast<long long>(blockIdx.x) * (kEmbThreads / 32) + threadIdx.x / 32;
+  const long long job = unit / a.columns;
+  const int at = static_cast<int>(unit - job * a.columns) * 32 * kCount, cols = a.dim - at;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (static_cast<int>(blockIdx.x) >= run_ctas) {
-    const float zero[8] = {};
-    const int v0 = (blockIdx.x - run_ctas) * kZeroRows;
-    for (int i = threadIdx.x / lanes; i < kZeroRows; i += per_cta) {
-      const int v = v0 + i;
-      if (v < a.vocab && a.begin[v] == a.begin[v + 1])
-        store_eight<kOutFp32, kVec>(static_cast<char*>(a.out) + (v * a.out_stride + at) * (kOutFp32 ? 4 : 2), lane, lanes,
-                                    cols, zero);
+  if (job >= a.runs) {
+    if (a.accumulate) return;  // rows without tokens keep what they have
+    const float zero[kCount] = {};
+    const long long v0 = (job - a.runs) * 32;
+    unsigned empty = __ballot_sync(0xffffffffu, v0 + lane < a.vocab && a.counts[v0 + lane] == 0);
+    while (empty) {
+      const long long v = v0 + __ffs(empty) - 1;
+      empty &= empty - 1;
+      store_eight<kOutFp32, kVec, kCount>(static_cast<char*>(a.out) + (v * a.out_stride + at) * kOutSize, lane, 32, cols, zero);
     }
     return;
   }
-  const int live = a.begin[a.vocab];
-  const long long run = static_cast<long long>(blockIdx.x) * per_cta + threadIdx.x / lanes;
-  const long long begin = run * kChunk;
-  if (begin >= live) return;
-  const int end = begin + kChunk < live ? static_cast<int>(begin) + kChunk : live;
-  int row = a.sorted[begin].y;
-  // a row that began before this run, or goes on after it, is summed in part
-  bool head = begin > 0 && a.sorted[begin - 1].y == row;
-  const bool open = end < live && a.sorted[end].y == a.sorted[end - 1].y;
-  float sum[8] = {};
-  auto put = [&](bool last) {
-    if (head || (last && open)) {
-      float* to = a.parts + (run * 2 + (head ? 0 : 1)) * a.pitch + at;
-      if (!head && lane == 0 && blockIdx.y == 0) a.crossing[1 + atomicAdd(a.crossing, 1)] = static_cast<int>(run);
+  const int run = static_cast<int>(job), live = a.live[0], heavy = 2 * a.chunk;
+  if (static_cast<long long>(run) * a.chunk >= live) return;
+  const int begin = run * a.chunk;
+  int p = begin, end = begin + a.chunk < live ? begin + a.chunk : live;
+  const int4 first = a.sorted[begin], last = a.sorted[end - 1];
+  // a row that began before this run: an earlier run sums it, or all in parts
+  if (first.z < begin && first.w - first.z <= heavy) p = first.w;
+  if (p >= end) return;
+  if (last.w - last.z <= heavy) end = last.w;  // the last row whole
+  float sum[kCount] = {};
+  int row = -1, row_begin = 0, row_end = 0;
+  auto put = [&]() {
+    if (row_end - row_begin > heavy) {
+      const int which = row_begin < begin ? 0 : 1;
+      float* to = a.parts + (run * 2LL + which) * a.pitch + at;
+      if (which == 1 && lane == 0 && at == 0)
+        a.heavy[atomicAdd(a.live + 1, 1)] = make_int4(run, row, (row_end - 1) / a.chunk - run + 1, 0);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const int c = column<kVec>(k, lane, lanes);
+      for (int k = 0; k < kCount; ++k) {
+        const int c = column<kVec>(k, lane, 32);
         if (c < cols) to[c] = sum[k];
       }
     } else {
-      put_row<kOutFp32, kVec>(a, row, at, lane, lanes, sum);
+      put_row<kOutFp32, kVec>(a, row, at, lane, sum);
     }
-    head = false;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum[k] = 0.0f;
+    for (int k = 0; k < kCount; ++k) sum[k] = 0.0f;
   };
-  for (int p = static_cast<int>(begin); p < end; p += kRows) {
-    int2 entry[kRows];
-    Eight<kFp32, kVec> raw[kRows];
+  // a lane holds one of the next 32 entries
+  int4 next = p + lane < end ? a.sorted[p + lane] : make_int4(0, -1, 0, 0);
+  for (; p < end; p += 32) {
+    const int4 mine = next;
+    if (p + 32 < end) next = p + 32 + lane < end ? a.sorted[p + 32 + lane] : make_int4(0, -1, 0, 0);
+    const int count = end - p < 32 ? end - p : 32;
+    for (int j = 0; j < count; j += kRows) {
+      Eight<kFp32, kVec, kCount> raw[kRows];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) entry[i] = p + i < end ? a.sorted[p + i] : make_int2(0, -1);
-#pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      load_eight<kFp32, kVec>(static_cast<const char*>(a.rows) + (entry[i].x * a.row_stride + at) * kSize, lane, lanes,
-                              entry[i].y >= 0 ? cols : 0, &raw[i]);
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (p + i >= end) break;
-      if (entry[i].y != row) {
-        put(false);
-        row = entry[i].y;
+      for (int i = 0; i < kRows; ++i) {
+        const int token = __shfl_sync(0xffffffffu, mine.x, (j + i) % 32);
+        load_eight<kFp32, kVec, kCount>(static_cast<const char*>(a.rows) + (token * a.row_stride + at) * kSize, lane, 32,
+                                        j + i < count ? cols : 0, &raw[i]);
       }
-      float x[8];
-      widen_eight<kFp32, kVec>(raw[i], x);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum[k] += x[k];
+      for (int i = 0; i < kRows; ++i) {
+        if (j + i >= count) break;
+        const int its = __shfl_sync(0xffffffffu, mine.y, j + i);
+        if (its != row) {
+          if (row >= 0) put();
+          row = its;
+          row_begin = __shfl_sync(0xffffffffu, mine.z, j + i);
+          row_end = __shfl_sync(0xffffffffu, mine.w, j + i);
+        }
+        float x[kCount];
+        widen_eight<kFp32, kVec, kCount>(raw[i], x);
+#pragma unroll
+        for (int k = 0; k < kCount; ++k) sum[k] += x[k];
+      }
     }
   }
-  put(true);
+  put();
 }
 
-// A row whose tokens lie in several runs: four columns a lane, every warp a
-// contiguous share of the parts, then warp after warp.
+// A row in parts: four columns a lane, every warp a contiguous share of the
+// parts, then warp after warp.
 template <bool kOutFp32>
 __global__ void __launch_bounds__(kJoinWarps * 32) embedding_join_kernel(const __grid_constant__ EmbArgs a) {
   __shared__ float4 sums[kJoinWarps][32];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const long long items = static_cast<long long>(a.crossing[0]) * a.slabs;
+  const long long items = static_cast<long long>(a.live[1]) * a.slabs;
   for (long long item = blockIdx.x; item < items; item += gridDim.x) {
-    const int run = a.crossing[1 + item / a.slabs], c = static_cast<int>(item % a.slabs) * 128 + lane * 4;
-    const int row = a.sorted[static_cast<long long>(run) * kChunk + kChunk - 1].y;
-    const int parts = (a.begin[row + 1] - 1) / kChunk - run + 1;  // one of this run, then of those behind it
-    const int share = (parts + kJoinWarps - 1) / kJoinWarps, from = warp * share;
-    const int to = from + share < parts ? from + share : parts;
+    const int4 e = a.heavy[item / a.slabs];  // first run, row, parts: one of that run, then of those behind it
+    const int c = static_cast<int>(item % a.slabs) * 128 + lane * 4;
+    const int share = (e.z + kJoinWarps - 1) / kJoinWarps, from = warp * share;
+    const int to = from + share < e.z ? from + share : e.z;
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (c < a.dim) {
 #pragma unroll 8
       for (int p = from; p < to; ++p) {
-        const float4 x = *reinterpret_cast<const float4*>(a.parts + ((static_cast<long long>(run) + p) * 2 + (p == 0)) * a.pitch + c);
+        const float4 x = *reinterpret_cast<const float4*>(a.parts + ((static_cast<long long>(e.x) + p) * 2 + (p == 0)) * a.pitch + c);
         s.x += x.x; s.y += x.y; s.z += x.z; s.w += x.w;
       }
     }
@@ -316,7 +382,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embedding_join_kernel(const _
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if (c + k >= a.dim) break;
-        const long long o = row * a.out_stride + c + k;
+        const long long o = e.y * a.out_stride + c + k;
         float x = all[k] * a.scale;
         if (a.accumulate) x += load_scalar(a.out, kOutFp32, o);
         store_scalar(a.out, kOutFp32, o, x);
@@ -326,22 +392,32 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embedding_join_kernel(const _
 }
 
 // ---- host ----------------------------------------------------------------------
-// The gradient's workspace: sorted tokens, rows' beginnings, list of rows in
-// parts, the parts (each 16-byte aligned).
+// The gradient's workspace (each part 16-byte aligned).
 struct Workspace {
-  long long sorted, begin, crossing, parts, total;
-  int runs, pitch;
+  long long sorted, counts, live, heavy, parts, total;
+  int runs, pitch, chunk;
+  long long heavy_rows;  // more tokens than that no rows can be in parts
 };
+// Long runs make few parts, short ones many warps: the longest that still gives
+// every SM 32 warps (of single elements, which the alignment may come to).
+int chunk_of(int64_t dim, int64_t tokens) {
+  const int64_t warps = (dim + 32 * kSumCount<1> - 1) / (32 * kSumCount<1>);
+  int chunk = kMostChunk;
+  while (chunk > kLeastChunk && tokens / chunk * warps < 32 * 152) chunk /= 2;
+  return chunk;
+}
 Workspace lay_out(const zero_embedding_config& c, int64_t tokens) {
   Workspace w{};
   auto up = [](long long x) { return (x + 15) / 16 * 16; };
-  w.runs = static_cast<int>((tokens + kChunk - 1) / kChunk);
+  w.chunk = chunk_of(c.dim, tokens);
+  w.heavy_rows = tokens / (2 * w.chunk + 1);
+  w.runs = static_cast<int>((tokens + w.chunk - 1) / w.chunk);
   w.pitch = static_cast<int>((c.dim + 3) / 4 * 4);
-  w.sorted = 0;
-  w.begin = up(tokens * 8);
-  w.crossing = w.begin + up((c.rows + 1) * 4);
-  w.parts = w.crossing + up((w.runs + 1LL) * 4);
-  w.total = w.parts + (w.runs > 1 ? w.runs * 2LL * w.pitch * 4 : 0);
+  w.counts = w.sorted + tokens * 16;
+  w.live = w.counts + up(c.rows * 4);
+  w.heavy = w.live + 16;
+  w.parts = w.heavy + w.heavy_rows * 16;
+  w.total = w.parts + (w.heavy_rows ? w.runs * 2LL * w.pitch * 4 : 0);
   return w;
 }
 
@@ -366,10 +442,28 @@ int lanes_of(const EmbArgs& a) {
   return power_of_two(need < kEmbThreads ? need : kEmbThreads);
 }
 
+template <typename Id>
+void launch_lookup(const EmbArgs& a, bool fp32, bool vec, dim3 grid, cudaStream_t s) {
+  if (fp32) {
+    if (vec) embedding_kernel<true, 8, Id><<<grid, kEmbThreads, 0, s>>>(a);
+    else embedding_kernel<true, 1, Id><<<grid, kEmbThreads, 0, s>>>(a);
+  } else {
+    if (vec) embedding_kernel<false, 8, Id><<<grid, kEmbThreads, 0, s>>>(a);
+    else embedding_kernel<false, 1, Id><<<grid, kEmbThreads, 0, s>>>(a);
+  }
+}
+template <typename Id>
+zero_status launch_sort(const EmbArgs& a, int shared, cudaStream_t s) {
+  // beyond what every kernel may have
+  if (shared > 12 * 1024 && allow_shared<embedding_sort_kernel<Id>, 160 * 1024>() != cudaSuccess)
+    return launch_status("embedding sort's shared memory");
+  embedding_sort_kernel<Id><<<a.remainders, kSortThreads, shared, s>>>(a);
+  return launch_status("embedding sort launch");
+}
 template <bool kFp32, bool kOutFp32>
-void launch_sum(const EmbArgs& a, bool vec, dim3 grid, int run_ctas, cudaStream_t s) {
-  if (vec) launch_after(embedding_sum_kernel<kFp32, kOutFp32, 8>, grid, dim3(kEmbThreads), 0, s, a, run_ctas);
-  else launch_after(embedding_sum_kernel<kFp32, kOutFp32, 1>, grid, dim3(kEmbThreads), 0, s, a, run_ctas);
+void launch_sum(const EmbArgs& a, bool vec, dim3 grid, cudaStream_t s) {
+  if (vec) launch_after(embedding_sum_kernel<kFp32, kOutFp32, 8>, grid, dim3(kEmbThreads), 0, s, a);
+  else launch_after(embedding_sum_kernel<kFp32, kOutFp32, 1>, grid, dim3(kEmbThreads), 0, s, a);
 }
 
 }  // namespace
@@ -415,16 +509,12 @@ zero_status zero_embedding(const zero_embedding_config* cfg, int64_t tokens, con
                    rows_aligned(out, out_stride, tokens, cfg->dtype);
   const long long per_cta = kEmbThreads / a.lanes, want = (tokens + per_cta - 1) / per_cta;
   const int slabs = (a.dim + a.lanes * 8 - 1) / (a.lanes * 8);
-  const long long most = static_cast<long long>(sm_count()) * (2048 / kEmbThreads);
+  const long long most = static_cast<long long>(sm_count()) * kLookupCtas;
   const dim3 grid(static_cast<unsigned>(want < most ? want : most), slabs);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cfg->dtype == ZERO_GRAD_FP32) {
-    if (vec) embedding_kernel<true, 8><<<grid, kEmbThreads, 0, s>>>(a);
-    else embedding_kernel<true, 1><<<grid, kEmbThreads, 0, s>>>(a);
-  } else {
-    if (vec) embedding_kernel<false, 8><<<grid, kEmbThreads, 0, s>>>(a);
-    else embedding_kernel<false, 1><<<grid, kEmbThreads, 0, s>>>(a);
-  }
+  const bool fp32 = cfg->dtype == ZERO_GRAD_FP32;
+  if (a.wide_ids) launch_lookup<long long>(a, fp32, vec, grid, s);
+  else launch_lookup<int>(a, fp32, vec, grid, s);
   return launch_status("embedding launch");
 }
 
@@ -468,38 +558,39 @@ zero_status zero_embedding_backward(const zero_embedding_config* cfg, int64_t to
   a.out_stride = dtable_stride;
   a.scale = cfg->scale;
   a.accumulate = accumulate;
-  a.sorted = reinterpret_cast<int2*>(at + w.sorted);
-  a.begin = reinterpret_cast<int*>(at + w.begin);
-  a.crossing = reinterpret_cast<int*>(at + w.crossing);
+  a.sorted = reinterpret_cast<int4*>(at + w.sorted);
+  a.counts = reinterpret_cast<int*>(at + w.counts);
+  a.live = reinterpret_cast<int*>(at + w.live);
+  a.heavy = reinterpret_cast<int4*>(at + w.heavy);
   a.parts = reinterpret_cast<float*>(at + w.parts);
   a.pitch = w.pitch;
   a.runs = w.runs;
+  a.chunk = w.chunk;
   a.slabs = (a.dim + 127) / 128;
-  a.lanes = lanes_of(a);
-  // a CTA of sorting per SM, more where its rows' counters would not fit
-  a.per_cta = (a.vocab + sm_count() - 1) / sm_count();
-  if (a.per_cta > kSortRows) a.per_cta = kSortRows;
-  const int sorting = (a.vocab + a.per_cta - 1) / a.per_cta;
-  const size_t counters = static_cast<size_t>(kSortWarps) * a.per_cta * sizeof(int);
+  // more sorting CTAs where the counters of their rows would not fit
+  a.remainders = kSortCtas;
+  while ((a.vocab + a.remainders - 1) / a.remainders > kSortRows) a.remainders *= 2;
+  a.per_cta = (a.vocab + a.remainders - 1) / a.remainders;
+  const int shared = (kSortWarps * a.per_cta + a.per_cta + 1) * static_cast<int>(sizeof(int));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // beyond what every kernel may have; set anew each time, as it belongs to the current context
-  if (counters > 48 * 1024 - 1024 &&
-      cudaFuncSetAttribute(embedding_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(kSortWarps * kSortRows * sizeof(int))) != cudaSuccess)
-    return launch_status("embedding sort's shared memory");
-  embedding_sort_kernel<<<sorting, kSortThreads, counters, s>>>(a);
-  if ((st = launch_status("embedding sort launch")) != ZERO_OK) return st;
+  st = a.wide_ids ? launch_sort<long long>(a, shared, s) : launch_sort<int>(a, shared, s);
+  if (st != ZERO_OK) return st;
   const bool fp32 = cfg->dtype == ZERO_GRAD_FP32, out32 = dtable_dtype == ZERO_GRAD_FP32;
   const bool vec = a.dim % 8 == 0 && rows_aligned(dout, dout_stride, tokens, cfg->dtype) &&
                    rows_aligned(dtable, dtable_stride, cfg->rows, dtable_dtype);
-  const int per_cta = kEmbThreads / a.lanes, run_ctas = (a.runs + per_cta - 1) / per_cta;
-  const int zero_ctas = accumulate ? 0 : (a.vocab + kZeroRows - 1) / kZeroRows;
-  const dim3 grid(run_ctas + zero_ctas, (a.dim + a.lanes * 8 - 1) / (a.lanes * 8));
-  if (fp32) out32 ? launch_sum<true, true>(a, vec, grid, run_ctas, s) : launch_sum<true, false>(a, vec, grid, run_ctas, s);
-  else out32 ? launch_sum<false, true>(a, vec, grid, run_ctas, s) : launch_sum<false, false>(a, vec, grid, run_ctas, s);
+  const int width = 32 * (vec ? kSumCount<8> : kSumCount<1>);
+  a.columns = (a.dim + width - 1) / width;
+  const long long jobs = a.runs + (accumulate ? 0 : (a.vocab + 31LL) / 32);
+  const long long ctas = (jobs * a.columns + kEmbThreads / 32 - 1) / (kEmbThreads / 32);
+  if (ctas > INT32_MAX) return refuse(ZERO_EINVAL, "tokens, rows and dim are too large together");
+  const dim3 grid(static_cast<unsigned>(ctas));
+  if (grid.x > 0) {
+    if (fp32) out32 ? launch_sum<true, true>(a, vec, grid, s) : launch_sum<true, false>(a, vec, grid, s);
+    else out32 ? launch_sum<false, true>(a, vec, grid, s) : launch_sum<false, false>(a, vec, grid, s);
+  }
   if ((st = launch_status("embedding sum launch")) != ZERO_OK) return st;
-  if (a.runs > 1) {  // one run has no row in parts
-    const long long items = static_cast<long long>(a.runs) * a.slabs, most = 8LL * sm_count();
+  if (w.heavy_rows > 0) {
+    const long long items = w.heavy_rows * a.slabs, most = 8LL * sm_count();
     const dim3 ctas(static_cast<unsigned>(items < most ? items : most));
     if (out32) launch_after(embedding_join_kernel<true>, ctas, dim3(kJoinWarps * 32), 0, s, a);
     else launch_after(embedding_join_kernel<false>, ctas, dim3(kJoinWarps * 32), 0, s, a);

@@ -14,11 +14,12 @@ constexpr int kPackGroup = 32;                  // columns that share a scale
 constexpr int kPackE4m3 = 1, kPackInt8 = 2;     // forms (0: none), as the public ones plus 1
 
 // Eight elements of a row as loaded.  kVec 8: eight neighbours from column
-// 8 * lane on, 16-byte aligned; kVec 1: columns lane, lane + lanes, ... (so that
-// neighbouring threads read neighbouring columns whatever the alignment).
-template <bool kFp32, int kVec>
+// 8 * lane on, 16-byte aligned; kVec 1: kCount (8, or fewer) columns lane,
+// lane + lanes, ... (so that neighbouring threads read neighbouring columns
+// whatever the alignment).
+template <bool kFp32, int kVec, int kCount = 8>
 struct Eight {
-  uint32_t w[kFp32 || kVec == 1 ? 8 : 4];
+  uint32_t w[kVec == 1 ? kCount : kFp32 ? 8 : 4];
 };
 
 // The column of element k of thread `lane` of `lanes`, from column `first` on.
@@ -29,8 +30,8 @@ __device__ __forceinline__ int column(int k, int lane, int lanes) {
 
 // How many of the thread's elements lie within `cols` columns are loaded; the
 // others are zero.  `row`: the row's first element.
-template <bool kFp32, int kVec>
-__device__ __forceinline__ void load_eight(const void* row, int lane, int lanes, int cols, Eight<kFp32, kVec>* v) {
+template <bool kFp32, int kVec, int kCount = 8>
+__device__ __forceinline__ void load_eight(const void* row, int lane, int lanes, int cols, Eight<kFp32, kVec, kCount>* v) {
   if constexpr (kVec == 8) {
 #pragma unroll
     for (int k = 0; k < (kFp32 ? 8 : 4); ++k) v->w[k] = 0u;
@@ -45,7 +46,7 @@ __device__ __forceinline__ void load_eight(const void* row, int lane, int lanes,
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kCount; ++k) {
       const int c = k * lanes + lane;
       v->w[k] = 0u;
       if (c < cols) {
@@ -56,10 +57,10 @@ __device__ __forceinline__ void load_eight(const void* row, int lane, int lanes,
   }
 }
 
-template <bool kFp32, int kVec>
-__device__ __forceinline__ void widen_eight(const Eight<kFp32, kVec>& v, float* x) {
+template <bool kFp32, int kVec, int kCount = 8>
+__device__ __forceinline__ void widen_eight(const Eight<kFp32, kVec, kCount>& v, float* x) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < kCount; ++k) {
     if constexpr (kFp32) x[k] = __uint_as_float(v.w[k]);
     else if constexpr (kVec == 8) x[k] = k % 2 ? bf16_hi(v.w[k / 2]) : bf16_lo(v.w[k / 2]);
     else x[k] = bf16_lo(v.w[k]);
@@ -88,7 +89,7 @@ __device__ __forceinline__ void forget_widened(T& v) {
   for (uint32_t& w : v.w) asm volatile("" : "+r"(w));
 }
 
-template <bool kFp32, int kVec>
+template <bool kFp32, int kVec, int kCount = 8>
 __device__ __forceinline__ void store_eight(void* row, int lane, int lanes, int cols, const float* x) {
   if constexpr (kVec == 8) {
     if (lane * 8 < cols) {
@@ -103,7 +104,7 @@ __device__ __forceinline__ void store_eight(void* row, int lane, int lanes, int 
     }
   } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < kCount; ++k) {
       const int c = k * lanes + lane;
       if (c < cols) {
         if constexpr (kFp32) static_cast<float*>(row)[c] = x[k];
