@@ -53,12 +53,19 @@ struct EmbArgs {
   int remainders, per_cta;     // sorting CTAs, rows of each
   int runs, chunk;             // runs of `chunk` sorted tokens
   int columns;                 // warps for the columns of a run
+  int zero_from, clear_rows;   // rows from there on are cleared beside the sorting, so many a CTA
+  int out_size, out_vec;       // bytes of an element of out; whether its rows are whole 16-byte words
 };
 
 // The row of an id, -1 if it has none.
 template <typename Id>
 __device__ __forceinline__ int row_of(Id id, int vocab) {
-  return id >= 0 && id < vocab ? static_cast<int>(id) : -1;
+  if constexpr (sizeof(Id) == 8) {
+    const unsigned low = static_cast<unsigned>(id), high = static_cast<unsigned>(static_cast<unsigned long long>(id) >> 32);
+    return high == 0u && low < static_cast<unsigned>(vocab) ? static_cast<int>(low) : -1;
+  } else {
+    return static_cast<unsigned>(id) < static_cast<unsigned>(vocab) ? id : -1;
+  }
 }
 
 template <bool kFp32, int kVec, typename Id>
@@ -139,8 +146,28 @@ __device__ __forceinline__ void walk_ids(const EmbArgs& a, const Share& own, F f
   }
 }
 
+// Zeros to rows whose tokens nobody has looked for yet, a warp a row.
+__device__ __forceinline__ void clear_rows(const EmbArgs& a, int first, int end) {
+  const int lane = threadIdx.x % 32;
+  for (int v = first + threadIdx.x / 32; v < end; v += kSortWarps) {
+    char* row = static_cast<char*>(a.out) + v * a.out_stride * a.out_size;
+    if (a.out_vec) {
+      for (int c = lane; c < a.dim * a.out_size / 16; c += 32) reinterpret_cast<uint4*>(row)[c] = make_uint4(0u, 0u, 0u, 0u);
+    } else if (a.out_size == 4) {
+      for (int c = lane; c < a.dim; c += 32) reinterpret_cast<uint32_t*>(row)[c] = 0u;
+    } else {
+      for (int c = lane; c < a.dim; c += 32) reinterpret_cast<uint16_t*>(row)[c] = 0;
+    }
+  }
+}
+
 template <typename Id>
-__global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __grid_constant__ EmbArgs a) {
+__global__ void __launch_bounds__(kSortThreads, 2) embedding_sort_kernel(const __grid_constant__ EmbArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (static_cast<int>(blockIdx.x) >= a.remainders) {
+    const int v = a.zero_from + (blockIdx.x - a.remainders) * a.clear_rows;
+    return clear_rows(a, v, a.vocab - v < a.clear_rows ? a.vocab : v + a.clear_rows);
+  }
   extern __shared__ int shared[];
   const Id* ids = static_cast<const Id*>(a.ids);
   __shared__ int2 lists[kSortWarps][kSortList];
@@ -159,22 +186,27 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
   if (b == 0 && threadIdx.x == 0) a.live[1] = 0;
   // the warp's tokens of this CTA's rows to its list; those of CTAs before it counted
   int before = 0, listed = 0;
-  for (long long t0 = own.begin; t0 < end; t0 += 32 * kSortLoads) {
+  auto take = [&](Id id, int token) {
+    const unsigned row = row_of(id, a.vocab), rest = row & own.mask;  // (unsigned)-1: none
+    const bool real = row != 0xFFFFFFFFu;
+    before += real && rest < static_cast<unsigned>(b);
+    const bool in = real && rest == static_cast<unsigned>(b);
+    const unsigned some = __ballot_sync(0xffffffffu, in);
+    if (some == 0u) return;
+    const int at = listed + __popc(some & lower);
+    if (in && at < kSortList) lists[warp][at] = make_int2(token, static_cast<int>(row >> shift));
+    listed += __popc(some);
+  };
+  long long t0 = own.begin;
+  for (; t0 + 32 * kSortLoads <= end; t0 += 32 * kSortLoads) {
     Id id[kSortLoads];
+    const Id* from = ids + t0 + lane;
 #pragma unroll
-    for (int u = 0; u < kSortLoads; ++u) id[u] = t0 + 32 * u + lane < end ? ids[t0 + 32 * u + lane] : -1;
+    for (int u = 0; u < kSortLoads; ++u) id[u] = from[32 * u];
 #pragma unroll
-    for (int u = 0; u < kSortLoads; ++u) {
-      const int row = row_of(id[u], a.vocab), rest = row & own.mask;
-      before += row >= 0 && rest < b;
-      const bool in = row >= 0 && rest == b;
-      const unsigned some = __ballot_sync(0xffffffffu, in);
-      if (some == 0u) continue;
-      const int at = listed + __popc(some & lower);
-      if (in && at < kSortList) lists[warp][at] = make_int2(static_cast<int>(t0) + 32 * u + lane, row >> shift);
-      listed += __popc(some);
-    }
+    for (int u = 0; u < kSortLoads; ++u) take(id[u], static_cast<int>(t0) + 32 * u + lane);
   }
+  for (; t0 < end; t0 += 32) take(t0 + lane < end ? ids[t0 + lane] : -1, static_cast<int>(t0) + lane);
   before = warp_total(before);
   if (lane == 0) sums[warp] = before;
   __syncthreads();
@@ -238,10 +270,12 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
   else walk_ids<Id>(a, own, place);
 }
 
-// A warp sums kSumCount elements a lane: eight of a vector, or two single ones,
-// so that narrow tables have warps enough.
+// A warp sums 8 elements a lane (vectors) or 2 (single ones, so that narrow
+// tables have warps enough).
 template <int kVec>
 constexpr int kSumCount = kVec == 8 ? 8 : 2;
+template <int kVec>
+constexpr int kSumColumns = 32 * kSumCount<kVec>;
 
 // The warp's columns, from `at` on, of a row of the table's gradient.
 template <bool kFp32, int kVec>
@@ -263,23 +297,34 @@ __device__ __forceinline__ void put_row(const EmbArgs& a, int row, int at, int l
   store_eight<kFp32, kVec, kCount>(to, lane, 32, a.dim - at, x);
 }
 
-// A warp takes 32 * kSumCount columns of a run, or of 32 rows that may have no
-// token.
+// Rows of whole vectors on their way to a warp, by asynchronous copies: 8 KB a
+// warp, 192 KB an SM.  (A row's address takes two dependent reads, so a warp
+// lives for a few latencies whatever it does: with four rows in registers at a
+// time the 32768 tokens' sums took 52 us.)
+template <bool kFp32>
+constexpr int kSumDepth = kFp32 ? 8 : 16;
+constexpr int kSumShared = kEmbThreads / 32 * 8192;
+
+// A warp takes kSumColumns columns of a run, or of 32 rows that may have no token.
 template <bool kFp32, bool kOutFp32, int kVec>
 __global__ void __launch_bounds__(kEmbThreads, 3) embedding_sum_kernel(const __grid_constant__ EmbArgs a) {
-  constexpr int kRows = kFp32 && kVec == 8 ? 4 : 8;  // in flight
   constexpr int kCount = kSumCount<kVec>;
+  constexpr int kRows = 8;  // in flight where elements are single
   constexpr long long kSize = kFp32 ? 4 : 2, kOutSize = kOutFp32 ? 4 : 2;
   const int lane = threadIdx.x % 32;
   const long long unit = static_cast<long long>(blockIdx.x) * (kEmbThreads / 32) + threadIdx.x / 32;
   const long long job = unit / a.columns;
-  const int at = static_cast<int>(unit - job * a.columns) * 32 * kCount, cols = a.dim - at;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (job >= a.runs) {
-    if (a.accumulate) return;  // rows without tokens keep what they have
+  const int at = static_cast<int>(unit - job * a.columns) * kSumColumns<kVec>, cols = a.dim - at;
+  // runs, which wait for what they read, and zeros, which only write, in turn
+  const int zeros = (a.zero_from + 31) / 32, both_kinds = 2 * (a.runs < zeros ? a.runs : zeros);
+  if (job >= static_cast<long long>(a.runs) + zeros) return;
+  const bool sums = job < both_kinds ? job % 2 == 0 : a.runs > zeros;
+  const long long mine_of_kind = job < both_kinds ? job / 2 : job - both_kinds / 2;
+  asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;" ::: "memory");
+  if (!sums) {
     const float zero[kCount] = {};
-    const long long v0 = (job - a.runs) * 32;
-    unsigned empty = __ballot_sync(0xffffffffu, v0 + lane < a.vocab && a.counts[v0 + lane] == 0);
+    const long long v0 = mine_of_kind * 32;
+    unsigned empty = __ballot_sync(0xffffffffu, v0 + lane < a.zero_from && a.counts[v0 + lane] == 0);
     while (empty) {
       const long long v = v0 + __ffs(empty) - 1;
       empty &= empty - 1;
@@ -287,62 +332,96 @@ __global__ void __launch_bounds__(kEmbThreads, 3) embedding_sum_kernel(const __g
     }
     return;
   }
-  const int run = static_cast<int>(job), live = a.live[0], heavy = 2 * a.chunk;
-  if (static_cast<long long>(run) * a.chunk >= live) return;
+  const int run = static_cast<int>(mine_of_kind), heavy = 2 * a.chunk;
   const int begin = run * a.chunk;
-  int p = begin, end = begin + a.chunk < live ? begin + a.chunk : live;
-  const int4 first = a.sorted[begin], last = a.sorted[end - 1];
+  // a lane holds three of the entries that a run can have (32, and 63 of its last row)
+  auto entry = [&](int q) {
+    return static_cast<long long>(begin) + q < a.tokens ? a.sorted[begin + q] : make_int4(0, -1, 0, 0);
+  };
+  const int4 now = entry(lane), next = entry(32 + lane), third = entry(64 + lane);
+  const int live = a.live[0];
+  if (begin >= live) return;
+  const int full = begin + a.chunk < live ? a.chunk : live - begin;
+  auto from = [&](int q, int x, int y, int z) { return __shfl_sync(0xffffffffu, q < 32 ? x : q < 64 ? y : z, q % 32); };
+  int q = 0, end = full;  // relative to begin
   // a row that began before this run: an earlier run sums it, or all in parts
-  if (first.z < begin && first.w - first.z <= heavy) p = first.w;
-  if (p >= end) return;
-  if (last.w - last.z <= heavy) end = last.w;  // the last row whole
-  float sum[kCount] = {};
+  const int first_begin = from(0, now.z, 0, 0), first_end = from(0, now.w, 0, 0);
+  if (first_begin < begin && first_end - first_begin <= heavy) q = first_end - begin;
+  if (q >= end) return;
+  const int last_begin = from(full - 1, now.z, 0, 0), last_end = from(full - 1, now.w, 0, 0);
+  if (last_end - last_begin <= heavy) end = last_end - begin;  // the last row whole
+  F2 sum[kCount / 2] = {};
   int row = -1, row_begin = 0, row_end = 0;
   auto put = [&]() {
-    if (row_end - row_begin > heavy) {
-      const int which = row_begin < begin ? 0 : 1;
-      float* to = a.parts + (run * 2LL + which) * a.pitch + at;
-      if (which == 1 && lane == 0 && at == 0)
-        a.heavy[atomicAdd(a.live + 1, 1)] = make_int4(run, row, (row_end - 1) / a.chunk - run + 1, 0);
+    const bool part = row_end - row_begin > heavy;
+    const int which = row_begin < begin ? 0 : 1;
+    if (part && which == 1 && lane == 0 && at == 0)
+      a.heavy[atomicAdd(a.live + 1, 1)] = make_int4(run, row, (row_end - 1) / a.chunk - run + 1, 0);
+    float x[kCount];
 #pragma unroll
-      for (int k = 0; k < kCount; ++k) {
-        const int c = column<kVec>(k, lane, 32);
-        if (c < cols) to[c] = sum[k];
-      }
-    } else {
-      put_row<kOutFp32, kVec>(a, row, at, lane, sum);
+    for (int k = 0; k < kCount / 2; ++k) {
+      split(sum[k], &x[2 * k], &x[2 * k + 1]);
+      sum[k] = 0;
     }
-#pragma unroll
-    for (int k = 0; k < kCount; ++k) sum[k] = 0.0f;
+    if (part) store_eight<true, kVec, kCount>(a.parts + (run * 2LL + which) * a.pitch + at, lane, 32, cols, x);
+    else put_row<kOutFp32, kVec>(a, row, at, lane, x);
   };
-  // a lane holds one of the next 32 entries
-  int4 next = p + lane < end ? a.sorted[p + lane] : make_int4(0, -1, 0, 0);
-  for (; p < end; p += 32) {
-    const int4 mine = next;
-    if (p + 32 < end) next = p + 32 + lane < end ? a.sorted[p + 32 + lane] : make_int4(0, -1, 0, 0);
-    const int count = end - p < 32 ? end - p : 32;
-    for (int j = 0; j < count; j += kRows) {
+  const char* rows = static_cast<const char*>(a.rows) + at * kSize;
+  auto row_at = [&](int i) { return rows + from(i, now.x, next.x, third.x) * a.row_stride * kSize; };
+  auto add = [&](int i, const Eight<kFp32, kVec, kCount>& raw) {
+    const int its = from(i, now.y, next.y, third.y);
+    if (its != row) {
+      if (row >= 0) put();
+      row = its;
+      row_begin = from(i, now.z, next.z, third.z);
+      row_end = from(i, now.w, next.w, third.w);
+    }
+    float x[kCount];
+    widen_eight<kFp32, kVec, kCount>(raw, x);
+#pragma unroll
+    for (int k = 0; k < kCount / 2; ++k) sum[k] = add2(sum[k], pair(x[2 * k], x[2 * k + 1]));
+  };
+  if constexpr (kVec == 8) {
+    constexpr int kDepth = kSumDepth<kFp32>, kWords = kFp32 ? 2 : 1;
+    extern __shared__ uint4 ring[];  // [warp][slot][word][lane]
+    uint4* const mine = ring + threadIdx.x / 32 * kDepth * kWords * 32 + lane;
+    const bool some = lane * 8 < cols;
+    auto fetch = [&](int i) {
+      if (i < end) {
+        const char* row_of_i = row_at(i) + lane * (kWords * 16);
+        if (some) {
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) copy_async<16>(mine + (i % kDepth * kWords + w) * 32, row_of_i + w * 16);
+        }
+      }
+      copy_commit();
+    };
+    for (int i = 0; i < kDepth; ++i) fetch(q + i);
+    for (; q < end; ++q) {
+      copy_wait<kDepth - 1>();
+      Eight<kFp32, 8, 8> raw{};
+      if (some) {
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          const uint4 u = mine[(q % kDepth * kWords + w) * 32];
+          raw.w[4 * w] = u.x; raw.w[4 * w + 1] = u.y; raw.w[4 * w + 2] = u.z; raw.w[4 * w + 3] = u.w;
+        }
+      }
+      add(q, raw);
+      fetch(q + kDepth);  // where this one was
+    }
+    copy_wait<0>();
+  } else {
+#pragma unroll 1
+    for (; q < end; q += kRows) {
       Eight<kFp32, kVec, kCount> raw[kRows];
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        const int token = __shfl_sync(0xffffffffu, mine.x, (j + i) % 32);
-        load_eight<kFp32, kVec, kCount>(static_cast<const char*>(a.rows) + (token * a.row_stride + at) * kSize, lane, 32,
-                                        j + i < count ? cols : 0, &raw[i]);
+        if (q + i < end) load_eight<kFp32, kVec, kCount>(row_at(q + i), lane, 32, cols, &raw[i]);
       }
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        if (j + i >= count) break;
-        const int its = __shfl_sync(0xffffffffu, mine.y, j + i);
-        if (its != row) {
-          if (row >= 0) put();
-          row = its;
-          row_begin = __shfl_sync(0xffffffffu, mine.z, j + i);
-          row_end = __shfl_sync(0xffffffffu, mine.w, j + i);
-        }
-        float x[kCount];
-        widen_eight<kFp32, kVec, kCount>(raw[i], x);
-#pragma unroll
-        for (int k = 0; k < kCount; ++k) sum[k] += x[k];
+        if (q + i < end) add(q + i, raw[i]);
       }
     }
   }
@@ -401,7 +480,7 @@ struct Workspace {
 // Long runs make few parts, short ones many warps: the longest that still gives
 // every SM 32 warps (of single elements, which the alignment may come to).
 int chunk_of(int64_t dim, int64_t tokens) {
-  const int64_t warps = (dim + 32 * kSumCount<1> - 1) / (32 * kSumCount<1>);
+  const int64_t warps = (dim + kSumColumns<1> - 1) / kSumColumns<1>;
   int chunk = kMostChunk;
   while (chunk > kLeastChunk && tokens / chunk * warps < 32 * 152) chunk /= 2;
   return chunk;
@@ -457,13 +536,16 @@ zero_status launch_sort(const EmbArgs& a, int shared, cudaStream_t s) {
   // beyond what every kernel may have
   if (shared > 12 * 1024 && allow_shared<embedding_sort_kernel<Id>, 160 * 1024>() != cudaSuccess)
     return launch_status("embedding sort's shared memory");
-  embedding_sort_kernel<Id><<<a.remainders, kSortThreads, shared, s>>>(a);
+  const int clearing = a.accumulate ? 0 : (a.vocab - a.zero_from + a.clear_rows - 1) / a.clear_rows;
+  embedding_sort_kernel<Id><<<a.remainders + clearing, kSortThreads, shared, s>>>(a);
   return launch_status("embedding sort launch");
 }
 template <bool kFp32, bool kOutFp32>
 void launch_sum(const EmbArgs& a, bool vec, dim3 grid, cudaStream_t s) {
-  if (vec) launch_after(embedding_sum_kernel<kFp32, kOutFp32, 8>, grid, dim3(kEmbThreads), 0, s, a);
-  else launch_after(embedding_sum_kernel<kFp32, kOutFp32, 1>, grid, dim3(kEmbThreads), 0, s, a);
+  if (vec) {
+    if (allow_shared<embedding_sum_kernel<kFp32, kOutFp32, 8>, kSumShared>() != cudaSuccess) return;  // the launch's error
+    launch_after(embedding_sum_kernel<kFp32, kOutFp32, 8>, grid, dim3(kEmbThreads), kSumShared, s, a);
+  } else launch_after(embedding_sum_kernel<kFp32, kOutFp32, 1>, grid, dim3(kEmbThreads), 0, s, a);
 }
 
 }  // namespace
@@ -573,14 +655,23 @@ zero_status zero_embedding_backward(const zero_embedding_config* cfg, int64_t to
   a.per_cta = (a.vocab + a.remainders - 1) / a.remainders;
   const int shared = (kSortWarps * a.per_cta + a.per_cta + 1) * static_cast<int>(sizeof(int));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  st = a.wide_ids ? launch_sort<long long>(a, shared, s) : launch_sort<int>(a, shared, s);
-  if (st != ZERO_OK) return st;
   const bool fp32 = cfg->dtype == ZERO_GRAD_FP32, out32 = dtable_dtype == ZERO_GRAD_FP32;
   const bool vec = a.dim % 8 == 0 && rows_aligned(dout, dout_stride, tokens, cfg->dtype) &&
                    rows_aligned(dtable, dtable_stride, cfg->rows, dtable_dtype);
-  const int width = 32 * (vec ? kSumCount<8> : kSumCount<1>);
+  // Memory has nothing to do while the tokens are sorted: the last rows, the rarest
+  // ids of most vocabularies, are cleared meanwhile whether or not they have
+  // tokens, about as many as the time is good for (2 KB a token: 32768 tokens
+  // take 11 us).
+  a.out_size = dtype_bytes(dtable_dtype);
+  a.out_vec = vec;
+  const long long row_bytes = static_cast<long long>(a.dim) * a.out_size, meanwhile = tokens * 2048 / row_bytes;
+  a.zero_from = accumulate ? 0 : static_cast<int>(meanwhile < a.vocab ? a.vocab - meanwhile : 0);
+  a.clear_rows = static_cast<int>(row_bytes < 65536 ? 65536 / row_bytes : 1);
+  st = a.wide_ids ? launch_sort<long long>(a, shared, s) : launch_sort<int>(a, shared, s);
+  if (st != ZERO_OK) return st;
+  const int width = vec ? kSumColumns<8> : kSumColumns<1>;
   a.columns = (a.dim + width - 1) / width;
-  const long long jobs = a.runs + (accumulate ? 0 : (a.vocab + 31LL) / 32);
+  const long long jobs = a.runs + (a.zero_from + 31LL) / 32;
   const long long ctas = (jobs * a.columns + kEmbThreads / 32 - 1) / (kEmbThreads / 32);
   if (ctas > INT32_MAX) return refuse(ZERO_EINVAL, "tokens, rows and dim are too large together");
   const dim3 grid(static_cast<unsigned>(ctas));

@@ -421,6 +421,7 @@ __global__ void __launch_bounds__(kBackwardWarps * 32, 1) norm_backward_kernel(c
   constexpr long long kSize = kFp32 ? 4 : 2;
   constexpr bool kAhead = kVec == 8;
   constexpr int kWords = kFp32 ? 2 : 1;  // 16-byte words of eight elements
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for all of this
   extern __shared__ __align__(16) float tables[];
   __shared__ float buffer[2][kNormWarps][2 * kRows];
   GroupSum<2 * kRows> sum(buffer, a.lanes);
