@@ -30,7 +30,7 @@ constexpr int kSortCtas = 128;    // a power of two
 constexpr int kSortRows = 1024;   // of a CTA at most: a counter for each and every warp, 128 KB
 constexpr int kSortLoads = 8;     // ids in flight per lane
 constexpr int kSortList = 128;    // tokens that a warp keeps, else it reads its ids again
-constexpr int kLeastChunk = 8, kMostChunk = 32;  // sorted tokens of a run
+constexpr int kLeastChunk = 8, kMostChunk = 16;  // sorted tokens of a run
 constexpr int kJoinWarps = 8;
 
 struct EmbArgs {
@@ -53,8 +53,6 @@ struct EmbArgs {
   int remainders, per_cta;     // sorting CTAs, rows of each
   int runs, chunk;             // runs of `chunk` sorted tokens
   int columns;                 // warps for the columns of a run
-  int zero_from, clear_rows;   // rows from there on are cleared beside the sorting, so many a CTA
-  int out_size, out_vec;       // bytes of an element of out; whether its rows are whole 16-byte words
 };
 
 // The row of an id, -1 if it has none.
@@ -146,28 +144,9 @@ __device__ __forceinline__ void walk_ids(const EmbArgs& a, const Share& own, F f
   }
 }
 
-// Zeros to rows whose tokens nobody has looked for yet, a warp a row.
-__device__ __forceinline__ void clear_rows(const EmbArgs& a, int first, int end) {
-  const int lane = threadIdx.x % 32;
-  for (int v = first + threadIdx.x / 32; v < end; v += kSortWarps) {
-    char* row = static_cast<char*>(a.out) + v * a.out_stride * a.out_size;
-    if (a.out_vec) {
-      for (int c = lane; c < a.dim * a.out_size / 16; c += 32) reinterpret_cast<uint4*>(row)[c] = make_uint4(0u, 0u, 0u, 0u);
-    } else if (a.out_size == 4) {
-      for (int c = lane; c < a.dim; c += 32) reinterpret_cast<uint32_t*>(row)[c] = 0u;
-    } else {
-      for (int c = lane; c < a.dim; c += 32) reinterpret_cast<uint16_t*>(row)[c] = 0;
-    }
-  }
-}
-
 template <typename Id>
-__global__ void __launch_bounds__(kSortThreads, 2) embedding_sort_kernel(const __grid_constant__ EmbArgs a) {
+__global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __grid_constant__ EmbArgs a) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (static_cast<int>(blockIdx.x) >= a.remainders) {
-    const int v = a.zero_from + (blockIdx.x - a.remainders) * a.clear_rows;
-    return clear_rows(a, v, a.vocab - v < a.clear_rows ? a.vocab : v + a.clear_rows);
-  }
   extern __shared__ int shared[];
   const Id* ids = static_cast<const Id*>(a.ids);
   __shared__ int2 lists[kSortWarps][kSortList];
@@ -270,12 +249,14 @@ __global__ void __launch_bounds__(kSortThreads, 2) embedding_sort_kernel(const _
   else walk_ids<Id>(a, own, place);
 }
 
-// A warp sums 8 elements a lane (vectors) or 2 (single ones, so that narrow
-// tables have warps enough).
+// A warp sums kSumParts times kSumCount elements a lane: 32 bytes of vectors, or
+// two single elements (so that narrow tables have warps enough).
+template <bool kFp32, int kVec>
+constexpr int kSumParts = kVec == 8 && !kFp32 ? 2 : 1;
 template <int kVec>
 constexpr int kSumCount = kVec == 8 ? 8 : 2;
-template <int kVec>
-constexpr int kSumColumns = 32 * kSumCount<kVec>;
+template <bool kFp32, int kVec>
+constexpr int kSumColumns = 32 * kSumParts<kFp32, kVec> * kSumCount<kVec>;
 
 // The warp's columns, from `at` on, of a row of the table's gradient.
 template <bool kFp32, int kVec>
@@ -297,121 +278,159 @@ __device__ __forceinline__ void put_row(const EmbArgs& a, int row, int at, int l
   store_eight<kFp32, kVec, kCount>(to, lane, 32, a.dim - at, x);
 }
 
-// Rows of whole vectors on their way to a warp, by asynchronous copies: 8 KB a
-// warp, 192 KB an SM.  (A row's address takes two dependent reads, so a warp
-// lives for a few latencies whatever it does: with four rows in registers at a
-// time the 32768 tokens' sums took 52 us.)
-template <bool kFp32>
-constexpr int kSumDepth = kFp32 ? 8 : 16;
-constexpr int kSumShared = kEmbThreads / 32 * 8192;
+// Rows of whole vectors come to a warp by asynchronous copies, kSumDepth (1 KB
+// each) on their way: a row's address takes two dependent reads, so a warp lives
+// for some latencies whatever it does, and registers would hold four.
+constexpr int kSumDepth = 8;
+constexpr int kSumThreads = 128, kSumWarps = kSumThreads / 32;  // few: a CTA lasts as long as its longest run
+constexpr int kSumShared = kSumWarps * kSumDepth * 1024;
+
+__host__ __device__ inline int ctas_of(long long jobs, int columns) {
+  return static_cast<int>((jobs * columns + kSumWarps - 1) / kSumWarps);
+}
 
 // A warp takes kSumColumns columns of a run, or of 32 rows that may have no token.
 template <bool kFp32, bool kOutFp32, int kVec>
-__global__ void __launch_bounds__(kEmbThreads, 3) embedding_sum_kernel(const __grid_constant__ EmbArgs a) {
-  constexpr int kCount = kSumCount<kVec>;
-  constexpr int kRows = 8;  // in flight where elements are single
+__global__ void __launch_bounds__(kSumThreads, 6) embedding_sum_kernel(const __grid_constant__ EmbArgs a) {
+  constexpr int kParts = kSumParts<kFp32, kVec>, kCount = kSumCount<kVec>, kPart = 32 * kCount;
   constexpr long long kSize = kFp32 ? 4 : 2, kOutSize = kOutFp32 ? 4 : 2;
   const int lane = threadIdx.x % 32;
-  const long long unit = static_cast<long long>(blockIdx.x) * (kEmbThreads / 32) + threadIdx.x / 32;
+  // CTAs of runs, which wait for what they read, and of zeros, which only write, in turn
+  const int zeros = a.accumulate ? 0 : (a.vocab + 31) / 32, run_ctas = ctas_of(a.runs, a.columns), zero_ctas = ctas_of(zeros, a.columns);
+  const int in_turn = 2 * (run_ctas < zero_ctas ? run_ctas : zero_ctas), b = blockIdx.x;
+  const bool sums = b < in_turn ? b % 2 == 0 : run_ctas > zero_ctas;
+  const long long unit = static_cast<long long>(b < in_turn ? b / 2 : b - in_turn / 2) * kSumWarps + threadIdx.x / 32;
   const long long job = unit / a.columns;
-  const int at = static_cast<int>(unit - job * a.columns) * kSumColumns<kVec>, cols = a.dim - at;
-  // runs, which wait for what they read, and zeros, which only write, in turn
-  const int zeros = (a.zero_from + 31) / 32, both_kinds = 2 * (a.runs < zeros ? a.runs : zeros);
-  if (job >= static_cast<long long>(a.runs) + zeros) return;
-  const bool sums = job < both_kinds ? job % 2 == 0 : a.runs > zeros;
-  const long long mine_of_kind = job < both_kinds ? job / 2 : job - both_kinds / 2;
+  if (job >= (sums ? a.runs : zeros)) return;
+  const int at = static_cast<int>(unit - job * a.columns) * kSumColumns<kFp32, kVec>, cols = a.dim - at;
   asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;" ::: "memory");
   if (!sums) {
     const float zero[kCount] = {};
-    const long long v0 = mine_of_kind * 32;
-    unsigned empty = __ballot_sync(0xffffffffu, v0 + lane < a.zero_from && a.counts[v0 + lane] == 0);
+    const long long v0 = job * 32;
+    unsigned empty = __ballot_sync(0xffffffffu, v0 + lane < a.vocab && a.counts[v0 + lane] == 0);
     while (empty) {
       const long long v = v0 + __ffs(empty) - 1;
       empty &= empty - 1;
-      store_eight<kOutFp32, kVec, kCount>(static_cast<char*>(a.out) + (v * a.out_stride + at) * kOutSize, lane, 32, cols, zero);
+#pragma unroll
+      for (int n = 0; n < kParts; ++n)
+        store_eight<kOutFp32, kVec, kCount>(static_cast<char*>(a.out) + (v * a.out_stride + at + n * kPart) * kOutSize, lane,
+                                            32, cols - n * kPart, zero);
     }
     return;
   }
-  const int run = static_cast<int>(mine_of_kind), heavy = 2 * a.chunk;
+  const int run = static_cast<int>(job), heavy = 2 * a.chunk;
   const int begin = run * a.chunk;
   // a lane holds three of the entries that a run can have (32, and 63 of its last row)
   auto entry = [&](int q) {
     return static_cast<long long>(begin) + q < a.tokens ? a.sorted[begin + q] : make_int4(0, -1, 0, 0);
   };
-  const int4 now = entry(lane), next = entry(32 + lane), third = entry(64 + lane);
+  int4 now = entry(lane), next = entry(32 + lane);
+  const int4 third = entry(64 + lane);
   const int live = a.live[0];
   if (begin >= live) return;
   const int full = begin + a.chunk < live ? a.chunk : live - begin;
-  auto from = [&](int q, int x, int y, int z) { return __shfl_sync(0xffffffffu, q < 32 ? x : q < 64 ? y : z, q % 32); };
   int q = 0, end = full;  // relative to begin
   // a row that began before this run: an earlier run sums it, or all in parts
-  const int first_begin = from(0, now.z, 0, 0), first_end = from(0, now.w, 0, 0);
+  const int first_begin = __shfl_sync(0xffffffffu, now.z, 0), first_end = __shfl_sync(0xffffffffu, now.w, 0);
   if (first_begin < begin && first_end - first_begin <= heavy) q = first_end - begin;
   if (q >= end) return;
-  const int last_begin = from(full - 1, now.z, 0, 0), last_end = from(full - 1, now.w, 0, 0);
+  const int last_begin = __shfl_sync(0xffffffffu, now.z, full - 1), last_end = __shfl_sync(0xffffffffu, now.w, full - 1);
   if (last_end - last_begin <= heavy) end = last_end - begin;  // the last row whole
-  F2 sum[kCount / 2] = {};
+  F2 sum[kParts][kCount / 2] = {};
   int row = -1, row_begin = 0, row_end = 0;
   auto put = [&]() {
     const bool part = row_end - row_begin > heavy;
     const int which = row_begin < begin ? 0 : 1;
     if (part && which == 1 && lane == 0 && at == 0)
       a.heavy[atomicAdd(a.live + 1, 1)] = make_int4(run, row, (row_end - 1) / a.chunk - run + 1, 0);
-    float x[kCount];
 #pragma unroll
-    for (int k = 0; k < kCount / 2; ++k) {
-      split(sum[k], &x[2 * k], &x[2 * k + 1]);
-      sum[k] = 0;
+    for (int n = 0; n < kParts; ++n) {
+      float x[kCount];
+#pragma unroll
+      for (int k = 0; k < kCount / 2; ++k) {
+        split(sum[n][k], &x[2 * k], &x[2 * k + 1]);
+        sum[n][k] = 0;
+      }
+      if (part) store_eight<true, kVec, kCount>(a.parts + (run * 2LL + which) * a.pitch + at + n * kPart, lane, 32,
+                                                cols - n * kPart, x);
+      else put_row<kOutFp32, kVec>(a, row, at + n * kPart, lane, x);
     }
-    if (part) store_eight<true, kVec, kCount>(a.parts + (run * 2LL + which) * a.pitch + at, lane, 32, cols, x);
-    else put_row<kOutFp32, kVec>(a, row, at, lane, x);
   };
-  const char* rows = static_cast<const char*>(a.rows) + at * kSize;
-  auto row_at = [&](int i) { return rows + from(i, now.x, next.x, third.x) * a.row_stride * kSize; };
-  auto add = [&](int i, const Eight<kFp32, kVec, kCount>& raw) {
-    const int its = from(i, now.y, next.y, third.y);
-    if (its != row) {
-      if (row >= 0) put();
-      row = its;
-      row_begin = from(i, now.z, next.z, third.z);
-      row_end = from(i, now.w, next.w, third.w);
-    }
+  const char* const rows = static_cast<const char*>(a.rows) + at * kSize;
+  // a group of 32 entries at a time: where a row begins among them
+  int group = 0;
+  unsigned begins = 0;
+  auto look = [&]() { begins = __ballot_sync(0xffffffffu, begin + group + lane == now.z); };
+  auto row_at = [&](int i) {  // of this group or the next
+    const int token = __shfl_sync(0xffffffffu, i - group < 32 ? now.x : next.x, i % 32);
+    return rows + token * a.row_stride * kSize;
+  };
+  auto open = [&](int i) {  // the row of entry i of this group
+    row = __shfl_sync(0xffffffffu, now.y, i % 32);
+    row_begin = __shfl_sync(0xffffffffu, now.z, i % 32);
+    row_end = __shfl_sync(0xffffffffu, now.w, i % 32);
+  };
+  auto add = [&](int n, const Eight<kFp32, kVec, kCount>& raw) {
     float x[kCount];
     widen_eight<kFp32, kVec, kCount>(raw, x);
 #pragma unroll
-    for (int k = 0; k < kCount / 2; ++k) sum[k] = add2(sum[k], pair(x[2 * k], x[2 * k + 1]));
+    for (int k = 0; k < kCount / 2; ++k) sum[n][k] = add2(sum[n][k], pair(x[2 * k], x[2 * k + 1]));
   };
+  while (q >= group + 32) {  // (a run that begins behind a short row of another)
+    group += 32;
+    now = next;
+    next = third;
+  }
+  look();
   if constexpr (kVec == 8) {
-    constexpr int kDepth = kSumDepth<kFp32>, kWords = kFp32 ? 2 : 1;
+    constexpr int kWords = 2;  // 16-byte words of a lane's row: of one part (fp32), of two
     extern __shared__ uint4 ring[];  // [warp][slot][word][lane]
-    uint4* const mine = ring + threadIdx.x / 32 * kDepth * kWords * 32 + lane;
-    const bool some = lane * 8 < cols;
-    auto fetch = [&](int i) {
+    uint4* const mine = ring + threadIdx.x / 32 * kSumDepth * kWords * 32 + lane;
+    const bool some[kWords] = {lane * 8 < cols, kFp32 ? lane * 8 < cols : lane * 8 + kPart < cols};
+    const int word = kFp32 ? 16 : kPart * 2, step = lane * (kFp32 ? 32 : 16);  // bytes
+    auto fetch = [&](int i, int slot) {
       if (i < end) {
-        const char* row_of_i = row_at(i) + lane * (kWords * 16);
-        if (some) {
+        const char* of_i = row_at(i) + step;
 #pragma unroll
-          for (int w = 0; w < kWords; ++w) copy_async<16>(mine + (i % kDepth * kWords + w) * 32, row_of_i + w * 16);
-        }
+        for (int w = 0; w < kWords; ++w)
+          if (some[w]) copy_async<16>(mine + (slot * kWords + w) * 32, of_i + w * word);
       }
       copy_commit();
     };
-    for (int i = 0; i < kDepth; ++i) fetch(q + i);
-    for (; q < end; ++q) {
-      copy_wait<kDepth - 1>();
-      Eight<kFp32, 8, 8> raw{};
-      if (some) {
 #pragma unroll
-        for (int w = 0; w < kWords; ++w) {
-          const uint4 u = mine[(q % kDepth * kWords + w) * 32];
-          raw.w[4 * w] = u.x; raw.w[4 * w + 1] = u.y; raw.w[4 * w + 2] = u.z; raw.w[4 * w + 3] = u.w;
-        }
+    for (int i = 0; i < kSumDepth; ++i) fetch(q + i, i);
+    // rolled: the code of a row's end is long, and would stand here kSumDepth times
+    int slot = 0;
+#pragma unroll 1
+    for (bool opens = true;; ++q, opens = false) {
+      if (q == group + 32) {
+        group += 32;
+        now = next;
+        next = third;
+        look();
       }
-      add(q, raw);
-      fetch(q + kDepth);  // where this one was
+      if (opens || q == end || (begins >> (q % 32) & 1u)) {
+        if (!opens) put();
+        if (q == end) break;
+        open(q);
+      }
+      copy_wait<kSumDepth - 1>();
+      uint4 u[kWords];
+#pragma unroll
+      for (int w = 0; w < kWords; ++w) u[w] = some[w] ? mine[(slot * kWords + w) * 32] : make_uint4(0u, 0u, 0u, 0u);
+      if constexpr (kFp32) {
+        add(0, Eight<true, 8, 8>{{u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w}});
+      } else {
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) add(w, Eight<false, 8, 8>{{u[w].x, u[w].y, u[w].z, u[w].w}});
+      }
+      fetch(q + kSumDepth, slot);  // where this one was
+      slot = (slot + 1) % kSumDepth;
     }
     copy_wait<0>();
   } else {
+    constexpr int kRows = 4;  // in flight
+    bool opens = true;
 #pragma unroll 1
     for (; q < end; q += kRows) {
       Eight<kFp32, kVec, kCount> raw[kRows];
@@ -421,11 +440,24 @@ __global__ void __launch_bounds__(kEmbThreads, 3) embedding_sum_kernel(const __g
       }
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        if (q + i < end) add(q + i, raw[i]);
+        const int here = q + i;
+        if (here >= end) break;
+        if (here == group + 32) {
+          group += 32;
+          now = next;
+          next = third;
+          look();
+        }
+        if (opens || (begins >> (here % 32) & 1u)) {
+          if (!opens) put();
+          open(here);
+        }
+        opens = false;
+        add(0, raw[i]);
       }
     }
+    put();
   }
-  put();
 }
 
 // A row in parts: four columns a lane, every warp a contiguous share of the
@@ -480,7 +512,7 @@ struct Workspace {
 // Long runs make few parts, short ones many warps: the longest that still gives
 // every SM 32 warps (of single elements, which the alignment may come to).
 int chunk_of(int64_t dim, int64_t tokens) {
-  const int64_t warps = (dim + kSumColumns<1> - 1) / kSumColumns<1>;
+  const int64_t warps = (dim + kSumColumns<false, 1> - 1) / kSumColumns<false, 1>;
   int chunk = kMostChunk;
   while (chunk > kLeastChunk && tokens / chunk * warps < 32 * 152) chunk /= 2;
   return chunk;
@@ -536,16 +568,15 @@ zero_status launch_sort(const EmbArgs& a, int shared, cudaStream_t s) {
   // beyond what every kernel may have
   if (shared > 12 * 1024 && allow_shared<embedding_sort_kernel<Id>, 160 * 1024>() != cudaSuccess)
     return launch_status("embedding sort's shared memory");
-  const int clearing = a.accumulate ? 0 : (a.vocab - a.zero_from + a.clear_rows - 1) / a.clear_rows;
-  embedding_sort_kernel<Id><<<a.remainders + clearing, kSortThreads, shared, s>>>(a);
+  embedding_sort_kernel<Id><<<a.remainders, kSortThreads, shared, s>>>(a);
   return launch_status("embedding sort launch");
 }
 template <bool kFp32, bool kOutFp32>
 void launch_sum(const EmbArgs& a, bool vec, dim3 grid, cudaStream_t s) {
   if (vec) {
     if (allow_shared<embedding_sum_kernel<kFp32, kOutFp32, 8>, kSumShared>() != cudaSuccess) return;  // the launch's error
-    launch_after(embedding_sum_kernel<kFp32, kOutFp32, 8>, grid, dim3(kEmbThreads), kSumShared, s, a);
-  } else launch_after(embedding_sum_kernel<kFp32, kOutFp32, 1>, grid, dim3(kEmbThreads), 0, s, a);
+    launch_after(embedding_sum_kernel<kFp32, kOutFp32, 8>, grid, dim3(kSumThreads), kSumShared, s, a);
+  } else launch_after(embedding_sum_kernel<kFp32, kOutFp32, 1>, grid, dim3(kSumThreads), 0, s, a);
 }
 
 }  // namespace
@@ -658,23 +689,13 @@ zero_status zero_embedding_backward(const zero_embedding_config* cfg, int64_t to
   const bool fp32 = cfg->dtype == ZERO_GRAD_FP32, out32 = dtable_dtype == ZERO_GRAD_FP32;
   const bool vec = a.dim % 8 == 0 && rows_aligned(dout, dout_stride, tokens, cfg->dtype) &&
                    rows_aligned(dtable, dtable_stride, cfg->rows, dtable_dtype);
-  // Memory has nothing to do while the tokens are sorted: the last rows, the rarest
-  // ids of most vocabularies, are cleared meanwhile whether or not they have
-  // tokens, about as many as the time is good for (2 KB a token: 32768 tokens
-  // take 11 us).
-  a.out_size = dtype_bytes(dtable_dtype);
-  a.out_vec = vec;
-  const long long row_bytes = static_cast<long long>(a.dim) * a.out_size, meanwhile = tokens * 2048 / row_bytes;
-  a.zero_from = accumulate ? 0 : static_cast<int>(meanwhile < a.vocab ? a.vocab - meanwhile : 0);
-  a.clear_rows = static_cast<int>(row_bytes < 65536 ? 65536 / row_bytes : 1);
   st = a.wide_ids ? launch_sort<long long>(a, shared, s) : launch_sort<int>(a, shared, s);
   if (st != ZERO_OK) return st;
-  const int width = vec ? kSumColumns<8> : kSumColumns<1>;
+  const int width = !vec ? kSumColumns<false, 1> : fp32 ? kSumColumns<true, 8> : kSumColumns<false, 8>;
   a.columns = (a.dim + width - 1) / width;
-  const long long jobs = a.runs + (a.zero_from + 31LL) / 32;
-  const long long ctas = (jobs * a.columns + kEmbThreads / 32 - 1) / (kEmbThreads / 32);
-  if (ctas > INT32_MAX) return refuse(ZERO_EINVAL, "tokens, rows and dim are too large together");
-  const dim3 grid(static_cast<unsigned>(ctas));
+  const long long zeros = accumulate ? 0 : (a.vocab + 31LL) / 32, jobs = a.runs + zeros;
+  if (jobs * a.columns / kSumWarps > INT32_MAX - 2) return refuse(ZERO_EINVAL, "tokens, rows and dim are too large together");
+  const dim3 grid(ctas_of(a.runs, a.columns) + ctas_of(zeros, a.columns));
   if (grid.x > 0) {
     if (fp32) out32 ? launch_sum<true, true>(a, vec, grid, s) : launch_sum<true, false>(a, vec, grid, s);
     else out32 ? launch_sum<false, true>(a, vec, grid, s) : launch_sum<false, false>(a, vec, grid, s);
