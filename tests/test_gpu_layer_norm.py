@@ -357,8 +357,7 @@ def test_tensor_checks():
     with pytest.raises(ValueError):
         ops.layer_norm(x[:-1], weight, bias, out=x[1:])
     for g, s, st in ((dy[:5], x, stats), (dy.bfloat16(), x, stats), (dy, x, stats[:5]), (dy, x, stats.double()),
-                     (dy[:5], packed, stats[:5]), (dy, packed._replace(codes=packed.codes[:, :32]), stats),
-                     (dy, packed._replace(scales=packed.scales.int()), stats), (dy, packed._replace(shape=torch.Size([6, 65])), stats)):
+                     (dy[:5], packed, stats[:5]), (dy[:, :32], packed, stats), (dy.view(2, 3, 64), packed, stats)):
         with pytest.raises(ValueError):
             ops.layer_norm_backward(g, s, weight, st)
     vector = torch.empty(100, device="cuda")

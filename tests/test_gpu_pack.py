@@ -29,7 +29,7 @@ def inputs(rows, cols, dtype, seed=0):
 
 def check(x, form, packed):
     codes, exponents, values = pack64(x, form)
-    assert packed.codes.dtype == form and packed.shape == x.shape and packed.dtype == x.dtype
+    assert packed.codes.dtype == packed.form == form and packed.shape == x.shape and packed.dtype == x.dtype
     assert torch.equal(packed.codes.float().cpu().double(), codes)
     assert torch.equal(packed.scales.cpu().long(), exponents + 127)
     for dtype in (None, FP32, BF16):
@@ -101,9 +101,9 @@ def test_shapes_and_reuse():
                        ops.unpack_activations(want).view(4, 6, 48).transpose(0, 1))
     row = ops.pack_activations(x[0], INT8)
     assert ops.unpack_activations(row).shape == (48,)
-    codes = packed.codes.data_ptr()
+    codes = packed.data.data_ptr()
     again = ops.pack_activations((2 * x).view(2, 3, 4, 48), INT8, out=packed)
-    assert again.codes.data_ptr() == codes
+    assert again.data.data_ptr() == codes
     assert torch.equal(ops.unpack_activations(again).view(24, 48), 2 * ops.unpack_activations(want))
     needs = x.clone().requires_grad_()
     assert not ops.unpack_activations(ops.pack_activations(needs, INT8)).requires_grad
@@ -140,17 +140,27 @@ def test_tensor_checks():
             ops.pack_activations(bad, out=packed)
     with pytest.raises(ValueError):
         ops.pack_activations(x, INT8, out=packed)
+    buffer = torch.zeros(2048, dtype=torch.uint8, device="cuda")
+    inside, beside = (buffer[at:at + 1536].view(FP32).view(6, 64) for at in (256, 400))
+    over = ops.PackedActivations(buffer[:396], E4M3, (6, 64), FP32)
     with pytest.raises(ValueError):
-        ops.pack_activations(packed.codes.view(FP32), out=packed)
-    for bad in (packed._replace(codes=packed.codes[:5]), packed._replace(codes=packed.codes.view(torch.uint8)),
-                packed._replace(scales=packed.scales[:, :1]), packed._replace(dtype=torch.half),
-                packed._replace(shape=torch.Size([])), packed._replace(shape=torch.Size([6, 70]))):
+        ops.pack_activations(inside, out=over)
+    ops.pack_activations(beside, out=over)
+    good = (packed.data, E4M3, (6, 64), FP32)
+    assert torch.equal(ops.unpack_activations(ops.PackedActivations(*good)), ops.unpack_activations(packed))
+    for i, bad in ((0, packed.data[:-1]), (0, packed.data.cpu()), (0, packed.data.view(torch.int8)),
+                   (0, packed.data.view(6, 66)), (0, packed.data.expand(2, 396)[:, ::2].reshape(-1)[:395]),
+                   (1, torch.uint8), (2, (6, 65)), (2, (6, 0)), (2, ()), (2, (-6, 64)), (2, (5, 64)), (3, torch.half)):
+        args = list(good)
+        args[i] = bad
         with pytest.raises(ValueError):
-            ops.unpack_activations(bad)
+            ops.PackedActivations(*args)
     with pytest.raises(ValueError):
         ops.unpack_activations(packed, torch.half)
-    for out in (x[:5], x.half(), x.t().contiguous().t(), packed.codes.view(FP32)):
+    for out in (x[:5], x.half(), x.t().contiguous().t()):
         with pytest.raises(ValueError):
             ops.unpack_activations(packed, out=out)
     with pytest.raises(ValueError):
         ops.unpack_activations(packed, BF16, out=x)
+    with pytest.raises(ValueError):
+        ops.unpack_activations(over, out=inside)

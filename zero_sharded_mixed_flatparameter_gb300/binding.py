@@ -103,6 +103,8 @@ _lock = threading.Lock()
 def load(path: str = LIB_PATH):
     """Load the CUDA library; raises if it is missing (no fallback exists)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -202,10 +204,6 @@ def _i32(values: Sequence[int]):
 
 def _ptrs(values: Sequence[int]):
     return (ctypes.c_void_p * max(len(values), 1))(*[int(v) if v else None for v in values])
-
-
-def _ref(struct):
-    return ctypes.byref(struct) if struct is not None else None
 
 
 def make_config(stage: int, n_ranks: int, grad_dtype: str = "bf16", lr: float = 1e-3, beta1: float = 0.9,
@@ -518,25 +516,31 @@ def zero_qk_norm_rope_backward(cfg: zero_qk_config, tokens: int, dq_out: zero_he
         dq_gain or None, dk_gain or None, dgain_dtype, workspace or None, workspace_bytes, stream or None))
 
 
+# The calls of every layer of a step: NULL is 0 here (and None for a struct).
 def zero_pack_activations(rows: int, cols: int, x: int, dtype: int, x_stride: int, packed: zero_packed,
                           stream: int = 0) -> None:
-    _check(load().zero_pack_activations(rows, cols, x or None, dtype, x_stride, _ref(packed), stream or None))
+    status = load().zero_pack_activations(rows, cols, x, dtype, x_stride, packed, stream)
+    if status:
+        _check(status)
 
 
 def zero_unpack_activations(rows: int, cols: int, packed: zero_packed, out: int, dtype: int, out_stride: int,
                             stream: int = 0) -> None:
-    _check(load().zero_unpack_activations(rows, cols, _ref(packed), out or None, dtype, out_stride, stream or None))
+    status = load().zero_unpack_activations(rows, cols, packed, out, dtype, out_stride, stream)
+    if status:
+        _check(status)
 
 
 def zero_layer_norm(cfg: zero_norm_config, rows: int, x: int, x_stride: int, weight: int, bias: int, y: int,
                     y_stride: int, stats: int, packed: zero_packed | None = None, stream: int = 0) -> None:
-    _check(load().zero_layer_norm(ctypes.byref(cfg), rows, x or None, x_stride, weight or None, bias or None, y or None,
-                                  y_stride, stats or None, _ref(packed), stream or None))
+    status = load().zero_layer_norm(cfg, rows, x, x_stride, weight, bias, y, y_stride, stats, packed, stream)
+    if status:
+        _check(status)
 
 
 def zero_layer_norm_backward_workspace_bytes(cfg: zero_norm_config, rows: int) -> int:
     n = ctypes.c_int64()
-    _check(load().zero_layer_norm_backward_workspace_bytes(ctypes.byref(cfg), rows, ctypes.byref(n)))
+    _check(load().zero_layer_norm_backward_workspace_bytes(cfg, rows, ctypes.byref(n)))
     return n.value
 
 
@@ -544,30 +548,32 @@ def zero_layer_norm_backward(cfg: zero_norm_config, rows: int, dy: int, dy_strid
                              packed: zero_packed | None, weight: int, stats: int, dx: int, dx_stride: int, dweight: int,
                              dbias: int, dgrad_dtype: int, workspace: int, workspace_bytes: int,
                              stream: int = 0) -> None:
-    _check(load().zero_layer_norm_backward(
-        ctypes.byref(cfg), rows, dy or None, dy_stride, x or None, x_stride, _ref(packed), weight or None, stats or None,
-        dx or None, dx_stride, dweight or None, dbias or None, dgrad_dtype, workspace or None, workspace_bytes,
-        stream or None))
+    status = load().zero_layer_norm_backward(cfg, rows, dy, dy_stride, x, x_stride, packed, weight, stats, dx, dx_stride,
+                                             dweight, dbias, dgrad_dtype, workspace, workspace_bytes, stream)
+    if status:
+        _check(status)
 
 
 def zero_embedding(cfg: zero_embedding_config, tokens: int, ids: int, table: int, table_stride: int, out: int,
                    out_stride: int, stream: int = 0) -> None:
-    _check(load().zero_embedding(ctypes.byref(cfg), tokens, ids or None, table or None, table_stride, out or None,
-                                 out_stride, stream or None))
+    status = load().zero_embedding(cfg, tokens, ids, table, table_stride, out, out_stride, stream)
+    if status:
+        _check(status)
 
 
 def zero_embedding_backward_workspace_bytes(cfg: zero_embedding_config, tokens: int) -> int:
     n = ctypes.c_int64()
-    _check(load().zero_embedding_backward_workspace_bytes(ctypes.byref(cfg), tokens, ctypes.byref(n)))
+    _check(load().zero_embedding_backward_workspace_bytes(cfg, tokens, ctypes.byref(n)))
     return n.value
 
 
 def zero_embedding_backward(cfg: zero_embedding_config, tokens: int, ids: int, dout: int, dout_stride: int, dtable: int,
                             dtable_dtype: int, dtable_stride: int, accumulate: int, workspace: int,
                             workspace_bytes: int, stream: int = 0) -> None:
-    _check(load().zero_embedding_backward(ctypes.byref(cfg), tokens, ids or None, dout or None, dout_stride,
-                                          dtable or None, dtable_dtype, dtable_stride, accumulate, workspace or None,
-                                          workspace_bytes, stream or None))
+    status = load().zero_embedding_backward(cfg, tokens, ids, dout, dout_stride, dtable, dtable_dtype, dtable_stride,
+                                            accumulate, workspace, workspace_bytes, stream)
+    if status:
+        _check(status)
 
 
 def zero_destroy(ctx: int) -> None:

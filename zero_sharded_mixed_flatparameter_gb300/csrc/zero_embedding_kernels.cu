@@ -30,8 +30,8 @@ constexpr int kSortCtas = 128;    // a power of two
 constexpr int kSortRows = 1024;   // of a CTA at most: a counter for each and every warp, 128 KB
 constexpr int kSortLoads = 8;     // ids in flight per lane
 constexpr int kSortList = 128;    // tokens that a warp keeps, else it reads its ids again
-constexpr int kLeastChunk = 8, kMostChunk = 16;  // sorted tokens of a run
-constexpr int kJoinWarps = 8;
+constexpr int kLeastChunk = 8, kMostChunk = 32;  // sorted tokens of a run
+constexpr int kJoinWarps = 16;
 
 struct EmbArgs {
   long long tokens;
@@ -702,7 +702,7 @@ zero_status zero_embedding_backward(const zero_embedding_config* cfg, int64_t to
   }
   if ((st = launch_status("embedding sum launch")) != ZERO_OK) return st;
   if (w.heavy_rows > 0) {
-    const long long items = w.heavy_rows * a.slabs, most = 8LL * sm_count();
+    const long long items = w.heavy_rows * a.slabs, most = 4LL * sm_count();
     const dim3 ctas(static_cast<unsigned>(items < most ? items : most));
     if (out32) launch_after(embedding_join_kernel<true>, ctas, dim3(kJoinWarps * 32), 0, s, a);
     else launch_after(embedding_join_kernel<false>, ctas, dim3(kJoinWarps * 32), 0, s, a);

@@ -12,7 +12,7 @@ from __future__ import annotations
 import contextlib
 import functools
 import operator
-from typing import NamedTuple, Optional, Sequence, Tuple, Union
+from typing import Optional, Sequence, Tuple, Union
 
 import torch
 from torch.autograd.function import once_differentiable
@@ -282,83 +282,98 @@ def qk_norm_rope_autograd(q, k, q_gain, k_gain, table, positions=None, *, eps: f
 
 
 # ---- rows of activations -------------------------------------------------------
+# Called for every layer of a step, or for every new token: checks stand together
+# and the usual layouts first, since the host's share of a small call is larger
+# than the kernel's.
 _FORMATS = {torch.float8_e4m3fn: B.ZERO_PACK_E4M3, torch.int8: B.ZERO_PACK_INT8}
 _GROUP = 32  # columns that share a scale
+_grad_enabled = torch.is_grad_enabled
 
 
 def _matrix(x: torch.Tensor, what: str, copy: bool = True) -> torch.Tensor:
-    """`x` as a matrix of its last dimension's rows; a copy where its strides allow no such view (refused unless
-    `copy`)."""
-    if x.dim() == 2:
-        pass
-    elif x.dim() == 0:
-        raise ValueError(f"{what} must have a dimension")
-    elif copy:
-        x = x.reshape(-1, x.size(-1)) if x.numel() else x.new_empty((x.shape[:-1].numel(), x.size(-1)))
-    elif x.numel() == 0:
-        return x.new_empty((x.shape[:-1].numel(), x.size(-1)))
-    else:
-        try:
-            x = x.view(-1, x.size(-1))
-        except RuntimeError:
-            raise ValueError(f"the rows of {what} must have one stride") from None
+    """`x`, which has columns, as a matrix of its last dimension's rows; a copy where its strides allow no such view
+    (refused unless `copy`)."""
+    if x.dim() != 2:
+        x = x.detach()
+        if x.numel() == 0:
+            x = x.new_empty((x.shape[:-1].numel(), x.size(-1)))
+        elif copy:
+            x = x.reshape(-1, x.size(-1))
+        else:
+            try:
+                x = x.view(-1, x.size(-1))
+            except RuntimeError:
+                raise ValueError(f"the rows of {what} must have one stride") from None
     if x.stride(1) != 1 and x.size(1) > 1:
         raise ValueError(f"the columns of {what} must be contiguous")
     return x
 
 
-def _check_rows(x: torch.Tensor, what: str) -> None:
-    if x.dtype not in _DTYPES or not x.is_cuda:
+def _check_rows(x: torch.Tensor, what: str) -> int:
+    """The type of a tensor of rows."""
+    dtype = _DTYPES.get(x.dtype)
+    if dtype is None or not x.is_cuda:
         raise ValueError(f"{what} must be a bf16 or fp32 CUDA tensor")
     if x.dim() == 0 or x.size(-1) == 0:
         raise ValueError(f"{what} must have columns")
+    return dtype
 
 
-def _check_vectors(cols: int, device: torch.device, what: str, *vectors: Optional[torch.Tensor]) -> Optional[torch.dtype]:
+def _check_vectors(cols: int, device: torch.device, what: str, *vectors: Optional[torch.Tensor]) -> Optional[int]:
     """The type that the given vectors share."""
     dtype = None
     for v in vectors:
         if v is None:
             continue
-        if v.dtype not in _DTYPES or v.shape != (cols,) or v.device != device or not v.is_contiguous() or \
-                dtype not in (None, v.dtype):
+        kind = _DTYPES.get(v.dtype)
+        if kind is None or v.shape != (cols,) or v.device != device or not v.is_contiguous() or dtype not in (None, kind):
             raise ValueError(f"{what} must be contiguous vectors of one entry per column and one type (bf16 or fp32)")
-        dtype = v.dtype
+        dtype = kind
     return dtype
 
 
-class PackedActivations(NamedTuple):
-    """A tensor in 8 bits: codes (rows, 32 * groups) of e4m3 or int8, a power of two (its exponent plus 127) per group
-    of 32 columns, the shape and the type of what was packed."""
-    codes: torch.Tensor
-    scales: torch.Tensor
-    shape: torch.Size
-    dtype: torch.dtype
+class PackedActivations:
+    """A tensor in 8 bits, as :func:`pack_activations` returns it.
+
+    ``data``: the bytes, codes of 32 columns a group, then a scale a group;
+    ``form``: torch.float8_e4m3fn or torch.int8; ``shape`` and ``dtype`` of what
+    was packed.  ``codes`` (rows, 32 * groups) and ``scales`` (rows, groups; the
+    power of two plus 127) are views of ``data``.
+    """
+    __slots__ = ("data", "form", "shape", "dtype", "rows", "cols", "_struct")
+
+    def __init__(self, data: torch.Tensor, form: torch.dtype, shape: Sequence[int], dtype: torch.dtype):
+        shape = torch.Size(shape)
+        if form not in _FORMATS or dtype not in _DTYPES or len(shape) == 0 or min(shape) < 0 or shape[-1] == 0:
+            raise ValueError("packed activations are e4m3 or int8 codes of a bf16 or fp32 tensor with columns")
+        rows, cols = shape[:-1].numel(), shape[-1]
+        if data.dtype != torch.uint8 or not data.is_cuda or not data.is_contiguous() or \
+                data.shape != (rows * -(-cols // _GROUP) * (_GROUP + 1),):
+            raise ValueError("data must be a contiguous CUDA vector of the codes' and scales' bytes")
+        self._set(data, form, shape, dtype, rows, cols)
+
+    def _set(self, data, form, shape, dtype, rows, cols):
+        self.data, self.form, self.shape, self.dtype, self.rows, self.cols = data, form, shape, dtype, rows, cols
+        at = data.data_ptr()
+        self._struct = B.zero_packed(at, at + rows * -(-cols // _GROUP) * _GROUP, _FORMATS[form])
+        return self
+
+    @property
+    def codes(self) -> torch.Tensor:
+        groups = -(-self.cols // _GROUP)
+        return self.data[:self.rows * groups * _GROUP].view(self.form).view(self.rows, groups * _GROUP)
+
+    @property
+    def scales(self) -> torch.Tensor:
+        groups = -(-self.cols // _GROUP)
+        return self.data[self.rows * groups * _GROUP:].view(self.rows, groups)
 
 
-def _new_packed(rows: int, x: torch.Tensor, dtype: torch.dtype) -> PackedActivations:
-    if dtype not in _FORMATS:
+def _new_packed(rows: int, cols: int, shape, dtype: torch.dtype, form: torch.dtype, device) -> PackedActivations:
+    if form not in _FORMATS:
         raise ValueError("activations are packed to torch.float8_e4m3fn or torch.int8")
-    groups = -(-x.size(-1) // _GROUP)
-    return PackedActivations(torch.empty((rows, groups * _GROUP), dtype=dtype, device=x.device),
-                             torch.empty((rows, groups), dtype=torch.uint8, device=x.device), x.shape, x.dtype)
-
-
-def _check_packed(packed: PackedActivations) -> Tuple[int, int]:
-    """Rows and columns of what was packed."""
-    codes, scales, shape, dtype = packed
-    if len(shape) == 0 or shape[-1] == 0 or dtype not in _DTYPES or codes.dtype not in _FORMATS or not codes.is_cuda:
-        raise ValueError("packed must be what pack_activations returns")
-    rows, cols = shape[:-1].numel(), shape[-1]
-    groups = -(-cols // _GROUP)
-    if codes.shape != (rows, groups * _GROUP) or scales.shape != (rows, groups) or scales.dtype != torch.uint8 or \
-            scales.device != codes.device or not codes.is_contiguous() or not scales.is_contiguous():
-        raise ValueError("the codes and scales of packed must be contiguous and fit its shape")
-    return rows, cols
-
-
-def _packed_struct(packed: PackedActivations) -> B.zero_packed:
-    return B.zero_packed(packed.codes.data_ptr(), packed.scales.data_ptr(), _FORMATS[packed.codes.dtype])
+    data = torch.empty(rows * -(-cols // _GROUP) * (_GROUP + 1), dtype=torch.uint8, device=device)
+    return PackedActivations.__new__(PackedActivations)._set(data, form, shape, dtype, rows, cols)
 
 
 def pack_activations(x: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, *,
@@ -372,18 +387,17 @@ def pack_activations(x: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, 
     write to.  What ``x`` requires a gradient for is not recorded: this keeps a
     tensor for the backward pass, as saving it would.
     """
-    _check_rows(x, "x")
-    m = _matrix(x.detach(), "x")
+    kind = _check_rows(x, "x")
+    m, device = _matrix(x, "x"), x.device
+    rows, cols = m.shape
     if out is None:
-        out = _new_packed(m.size(0), x, dtype)
+        out = _new_packed(rows, cols, x.shape, x.dtype, dtype, device)
     else:
-        _check_packed(out)
-        if out.shape != x.shape or out.dtype != x.dtype or out.codes.dtype != dtype or out.codes.device != x.device:
+        if out.shape != x.shape or out.dtype != x.dtype or out.form != dtype or out.data.device != device:
             raise ValueError("out must have x's shape, type and device, and codes of dtype")
-        _check_memory((out.codes, out.scales), ((), (), (m,)))
-    with _on(x.device):
-        B.zero_pack_activations(m.size(0), m.size(1), m.data_ptr(), _DTYPES[x.dtype], m.stride(0), _packed_struct(out),
-                                _stream(x.device))
+        _check_memory((out.data,), ((), (m,)))
+    with _on(device):
+        B.zero_pack_activations(rows, cols, m.data_ptr(), kind, m.stride(0), out._struct, current_stream(device.index))
     return out
 
 
@@ -391,30 +405,24 @@ def unpack_activations(packed: PackedActivations, dtype: Optional[torch.dtype] =
                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values that ``packed`` stands for, in the type of what was packed or
     ``dtype`` (bf16 or fp32; both hold them exactly, but for bf16 subnormals)."""
-    rows, cols = _check_packed(packed)
-    device = packed.codes.device
+    device = packed.data.device
     if out is None:
-        out = torch.empty(packed.shape, dtype=packed.dtype if dtype is None else dtype, device=device)
-        if out.dtype not in _DTYPES:
+        kind = _DTYPES.get(dtype or packed.dtype)
+        if kind is None:
             raise ValueError("dtype must be bf16 or fp32")
-        m = out
-        stride = cols
+        out = torch.empty(packed.shape, dtype=dtype or packed.dtype, device=device)
+        at, stride = out.data_ptr(), packed.cols
     else:
         _no_graph("unpack_activations", out)
-        if out.shape != packed.shape or out.device != device or out.dtype not in _DTYPES or dtype not in (None, out.dtype):
+        kind = _DTYPES.get(out.dtype)
+        if kind is None or out.shape != packed.shape or out.device != device or dtype not in (None, out.dtype):
             raise ValueError("out must be a bf16 or fp32 tensor of packed's shape and device")
         m = _matrix(out, "out", copy=False)
-        _check_memory((m,), ((), (packed.codes, packed.scales)))
-        stride = m.stride(0)
+        _check_memory((m,), ((), (packed.data,)))
+        at, stride = m.data_ptr(), m.stride(0)
     with _on(device):
-        B.zero_unpack_activations(rows, cols, _packed_struct(packed), m.data_ptr(), _DTYPES[out.dtype], stride,
-                                  _stream(device))
+        B.zero_unpack_activations(packed.rows, packed.cols, packed._struct, at, kind, stride, current_stream(device.index))
     return out
-
-
-def _check_norm(x, weight, bias):
-    _check_rows(x, "x")
-    return _check_vectors(x.size(-1), x.device, "weight and bias", weight, bias) or torch.float32
 
 
 def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Optional[torch.Tensor] = None, *,
@@ -432,24 +440,27 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     Inputs that require gradients are refused: :func:`layer_norm_autograd`
     records them.
     """
-    _no_graph("layer_norm (layer_norm_autograd does)", x, weight, bias)
-    vector_dtype = _check_norm(x, weight, bias)
-    m, device = _matrix(x, "x"), x.device
+    if _grad_enabled():
+        _no_graph("layer_norm (layer_norm_autograd does)", x, weight, bias)
+    kind, device = _check_rows(x, "x"), x.device
+    m = _matrix(x, "x")
+    rows, cols = m.shape
+    vector_kind = _check_vectors(cols, device, "weight and bias", weight, bias)
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=device)
-        y, y_stride = out, x.size(-1)
+        y, y_stride = out, cols
     else:
         _check_like((out,), (x,))
         y = _matrix(out, "out", copy=False)
         y_stride = y.stride(0)
         _check_memory((y,), ((m,),))
-    rows, cols = m.shape
     stats = torch.empty((rows, 2), dtype=torch.float32, device=device)
-    packed = None if pack is None else _new_packed(rows, x, pack)
+    packed = None if pack is None else _new_packed(rows, cols, x.shape, x.dtype, pack, device)
+    cfg = _norm_config(cols, 1 if center else 0, kind, vector_kind or 0, float(eps))
     with _on(device):
-        B.zero_layer_norm(_norm_config(cols, 1 if center else 0, _DTYPES[x.dtype], _DTYPES[vector_dtype], float(eps)),
-                          rows, m.data_ptr(), m.stride(0), _ptr(weight), _ptr(bias), y.data_ptr(), y_stride,
-                          stats.data_ptr(), None if packed is None else _packed_struct(packed), _stream(device))
+        B.zero_layer_norm(cfg, rows, m.data_ptr(), m.stride(0), 0 if weight is None else weight.data_ptr(),
+                          0 if bias is None else bias.data_ptr(), y.data_ptr(), y_stride, stats.data_ptr(),
+                          None if packed is None else packed._struct, current_stream(device.index))
     return (out, stats) if packed is None else (out, stats, packed)
 
 
@@ -473,21 +484,20 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivatio
     gradients are refused.
     """
     kept = isinstance(x, PackedActivations)
-    _no_graph("layer_norm_backward", dy, None if kept else x, weight)
-    _check_rows(dy, "dy")
-    device, cols = dy.device, dy.size(-1)
-    vector_dtype = _check_vectors(cols, device, "weight", weight) or torch.float32
+    if _grad_enabled():
+        _no_graph("layer_norm_backward", dy, None if kept else x, weight)
+    kind, device = _check_rows(dy, "dy"), dy.device
     g = _matrix(dy, "dy")
-    rows = g.size(0)
+    rows, cols = g.shape
+    vector_kind = _check_vectors(cols, device, "weight", weight)
     if kept:
-        _check_packed(x)
-        if x.shape != dy.shape or x.codes.device != device:
+        if x.shape != dy.shape or x.data.device != device:
             raise ValueError("x and dy must agree in shape and device")
         m = None
     else:
         _check_like((dy,), (x,))
         m = _matrix(x, "x")
-    if stats.shape != (rows, 2) or stats.dtype != torch.float32 or stats.device != device or not stats.is_contiguous():
+    if stats.dtype != torch.float32 or stats.shape != (rows, 2) or stats.device != device or not stats.is_contiguous():
         raise ValueError("stats must be the contiguous fp32 tensor (rows, 2) of the forward pass")
     if out is None:
         out = torch.empty(dy.shape, dtype=dy.dtype, device=device)
@@ -498,26 +508,27 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivatio
         d_stride = d.stride(0)
         _check_memory((d,), ((g,) if m is None else (g, m),))
         if kept:
-            _check_memory((d,), ((), (x.codes, x.scales)))
-    given = _check_vectors(cols, device, "weight_out and bias_out", weight_out, bias_out)
-    if given is not None:
-        _check_memory([v for v in (weight_out, bias_out) if v is not None], ())
-    if weight is not None and weight_out is None:
-        weight_out = torch.empty(cols, dtype=given or torch.float32, device=device)
-    if not bias:
-        if bias_out is not None:
+            _check_memory((d,), ((), (x.data,)))
+    given = None
+    if weight_out is not None or bias_out is not None:
+        given = _check_vectors(cols, device, "weight_out and bias_out", weight_out, bias_out)
+        if bias_out is not None and not bias:
             raise ValueError("bias_out without a bias")
-    elif bias_out is None:
-        bias_out = torch.empty(cols, dtype=given or torch.float32, device=device)
-    wanted = weight_out if weight_out is not None else bias_out
+        _check_memory([v for v in (weight_out, bias_out) if v is not None], ())
+    vectors = torch.bfloat16 if given == B.ZERO_GRAD_BF16 else torch.float32
+    if weight is not None and weight_out is None:
+        weight_out = torch.empty(cols, dtype=vectors, device=device)
+    if bias and bias_out is None:
+        bias_out = torch.empty(cols, dtype=vectors, device=device)
+    need = 0 if weight_out is None and bias_out is None else _norm_workspace(cols, rows, device.index)
+    cfg = _norm_config(cols, 1 if center else 0, kind, vector_kind or 0, 0.0)
     with _on(device):
-        need = 0 if wanted is None else _norm_workspace(cols, rows, device.index)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        workspace = torch.empty(need or 16, dtype=torch.uint8, device=device)
         B.zero_layer_norm_backward(
-            _norm_config(cols, 1 if center else 0, _DTYPES[dy.dtype], _DTYPES[vector_dtype], 0.0), rows, g.data_ptr(),
-            g.stride(0), _ptr(m), 0 if m is None else m.stride(0), _packed_struct(x) if kept else None, _ptr(weight),
-            stats.data_ptr(), d.data_ptr(), d_stride, _ptr(weight_out), _ptr(bias_out),
-            _DTYPES[torch.float32 if wanted is None else wanted.dtype], workspace.data_ptr(), need, _stream(device))
+            cfg, rows, g.data_ptr(), g.stride(0), 0 if kept else m.data_ptr(), 0 if kept else m.stride(0),
+            x._struct if kept else None, 0 if weight is None else weight.data_ptr(), stats.data_ptr(), d.data_ptr(),
+            d_stride, _ptr(weight_out), _ptr(bias_out), _DTYPES[vectors], workspace.data_ptr(), need,
+            current_stream(device.index))
     return out, weight_out, bias_out
 
 
@@ -531,20 +542,19 @@ class _LayerNorm(torch.autograd.Function):
     def forward(ctx, x, weight, bias, eps, center, pack):
         x = _with_rows(x)
         y, stats, *packed = layer_norm(x, weight, bias, eps=eps, center=center, pack=pack)
+        ctx.center, ctx.packed = center, None
         if packed:
-            codes, scales, ctx.shape, ctx.dtype = packed[0]
-            ctx.save_for_backward(weight, bias, stats, codes, scales)
-        else:
-            ctx.save_for_backward(weight, bias, stats, x)
-        ctx.center = center
+            ctx.packed = pack, x.shape, x.dtype
+            x = packed[0].data
+        ctx.save_for_backward(x, weight, bias, stats)
         return y
 
     @staticmethod
     @once_differentiable  # a second derivative raises: the kernels record no graph
     def backward(ctx, dy):
-        weight, bias, stats, x, *scales = ctx.saved_tensors
-        if scales:
-            x = PackedActivations(x, scales[0], ctx.shape, ctx.dtype)
+        x, weight, bias, stats = ctx.saved_tensors
+        if ctx.packed:
+            x = PackedActivations(x, *ctx.packed)
         dx, dweight, dbias = layer_norm_backward(_with_rows(dy), x, weight, stats, center=ctx.center,
                                                  bias=bias is not None)
         return (dx, dweight.to(weight.dtype) if weight is not None else None,
@@ -564,10 +574,12 @@ def layer_norm_autograd(x, weight=None, bias=None, *, eps: float = 1e-5, center:
 _ID_BYTES = {torch.int32: 4, torch.int64: 8}
 
 
-def _check_ids(ids: torch.Tensor) -> torch.Tensor:
-    if ids.dtype not in _ID_BYTES or not ids.is_cuda:
-        raise ValueError("ids must be an int32 or int64 CUDA tensor")
-    return ids if ids.is_contiguous() else ids.contiguous()
+def _check_ids(ids: torch.Tensor, device: torch.device) -> Tuple[torch.Tensor, int]:
+    """`ids` contiguous, and the bytes of one."""
+    size = _ID_BYTES.get(ids.dtype)
+    if size is None or ids.device != device:
+        raise ValueError("ids must be an int32 or int64 tensor on the device of the others")
+    return (ids if ids.is_contiguous() else ids.contiguous()), size
 
 
 def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0,
@@ -580,29 +592,26 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0,
     fills ``out``) ids.shape + (dim,).  A ``table`` that requires a gradient is
     refused: :func:`embedding_autograd` records it.
     """
-    _no_graph("embedding (embedding_autograd does)", table)
-    if table.dim() != 2:
-        raise ValueError("table must be a matrix")
-    _check_rows(table, "table")
-    device, (rows, dim) = table.device, table.shape
-    ids = _check_ids(ids)
-    if ids.device != device:
-        raise ValueError("ids and table must be on one device")
-    if table.stride(1) != 1 and dim > 1:
-        raise ValueError("the columns of table must be contiguous")
+    if _grad_enabled():
+        _no_graph("embedding (embedding_autograd does)", table)
+    kind, device = _check_rows(table, "table"), table.device
+    if table.dim() != 2 or (table.stride(1) != 1 and table.size(1) > 1):
+        raise ValueError("table must be a matrix with contiguous columns")
+    rows, dim = table.shape
+    ids, size = _check_ids(ids, device)
     if out is None:
         out = torch.empty((*ids.shape, dim), dtype=table.dtype, device=device)
-        y, stride = out, dim
+        at, stride = out.data_ptr(), dim
     else:
         if out.shape != (*ids.shape, dim) or out.dtype != table.dtype or out.device != device:
             raise ValueError("out must have the shape of ids and dim, and table's type and device")
         y = _matrix(out, "out", copy=False)
-        stride = y.stride(0)
+        at, stride = y.data_ptr(), y.stride(0)
         _check_memory((y,), ((), (table, ids)))
+    cfg = _embedding_config(rows, dim, kind, size, float(scale))
     with _on(device):
-        B.zero_embedding(_embedding_config(rows, dim, _DTYPES[table.dtype], _ID_BYTES[ids.dtype], float(scale)),
-                         ids.numel(), ids.data_ptr(), table.data_ptr(), table.stride(0), y.data_ptr(), stride,
-                         _stream(device))
+        B.zero_embedding(cfg, ids.numel(), ids.data_ptr(), table.data_ptr(), table.stride(0), at, stride,
+                         current_stream(device.index))
     return out
 
 
@@ -621,28 +630,29 @@ def embedding_backward(dy: torch.Tensor, ids: torch.Tensor, rows: int, *, scale:
     zeroed; with ``accumulate`` the sums are added to ``out`` instead, and those
     rows stay as they are.
     """
-    _no_graph("embedding_backward", dy, out)
-    _check_rows(dy, "dy")
-    ids, rows, device, dim = _check_ids(ids), operator.index(rows), dy.device, dy.size(-1)
-    if dy.shape != (*ids.shape, dim) or ids.device != device:
-        raise ValueError("dy must have the shape of ids and one more dimension, on one device")
+    if _grad_enabled():
+        _no_graph("embedding_backward", dy, out)
+    kind, device, dim, rows = _check_rows(dy, "dy"), dy.device, dy.size(-1), operator.index(rows)
+    ids, size = _check_ids(ids, device)
+    if dy.shape[:-1] != ids.shape:
+        raise ValueError("dy must have the shape of ids and one more dimension")
     g = _matrix(dy, "dy")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs an out to add to")
-        out = torch.empty((rows, dim), dtype=dy.dtype, device=device)
+        out, out_kind = torch.empty((rows, dim), dtype=dy.dtype, device=device), kind
     else:
-        if out.shape != (rows, dim) or out.dtype not in _DTYPES or out.device != device or (
-                out.stride(1) != 1 and dim > 1):
+        out_kind = _DTYPES.get(out.dtype)
+        if out_kind is None or out.shape != (rows, dim) or out.device != device or (out.stride(1) != 1 and dim > 1):
             raise ValueError("out must be a bf16 or fp32 matrix (rows, dim) with contiguous columns")
         _check_memory((out,), ((), (g, ids)))
+    tokens = ids.numel()
+    cfg, need = _embedding_config(rows, dim, kind, size, float(scale)), _embedding_workspace(rows, dim, tokens)
     with _on(device):
-        need = _embedding_workspace(rows, dim, ids.numel())
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        B.zero_embedding_backward(_embedding_config(rows, dim, _DTYPES[dy.dtype], _ID_BYTES[ids.dtype], float(scale)),
-                                  ids.numel(), ids.data_ptr(), g.data_ptr(), g.stride(0), out.data_ptr(),
-                                  _DTYPES[out.dtype], out.stride(0), 1 if accumulate else 0, workspace.data_ptr(),
-                                  need, _stream(device))
+        B.zero_embedding_backward(cfg, tokens, ids.data_ptr(), g.data_ptr(), g.stride(0), out.data_ptr(), out_kind,
+                                  out.stride(0), 1 if accumulate else 0, workspace.data_ptr(), need,
+                                  current_stream(device.index))
     return out
 
 
