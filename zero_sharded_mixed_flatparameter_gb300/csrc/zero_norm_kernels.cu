@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kLaneThreads, kLaneCtas) norm_lanes_forward_ke
       if (a.form != 0) {
         F2 pairs[4];
         to_pairs(x[i], pairs);
-        pack_eight<8>(pairs, lane, lanes, a.groups, real, a.form, a.codes + r * a.groups * kPackGroup,
+        pack_eight(pairs, lane, lanes, a.groups, real, a.form, a.codes + r * a.groups * kPackGroup,
                       a.scales + r * a.groups);
       }
       const float rstd = rsqrtf(fmaf(total[i], a.inv_cols, a.eps));
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kLaneThreads, kLaneCtas) norm_lanes_backward_k
   for (long long r0 = first; r0 < a.rows; r0 += step * kRows) {
     const long long mine = r0 + threadIdx.x / lanes;
     Eight<kFp32, 8> raw[kRows], grad[kRows];
-    EightCodes<8> codes[kRows];
+    EightCodes codes[kRows];
     float2 stats[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(kLaneThreads, kLaneCtas) norm_lanes_backward_k
       const bool real = r < a.rows;
       stats[i] = real ? a.stats[r] : make_float2(0.0f, 0.0f);
       if constexpr (kPacked) {
-        load_codes<8>(a.codes + r * a.groups * kPackGroup, a.scales + r * a.groups, lane, lanes, real ? a.groups : 0, &codes[i]);
+        load_codes(a.codes + r * a.groups * kPackGroup, a.scales + r * a.groups, lane, real ? a.groups : 0, &codes[i]);
       } else {
         load_eight<kFp32, 8>(static_cast<const char*>(a.x) + r * a.x_stride * kSize, lane, lanes, real ? a.cols : 0, &raw[i]);
       }
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kLaneThreads, kLaneCtas) norm_lanes_backward_k
     for (int i = 0; i < kRows; ++i) {
       if constexpr (kPacked) {
         F2 pairs[4];
-        widen_codes<8>(codes[i], a.form, pairs);
+        widen_codes(codes[i], a.form, pairs);
         from_pairs(pairs, xn[i]);
       } else {
         widen_eight<kFp32, 8>(raw[i], xn[i]);
@@ -291,12 +291,14 @@ struct GroupSum {
 template <bool kFp32, int kVec, int kN>
 constexpr int kForwardRows = kN * (kFp32 || kVec == 1 ? 2 : 1) >= 8 ? 1 : kN * (kFp32 || kVec == 1 ? 2 : 1) >= 4 ? 2 : 4;
 
-template <bool kFp32, int kVec, int kN, bool kPack>
+// kForm: of the 8-bit form, 0: none.
+template <bool kFp32, int kVec, int kN, int kForm>
 __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(const __grid_constant__ NormArgs a) {
   constexpr int kRows = kForwardRows<kFp32, kVec, kN>;  // in flight
   constexpr long long kSize = kFp32 ? 4 : 2;
   extern __shared__ __align__(16) float tables[];
   __shared__ float buffer[2][kNormWarps][kRows];
+  __shared__ __align__(16) float turned[kVec == 1 && kForm ? kForwardWarps : 1][256];
   GroupSum<kRows> sum(buffer, a.lanes);
   const Slots<kVec, kN> own{a.lanes, static_cast<int>(threadIdx.x) % a.lanes};
   float *weight = tables, *bias = tables + kN * 8 * a.lanes;
@@ -389,9 +391,19 @@ __global__ void __launch_bounds__(kForwardWarps * 32, 1) norm_forward_kernel(con
         F2 x[4];
         forget_widened(raw[i][n]);
         widen_pairs<kFp32, kVec>(raw[i][n], x);
-        if constexpr (kPack) {
-          pack_eight<kVec>(x, own.lane_of(n), own.lanes, a.groups - own.at(n) / kPackGroup, real, a.form,
-                           a.codes + r * a.groups * kPackGroup + own.at(n), a.scales + r * a.groups + own.at(n) / kPackGroup);
+        if constexpr (kForm && kVec == 8) {
+          pack_eight(x, own.lane_of(n), own.lanes, a.groups, real, kForm, a.codes + r * a.groups * kPackGroup,
+                     a.scales + r * a.groups);
+        } else if constexpr (kForm) {
+          F2 p[4];
+          to_neighbours(x, turned[threadIdx.x / 32], p);
+          uint32_t byte;
+          const uint2 c = encode_eight(p, 4, kForm, &byte);
+          const int g = turned_group(n, own.lane, own.lanes);
+          if (real && g < a.groups) {
+            *reinterpret_cast<uint2*>(a.codes + (r * a.groups + g) * kPackGroup + own.lane % 4 * 8) = c;
+            if (own.lane % 4 == 0) a.scales[r * a.groups + g] = static_cast<uint8_t>(byte);
+          }
         }
         const F2 rstd = both(total[i]);
 #pragma unroll
@@ -415,15 +427,17 @@ constexpr int kStages = 3;
 template <bool kFp32, int kN, bool kPacked>
 constexpr int kTurnBytes = kBackwardRows<kFp32, 8, kN> * kN * (16 * (kFp32 ? 2 : 1) + (kPacked ? 8 : 16 * (kFp32 ? 2 : 1)));
 
-template <bool kFp32, int kVec, int kN, bool kPacked>
+template <bool kFp32, int kVec, int kN, int kForm>
 __global__ void __launch_bounds__(kBackwardWarps * 32, 1) norm_backward_kernel(const __grid_constant__ NormArgs a) {
   constexpr int kRows = kBackwardRows<kFp32, kVec, kN>;
   constexpr long long kSize = kFp32 ? 4 : 2;
+  constexpr bool kPacked = kForm != 0;  // x comes from its 8-bit form
   constexpr bool kAhead = kVec == 8;
   constexpr int kWords = kFp32 ? 2 : 1;  // 16-byte words of eight elements
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join waits for all of this
   extern __shared__ __align__(16) float tables[];
   __shared__ float buffer[2][kNormWarps][2 * kRows];
+  __shared__ __align__(16) float turned[kVec == 1 && kPacked ? kBackwardWarps : 1][256];
   GroupSum<2 * kRows> sum(buffer, a.lanes);
   const Slots<kVec, kN> own{a.lanes, static_cast<int>(threadIdx.x) % a.lanes};
   const int groups = blockDim.x / a.lanes, group = threadIdx.x / a.lanes;
@@ -486,7 +500,7 @@ __global__ void __launch_bounds__(kBackwardWarps * 32, 1) norm_backward_kernel(c
   int stage = 0;
   for (long long r0 = mine; r0 < a.rows; r0 += step) {
     Eight<kFp32, kVec> raw[kRows][kN], grad[kRows][kN];
-    EightCodes<kVec> codes[kRows][kN];
+    EightCodes codes[kRows][kN];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       stats[i] = next_stats[i];
@@ -529,9 +543,10 @@ __global__ void __launch_bounds__(kBackwardWarps * 32, 1) norm_backward_kernel(c
         const char* drow = static_cast<const char*>(a.dy) + r * a.dy_stride * kSize;
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
-          if constexpr (kPacked) {
-            load_codes<kVec>(a.codes + r * a.groups * kPackGroup + own.at(n), a.scales + r * a.groups + own.at(n) / kPackGroup,
-                             own.lane_of(n), own.lanes, real ? a.groups - own.at(n) / kPackGroup : 0, &codes[i][n]);
+          if constexpr (kPacked) {  // of a group of the warp's, to be turned
+            const int g = turned_group(n, own.lane, own.lanes);
+            load_codes(a.codes + (r * a.groups + g) * kPackGroup, a.scales + r * a.groups + g, own.lane % 4,
+                       real && g < a.groups ? 1 : 0, &codes[i][n]);
           } else {
             load_eight<kFp32, kVec>(row + own.at(n) * kSize, own.lane_of(n), own.lanes, real ? a.cols - own.at(n) : 0,
                                     &raw[i][n]);
@@ -543,8 +558,15 @@ __global__ void __launch_bounds__(kBackwardWarps * 32, 1) norm_backward_kernel(c
     }
     // xn, and dy (columns past the last: dy is zero, and what they add to sums, too)
     auto values = [&](int i, int n, F2* xn, F2* g) {
-      if constexpr (kPacked) widen_codes<kVec>(codes[i][n], a.form, xn);
-      else widen_pairs<kFp32, kVec>(raw[i][n], xn);
+      if constexpr (kPacked) {
+        widen_codes(codes[i][n], kForm, xn);
+        if constexpr (kVec == 1) {
+          F2 p[4] = {xn[0], xn[1], xn[2], xn[3]};
+          to_singles(p, turned[threadIdx.x / 32], xn);
+        }
+      } else {
+        widen_pairs<kFp32, kVec>(raw[i][n], xn);
+      }
       widen_pairs<kFp32, kVec>(grad[i][n], g);
       const F2 less = both(-stats[i].x), rstd = both(stats[i].y);
 #pragma unroll
@@ -798,17 +820,19 @@ int most_parts(int cols, long long rows) {
   return a > b ? a : b;
 }
 
-template <auto kKernel>
+// kMost: of dynamic shared memory.
+template <auto kKernel, int kMost>
 void launch_with(const NormArgs& a, const Shape& s, int ctas, int bytes, cudaStream_t st) {
-  if (bytes > 40 * 1024 && allow_shared<kKernel>() != cudaSuccess) return;  // reported as the launch's error
+  if (bytes > 20 * 1024 && allow_shared<kKernel, kMost>() != cudaSuccess) return;  // reported as the launch's error
   kKernel<<<ctas, s.threads, bytes, st>>>(a);
 }
 
 template <bool kFp32, int kVec, int kN>
 void launch_forward_n(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st) {
   const int bytes = 2 * kN * 8 * s.lanes * static_cast<int>(sizeof(float));
-  if (a.form) launch_with<norm_forward_kernel<kFp32, kVec, kN, true>>(a, s, ctas, bytes, st);
-  else launch_with<norm_forward_kernel<kFp32, kVec, kN, false>>(a, s, ctas, bytes, st);
+  if (a.form == 0) launch_with<norm_forward_kernel<kFp32, kVec, kN, 0>, 64 * 1024>(a, s, ctas, bytes, st);
+  else if (a.form == kPackE4m3) launch_with<norm_forward_kernel<kFp32, kVec, kN, kPackE4m3>, 64 * 1024>(a, s, ctas, bytes, st);
+  else launch_with<norm_forward_kernel<kFp32, kVec, kN, kPackInt8>, 64 * 1024>(a, s, ctas, bytes, st);
 }
 template <bool kFp32, int kVec>
 void launch_forward(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st) {
@@ -822,19 +846,25 @@ void launch_forward(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st
   if (s.n == 2) launch_forward_n<kFp32, kVec, 2>(a, s, ctas, st);
   else launch_forward_n<kFp32, kVec, 1>(a, s, ctas, st);
 }
-template <bool kFp32, int kVec, int kN, bool kPacked>
+template <bool kFp32, int kVec, int kN, int kForm>
 void launch_backward_n(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st) {
   const int bytes = kN * 8 * s.lanes * static_cast<int>(sizeof(float)) +
-                    (kVec == 8 ? kStages * kTurnBytes<kFp32, kN, kPacked> * s.threads : 0);
-  launch_with<norm_backward_kernel<kFp32, kVec, kN, kPacked>>(a, s, ctas, bytes, st);
+                    (kVec == 8 ? kStages * kTurnBytes<kFp32, kN, kForm != 0> * s.threads : 0);
+  launch_with<norm_backward_kernel<kFp32, kVec, kN, kForm>, (kVec == 8 ? 225 : 32) * 1024>(a, s, ctas, bytes, st);
 }
-template <bool kFp32, int kVec, bool kPacked>
-void launch_backward(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st) {
+template <bool kFp32, int kVec, int kForm>
+void launch_backward_form(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st) {
   if constexpr (kVec == 8) {
-    if (s.lanes < 32) return norm_lanes_backward_kernel<kFp32, kPacked><<<ctas, s.threads, 0, st>>>(a);
+    if (s.lanes < 32) return norm_lanes_backward_kernel<kFp32, kForm != 0><<<ctas, s.threads, 0, st>>>(a);
   }
-  if (s.n == 2) launch_backward_n<kFp32, kVec, 2, kPacked>(a, s, ctas, st);
-  else launch_backward_n<kFp32, kVec, 1, kPacked>(a, s, ctas, st);
+  if (s.n == 2) launch_backward_n<kFp32, kVec, 2, kForm>(a, s, ctas, st);
+  else launch_backward_n<kFp32, kVec, 1, kForm>(a, s, ctas, st);
+}
+template <bool kFp32, int kVec>
+void launch_backward(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st) {
+  if (a.form == 0) launch_backward_form<kFp32, kVec, 0>(a, s, ctas, st);
+  else if (a.form == kPackE4m3) launch_backward_form<kFp32, kVec, kPackE4m3>(a, s, ctas, st);
+  else launch_backward_form<kFp32, kVec, kPackInt8>(a, s, ctas, st);
 }
 template <bool kFp32, bool kPacked>
 void launch_wide_backward(const NormArgs& a, int ctas, cudaStream_t st) {
@@ -1001,11 +1031,11 @@ zero_status zero_layer_norm_backward(const zero_norm_config* cfg, int64_t rows, 
       if (fp32) packed ? launch_wide_backward<true, true>(a, ctas, cs) : launch_wide_backward<true, false>(a, ctas, cs);
       else packed ? launch_wide_backward<false, true>(a, ctas, cs) : launch_wide_backward<false, false>(a, ctas, cs);
     } else if (s.vec) {
-      if (fp32) packed ? launch_backward<true, 8, true>(a, s, ctas, cs) : launch_backward<true, 8, false>(a, s, ctas, cs);
-      else packed ? launch_backward<false, 8, true>(a, s, ctas, cs) : launch_backward<false, 8, false>(a, s, ctas, cs);
+      if (fp32) launch_backward<true, 8>(a, s, ctas, cs);
+      else launch_backward<false, 8>(a, s, ctas, cs);
     } else {
-      if (fp32) packed ? launch_backward<true, 1, true>(a, s, ctas, cs) : launch_backward<true, 1, false>(a, s, ctas, cs);
-      else packed ? launch_backward<false, 1, true>(a, s, ctas, cs) : launch_backward<false, 1, false>(a, s, ctas, cs);
+      if (fp32) launch_backward<true, 1>(a, s, ctas, cs);
+      else launch_backward<false, 1>(a, s, ctas, cs);
     }
     if ((st = launch_status("layer norm backward launch")) != ZERO_OK) return st;
   }

@@ -10,10 +10,7 @@ namespace zfs {
 namespace {
 
 constexpr int kPackThreads = 256;
-template <int kVec>
-constexpr int kPackRows = kVec == 8 ? 4 : 1;  // in flight
-template <int kVec>
-constexpr int kPackCtas = kVec == 8 ? 5 : 4;  // of an SM (48, 64 registers)
+constexpr int kPackCtas = 5;  // of an SM (48 registers)
 
 struct PackArgs {
   long long rows;
@@ -25,10 +22,12 @@ struct PackArgs {
 };
 
 // A thread takes eight columns of kRows rows at a time, `lanes` threads a row.
-template <bool kFp32, int kVec, bool kPack>
-__global__ void __launch_bounds__(kPackThreads, kPackCtas<kVec>) pack_kernel(const __grid_constant__ PackArgs a) {
-  constexpr int kRows = kPackRows<kVec>;
+// kAligned: whole 16-byte words, else a warp's lanes all hold one row.
+template <bool kFp32, bool kAligned, bool kPack, int kForm>
+__global__ void __launch_bounds__(kPackThreads, kPackCtas) pack_kernel(const __grid_constant__ PackArgs a) {
+  constexpr int kRows = kAligned ? 4 : kPack ? 2 : 1;  // in flight
   constexpr long long kSize = kFp32 ? 4 : 2;
+  __shared__ __align__(16) float turned[kAligned || kPack ? 1 : kPackThreads / 32][256];
   const int lanes = a.lanes, lane = threadIdx.x % lanes, per_cta = kPackThreads / lanes;
   const long long step = static_cast<long long>(gridDim.x) * per_cta;
   const long long first = static_cast<long long>(blockIdx.x) * per_cta;
@@ -36,18 +35,19 @@ __global__ void __launch_bounds__(kPackThreads, kPackCtas<kVec>) pack_kernel(con
     const long long mine = r0 + threadIdx.x / lanes;
     for (int at = 0; at < a.cols; at += lanes * 8) {
       const int cols = a.cols - at, groups = a.groups - at / kPackGroup;
-      Eight<kFp32, kVec> raw[kRows];
-      EightCodes<kVec> codes[kRows];
+      Eight<kFp32, 8> raw[kRows];
+      EightCodes codes[kRows];
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const long long r = mine + step * i;
         const bool real = r < a.rows;
         if constexpr (kPack) {
-          load_eight<kFp32, kVec>(static_cast<const char*>(a.x) + (r * a.x_stride + at) * kSize, lane, lanes,
-                                  real ? cols : 0, &raw[i]);
+          const char* row = static_cast<const char*>(a.x) + (r * a.x_stride + at) * kSize;
+          if constexpr (kAligned) load_eight<kFp32, 8>(row, lane, lanes, real ? cols : 0, &raw[i]);
+          else load_neighbours<kFp32>(row, lane, real ? cols : 0, &raw[i]);
         } else {
-          load_codes<kVec>(a.codes + r * a.groups * kPackGroup + at, a.scales + r * a.groups + at / kPackGroup, lane,
-                           lanes, real ? groups : 0, &codes[i]);
+          load_codes(a.codes + r * a.groups * kPackGroup + at, a.scales + r * a.groups + at / kPackGroup, lane,
+                     real ? groups : 0, &codes[i]);
         }
       }
 #pragma unroll
@@ -55,13 +55,18 @@ __global__ void __launch_bounds__(kPackThreads, kPackCtas<kVec>) pack_kernel(con
         const long long r = mine + step * i;
         F2 x[4];
         if constexpr (kPack) {
-          widen_pairs<kFp32, kVec>(raw[i], x);
-          pack_eight<kVec>(x, lane, lanes, groups, r < a.rows, a.form, a.codes + r * a.groups * kPackGroup + at,
-                           a.scales + r * a.groups + at / kPackGroup);
+          widen_pairs<kFp32, 8>(raw[i], x);
+          pack_eight(x, lane, lanes, groups, r < a.rows, kForm, a.codes + r * a.groups * kPackGroup + at,
+                     a.scales + r * a.groups + at / kPackGroup);
         } else {
-          widen_codes<kVec>(codes[i], a.form, x);
-          if (r < a.rows) {
-            store_pairs<kFp32, kVec>(static_cast<char*>(a.x) + (r * a.x_stride + at) * kSize, lane, lanes, cols, x);
+          widen_codes(codes[i], kForm, x);
+          char* row = static_cast<char*>(a.x) + (r * a.x_stride + at) * kSize;
+          const bool real = r < a.rows;
+          if constexpr (kAligned) {
+            if (real) store_pairs<kFp32, 8>(row, lane, lanes, cols, x);
+          } else {
+            const int skip = lane / 32 * 256;  // the same row for the whole warp
+            store_neighbours<kFp32>(row + skip * kSize, real ? cols - skip : 0, x, turned[threadIdx.x / 32]);
           }
         }
       }
@@ -69,14 +74,14 @@ __global__ void __launch_bounds__(kPackThreads, kPackCtas<kVec>) pack_kernel(con
   }
 }
 
-template <bool kPack>
-void launch_pack(const PackArgs& a, bool fp32, bool vec, int ctas, cudaStream_t s) {
+template <bool kPack, int kForm>
+void launch_pack(const PackArgs& a, bool fp32, bool aligned, int ctas, cudaStream_t s) {
   if (fp32) {
-    if (vec) pack_kernel<true, 8, kPack><<<ctas, kPackThreads, 0, s>>>(a);
-    else pack_kernel<true, 1, kPack><<<ctas, kPackThreads, 0, s>>>(a);
+    if (aligned) pack_kernel<true, true, kPack, kForm><<<ctas, kPackThreads, 0, s>>>(a);
+    else pack_kernel<true, false, kPack, kForm><<<ctas, kPackThreads, 0, s>>>(a);
   } else {
-    if (vec) pack_kernel<false, 8, kPack><<<ctas, kPackThreads, 0, s>>>(a);
-    else pack_kernel<false, 1, kPack><<<ctas, kPackThreads, 0, s>>>(a);
+    if (aligned) pack_kernel<false, true, kPack, kForm><<<ctas, kPackThreads, 0, s>>>(a);
+    else pack_kernel<false, false, kPack, kForm><<<ctas, kPackThreads, 0, s>>>(a);
   }
 }
 
@@ -102,16 +107,16 @@ zero_status convert(int64_t rows, int64_t cols, const void* x, int32_t dtype, in
   a.x_stride = x_stride;
   a.codes = static_cast<uint8_t*>(packed->codes);
   a.scales = static_cast<uint8_t*>(packed->scales);
-  const bool vec = cols % 8 == 0 && rows_aligned(x, x_stride, rows, dtype);
-  // whole groups for a warp's lanes where elements are single
+  const bool aligned = cols % 8 == 0 && rows_aligned(x, x_stride, rows, dtype);
   const int need = (a.cols + 7) / 8, lanes = power_of_two(need < kPackThreads ? need : kPackThreads);
-  a.lanes = vec || lanes >= 32 ? lanes : 32;
+  a.lanes = aligned || lanes >= 32 ? lanes : 32;
   const long long per_cta = kPackThreads / a.lanes, want = (rows + per_cta - 1) / per_cta;
-  const long long most = static_cast<long long>(sm_count()) * (vec ? kPackCtas<8> : kPackCtas<1>);
+  const long long most = static_cast<long long>(sm_count()) * kPackCtas;
   const int ctas = static_cast<int>(want < most ? want : most);
+  const bool fp32 = dtype == ZERO_GRAD_FP32, e4m3 = a.form == kPackE4m3;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (pack) launch_pack<true>(a, dtype == ZERO_GRAD_FP32, vec, ctas, s);
-  else launch_pack<false>(a, dtype == ZERO_GRAD_FP32, vec, ctas, s);
+  if (pack) e4m3 ? launch_pack<true, kPackE4m3>(a, fp32, aligned, ctas, s) : launch_pack<true, kPackInt8>(a, fp32, aligned, ctas, s);
+  else e4m3 ? launch_pack<false, kPackE4m3>(a, fp32, aligned, ctas, s) : launch_pack<false, kPackInt8>(a, fp32, aligned, ctas, s);
   return launch_status(pack ? "pack launch" : "unpack launch");
 }
 

@@ -13,6 +13,45 @@ namespace zfs {
 constexpr int kPackGroup = 32;                  // columns that share a scale
 constexpr int kPackE4m3 = 1, kPackInt8 = 2;     // forms (0: none), as the public ones plus 1
 
+// Two fp32 values in one register pair: the packed instructions round each like
+// the single ones, at half the instructions.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 both(float x) { return pair(x, x); }
+__device__ __forceinline__ void split(F2 v, float* lo, float* hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v)); }
+__device__ __forceinline__ float sum_of(F2 v) {
+  float lo, hi;
+  split(v, &lo, &hi);
+  return lo + hi;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ void to_pairs(const float* x, F2* p) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) p[k] = pair(x[2 * k], x[2 * k + 1]);
+}
+__device__ __forceinline__ void from_pairs(const F2* p, float* x) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) split(p[k], &x[2 * k], &x[2 * k + 1]);
+}
+
 // Eight elements of a row as loaded.  kVec 8: eight neighbours from column
 // 8 * lane on, 16-byte aligned; kVec 1: kCount (8, or fewer) columns lane,
 // lane + lanes, ... (so that neighbouring threads read neighbouring columns
@@ -67,6 +106,43 @@ __device__ __forceinline__ void widen_eight(const Eight<kFp32, kVec, kCount>& v,
   }
 }
 
+// Eight neighbours of a row at any alignment: single loads, of which a line's
+// later ones find it in L1.
+template <bool kFp32>
+__device__ __forceinline__ void load_neighbours(const void* row, int lane, int cols, Eight<kFp32, 8>* v) {
+  uint32_t u[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int c = lane * 8 + k;
+    u[k] = 0u;
+    if (c < cols) {
+      if constexpr (kFp32) u[k] = static_cast<const uint32_t*>(row)[c];
+      else u[k] = static_cast<const uint16_t*>(row)[c];
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < (kFp32 ? 8 : 4); ++k) v->w[k] = kFp32 ? u[k] : u[2 * k] | u[2 * k + 1] << 16;
+}
+// A warp's 256 neighbours to a row at any alignment, turned in shared memory so
+// that every store writes 32 neighbours.  `cols`: of the warp's.
+template <bool kFp32>
+__device__ __forceinline__ void store_neighbours(void* row, int cols, const F2* p, float* turned) {
+  const int lane = threadIdx.x % 32;
+  F2* mine = reinterpret_cast<F2*>(turned) + lane * 4;
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) mine[k] = p[k];
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int c = k * 32 + lane;
+    if (c < cols) {
+      if constexpr (kFp32) static_cast<float*>(row)[c] = turned[c];
+      else static_cast<uint16_t*>(row)[c] = to_bf16_bits(turned[c]);
+    }
+  }
+}
+
 // Asynchronous copies of a thread's own bytes to its own place in shared memory:
 // it waits for its own groups of copies, with no barrier and nothing to poll.
 template <int kBytes>
@@ -112,45 +188,6 @@ __device__ __forceinline__ void store_eight(void* row, int lane, int lanes, int 
       }
     }
   }
-}
-
-// Two fp32 values in one register pair: the packed instructions round each like
-// the single ones, at half the instructions.
-using F2 = unsigned long long;
-__device__ __forceinline__ F2 pair(float lo, float hi) {
-  F2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ F2 both(float x) { return pair(x, x); }
-__device__ __forceinline__ void split(F2 v, float* lo, float* hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v)); }
-__device__ __forceinline__ float sum_of(F2 v) {
-  float lo, hi;
-  split(v, &lo, &hi);
-  return lo + hi;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-  F2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-  F2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-  F2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ void to_pairs(const float* x, F2* p) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) p[k] = pair(x[2 * k], x[2 * k + 1]);
-}
-__device__ __forceinline__ void from_pairs(const F2* p, float* x) {
-#pragma unroll
-  for (int k = 0; k < 4; ++k) split(p[k], &x[2 * k], &x[2 * k + 1]);
 }
 
 template <bool kFp32, int kVec>
@@ -233,98 +270,97 @@ __device__ __forceinline__ float decode1(uint32_t code, int form) {
   return static_cast<float>(static_cast<int8_t>(code));
 }
 
-// Writes the 8-bit form of the thread's eight elements; every lane of the warp
-// calls it.  `lanes`: threads that hold the row (a power of two below 32, or a
-// multiple of 32); `write`: the thread's row exists.  Codes past the last column
-// of the last group are zero.
-template <int kVec>
-__device__ __forceinline__ void pack_eight(const F2* p, int lane, int lanes, int groups, bool write, int form,
-                                           uint8_t* codes, uint8_t* scales) {
+// The codes of the thread's eight neighbours, a quarter of a group whose others
+// the next lanes hold, and the group's scale; every lane of the warp calls it.
+// quarters: lanes that hold a part of the group (the rest of it does not exist).
+__device__ __forceinline__ uint2 encode_eight(const F2* p, int quarters, int form, uint32_t* byte) {
   float x[8];
   from_pairs(p, x);
-  if constexpr (kVec == 8) {
-    uint32_t m = 0;
+  uint32_t m = 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7FFFFFFFu);
+  for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(x[k]) & 0x7FFFFFFFu);
 #pragma unroll
-    for (int o = 1; o < 4; o <<= 1) {
-      const uint32_t other = __shfl_xor_sync(0xffffffffu, m, o);
-      if (o < lanes) m = max(m, other);
-    }
-    const uint32_t byte = scale_byte(m, form);
-    const F2 inv = both(inverse_scale(byte));
-    F2 q[4];
+  for (int o = 1; o < 4; o <<= 1) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, m, o);
+    if (o < quarters) m = max(m, other);
+  }
+  *byte = scale_byte(m, form);
+  const F2 inv = both(inverse_scale(*byte));
+  F2 q[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) q[k] = mul2(p[k], inv);
-    float s[8];
-    from_pairs(q, s);
-    uint2 c = make_uint2(encode4(s, form), encode4(s + 4, form));
-    if (byte == 255u) c = make_uint2(0u, 0u);
-    if (write && lane < groups * 4) {
-      *reinterpret_cast<uint2*>(codes + static_cast<long long>(lane) * 8) = c;
-      if (lane % 4 == 0) scales[lane / 4] = static_cast<uint8_t>(byte);
-      // fewer lanes than a group's quarters: the rest of the only group
-      if (lane + 1 == lanes) {
-        for (int q4 = lanes; q4 < 4; ++q4) *reinterpret_cast<uint2*>(codes + q4 * 8) = make_uint2(0u, 0u);
-      }
-    }
-  } else {
-    // every element's group is a warp's: eight independent ones
-    uint32_t byte[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      byte[k] = scale_byte(__reduce_max_sync(0xffffffffu, __float_as_uint(x[k]) & 0x7FFFFFFFu), form);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int at = k * lanes + lane;
-      if (write && at / kPackGroup < groups) {
-        codes[at] = static_cast<uint8_t>(byte[k] == 255u ? 0u : encode1(x[k] * inverse_scale(byte[k]), form));
-        if (lane % 32 == 0) scales[at / kPackGroup] = static_cast<uint8_t>(byte[k]);
-      }
+  for (int k = 0; k < 4; ++k) q[k] = mul2(p[k], inv);
+  from_pairs(q, x);
+  return *byte == 255u ? make_uint2(0u, 0u) : make_uint2(encode4(x, form), encode4(x + 4, form));
+}
+
+// Writes the 8-bit form of the thread's eight neighbours (from column 8 * lane
+// on); every lane of the warp calls it.  `lanes`: threads that hold the row (a
+// power of two below 32, or a multiple of 32); `write`: the thread's row exists.
+// Codes past the last column of the last group are zero.
+__device__ __forceinline__ void pack_eight(const F2* p, int lane, int lanes, int groups, bool write, int form,
+                                           uint8_t* codes, uint8_t* scales) {
+  uint32_t byte;
+  const uint2 c = encode_eight(p, lanes < 4 ? lanes : 4, form, &byte);
+  if (write && lane < groups * 4) {
+    *reinterpret_cast<uint2*>(codes + static_cast<long long>(lane) * 8) = c;
+    if (lane % 4 == 0) scales[lane / 4] = static_cast<uint8_t>(byte);
+    // fewer lanes than a group's quarters: the rest of the only group
+    if (lanes < 4 && lane + 1 == lanes) {
+      for (int q = lanes; q < 4; ++q) *reinterpret_cast<uint2*>(codes + q * 8) = make_uint2(0u, 0u);
     }
   }
 }
 
-// The thread's eight elements in 8 bits, as loaded, and as values.
-template <int kVec>
-struct EightCodes {
-  uint32_t w[kVec == 8 ? 3 : 8];  // kVec 8: codes, the scale's byte; kVec 1: code | scale << 8
-};
-template <int kVec>
-__device__ __forceinline__ void load_codes(const uint8_t* codes, const uint8_t* scales, int lane, int lanes, int groups,
-                                           EightCodes<kVec>* v) {
-  if constexpr (kVec == 8) {
-    v->w[0] = v->w[1] = v->w[2] = 0u;
-    if (lane < groups * 4) {
-      const uint2 c = __ldcs(reinterpret_cast<const uint2*>(codes + static_cast<long long>(lane) * 8));
-      v->w[0] = c.x; v->w[1] = c.y;
-      v->w[2] = scales[lane / 4];
-    }
-  } else {
+// Single elements (column k * lanes + lane) are turned within the warp, in its
+// 256 floats of shared memory, into eight neighbours of one of its eight groups of
+// 32 columns, and back.
+__device__ __forceinline__ void to_neighbours(const F2* singles, float* turned, F2* p) {
+  const int l = threadIdx.x % 32;
+  float x[8];
+  from_pairs(singles, x);
+  __syncwarp();
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int at = k * lanes + lane;
-      v->w[k] = 0u;
-      if (at < groups * kPackGroup)
-        v->w[k] = codes[at] | static_cast<uint32_t>(scales[at / kPackGroup]) << 8;
-    }
+  for (int k = 0; k < 8; ++k) turned[k * 32 + l] = x[k];
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) p[k] = reinterpret_cast<const F2*>(turned)[l * 4 + k];
+}
+__device__ __forceinline__ void to_singles(const F2* p, float* turned, F2* singles) {
+  const int l = threadIdx.x % 32;
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) reinterpret_cast<F2*>(turned)[l * 4 + k] = p[k];
+  __syncwarp();
+  float x[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x[k] = turned[k * 32 + l];
+  to_pairs(x, singles);
+}
+// The group of the n-th eight single elements whose neighbours this thread then has.
+__device__ __forceinline__ int turned_group(int n, int lane, int lanes) {
+  return (n * 8 + lane % 32 / 4) * (lanes / 32) + lane / 32;
+}
+
+// The thread's eight neighbours in 8 bits, as loaded, and as values.
+struct EightCodes {
+  uint32_t w[3];  // codes, the scale's byte
+};
+__device__ __forceinline__ void load_codes(const uint8_t* codes, const uint8_t* scales, int lane, int groups, EightCodes* v) {
+  v->w[0] = v->w[1] = v->w[2] = 0u;
+  if (lane < groups * 4) {
+    const uint2 c = __ldcs(reinterpret_cast<const uint2*>(codes + static_cast<long long>(lane) * 8));
+    v->w[0] = c.x; v->w[1] = c.y;
+    v->w[2] = scales[lane / 4];
   }
 }
-template <int kVec>
-__device__ __forceinline__ void widen_codes(const EightCodes<kVec>& v, int form, F2* p) {
+__device__ __forceinline__ void widen_codes(const EightCodes& v, int form, F2* p) {
   float x[8];
-  if constexpr (kVec == 8) {
-    const F2 s = both(scale_value(v.w[2]));
-    decode4(v.w[0], form, x);
-    decode4(v.w[1], form, x + 4);
-    to_pairs(x, p);
+  const F2 s = both(scale_value(v.w[2]));
+  decode4(v.w[0], form, x);
+  decode4(v.w[1], form, x + 4);
+  to_pairs(x, p);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) p[k] = mul2(p[k], s);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = decode1(v.w[k] & 0xFFu, form) * scale_value(v.w[k] >> 8);
-    to_pairs(x, p);
-  }
+  for (int k = 0; k < 4; ++k) p[k] = mul2(p[k], s);
 }
 
 }  // namespace zfs

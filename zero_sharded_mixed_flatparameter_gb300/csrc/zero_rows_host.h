@@ -47,7 +47,7 @@ inline int power_of_two(int x) {
 // Lets a kernel have kMostShared bytes of dynamic shared memory, once a context
 // (the limit belongs to it); its static part and 1 KB of the system's come on top
 // of that, to 228 KB.
-template <auto kKernel, int kMostShared = 225 * 1024>
+template <auto kKernel, int kMostShared>
 cudaError_t allow_shared() {
   static std::atomic<unsigned long long> done{~0ull};
   unsigned long long id = 0;
