@@ -114,13 +114,16 @@ def pack64(x: torch.Tensor, form: torch.dtype):
 
 
 def embedding_backward64(dy, ids, rows, scale):
-    """The gradient and the room for fp32 arithmetic in it: a run of 32 tokens,
-    up to 64 parts a warp, 8 warps: below 128 additions in a row; the factor."""
+    """The gradient and the room for fp32 arithmetic in it: a row of n tokens is
+    summed up to 64 + n / 128 times in a row (up to 63 tokens of a run, or parts
+    of 8 tokens at least, a sixteenth of them a warp, then 16 warps), then scaled."""
     dy, ids = dy.double().reshape(-1, dy.shape[-1]), ids.reshape(-1).long()
     want = torch.zeros(rows, dy.shape[1], dtype=torch.float64)
     room = torch.zeros_like(want)
+    count = torch.zeros(rows, 1, dtype=torch.float64)
     for t, i in enumerate(ids.tolist()):
         if 0 <= i < rows:
             want[i] += dy[t]
             room[i] += dy[t].abs()
-    return scale * want, 128 * U32 * abs(scale) * room
+            count[i] += 1
+    return scale * want, (66 + count / 128) * U32 * abs(scale) * room

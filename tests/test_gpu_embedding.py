@@ -53,7 +53,7 @@ CASES = [  # tokens, rows, dim, how ids are spread
     (33, 40, 16, "one"), (64, 5, 40, "one"), (65, 1000, 24, "any"), (700, 50, 264, "text"), (1000, 1, 100, "one"),
     (1500, 700, 321, "text"), (2000, 3, 12, "text"), (3001, 3000, 64, "any"), (1025, 153, 8, "text"),
     (100, 5000, 2056, "any"), (4000, 5, 2048, "text"), (90, 20, 4100, "text"), (2500, 60000, 16, "text"),
-    (400, 260000, 8, "any")]
+    (400, 260000, 8, "any"), (20000, 3, 8, "one"), (9000, 2, 24, "text"), (17000, 200, 16, "text")]
 
 
 @pytest.mark.parametrize("id_dtype", [torch.int32, torch.int64], ids=["int32", "int64"])

@@ -362,6 +362,7 @@ def test_tensor_checks():
             ops.layer_norm_backward(g, s, weight, st)
     vector = torch.empty(100, device="cuda")
     for more in (dict(out=x[:5]), dict(weight_out=vector[:63]), dict(weight_out=vector[:64], bias_out=vector[30:94]),
-                 dict(weight_out=vector[:64].bfloat16(), bias_out=vector[:64]), dict(bias=False, bias_out=vector[:64])):
+                 dict(weight_out=vector[:64].bfloat16(), bias_out=vector[:64]), dict(bias=False, bias_out=vector[:64]),
+                 dict(weight_out=x[2]), dict(bias_out=dy[0])):
         with pytest.raises(ValueError):
             ops.layer_norm_backward(dy, x, weight, stats, **more)

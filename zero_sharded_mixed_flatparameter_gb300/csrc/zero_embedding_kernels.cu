@@ -689,12 +689,12 @@ zero_status zero_embedding_backward(const zero_embedding_config* cfg, int64_t to
   const bool fp32 = cfg->dtype == ZERO_GRAD_FP32, out32 = dtable_dtype == ZERO_GRAD_FP32;
   const bool vec = a.dim % 8 == 0 && rows_aligned(dout, dout_stride, tokens, cfg->dtype) &&
                    rows_aligned(dtable, dtable_stride, cfg->rows, dtable_dtype);
-  st = a.wide_ids ? launch_sort<long long>(a, shared, s) : launch_sort<int>(a, shared, s);
-  if (st != ZERO_OK) return st;
   const int width = !vec ? kSumColumns<false, 1> : fp32 ? kSumColumns<true, 8> : kSumColumns<false, 8>;
   a.columns = (a.dim + width - 1) / width;
   const long long zeros = accumulate ? 0 : (a.vocab + 31LL) / 32, jobs = a.runs + zeros;
   if (jobs * a.columns / kSumWarps > INT32_MAX - 2) return refuse(ZERO_EINVAL, "tokens, rows and dim are too large together");
+  st = a.wide_ids ? launch_sort<long long>(a, shared, s) : launch_sort<int>(a, shared, s);
+  if (st != ZERO_OK) return st;
   const dim3 grid(ctas_of(a.runs, a.columns) + ctas_of(zeros, a.columns));
   if (grid.x > 0) {
     if (fp32) out32 ? launch_sum<true, true>(a, vec, grid, s) : launch_sum<true, false>(a, vec, grid, s);

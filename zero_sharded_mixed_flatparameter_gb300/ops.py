@@ -514,7 +514,7 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivatio
         given = _check_vectors(cols, device, "weight_out and bias_out", weight_out, bias_out)
         if bias_out is not None and not bias:
             raise ValueError("bias_out without a bias")
-        _check_memory([v for v in (weight_out, bias_out) if v is not None], ())
+        _check_memory([v for v in (weight_out, bias_out) if v is not None], ((), (), (g, d, x.data if kept else m)))
     vectors = torch.bfloat16 if given == B.ZERO_GRAD_BF16 else torch.float32
     if weight is not None and weight_out is None:
         weight_out = torch.empty(cols, dtype=vectors, device=device)
