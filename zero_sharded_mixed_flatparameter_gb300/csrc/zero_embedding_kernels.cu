@@ -12,6 +12,12 @@
 // last row, and writes zeros to the rows without tokens; a row of more than twice
 // as many tokens is summed in parts, one a run.  The third joins the parts in order.
 // Each sum has one order: the same call gives the same bits.
+//
+// 32768 tokens of a text (ids by 1 / id), 40960 x 2048 bf16: the lookup 32 us, 5.3
+// TB/s of the rows in use and the 134 MB written; the gradient 68 us: sorting 10
+// (instructions: every CTA looks at every id), sums 48 (126 MB read, 168 written:
+// 6.1 TB/s), joining 7 (latency of its four dependent reads).  All tokens the same:
+// 30 + 47 + 18.  5003 tokens, 1009 x 321 fp32: 16 us, latencies one after another.
 
 #include <cmath>
 
@@ -24,7 +30,7 @@ namespace zfs {
 namespace {
 
 constexpr int kEmbThreads = 256;
-constexpr int kLookupCtas = 4;    // of an SM
+constexpr int kLookupCtas = 4;    // of an SM: four rows of 16 bytes a thread in flight
 constexpr int kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSortCtas = 128;    // a power of two
 constexpr int kSortRows = 1024;   // of a CTA at most: a counter for each and every warp, 128 KB

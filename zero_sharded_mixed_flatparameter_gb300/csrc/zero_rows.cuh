@@ -76,10 +76,10 @@ __device__ __forceinline__ void load_eight(const void* row, int lane, int lanes,
     for (int k = 0; k < (kFp32 ? 8 : 4); ++k) v->w[k] = 0u;
     if (lane * 8 < cols) {
       const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(row) + static_cast<long long>(lane) * (kFp32 ? 32 : 16));
-      const uint4 u = __ldcs(p);
+      const uint4 u = *p;
       v->w[0] = u.x; v->w[1] = u.y; v->w[2] = u.z; v->w[3] = u.w;
       if constexpr (kFp32) {
-        const uint4 t = __ldcs(p + 1);
+        const uint4 t = p[1];
         v->w[4] = t.x; v->w[5] = t.y; v->w[6] = t.z; v->w[7] = t.w;
       }
     }

@@ -10,6 +10,7 @@ is no CPU path.
 from __future__ import annotations
 
 import contextlib
+import ctypes
 import functools
 import operator
 from typing import Optional, Sequence, Tuple, Union
@@ -26,8 +27,18 @@ _CURRENT = contextlib.nullcontext()
 # identity, such as a tensor, could change its value under a kept entry)
 _ns_config = functools.lru_cache(maxsize=64)(B.make_ns_config)
 _qk_config = functools.lru_cache(maxsize=64)(B.zero_qk_config)
-_norm_config = functools.lru_cache(maxsize=64)(B.zero_norm_config)
-_embedding_config = functools.lru_cache(maxsize=64)(B.zero_embedding_config)
+
+
+@functools.lru_cache(maxsize=64)
+def _norm_config(*values):
+    return ctypes.byref(B.zero_norm_config(*values))
+
+
+@functools.lru_cache(maxsize=64)
+def _embedding_config(*values):
+    return ctypes.byref(B.zero_embedding_config(*values))
+
+
 _CONTIGUOUS = torch.contiguous_format
 
 
@@ -290,6 +301,18 @@ _GROUP = 32  # columns that share a scale
 _grad_enabled = torch.is_grad_enabled
 
 
+def _call(function, device: torch.device, *args) -> None:
+    """A C function on the device's current stream."""
+    index = device.index
+    if current_device() == index:
+        status = function(*args, current_stream(index))
+    else:
+        with torch.cuda.device(device):
+            status = function(*args, current_stream(index))
+    if status:
+        B._check(status)
+
+
 def _matrix(x: torch.Tensor, what: str, copy: bool = True) -> torch.Tensor:
     """`x`, which has columns, as a matrix of its last dimension's rows; a copy where its strides allow no such view
     (refused unless `copy`)."""
@@ -319,17 +342,14 @@ def _check_rows(x: torch.Tensor, what: str) -> int:
     return dtype
 
 
-def _check_vectors(cols: int, device: torch.device, what: str, *vectors: Optional[torch.Tensor]) -> Optional[int]:
-    """The type that the given vectors share."""
-    dtype = None
-    for v in vectors:
-        if v is None:
-            continue
-        kind = _DTYPES.get(v.dtype)
-        if kind is None or v.shape != (cols,) or v.device != device or not v.is_contiguous() or dtype not in (None, kind):
-            raise ValueError(f"{what} must be contiguous vectors of one entry per column and one type (bf16 or fp32)")
-        dtype = kind
-    return dtype
+def _check_vector(v: torch.Tensor, cols: int, device: torch.device, kind: Optional[int]) -> int:
+    """The type of a vector, which must be `kind` if that is given."""
+    its = _DTYPES.get(v.dtype)
+    if its is None or kind not in (None, its) or v.device != device or v.dim() != 1 or v.numel() != cols or \
+            not v.is_contiguous():
+        raise ValueError("weight, bias and their gradients must be contiguous vectors of one entry per column, those of "
+                         "one call of one type (bf16 or fp32)")
+    return its
 
 
 class PackedActivations:
@@ -355,7 +375,7 @@ class PackedActivations:
     def _set(self, data, form, shape, dtype, rows, cols):
         self.data, self.form, self.shape, self.dtype, self.rows, self.cols = data, form, shape, dtype, rows, cols
         at = data.data_ptr()
-        self._struct = B.zero_packed(at, at + rows * -(-cols // _GROUP) * _GROUP, _FORMATS[form])
+        self._struct = ctypes.byref(B.zero_packed(at, at + rows * -(-cols // _GROUP) * _GROUP, _FORMATS[form]))
         return self
 
     @property
@@ -396,8 +416,7 @@ def pack_activations(x: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, 
         if out.shape != x.shape or out.dtype != x.dtype or out.form != dtype or out.data.device != device:
             raise ValueError("out must have x's shape, type and device, and codes of dtype")
         _check_memory((out.data,), ((), (m,)))
-    with _on(device):
-        B.zero_pack_activations(rows, cols, m.data_ptr(), kind, m.stride(0), out._struct, current_stream(device.index))
+    _call(B.load().zero_pack_activations, device, rows, cols, m.data_ptr(), kind, m.stride(0), out._struct)
     return out
 
 
@@ -420,8 +439,7 @@ def unpack_activations(packed: PackedActivations, dtype: Optional[torch.dtype] =
         m = _matrix(out, "out", copy=False)
         _check_memory((m,), ((), (packed.data,)))
         at, stride = m.data_ptr(), m.stride(0)
-    with _on(device):
-        B.zero_unpack_activations(packed.rows, packed.cols, packed._struct, at, kind, stride, current_stream(device.index))
+    _call(B.load().zero_unpack_activations, device, packed.rows, packed.cols, packed._struct, at, kind, stride)
     return out
 
 
@@ -445,7 +463,9 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     kind, device = _check_rows(x, "x"), x.device
     m = _matrix(x, "x")
     rows, cols = m.shape
-    vector_kind = _check_vectors(cols, device, "weight and bias", weight, bias)
+    vector_kind = None if weight is None else _check_vector(weight, cols, device, None)
+    if bias is not None:
+        vector_kind = _check_vector(bias, cols, device, vector_kind)
     if out is None:
         out = torch.empty(x.shape, dtype=x.dtype, device=device)
         y, y_stride = out, cols
@@ -457,16 +477,16 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     stats = torch.empty((rows, 2), dtype=torch.float32, device=device)
     packed = None if pack is None else _new_packed(rows, cols, x.shape, x.dtype, pack, device)
     cfg = _norm_config(cols, 1 if center else 0, kind, vector_kind or 0, float(eps))
-    with _on(device):
-        B.zero_layer_norm(cfg, rows, m.data_ptr(), m.stride(0), 0 if weight is None else weight.data_ptr(),
-                          0 if bias is None else bias.data_ptr(), y.data_ptr(), y_stride, stats.data_ptr(),
-                          None if packed is None else packed._struct, current_stream(device.index))
+    _call(B.load().zero_layer_norm, device, cfg, rows, m.data_ptr(), m.stride(0),
+          0 if weight is None else weight.data_ptr(), 0 if bias is None else bias.data_ptr(), y.data_ptr(), y_stride,
+          stats.data_ptr(), None if packed is None else packed._struct)
     return (out, stats) if packed is None else (out, stats, packed)
 
 
 @functools.lru_cache(maxsize=256)
 def _norm_workspace(cols: int, rows: int, device: int) -> int:
-    return B.zero_layer_norm_backward_workspace_bytes(B.zero_norm_config(cols, 1, 0, 0, 0.0), rows)
+    with torch.cuda.device(device):
+        return B.zero_layer_norm_backward_workspace_bytes(B.zero_norm_config(cols, 1, 0, 0, 0.0), rows)
 
 
 def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivations], weight: Optional[torch.Tensor],
@@ -489,7 +509,7 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivatio
     kind, device = _check_rows(dy, "dy"), dy.device
     g = _matrix(dy, "dy")
     rows, cols = g.shape
-    vector_kind = _check_vectors(cols, device, "weight", weight)
+    vector_kind = None if weight is None else _check_vector(weight, cols, device, None)
     if kept:
         if x.shape != dy.shape or x.data.device != device:
             raise ValueError("x and dy must agree in shape and device")
@@ -511,7 +531,8 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivatio
             _check_memory((d,), ((), (x.data,)))
     given = None
     if weight_out is not None or bias_out is not None:
-        given = _check_vectors(cols, device, "weight_out and bias_out", weight_out, bias_out)
+        for v in (weight_out, bias_out):
+            given = given if v is None else _check_vector(v, cols, device, given)
         if bias_out is not None and not bias:
             raise ValueError("bias_out without a bias")
         _check_memory([v for v in (weight_out, bias_out) if v is not None], ((), (), (g, d, x.data if kept else m)))
@@ -522,13 +543,11 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivatio
         bias_out = torch.empty(cols, dtype=vectors, device=device)
     need = 0 if weight_out is None and bias_out is None else _norm_workspace(cols, rows, device.index)
     cfg = _norm_config(cols, 1 if center else 0, kind, vector_kind or 0, 0.0)
-    with _on(device):
-        workspace = torch.empty(need or 16, dtype=torch.uint8, device=device)
-        B.zero_layer_norm_backward(
-            cfg, rows, g.data_ptr(), g.stride(0), 0 if kept else m.data_ptr(), 0 if kept else m.stride(0),
-            x._struct if kept else None, 0 if weight is None else weight.data_ptr(), stats.data_ptr(), d.data_ptr(),
-            d_stride, _ptr(weight_out), _ptr(bias_out), _DTYPES[vectors], workspace.data_ptr(), need,
-            current_stream(device.index))
+    workspace = torch.empty(need or 16, dtype=torch.uint8, device=device)
+    _call(B.load().zero_layer_norm_backward, device, cfg, rows, g.data_ptr(), g.stride(0),
+          0 if kept else m.data_ptr(), 0 if kept else m.stride(0), x._struct if kept else None,
+          0 if weight is None else weight.data_ptr(), stats.data_ptr(), d.data_ptr(), d_stride, _ptr(weight_out),
+          _ptr(bias_out), _DTYPES[vectors], workspace.data_ptr(), need)
     return out, weight_out, bias_out
 
 
@@ -609,9 +628,7 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0,
         at, stride = y.data_ptr(), y.stride(0)
         _check_memory((y,), ((), (table, ids)))
     cfg = _embedding_config(rows, dim, kind, size, float(scale))
-    with _on(device):
-        B.zero_embedding(cfg, ids.numel(), ids.data_ptr(), table.data_ptr(), table.stride(0), at, stride,
-                         current_stream(device.index))
+    _call(B.load().zero_embedding, device, cfg, ids.numel(), ids.data_ptr(), table.data_ptr(), table.stride(0), at, stride)
     return out
 
 
@@ -648,11 +665,9 @@ def embedding_backward(dy: torch.Tensor, ids: torch.Tensor, rows: int, *, scale:
         _check_memory((out,), ((), (g, ids)))
     tokens = ids.numel()
     cfg, need = _embedding_config(rows, dim, kind, size, float(scale)), _embedding_workspace(rows, dim, tokens)
-    with _on(device):
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        B.zero_embedding_backward(cfg, tokens, ids.data_ptr(), g.data_ptr(), g.stride(0), out.data_ptr(), out_kind,
-                                  out.stride(0), 1 if accumulate else 0, workspace.data_ptr(), need,
-                                  current_stream(device.index))
+    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    _call(B.load().zero_embedding_backward, device, cfg, tokens, ids.data_ptr(), g.data_ptr(), g.stride(0),
+          out.data_ptr(), out_kind, out.stride(0), 1 if accumulate else 0, workspace.data_ptr(), need)
     return out
 
 
