@@ -19,8 +19,8 @@
 // instruction): both passes were bound by instructions without.
 //
 // 32768 x 2048 bf16, weight and bias: forward 46 us, 5.9 TB/s of the 268 MB read
-// and written; backward 71 us, 5.6 TB/s of 403 MB, 2 of them the join of the
-// column sums.  16384 x 2048 with the 8-bit form (e4m3), both directions: 75 us for
+// and written; backward 67 us, 6.0 TB/s of 403 MB, 3 of them the join of the
+// column sums.  16384 x 2048 with the 8-bit form (e4m3), both directions: 74 us for
 // 338 MB, bound by instructions (the codes' conversions, twice in the backward
 // pass).  5003 x 1301 fp32 backward: 24 us for 78 MB, single elements with a
 // row of a group in flight.
@@ -462,36 +462,49 @@ __global__ void __launch_bounds__(kBackwardWarps * 32, 1) norm_backward_kernel(c
   const long long step = static_cast<long long>(gridDim.x) * groups * kRows;
   const long long mine = blockIdx.x + static_cast<long long>(gridDim.x) * group;
   F2 dw[kN][4] = {}, db[kN][4] = {};
-  // the copies' places: [stage][row][n][dy's words, then x's][thread]
-  constexpr int kTurn = kAhead ? kTurnBytes<kFp32, kN, kPacked> : 0;
+  // the copies' places: [stage][dy's words, then x's or its codes][row][n][thread]
+  constexpr int kPitch = kBackwardWarps * 32;
+  constexpr int kTurn = kAhead ? kTurnBytes<kFp32, kN, kPacked> * kPitch : 0;
   char* const ring = reinterpret_cast<char*>(tables + kN * 8 * a.lanes);
-  auto place = [&](int stage, int i, int n, int word) {  // of dy's words, x's words and x's codes
-    const int at = kRows * kN * 16 * word + (i * kN + n) * (word < 2 * kWords && !(kPacked && word >= kWords) ? 16 : 8);
-    return ring + (static_cast<size_t>(stage) * kTurn + at) * blockDim.x +
-           threadIdx.x * (kPacked && word >= kWords ? 8 : 16);
+  auto place = [&](int stage, int i, int n, int word) {
+    if (kPacked && word == kWords)
+      return ring + stage * kTurn + (kRows * kN * kWords * 16 + (i * kN + n) * 8) * kPitch + threadIdx.x * 8;
+    return ring + stage * kTurn + ((kRows * word + i) * kN + n) * 16 * kPitch + threadIdx.x * 16;
   };
-  auto copy = [&](long long r0, int stage) {
+  // Where the thread's first words of the next turn to copy lie: moved on where x
+  // is whole; beside codes and scales there are no registers for that.
+  const long long apart = static_cast<long long>(gridDim.x) * groups;
+  const long long x_pitch = a.x_stride * kSize, dy_pitch = a.dy_stride * kSize;
+  const char* next_x = static_cast<const char*>(a.x) + mine * x_pitch + own.lane * (16 * kWords);
+  const char* next_dy = static_cast<const char*>(a.dy) + mine * dy_pitch + own.lane * (16 * kWords);
+  long long next_row = mine;
+  auto copy = [&](int stage) {
     if constexpr (kAhead) {
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
-        const long long r = r0 + static_cast<long long>(gridDim.x) * groups * i;
-        if (r < a.rows) {
-          const char* row = static_cast<const char*>(a.x) + r * a.x_stride * kSize;
-          const char* drow = static_cast<const char*>(a.dy) + r * a.dy_stride * kSize;
+        const long long r = next_row + apart * i;
+        if (r >= a.rows) break;
+        const char* from = kPacked ? static_cast<const char*>(a.dy) + r * dy_pitch + own.lane * (16 * kWords)
+                                   : next_dy + apart * i * dy_pitch;
 #pragma unroll
-          for (int n = 0; n < kN; ++n) {
-            const int v = own.lane_of(n);
-            if (v * 8 >= a.cols) continue;
+        for (int n = 0; n < kN; ++n) {
+          if (own.lane_of(n) * 8 >= a.cols) break;
 #pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-              copy_async<16>(place(stage, i, n, w), drow + (v * kWords + w) * 16LL);
-              if constexpr (!kPacked) copy_async<16>(place(stage, i, n, kWords + w), row + (v * kWords + w) * 16LL);
-            }
-            if constexpr (kPacked) copy_async<8>(place(stage, i, n, kWords), a.codes + r * a.groups * kPackGroup + v * 8LL);
+          for (int w = 0; w < kWords; ++w) {
+            copy_async<16>(place(stage, i, n, w), from + n * own.lanes * (16 * kWords) + w * 16);
+            if constexpr (!kPacked)
+              copy_async<16>(place(stage, i, n, kWords + w), next_x + apart * i * x_pitch + n * own.lanes * (16 * kWords) + w * 16);
           }
+          if constexpr (kPacked)
+            copy_async<8>(place(stage, i, n, kWords), a.codes + r * a.groups * kPackGroup + own.lane_of(n) * 8LL);
         }
       }
       copy_commit();
+      next_row += step;
+      if constexpr (!kPacked) {
+        next_x += step * x_pitch;
+        next_dy += step * dy_pitch;
+      }
     }
   };
   // what a turn needs beside: the rows' statistics and scales, a turn ahead
@@ -510,7 +523,7 @@ __global__ void __launch_bounds__(kBackwardWarps * 32, 1) norm_backward_kernel(c
     }
   };
 #pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) copy(mine + step * s, s);
+  for (int s = 0; s < kStages - 1; ++s) copy(s);
   look_ahead(mine);
   for (int four = threadIdx.x; four < kN * 2 * a.lanes; four += blockDim.x)
     own.store_four(tables, four, own.load_four(a.weight, a.weight_fp32, four, a.cols, 1.0f));
@@ -527,7 +540,7 @@ __global__ void __launch_bounds__(kBackwardWarps * 32, 1) norm_backward_kernel(c
     }
     look_ahead(r0 + step);
     if constexpr (kAhead) {
-      copy(r0 + step * (kStages - 1), (stage + kStages - 1) % kStages);  // where the turn before this one was
+      copy((stage + kStages - 1) % kStages);  // where the turn before this one was
       copy_wait<kStages - 1>();
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
@@ -574,21 +587,21 @@ __global__ void __launch_bounds__(kBackwardWarps * 32, 1) norm_backward_kernel(c
         }
       }
     }
-    // xn, and dy (columns past the last: dy is zero, and what they add to sums, too)
-    auto values = [&](int i, int n, F2* xn, F2* g) {
+    // x less the mean, and dy (columns past the last: dy is zero, and what they add to sums, too)
+    auto values = [&](int i, int n, F2* d, F2* g) {
       if constexpr (kPacked) {
-        widen_codes(codes[i][n], kForm, xn);
+        widen_codes(codes[i][n], kForm, d);
         if constexpr (kVec == 1) {
-          F2 p[4] = {xn[0], xn[1], xn[2], xn[3]};
-          to_singles(p, turned[threadIdx.x / 32], xn);
+          F2 p[4] = {d[0], d[1], d[2], d[3]};
+          to_singles(p, turned[threadIdx.x / 32], d);
         }
       } else {
-        widen_pairs<kFp32, kVec>(raw[i][n], xn);
+        widen_pairs<kFp32, kVec>(raw[i][n], d);
       }
       widen_pairs<kFp32, kVec>(grad[i][n], g);
-      const F2 less = both(-stats[i].x), rstd = both(stats[i].y);
+      const F2 less = both(-stats[i].x);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) xn[k] = mul2(add2(xn[k], less), rstd);
+      for (int k = 0; k < 4; ++k) d[k] = add2(d[k], less);
     };
     F2 one[kRows] = {}, two[kRows] = {};
 #pragma unroll
@@ -599,8 +612,10 @@ __global__ void __launch_bounds__(kBackwardWarps * 32, 1) norm_backward_kernel(c
       for (int i = 0; i < kRows; ++i) {
         F2 xn[4], g[4];
         values(i, n, xn, g);
+        const F2 rstd = both(stats[i].y);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
+          xn[k] = mul2(xn[k], rstd);
           dw[n][k] = fma2(g[k], xn[k], dw[n][k]);
           db[n][k] = add2(db[n][k], g[k]);
           g[k] = mul2(g[k], w[k]);
@@ -624,15 +639,15 @@ __global__ void __launch_bounds__(kBackwardWarps * 32, 1) norm_backward_kernel(c
       for (int i = 0; i < kRows; ++i) {
         const long long r = r0 + static_cast<long long>(gridDim.x) * groups * i;
         if (r >= a.rows) continue;
-        const F2 m1 = both(a.center ? -total[2 * i] * a.inv_cols : 0.0f), m2 = both(-total[2 * i + 1] * a.inv_cols);
-        const F2 rstd = both(stats[i].y);
-        F2 xn[4], g[4];
+        const F2 m1 = both(a.center ? -total[2 * i] * a.inv_cols : 0.0f), rstd = both(stats[i].y);
+        const F2 m2 = both(-total[2 * i + 1] * a.inv_cols * stats[i].y);  // of x less the mean
+        F2 d[4], g[4];
         if constexpr (kPacked) forget_widened(codes[i][n]);
         else forget_widened(raw[i][n]);
         forget_widened(grad[i][n]);
-        values(i, n, xn, g);
+        values(i, n, d, g);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) g[k] = mul2(rstd, fma2(xn[k], m2, fma2(g[k], w[k], m1)));
+        for (int k = 0; k < 4; ++k) g[k] = mul2(rstd, fma2(d[k], m2, fma2(g[k], w[k], m1)));
         store_pairs<kFp32, kVec>(static_cast<char*>(a.out) + (r * a.out_stride + own.at(n)) * kSize, own.lane_of(n),
                                  own.lanes, a.cols - own.at(n), g);
       }
@@ -867,7 +882,7 @@ void launch_forward(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st
 template <bool kFp32, int kVec, int kN, int kForm>
 void launch_backward_n(const NormArgs& a, const Shape& s, int ctas, cudaStream_t st) {
   const int bytes = kN * 8 * s.lanes * static_cast<int>(sizeof(float)) +
-                    (kVec == 8 ? kStages * kTurnBytes<kFp32, kN, kForm != 0> * s.threads : 0);
+                    (kVec == 8 ? kStages * kTurnBytes<kFp32, kN, kForm != 0> * kBackwardWarps * 32 : 0);
   launch_with<norm_backward_kernel<kFp32, kVec, kN, kForm>, (kVec == 8 ? 225 : 32) * 1024>(a, s, ctas, bytes, st);
 }
 template <bool kFp32, int kVec, int kForm>
