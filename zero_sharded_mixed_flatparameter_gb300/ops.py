@@ -5,6 +5,11 @@ gradients, and activations kept in 8 bits (:func:`pack_activations`).
 Each is a thin call of the C function of the same name: checks, the output and
 workspace tensors, the current stream.  Tensors stay on one CUDA device; there
 is no CPU path.
+
+The functions without autograd can be captured into CUDA graphs as they are.  Of
+the ``*_autograd`` ones, capture the forward and the backward pass together, while
+no graph of an earlier forward pass over the same leaves is alive: torch would
+make the capture wait for that one's stream.
 """
 
 from __future__ import annotations
