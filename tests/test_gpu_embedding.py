@@ -53,7 +53,8 @@ CASES = [  # tokens, rows, dim, how ids are spread
     (33, 40, 16, "one"), (64, 5, 40, "one"), (65, 1000, 24, "any"), (700, 50, 264, "text"), (1000, 1, 100, "one"),
     (1500, 700, 321, "text"), (2000, 3, 12, "text"), (3001, 3000, 64, "any"), (1025, 153, 8, "text"),
     (100, 5000, 2056, "any"), (4000, 5, 2048, "text"), (90, 20, 4100, "text"), (2500, 60000, 16, "text"),
-    (400, 260000, 8, "any"), (20000, 3, 8, "one"), (9000, 2, 24, "text"), (17000, 200, 16, "text")]
+    (400, 260000, 8, "any"), (20000, 3, 8, "one"), (9000, 2, 24, "text"), (17000, 200, 16, "text"),
+    (1300, 90, 511, "text"), (1300, 90, 513, "text"), (700, 300, 1001, "any"), (600, 4, 777, "one")]
 
 
 @pytest.mark.parametrize("id_dtype", [torch.int32, torch.int64], ids=["int32", "int64"])
@@ -192,6 +193,16 @@ def test_offsets_past_32_bits():
     ops.embedding_backward(dy, ids, rows, out=table)
     assert (table[rows - 1] == 2.0).all() and (table[rows - 2] == 1.0).all() and (table[0] == 1.0).all()
     assert float(table.sum(dtype=torch.float64)) == 4.0 * dim
+    # the same of the looked up rows and their gradient
+    tokens, dim = 39, 64
+    stride = (1 << 31) // (tokens - 1) // 64 * 64 + 64
+    big = table.view(-1)[:(tokens - 1) * stride + dim].as_strided((tokens, dim), (stride, 1))
+    ids, dy = make_ids(tokens, 9, "text").cuda(), normal(tokens, dim, dtype=BF16).cuda()
+    big.copy_(dy)
+    assert torch.equal(ops.embedding_backward(big, ids, 9), ops.embedding_backward(dy, ids, 9))
+    small = normal(9, dim, dtype=BF16).cuda()
+    ops.embedding(ids, small, out=big)
+    assert torch.equal(big, ops.embedding(ids, small))
 
 
 def test_autograd():

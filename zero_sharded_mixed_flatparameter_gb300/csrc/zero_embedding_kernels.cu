@@ -255,20 +255,22 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
   else walk_ids<Id>(a, own, place);
 }
 
-// A warp sums kSumParts times kSumCount elements a lane: 32 bytes of vectors, or
-// two single elements (so that narrow tables have warps enough).
-template <bool kFp32, int kVec>
-constexpr int kSumParts = kVec == 8 && !kFp32 ? 2 : 1;
-template <int kVec>
-constexpr int kSumCount = kVec == 8 ? 8 : 2;
-template <bool kFp32, int kVec>
-constexpr int kSumColumns = 32 * kSumParts<kFp32, kVec> * kSumCount<kVec>;
+// What a lane of a summing warp holds: 32 bytes of vectors, eight single elements,
+// or two (so that narrow tables have warps enough: below kNarrow columns).
+enum : int { kVectors = 8, kSingles = 1, kFewSingles = 0 };
+constexpr int kNarrow = 512;
+template <bool kFp32, int kMode>
+constexpr int kSumParts = kMode == kVectors && !kFp32 ? 2 : 1;
+template <int kMode>
+constexpr int kSumCount = kMode == kFewSingles ? 2 : 8;
+template <bool kFp32, int kMode>
+constexpr int kSumColumns = 32 * kSumParts<kFp32, kMode> * kSumCount<kMode>;
 
 // The warp's columns, from `at` on, of a row of the table's gradient.
-template <bool kFp32, int kVec>
+template <bool kFp32, int kMode>
 __device__ __forceinline__ void put_row(const EmbArgs& a, int row, int at, int lane, const float* sum) {
   constexpr long long kSize = kFp32 ? 4 : 2;
-  constexpr int kCount = kSumCount<kVec>;
+  constexpr int kVec = kMode == kVectors ? 8 : 1, kCount = kSumCount<kMode>;
   char* to = static_cast<char*>(a.out) + (row * a.out_stride + at) * kSize;
   float x[kCount];
 #pragma unroll
@@ -296,9 +298,9 @@ __host__ __device__ inline int ctas_of(long long jobs, int columns) {
 }
 
 // A warp takes kSumColumns columns of a run, or of 32 rows that may have no token.
-template <bool kFp32, bool kOutFp32, int kVec>
+template <bool kFp32, bool kOutFp32, int kMode>
 __global__ void __launch_bounds__(kSumThreads, 6) embedding_sum_kernel(const __grid_constant__ EmbArgs a) {
-  constexpr int kParts = kSumParts<kFp32, kVec>, kCount = kSumCount<kVec>, kPart = 32 * kCount;
+  constexpr int kVec = kMode == kVectors ? 8 : 1, kParts = kSumParts<kFp32, kMode>, kCount = kSumCount<kMode>, kPart = 32 * kCount;
   constexpr long long kSize = kFp32 ? 4 : 2, kOutSize = kOutFp32 ? 4 : 2;
   const int lane = threadIdx.x % 32;
   // CTAs of runs, which wait for what they read, and of zeros, which only write, in turn
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kSumThreads, 6) embedding_sum_kernel(const __g
   const long long unit = static_cast<long long>(b < in_turn ? b / 2 : b - in_turn / 2) * kSumWarps + threadIdx.x / 32;
   const long long job = unit / a.columns;
   if (job >= (sums ? a.runs : zeros)) return;
-  const int at = static_cast<int>(unit - job * a.columns) * kSumColumns<kFp32, kVec>, cols = a.dim - at;
+  const int at = static_cast<int>(unit - job * a.columns) * kSumColumns<kFp32, kMode>, cols = a.dim - at;
   asm volatile("griddepcontrol.launch_dependents;\ngriddepcontrol.wait;" ::: "memory");
   if (!sums) {
     const float zero[kCount] = {};
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(kSumThreads, 6) embedding_sum_kernel(const __g
       }
       if (part) store_eight<true, kVec, kCount>(a.parts + (run * 2LL + which) * a.pitch + at + n * kPart, lane, 32,
                                                 cols - n * kPart, x);
-      else put_row<kOutFp32, kVec>(a, row, at + n * kPart, lane, x);
+      else put_row<kOutFp32, kMode>(a, row, at + n * kPart, lane, x);
     }
   };
   const char* const rows = static_cast<const char*>(a.rows) + at * kSize;
@@ -518,7 +520,8 @@ struct Workspace {
 // Long runs make few parts, short ones many warps: the longest that still gives
 // every SM 32 warps (of single elements, which the alignment may come to).
 int chunk_of(int64_t dim, int64_t tokens) {
-  const int64_t warps = (dim + kSumColumns<false, 1> - 1) / kSumColumns<false, 1>;
+  const int64_t width = dim < kNarrow ? kSumColumns<false, kFewSingles> : kSumColumns<false, kSingles>;
+  const int64_t warps = (dim + width - 1) / width;
   int chunk = kMostChunk;
   while (chunk > kLeastChunk && tokens / chunk * warps < 32 * 152) chunk /= 2;
   return chunk;
@@ -578,11 +581,16 @@ zero_status launch_sort(const EmbArgs& a, int shared, cudaStream_t s) {
   return launch_status("embedding sort launch");
 }
 template <bool kFp32, bool kOutFp32>
-void launch_sum(const EmbArgs& a, bool vec, dim3 grid, cudaStream_t s) {
-  if (vec) {
-    if (allow_shared<embedding_sum_kernel<kFp32, kOutFp32, 8>, kSumShared>() != cudaSuccess) return;  // the launch's error
-    launch_after(embedding_sum_kernel<kFp32, kOutFp32, 8>, grid, dim3(kSumThreads), kSumShared, s, a);
-  } else launch_after(embedding_sum_kernel<kFp32, kOutFp32, 1>, grid, dim3(kSumThreads), 0, s, a);
+void launch_sum(const EmbArgs& a, int mode, dim3 grid, cudaStream_t s) {
+  const dim3 block(kSumThreads);
+  if (mode == kVectors) {
+    if (allow_shared<embedding_sum_kernel<kFp32, kOutFp32, kVectors>, kSumShared>() != cudaSuccess) return;  // the launch's error
+    launch_after(embedding_sum_kernel<kFp32, kOutFp32, kVectors>, grid, block, kSumShared, s, a);
+  } else if (mode == kSingles) {
+    launch_after(embedding_sum_kernel<kFp32, kOutFp32, kSingles>, grid, block, 0, s, a);
+  } else {
+    launch_after(embedding_sum_kernel<kFp32, kOutFp32, kFewSingles>, grid, block, 0, s, a);
+  }
 }
 
 }  // namespace
@@ -695,7 +703,8 @@ zero_status zero_embedding_backward(const zero_embedding_config* cfg, int64_t to
   const bool fp32 = cfg->dtype == ZERO_GRAD_FP32, out32 = dtable_dtype == ZERO_GRAD_FP32;
   const bool vec = a.dim % 8 == 0 && rows_aligned(dout, dout_stride, tokens, cfg->dtype) &&
                    rows_aligned(dtable, dtable_stride, cfg->rows, dtable_dtype);
-  const int width = !vec ? kSumColumns<false, 1> : fp32 ? kSumColumns<true, 8> : kSumColumns<false, 8>;
+  const int mode = vec ? kVectors : a.dim < kNarrow ? kFewSingles : kSingles;
+  const int width = mode == kFewSingles ? kSumColumns<false, kFewSingles> : mode == kSingles || fp32 ? kSumColumns<true, kVectors> : kSumColumns<false, kVectors>;
   a.columns = (a.dim + width - 1) / width;
   const long long zeros = accumulate ? 0 : (a.vocab + 31LL) / 32, jobs = a.runs + zeros;
   if (jobs * a.columns / kSumWarps > INT32_MAX - 2) return refuse(ZERO_EINVAL, "tokens, rows and dim are too large together");
@@ -703,8 +712,8 @@ zero_status zero_embedding_backward(const zero_embedding_config* cfg, int64_t to
   if (st != ZERO_OK) return st;
   const dim3 grid(ctas_of(a.runs, a.columns) + ctas_of(zeros, a.columns));
   if (grid.x > 0) {
-    if (fp32) out32 ? launch_sum<true, true>(a, vec, grid, s) : launch_sum<true, false>(a, vec, grid, s);
-    else out32 ? launch_sum<false, true>(a, vec, grid, s) : launch_sum<false, false>(a, vec, grid, s);
+    if (fp32) out32 ? launch_sum<true, true>(a, mode, grid, s) : launch_sum<true, false>(a, mode, grid, s);
+    else out32 ? launch_sum<false, true>(a, mode, grid, s) : launch_sum<false, false>(a, mode, grid, s);
   }
   if ((st = launch_status("embedding sum launch")) != ZERO_OK) return st;
   if (w.heavy_rows > 0) {
