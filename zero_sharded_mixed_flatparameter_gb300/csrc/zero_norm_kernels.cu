@@ -818,7 +818,7 @@ struct Shape {
 };
 // most: the largest kN that the pass has registers for (single elements: 2).
 // Where every row can have an SM to itself, it is spread over as many warps as
-// there are (1 row of 2048: 2.0 us of device time, 3.7 us as one warp of many).
+// there are (1 row of 2048: 2.6 us of device time, 3.7 us as one warp of many).
 Shape shape_of(int cols, long long rows, bool vec, int most, int cta_warps) {
   if (cols > kNormWidest) return {0, kWideThreads, 0, false};
   const int eights = (cols + 7) / 8;
