@@ -337,6 +337,11 @@ def _matrix(x: torch.Tensor, what: str, copy: bool = True) -> torch.Tensor:
     return x
 
 
+def _new_like(x: torch.Tensor) -> torch.Tensor:
+    """A contiguous tensor of x's shape, type and device."""
+    return torch.empty_like(x) if x.is_contiguous() else torch.empty_like(x, memory_format=_CONTIGUOUS)
+
+
 def _check_rows(x: torch.Tensor, what: str) -> int:
     """The type of a tensor of rows."""
     dtype = _DTYPES.get(x.dtype)
@@ -463,7 +468,8 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     Inputs that require gradients are refused: :func:`layer_norm_autograd`
     records them.
     """
-    if _grad_enabled():
+    if _grad_enabled() and (x.requires_grad or weight is not None and weight.requires_grad
+                            or bias is not None and bias.requires_grad):
         _no_graph("layer_norm (layer_norm_autograd does)", x, weight, bias)
     kind, device = _check_rows(x, "x"), x.device
     m = _matrix(x, "x")
@@ -472,7 +478,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     if bias is not None:
         vector_kind = _check_vector(bias, cols, device, vector_kind)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=device)
+        out = _new_like(x)
         y, y_stride = out, cols
     else:
         _check_like((out,), (x,))
@@ -509,7 +515,8 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivatio
     gradients are refused.
     """
     kept = isinstance(x, PackedActivations)
-    if _grad_enabled():
+    if _grad_enabled() and (dy.requires_grad or not kept and x.requires_grad
+                            or weight is not None and weight.requires_grad):
         _no_graph("layer_norm_backward", dy, None if kept else x, weight)
     kind, device = _check_rows(dy, "dy"), dy.device
     g = _matrix(dy, "dy")
@@ -525,7 +532,7 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivatio
     if stats.dtype != torch.float32 or stats.shape != (rows, 2) or stats.device != device or not stats.is_contiguous():
         raise ValueError("stats must be the contiguous fp32 tensor (rows, 2) of the forward pass")
     if out is None:
-        out = torch.empty(dy.shape, dtype=dy.dtype, device=device)
+        out = _new_like(dy)
         d, d_stride = out, cols
     else:
         _check_like((out,), (dy,))
@@ -616,7 +623,7 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0,
     fills ``out``) ids.shape + (dim,).  A ``table`` that requires a gradient is
     refused: :func:`embedding_autograd` records it.
     """
-    if _grad_enabled():
+    if table.requires_grad:
         _no_graph("embedding (embedding_autograd does)", table)
     kind, device = _check_rows(table, "table"), table.device
     if table.dim() != 2 or (table.stride(1) != 1 and table.size(1) > 1):
@@ -652,7 +659,7 @@ def embedding_backward(dy: torch.Tensor, ids: torch.Tensor, rows: int, *, scale:
     zeroed; with ``accumulate`` the sums are added to ``out`` instead, and those
     rows stay as they are.
     """
-    if _grad_enabled():
+    if dy.requires_grad or out is not None and out.requires_grad:
         _no_graph("embedding_backward", dy, out)
     kind, device, dim, rows = _check_rows(dy, "dy"), dy.device, dy.size(-1), operator.index(rows)
     ids, size = _check_ids(ids, device)
