@@ -127,3 +127,45 @@ def embedding_backward64(dy, ids, rows, scale):
             room[i] += dy[t].abs()
             count[i] += 1
     return scale * want, (66 + count / 128) * U32 * abs(scale) * room
+
+
+def power_of_two(e: torch.Tensor) -> torch.Tensor:
+    """2^e in 64 bits, by the bits (-1022 <= e <= 1023)."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
+def pack64_many(x: torch.Tensor, form: torch.dtype):
+    """`pack64` for large matrices, on the device of `x`: all groups at once."""
+    limit = 448.0 if form == E4M3 else 127.0
+    rows, cols = x.shape
+    groups = -(-cols // GROUP)
+    v = torch.zeros(rows, groups * GROUP, dtype=torch.float64, device=x.device)
+    v[:, :cols] = x.double()
+    v = v.view(rows, groups, GROUP)
+    finite = v.isfinite().all(2)
+    v = torch.where(finite[..., None], v, 0.0)
+    top = v.abs().amax(2)
+    top = top.clamp(min=2.0 ** -160)  # (any below 2^-126)
+    e = torch.frexp(top / limit).exponent.long().clamp(min=-126)  # right, or one off; an exact comparison decides
+    e = torch.where(top > limit * power_of_two(e), e + 1, e)
+    e = torch.where((e > -126) & (top <= limit * power_of_two(e - 1)), e - 1, e)
+    v = v / power_of_two(e)[..., None]
+    if form == E4M3:
+        step = power_of_two(torch.frexp(v.abs().clamp(min=2.0 ** -6)).exponent.long() - 1 - 3)
+        codes = torch.round(v / step) * step
+    else:
+        codes = torch.round(v)
+    values = torch.where(finite[..., None], codes * power_of_two(e)[..., None], math.nan)
+    return (codes.view(rows, -1), torch.where(finite, e, 128), values.view(rows, -1)[:, :cols])
+
+
+def embedding_backward64_many(dy, ids, rows, scale):
+    """`embedding_backward64` for many tokens, on the device of `dy`, with the same room."""
+    dy, ids = dy.double().reshape(-1, dy.shape[-1]), ids.reshape(-1).long()
+    live = (ids >= 0) & (ids < rows)
+    ids, dy = ids[live], dy[live]
+    want = torch.zeros(rows, dy.shape[1], dtype=torch.float64, device=dy.device)
+    room, count = torch.zeros_like(want), torch.bincount(ids, minlength=rows)[:, None]
+    want.index_add_(0, ids, dy)
+    room.index_add_(0, ids, dy.abs())
+    return scale * want, (66 + count / 128) * U32 * abs(scale) * room
