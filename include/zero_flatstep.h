@@ -808,7 +808,7 @@ typedef struct zero_norm_config {
  *   y = (x - mean) * rstd * weight + bias
  * in fp32, rounded once; a row whose squares exceed fp32's range has rstd 0.
  *  weight, bias   cols elements of weight_dtype, or NULL: none
- *  y              may be x itself (same stride), else must not overlap it
+ *  y              may be x itself (same stride), else must not overlap an input
  *  stats          fp32 [rows][2]: mean and rstd, which the backward pass reads;
  *                 8-byte aligned, or NULL: not wanted
  *  packed         takes the 8-bit form of x in the same pass, or NULL
@@ -830,7 +830,8 @@ zero_status zero_layer_norm_backward_workspace_bytes(const zero_norm_config* cfg
  *  x, packed         the forward input, or (x NULL) its 8-bit form; the entries
  *                    it stands for take the input's place, the statistics stay
  *  stats             as zero_layer_norm wrote them
- *  dx                may be dy or x itself (same stride), else must not overlap them
+ *  dx                may be dy or x itself (same stride), else must not overlap
+ *                    an input
  *  dweight, dbias    cols elements of dgrad_dtype (zero_grad_dtype), overwritten
  *                    (zeros for 0 rows); NULL: not wanted
  *  workspace         device scratch, 16-byte aligned (not read where neither of

@@ -464,7 +464,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
     statistics (fp32, rows x 2: mean and 1 / deviation), which the backward pass
     reads; with ``pack`` (torch.float8_e4m3fn or torch.int8) also ``x`` in 8 bits
     (:class:`PackedActivations`), written in the same pass, which it can read in
-    place of ``x``.  ``out`` may be ``x``, and must not overlap it otherwise.
+    place of ``x``.  ``out`` may be ``x``, and must not overlap an input otherwise.
     Inputs that require gradients are refused: :func:`layer_norm_autograd`
     records them.
     """
@@ -484,7 +484,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
         _check_like((out,), (x,))
         y = _matrix(out, "out", copy=False)
         y_stride = y.stride(0)
-        _check_memory((y,), ((m,),))
+        _check_memory((y,), ((m,), [v for v in (weight, bias) if v is not None]))
     stats = torch.empty((rows, 2), dtype=torch.float32, device=device)
     packed = None if pack is None else _new_packed(rows, cols, x.shape, x.dtype, pack, device)
     cfg = _norm_config(cols, 1 if center else 0, kind, vector_kind or 0, float(eps))
@@ -509,7 +509,7 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivatio
     ``x``: the forward input, or its 8-bit form, whose values then take the
     input's place.  ``stats``, ``center``: as in the forward pass; dweight is None
     without a weight, dbias with ``bias=False``.  ``out`` may be ``dy`` or ``x``,
-    and must not overlap them otherwise.  ``weight_out``, ``bias_out``: vectors of
+    and must not overlap an input otherwise.  ``weight_out``, ``bias_out``: vectors of
     one type, bf16 or fp32, to write those gradients to, such as slices of a
     replica's flat gradient; new fp32 vectors otherwise.  Inputs that require
     gradients are refused.
@@ -538,9 +538,8 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivatio
         _check_like((out,), (dy,))
         d = _matrix(out, "out", copy=False)
         d_stride = d.stride(0)
-        _check_memory((d,), ((g,) if m is None else (g, m),))
-        if kept:
-            _check_memory((d,), ((), (x.data,)))
+        others = [stats] if weight is None else [stats, weight]
+        _check_memory((d,), ((g,), [*others, x.data]) if kept else ((g, m), others))
     given = None
     if weight_out is not None or bias_out is not None:
         for v in (weight_out, bias_out):
