@@ -737,7 +737,7 @@ zero_status zero_qk_backward_workspace_bytes(const zero_qk_config* cfg, int64_t 
  * gradients are not read into any sum).  The gain sums are fp32 in a fixed
  * order: the same call gives the same bits.
  *  dq, dk            may be dq_out, dk_out or q, k themselves (same strides), else
- *                    must not overlap them
+ *                    must not overlap an input
  *  dq_gain, dk_gain  head_dim elements of dgain_dtype (zero_grad_dtype),
  *                    overwritten (zeros for 0 tokens or heads); NULL: not
  *                    wanted

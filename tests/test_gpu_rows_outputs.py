@@ -54,3 +54,31 @@ def test_outputs_over_weights_and_statistics():
         grads = ops.layer_norm_backward(dy, source, w, stats)
         for g, e in zip(ops.layer_norm_backward(dy, source, beside, stats, out=y), grads):
             assert torch.equal(g, e)
+
+
+def test_norm_and_rotation_over_gains_table_and_positions():
+    tokens, dim = 5, 32
+    q, k, dq, dk = normal(tokens, 3, dim), normal(tokens, 2, dim), normal(tokens, 3, dim, seed=1), normal(tokens, 2, dim, seed=1)
+    gains, table = (normal(dim), normal(dim, seed=1)), normal(8, 16).cos()
+    positions = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    buffer = normal(q.numel() + 200, seed=2)
+    out = (buffer[:q.numel()].view_as(q), torch.empty_like(k))
+    before = buffer.clone()
+    end = buffer[q.numel() - 1:]  # the last element of the one output and what is behind it
+    for bad in ((end[:dim], gains[1], table, positions), (gains[0], end[:dim], table, positions),
+                (None, None, end[:128].view(8, 16), positions), (*gains, table, end[:tokens].view(torch.int32))):
+        with pytest.raises(ValueError):
+            ops.qk_norm_rope(q, k, *bad, out=out)
+        with pytest.raises(ValueError):
+            ops.qk_norm_rope_backward(dq, dk, q, k, *bad, out=out)
+    with pytest.raises(ValueError):  # one output over another
+        ops.qk_norm_rope_backward(dq, dk, q, k, *gains, table, positions, out=out, gain_out=(end[:dim], torch.empty_like(gains[0])))
+    assert torch.equal(buffer, before), "a refused call writes nothing"
+    want = ops.qk_norm_rope_backward(dq, dk, q, k, *gains, table, positions)
+    beside = (end[1:1 + dim], end[1 + dim:1 + 2 * dim])
+    for g, e in zip(ops.qk_norm_rope_backward(dq, dk, q, k, *gains, table, positions, out=out, gain_out=beside), want):
+        assert torch.equal(g, e)
+    beside[0].copy_(gains[0])
+    for g, e in zip(ops.qk_norm_rope(q, k, beside[0], gains[1], table, positions, out=out),
+                    ops.qk_norm_rope(q, k, *gains, table, positions)):
+        assert torch.equal(g, e)

@@ -94,6 +94,10 @@ def _same(a: torch.Tensor, b: torch.Tensor) -> bool:
         n == 1 or s == t for n, s, t in zip(a.shape, a.stride(), b.stride()))
 
 
+def _given(*tensors: Optional[torch.Tensor]) -> list:
+    return [t for t in tensors if t is not None]
+
+
 def _check_memory(outs, ins) -> None:
     """Refuses outputs that overlap themselves, one another or an input; output
     i may be one of ins[i] itself (each element is read before it is written)."""
@@ -207,7 +211,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_gain: Optional[torch.Tensor
     be strided views of one projection's output.  ``table`` holds per position
     the rotary_dim/2 cosines, then the sines; rotary_dim is its width.  A
     position outside the table marks padding: zeros.  ``out`` may be (q, k),
-    and must not overlap them otherwise.
+    and must not overlap an input otherwise.
     Inputs that require gradients are refused: :func:`qk_norm_rope_autograd`
     records them.
     """
@@ -217,7 +221,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_gain: Optional[torch.Tensor
         out = (torch.empty_like(q, memory_format=_CONTIGUOUS), torch.empty_like(k, memory_format=_CONTIGUOUS))
     else:
         _check_like(out, (q, k))
-        _check_memory(out, ((q,), (k,)))
+        _check_memory(out, ((q,), (k,), _given(q_gain, k_gain, table, positions)))
     device = q.device
     with _on(device):
         B.zero_qk_norm_rope(cfg, tokens, _heads(q), _heads(k), _ptr(q_gain), _ptr(k_gain), table.data_ptr(),
@@ -238,7 +242,7 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
                           gain_out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None):
     """Gradients (dq, dk, dq_gain, dk_gain) of :func:`qk_norm_rope`'s inputs.
 
-    ``out`` may be (dq_out, dk_out) or (q, k), and must not overlap them otherwise.
+    ``out`` may be (dq_out, dk_out) or (q, k), and must not overlap an input otherwise.
     ``gain_out``: two vectors of head_dim elements, bf16 or fp32, to write the
     gain gradients to, such as slices of a replica's flat gradient; new fp32
     vectors otherwise.  Inputs that require gradients are refused, as in
@@ -251,7 +255,7 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
         out = (torch.empty_like(q, memory_format=_CONTIGUOUS), torch.empty_like(k, memory_format=_CONTIGUOUS))
     else:
         _check_like(out, (q, k))
-        _check_memory(out, ((dq_out, q), (dk_out, k)))
+        _check_memory(out, ((dq_out, q), (dk_out, k), _given(q_gain, k_gain, table, positions)))
     device, dim = q.device, cfg.head_dim
     if gain_out is None:
         gain_out = (torch.empty(dim, dtype=torch.float32, device=device),
@@ -261,7 +265,7 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
             if g.dtype not in _DTYPES or g.dtype != gain_out[0].dtype or g.shape != (dim,) or g.device != device \
                     or not g.is_contiguous():
                 raise ValueError("gain_out must be two contiguous vectors of head_dim elements and one type")
-        _check_memory(gain_out, ())
+        _check_memory(gain_out, ((), (), out))
     with _on(device):
         need = max(_backward_workspace(cfg.q_heads, cfg.k_heads, dim, tokens, device.index), 16)
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
@@ -484,7 +488,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
         _check_like((out,), (x,))
         y = _matrix(out, "out", copy=False)
         y_stride = y.stride(0)
-        _check_memory((y,), ((m,), [v for v in (weight, bias) if v is not None]))
+        _check_memory((y,), ((m,), _given(weight, bias)))
     stats = torch.empty((rows, 2), dtype=torch.float32, device=device)
     packed = None if pack is None else _new_packed(rows, cols, x.shape, x.dtype, pack, device)
     cfg = _norm_config(cols, 1 if center else 0, kind, vector_kind or 0, float(eps))
@@ -538,7 +542,7 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivatio
         _check_like((out,), (dy,))
         d = _matrix(out, "out", copy=False)
         d_stride = d.stride(0)
-        others = [stats] if weight is None else [stats, weight]
+        others = _given(stats, weight)
         _check_memory((d,), ((g,), [*others, x.data]) if kept else ((g, m), others))
     given = None
     if weight_out is not None or bias_out is not None:
@@ -546,7 +550,7 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivatio
             given = given if v is None else _check_vector(v, cols, device, given)
         if bias_out is not None and not bias:
             raise ValueError("bias_out without a bias")
-        _check_memory([v for v in (weight_out, bias_out) if v is not None], ((), (), (g, d, x.data if kept else m)))
+        _check_memory(_given(weight_out, bias_out), ((), (), (g, d, x.data if kept else m)))
     vectors = torch.bfloat16 if given == B.ZERO_GRAD_BF16 else torch.float32
     if weight is not None and weight_out is None:
         weight_out = torch.empty(cols, dtype=vectors, device=device)
