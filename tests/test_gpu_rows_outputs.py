@@ -82,3 +82,38 @@ def test_norm_and_rotation_over_gains_table_and_positions():
     for g, e in zip(ops.qk_norm_rope(q, k, beside[0], gains[1], table, positions, out=out),
                     ops.qk_norm_rope(q, k, *gains, table, positions)):
         assert torch.equal(g, e)
+
+
+def calls_with_outputs():
+    """Every operator with outputs of the caller's: a function of a tuple of them, and their shapes."""
+    x, dy, w, b = normal(6, 64), normal(6, 64, seed=1), normal(64), normal(64, seed=1)
+    _, stats, packed = ops.layer_norm(x, w, b, pack=torch.int8)
+    ids, table = torch.tensor([0, 2, 2], device="cuda"), normal(5, 16)
+    q, k, dq, dk = normal(4, 3, 32), normal(4, 2, 32), normal(4, 3, 32, seed=1), normal(4, 2, 32, seed=1)
+    rest = normal(32), normal(32, seed=1), normal(8, 16).cos()
+    return [
+        (lambda out: ops.layer_norm(x, w, b, out=out[0]), [(6, 64)]),
+        (lambda out: ops.layer_norm_backward(dy, x, w, stats, out=out[0], weight_out=out[1], bias_out=out[2]), [(6, 64), (64,), (64,)]),
+        (lambda out: ops.unpack_activations(packed, out=out[0]), [(6, 64)]),
+        (lambda out: ops.embedding(ids, table, out=out[0]), [(3, 16)]),
+        (lambda out: ops.embedding_backward(dy[:3, :16], ids, 5, out=out[0]), [(5, 16)]),
+        (lambda out: ops.embedding_backward(dy[:3, :16], ids, 5, out=out[0], accumulate=True), [(5, 16)]),
+        (lambda out: ops.qk_norm_rope(q, k, *rest, out=out), [q.shape, k.shape]),
+        (lambda out: ops.qk_norm_rope_backward(dq, dk, q, k, *rest, out=out[:2], gain_out=out[2:]), [q.shape, k.shape, (32,), (32,)]),
+        (lambda out: ops.orthogonalize(x, out=out[0]), [(6, 64)])]
+
+
+@pytest.mark.parametrize("which", range(9))
+def test_outputs_that_require_gradients(which):
+    call, shapes = calls_with_outputs()[which]
+    dtype = torch.bfloat16 if which == 8 else torch.float32
+    for i in range(len(shapes)):
+        outs = tuple(torch.zeros(s, device="cuda", dtype=dtype) for s in shapes)
+        for leaf in (outs[i].clone().requires_grad_(), outs[i].clone().requires_grad_() * 1):
+            some = (*outs[:i], leaf, *outs[i + 1:])
+            with pytest.raises(ValueError):
+                call(some)
+            assert (leaf == 0).all()
+            with torch.no_grad():  # as torch's own calls into a leaf
+                call(some)
+            assert not (leaf == 0).all()

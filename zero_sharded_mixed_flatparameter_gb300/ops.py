@@ -62,6 +62,12 @@ def _no_graph(what: str, *tensors: Optional[torch.Tensor]) -> None:
         raise ValueError(f"{what} records no gradient: detach its inputs or call it under torch.no_grad()")
 
 
+def _no_leaf(*outs: Optional[torch.Tensor]) -> None:
+    """An output that requires a gradient is refused: torch.autograd would not learn of what is written."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in outs):
+        raise ValueError("an output requires a gradient: detach it or call under torch.no_grad()")
+
+
 def _layout(x: torch.Tensor) -> Tuple[int, int, list]:
     """Byte address, bytes of a contiguous run and the (stride, size) of the other dimensions, largest stride first."""
     size = x.element_size()
@@ -136,6 +142,7 @@ def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients: Sequence[flo
             out.size(-1) > 1 and out.stride(-1) != 1):
         raise ValueError("out must be a bf16 tensor of x's shape and device with contiguous columns")
     else:
+        _no_leaf(out)
         _check_memory((out,), ((), (x,)))
     batch, rows, cols = (1, *x.shape) if x.dim() == 2 else x.shape
     cfg = _ns_config(operator.index(steps), tuple(map(float, coefficients)), float(eps))
@@ -220,6 +227,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_gain: Optional[torch.Tensor
     if out is None:
         out = (torch.empty_like(q, memory_format=_CONTIGUOUS), torch.empty_like(k, memory_format=_CONTIGUOUS))
     else:
+        _no_leaf(*out)
         _check_like(out, (q, k))
         _check_memory(out, ((q,), (k,), _given(q_gain, k_gain, table, positions)))
     device = q.device
@@ -254,6 +262,7 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
     if out is None:
         out = (torch.empty_like(q, memory_format=_CONTIGUOUS), torch.empty_like(k, memory_format=_CONTIGUOUS))
     else:
+        _no_leaf(*out)
         _check_like(out, (q, k))
         _check_memory(out, ((dq_out, q), (dk_out, k), _given(q_gain, k_gain, table, positions)))
     device, dim = q.device, cfg.head_dim
@@ -261,6 +270,7 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
         gain_out = (torch.empty(dim, dtype=torch.float32, device=device),
                     torch.empty(dim, dtype=torch.float32, device=device))
     else:
+        _no_leaf(*gain_out)
         for g in gain_out:
             if g.dtype not in _DTYPES or g.dtype != gain_out[0].dtype or g.shape != (dim,) or g.device != device \
                     or not g.is_contiguous():
@@ -446,7 +456,7 @@ def unpack_activations(packed: PackedActivations, dtype: Optional[torch.dtype] =
         out = torch.empty(packed.shape, dtype=dtype or packed.dtype, device=device)
         at, stride = out.data_ptr(), packed.cols
     else:
-        _no_graph("unpack_activations", out)
+        _no_leaf(out)
         kind = _DTYPES.get(out.dtype)
         if kind is None or out.shape != packed.shape or out.device != device or dtype not in (None, out.dtype):
             raise ValueError("out must be a bf16 or fp32 tensor of packed's shape and device")
@@ -485,6 +495,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
         out = _new_like(x)
         y, y_stride = out, cols
     else:
+        _no_leaf(out)
         _check_like((out,), (x,))
         y = _matrix(out, "out", copy=False)
         y_stride = y.stride(0)
@@ -539,6 +550,7 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivatio
         out = _new_like(dy)
         d, d_stride = out, cols
     else:
+        _no_leaf(out)
         _check_like((out,), (dy,))
         d = _matrix(out, "out", copy=False)
         d_stride = d.stride(0)
@@ -546,6 +558,7 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivatio
         _check_memory((d,), ((g,), [*others, x.data]) if kept else ((g, m), others))
     given = None
     if weight_out is not None or bias_out is not None:
+        _no_leaf(weight_out, bias_out)
         for v in (weight_out, bias_out):
             given = given if v is None else _check_vector(v, cols, device, given)
         if bias_out is not None and not bias:
@@ -637,6 +650,7 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0,
         out = torch.empty((*ids.shape, dim), dtype=table.dtype, device=device)
         at, stride = out.data_ptr(), dim
     else:
+        _no_leaf(out)
         if out.shape != (*ids.shape, dim) or out.dtype != table.dtype or out.device != device:
             raise ValueError("out must have the shape of ids and dim, and table's type and device")
         y = _matrix(out, "out", copy=False)
@@ -662,8 +676,8 @@ def embedding_backward(dy: torch.Tensor, ids: torch.Tensor, rows: int, *, scale:
     zeroed; with ``accumulate`` the sums are added to ``out`` instead, and those
     rows stay as they are.
     """
-    if dy.requires_grad or out is not None and out.requires_grad:
-        _no_graph("embedding_backward", dy, out)
+    if dy.requires_grad:
+        _no_graph("embedding_backward", dy)
     kind, device, dim, rows = _check_rows(dy, "dy"), dy.device, dy.size(-1), operator.index(rows)
     ids, size = _check_ids(ids, device)
     if dy.shape[:-1] != ids.shape:
@@ -674,6 +688,7 @@ def embedding_backward(dy: torch.Tensor, ids: torch.Tensor, rows: int, *, scale:
             raise ValueError("accumulate needs an out to add to")
         out, out_kind = torch.empty((rows, dim), dtype=dy.dtype, device=device), kind
     else:
+        _no_leaf(out)
         out_kind = _DTYPES.get(out.dtype)
         if out_kind is None or out.shape != (rows, dim) or out.device != device or (out.stride(1) != 1 and dim > 1):
             raise ValueError("out must be a bf16 or fp32 matrix (rows, dim) with contiguous columns")
