@@ -117,3 +117,37 @@ def test_outputs_that_require_gradients(which):
             with torch.no_grad():  # as torch's own calls into a leaf
                 call(some)
             assert not (leaf == 0).all()
+
+
+@pytest.mark.parametrize("which", range(9))
+def test_autograd_learns_of_what_is_written(which):
+    call, shapes = calls_with_outputs()[which]
+    dtype = torch.bfloat16 if which == 8 else torch.float32
+    for i in range(len(shapes)):
+        outs = tuple(torch.zeros(s, device="cuda", dtype=dtype) for s in shapes)
+        versions = [o._version for o in outs]
+        leaf = torch.ones_like(outs[i]).requires_grad_()
+        product = leaf * outs[i]  # keeps outs[i] for the leaf's gradient
+        call(outs)
+        assert all(o._version > v for o, v in zip(outs, versions))
+        with pytest.raises(RuntimeError):
+            product.sum().backward()
+    with torch.inference_mode():  # such tensors have no version
+        call(tuple(torch.zeros(s, device="cuda", dtype=dtype) for s in shapes))
+
+
+def test_autograd_learns_of_codes_written_again():
+    x = normal(6, 64)
+    packed = ops.pack_activations(x)
+    version = packed.data._version
+    ops.pack_activations(2 * x, out=packed)
+    assert packed.data._version > version
+
+
+def test_a_kept_input_that_changes_is_found():
+    # the norm keeps x; a lookup into the same memory comes before its backward pass
+    x, w = normal(3, 16), normal(16).requires_grad_()
+    y = ops.layer_norm_autograd(x, w)
+    ops.embedding(torch.tensor([1, 0, 1], device="cuda"), normal(2, 16, seed=3), out=x)
+    with pytest.raises(RuntimeError):
+        y.sum().backward()

@@ -68,6 +68,11 @@ def _no_leaf(*outs: Optional[torch.Tensor]) -> None:
         raise ValueError("an output requires a gradient: detach it or call under torch.no_grad()")
 
 
+# Tells torch.autograd that the kernels wrote to tensors of the caller's, so that a
+# backward pass that saved one of them raises instead of reading what is there now.
+_written = torch.autograd.graph.increment_version
+
+
 def _layout(x: torch.Tensor) -> Tuple[int, int, list]:
     """Byte address, bytes of a contiguous run and the (stride, size) of the other dimensions, largest stride first."""
     size = x.element_size()
@@ -144,6 +149,7 @@ def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients: Sequence[flo
     else:
         _no_leaf(out)
         _check_memory((out,), ((), (x,)))
+        _written(out)
     batch, rows, cols = (1, *x.shape) if x.dim() == 2 else x.shape
     cfg = _ns_config(operator.index(steps), tuple(map(float, coefficients)), float(eps))
     with _on(x.device):
@@ -230,6 +236,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_gain: Optional[torch.Tensor
         _no_leaf(*out)
         _check_like(out, (q, k))
         _check_memory(out, ((q,), (k,), _given(q_gain, k_gain, table, positions)))
+        _written(out)
     device = q.device
     with _on(device):
         B.zero_qk_norm_rope(cfg, tokens, _heads(q), _heads(k), _ptr(q_gain), _ptr(k_gain), table.data_ptr(),
@@ -265,6 +272,7 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
         _no_leaf(*out)
         _check_like(out, (q, k))
         _check_memory(out, ((dq_out, q), (dk_out, k), _given(q_gain, k_gain, table, positions)))
+        _written(out)
     device, dim = q.device, cfg.head_dim
     if gain_out is None:
         gain_out = (torch.empty(dim, dtype=torch.float32, device=device),
@@ -276,6 +284,7 @@ def qk_norm_rope_backward(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.T
                     or not g.is_contiguous():
                 raise ValueError("gain_out must be two contiguous vectors of head_dim elements and one type")
         _check_memory(gain_out, ((), (), out))
+        _written(gain_out)
     with _on(device):
         need = max(_backward_workspace(cfg.q_heads, cfg.k_heads, dim, tokens, device.index), 16)
         workspace = torch.empty(need, dtype=torch.uint8, device=device)
@@ -440,6 +449,7 @@ def pack_activations(x: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, 
         if out.shape != x.shape or out.dtype != x.dtype or out.form != dtype or out.data.device != device:
             raise ValueError("out must have x's shape, type and device, and codes of dtype")
         _check_memory((out.data,), ((), (m,)))
+        _written(out.data)
     _call(B.load().zero_pack_activations, device, rows, cols, m.data_ptr(), kind, m.stride(0), out._struct)
     return out
 
@@ -462,6 +472,7 @@ def unpack_activations(packed: PackedActivations, dtype: Optional[torch.dtype] =
             raise ValueError("out must be a bf16 or fp32 tensor of packed's shape and device")
         m = _matrix(out, "out", copy=False)
         _check_memory((m,), ((), (packed.data,)))
+        _written(out)
         at, stride = m.data_ptr(), m.stride(0)
     _call(B.load().zero_unpack_activations, device, packed.rows, packed.cols, packed._struct, at, kind, stride)
     return out
@@ -500,6 +511,7 @@ def layer_norm(x: torch.Tensor, weight: Optional[torch.Tensor] = None, bias: Opt
         y = _matrix(out, "out", copy=False)
         y_stride = y.stride(0)
         _check_memory((y,), ((m,), _given(weight, bias)))
+        _written(out)
     stats = torch.empty((rows, 2), dtype=torch.float32, device=device)
     packed = None if pack is None else _new_packed(rows, cols, x.shape, x.dtype, pack, device)
     cfg = _norm_config(cols, 1 if center else 0, kind, vector_kind or 0, float(eps))
@@ -556,6 +568,7 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivatio
         d_stride = d.stride(0)
         others = _given(stats, weight)
         _check_memory((d,), ((g,), [*others, x.data]) if kept else ((g, m), others))
+        _written(out)
     given = None
     if weight_out is not None or bias_out is not None:
         _no_leaf(weight_out, bias_out)
@@ -563,7 +576,9 @@ def layer_norm_backward(dy: torch.Tensor, x: Union[torch.Tensor, PackedActivatio
             given = given if v is None else _check_vector(v, cols, device, given)
         if bias_out is not None and not bias:
             raise ValueError("bias_out without a bias")
-        _check_memory(_given(weight_out, bias_out), ((), (), (g, d, x.data if kept else m)))
+        mine = _given(weight_out, bias_out)
+        _check_memory(mine, ((), (), (g, d, x.data if kept else m)))
+        _written(mine)
     vectors = torch.bfloat16 if given == B.ZERO_GRAD_BF16 else torch.float32
     if weight is not None and weight_out is None:
         weight_out = torch.empty(cols, dtype=vectors, device=device)
@@ -656,6 +671,7 @@ def embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0,
         y = _matrix(out, "out", copy=False)
         at, stride = y.data_ptr(), y.stride(0)
         _check_memory((y,), ((), (table, ids)))
+        _written(out)
     cfg = _embedding_config(rows, dim, kind, size, float(scale))
     _call(B.load().zero_embedding, device, cfg, ids.numel(), ids.data_ptr(), table.data_ptr(), table.stride(0), at, stride)
     return out
@@ -693,6 +709,7 @@ def embedding_backward(dy: torch.Tensor, ids: torch.Tensor, rows: int, *, scale:
         if out_kind is None or out.shape != (rows, dim) or out.device != device or (out.stride(1) != 1 and dim > 1):
             raise ValueError("out must be a bf16 or fp32 matrix (rows, dim) with contiguous columns")
         _check_memory((out,), ((), (g, ids)))
+        _written(out)
     tokens = ids.numel()
     cfg, need = _embedding_config(rows, dim, kind, size, float(scale)), _embedding_workspace(rows, dim, tokens)
     workspace = torch.empty(need, dtype=torch.uint8, device=device)
