@@ -779,7 +779,8 @@ typedef struct zero_packed {
  * zero_pack_activations — codes and scales of a matrix; zero_unpack_activations
  * — the values they stand for, rounded to dtype (exact, but for bf16
  * subnormals).
- *  cols    1..2^24; row r of the matrix begins at r * stride elements
+ *  cols    1..2^24; row r of the matrix begins at r * stride elements; the
+ *          stride of an output is at least cols
  * rows of 0: ZERO_OK without device work.  Errors: ZERO_EINVAL; ZERO_ECUDA.
  */
 zero_status zero_pack_activations(int64_t rows, int64_t cols, const void* x, int32_t dtype, int64_t x_stride,
@@ -808,7 +809,8 @@ typedef struct zero_norm_config {
  *   y = (x - mean) * rstd * weight + bias
  * in fp32, rounded once; a row whose squares exceed fp32's range has rstd 0.
  *  weight, bias   cols elements of weight_dtype, or NULL: none
- *  y              may be x itself (same stride), else must not overlap an input
+ *  y              may be x itself (same stride), else must not overlap an input;
+ *                 a stride of at least cols
  *  stats          fp32 [rows][2]: mean and rstd, which the backward pass reads;
  *                 8-byte aligned, or NULL: not wanted
  *  packed         takes the 8-bit form of x in the same pass, or NULL
@@ -831,7 +833,7 @@ zero_status zero_layer_norm_backward_workspace_bytes(const zero_norm_config* cfg
  *                    it stands for take the input's place, the statistics stay
  *  stats             as zero_layer_norm wrote them
  *  dx                may be dy or x itself (same stride), else must not overlap
- *                    an input
+ *                    an input; a stride of at least cols
  *  dweight, dbias    cols elements of dgrad_dtype (zero_grad_dtype), overwritten
  *                    (zeros for 0 rows); NULL: not wanted
  *  workspace         device scratch, 16-byte aligned (not read where neither of
@@ -863,7 +865,8 @@ typedef struct zero_embedding_config {
  * zero_embedding — out[t] = scale * table[ids[t]], rounded once; zeros where the
  * id is outside [0, rows) (padding).
  *  tokens   0..2^30 (0: ZERO_OK without device work)
- *  table, out   rows at multiples of their stride (elements)
+ *  table, out   rows at multiples of their stride (elements); that of out is at
+ *               least dim
  * Errors: ZERO_EINVAL; ZERO_ECUDA.
  */
 zero_status zero_embedding(const zero_embedding_config* cfg, int64_t tokens, const void* ids, const void* table,
@@ -876,7 +879,8 @@ zero_status zero_embedding_backward_workspace_bytes(const zero_embedding_config*
  * zero_embedding_backward — dtable[v] = scale * sum of dout[t] over the tokens t
  * with ids[t] = v.  The tokens are sorted by row, the sums fp32 in an order that
  * the ids fix: the same call gives the same bits.
- *  dtable      dtable_dtype (zero_grad_dtype), must not overlap dout or ids
+ *  dtable      dtable_dtype (zero_grad_dtype), must not overlap dout or ids; a
+ *              stride of at least dim
  *  accumulate  0: every row is written (zeros without tokens); 1: the sums are
  *              added to what is there, rows without tokens stay as they are
  *  workspace   device scratch, 16-byte aligned

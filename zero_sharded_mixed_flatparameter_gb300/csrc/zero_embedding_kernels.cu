@@ -620,6 +620,7 @@ zero_status zero_embedding(const zero_embedding_config* cfg, int64_t tokens, con
       (st = check_rows(table, table_stride, cfg->dtype, "table is NULL or misaligned, or its stride negative")) != ZERO_OK)
     return st;
   if ((st = check_rows(out, out_stride, cfg->dtype, "out is NULL or misaligned, or its stride negative")) != ZERO_OK) return st;
+  if (rows_overlap(out_stride, tokens, cfg->dim)) return refuse(ZERO_EINVAL, "out's stride makes its rows overlap");
   EmbArgs a{};
   a.tokens = tokens;
   a.vocab = static_cast<int>(cfg->rows);
@@ -664,6 +665,7 @@ zero_status zero_embedding_backward(const zero_embedding_config* cfg, int64_t to
   if (cfg->rows == 0 || (accumulate && tokens == 0)) return ZERO_OK;
   if ((st = check_rows(dtable, dtable_stride, dtable_dtype, "dtable is NULL or misaligned, or its stride negative")) != ZERO_OK)
     return st;
+  if (rows_overlap(dtable_stride, cfg->rows, cfg->dim)) return refuse(ZERO_EINVAL, "dtable's stride makes its rows overlap");
   if (tokens > 0) {
     if (misplaced(ids, cfg->id_bytes)) return refuse(ZERO_EINVAL, "ids are NULL or misaligned");
     if ((st = check_rows(dout, dout_stride, cfg->dtype, "dout is NULL or misaligned, or its stride negative")) != ZERO_OK)

@@ -972,6 +972,7 @@ zero_status zero_layer_norm(const zero_norm_config* cfg, int64_t rows, const voi
   const int vsz = dtype_bytes(cfg->weight_dtype);
   if ((st = check_matrix(x, x_stride, cfg->dtype, "x is NULL or misaligned, or its stride negative")) != ZERO_OK) return st;
   if ((st = check_matrix(y, y_stride, cfg->dtype, "y is NULL or misaligned, or its stride negative")) != ZERO_OK) return st;
+  if (rows_overlap(y_stride, rows, cfg->cols)) return refuse(ZERO_EINVAL, "y's stride makes its rows overlap");
   if ((weight && misplaced(weight, vsz)) || (bias && misplaced(bias, vsz)))
     return refuse(ZERO_EINVAL, "weight or bias is misaligned");
   if (stats && misplaced(stats, 8)) return refuse(ZERO_EINVAL, "stats is misaligned");
@@ -1031,6 +1032,7 @@ zero_status zero_layer_norm_backward(const zero_norm_config* cfg, int64_t rows, 
   if (rows > 0) {
     if ((st = check_matrix(dy, dy_stride, cfg->dtype, "dy is NULL or misaligned, or its stride negative")) != ZERO_OK) return st;
     if ((st = check_matrix(dx, dx_stride, cfg->dtype, "dx is NULL or misaligned, or its stride negative")) != ZERO_OK) return st;
+    if (rows_overlap(dx_stride, rows, cfg->cols)) return refuse(ZERO_EINVAL, "dx's stride makes its rows overlap");
     if (packed) {
       if ((st = check_packed(packed, &a)) != ZERO_OK) return st;
     } else if ((st = check_matrix(x, x_stride, cfg->dtype, "x is NULL or misaligned, or its stride negative")) != ZERO_OK) {

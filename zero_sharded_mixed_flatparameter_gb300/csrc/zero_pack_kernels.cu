@@ -103,6 +103,7 @@ zero_status convert(int64_t rows, int64_t cols, const void* x, int32_t dtype, in
   if (rows == 0) return ZERO_OK;
   if (misplaced(x, dtype_bytes(dtype)) || x_stride < 0)
     return refuse(ZERO_EINVAL, "the matrix is NULL or misaligned, or its stride negative");
+  if (!pack && rows_overlap(x_stride, rows, cols)) return refuse(ZERO_EINVAL, "out's stride makes its rows overlap");
   if (misplaced(packed->codes, 16) || !packed->scales)
     return refuse(ZERO_EINVAL, "codes or scales are NULL or misaligned");
   PackArgs a{};

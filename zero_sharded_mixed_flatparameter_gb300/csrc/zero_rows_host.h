@@ -25,6 +25,9 @@ inline bool misplaced(const void* p, int alignment) { return !p || reinterpret_c
 inline bool is_dtype(int d) { return d == ZERO_GRAD_BF16 || d == ZERO_GRAD_FP32; }
 inline int dtype_bytes(int d) { return d == ZERO_GRAD_FP32 ? 4 : 2; }
 
+// Rows that are written must not share elements: several threads would write them.
+inline bool rows_overlap(long long stride, long long rows, long long cols) { return rows > 1 && stride < cols; }
+
 inline zero_status launch_status(const char* what) {
   const cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess) return ZERO_OK;
