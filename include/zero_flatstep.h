@@ -879,6 +879,8 @@ zero_status zero_embedding_backward_workspace_bytes(const zero_embedding_config*
  * zero_embedding_backward — dtable[v] = scale * sum of dout[t] over the tokens t
  * with ids[t] = v.  The tokens are sorted by row, the sums fp32 in an order that
  * the ids fix: the same call gives the same bits.
+ *  tokens      0..2^30, and at most 2^50 over the rows rounded up to a power of
+ *              two: every 1024 rows (from 2^17 rows on) read all ids
  *  dtable      dtable_dtype (zero_grad_dtype), must not overlap dout or ids; a
  *              stride of at least dim
  *  accumulate  0: every row is written (zeros without tokens); 1: the sums are

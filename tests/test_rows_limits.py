@@ -18,3 +18,14 @@ def test_rows_of_an_output_that_overlap(stride):
     refused(B.zero_embedding, cfg, 4, P, P, 64, P, stride)
     for accumulate in (0, 1):
         refused(B.zero_embedding_backward, cfg, 4, P, P, 64, P, 1, stride, accumulate, P, 1 << 40)
+
+
+@pytest.mark.parametrize("rows,most", [(1 << 30, 1 << 20), ((1 << 29) + 1, 1 << 20), (1 << 24, 1 << 26), ((1 << 20) + 1, 1 << 29)])
+def test_a_sort_of_many_seconds(rows, most):
+    cfg = embedding_config(rows=rows, dim=1)
+    need = B.zero_embedding_backward_workspace_bytes(cfg, most)
+    assert need >= 16 * most + 4 * rows
+    refused(B.zero_embedding_backward_workspace_bytes, cfg, most + 1)
+    refused(B.zero_embedding_backward, cfg, most + 1, P, P, 1, P, 1, 1, 0, P, 1 << 60)
+    for fewer in (1, 1 << 17, 1 << 20):  # rows that a vocabulary has: any number of tokens
+        B.zero_embedding_backward_workspace_bytes(embedding_config(rows=fewer, dim=1), 1 << 30)

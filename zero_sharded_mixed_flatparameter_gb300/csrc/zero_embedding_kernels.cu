@@ -541,6 +541,17 @@ Workspace lay_out(const zero_embedding_config& c, int64_t tokens) {
   return w;
 }
 
+// Sorting CTAs: more where the counters of their rows would not fit.
+int remainders_of(int64_t rows) {
+  int remainders = kSortCtas;
+  while ((rows + remainders - 1) / remainders > kSortRows) remainders *= 2;
+  return remainders;
+}
+// Every sorting CTA looks at every id: together 170 ids a nanosecond where they
+// read them again (2^24 tokens, 2^20 rows: 103 ms), 1600 where lists hold their tokens
+// (2^22, 2^22: 11 ms).  More looks than this would hold the GPU for many seconds.
+constexpr int64_t kMostLooks = 1LL << 40;
+
 zero_status check_embedding(const zero_embedding_config* c, int64_t tokens) {
   if (!c) return refuse(ZERO_EINVAL, "config is NULL");
   if (tokens < 0 || tokens > (1LL << 30)) return refuse(ZERO_EINVAL, "tokens not in 0..2^30");
@@ -549,6 +560,13 @@ zero_status check_embedding(const zero_embedding_config* c, int64_t tokens) {
   if (!is_dtype(c->dtype)) return refuse(ZERO_EINVAL, "dtype is neither bf16 (0) nor fp32 (1)");
   if (c->id_bytes != 4 && c->id_bytes != 8) return refuse(ZERO_EINVAL, "ids must have 4 or 8 bytes");
   if (!std::isfinite(c->scale)) return refuse(ZERO_EINVAL, "scale must be finite");
+  return ZERO_OK;
+}
+
+zero_status check_backward(const zero_embedding_config* c, int64_t tokens) {
+  const zero_status st = check_embedding(c, tokens);
+  if (st != ZERO_OK) return st;
+  if (tokens > kMostLooks / remainders_of(c->rows)) return refuse(ZERO_EINVAL, "rows and tokens are too many together");
   return ZERO_OK;
 }
 
@@ -648,7 +666,7 @@ zero_status zero_embedding(const zero_embedding_config* cfg, int64_t tokens, con
 
 zero_status zero_embedding_backward_workspace_bytes(const zero_embedding_config* cfg, int64_t tokens, int64_t* bytes) {
   if (!bytes) return zfs::refuse(ZERO_EINVAL, "bytes is NULL");
-  const zero_status st = zfs::check_embedding(cfg, tokens);
+  const zero_status st = zfs::check_backward(cfg, tokens);
   if (st != ZERO_OK) return st;
   *bytes = zfs::lay_out(*cfg, tokens).total;
   return ZERO_OK;
@@ -658,7 +676,7 @@ zero_status zero_embedding_backward(const zero_embedding_config* cfg, int64_t to
                                     int64_t dout_stride, void* dtable, int32_t dtable_dtype, int64_t dtable_stride,
                                     int32_t accumulate, void* workspace, int64_t workspace_bytes, void* stream) {
   using namespace zfs;
-  zero_status st = check_embedding(cfg, tokens);
+  zero_status st = check_backward(cfg, tokens);
   if (st != ZERO_OK) return st;
   if (!is_dtype(dtable_dtype)) return refuse(ZERO_EINVAL, "dtable_dtype is neither bf16 (0) nor fp32 (1)");
   if (accumulate != 0 && accumulate != 1) return refuse(ZERO_EINVAL, "accumulate must be 0 or 1");
@@ -696,9 +714,7 @@ zero_status zero_embedding_backward(const zero_embedding_config* cfg, int64_t to
   a.runs = w.runs;
   a.chunk = w.chunk;
   a.slabs = (a.dim + 127) / 128;
-  // more sorting CTAs where the counters of their rows would not fit
-  a.remainders = kSortCtas;
-  while ((a.vocab + a.remainders - 1) / a.remainders > kSortRows) a.remainders *= 2;
+  a.remainders = remainders_of(a.vocab);
   a.per_cta = (a.vocab + a.remainders - 1) / a.remainders;
   const int shared = (kSortWarps * a.per_cta + a.per_cta + 1) * static_cast<int>(sizeof(int));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
