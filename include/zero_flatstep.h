@@ -757,10 +757,11 @@ zero_status zero_qk_norm_rope_backward(const zero_qk_config* cfg, int64_t tokens
  * a row.  A scale is the smallest power of two, from 2^-126 on, under which the
  * group's largest magnitude is at most the format's (448; 127): an element is
  * divided by it exactly and rounded once, to nearest, ties to even.  A group
- * with an inf or NaN in it reads as NaN.
+ * with an inf or NaN in it reads as NaN; an entry that rounds up to 2^128 (from
+ * 31/32 of it on in e4m3, above 127/128 as whole numbers) reads as inf.
  */
-#define ZERO_PACK_E4M3 0  /* 4 significant bits: off by at most 2^-4 of itself */
-#define ZERO_PACK_INT8 1  /* whole numbers: off by at most 2^-7 of the group's largest */
+#define ZERO_PACK_E4M3 0  /* 4 significant bits: off by at most 2^-4 of itself or, below 2^-6 scales, 2^-10 of the scale */
+#define ZERO_PACK_INT8 1  /* whole numbers: off by at most half a scale, 1/127 of the group's largest (from 2^-120 on) */
 
 /*
  * The 8-bit form of a matrix (device memory):
@@ -778,7 +779,7 @@ typedef struct zero_packed {
 /*
  * zero_pack_activations — codes and scales of a matrix; zero_unpack_activations
  * — the values they stand for, rounded to dtype (exact, but for bf16
- * subnormals).
+ * subnormals and 2^128: inf).
  *  cols    1..2^24; row r of the matrix begins at r * stride elements; the
  *          stride of an output is at least cols
  * rows of 0: ZERO_OK without device work.  Errors: ZERO_EINVAL; ZERO_ECUDA.

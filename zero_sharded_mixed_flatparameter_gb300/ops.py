@@ -434,9 +434,11 @@ def pack_activations(x: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, 
     """``x`` (bf16 or fp32, any shape, columns contiguous) in 8 bits, with a
     power-of-two scale for every 32 columns of a row.
 
-    ``dtype``: torch.float8_e4m3fn (each entry within 2^-4 of itself) or
-    torch.int8 (within 2^-7 of its group's largest).  A group with an inf or NaN
-    reads as NaN.  ``out``: an earlier result of the same shape and types to
+    ``dtype``: torch.float8_e4m3fn (each entry within 2^-4 of itself or, where it is
+    smaller than 2^-6 of the scale, within 2^-10 of the scale; the group's largest is
+    above 224 scales) or torch.int8 (within half a scale, 1/127 of its group's
+    largest).  A group with an inf or NaN reads as NaN; finite entries that round up
+    to 2^128 read as inf.  ``out``: an earlier result of the same shape and types to
     write to.  What ``x`` requires a gradient for is not recorded: this keeps a
     tensor for the backward pass, as saving it would.
     """
@@ -457,7 +459,8 @@ def pack_activations(x: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, 
 def unpack_activations(packed: PackedActivations, dtype: Optional[torch.dtype] = None, *,
                        out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values that ``packed`` stands for, in the type of what was packed or
-    ``dtype`` (bf16 or fp32; both hold them exactly, but for bf16 subnormals)."""
+    ``dtype`` (bf16 or fp32; both hold them exactly, but for bf16 subnormals and
+    2^128, which becomes inf)."""
     device = packed.data.device
     if out is None:
         kind = _DTYPES.get(dtype or packed.dtype)
