@@ -384,12 +384,7 @@ __global__ void __launch_bounds__(kSumThreads, 6) embedding_sum_kernel(const __g
 #pragma unroll
     for (int k = 0; k < kCount / 2; ++k) sum[n][k] = add2(sum[n][k], pair(x[2 * k], x[2 * k + 1]));
   };
-  while (q >= group + 32) {  // (a run that begins behind a short row of another)
-    group += 32;
-    now = next;
-    next = third;
-  }
-  look();
+  look();  // q is below 32: it lies within the run
   if constexpr (kVec == 8) {
     constexpr int kWords = 2;  // 16-byte words of a lane's row: of one part (fp32), of two
     extern __shared__ uint4 ring[];  // [warp][slot][word][lane]
