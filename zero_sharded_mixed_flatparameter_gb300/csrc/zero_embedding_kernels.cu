@@ -256,7 +256,8 @@ __global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const __gr
 }
 
 // What a lane of a summing warp holds: 32 bytes of vectors, eight single elements,
-// or two (so that narrow tables have warps enough: below kNarrow columns).
+// or two (so that narrow tables have warps enough: below kNarrow fp32 or 2 kNarrow
+// bf16 columns).
 enum : int { kVectors = 8, kSingles = 1, kFewSingles = 0 };
 constexpr int kNarrow = 512;
 template <bool kFp32, int kMode>
@@ -513,12 +514,17 @@ struct Workspace {
   long long heavy_rows;  // more tokens than that no rows can be in parts
 };
 // Long runs make few parts, short ones many warps: the longest that still gives
-// every SM 32 warps (of single elements, which the alignment may come to).
+// every one of 152 SMs 32 warps (152 whatever the device: the workspace's size is
+// asked for without one), counting warps of 256 columns, 64 below kNarrow: single
+// elements, which the alignment may come to.  (bf16 of kNarrow to 2 kNarrow columns
+// has four times as many; its best run is no other: 32768 tokens x 769 in runs of
+// 8, 16, 32: 71, 66, 65 us, x 1001: 85, 77, 75, 8192 tokens x 1001: 27, 26, 29.)
+constexpr int kRunWarps = 32 * 152;
 int chunk_of(int64_t dim, int64_t tokens) {
   const int64_t width = dim < kNarrow ? kSumColumns<false, kFewSingles> : kSumColumns<false, kSingles>;
   const int64_t warps = (dim + width - 1) / width;
   int chunk = kMostChunk;
-  while (chunk > kLeastChunk && tokens / chunk * warps < 32 * 152) chunk /= 2;
+  while (chunk > kLeastChunk && tokens / chunk * warps < kRunWarps) chunk /= 2;
   return chunk;
 }
 Workspace lay_out(const zero_embedding_config& c, int64_t tokens) {
@@ -716,7 +722,10 @@ zero_status zero_embedding_backward(const zero_embedding_config* cfg, int64_t to
   const bool fp32 = cfg->dtype == ZERO_GRAD_FP32, out32 = dtable_dtype == ZERO_GRAD_FP32;
   const bool vec = a.dim % 8 == 0 && rows_aligned(dout, dout_stride, tokens, cfg->dtype) &&
                    rows_aligned(dtable, dtable_stride, cfg->rows, dtable_dtype);
-  // (4096 x 1001 bf16: 58 us with two elements a lane, 62 with eight; x 2047: 121 and 114)
+  // unaligned rows, us with two single elements a lane | with eight:
+  //   bf16, 4096 tokens x 769, 1001, 1301:  17, 18, 21 | 19, 19, 19;  32768 x 513, 1001:  46, 65 | 55, 68
+  //   fp32, 4096 tokens x 449, 769, 1001:   15, 18, 19 | 19, 17, 18;  32768 x 257, 513:   40, 47 | 44, 40
+  // (32768 x 1301 bf16 would gain, too: 76 | 96; the border does not look at the tokens)
   const int mode = vec ? kVectors : a.dim < (fp32 ? kNarrow : 2 * kNarrow) ? kFewSingles : kSingles;
   const int width = mode == kFewSingles ? kSumColumns<false, kFewSingles> : mode == kSingles || fp32 ? kSumColumns<true, kVectors> : kSumColumns<false, kVectors>;
   a.columns = (a.dim + width - 1) / width;
