@@ -22,7 +22,7 @@
 #include <cmath>
 
 #include "zero_flatstep.h"
-#include "zero_norm_internal.h"
+#include "zero_embedding_internal.h"
 #include "zero_rows.cuh"
 #include "zero_rows_host.h"
 
@@ -272,6 +272,7 @@ template <bool kFp32, int kMode>
 __device__ __forceinline__ void put_row(const EmbArgs& a, int row, int at, int lane, const float* sum) {
   constexpr long long kSize = kFp32 ? 4 : 2;
   constexpr int kVec = kMode == kVectors ? 8 : 1, kCount = kSumCount<kMode>;
+  if (!ZFS_CHECK(row >= 0 && row < a.vocab)) return;
   char* to = static_cast<char*>(a.out) + (row * a.out_stride + at) * kSize;
   float x[kCount];
 #pragma unroll
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(kSumThreads, 6) embedding_sum_kernel(const __g
   auto look = [&]() { begins = __ballot_sync(0xffffffffu, begin + group + lane == now.z); };
   auto row_at = [&](int i) {  // of this group or the next
     const int token = __shfl_sync(0xffffffffu, i - group < 32 ? now.x : next.x, i % 32);
-    return rows + token * a.row_stride * kSize;
+    return rows + (ZFS_CHECK(token >= 0 && token < a.tokens) ? token : 0) * a.row_stride * kSize;
   };
   auto open = [&](int i) {  // the row of entry i of this group
     row = __shfl_sync(0xffffffffu, now.y, i % 32);
@@ -474,6 +475,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) embedding_join_kernel(const _
   const long long items = static_cast<long long>(a.live[1]) * a.slabs;
   for (long long item = blockIdx.x; item < items; item += gridDim.x) {
     const int4 e = a.heavy[item / a.slabs];  // first run, row, parts: one of that run, then of those behind it
+    if (!ZFS_CHECK(e.x >= 0 && e.z > 0 && e.z <= a.runs - e.x && e.y >= 0 && e.y < a.vocab)) continue;
     const int c = static_cast<int>(item % a.slabs) * 128 + lane * 4;
     const int share = (e.z + kJoinWarps - 1) / kJoinWarps, from = warp * share;
     const int to = from + share < e.z ? from + share : e.z;

@@ -28,7 +28,6 @@
 #include <cmath>
 
 #include "zero_flatstep.h"
-#include "zero_norm_internal.h"
 #include "zero_rows.cuh"
 #include "zero_rows_host.h"
 
@@ -945,16 +944,6 @@ void fill(const zero_norm_config* c, int64_t rows, NormArgs* a) {
 }
 
 }  // namespace
-
-unsigned int norm_debug_failures() {
-#ifdef ZFS_DEBUG_CHECKS
-  unsigned int v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_debug_failures, sizeof v) != cudaSuccess) return 0xFFFFFFFFu;
-  return v;
-#else
-  return 0;
-#endif
-}
 
 }  // namespace zfs
 

@@ -9,7 +9,6 @@
 // floor is 4.8.
 
 #include "zero_flatstep.h"
-#include "zero_norm_internal.h"
 #include "zero_rows.cuh"
 #include "zero_rows_host.h"
 
@@ -129,16 +128,6 @@ zero_status convert(int64_t rows, int64_t cols, const void* x, int32_t dtype, in
 }
 
 }  // namespace
-
-unsigned int pack_debug_failures() {
-#ifdef ZFS_DEBUG_CHECKS
-  unsigned int v = 0;
-  if (cudaMemcpyFromSymbol(&v, g_debug_failures, sizeof v) != cudaSuccess) return 0xFFFFFFFFu;
-  return v;
-#else
-  return 0;
-#endif
-}
 
 }  // namespace zfs
 

@@ -35,10 +35,10 @@
 
 #include "zero_flatstep.h"
 #include "zero_aux_internal.h"
+#include "zero_embedding_internal.h"
 #include "zero_host.h"
 #include "zero_internal.h"
 #include "zero_muon_internal.h"
-#include "zero_norm_internal.h"
 #include "zero_qk_internal.h"
 
 namespace {
@@ -1547,7 +1547,7 @@ zero_status zero_debug_check_failures(uint32_t* count) {
 #ifdef ZFS_DEBUG_CHECKS
   const unsigned int counts[] = {zfs::step_debug_failures(), zfs::aux_debug_failures(), zfs::muon_debug_failures(),
                                  zfs::ns_gemm_debug_failures(), zfs::thin_debug_failures(), zfs::qk_debug_failures(),
-                                 zfs::norm_debug_failures(), zfs::pack_debug_failures(), zfs::embedding_debug_failures()};
+                                 zfs::embedding_debug_failures()};
   unsigned int sum = 0;
   for (unsigned int c : counts) {
     if (c == 0xFFFFFFFFu) return fail(nullptr, ZERO_ECUDA, "cannot read the check counters");
