@@ -64,8 +64,9 @@ def _no_graph(what: str, *tensors: Optional[torch.Tensor]) -> None:
 
 def _no_leaf(*outs: Optional[torch.Tensor]) -> None:
     """An output that requires a gradient is refused: torch.autograd would not learn of what is written."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in outs):
-        raise ValueError("an output requires a gradient: detach it or call under torch.no_grad()")
+    for t in outs:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("an output requires a gradient: detach it or call under torch.no_grad()")
 
 
 # Tells torch.autograd that the kernels wrote to tensors of the caller's, so that a
@@ -73,9 +74,11 @@ def _no_leaf(*outs: Optional[torch.Tensor]) -> None:
 _written = torch.autograd.graph.increment_version
 
 
-def _layout(x: torch.Tensor) -> Tuple[int, int, list]:
+def _layout(x: torch.Tensor) -> Tuple[int, int, Sequence]:
     """Byte address, bytes of a contiguous run and the (stride, size) of the other dimensions, largest stride first."""
     size = x.element_size()
+    if x.is_contiguous():
+        return x.data_ptr(), x.numel() * size, ()
     dims = sorted(((st * size, n) for n, st in zip(x.shape, x.stride()) if n > 1), reverse=True)
     run = size
     while dims and dims[-1][0] == run:
@@ -84,7 +87,7 @@ def _layout(x: torch.Tensor) -> Tuple[int, int, list]:
 
 
 def _span(run: int, dims) -> int:
-    return run + sum(stride * (n - 1) for stride, n in dims)
+    return run + sum(stride * (n - 1) for stride, n in dims) if dims else run
 
 
 def _apart(at: int, run: int, dims, other_run: int, other_dims) -> bool:
@@ -116,12 +119,19 @@ def _check_memory(outs, ins) -> None:
         if out.numel() == 0:
             continue
         at, run, dims = _layout(out)
-        if any(stride < _span(run, dims[d + 1:]) for d, (stride, _) in enumerate(dims)):
+        if dims and any(stride < _span(run, dims[d + 1:]) for d, (stride, _) in enumerate(dims)):
             raise ValueError("an output's elements overlap one another")
-        others = [*outs[:i], *(t for j, some in enumerate(ins) for t in some if j != i or not _same(t, out))]
-        for there, other_run, other_dims in (_layout(t) for t in others if t.numel()):
-            if not _apart(there - at, run, dims, other_run, other_dims):
-                raise ValueError("an output overlaps another tensor of the call")
+        end = at + _span(run, dims)
+        for j, some in enumerate((outs[:i], *ins), -1):
+            for t in some:
+                there = t.data_ptr()
+                if there >= end or t.numel() == 0:  # the usual case: memory of its own
+                    continue
+                _, other_run, other_dims = _layout(t)
+                if there + _span(other_run, other_dims) <= at or j == i and _same(t, out):
+                    continue
+                if not _apart(there - at, run, dims, other_run, other_dims):
+                    raise ValueError("an output overlaps another tensor of the call")
 
 
 def orthogonalize(x: torch.Tensor, *, steps: int = 5, coefficients: Sequence[float] = (3.4445, -4.7750, 2.0315),
