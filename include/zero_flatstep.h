@@ -808,7 +808,9 @@ typedef struct zero_norm_config {
  * zero_layer_norm — for every row x
  *   mean = sum x / cols (center 0: 0),  rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
  *   y = (x - mean) * rstd * weight + bias
- * in fp32, rounded once; a row whose squares exceed fp32's range has rstd 0.
+ * in fp32, rounded once; a row whose squares exceed fp32's range (entries from
+ * about 1e19 on) has rstd 0, and squares below it (entries under about 1e-19)
+ * are lost beside any eps of an ordinary size, but leave rstd inf with eps 0.
  *  weight, bias   cols elements of weight_dtype, or NULL: none
  *  y              may be x itself (same stride), else must not overlap an input;
  *                 a stride of at least cols

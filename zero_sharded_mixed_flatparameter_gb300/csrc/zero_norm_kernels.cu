@@ -18,12 +18,18 @@
 // SM, so that the column sums come in 152 parts.  Arithmetic is packed (two fp32 an
 // instruction): both passes were bound by instructions without.
 //
-// 32768 x 2048 bf16, weight and bias: forward 46 us, 5.9 TB/s of the 268 MB read
-// and written; backward 67 us, 6.0 TB/s of 403 MB, 3 of them the join of the
-// column sums.  16384 x 2048 with the 8-bit form (e4m3), both directions: 74 us for
-// 338 MB, bound by instructions (the codes' conversions, twice in the backward
-// pass).  5003 x 1301 fp32 backward: 24 us for 78 MB, single elements with a
-// row of a group in flight.
+// Device times.  32768 x 2048 bf16, weight and bias: forward 46 us, 5.9 TB/s of the
+// 268 MB read and written; backward 67 us, 6.0 TB/s of 403 MB, 3 of them the join
+// of the column sums.  16384 x 2048 with the 8-bit form (e4m3), both directions: 74
+// us for 338 MB.  There neither memory (42 % in use) nor issue slots (56 % forward,
+// 65 % backward) are full: 16 to 20 warps an SM, a quarter of what it holds, convert
+// codes between the sums they wait for; the backward pass decodes twice, and sums
+// dbias and a mean of g that the form without them does not need.  16384 x 2048
+// fp32: 46 us forward, 105 backward (268, 403 MB).  Widths that are no multiple of
+// 8 columns go as single elements, with fewer rows in flight: 5003 x 1301 fp32 14
+// us forward, 24 backward (52, 78 MB); 32768 x 2047 bf16 forward 78 us.  Beyond
+// 8192 columns a CTA walks over the row: 4096 x 8192 bf16 32 us forward, 50
+// backward, 4096 x 8200 97 and 122.
 
 #include <cmath>
 
