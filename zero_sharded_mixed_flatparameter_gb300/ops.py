@@ -445,9 +445,9 @@ def pack_activations(x: torch.Tensor, dtype: torch.dtype = torch.float8_e4m3fn, 
     power-of-two scale for every 32 columns of a row.
 
     ``dtype``: torch.float8_e4m3fn (each entry within 2^-4 of itself or, where it is
-    smaller than 2^-6 of the scale, within 2^-10 of the scale; the group's largest is
-    above 224 scales) or torch.int8 (within half a scale, 1/127 of its group's
-    largest).  A group with an inf or NaN reads as NaN; finite entries that round up
+    smaller than 2^-6 of the scale, within 2^-10 of the scale) or torch.int8 (within
+    half a scale).  But for the smallest scale, 2^-126, the group's largest is above
+    224 or 63.5 scales: whole numbers are within 1/127 of it.  A group with an inf or NaN reads as NaN; finite entries that round up
     to 2^128 read as inf.  ``out``: an earlier result of the same shape and types to
     write to.  What ``x`` requires a gradient for is not recorded: this keeps a
     tensor for the backward pass, as saving it would.
